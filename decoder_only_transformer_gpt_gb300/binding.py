@@ -13,7 +13,8 @@ import numpy as np
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgpt_gb300.so")
 
-GPT_OK, GPT_EINVAL, GPT_ECONFIG, GPT_ESEQ, GPT_ETOKEN, GPT_ECUDA, GPT_ENOMEM, GPT_EDEVICE, GPT_EUNSUPPORTED = range(9)
+GPT_OK, GPT_EINVAL, GPT_ECONFIG, GPT_ESEQ, GPT_ETOKEN, GPT_ECUDA, GPT_ENOMEM, GPT_EDEVICE, GPT_EUNSUPPORTED, \
+    GPT_EPAGE = range(10)
 # parameters of gpt_grad, in the library's order; the per-block ones take a layer index
 GRAD_PARAMS = ("wte", "wpe", "lnf_g", "lnf_b", "ln1_g", "ln1_b", "attn_w", "attn_b", "proj_w", "proj_b",
                "ln2_g", "ln2_b", "fc_w", "fc_b", "mp_w", "mp_b", "head")
@@ -96,6 +97,9 @@ def load(path: str = LIB_PATH):
         "gptk_embed": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
         "gptk_lmhead_ce": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp]),
         "gptk_lmhead_ce_noalloc": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, vp, vp]),
+        "gptk_paged_store": (ctypes.c_int, [vp] * 6 + [i32] * 8 + [vp]),
+        "gptk_paged_attention": (ctypes.c_int, [vp] * 7 + [i32] * 9 + [vp]),
+        "gptk_paged_evict": (ctypes.c_int, [vp] * 7 + [i32] * 10 + [vp]),
         "gptk_mean": (ctypes.c_int, [vp, i32, vp, vp]),
         "gptk_status": (ctypes.c_int, [vp]),
     }
@@ -356,6 +360,81 @@ def lmhead_ce_noalloc(h, wte, targets, nll, err=None, stream=None):
     V = wte.shape[0]
     _check(lib.gptk_lmhead_ce_noalloc(_ptr(h), _ptr(wte), _ptr(targets), _ptr(nll), M, V, C, _ptr(err),
                                       _stream(stream)), "gptk_lmhead_ce_noalloc")
+
+
+def _take(name: str, t, dtype, shape) -> None:
+    """Refuse a tensor whose type, shape, layout or device the kernels cannot take (shape: None for any extent)."""
+    import torch
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, needs {dtype}")
+    if len(t.shape) != len(shape) or any(e is not None and e != n for e, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {tuple('any' if e is None else e for e in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, needs the current CUDA device")
+
+
+def _pool_dims(pool, weight, table):
+    """(pages, Hkv, page, D, B, max_pages) of a paged cache, its tensors checked."""
+    import torch
+    if pool.dim() != 5 or pool.shape[1] != 2:
+        raise ValueError(f"pool: shape {tuple(pool.shape)}, needs [pages, 2, Hkv, page, D]")
+    pages, _, Hkv, page, D = pool.shape
+    _take("pool", pool, torch.bfloat16, (pages, 2, Hkv, page, D))
+    if weight is not None:
+        _take("weight", weight, torch.float32, (pages, Hkv, page))
+    _take("table", table, torch.int32, (None, None))
+    return pages, Hkv, page, D, table.shape[0], table.shape[1]
+
+
+def paged_store(qkv, pool, table, H: int, start=None, count=None, weight=None, stream=None):
+    """Keys and values of qkv [B, T, (H + 2 Hkv) D] into rows start[b] + t (t < count[b]) of the paged cache."""
+    import torch
+    lib = load()
+    pages, Hkv, page, D, B, max_pages = _pool_dims(pool, weight, table)
+    _take("qkv", qkv, torch.bfloat16, (B, None, (H + 2 * Hkv) * D))
+    if start is not None:
+        _take("start", start, torch.int32, (B,))
+    if count is not None:
+        _take("count", count, torch.int32, (B,))
+    _check(lib.gptk_paged_store(_ptr(qkv), _ptr(pool), _ptr(weight), _ptr(table), _ptr(start), _ptr(count), B,
+                                qkv.shape[1], H, Hkv, D, pages, page, max_pages, _stream(stream)), "gptk_paged_store")
+
+
+def paged_attention(qkv, pool, table, lens, y, H: int, lse2=None, weight=None, window: int = 0, sinks: int = 0,
+                    stream=None):
+    """One new token per sequence, qkv [B, (H + 2 Hkv) D]: stored at row lens[b], its attention in y [B, H D].
+
+    window 0 sees every cached row, else the last `window` rows and the first `sinks`; weight (optional) sums
+    each row's attention weight, lse2 [B, H] (optional) takes the log-sum-exp. lens[b] < 0 skips row b."""
+    import torch
+    lib = load()
+    pages, Hkv, page, D, B, max_pages = _pool_dims(pool, weight, table)
+    _take("qkv", qkv, torch.bfloat16, (B, (H + 2 * Hkv) * D))
+    _take("lens", lens, torch.int32, (B,))
+    _take("y", y, torch.bfloat16, (B, H * D))
+    if lse2 is not None:
+        _take("lse2", lse2, torch.float32, (B, H))
+    _check(lib.gptk_paged_attention(_ptr(qkv), _ptr(pool), _ptr(weight), _ptr(table), _ptr(lens), _ptr(y), _ptr(lse2), B,
+                                    H, Hkv, D, pages, page, max_pages, window, sinks, _stream(stream)),
+           "gptk_paged_attention")
+
+
+def paged_evict(pool, weight, table, lens, dst_table, new_lens, kept, budget: int, sinks: int = 0, recent: int = 0,
+                stream=None):
+    """Keep budget rows per sequence and key head (first `sinks`, last `recent`, largest weights between), in order,
+    in the pages of dst_table (`table` itself: in place); kept [B, Hkv, budget] names them, -1 behind the last."""
+    import torch
+    lib = load()
+    pages, Hkv, page, D, B, max_pages = _pool_dims(pool, weight, table)
+    _take("lens", lens, torch.int32, (B,))
+    _take("dst_table", dst_table, torch.int32, (B, None))
+    _take("new_lens", new_lens, torch.int32, (B,))
+    _take("kept", kept, torch.int32, (B, Hkv, budget))
+    _check(lib.gptk_paged_evict(_ptr(pool), _ptr(weight), _ptr(table), _ptr(lens), _ptr(dst_table), _ptr(new_lens),
+                                _ptr(kept), B, Hkv, D, pages, page, max_pages, dst_table.shape[1], budget, sinks, recent,
+                                _stream(stream)), "gptk_paged_evict")
 
 
 def mean(nll, loss, stream=None):

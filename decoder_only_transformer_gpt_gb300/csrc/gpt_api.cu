@@ -125,6 +125,7 @@ const char* gpt_strerror(int code) {
     case GPT_ENOMEM: return "out of memory";
     case GPT_EDEVICE: return "device-side failure (expired wait or misaligned shared memory)";
     case GPT_EUNSUPPORTED: return "unsupported device (needs sm_103, GB300)";
+    case GPT_EPAGE: return "page number outside the pool, or a length past the page table";
     default: return "unknown status";
   }
 }

@@ -34,6 +34,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 }  // namespace
 
+int* gptgb::step_err_word() { return err_word(); }
+
 extern "C" {
 
 int gptk_gemm(const void* A, const void* W, const float* bias, void* out, int32_t M, int32_t N, int32_t K,
@@ -311,6 +313,7 @@ int gptk_status(void* stream) {
   GPT_CUDA(cudaMemset(err, 0, sizeof(int)));
   if (h == GPT_DEV_OK) return GPT_OK;
   if (h == GPT_DEV_ETOKEN || h == GPT_DEV_ETARGET) return GPT_ETOKEN;
+  if (h == GPT_DEV_EPAGE) return GPT_EPAGE;
   return GPT_EDEVICE;
 }
 

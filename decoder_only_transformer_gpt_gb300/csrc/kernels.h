@@ -14,6 +14,7 @@ enum : int {
   GPT_DEV_ETARGET = 2,    // a target outside [0, V)
   GPT_DEV_ETIMEOUT = 3,   // a bounded wait expired
   GPT_DEV_EALIGN = 4,     // dynamic shared memory not 1024-byte aligned
+  GPT_DEV_EPAGE = 5,      // paged cache: a page number outside the pool, or a length past the page table
 };
 
 enum Epilogue : int {
@@ -204,6 +205,31 @@ cudaError_t launch_set_int(int* p, int v, cudaStream_t s);
 constexpr int kSampleMaxV = 55296;
 cudaError_t launch_sample(const float* logits, int B, int V, float temperature, int top_k, float top_p,
                           const float* uniform, int32_t* out, cudaStream_t s);
+// ---- paged key/value cache (bf16; k_paged.cu)
+// pool [pages][2][Hkv][page][D]: per page the keys of every key head, then the values; row r of sequence b
+// lies in page table[b][r / page] at slot r % page, page = 1 << page_log2. weight (nullable) fp32
+// [pages][Hkv][page]: one running sum of attention weight per cached row and key head.
+constexpr int kPagedMaxB = 8192;
+struct PagedCache {
+  void* pool;
+  float* weight;
+  const int32_t* table;   // [B][max_pages]
+  int pages, page_log2, max_pages, Hkv;
+};
+// Rows start[b] + t (start nullable: 0) of sequence b = keys and values of qkv[b, t] for t < count[b]
+// (nullable: T); their weights become 0.
+cudaError_t launch_paged_store(const PagedCache& c, const void* qkv, const int32_t* start, const int32_t* count, int B,
+                               int T, int H, int D, int* err, cudaStream_t s);
+// One new token per sequence: stores its key and value at row lens[b], attends over the seen rows of 0..lens[b]
+// (window 0: all; else those less than window rows back, and the first `sinks`).
+cudaError_t launch_paged_attention(const PagedCache& c, const void* qkv, const int32_t* lens, void* y, float* lse2,
+                                   int B, int H, int D, int window, int sinks, int* err, cudaStream_t s);
+// Keeps budget rows per sequence and key head (the first `sinks`, the last `recent`, the largest weights
+// between) in order, in the pages of dst_table.
+cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const int32_t* dst_table, int dst_max_pages,
+                               int32_t* new_lens, int32_t* kept, int B, int D, int budget, int sinks, int recent,
+                               int* err, cudaStream_t s);
+
 // cache[b][t][0:2C] = qkv[b, t][C:3C] for a prompt of T tokens.
 cudaError_t launch_kv_store(const void* qkv, void* cache_layer, int B, int T, int C, int ctx, cudaStream_t s);
 

@@ -104,6 +104,8 @@ int gemm_bf16_long(gpt_model* m, const CUtensorMap& tmA, const CUtensorMap& tmB,
 int gemm_bf16_gelu_u(gpt_model* m, const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tm_g,
                      const CUtensorMap& tm_u, int M, int N, int K, const float* bias, void* g, cudaStream_t s);
 int shape_ok(const gpt_model* m, int B, int T);
+// the per-step entries' device error word (gptk.cu), read by gptk_status(); nullptr: it could not be allocated
+int* step_err_word();
 // thread-local text of the last failing CUDA call
 void set_detail(const char* what, cudaError_t e);
 void set_detail_text(const char* text);

@@ -43,7 +43,9 @@ enum {
   GPT_ECUDA = 5,       /* a CUDA runtime or driver call failed */
   GPT_ENOMEM = 6,      /* device or pinned-host allocation failed */
   GPT_EDEVICE = 7,     /* a kernel's bounded wait expired or its shared memory was misaligned */
-  GPT_EUNSUPPORTED = 8 /* the device is not sm_103 (GB300) or lacks the resources */
+  GPT_EUNSUPPORTED = 8, /* the device is not sm_103 (GB300) or lacks the resources */
+  GPT_EPAGE = 9        /* paged cache: a page number outside the pool, or a length past the page table;
+                          found on the device */
 };
 
 /* Model hyper-parameters ("Day 16 从零组装 MiniGPT" §三, GPTConfig). */

@@ -133,6 +133,58 @@ int gptk_lmhead_ce(const void* h, const void* wte, const int32_t* targets, float
 int gptk_lmhead_ce_noalloc(const void* h, const void* wte, const int32_t* targets, float* nll,
                            int32_t M, int32_t V, int32_t C, int32_t* d_err, void* stream);
 
+/*
+ * Paged key/value cache (bf16, D in {32, 64}): the cached keys and values of many sequences of different lengths in
+ * one pool of pages. The source pages describe the cache of a single sequence ("预训练一个 Mini GPT", the sections on
+ * the KV cache); pages, the window and the eviction below are this library's extension of it.
+ *   pool    [pages][2][Hkv][page][D] bf16: per page the rows of every key head's keys, then of their values
+ *   weight  [pages][Hkv][page] fp32 or NULL: per cached row and key head, the attention weight it has received
+ *   table   [B][max_pages] int32: row r of sequence b lies in page table[b][r / page] at slot r % page
+ * page is a power of two, 8..256. H query heads share Hkv key heads (H a multiple of Hkv): query head h reads key
+ * head h / (H / Hkv). A token's qkv row holds H D queries, Hkv D keys, Hkv D values, as the output of one product.
+ * All arrays are device memory of the current device, pool, qkv and y 16-byte aligned. B <= 8192.
+ * GPT_EINVAL: null pointers or sizes; GPT_ECONFIG: D, H % Hkv or alignment. Checked on the device: a page number
+ * outside [0, pages) or a row past max_pages * page is neither read nor written, and gptk_status() then returns
+ * GPT_EPAGE (what the call wrote for that sequence is unspecified).
+ *
+ * gptk_paged_store: rows start[b] + t of sequence b take the keys and values of qkv[b][t] ([B, T, (H + 2 Hkv) D])
+ * for t < count[b]; their weights become 0. start NULL: 0; count NULL: T (more than T counts as T). No two of the
+ * stored rows may share a place.
+ */
+int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* table, const int32_t* start,
+                     const int32_t* count, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t D, int32_t pages,
+                     int32_t page, int32_t max_pages, void* stream);
+
+/*
+ * Attention of one new token per sequence over its cached rows. Sequence b holds rows 0..lens[b]-1; its new token,
+ * qkv[b] ([B, (H + 2 Hkv) D]), becomes row n = lens[b] (key and value are stored there), and its queries see the
+ * rows r <= n with n - r < window or r < sinks (window 0: all of them):
+ *   y[b, h] = sum_r a_r u_r,  a = softmax(q_h . k_r / sqrt(D))     bf16 [B, H D]
+ *   lse2[b, h] = log2 sum_r 2^(q_h . k_r log2(e) / sqrt(D))         fp32 [B, H], NULL: not wanted
+ *   weight(r, key head) += the sum of a_r over the head's H / Hkv queries (r < n); = that sum for row n
+ * lens[b] < 0: no sequence; nothing of row b is read or written. The caller counts lens up (one cache per layer
+ * shares one lens). Sequences may share the pages of rows below their own; the new rows' pages are their own. fp32
+ * scores and sums; the probabilities are rounded to bf16 for the product with the values.
+ */
+int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32_t* table, const int32_t* lens, void* y,
+                         float* lse2, int32_t B, int32_t H, int32_t Hkv, int32_t D, int32_t pages, int32_t page,
+                         int32_t max_pages, int32_t window, int32_t sinks, void* stream);
+
+/*
+ * Eviction by summed attention weight, for every sequence and key head by itself: of rows 0..lens[b]-1 keeps the
+ * first `sinks`, the last `recent`, and between them the rows of the largest weight, budget rows in all (every row
+ * where lens[b] <= budget; equal weights: the lowest rows; a NaN weight counts as the smallest; sinks + recent <=
+ * budget). The kept rows, their weights with them, become rows 0.. of dst_table [B][dst_max_pages] in their order;
+ * kept[b][head][i] (int32 [B, Hkv, budget]) is the row that row i was, -1 behind the last; new_lens[b] =
+ * min(lens[b], budget) (lens[b] itself where it is negative; new_lens must not be lens). dst_table either is
+ * `table`, or starts every sequence with the same pages (in place), or names pages that no sequence of `table`
+ * holds, each once; the old rows then stay as they were.
+ */
+int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int32_t* lens, const int32_t* dst_table,
+                     int32_t* new_lens, int32_t* kept, int32_t B, int32_t Hkv, int32_t D, int32_t pages, int32_t page,
+                     int32_t max_pages, int32_t dst_max_pages, int32_t budget, int32_t sinks, int32_t recent,
+                     void* stream);
+
 /* Deterministic mean of nll[0..M) into *loss (device fp32). */
 int gptk_mean(const float* nll, int32_t M, float* loss, void* stream);
 
