@@ -97,6 +97,8 @@ def load(path: str = LIB_PATH):
         "gptk_embed": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
         "gptk_lmhead_ce": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp]),
         "gptk_lmhead_ce_noalloc": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, vp, vp]),
+        "gptk_attention_window": (ctypes.c_int, [vp] * 3 + [i32] * 7 + [vp]),
+        "gptk_attention_window_bwd": (ctypes.c_int, [vp] * 5 + [i32] * 7 + [vp]),
         "gptk_paged_store": (ctypes.c_int, [vp] * 6 + [i32] * 8 + [vp]),
         "gptk_paged_attention": (ctypes.c_int, [vp] * 7 + [i32] * 9 + [vp]),
         "gptk_paged_evict": (ctypes.c_int, [vp] * 7 + [i32] * 10 + [vp]),
@@ -373,6 +375,42 @@ def _take(name: str, t, dtype, shape) -> None:
         raise ValueError(f"{name}: not contiguous")
     if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: on {t.device}, needs the current CUDA device")
+
+
+def _qkv_dims(qkv, H: int, Hkv: int):
+    """(B, T, D) of fused rows [B, T, (H + 2 Hkv) D]."""
+    if qkv.dim() != 3 or H < 1 or Hkv < 1 or qkv.shape[2] % (H + 2 * Hkv):
+        raise ValueError(f"qkv: shape {tuple(qkv.shape)}, needs [B, T, (H + 2 Hkv) D] for H = {H}, Hkv = {Hkv}")
+    B, T, row = qkv.shape
+    return B, T, row // (H + 2 * Hkv)
+
+
+def attention_window(qkv, y, H: int, Hkv: int, window: int, sinks: int = 0, lse2=None, stream=None):
+    """Causal attention over the last `window` keys and the first `sinks`: qkv [B, T, (H + 2 Hkv) D] -> y [B, T, H D];
+    lse2 [B, H, T] (optional, needed by the derivative) takes each row's base-2 log-sum-exp."""
+    import torch
+    lib = load()
+    B, T, D = _qkv_dims(qkv, H, Hkv)
+    _take("qkv", qkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D))
+    _take("y", y, torch.bfloat16, (B, T, H * D))
+    if lse2 is not None:
+        _take("lse2", lse2, torch.float32, (B, H, T))
+    _check(lib.gptk_attention_window(_ptr(qkv), _ptr(y), _ptr(lse2), B, T, H, Hkv, D, window, sinks, _stream(stream)),
+           "gptk_attention_window")
+
+
+def attention_window_bwd(qkv, y, dy, lse2, dqkv, H: int, Hkv: int, window: int, sinks: int = 0, stream=None):
+    """dqkv of attention_window from its input, output, log-sum-exp and the output's gradient dy [B, T, H D]."""
+    import torch
+    lib = load()
+    B, T, D = _qkv_dims(qkv, H, Hkv)
+    _take("qkv", qkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D))
+    _take("y", y, torch.bfloat16, (B, T, H * D))
+    _take("dy", dy, torch.bfloat16, (B, T, H * D))
+    _take("lse2", lse2, torch.float32, (B, H, T))
+    _take("dqkv", dqkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D))
+    _check(lib.gptk_attention_window_bwd(_ptr(qkv), _ptr(y), _ptr(dy), _ptr(lse2), _ptr(dqkv), B, T, H, Hkv, D, window,
+                                         sinks, _stream(stream)), "gptk_attention_window_bwd")
 
 
 def _pool_dims(pool, weight, table):

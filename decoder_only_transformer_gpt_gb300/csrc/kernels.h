@@ -158,6 +158,17 @@ cudaError_t launch_attention_bwd_tc(const CUtensorMap& tm_qkv, const CUtensorMap
                                     float* dsum, float* dqacc, void* dqkv, int B, int T, int H, int D, int* err,
                                     int* sched, cudaStream_t s);
 
+// Sliding window with sinks: query t sees key s if s <= t and (t - s < window or s < sinks); H query heads share Hkv
+// key heads; rows [B][T][(H + 2 Hkv) D]. window >= 1, T < 2^30. tm_y: make_tmap_attn_out over y [B][T][H D];
+// lse2 as for launch_attention_tc, nullable.
+cudaError_t launch_attention_window_tc(const CUtensorMap& tm_qkv, const CUtensorMap& tm_y, int B, int T, int H, int Hkv,
+                                       int D, int window, int sinks, int* err, float* lse2, cudaStream_t s);
+// Its derivative: maps, scratch and launches as for launch_attention_bwd_tc (tm_dkv over dqkv's rows).
+cudaError_t launch_attention_window_bwd_tc(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
+                                           const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2,
+                                           float* dsum, float* dqacc, void* dqkv, int B, int T, int H, int Hkv, int D,
+                                           int window, int sinks, int* err, cudaStream_t s);
+
 // One parameter tensor for the optimiser: values [off, off + n) of the flat gradient, master and
 // moment arrays, stored at dst (bf16 when bf16 != 0, else fp32); decay: decoupled weight decay applies.
 struct OptSeg {

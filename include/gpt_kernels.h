@@ -85,6 +85,28 @@ int gptk_attention_bwd(const void* qkv, const void* y, const void* dy, const flo
                        int32_t T, int32_t H, int32_t D, void* stream);
 
 /*
+ * Sliding-window attention with sinks (bf16; the source pages attend to the whole past, §25.2: a window at least as
+ * long as the sequence gives that): query t sees key s if s <= t and (t - s < window or s < sinks), window >= 1.
+ * qkv [B, T, (H + 2 Hkv) D]: a token's H queries, Hkv keys, Hkv values (Q, K, U thirds where Hkv = H); query head h
+ * reads key head h / (H / Hkv). y [B, T, H D], heads merged; lse2 fp32 [B, H, T] or NULL: each row's base-2
+ * log-sum-exp of its seen scaled scores, as for gptk_attention_lse. fp32 scores and sums; the probabilities are
+ * rounded to bf16 for the product with the values. A sequence shorter than T is padded behind its end (rows of finite
+ * numbers): no real token sees the padding. D in {32, 64}, H a multiple of Hkv, 16-byte aligned arrays
+ * (GPT_ECONFIG otherwise), T < 2^30, B T < 2^31.
+ */
+int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t D,
+                          int32_t window, int32_t sinks, void* stream);
+
+/*
+ * Its derivative: from qkv, y and lse2 of gptk_attention_window (the same window and sinks) and dy [B, T, H D], writes
+ * dqkv [B, T, (H + 2 Hkv) D]: dQ, and dK and dU summed over the H / Hkv query heads of a key head. Rows behind a
+ * padded sequence's end take no part where their dy is zero. Scratch (4 B T H (D + 1) bytes) is
+ * allocated on the stream and freed there. dQ's fp32 additions come in an order that varies between runs.
+ */
+int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, const float* lse2, void* dqkv, int32_t B,
+                              int32_t T, int32_t H, int32_t Hkv, int32_t D, int32_t window, int32_t sinks, void* stream);
+
+/*
  * LayerNorm over rows of x [M, C] fp32 ("预训练一个 Mini GPT" 第4步; "GPT-1 学习笔记" §3.2):
  * out (dtype) = (x - mean)/sqrt(var + eps) * g + b; out_f32 (fp32, may alias x, may be NULL)
  * receives the same values in fp32. C must be a multiple of 8 and at most 2048.
