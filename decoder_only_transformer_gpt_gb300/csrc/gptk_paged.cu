@@ -64,7 +64,10 @@ int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32
   PagedCache c;
   const int rc = paged_cache(&c, pool, weight, table, B, Hkv, D, pages, page, max_pages);
   if (rc != GPT_OK) return rc;
-  if (H % Hkv || !aligned16(qkv) || !aligned16(y)) return GPT_ECONFIG;
+  if (H % Hkv || H / Hkv > kPagedMaxGroup || !aligned16(qkv) || !aligned16(y)) return GPT_ECONFIG;
+  // the units of 32 rows are numbered with 32 bits, and with 64 over all heads
+  const int64_t units = static_cast<int64_t>(B) * ((static_cast<int64_t>(max_pages) * page + 31) / 32);
+  if (units > 0x7fffffffLL || units * Hkv > (1LL << 40)) return GPT_EINVAL;
   int* err = step_err_word();
   if (!err) return GPT_ENOMEM;
   return finish("paged attention", launch_paged_attention(c, qkv, lens, y, lse2, B, H, D, window, sinks, err,

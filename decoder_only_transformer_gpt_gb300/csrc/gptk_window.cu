@@ -60,7 +60,7 @@ int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, co
   // scratch on the stream: the fp32 dQ accumulator and Dsum
   const size_t acc_b = M * C * sizeof(float), dsum_b = M * H * sizeof(float);
   uint8_t* ws = nullptr;
-  cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&ws), acc_b + dsum_b, s);
+  cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&ws), acc_b + dsum_b, s);
   if (e != cudaSuccess) {
     set_detail("window attention derivative scratch", e);
     return e == cudaErrorMemoryAllocation ? GPT_ENOMEM : GPT_ECUDA;
@@ -70,13 +70,13 @@ int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, co
   CUtensorMap tq, tdy, tdkv, tdq;
   if (!(make_tmap_qkv(&tq, qkv, B, T, row, D) && make_tmap_qkv(&tdy, dy, B, T, C, D) &&
         make_tmap_attn_out(&tdkv, dqkv, B, T, row, D) && make_tmap_bt_f32(&tdq, dqacc, B, T, C))) {
-    cudaFreeAsync(ws, s);
+    scratch_free(ws, s);
     set_detail_text("window attention derivative tensor maps");
     return GPT_ECUDA;
   }
   e = launch_attention_window_bwd_tc(tq, tdy, tdkv, tdq, y, dy, lse2, dsum, dqacc, dqkv, B, T, H, Hkv, D, window, sinks,
                                      err, s);
-  cudaFreeAsync(ws, s);
+  scratch_free(ws, s);
   if (e != cudaSuccess) {
     set_detail("window attention derivative", e);
     return GPT_ECUDA;

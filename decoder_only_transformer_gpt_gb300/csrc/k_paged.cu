@@ -84,102 +84,498 @@ paged_store_kernel(PagedCache c, const uint4* __restrict__ qkv, const int32_t* _
 }
 
 // ---------------------------------------------------------------- attention of one new token
+//
+// Bound by reading the cache: 4 D bytes per seen row and key head, once. What the design does for that:
+//  * Work is cut by rows, not by sequences. A unit is 32 consecutive seen rows of one (sequence, key head, group of
+//    up to 16 query heads); all units form one list (sequence-major) and every warp of the grid takes an equal
+//    contiguous range of it, so ragged lengths, one long sequence or a single one all load the machine evenly. A warp
+//    that holds all units of a (sequence, head group) writes its output; the others write a partial result (maximum,
+//    sum, unnormalised output), at most two per warp, which a second kernel joins in a fixed order.
+//  * A warp streams its units through its own ring of kStages stages of shared memory (cp.async, 16 bytes a lane,
+//    whole rows), with no barrier across warps; the page numbers of a unit are loaded one unit before its rows. Rows
+//    are found through the table one by one, so windows, sinks and pages may end anywhere in a unit. Rows that are
+//    not seen are not read (their shared memory is filled with zeros).
+//  * The scores and the product with the values are mma.sync m16n8k16 with the query heads of the group as the 16
+//    rows: with at most 16 rows of queries per key head the tensor core's rate does not matter (a tcgen05 tile
+//    would have 128), but shared keys and values are unpacked once for all heads. P is rounded to bf16 for that
+//    product (2^-8 of sum a |u| at most); scores, maxima, sums and outputs stay fp32.
+constexpr int kStages = 3;
+constexpr int kUnit = 32;                 // seen rows per unit
 
-// One block per (key head, sequence); its G query heads one after the other. Warp w takes 32-row chunks
-// w, w + 8, ..: lane = row for the scores, lane = D / 32 columns for the values; running maximum and sum per
-// warp, warps merged in a fixed order. A last pass adds the weights (scores once more).
-constexpr int kDecWarps = 8;
+template <int D, int QR>
+struct DecCfg {
+  static constexpr int ROWB = D * 2;
+  static constexpr int U = D / 8;                                 // 16-byte units per row
+  static constexpr int TILE = kUnit * ROWB;                       // keys, or values, of a unit
+  static constexpr int STAGE = 2 * TILE + QR * ROWB;              // + the query rows where a unit starts a segment
+  static constexpr int WARP = kStages * STAGE + 128;              // + the stages' row masks
+};
 
+// Where the partial results of a launch lie (device scratch).
+struct DecScratch {
+  int* prefix;        // [B + 1] units of the sequences before b, per head group
+  float* o;           // [warps][2][QR][D] unnormalised partial outputs
+  float2* ml;         // [warps][2][QR] their maxima (log2 units) and sums
+  float* lse;         // [B][H] log2-sum-exp of segments held by one warp
+  float* score;       // [B][H][score_ld] scores in log2 units by seen row, or nullptr (no weights wanted)
+  int score_ld;
+};
+
+struct DecShape {
+  int B, H, G, mg;    // mg: head groups of up to 16 per key head
+  int window, sinks;
+  float scale_log2;
+};
+
+// First unit of warp g's range of `total` units dealt to n warps.
+__device__ __forceinline__ long long range_start(long long total, int g, int n) { return total * g / n; }
+// Warps that take part: every range holds a unit at least.
+__device__ __forceinline__ int active_warps(long long total, int n) { return total < n ? static_cast<int>(total) : n; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool copy) {
+  const int n = copy ? 16 : 0;                       // 0: the 16 bytes are zeros, src is not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte unit u of row r in a tile of rows of D bf16, permuted within 128 bytes so that the eight
+// rows of an ldmatrix fall into different banks.
 template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32)
-paged_attention_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const int32_t* __restrict__ lens,
-                       __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, int H, int window, int sinks,
-                       float scale_log2, int* err) {
+__device__ __forceinline__ uint32_t tile_at(int r, int u) {
+  return D == 64 ? r * 128 + ((u ^ (r & 7)) << 4) : r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+}
+
+// The list position of a unit: sequence, head group (key head * mg + group), tile of the sequence's seen rows.
+struct Unit {
+  int b, hm, tile, nt, last;
+  Seen seen;
+};
+
+template <int D, int QR>
+__global__ void __launch_bounds__(256, 1)
+paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const int32_t* __restrict__ lens,
+                   __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, DecShape w, DecScratch ws, int* err) {
+  using Cfg = DecCfg<D, QR>;
+  constexpr int U = Cfg::U;
+  constexpr int RPI = 32 / U;                        // rows per copy instruction of a warp
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+  int* s_prefix = reinterpret_cast<int*>(smem + nwarps * Cfg::WARP);     // [B + 1]
+  int* s_len = s_prefix + w.B + 1;                                       // [B]
+  __shared__ int s_sum[8];
   pdl_wait();
   pdl_trigger();
-  constexpr int CPL = D / 32;
-  __shared__ float sq[D];
-  __shared__ float sm[kDecWarps], sl[kDecWarps], so[kDecWarps][D];
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = H / c.Hkv;
-  const int last = __ldg(lens + b);
-  if (last < 0) return;
-  if (last >= static_cast<long long>(c.max_pages) << c.page_log2) {
-    if (threadIdx.x == 0) record_error(err, GPT_DEV_EPAGE);
-    return;
+
+  // units per sequence and their prefix sums (per head group)
+  const long long cap = static_cast<long long>(c.max_pages) << c.page_log2;
+  if (threadIdx.x == 0) s_prefix[0] = 0;
+  int carry = 0;
+  for (int b0 = 0; b0 < w.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    int last = -1, x = 0;
+    if (b < w.B) {
+      last = __ldg(lens + b);
+      if (last >= cap) {
+        record_error(err, GPT_DEV_EPAGE);
+        last = -1;
+      }
+      if (last >= 0) x = (seen_rows(last + 1, w.window, w.sinks).n + kUnit - 1) / kUnit;
+      s_len[b] = last;
+    }
+    int incl = x;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, k);
+      if (lane >= k) incl += v;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int before = carry;
+    for (int i = 0; i < nwarps; ++i) {
+      if (i < warp) before += s_sum[i];
+      carry += s_sum[i];
+    }
+    if (b < w.B) s_prefix[b + 1] = before + incl;
+    __syncthreads();
   }
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= w.B; b += blockDim.x) ws.prefix[b] = s_prefix[b];
+
+  const int HM = c.Hkv * w.mg;
+  const long long total = static_cast<long long>(carry) * HM;
+  const int NW = active_warps(total, static_cast<int>(gridDim.x) * nwarps);
+  const int gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  if (gw >= NW) return;                              // no barrier of the block follows
+  const long long u0 = range_start(total, gw, NW);
+  const int count = static_cast<int>(range_start(total, gw + 1, NW) - u0);
+
+  uint8_t* ring = smem + warp * Cfg::WARP;
+  const uint32_t ring_a = smem_u32(ring);
+  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(ring + kStages * Cfg::STAGE);
+  const int row = w.H + 2 * c.Hkv;                   // heads of a token's row
+  const int pmask = (1 << c.page_log2) - 1;
+  const size_t vstep = (static_cast<size_t>(c.Hkv) << c.page_log2) * D;   // from a page's keys to its values
+  const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(c.pool);
+
+  auto set_seq = [&](Unit& x) {                      // the sequence's lengths (b has units)
+    x.nt = s_prefix[x.b + 1] - s_prefix[x.b];
+    x.last = s_len[x.b];
+    x.seen = seen_rows(x.last + 1, w.window, w.sinks);
+  };
+  auto advance = [&](Unit& x) {
+    if (++x.tile < x.nt) return;
+    x.tile = 0;
+    if (++x.hm < HM) return;
+    x.hm = 0;
+    do ++x.b; while (x.b < w.B && s_prefix[x.b + 1] == s_prefix[x.b]);
+    if (x.b < w.B) set_seq(x);
+  };
+  Unit at;                                           // the unit that is computed next
+  {
+    const int target = static_cast<int>(u0 / HM);    // the sequence with prefix[b] <= target < prefix[b + 1]
+    int lo = 0, hi = w.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_prefix[mid + 1] > target) hi = mid;
+      else lo = mid + 1;
+    }
+    at.b = lo;
+    set_seq(at);
+    const long long r = u0 - static_cast<long long>(s_prefix[lo]) * HM;
+    at.hm = static_cast<int>(r / at.nt);
+    at.tile = static_cast<int>(r - static_cast<long long>(at.hm) * at.nt);
+  }
+  Unit next = at;                                    // the unit whose rows are copied next
+  int page = -1;                                     // its row's page, this lane
+  auto look_up = [&]() {
+    const int v = next.tile * kUnit + lane;
+    page = -1;
+    if (v < next.seen.n)
+      page = __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (seen_row(next.seen, v) >> c.page_log2));
+  };
+  int issued = 0;
+  auto issue = [&]() {                               // copies unit `next` into stage issued % kStages, steps on
+    const int st = issued % kStages;
+    const uint32_t sk = ring_a + st * Cfg::STAGE, sv = sk + Cfg::TILE, sq = sv + Cfg::TILE;
+    const int kh = next.hm / w.mg, g0 = (next.hm - kh * w.mg) * 16;
+    const int v = next.tile * kUnit + lane, r = seen_row(next.seen, v);
+    const __nv_bfloat16* tok = qkv + static_cast<size_t>(next.b) * row * D;
+    const __nv_bfloat16* kp = pool;
+    size_t dv = vstep;
+    bool ok = v < next.seen.n;
+    if (ok && r == next.last) {                      // the new token's own row comes from qkv
+      kp = tok + static_cast<size_t>(w.H + kh) * D;
+      dv = static_cast<size_t>(c.Hkv) * D;
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.pages)) record_error(err, GPT_DEV_EPAGE);
+    } else if (ok) {
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(c.pages)) {
+        kp = pool + row_at(c, page, 0, kh, r & pmask) * D;
+      } else {
+        ok = false;
+        record_error(err, GPT_DEV_EPAGE);
+      }
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) masks[st] = mask;
+    const unsigned long long ka = reinterpret_cast<unsigned long long>(kp);
+    const unsigned long long va = reinterpret_cast<unsigned long long>(kp + (ok ? dv : 0));
+    const int u = lane % U;
+#pragma unroll
+    for (int i = 0; i < kUnit / RPI; ++i) {
+      const int rr = i * RPI + lane / U;
+      const bool have = (mask >> rr) & 1u;
+      const unsigned long long k = __shfl_sync(0xffffffffu, ka, rr), x = __shfl_sync(0xffffffffu, va, rr);
+      cp_async16(sk + tile_at<D>(rr, u), reinterpret_cast<const uint8_t*>(k) + 16 * u, have);
+      cp_async16(sv + tile_at<D>(rr, u), reinterpret_cast<const uint8_t*>(x) + 16 * u, have);
+    }
+    if (issued == 0 || next.tile == 0) {             // a segment starts: its queries (rows past the group: zeros)
+      const int gn = min(w.G - g0, 16);
+#pragma unroll
+      for (int i = 0; i < (QR + RPI - 1) / RPI; ++i) {
+        const int rr = i * RPI + lane / U;
+        if (rr < QR)
+          cp_async16(sq + tile_at<D>(rr, u), tok + static_cast<size_t>(kh * w.G + g0 + min(rr, gn - 1)) * D + 8 * u, rr < gn);
+      }
+    }
+    ++issued;
+    advance(next);
+  };
+  look_up();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (issued < count) {
+      issue();
+      if (issued < count) look_up();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  constexpr int NT = D / 8;                          // 8-column output tiles
+  float o[NT][4];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // rows lane / 4 and lane / 4 + 8
+  uint32_t qf[D / 16][4];
+  int piece0 = 0;                                    // the segment's first unit in this warp's range
+  const int qrow = lane >> 2, qcol = 2 * (lane & 3);
+  for (int n = 0; n < count; ++n) {
+    if (issued < count) {
+      issue();
+      if (issued < count) look_up();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+    const int st = n % kStages;
+    const uint32_t sk = ring_a + st * Cfg::STAGE, sv = sk + Cfg::TILE, sq = sv + Cfg::TILE;
+    const uint32_t mask = masks[st];
+    const int kh = at.hm / w.mg, g0 = (at.hm - kh * w.mg) * 16, gn = min(w.G - g0, 16);
+    if (n == 0 || at.tile == 0) {
+      piece0 = n;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+      // A operand: matrices rows 0-7 / 8-15 (units 2 k, 2 k + 1 of the 16 columns)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        if constexpr (QR == 16) {
+          uint32_t f[4];
+          ldmatrix4(f, sq + tile_at<D>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)));
+          qf[k][0] = f[0]; qf[k][1] = f[1]; qf[k][2] = f[2]; qf[k][3] = f[3];
+        } else {
+          if ((k & 1) == 0) {                        // units 2 k .. 2 k + 3 of rows 0-7: two steps at once
+            uint32_t f[4];
+            ldmatrix4(f, sq + tile_at<D>(lane & 7, 2 * k + (lane >> 3)));
+            qf[k][0] = f[0]; qf[k][1] = 0u; qf[k][2] = f[1]; qf[k][3] = 0u;
+            qf[k + 1][0] = f[2]; qf[k + 1][1] = 0u; qf[k + 1][2] = f[3]; qf[k + 1][3] = 0u;
+          }
+        }
+      }
+    }
+    // scores of 32 rows: four 8-column tiles
+    float s[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[j][i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t f[4];
+        ldmatrix4(f, sk + tile_at<D>(8 * j + (lane & 7), 4 * k + (lane >> 3)));
+        mma_16816(s[j], qf[2 * k], f[0], f[1]);
+        mma_16816(s[j], qf[2 * k + 1], f[2], f[3]);
+      }
+    }
+    constexpr int RH = QR == 16 ? 2 : 1;             // row halves in use
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 2 * RH; ++i)
+        s[j][i] = (mask >> (8 * j + qcol + (i & 1))) & 1u ? s[j][i] * w.scale_log2 : -INFINITY;
+    if (ws.score != nullptr) {
+#pragma unroll
+      for (int rh = 0; rh < RH; ++rh) {
+        const int g = g0 + qrow + 8 * rh;
+        if (qrow + 8 * rh < gn) {
+          float* dst = ws.score + (static_cast<size_t>(at.b) * w.H + kh * w.G + g) * ws.score_ld + at.tile * kUnit + qcol;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(s[j][2 * rh], s[j][2 * rh + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int rh = 0; rh < RH; ++rh) {
+      float mx = m[rh];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx = fmax3(mx, s[j][2 * rh], s[j][2 * rh + 1]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float ref = mx == -INFINITY ? 0.0f : mx;   // nothing seen so far (bad pages): every term is 2^-inf
+      const float a = ex2_approx(m[rh] - ref);
+      m[rh] = mx;
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[j][2 * rh] = ex2_approx(s[j][2 * rh] - ref);
+        s[j][2 * rh + 1] = ex2_approx(s[j][2 * rh + 1] - ref);
+        sum += s[j][2 * rh] + s[j][2 * rh + 1];
+      }
+      l[rh] = l[rh] * a + sum;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        o[j][2 * rh] *= a;
+        o[j][2 * rh + 1] *= a;
+      }
+    }
+    // O += P U: two steps of 16 rows
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t p[4];
+      p[0] = pack_bf16x2(s[2 * k][0], s[2 * k][1]);
+      p[2] = pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]);
+      p[1] = RH == 2 ? pack_bf16x2(s[2 * k][2], s[2 * k][3]) : 0u;
+      p[3] = RH == 2 ? pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3]) : 0u;
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) {
+        uint32_t f[4];
+        ldmatrix4_trans(f, sv + tile_at<D>(16 * k + (lane & 15), 2 * j + (lane >> 4)));
+        mma_16816(o[2 * j], p, f[0], f[1]);
+        mma_16816(o[2 * j + 1], p, f[2], f[3]);
+      }
+    }
+    const bool ends = at.tile == at.nt - 1;
+    if (ends && g0 == 0) {                           // the sequence's newest row: into the cache
+      const int pg = __ldg(c.table + static_cast<size_t>(at.b) * c.max_pages + (at.last >> c.page_log2));
+      if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages) && lane < 2 * U) {
+        const int which = lane / U, u = lane % U;
+        const __nv_bfloat16* src = qkv + (static_cast<size_t>(at.b) * row + w.H + which * c.Hkv + kh) * D;
+        reinterpret_cast<uint4*>(c.pool)[row_at(c, pg, which, kh, at.last & pmask) * U + u] =
+            __ldg(reinterpret_cast<const uint4*>(src) + u);
+        if (c.weight && lane == 0) c.weight[weight_at(c, pg, kh, at.last & pmask)] = 0.0f;   // summed up by the join
+      }
+    }
+    if (ends || n == count - 1) {                    // the piece is done
+      const bool whole = ends && piece0 + at.nt == n + 1;   // it holds all of the segment's units
+      const size_t slot = static_cast<size_t>(gw) * 2 + (piece0 == 0 ? 0 : 1);
+#pragma unroll
+      for (int rh = 0; rh < RH; ++rh) {
+        float lt = l[rh];
+        lt += __shfl_xor_sync(0xffffffffu, lt, 1);
+        lt += __shfl_xor_sync(0xffffffffu, lt, 2);
+        const int r = qrow + 8 * rh;
+        if (r >= gn) continue;
+        if (whole) {
+          const size_t head = static_cast<size_t>(at.b) * w.H + kh * w.G + g0 + r;
+          const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<uint32_t*>(y + head * D + 8 * j + qcol) = pack_bf16x2(o[j][2 * rh] * inv, o[j][2 * rh + 1] * inv);
+          if ((lane & 3) == 0) {
+            const float v = m[rh] + log2f(lt);
+            ws.lse[head] = v;
+            if (lse2) lse2[head] = v;
+          }
+        } else {
+          float* dst = ws.o + (slot * QR + r) * D + qcol;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][2 * rh], o[j][2 * rh + 1]);
+          if ((lane & 3) == 0) ws.ml[slot * QR + r] = make_float2(m[rh], lt);
+        }
+      }
+    }
+    advance(at);
+    __syncwarp();                                    // the stage is read before it is filled again
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Joins the partial results of a (sequence, key head), and adds the attention weights of its seen rows: block
+// (key head, z, sequence) takes rows z kJoinRows, + kJoinRows, then on in steps of the grid; blocks z > 0 only that.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 1024;
+
+template <int D, int QR>
+__global__ void __launch_bounds__(kJoinThreads)
+paged_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16* __restrict__ y, float* __restrict__ lse2,
+                  DecShape w, DecScratch ws, int warps, int* err) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int P = kJoinThreads / D;                // pieces summed side by side
+  __shared__ float s_lse[kPagedMaxGroup];
+  __shared__ float s_o[P][D];
+  const int kh = blockIdx.x, b = blockIdx.z;
+  const int p0 = ws.prefix[b], nt = ws.prefix[b + 1] - p0;
+  if (nt == 0 || (blockIdx.y > 0 && static_cast<long long>(blockIdx.y) * kJoinRows >= static_cast<long long>(nt) * kUnit)) return;
+  const int HM = c.Hkv * w.mg;
+  const long long total = static_cast<long long>(ws.prefix[w.B]) * HM;
+  const int NW = active_warps(total, warps);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int mt = 0; mt < w.mg; ++mt) {
+    const long long t0 = static_cast<long long>(p0) * HM + static_cast<long long>(kh * w.mg + mt) * nt, t1 = t0 + nt;
+    int g1 = static_cast<int>(t0 * NW / total);      // the warp that holds the first unit
+    while (range_start(total, g1, NW) > t0) --g1;
+    while (range_start(total, g1 + 1, NW) <= t0) ++g1;
+    int g2 = static_cast<int>((t1 - 1) * NW / total);   // and the last
+    while (range_start(total, g2, NW) > t1 - 1) --g2;
+    while (range_start(total, g2 + 1, NW) <= t1 - 1) ++g2;
+    const int gn = min(w.G - mt * 16, 16);
+    const size_t head0 = static_cast<size_t>(b) * w.H + kh * w.G + mt * 16;
+    // a piece is its warp's first (slot 0) unless its segment starts behind the warp's start: only g1's can
+    const size_t slot1 = static_cast<size_t>(g1) * 2 + (range_start(total, g1, NW) == t0 ? 0 : 1);
+    auto slot_of = [&](int g) { return g == g1 ? slot1 : static_cast<size_t>(g) * 2; };
+    if (g1 == g2) {                                  // one warp held it all and wrote the output
+      if (tid < gn) s_lse[mt * 16 + tid] = ws.lse[head0 + tid];
+      __syncthreads();
+      continue;
+    }
+    for (int r = warp; r < gn; r += kJoinThreads / 32) {   // log-sum-exp: one warp per row
+      float mx = -INFINITY;
+      for (int g = g1 + lane; g <= g2; g += 32) mx = fmaxf(mx, ws.ml[slot_of(g) * QR + r].x);
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+      float lt = 0.0f;
+      for (int g = g1 + lane; g <= g2; g += 32) {
+        const float2 x = ws.ml[slot_of(g) * QR + r];
+        if (x.x != -INFINITY) lt += x.y * exp2f(x.x - mx);
+      }
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+      if (lane == 0) s_lse[mt * 16 + r] = mx + log2f(lt);
+    }
+    __syncthreads();
+    if (blockIdx.y > 0) continue;
+    const int d = tid % D, part = tid / D;
+    for (int r = 0; r < gn; ++r) {
+      const float lse = s_lse[mt * 16 + r];
+      float acc = 0.0f;
+#pragma unroll 4
+      for (int g = g1 + part; g <= g2; g += P) {
+        const size_t sl = slot_of(g) * QR + r;
+        const float m = ws.ml[sl].x;
+        const float x = ws.o[sl * D + d];
+        acc = fmaf(x, m == -INFINITY ? 0.0f : exp2f(m - lse), acc);
+      }
+      s_o[part][d] = acc;
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int k = 1; k < P; ++k) acc += s_o[k][d];
+        y[(head0 + r) * D + d] = __float2bfloat16(acc);
+        if (lse2 && d == 0) lse2[head0 + r] = lse;
+      }
+      __syncthreads();
+    }
+  }
+  if (ws.score == nullptr) return;
+  const int last = __ldg(lens + b);
+  const Seen sn = seen_rows(last + 1, w.window, w.sinks);
   const int pmask = (1 << c.page_log2) - 1;
   const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
-  __nv_bfloat16* pool = static_cast<__nv_bfloat16*>(c.pool);
-  const __nv_bfloat16* tok = qkv + static_cast<size_t>(b) * (H + 2 * c.Hkv) * D;
-  if (threadIdx.x < 2 * D) {                         // the token's own row
-    const int which = threadIdx.x / D, d = threadIdx.x % D;
-    const int pg = page_of(c, trow, last, err);
-    if (pg >= 0) pool[row_at(c, pg, which, h, last & pmask) * D + d] = tok[(H + which * c.Hkv + h) * D + d];
-    if (pg >= 0 && c.weight && threadIdx.x == 0) c.weight[weight_at(c, pg, h, last & pmask)] = 0.0f;
-  }
-  __syncthreads();
-  const Seen sn = seen_rows(last + 1, window, sinks);
-  auto score = [&](int pg, int r) {
-    const __nv_bfloat16* k = pool + row_at(c, pg, 0, h, r & pmask) * D;
-    float s = 0.0f;
-    for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(k[d]), sq[d], s);
-    return s * scale_log2;
-  };
-  for (int g = 0; g < G; ++g) {
-    const int head = h * G + g;
-    if (threadIdx.x < D) sq[threadIdx.x] = __bfloat162float(tok[head * D + threadIdx.x]);
-    __syncthreads();
-    float m = -INFINITY, l = 0.0f, o[CPL] = {};
-    for (int v0 = warp * 32; v0 < sn.n; v0 += kDecWarps * 32) {
-      const int v = v0 + lane;
-      int pg = -1, r = 0;
-      if (v < sn.n) {
-        r = seen_row(sn, v);
-        pg = page_of(c, trow, r, err);
-      }
-      const float s = pg >= 0 ? score(pg, r) : -INFINITY;
-      float mx = s;
-      for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-      const float mn = fmaxf(m, mx);
-      if (mn == -INFINITY) continue;
-      const float a = exp2f(m - mn), p = exp2f(s - mn);
-      m = mn;
-      float ps = p;
-      for (int k = 16; k > 0; k >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, k);
-      l = l * a + ps;
-      for (int k = 0; k < CPL; ++k) o[k] *= a;
-      for (int i = 0; i < 32; ++i) {
-        const float pi = __shfl_sync(0xffffffffu, p, i);
-        const int pgi = __shfl_sync(0xffffffffu, pg, i), ri = __shfl_sync(0xffffffffu, r, i);
-        if (pgi < 0) continue;
-        const __nv_bfloat16* u = pool + row_at(c, pgi, 1, h, ri & pmask) * D + lane * CPL;
-        for (int k = 0; k < CPL; ++k) o[k] = fmaf(pi, __bfloat162float(u[k]), o[k]);
-      }
+  const float* score = ws.score + (static_cast<size_t>(b) * w.H + kh * w.G) * ws.score_ld;
+  for (long long v0 = static_cast<long long>(blockIdx.y) * kJoinRows; v0 < sn.n; v0 += static_cast<long long>(gridDim.y) * kJoinRows) {
+    for (int i = tid; i < kJoinRows && v0 + i < sn.n; i += kJoinThreads) {
+      const int v = static_cast<int>(v0) + i;
+      float sum = 0.0f;
+      for (int r = 0; r < w.G; ++r) sum += exp2f(score[static_cast<size_t>(r) * ws.score_ld + v] - s_lse[r]);
+      const int row = seen_row(sn, v);
+      const int pg = page_of(c, trow, row, err);
+      // atomic: sequences may share a page (each adds to a row once, so a page of one sequence has one order)
+      if (pg >= 0) atomicAdd(c.weight + weight_at(c, pg, kh, row & pmask), sum);
     }
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-    for (int k = 0; k < CPL; ++k) so[warp][lane * CPL + k] = o[k];
-    __syncthreads();
-    float mt = -INFINITY, lt = 0.0f;
-    for (int w = 0; w < kDecWarps; ++w) mt = fmaxf(mt, sm[w]);
-    for (int w = 0; w < kDecWarps; ++w) lt += sm[w] == -INFINITY ? 0.0f : sl[w] * exp2f(sm[w] - mt);
-    if (threadIdx.x < D) {
-      float a = 0.0f;
-      for (int w = 0; w < kDecWarps; ++w) a += sm[w] == -INFINITY ? 0.0f : so[w][threadIdx.x] * exp2f(sm[w] - mt);
-      y[(static_cast<size_t>(b) * H + head) * D + threadIdx.x] = __float2bfloat16(lt > 0.0f ? a / lt : 0.0f);
-    }
-    const float lse = mt + log2f(lt);
-    if (lse2 && threadIdx.x == 0) lse2[static_cast<size_t>(b) * H + head] = lse;
-    if (c.weight && lt > 0.0f) {
-      for (int v = threadIdx.x; v < sn.n; v += kDecWarps * 32) {
-        const int r = seen_row(sn, v);
-        const int pg = page_of(c, trow, r, err);
-        // added atomically: sequences may share a page (the sum of a page of one sequence has a fixed order)
-        if (pg >= 0) atomicAdd(c.weight + weight_at(c, pg, h, r & pmask), exp2f(score(pg, r) - lse));
-      }
-    }
-    __syncthreads();
   }
 }
 
@@ -328,17 +724,70 @@ cudaError_t launch_paged_store(const PagedCache& c, const void* qkv, const int32
   return launch_k(paged_store_kernel<32>, grid, dim3(256), 0, s, c, x, start, count, T, H, err);
 }
 
+namespace {
+
+template <int D, int QR>
+cudaError_t launch_decode(const PagedCache& c, const __nv_bfloat16* qkv, const int32_t* lens, __nv_bfloat16* y, float* lse2,
+                          DecShape w, int* err, cudaStream_t s) {
+  using Cfg = DecCfg<D, QR>;
+  int dev = 0, num_sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // one block per SM with as many warps (rings) as its shared memory holds beside the lists, 8 at most
+  const size_t lists = (2 * static_cast<size_t>(w.B) + 1) * sizeof(int);
+  const size_t room = 232448 - 256 - lists;
+  const int warps = room / Cfg::WARP < 8 ? static_cast<int>(room / Cfg::WARP) : 8;
+  const size_t smem = static_cast<size_t>(warps) * Cfg::WARP + lists;
+  e = cudaFuncSetAttribute(paged_split_kernel<D, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int NW = num_sms * warps;
+  long long seen_max = static_cast<long long>(c.max_pages) << c.page_log2;
+  if (w.window > 0 && static_cast<long long>(w.window) + w.sinks < seen_max) seen_max = w.window + w.sinks;
+  const int score_ld = static_cast<int>((seen_max + kUnit - 1) / kUnit * kUnit);
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t pre_b = up((w.B + 1) * sizeof(int)), o_b = up(static_cast<size_t>(NW) * 2 * QR * D * sizeof(float)),
+               ml_b = up(static_cast<size_t>(NW) * 2 * QR * sizeof(float2)), lse_b = up(static_cast<size_t>(w.B) * w.H * sizeof(float)),
+               sc_b = c.weight ? static_cast<size_t>(w.B) * w.H * score_ld * sizeof(float) : 0;
+  uint8_t* p = nullptr;
+  e = scratch_alloc(reinterpret_cast<void**>(&p), pre_b + o_b + ml_b + lse_b + sc_b, s);
+  if (e != cudaSuccess) return e;
+  DecScratch ws;
+  ws.prefix = reinterpret_cast<int*>(p);
+  ws.o = reinterpret_cast<float*>(p + pre_b);
+  ws.ml = reinterpret_cast<float2*>(p + pre_b + o_b);
+  ws.lse = reinterpret_cast<float*>(p + pre_b + o_b + ml_b);
+  ws.score = c.weight ? reinterpret_cast<float*>(p + pre_b + o_b + ml_b + lse_b) : nullptr;
+  ws.score_ld = score_ld;
+  e = launch_k(paged_split_kernel<D, QR>, dim3(num_sms), dim3(32 * warps), smem, s, c, qkv, lens, y, lse2, w, ws, err);
+  if (e == cudaSuccess) {
+    const long long chunks = c.weight ? (seen_max + kJoinRows - 1) / kJoinRows : 1;
+    e = launch_k(paged_join_kernel<D, QR>,
+                 dim3(static_cast<unsigned>(c.Hkv), static_cast<unsigned>(chunks < 65535 ? chunks : 65535), static_cast<unsigned>(w.B)),
+                 dim3(kJoinThreads), 0, s, c, lens, y, lse2, w, ws, NW, err);
+  }
+  const cudaError_t f = scratch_free(p, s);
+  return e != cudaSuccess ? e : f;
+}
+
+}  // namespace
+
 cudaError_t launch_paged_attention(const PagedCache& c, const void* qkv, const int32_t* lens, void* y, float* lse2,
                                    int B, int H, int D, int window, int sinks, int* err, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(c.Hkv), static_cast<unsigned>(B));
-  const float sc = kLog2e / sqrtf(static_cast<float>(D));
+  DecShape w;
+  w.B = B;
+  w.H = H;
+  w.G = H / c.Hkv;
+  w.mg = (w.G + 15) / 16;
+  w.window = window;
+  w.sinks = sinks;
+  w.scale_log2 = kLog2e / sqrtf(static_cast<float>(D));
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(qkv);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(y);
+  // up to 8 query heads per key head need half of the 16 query rows in shared memory and registers
   if (D == 64)
-    return launch_k(paged_attention_kernel<64>, grid, dim3(kDecWarps * 32), 0, s, c, x, lens, o, lse2, H, window, sinks,
-                    sc, err);
-  return launch_k(paged_attention_kernel<32>, grid, dim3(kDecWarps * 32), 0, s, c, x, lens, o, lse2, H, window, sinks,
-                  sc, err);
+    return w.G <= 8 ? launch_decode<64, 8>(c, x, lens, o, lse2, w, err, s) : launch_decode<64, 16>(c, x, lens, o, lse2, w, err, s);
+  return w.G <= 8 ? launch_decode<32, 8>(c, x, lens, o, lse2, w, err, s) : launch_decode<32, 16>(c, x, lens, o, lse2, w, err, s);
 }
 
 cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const int32_t* dst_table, int dst_max_pages,

@@ -216,11 +216,17 @@ cudaError_t launch_set_int(int* p, int v, cudaStream_t s);
 constexpr int kSampleMaxV = 55296;
 cudaError_t launch_sample(const float* logits, int B, int V, float temperature, int top_k, float top_p,
                           const float* uniform, int32_t* out, cudaStream_t s);
+// Scratch on a stream from a pool that the library keeps per device (gptk.cu): as cudaMallocAsync / cudaFreeAsync,
+// but freed memory stays with the library, so that a call after a synchronisation does not map it anew.
+cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t s);
+cudaError_t scratch_free(void* p, cudaStream_t s);
+
 // ---- paged key/value cache (bf16; k_paged.cu)
 // pool [pages][2][Hkv][page][D]: per page the keys of every key head, then the values; row r of sequence b
 // lies in page table[b][r / page] at slot r % page, page = 1 << page_log2. weight (nullable) fp32
 // [pages][Hkv][page]: one running sum of attention weight per cached row and key head.
-constexpr int kPagedMaxB = 8192;
+constexpr int kPagedMaxB = 8192;       // sequences of a call (their lengths are held in shared memory)
+constexpr int kPagedMaxGroup = 128;    // query heads per key head of paged attention
 struct PagedCache {
   void* pool;
   float* weight;

@@ -163,7 +163,7 @@ int gptk_lmhead_ce_noalloc(const void* h, const void* wte, const int32_t* target
  *   weight  [pages][Hkv][page] fp32 or NULL: per cached row and key head, the attention weight it has received
  *   table   [B][max_pages] int32: row r of sequence b lies in page table[b][r / page] at slot r % page
  * page is a power of two, 8..256. H query heads share Hkv key heads (H a multiple of Hkv): query head h reads key
- * head h / (H / Hkv). A token's qkv row holds H D queries, Hkv D keys, Hkv D values, as the output of one product.
+ * head h / (H / Hkv), H / Hkv <= 128 for the attention. A token's qkv row holds H D queries, Hkv D keys, Hkv D values, as the output of one product.
  * All arrays are device memory of the current device, pool, qkv and y 16-byte aligned. B <= 8192.
  * GPT_EINVAL: null pointers or sizes; GPT_ECONFIG: D, H % Hkv or alignment. Checked on the device: a page number
  * outside [0, pages) or a row past max_pages * page is neither read nor written, and gptk_status() then returns
@@ -184,7 +184,10 @@ int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* 
  *   y[b, h] = sum_r a_r u_r,  a = softmax(q_h . k_r / sqrt(D))     bf16 [B, H D]
  *   lse2[b, h] = log2 sum_r 2^(q_h . k_r log2(e) / sqrt(D))         fp32 [B, H], NULL: not wanted
  *   weight(r, key head) += the sum of a_r over the head's H / Hkv queries (r < n); = that sum for row n
- * lens[b] < 0: no sequence; nothing of row b is read or written. The caller counts lens up (one cache per layer
+ * lens[b] < 0: no sequence; nothing of row b is read or written. B max_pages page / 32 < 2^31, and times Hkv
+ * <= 2^40 (GPT_EINVAL otherwise). Scratch (about 10 MB at most, and with weights 4 bytes per query head and seen row
+ * that the table has room for) is taken on the stream from a pool that the library keeps; make a process's first call
+ * before any stream capture. The caller counts lens up (one cache per layer
  * shares one lens). Sequences may share the pages of rows below their own; the new rows' pages are their own. fp32
  * scores and sums; the probabilities are rounded to bf16 for the product with the values.
  */

@@ -67,7 +67,8 @@ def test_attention_arguments(lib):
     from decoder_only_transformer_gpt_gb300 import binding
     for bad in (dict(qkv=None), dict(lens=None), dict(y=None), dict(H=0), dict(window=-1), dict(sinks=-1)):
         assert _attend(lib, **bad) == binding.GPT_EINVAL, bad
-    for bad in (dict(H=5), dict(qkv=ODD), dict(y=ODD)):
+    assert _attend(lib, B=8192, max_pages=1 << 26, page=16) == binding.GPT_EINVAL
+    for bad in (dict(H=5), dict(qkv=ODD), dict(y=ODD), dict(H=258)):
         assert _attend(lib, **bad) == binding.GPT_ECONFIG, bad
 
 
