@@ -364,80 +364,105 @@ def lmhead_ce_noalloc(h, wte, targets, nll, err=None, stream=None):
                                       _stream(stream)), "gptk_lmhead_ce_noalloc")
 
 
-def _take(name: str, t, dtype, shape) -> None:
-    """Refuse a tensor whose type, shape, layout or device the kernels cannot take (shape: None for any extent)."""
-    import torch
-    if t.dtype != dtype:
+# The operators below are called per layer and token, so their checks are kept to attribute reads (about 0.4 us a
+# tensor; 8 us of the call's host time went to them and the stream object in a first form).
+
+_torch = None
+
+
+def _cuda(stream):
+    """(torch, the current device's index, the stream to launch on as an integer)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if not _torch.cuda.is_initialized():             # no tensor can be on a GPU yet
+        return _torch, 0, 0
+    dev = _torch.cuda.current_device()
+    return _torch, dev, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _refuse(name: str, t, dtype, shape, dev) -> None:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, needs {dtype}")
-    if len(t.shape) != len(shape) or any(e is not None and e != n for e, n in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {tuple('any' if e is None else e for e in shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, needs the current CUDA device")
+    raise ValueError(f"{name}: on {t.device}, needs the current CUDA device")
+
+
+def _arg(name: str, t, dtype, shape, dev) -> int:
+    """The address of a tensor whose type, shape, layout and device the kernels can take; ValueError otherwise."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
 def _qkv_dims(qkv, H: int, Hkv: int):
     """(B, T, D) of fused rows [B, T, (H + 2 Hkv) D]."""
-    if qkv.dim() != 3 or H < 1 or Hkv < 1 or qkv.shape[2] % (H + 2 * Hkv):
-        raise ValueError(f"qkv: shape {tuple(qkv.shape)}, needs [B, T, (H + 2 Hkv) D] for H = {H}, Hkv = {Hkv}")
-    B, T, row = qkv.shape
+    shape = qkv.shape
+    if len(shape) != 3 or H < 1 or Hkv < 1 or shape[2] % (H + 2 * Hkv):
+        raise ValueError(f"qkv: shape {tuple(shape)}, needs [B, T, (H + 2 Hkv) D] for H = {H}, Hkv = {Hkv}")
+    B, T, row = shape
     return B, T, row // (H + 2 * Hkv)
 
 
 def attention_window(qkv, y, H: int, Hkv: int, window: int, sinks: int = 0, lse2=None, stream=None):
     """Causal attention over the last `window` keys and the first `sinks`: qkv [B, T, (H + 2 Hkv) D] -> y [B, T, H D];
     lse2 [B, H, T] (optional, needed by the derivative) takes each row's base-2 log-sum-exp."""
-    import torch
-    lib = load()
+    lib = _LIB or load()
+    torch, dev, s = _cuda(stream)
     B, T, D = _qkv_dims(qkv, H, Hkv)
-    _take("qkv", qkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D))
-    _take("y", y, torch.bfloat16, (B, T, H * D))
-    if lse2 is not None:
-        _take("lse2", lse2, torch.float32, (B, H, T))
-    _check(lib.gptk_attention_window(_ptr(qkv), _ptr(y), _ptr(lse2), B, T, H, Hkv, D, window, sinks, _stream(stream)),
-           "gptk_attention_window")
+    bf16 = torch.bfloat16
+    rc = lib.gptk_attention_window(_arg("qkv", qkv, bf16, (B, T, (H + 2 * Hkv) * D), dev),
+                                   _arg("y", y, bf16, (B, T, H * D), dev),
+                                   None if lse2 is None else _arg("lse2", lse2, torch.float32, (B, H, T), dev),
+                                   B, T, H, Hkv, D, window, sinks, s)
+    if rc:
+        _check(rc, "gptk_attention_window")
 
 
 def attention_window_bwd(qkv, y, dy, lse2, dqkv, H: int, Hkv: int, window: int, sinks: int = 0, stream=None):
     """dqkv of attention_window from its input, output, log-sum-exp and the output's gradient dy [B, T, H D]."""
-    import torch
-    lib = load()
+    lib = _LIB or load()
+    torch, dev, s = _cuda(stream)
     B, T, D = _qkv_dims(qkv, H, Hkv)
-    _take("qkv", qkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D))
-    _take("y", y, torch.bfloat16, (B, T, H * D))
-    _take("dy", dy, torch.bfloat16, (B, T, H * D))
-    _take("lse2", lse2, torch.float32, (B, H, T))
-    _take("dqkv", dqkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D))
-    _check(lib.gptk_attention_window_bwd(_ptr(qkv), _ptr(y), _ptr(dy), _ptr(lse2), _ptr(dqkv), B, T, H, Hkv, D, window,
-                                         sinks, _stream(stream)), "gptk_attention_window_bwd")
+    bf16, rows, out = torch.bfloat16, (B, T, (H + 2 * Hkv) * D), (B, T, H * D)
+    rc = lib.gptk_attention_window_bwd(_arg("qkv", qkv, bf16, rows, dev), _arg("y", y, bf16, out, dev),
+                                       _arg("dy", dy, bf16, out, dev),
+                                       _arg("lse2", lse2, torch.float32, (B, H, T), dev),
+                                       _arg("dqkv", dqkv, bf16, rows, dev), B, T, H, Hkv, D, window, sinks, s)
+    if rc:
+        _check(rc, "gptk_attention_window_bwd")
 
 
-def _pool_dims(pool, weight, table):
-    """(pages, Hkv, page, D, B, max_pages) of a paged cache, its tensors checked."""
-    import torch
-    if pool.dim() != 5 or pool.shape[1] != 2:
-        raise ValueError(f"pool: shape {tuple(pool.shape)}, needs [pages, 2, Hkv, page, D]")
-    pages, _, Hkv, page, D = pool.shape
-    _take("pool", pool, torch.bfloat16, (pages, 2, Hkv, page, D))
-    if weight is not None:
-        _take("weight", weight, torch.float32, (pages, Hkv, page))
-    _take("table", table, torch.int32, (None, None))
-    return pages, Hkv, page, D, table.shape[0], table.shape[1]
+def _cache(torch, pool, weight, table, dev):
+    """(pages, Hkv, page, D, B, max_pages, addresses of pool, weight and table) of a paged cache."""
+    shape, tshape = pool.shape, table.shape
+    if len(shape) != 5 or shape[1] != 2:
+        raise ValueError(f"pool: shape {tuple(shape)}, needs [pages, 2, Hkv, page, D]")
+    if len(tshape) != 2:
+        raise ValueError(f"table: shape {tuple(tshape)}, needs [B, max_pages]")
+    pages, _, Hkv, page, D = shape
+    return (pages, Hkv, page, D, tshape[0], tshape[1], _arg("pool", pool, torch.bfloat16, shape, dev),
+            None if weight is None else _arg("weight", weight, torch.float32, (pages, Hkv, page), dev),
+            _arg("table", table, torch.int32, tshape, dev))
 
 
 def paged_store(qkv, pool, table, H: int, start=None, count=None, weight=None, stream=None):
     """Keys and values of qkv [B, T, (H + 2 Hkv) D] into rows start[b] + t (t < count[b]) of the paged cache."""
-    import torch
-    lib = load()
-    pages, Hkv, page, D, B, max_pages = _pool_dims(pool, weight, table)
-    _take("qkv", qkv, torch.bfloat16, (B, None, (H + 2 * Hkv) * D))
-    if start is not None:
-        _take("start", start, torch.int32, (B,))
-    if count is not None:
-        _take("count", count, torch.int32, (B,))
-    _check(lib.gptk_paged_store(_ptr(qkv), _ptr(pool), _ptr(weight), _ptr(table), _ptr(start), _ptr(count), B,
-                                qkv.shape[1], H, Hkv, D, pages, page, max_pages, _stream(stream)), "gptk_paged_store")
+    lib = _LIB or load()
+    torch, dev, s = _cuda(stream)
+    pages, Hkv, page, D, B, max_pages, p, w, tb = _cache(torch, pool, weight, table, dev)
+    i32, shape = torch.int32, qkv.shape
+    T = shape[1] if len(shape) == 3 else 0
+    rc = lib.gptk_paged_store(_arg("qkv", qkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D), dev), p, w, tb,
+                              None if start is None else _arg("start", start, i32, (B,), dev),
+                              None if count is None else _arg("count", count, i32, (B,), dev),
+                              B, T, H, Hkv, D, pages, page, max_pages, s)
+    if rc:
+        _check(rc, "gptk_paged_store")
 
 
 def paged_attention(qkv, pool, table, lens, y, H: int, lse2=None, weight=None, window: int = 0, sinks: int = 0,
@@ -446,33 +471,33 @@ def paged_attention(qkv, pool, table, lens, y, H: int, lse2=None, weight=None, w
 
     window 0 sees every cached row, else the last `window` rows and the first `sinks`; weight (optional) sums
     each row's attention weight, lse2 [B, H] (optional) takes the log-sum-exp. lens[b] < 0 skips row b."""
-    import torch
-    lib = load()
-    pages, Hkv, page, D, B, max_pages = _pool_dims(pool, weight, table)
-    _take("qkv", qkv, torch.bfloat16, (B, (H + 2 * Hkv) * D))
-    _take("lens", lens, torch.int32, (B,))
-    _take("y", y, torch.bfloat16, (B, H * D))
-    if lse2 is not None:
-        _take("lse2", lse2, torch.float32, (B, H))
-    _check(lib.gptk_paged_attention(_ptr(qkv), _ptr(pool), _ptr(weight), _ptr(table), _ptr(lens), _ptr(y), _ptr(lse2), B,
-                                    H, Hkv, D, pages, page, max_pages, window, sinks, _stream(stream)),
-           "gptk_paged_attention")
+    lib = _LIB or load()
+    torch, dev, s = _cuda(stream)
+    pages, Hkv, page, D, B, max_pages, p, w, tb = _cache(torch, pool, weight, table, dev)
+    bf16 = torch.bfloat16
+    rc = lib.gptk_paged_attention(_arg("qkv", qkv, bf16, (B, (H + 2 * Hkv) * D), dev), p, w, tb,
+                                  _arg("lens", lens, torch.int32, (B,), dev), _arg("y", y, bf16, (B, H * D), dev),
+                                  None if lse2 is None else _arg("lse2", lse2, torch.float32, (B, H), dev),
+                                  B, H, Hkv, D, pages, page, max_pages, window, sinks, s)
+    if rc:
+        _check(rc, "gptk_paged_attention")
 
 
 def paged_evict(pool, weight, table, lens, dst_table, new_lens, kept, budget: int, sinks: int = 0, recent: int = 0,
                 stream=None):
     """Keep budget rows per sequence and key head (first `sinks`, last `recent`, largest weights between), in order,
     in the pages of dst_table (`table` itself: in place); kept [B, Hkv, budget] names them, -1 behind the last."""
-    import torch
-    lib = load()
-    pages, Hkv, page, D, B, max_pages = _pool_dims(pool, weight, table)
-    _take("lens", lens, torch.int32, (B,))
-    _take("dst_table", dst_table, torch.int32, (B, None))
-    _take("new_lens", new_lens, torch.int32, (B,))
-    _take("kept", kept, torch.int32, (B, Hkv, budget))
-    _check(lib.gptk_paged_evict(_ptr(pool), _ptr(weight), _ptr(table), _ptr(lens), _ptr(dst_table), _ptr(new_lens),
-                                _ptr(kept), B, Hkv, D, pages, page, max_pages, dst_table.shape[1], budget, sinks, recent,
-                                _stream(stream)), "gptk_paged_evict")
+    lib = _LIB or load()
+    torch, dev, s = _cuda(stream)
+    pages, Hkv, page, D, B, max_pages, p, w, tb = _cache(torch, pool, weight, table, dev)
+    i32, dshape = torch.int32, dst_table.shape
+    dst_pages = dshape[1] if len(dshape) == 2 else 0
+    rc = lib.gptk_paged_evict(p, w, tb, _arg("lens", lens, i32, (B,), dev),
+                              _arg("dst_table", dst_table, i32, (B, dst_pages), dev),
+                              _arg("new_lens", new_lens, i32, (B,), dev), _arg("kept", kept, i32, (B, Hkv, budget), dev),
+                              B, Hkv, D, pages, page, max_pages, dst_pages, budget, sinks, recent, s)
+    if rc:
+        _check(rc, "gptk_paged_evict")
 
 
 def mean(nll, loss, stream=None):

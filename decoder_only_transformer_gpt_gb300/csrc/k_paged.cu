@@ -55,7 +55,11 @@ __device__ __forceinline__ int seen_row(const Seen& s, int v) { return v < s.hea
 
 // ---------------------------------------------------------------- store
 
-// One thread per 16 bytes of a token's keys and values. Bound by memory: 8 D bytes moved per row and key head.
+// Bound by memory: 8 D bytes moved per row and key head. A block takes 16 tokens of a sequence: their places are
+// looked up once into shared memory, then its threads walk the tokens' 16-byte units, four copies in flight each (one
+// per thread left the loads' latency open: 17.4 us for 16 prompts of up to 1,024 tokens x 12 heads).
+constexpr int kStoreTokens = 16;
+
 template <int D>
 __global__ void __launch_bounds__(256)
 paged_store_kernel(PagedCache c, const uint4* __restrict__ qkv, const int32_t* __restrict__ start,
@@ -63,24 +67,55 @@ paged_store_kernel(PagedCache c, const uint4* __restrict__ qkv, const int32_t* _
   pdl_wait();
   pdl_trigger();
   constexpr int U = D / 8;                           // 16-byte units of a row
-  const int b = blockIdx.y;
-  const int per_tok = 2 * c.Hkv * U;
-  const int n = count ? min(__ldg(count + b), T) : T;
-  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= static_cast<long long>(n) * per_tok) return;
-  const int t = static_cast<int>(i / per_tok), e = static_cast<int>(i - static_cast<long long>(t) * per_tok);
-  const int which = e / (c.Hkv * U), h = (e / U) % c.Hkv, u = e % U;
-  const long long r = (start ? static_cast<long long>(__ldg(start + b)) : 0) + t;
-  if (r < 0 || r >= static_cast<long long>(c.max_pages) << c.page_log2) {
-    record_error(err, GPT_DEV_EPAGE);
-    return;
+  __shared__ long long s_row[kStoreTokens];          // row (of D elements) of the token's key of head 0; -1: nowhere
+  __shared__ long long s_weight[kStoreTokens];
+  const int b = blockIdx.y, t0 = blockIdx.x * kStoreTokens;
+  const int n = (count ? min(__ldg(count + b), T) : T) - t0;          // tokens from t0 on
+  if (n <= 0) return;
+  if (threadIdx.x < kStoreTokens) {
+    long long row = -1, weight = 0;
+    if (threadIdx.x < n) {
+      const long long r = (start ? static_cast<long long>(__ldg(start + b)) : 0) + t0 + threadIdx.x;
+      if (r < 0 || r >= static_cast<long long>(c.max_pages) << c.page_log2) {
+        record_error(err, GPT_DEV_EPAGE);
+      } else {
+        const int pg = page_of(c, c.table + static_cast<size_t>(b) * c.max_pages, static_cast<int>(r), err);
+        const int slot = static_cast<int>(r) & ((1 << c.page_log2) - 1);
+        if (pg >= 0) {
+          row = static_cast<long long>(row_at(c, pg, 0, 0, slot));
+          weight = static_cast<long long>(weight_at(c, pg, 0, slot));
+        }
+      }
+    }
+    s_row[threadIdx.x] = row;
+    s_weight[threadIdx.x] = weight;
   }
-  const int pg = page_of(c, c.table + static_cast<size_t>(b) * c.max_pages, static_cast<int>(r), err);
-  if (pg < 0) return;
-  const int slot = static_cast<int>(r) & ((1 << c.page_log2) - 1);
-  const uint4 v = __ldg(qkv + (static_cast<size_t>(b) * T + t) * (H + 2 * c.Hkv) * U + H * U + e);
-  reinterpret_cast<uint4*>(c.pool)[row_at(c, pg, which, h, slot) * U + u] = v;
-  if (c.weight && which == 0 && u == 0) c.weight[weight_at(c, pg, h, slot)] = 0.0f;
+  __syncthreads();
+  const int per_tok = 2 * c.Hkv * U, all = min(n, kStoreTokens) * per_tok;
+  const uint4* src = qkv + (static_cast<size_t>(b) * T + t0) * (H + 2 * c.Hkv) * U + static_cast<size_t>(H) * U;
+  uint4* pool = reinterpret_cast<uint4*>(c.pool);
+  constexpr int K = 4;
+  for (int i0 = threadIdx.x; i0 < all; i0 += K * 256) {
+    uint4 v[K];
+    long long dst[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = i0 + k * 256, t = i / per_tok, e = i - t * per_tok;   // e: (keys or values, head, unit)
+      dst[k] = -1;
+      if (i < all && s_row[t] >= 0) {
+        v[k] = __ldg(src + static_cast<size_t>(t) * (H + 2 * c.Hkv) * U + e);
+        dst[k] = (s_row[t] + (static_cast<long long>(e / U) << c.page_log2)) * U + e % U;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (dst[k] >= 0) pool[dst[k]] = v[k];
+  }
+  if (c.weight)
+    for (int i = threadIdx.x; i < min(n, kStoreTokens) * c.Hkv; i += 256) {
+      const int t = i / c.Hkv, h = i - t * c.Hkv;
+      if (s_row[t] >= 0) c.weight[s_weight[t] + (static_cast<long long>(h) << c.page_log2)] = 0.0f;
+    }
 }
 
 // ---------------------------------------------------------------- attention of one new token
@@ -588,43 +623,26 @@ __device__ __forceinline__ uint32_t weight_rank(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Two kernels. The first chooses the rows of one (sequence, key head) per block: it turns the weights into ranks in
+// shared memory once (through the table, all loads independent; lists that do not fit are read again by each pass),
+// finds the rank of the smallest kept weight by three passes over 11, 11 and 10 bits (a histogram of the rows that
+// agree so far), and writes the kept rows in order: every warp counts its own stretch of rows, then places them
+// behind the stretches before. Equal weights are kept from the lowest row on. The second moves the rows.
 constexpr int kEvThreads = 512;
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvBins = 2048;
 
-// The inclusive prefix sum of x over the block, and the total.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int k = 1; k < 32; k <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, k);
-    if (lane >= k) x += y;
-  }
-  __syncthreads();                                   // the previous scan's sums have been read
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kEvThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    all += warp_sums[w];
-  }
-  *total = all;
-  return x + before;
-}
-
-// One block per (key head, sequence). Selection: the rank of the smallest kept weight by four passes over 8 bits
-// each (a histogram of the rows that agree so far); equal weights are kept from the lowest row on. Then the
-// kept rows' numbers are written in order, and the rows move to the front: row i's source is at or behind i, so
-// a chunk's rows are all read before any of them is written and no later chunk reads what this one wrote.
-template <int D>
 __global__ void __launch_bounds__(kEvThreads)
-paged_evict_kernel(PagedCache c, const int32_t* __restrict__ lens, const int32_t* dst_table, int dst_max_pages,
-                   int32_t* __restrict__ new_lens, int32_t* kept, int budget, int sinks, int recent, int* err) {
+paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __restrict__ new_lens,
+                    int32_t* __restrict__ kept, int budget, int sinks, int recent, int room, int* err) {
   pdl_wait();
   pdl_trigger();
-  constexpr int U = D / 8;
-  __shared__ int hist[256], sums[kEvThreads / 32], pick[2];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  extern __shared__ uint32_t s_rank[];               // [room] ranks of rows sinks, sinks + 1, ..
+  __shared__ int hist[kEvBins];
+  __shared__ int s_sum[kEvWarps], s_tie[kEvWarps], pick[2];
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pmask = (1 << c.page_log2) - 1;
   const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
-  const int32_t* drow = dst_table + static_cast<size_t>(b) * dst_max_pages;
   int32_t* out = kept + (static_cast<size_t>(b) * c.Hkv + h) * budget;
   int n = __ldg(lens + b);
   if (n > static_cast<long long>(c.max_pages) << c.page_log2) {
@@ -634,79 +652,163 @@ paged_evict_kernel(PagedCache c, const int32_t* __restrict__ lens, const int32_t
   const int m = min(n, budget);                      // rows kept
   if (h == 0 && tid == 0) new_lens[b] = m;
   for (int i = max(m, 0) + tid; i < budget; i += kEvThreads) out[i] = -1;
-  if (m <= 0) return;
-  auto rank_of = [&](int r) -> uint32_t {
-    const int pg = page_of(c, trow, r, err);
-    return pg < 0 ? 0u : weight_rank(c.weight[weight_at(c, pg, h, r & pmask)]);
-  };
   if (n <= budget) {
     for (int i = tid; i < m; i += kEvThreads) out[i] = i;
-  } else {
-    const int lo = sinks, hi = n - recent;           // rows chosen by weight: [lo, hi)
-    int want = budget - sinks - recent;              // how many of them
-    uint32_t prefix = 0;                             // the leading bits of the smallest kept rank
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kEvThreads) hist[i] = 0;
-      __syncthreads();
-      for (int r = lo + tid; r < hi; r += kEvThreads) {
-        const uint32_t k = rank_of(r);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int left = want, d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        pick[0] = d;
-        pick[1] = left;                              // still to take among those with this digit
-      }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(pick[0]) << shift;
-      want = pick[1];
-      __syncthreads();
-    }
-    // want rows of rank == prefix are kept (the first ones), and every row of a higher rank
-    const bool any = budget > sinks + recent;
-    int ties = 0, base = 0;
-    for (int r0 = 0; r0 < n; r0 += kEvThreads) {
-      const int r = r0 + tid;
-      bool keep = r < n && (r < lo || r >= hi), tie = false;
-      if (r >= lo && r < hi && any) {
-        const uint32_t k = rank_of(r);
-        keep = k > prefix;
-        tie = k == prefix;
-      }
-      int total;
-      const int ti = block_scan(tie ? 1 : 0, sums, &total);
-      if (tie) keep = ties + ti <= want;
-      ties += total;
-      const int at = block_scan(keep ? 1 : 0, sums, &total);
-      if (keep) out[base + at - 1] = r;
-      base += total;
+    return;
+  }
+  const int lo = sinks, mid = n - recent - sinks;    // rows chosen by weight: lo .. lo + mid - 1
+  int want = budget - sinks - recent;                // how many of them
+  const bool any = want > 0, fits = mid <= room;
+  auto load = [&](int i) -> uint32_t {
+    const int r = lo + i, pg = page_of(c, trow, r, err);
+    return pg < 0 ? 0u : weight_rank(__ldg(c.weight + weight_at(c, pg, h, r & pmask)));
+  };
+  if (any && fits) {
+    constexpr int K = 4;                             // independent loads in flight per thread
+    for (int i0 = tid; i0 < mid; i0 += K * kEvThreads) {
+      uint32_t k[K];
+#pragma unroll
+      for (int j = 0; j < K; ++j) k[j] = i0 + j * kEvThreads < mid ? load(i0 + j * kEvThreads) : 0u;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (i0 + j * kEvThreads < mid) s_rank[i0 + j * kEvThreads] = k[j];
     }
   }
-  __syncthreads();                                   // out[] is read below by other threads of the block
-  constexpr int RPB = kEvThreads / U;                // rows per chunk: one 16-byte unit per thread
-  uint4* pool = static_cast<uint4*>(c.pool);
-  for (int i0 = 0; i0 < m; i0 += RPB) {
-    const int i = i0 + tid / U, u = tid % U;
-    int src = -1, dst = -1, r = 0;
-    uint4 kx, vx;
-    float w = 0.0f;
-    if (i < m) {
-      r = out[i];
-      src = page_of(c, trow, r, err);
-      dst = page_of(c, drow, i, err);
-      if (src >= 0) {
-        kx = pool[row_at(c, src, 0, h, r & pmask) * U + u];
-        vx = pool[row_at(c, src, 1, h, r & pmask) * U + u];
-        if (u == 0) w = c.weight[weight_at(c, src, h, r & pmask)];
-      }
+  auto rank = [&](int i) { return fits ? s_rank[i] : load(i); };
+  uint32_t prefix = 0;                               // the leading bits of the smallest kept rank
+  int low = 32;                                      // bits below them
+  for (int pass = 0; pass < 3 && any; ++pass) {
+    const int bits = pass == 2 ? 10 : 11, shift = low - bits;
+    for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < mid; i += kEvThreads) {
+      const uint32_t k = rank(i);
+      if (low == 32 || (k >> low) == (prefix >> low)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
     }
     __syncthreads();
-    if (src >= 0 && dst >= 0) {
-      pool[row_at(c, dst, 0, h, i & pmask) * U + u] = kx;
-      pool[row_at(c, dst, 1, h, i & pmask) * U + u] = vx;
-      if (u == 0) c.weight[weight_at(c, dst, h, i & pmask)] = w;
+    // the bin where the count from the top reaches `want`: thread t sums bins 4 t .. 4 t + 3
+    constexpr int BPT = kEvBins / kEvThreads;
+    int c4[BPT], own = 0;
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) own += c4[j] = hist[tid * BPT + j];
+    int above = own;                                 // counts of this and the later lanes
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int v = __shfl_down_sync(0xffffffffu, above, k);
+      if (lane + k < 32) above += v;
+    }
+    if (lane == 0) s_sum[warp] = above;
+    __syncthreads();
+    for (int w = warp + 1; w < kEvWarps; ++w) above += s_sum[w];
+    above -= own;                                    // rows in bins behind this thread's
+    if (above < want && above + own >= want) {       // one thread
+      int left = want - above, j = BPT - 1;
+#pragma unroll
+      for (int k = BPT - 1; k > 0; --k)
+        if (j == k && c4[k] < left) { left -= c4[k]; --j; }
+      pick[0] = tid * BPT + j;
+      pick[1] = left;                                // still to take among the rows of that bin
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(pick[0]) << shift;
+    want = pick[1];
+    low = shift;
+  }
+  // kept: every row of a rank above prefix, the first `want` of rank prefix, and the rows outside [lo, lo + mid)
+  const int per = ((n + kEvWarps - 1) / kEvWarps + 31) / 32 * 32;   // rows of a warp's stretch
+  const int first = min(n, warp * per), end = min(n, first + per);
+  auto kind = [&](int r) -> int {                    // 2 kept, 1 of rank prefix, 0 gone
+    const int i = r - lo;
+    if (r >= end) return 0;
+    if (i < 0 || i >= mid) return 2;
+    if (!any) return 0;
+    const uint32_t k = rank(i);
+    return k > prefix ? 2 : (k == prefix ? 1 : 0);
+  };
+  int sure = 0, ties = 0;
+  for (int r0 = first; r0 < end; r0 += 32) {
+    const int k = kind(r0 + lane);
+    sure += __popc(__ballot_sync(0xffffffffu, k == 2));
+    ties += __popc(__ballot_sync(0xffffffffu, k == 1));
+  }
+  __syncthreads();
+  if (lane == 0) {
+    s_sum[warp] = sure;
+    s_tie[warp] = ties;
+  }
+  __syncthreads();
+  int at = 0, seen_ties = 0;
+  for (int w = 0; w < warp; ++w) {
+    at += s_sum[w];
+    seen_ties += s_tie[w];
+  }
+  at += min(seen_ties, want);                        // ties before this stretch that are kept
+  for (int r0 = first; r0 < end; r0 += 32) {
+    const int r = r0 + lane, k = kind(r);
+    const uint32_t tie = __ballot_sync(0xffffffffu, k == 1), below = (1u << lane) - 1u;
+    const bool keep = k == 2 || (k == 1 && seen_ties + __popc(tie & below) < want);
+    const uint32_t all = __ballot_sync(0xffffffffu, keep);
+    if (keep) out[at + __popc(all & below)] = r;
+    at += __popc(all);
+    seen_ties += __popc(tie);
+  }
+}
+
+// Moves the kept rows of one (sequence, key head), a cluster of blocks each: 8 D bytes per row, bound by memory. Row i
+// comes from a row at or behind i, so in place a chunk's rows are all read before any of them is written (a cluster
+// barrier between), and no later chunk reads what this one wrote. Into other pages no order is needed.
+constexpr int kMoveBlocks = 8;
+constexpr int kMoveThreads = 256;
+
+template <int D>
+__global__ void __cluster_dims__(kMoveBlocks, 1, 1) __launch_bounds__(kMoveThreads)
+paged_move_kernel(PagedCache c, const int32_t* __restrict__ dst_table, int dst_max_pages, const int32_t* __restrict__ kept,
+                  int budget, int* err) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int U = D / 8;
+  constexpr int ROWS = kMoveThreads / U;             // rows a block copies at once
+  constexpr int K = 4;                               // times that, in flight
+  constexpr int CHUNK = kMoveBlocks * ROWS * K;
+  const int h = blockIdx.y, b = blockIdx.z, part = blockIdx.x, u = threadIdx.x % U;
+  const int pmask = (1 << c.page_log2) - 1;
+  const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
+  const int32_t* drow = dst_table + static_cast<size_t>(b) * dst_max_pages;
+  const int32_t* rows = kept + (static_cast<size_t>(b) * c.Hkv + h) * budget;
+  const bool in_place = __ldg(trow) == __ldg(drow);
+  uint4* pool = static_cast<uint4*>(c.pool);
+  const size_t vstep = (static_cast<size_t>(c.Hkv) << c.page_log2) * U;   // from a page's keys to its values
+  for (int i0 = 0; i0 < budget; i0 += CHUNK) {
+    if (__ldg(rows + i0) < 0) break;                 // behind the last row (the same for the whole cluster)
+    uint4 kx[K], vx[K];
+    float wx[K];
+    long long to[K];
+    long long wto[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = i0 + (k * kMoveBlocks + part) * ROWS + threadIdx.x / U;
+      to[k] = -1;
+      const int r = i < budget ? __ldg(rows + i) : -1;
+      if (r < 0) continue;
+      const int src = page_of(c, trow, r, err), dst = page_of(c, drow, i, err);
+      if (src < 0 || dst < 0) continue;
+      const uint4* from = pool + row_at(c, src, 0, h, r & pmask) * U + u;
+      kx[k] = from[0];
+      vx[k] = from[vstep];
+      if (u == 0) wx[k] = c.weight[weight_at(c, src, h, r & pmask)];
+      to[k] = static_cast<long long>(row_at(c, dst, 0, h, i & pmask) * U + u);
+      wto[k] = static_cast<long long>(weight_at(c, dst, h, i & pmask));
+    }
+    if (in_place) {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (to[k] < 0) continue;
+      pool[to[k]] = kx[k];
+      pool[to[k] + static_cast<long long>(vstep)] = vx[k];
+      if (u == 0) c.weight[wto[k]] = wx[k];
     }
   }
 }
@@ -715,10 +817,7 @@ paged_evict_kernel(PagedCache c, const int32_t* __restrict__ lens, const int32_t
 
 cudaError_t launch_paged_store(const PagedCache& c, const void* qkv, const int32_t* start, const int32_t* count, int B,
                                int T, int H, int D, int* err, cudaStream_t s) {
-  const long long units = static_cast<long long>(T) * 2 * c.Hkv * (D / 8);
-  const long long blocks = (units + 255) / 256;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(B));
+  const dim3 grid(static_cast<unsigned>((T - 1) / kStoreTokens + 1), static_cast<unsigned>(B));
   const uint4* x = static_cast<const uint4*>(qkv);
   if (D == 64) return launch_k(paged_store_kernel<64>, grid, dim3(256), 0, s, c, x, start, count, T, H, err);
   return launch_k(paged_store_kernel<32>, grid, dim3(256), 0, s, c, x, start, count, T, H, err);
@@ -793,12 +892,21 @@ cudaError_t launch_paged_attention(const PagedCache& c, const void* qkv, const i
 cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const int32_t* dst_table, int dst_max_pages,
                                int32_t* new_lens, int32_t* kept, int B, int D, int budget, int sinks, int recent,
                                int* err, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(c.Hkv), static_cast<unsigned>(B));
+  // ranks for the longest list that the table allows, as far as shared memory goes
+  const long long rows = (static_cast<long long>(c.max_pages) << c.page_log2) - sinks - recent;
+  const long long most = (232448 - 16384) / 4;
+  const int room = static_cast<int>(rows < 0 ? 0 : (rows < most ? rows : most));
+  cudaError_t e = cudaFuncSetAttribute(paged_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room * 4);
+  if (e != cudaSuccess) return e;
+  e = launch_k(paged_choose_kernel, dim3(static_cast<unsigned>(c.Hkv), static_cast<unsigned>(B)), dim3(kEvThreads),
+               static_cast<size_t>(room) * 4, s, c, lens, new_lens, kept, budget, sinks, recent, room, err);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(kMoveBlocks, static_cast<unsigned>(c.Hkv), static_cast<unsigned>(B));
   if (D == 64)
-    return launch_k(paged_evict_kernel<64>, grid, dim3(kEvThreads), 0, s, c, lens, dst_table, dst_max_pages, new_lens,
-                    kept, budget, sinks, recent, err);
-  return launch_k(paged_evict_kernel<32>, grid, dim3(kEvThreads), 0, s, c, lens, dst_table, dst_max_pages, new_lens, kept,
-                  budget, sinks, recent, err);
+    return launch_k(paged_move_kernel<64>, grid, dim3(kMoveThreads), 0, s, c, dst_table, dst_max_pages,
+                    static_cast<const int32_t*>(kept), budget, err);
+  return launch_k(paged_move_kernel<32>, grid, dim3(kMoveThreads), 0, s, c, dst_table, dst_max_pages,
+                  static_cast<const int32_t*>(kept), budget, err);
 }
 
 }  // namespace gptgb
