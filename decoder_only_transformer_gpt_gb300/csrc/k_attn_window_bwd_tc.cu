@@ -5,17 +5,18 @@
 //   dA = dY U^T,  dS = A * (dA - Dsum),  dQ = dS K / sqrt(D),  dK = dS^T Q / sqrt(D),  dU = A^T dY,
 // where dK and dU of a key head sum over the G query heads that share it.
 //
-// A work item is one (b, key head) and one 128-key tile j; it walks the query tiles that see those keys (from j to
-// the one whose window ends there; to the sequence's end where the tile holds a sink), head after head of the
-// group, so the group's sum stays in the accumulators. Items are dealt statically, the sink tiles first, forwards
-// and backwards in turn: the others cost the same, and no work counter has to be cleared.
+// A work item is one (b, key head), one 128-key tile j and a segment of the query tiles that see it (from j to the
+// one whose window ends there; to the sequence's end where the tile holds a sink), head after head of the group, so
+// that a group's sum stays in the accumulators. Items are dealt statically, the sink tiles first, forwards and
+// backwards in turn, and no work counter has to be cleared.
 // Each query tile is taken in two halves g of 64 queries with a tensor-memory buffer each (key = TMEM lane); K_j and
 // U_j sit in tensor memory (columns [448, 448 + D)), copied there once per item by the output warps:
 //   S^T_g  = K_j Q_{i,g}^T     M=128 keys, N=64 queries, K=D    columns [128 g, 128 g + 64)
 //   dP^T_g = U_j dY_{i,g}^T    M=128, N=64, K=D                 columns [128 g + 64, 128 g + 128)
-// Four derivative warps (one thread per key) turn a half into P^T = 2^(S^T log2(e)/sqrt(D) - lse2[q]) and
+// Four derivative warps per half (one thread per key) turn it into P^T = 2^(S^T log2(e)/sqrt(D) - lse2[q]) and
 // dS^T = P^T (dP^T - Dsum[q]), rounded to bf16 for the products below (the type the tensor core multiplies: 2^-8
-// of each term) while the tensor core works on the other half; a warp writes plain zeros for a half of which its
+// of each term) while the tensor core and the other four work on the other half (with one set of four warps
+// for both halves a step took 1.8 us: each scheduler had one warp, whose waits nothing covered); a warp writes plain zeros for a half of which its
 // 32 keys are not seen. dS^T also goes to shared memory (the MN-major A operand of dQ). Then
 //   dU_j += P^T_g dY_{i,g}     A from tensor memory, B = dY rows read MN-major    columns [256, 256 + D)
 //   dK_j += dS^T_g Q_{i,g}     A from tensor memory, B = Q rows read MN-major     columns [320, 320 + D)
@@ -23,8 +24,8 @@
 // Four output warps add each dQ_i tile into an fp32 [B][T][H D] buffer with TMA reduce-adds (the order of a query
 // tile's few additions varies, below a bf16 step of the result) and, at the end of an item, store dK_j / sqrt(D)
 // and dU_j by TMA. A last kernel rounds dQ to bf16.
-// Warps (320 threads, one persistent CTA per SM): 0 producer; 1 TMEM allocator and MMA issuer; 2-5 softmax
-// derivative (thread = key row); 6-9 output.
+// Warps (448 threads, one persistent CTA per SM): 0 producer; 1 TMEM allocator and MMA issuer; 2-5 and 6-9 softmax
+// derivative of half 0 and 1 (thread = key row); 10-13 output.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -37,9 +38,11 @@ namespace {
 
 constexpr int BT = 128;                 // rows per key or query tile
 constexpr int HQ = 64;                  // queries per half tile
-constexpr int THREADS = 320;
+constexpr int THREADS = 448;
 constexpr int TMEM_COLS = 512;
 constexpr int NQ = 2;                   // query-tile ring stages
+constexpr int SR = 4;                   // items announced ahead
+constexpr int kConsumers = 13;          // warps that read each announced item: MMA, 8 derivative, 4 output
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kColDU = 256, kColDK = 320, kColDQ = 384;   // half g: S^T at 128 g, dP^T at 128 g + 64
 constexpr uint32_t kColK = 448;         // K_j (bf16 pairs, D / 2 columns), then U_j: the item's A operands
@@ -63,7 +66,7 @@ struct BwdCfg {
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-struct __align__(8) BwdBars {
+struct __align__(16) BwdBars {
   uint64_t kv_full[2], kv_empty[2];     // K_j, U_j of an item (buffer r % 2)
   uint64_t q_full[NQ], q_empty[NQ];     // Q_i, dY_i, -lse2 and -Dsum of a query tile
   uint64_t s_full[2];                   // S^T and dP^T of half g are in tensor memory
@@ -74,7 +77,10 @@ struct __align__(8) BwdBars {
   uint64_t acc_free;                    // the output warps read them (4 warps)
   uint64_t kvt_full;                    // the item's K_j and U_j are in tensor memory (4 warps)
   uint64_t kvt_free;                    // the last product reading them has completed
+  uint64_t item_full[SR];               // slot r % SR holds the CTA's r-th item (from the producer)
+  uint64_t item_empty[SR];              // every other warp has read it
   uint64_t drain;
+  __align__(16) int item[SR][8];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -82,35 +88,79 @@ static_assert(sizeof(BwdBars) <= 512, "barrier block");
 
 __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
-// What a launch computes, and its items.
+// What a launch computes, and how it is cut. Items: one (b, key head), one key tile j, and a segment of that tile's
+// steps. The tiles with sinks see every later query tile and would keep one CTA busy long after the others (and a few
+// heads with long windows would leave most CTAs idle), so the tiles of each of the two classes are cut into nseg
+// segments; where nseg > 1 a segment's dK and dU go to fp32 slabs that the last kernel sums in order.
 struct WinBwdShape {
   int T, H, Hkv, G, window, sinks;   // window >= 1
   int n_qt, sink_tiles, BK;          // BK = B Hkv
-  int n_items;
+  int nseg_s, nseg_w;                // segments per tile with sinks, per other tile
+  int n_sink_items, n_items;
 };
 
-// Item r of this CTA, or -1.
-__device__ __forceinline__ int item_of(const WinBwdShape& w, int r) {
-  const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-  const long long i = static_cast<long long>(r) * g + ((r & 1) ? g - 1 - c : c);
-  return i < w.n_items ? static_cast<int>(i) : -1;
-}
-
-// Key tile j of key head kh: step e is query tile j + e % cnt of query head kh G + e / cnt.
+// Step e0 <= e < e1 is query tile j + e % cnt of query head kh G + e / cnt.
 struct Item {
-  int b, kh, j, cnt, steps;
+  int b, kh, j, cnt, e0, steps, slot;   // slot: of the fp32 slab, -1: dK and dU are complete
+  __device__ __forceinline__ int first_tile() const { return j + e0 % cnt; }
+  __device__ __forceinline__ int first_head(int G) const { return kh * G + e0 / cnt; }
 };
+
+__host__ __device__ __forceinline__ int tile_count(const WinBwdShape& w, int j) {   // query tiles that see key tile j
+  const long long end = j < w.sink_tiles ? w.n_qt : (static_cast<long long>(j) * BT + BT - 1 + w.window - 1) / BT + 1;
+  return (end < w.n_qt ? static_cast<int>(end) : w.n_qt) - j;
+}
+// First step of segment `seg` of nseg.
+__device__ __forceinline__ int seg_start(int steps, int seg, int nseg) {
+  return static_cast<int>(static_cast<long long>(steps) * seg / nseg);
+}
 
 __device__ __forceinline__ Item decode_item(const WinBwdShape& w, int item) {
   Item x;
-  x.j = item / w.BK;
-  const int bk = item - x.j * w.BK;
+  const bool sink = item < w.n_sink_items;
+  const int nseg = sink ? w.nseg_s : w.nseg_w;
+  const int k = sink ? item : item - w.n_sink_items;
+  const int q = k / w.BK, bk = k - q * w.BK, seg = q % nseg;
+  x.j = q / nseg + (sink ? 0 : w.sink_tiles);
   x.b = bk / w.Hkv;
   x.kh = bk - x.b * w.Hkv;
-  const long long end = x.j < w.sink_tiles ? w.n_qt : (static_cast<long long>(x.j) * BT + BT - 1 + w.window - 1) / BT + 1;
-  x.cnt = (end < w.n_qt ? static_cast<int>(end) : w.n_qt) - x.j;
-  x.steps = w.G * x.cnt;
+  x.cnt = tile_count(w, x.j);
+  const int steps = w.G * x.cnt;
+  x.e0 = seg_start(steps, seg, nseg);
+  x.steps = seg_start(steps, seg + 1, nseg) - x.e0;
+  x.slot = nseg == 1 ? -1 : item - (w.nseg_s == 1 ? w.n_sink_items : 0);
   return x;
+}
+
+// The CTA's items in turn, for its producer: forwards and backwards over the grid, empty segments left out.
+struct Items {
+  int round = -1;
+  __device__ __forceinline__ bool next(const WinBwdShape& w, Item& x) {
+    const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    while (true) {
+      ++round;
+      const long long i = static_cast<long long>(round) * g + ((round & 1) ? g - 1 - c : c);
+      if (i >= w.n_items) return false;
+      x = decode_item(w, static_cast<int>(i));
+      if (x.steps > 0) return true;
+    }
+  }
+};
+
+// What the other warps need of an item. The producer decodes it (a chain of divisions that each warp's first step of
+// the item would wait for) and announces it through a ring of SR slots; steps 0 ends the list.
+struct Step0 {
+  int b, kh, j, end, i, head, steps, slot;   // query tiles [j, end); the first step's tile and head
+};
+__device__ __forceinline__ bool next_item(BwdBars* bars, int r, Step0& x, volatile int* abort_flag, int* err, int lane) {
+  const int slot = r % SR;
+  if (!mbar_wait_warp(&bars->item_full[slot], static_cast<uint32_t>(r / SR) & 1u, abort_flag, err)) return false;
+  const int4* v = reinterpret_cast<const int4*>(bars->item[slot]);
+  const int4 p = v[0], q = v[1];
+  x = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
+  return x.steps > 0;
 }
 
 // 16-byte unit u of row r of a staging box (rows of `rowb` bytes) in the TMA swizzle of that width.
@@ -178,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_dy,
                    const __grid_constant__ CUtensorMap tm_dkv, const __grid_constant__ CUtensorMap tm_dq,
                    const float* __restrict__ lse2, const float* __restrict__ dsum, const WinBwdShape w, float sl2,
-                   float rsd, int* err) {
+                   float rsd, float* slabs, int* err) {
   using Cfg = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw + Cfg::OFF_BAR);
@@ -209,6 +259,10 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
     mbar_init(&bars->acc_free, 4);
     mbar_init(&bars->kvt_full, 4);
     mbar_init(&bars->kvt_free, 1);
+    for (int i = 0; i < SR; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], kConsumers);
+    }
     mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -226,6 +280,7 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
   const uint32_t tmem_base = bars->tmem_base;
   pdl_wait();
   pdl_trigger();
+  asm volatile("fence.proxy.async.global;" ::: "memory");   // the cleared dQ buffer, before TMA adds into it
 
   uint8_t* sK = smem_raw + Cfg::OFF_K;
   uint8_t* sU = smem_raw + Cfg::OFF_U;
@@ -239,10 +294,19 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
     uint32_t qcount = 0;
     bool ok = true;
     uint32_t issued_kv = 0, par_kv = 0, issued_q = 0, par_q = 0;
+    Items items;
+    Item x;
     for (int r = 0; ok; ++r) {
-      const int item = item_of(w, r);
-      if (item < 0) break;
-      const Item x = decode_item(w, item);
+      const bool have = items.next(w, x);
+      const int slot = r % SR;
+      if (r >= SR && !mbar_wait_warp(&bars->item_empty[slot], static_cast<uint32_t>(r / SR - 1) & 1u, abort_flag, err)) break;
+      if (lane == 0) {
+        int4* v = reinterpret_cast<int4*>(bars->item[slot]);
+        v[0] = have ? make_int4(x.b, x.kh, x.j, x.j + x.cnt) : make_int4(0, 0, 0, 0);
+        v[1] = have ? make_int4(x.first_tile(), x.first_head(w.G), x.steps, x.slot) : make_int4(0, 0, 0, 0);
+        mbar_arrive(&bars->item_full[slot]);
+      }
+      if (!have) break;
       const int kb = r & 1;
       if (r >= 2 && !mbar_wait_warp(&bars->kv_empty[kb], static_cast<uint32_t>((r >> 1) - 1) & 1u, abort_flag, err)) break;
       if (lane == 0) {
@@ -255,7 +319,7 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       // the rows' -lse2 and -Dsum by query pair (plain loads; rows past T read nothing), each tile's
       // fetched one tile ahead so that their latency passes while the producer waits for a free slot
       float nl[BT / 32], nd[BT / 32];
-      int head = x.kh * w.G, i = x.j;                // query head and tile of the step to fetch
+      int head = x.first_head(w.G), i = x.first_tile();   // query head and tile of the step to fetch
       auto fetch_rows = [&]() {
         const size_t row = (static_cast<size_t>(x.b) * H + head) * T;
 #pragma unroll
@@ -339,9 +403,9 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
                             desc_add(qmn0, qoff + kk * 16 * Cfg::ROWB), id_acc, (first && kk == 0) ? 0u : 1u);
     };
     int r = 0;
-    const int item0 = item_of(w, 0);
-    bool ok = item0 >= 0;
-    int steps = ok ? decode_item(w, item0).steps : 0, e = 0, kb = 0;
+    Step0 x;
+    bool ok = next_item(bars, 0, x, abort_flag, err, lane);
+    int steps = ok ? x.steps : 0, e = 0, kb = 0;
     uint32_t qcount = 0, qs = 0, tiles = 0;
     if (ok)
       ok = mbar_wait_warp(&bars->kv_full[0], 0u, abort_flag, err) && mbar_wait_warp(&bars->q_full[0], 0u, abort_flag, err) &&
@@ -363,12 +427,11 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       bool has_next = !last;
       int r2 = r, e2 = e + 1, steps2 = steps, kb2 = kb;
       if (last) {
-        const int item2 = item_of(w, r + 1);
-        has_next = item2 >= 0;
+        has_next = next_item(bars, r + 1, x, abort_flag, err, lane);
         if (has_next) {
           r2 = r + 1;
           e2 = 0;
-          steps2 = decode_item(w, item2).steps;
+          steps2 = x.steps;
           kb2 = r2 & 1;
           if (!mbar_wait_warp(&bars->kv_full[kb2], static_cast<uint32_t>(r2 >> 1) & 1u, abort_flag, err)) break;
           if (!mbar_wait_warp(&bars->kvt_full, static_cast<uint32_t>(r2) & 1u, abort_flag, err)) break;
@@ -407,61 +470,56 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
     }
     tc_commit_warp(&bars->drain);
     mbar_wait_drain(&bars->drain, 0);
-  } else if (warp < 6) {
-    // ------------------------------------------------ softmax derivative (thread = key row)
+  } else if (warp < 10) {
+    // ------------------------------------------------ softmax derivative (thread = key row; group g: half g)
+    const int g = warp < 6 ? 0 : 1;
     const int sub = warp & 3;
     const int kr = sub * 32 + lane;                  // key row within the tile = TMEM lane
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(sub * 32) << 16);
-    uint32_t qcount = 0, tiles = 0;
+    uint32_t tiles = 0;
     bool ok = true;
-    for (int r = 0; ok; ++r) {
-      const int item = item_of(w, r);
-      if (item < 0) break;
-      const Item x = decode_item(w, item);
+    Step0 x;
+    for (int r = 0; ok && next_item(bars, r, x, abort_flag, err, lane); ++r) {
       const int s0 = x.j * BT + sub * 32;              // the warp's first key
       // the last query that sees this thread's key, and the same for the warp's first and last key
       const int far = T - 1;
       const int end = s0 + lane < w.sinks ? far : static_cast<int>(min(static_cast<long long>(far), static_cast<long long>(s0) + lane + w.window - 1));
       const int end_lo = s0 + 31 < w.sinks ? far : static_cast<int>(min(static_cast<long long>(far), static_cast<long long>(s0 < w.sinks ? w.sinks : s0) + w.window - 1));
       const int end_hi = s0 < w.sinks ? far : static_cast<int>(min(static_cast<long long>(far), static_cast<long long>(s0) + 31 + w.window - 1));
-      int i = x.j;
-      for (int e = 0; e < x.steps; ++e, ++qcount, ++tiles) {
-        const uint32_t qs = qcount % NQ;
-        if (!mbar_wait_warp(&bars->q_full[qs], (qcount / NQ) & 1u, abort_flag, err)) { ok = false; break; }
-        const float4* ld = reinterpret_cast<const float4*>(sLD + qs * (2 * BT));
-        uint8_t* ds_row = sDS + (tiles & 1u) * Cfg::DS_BUF + kr * 128;
-#pragma unroll 1                                 // rolled, like the chunk loop inside: smaller code
-        for (int g = 0; g < 2; ++g) {
-          if (!mbar_wait_warp(&bars->s_full[g], tiles & 1u, abort_flag, err)) { ok = false; break; }
-          tc_fence_after();
-          // query q0 + ql is kept for lo <= ql <= hi. The choice of path is the warp's: the TMEM loads in it
-          // are warp-wide (.aligned).
-          const int q0 = i * BT + g * HQ;
-          if (q0 > end_hi || q0 + HQ - 1 < s0) {
-            zero_half(tb + 128 * g, ds_row + g * (BT * 128), kr);
-          } else if (q0 < s0 + 31 || q0 + HQ - 1 > end_lo) {
-            const int hi = end - q0, lo = s0 + lane - q0;
-            const uint64_t below_hi = hi < 0 ? 0ull : (hi >= HQ - 1 ? ~0ull : (2ull << hi) - 1ull);
-            const uint64_t from_lo = lo >= HQ ? 0ull : (~0ull << (lo > 0 ? lo : 0));
-            derivative_half<true>(tb + 128 * g, ld + 32 * g, sl2, below_hi & from_lo, ds_row + g * (BT * 128), kr);
-          } else {
-            derivative_half<false>(tb + 128 * g, ld + 32 * g, sl2, ~0ull, ds_row + g * (BT * 128), kr);
-          }
-          tmem_st_wait();
-          fence_proxy_async_smem();                  // dS in shared memory is read by the dQ product
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->p_full[g]);
+      int i = x.i;
+      for (int e = 0; e < x.steps; ++e, ++tiles) {
+        const uint32_t qs = tiles % NQ;
+        if (!mbar_wait_warp(&bars->q_full[qs], (tiles / NQ) & 1u, abort_flag, err)) { ok = false; break; }
+        const float4* ld = reinterpret_cast<const float4*>(sLD + qs * (2 * BT)) + 32 * g;
+        uint8_t* ds_row = sDS + (tiles & 1u) * Cfg::DS_BUF + g * (BT * 128) + kr * 128;
+        if (!mbar_wait_warp(&bars->s_full[g], tiles & 1u, abort_flag, err)) { ok = false; break; }
+        tc_fence_after();
+        // query q0 + ql is kept for lo <= ql <= hi. The choice of path is the warp's: the TMEM loads in it
+        // are warp-wide (.aligned).
+        const int q0 = i * BT + g * HQ;
+        if (q0 > end_hi || q0 + HQ - 1 < s0) {
+          zero_half(tb + 128 * g, ds_row, kr);
+        } else if (q0 < s0 + 31 || q0 + HQ - 1 > end_lo) {
+          const int hi = end - q0, lo = s0 + lane - q0;
+          const uint64_t below_hi = hi < 0 ? 0ull : (hi >= HQ - 1 ? ~0ull : (2ull << hi) - 1ull);
+          const uint64_t from_lo = lo >= HQ ? 0ull : (~0ull << (lo > 0 ? lo : 0));
+          derivative_half<true>(tb + 128 * g, ld, sl2, below_hi & from_lo, ds_row, kr);
+        } else {
+          derivative_half<false>(tb + 128 * g, ld, sl2, ~0ull, ds_row, kr);
         }
-        if (!ok) break;
-        if (++i == x.j + x.cnt) i = x.j;
+        tmem_st_wait();
+        fence_proxy_async_smem();                    // dS in shared memory is read by the dQ product
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[g]);
+        if (++i == x.end) i = x.j;
       }
     }
   } else {
     // ------------------------------------------------ output: dQ reduce-adds and conversion, dK and dU stores
     const int sub = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(sub * 32) << 16;
-    uint8_t* stg = smem_raw + Cfg::OFF_STG + (warp - 6) * 8192;
+    uint8_t* stg = smem_raw + Cfg::OFF_STG + (warp - 10) * 8192;
     // K_j and U_j (item buffer kb) into tensor memory as the scores' A operands: this warp's 32 key rows,
     // each row's D values as bf16 pairs
     auto stage_kv = [&](int kb) {
@@ -491,17 +549,18 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
     };
     uint32_t tiles = 0;
     bool ok = true;
-    int item = item_of(w, 0);
-    if (item >= 0) {
+    Step0 x, x_next;
+    bool have = next_item(bars, 0, x, abort_flag, err, lane);
+    if (have) {
       ok = mbar_wait_warp(&bars->kv_full[0], 0u, abort_flag, err);
       if (ok) stage_kv(0);
     }
-    for (int r = 0; ok && item >= 0; ++r) {
-      const Item x = decode_item(w, item);
-      const int item_next = item_of(w, r + 1);
-      int i = x.j, head = x.kh * w.G;
+    for (int r = 0; ok && have; ++r) {
+      bool have_next = false;
+      int i = x.i, head = x.head;
       for (int e = 0; e < x.steps; ++e, ++tiles) {
-        if (e == x.steps - 1 && item_next >= 0) {
+        if (e == x.steps - 1) have_next = next_item(bars, r + 1, x_next, abort_flag, err, lane);
+        if (e == x.steps - 1 && have_next) {
           // before the item's last dQ: the next item's K_j, U_j, once the item's last scores have read theirs
           if (!mbar_wait_warp(&bars->kvt_free, static_cast<uint32_t>(r) & 1u, abort_flag, err) ||
               !mbar_wait_warp(&bars->kv_full[(r + 1) & 1], static_cast<uint32_t>((r + 1) >> 1) & 1u, abort_flag, err)) {
@@ -510,6 +569,65 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
           }
           tc_fence_after();
           stage_kv((r + 1) & 1);
+        }
+        if (e == x.steps - 1) {
+          // the item's dK and dU, complete before its last dQ: read first, so that the next item's products may start
+          if (!mbar_wait_warp(&bars->acc_full, static_cast<uint32_t>(r) & 1u, abort_flag, err)) { ok = false; break; }
+          tc_fence_after();
+          constexpr int ROWB = Cfg::ROWB;
+          if (x.slot >= 0) {                         // one of several segments: unscaled fp32
+#pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+              float4* dst = reinterpret_cast<float4*>(slabs + ((static_cast<size_t>(x.slot) * 2 + which) * BT + sub * 32 + lane) * D);
+#pragma unroll 1
+              for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem_base + (which ? kColDU : kColDK) + lane_off + 32 * cc, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  dst[8 * cc + u] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
+                                                __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->acc_free);
+          } else {
+            uint32_t pk[D / 2], pu[D / 2];           // bf16 rows: dK / sqrt(D), dU
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(tmem_base + kColDK + lane_off + 32 * cc, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                pk[16 * cc + u] = pack_bf16x2(__uint_as_float(v[2 * u]) * rsd, __uint_as_float(v[2 * u + 1]) * rsd);
+              tmem_ld_32x32b_x32(tmem_base + kColDU + lane_off + 32 * cc, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                pu[16 * cc + u] = pack_bf16x2(__uint_as_float(v[2 * u]), __uint_as_float(v[2 * u + 1]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->acc_free);
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < ROWB / 16; ++u) {    // box 0, box 1
+              const int at = lane * ROWB + (swz_unit(ROWB, lane, u) << 4);
+              *reinterpret_cast<uint4*>(stg + at) = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+              *reinterpret_cast<uint4*>(stg + 4096 + at) = make_uint4(pu[4 * u], pu[4 * u + 1], pu[4 * u + 2], pu[4 * u + 3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tm_dkv, stg, kcol + x.kh * D, x.j * BT + sub * 32, x.b);
+              tma_store_3d(&tm_dkv, stg + 4096, ucol + x.kh * D, x.j * BT + sub * 32, x.b);
+              bulk_commit();
+            }
+          }
         }
         if (!mbar_wait_warp(&bars->dq_full, tiles & 1u, abort_flag, err)) { ok = false; break; }
         tc_fence_after();
@@ -541,51 +659,14 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
             tma_reduce_add_3d(&tm_dq, stg + cc * 4096, head * D + 32 * cc, i * BT + sub * 32, x.b);
           bulk_commit();
         }
-        if (++i == x.j + x.cnt) {
+        if (++i == x.end) {
           i = x.j;
           ++head;
         }
       }
       if (!ok) break;
-      // the item's dK and dU
-      if (!mbar_wait_warp(&bars->acc_full, static_cast<uint32_t>(r) & 1u, abort_flag, err)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t kv[D], uv[D];
-#pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t (&k32)[32] = *reinterpret_cast<uint32_t (*)[32]>(kv + 32 * cc);
-        uint32_t (&u32)[32] = *reinterpret_cast<uint32_t (*)[32]>(uv + 32 * cc);
-        tmem_ld_32x32b_x32(tmem_base + kColDK + lane_off + 32 * cc, k32);
-        tmem_ld_32x32b_x32(tmem_base + kColDU + lane_off + 32 * cc, u32);
-      }
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->acc_free);
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
-      constexpr int ROWB = Cfg::ROWB;
-#pragma unroll
-      for (int u = 0; u < ROWB / 16; ++u) {          // bf16 rows of D values: dK / sqrt(D) in box 0, dU in box 1
-        const uint4 wk = make_uint4(pack_bf16x2(__uint_as_float(kv[8 * u]) * rsd, __uint_as_float(kv[8 * u + 1]) * rsd),
-                                    pack_bf16x2(__uint_as_float(kv[8 * u + 2]) * rsd, __uint_as_float(kv[8 * u + 3]) * rsd),
-                                    pack_bf16x2(__uint_as_float(kv[8 * u + 4]) * rsd, __uint_as_float(kv[8 * u + 5]) * rsd),
-                                    pack_bf16x2(__uint_as_float(kv[8 * u + 6]) * rsd, __uint_as_float(kv[8 * u + 7]) * rsd));
-        const uint4 wu = make_uint4(pack_bf16x2(__uint_as_float(uv[8 * u]), __uint_as_float(uv[8 * u + 1])),
-                                    pack_bf16x2(__uint_as_float(uv[8 * u + 2]), __uint_as_float(uv[8 * u + 3])),
-                                    pack_bf16x2(__uint_as_float(uv[8 * u + 4]), __uint_as_float(uv[8 * u + 5])),
-                                    pack_bf16x2(__uint_as_float(uv[8 * u + 6]), __uint_as_float(uv[8 * u + 7])));
-        *reinterpret_cast<uint4*>(stg + lane * ROWB + (swz_unit(ROWB, lane, u) << 4)) = wk;
-        *reinterpret_cast<uint4*>(stg + 4096 + lane * ROWB + (swz_unit(ROWB, lane, u) << 4)) = wu;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(&tm_dkv, stg, kcol + x.kh * D, x.j * BT + sub * 32, x.b);
-        tma_store_3d(&tm_dkv, stg + 4096, ucol + x.kh * D, x.j * BT + sub * 32, x.b);
-        bulk_commit();
-      }
-      item = item_next;
+      x = x_next;
+      have = have_next;
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -600,11 +681,12 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
 }
 
 // Dsum[(b H + h) T + t] = sum_d dY[b, t, h D + d] Y[b, t, h D + d]: one warp per row, D / 8 lanes per
-// head with 16-byte loads, so each load instruction of the warp reads 512 contiguous bytes of the row.
+// head with 16-byte loads, so each load instruction of the warp reads 512 contiguous bytes of the row. It also clears
+// the row of the dQ accumulator (a memset of its own took a launch and as long again).
 template <int D>
 __global__ void __launch_bounds__(256)
 attn_window_dsum_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16* __restrict__ dy, float* __restrict__ dsum,
-                     int M, int T, int H) {
+                        float* __restrict__ dqacc, int M, int T, int H) {
   pdl_wait();
   pdl_trigger();
   const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -620,6 +702,8 @@ attn_window_dsum_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16
     float acc = 0.0f;
     if (v < nv) {
       const uint4 a = __ldg(a4 + v), o = __ldg(o4 + v);
+      float4* z = reinterpret_cast<float4*>(dqacc + static_cast<size_t>(row) * C) + 2 * v;
+      z[0] = z[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, ow[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -633,63 +717,67 @@ attn_window_dsum_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16
   }
 }
 
-// dqkv[m, c] = bf16(dqacc[m, c] / sqrt(D)) for the first C = H D of a row's `row` columns: four consecutive floats
-// per thread and step, so each warp access covers 512 contiguous bytes.
+// The first `nblk` blocks: dqkv[m, c] = bf16(dqacc[m, c] / sqrt(D)) for the first C = H D of a row's columns, four
+// consecutive floats per thread and step, so each warp access covers 512 contiguous bytes. Later blocks: dK and dU of
+// the key tiles that were cut into segments, their slabs summed in order.
+template <int D>
 __global__ void __launch_bounds__(256)
-attn_window_dq_kernel(const float* __restrict__ dqacc, __nv_bfloat16* __restrict__ dqkv, int M, int C, int row, float rsd) {
+attn_window_finish_kernel(const float* __restrict__ dqacc, const float* __restrict__ slabs, __nv_bfloat16* __restrict__ dqkv,
+                          int M, const WinBwdShape w, int nblk, float rsd) {
   pdl_wait();
   pdl_trigger();
-  const int c4n = C / 4;
-  const long long n = static_cast<long long>(M) * c4n;
-  for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < n;
-       e += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int m = static_cast<int>(e / c4n), c = static_cast<int>(e - static_cast<long long>(m) * c4n) * 4;
-    const float4 a = __ldg(reinterpret_cast<const float4*>(dqacc) + e);
-    *reinterpret_cast<uint2*>(dqkv + static_cast<size_t>(m) * row + c) =
-        make_uint2(pack_bf16x2(a.x * rsd, a.y * rsd), pack_bf16x2(a.z * rsd, a.w * rsd));
+  const int C = w.H * D, row = C + 2 * w.Hkv * D;
+  if (static_cast<int>(blockIdx.x) < nblk) {
+    const int c4n = C / 4;
+    const long long n = static_cast<long long>(M) * c4n;
+    for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < n;
+         e += static_cast<long long>(nblk) * blockDim.x) {
+      const int m = static_cast<int>(e / c4n), c = static_cast<int>(e - static_cast<long long>(m) * c4n) * 4;
+      const float4 a = __ldg(reinterpret_cast<const float4*>(dqacc) + e);
+      *reinterpret_cast<uint2*>(dqkv + static_cast<size_t>(m) * row + c) =
+          make_uint2(pack_bf16x2(a.x * rsd, a.y * rsd), pack_bf16x2(a.z * rsd, a.w * rsd));
+    }
+    return;
   }
+  // the tile's first item: the cut tiles are those with sinks (if nseg_s > 1), then the others (if nseg_w > 1)
+  constexpr int PARTS = 2 * BT * (D / 4) / 256;      // blocks per tile: four floats of the tile per thread
+  int k = (static_cast<int>(blockIdx.x) - nblk) / PARTS;
+  const int part = (static_cast<int>(blockIdx.x) - nblk) % PARTS;
+  const int sinks = w.nseg_s > 1 ? w.sink_tiles * w.BK : 0;
+  const bool sink = k < sinks;
+  if (!sink) k -= sinks;
+  const int nseg = sink ? w.nseg_s : w.nseg_w;
+  const int jj = k / w.BK, bk = k - jj * w.BK, j = jj + (sink ? 0 : w.sink_tiles);
+  const int slot0 = (sink ? 0 : (w.nseg_s > 1 ? w.n_sink_items : 0)) + jj * nseg * w.BK + bk;
+  const int steps = w.G * tile_count(w, j);
+  const int b = bk / w.Hkv, kh = bk - b * w.Hkv;
+  const int i = part * 256 + threadIdx.x;
+  const int which = i / (BT * (D / 4)), r = i / (D / 4) % BT, c = i % (D / 4);
+  if (j * BT + r >= w.T) return;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s < nseg; ++s) {
+    if (seg_start(steps, s, nseg) == seg_start(steps, s + 1, nseg)) continue;   // an empty segment has no slab
+    const float4 v = __ldg(reinterpret_cast<const float4*>(slabs) + static_cast<size_t>(slot0 + s * w.BK) * (2 * BT * (D / 4)) + i);
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  const float f = which ? 1.0f : rsd;
+  *reinterpret_cast<uint2*>(dqkv + (static_cast<size_t>(b) * w.T + j * BT + r) * row + C + (which * w.Hkv + kh) * D + 4 * c) =
+      make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
 }
 
-template <int D>
-cudaError_t launch_bwd_d(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
-                         const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2, float* dsum,
-                         float* dqacc, void* dqkv, int B, WinBwdShape w, int* err, cudaStream_t s) {
-  using Cfg = BwdCfg<D>;
-  int dev = 0, num_sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_window_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-  if (e != cudaSuccess) return e;
-  const int M = B * w.T, C = w.H * D;
-  const long long items = static_cast<long long>(w.n_qt) * w.BK;
-  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  w.n_items = static_cast<int>(items);
-  const float rsd = 1.0f / sqrtf(static_cast<float>(D));
-  const float sl2 = rsd * kLog2e;
-  e = cudaMemsetAsync(dqacc, 0, static_cast<size_t>(M) * C * sizeof(float), s);
-  if (e != cudaSuccess) return e;
-  e = launch_k(attn_window_dsum_kernel<D>, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s,
-               static_cast<const __nv_bfloat16*>(y), static_cast<const __nv_bfloat16*>(dy), dsum, M, w.T, w.H);
-  if (e != cudaSuccess) return e;
-  const int grid = static_cast<int>(items < num_sms ? items : num_sms);
-  e = launch_k(attn_window_bwd_tc_kernel<D>, dim3(grid), dim3(THREADS), static_cast<size_t>(Cfg::SMEM), s, tm_qkv, tm_dy,
-               tm_dkv, tm_dq, lse2, static_cast<const float*>(dsum), w, sl2, rsd, err);
-  if (e != cudaSuccess) return e;
-  const long long n4 = static_cast<long long>(M) * (C / 4);
-  const long long cblocks = (n4 + 255) / 256;
-  const int cgrid = static_cast<int>(cblocks < 8LL * num_sms ? cblocks : 8LL * num_sms);
-  return launch_k(attn_window_dq_kernel, dim3(cgrid), dim3(256), 0, s, static_cast<const float*>(dqacc),
-                  static_cast<__nv_bfloat16*>(dqkv), M, C, (w.H + 2 * w.Hkv) * D, rsd);
-}
+// Cuts the launch into items; the fp32 slabs that it needs.
+struct WinBwdPlan {
+  WinBwdShape w;
+  int slabs, cut_tiles;
+};
 
-}  // namespace
-
-cudaError_t launch_attention_window_bwd_tc(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
-                                           const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2,
-                                           float* dsum, float* dqacc, void* dqkv, int B, int T, int H, int Hkv, int D,
-                                           int window, int sinks, int* err, cudaStream_t s) {
-  WinBwdShape w = {};
+bool plan_bwd(int B, int T, int H, int Hkv, int window, int sinks, int num_sms, WinBwdPlan* p) {
+  WinBwdShape& w = p->w;
+  w = {};
   w.T = T;
   w.H = H;
   w.Hkv = Hkv;
@@ -699,8 +787,78 @@ cudaError_t launch_attention_window_bwd_tc(const CUtensorMap& tm_qkv, const CUte
   w.n_qt = (T + BT - 1) / BT;
   w.sink_tiles = (w.sinks + BT - 1) / BT;
   w.BK = B * Hkv;
-  if (D == 64) return launch_bwd_d<64>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, dsum, dqacc, dqkv, B, w, err, s);
-  if (D == 32) return launch_bwd_d<32>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, dsum, dqacc, dqkv, B, w, err, s);
+  const int rest = w.n_qt - w.sink_tiles;
+  const long long big_s = w.sink_tiles ? static_cast<long long>(w.G) * w.n_qt : 0;
+  const long long big_w = rest ? static_cast<long long>(w.G) * tile_count(w, w.sink_tiles) : 0;
+  // a CTA's fair share of the steps; a tile that has more is cut into segments of about half of it, but of 8 steps
+  // at least (a segment costs its K and U tiles and, at its end, 64 KB of fp32 sums)
+  const long long share = ((big_s * w.sink_tiles + big_w * rest) * w.BK + num_sms - 1) / num_sms;
+  const long long len = share / 2 > 8 ? share / 2 : 8;
+  const long long ns = big_s > share && big_s > len ? (big_s + len - 1) / len : 1;
+  const long long nw = big_w > share && big_w > len ? (big_w + len - 1) / len : 1;
+  const long long sink_items = ns * w.sink_tiles * w.BK, items = sink_items + nw * rest * w.BK;
+  if (items > 0x7fffffffLL || big_s > 0x7fffffffLL || big_w > 0x7fffffffLL) return false;
+  w.nseg_s = static_cast<int>(ns);
+  w.nseg_w = static_cast<int>(nw);
+  w.n_sink_items = static_cast<int>(sink_items);
+  w.n_items = static_cast<int>(items);
+  p->slabs = static_cast<int>((ns > 1 ? sink_items : 0) + (nw > 1 ? items - sink_items : 0));
+  p->cut_tiles = ((ns > 1 ? w.sink_tiles : 0) + (nw > 1 ? rest : 0)) * w.BK;
+  return true;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
+
+template <int D>
+cudaError_t launch_bwd_d(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
+                         const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2, float* dsum,
+                         float* dqacc, float* slabs, void* dqkv, int B, const WinBwdPlan& plan, int num_sms, int* err,
+                         cudaStream_t s) {
+  using Cfg = BwdCfg<D>;
+  const WinBwdShape& w = plan.w;
+  cudaError_t e = cudaFuncSetAttribute(attn_window_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  const int M = B * w.T, C = w.H * D;
+  const float rsd = 1.0f / sqrtf(static_cast<float>(D));
+  const float sl2 = rsd * kLog2e;
+  e = launch_k(attn_window_dsum_kernel<D>, dim3(static_cast<unsigned>((M - 1) / 8 + 1)), dim3(256), 0, s,
+               static_cast<const __nv_bfloat16*>(y), static_cast<const __nv_bfloat16*>(dy), dsum, dqacc, M, w.T, w.H);
+  if (e != cudaSuccess) return e;
+  const int grid = w.n_items < num_sms ? w.n_items : num_sms;
+  e = launch_k(attn_window_bwd_tc_kernel<D>, dim3(grid), dim3(THREADS), static_cast<size_t>(Cfg::SMEM), s, tm_qkv, tm_dy,
+               tm_dkv, tm_dq, lse2, static_cast<const float*>(dsum), w, sl2, rsd, slabs, err);
+  if (e != cudaSuccess) return e;
+  const long long n4 = static_cast<long long>(M) * (C / 4);
+  const long long cblocks = (n4 + 255) / 256;
+  const int nblk = static_cast<int>(cblocks < 8LL * num_sms ? cblocks : 8LL * num_sms);
+  return launch_k(attn_window_finish_kernel<D>, dim3(nblk + plan.cut_tiles * (2 * BT * (D / 4) / 256)), dim3(256), 0, s, static_cast<const float*>(dqacc),
+                  static_cast<const float*>(slabs), static_cast<__nv_bfloat16*>(dqkv), M, w, nblk, rsd);
+}
+
+}  // namespace
+
+size_t attention_window_bwd_slab_bytes(int B, int T, int H, int Hkv, int D, int window, int sinks) {
+  WinBwdPlan p;
+  const int num_sms = sm_count();
+  if (num_sms <= 0 || !plan_bwd(B, T, H, Hkv, window, sinks, num_sms, &p)) return 0;
+  return static_cast<size_t>(p.slabs) * 2 * BT * D * sizeof(float);
+}
+
+cudaError_t launch_attention_window_bwd_tc(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
+                                           const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2,
+                                           float* dsum, float* dqacc, float* slabs, void* dqkv, int B, int T, int H,
+                                           int Hkv, int D, int window, int sinks, int* err, cudaStream_t s) {
+  WinBwdPlan p;
+  const int num_sms = sm_count();
+  if (num_sms <= 0 || !plan_bwd(B, T, H, Hkv, window, sinks, num_sms, &p)) return cudaErrorInvalidValue;
+  if (D == 64)
+    return launch_bwd_d<64>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, dsum, dqacc, slabs, dqkv, B, p, num_sms, err, s);
+  if (D == 32)
+    return launch_bwd_d<32>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, dsum, dqacc, slabs, dqkv, B, p, num_sms, err, s);
   return cudaErrorInvalidValue;
 }
 

@@ -242,3 +242,9 @@ def test_two_calls_at_once(gpt_lib):
     torch.cuda.synchronize()
     for (qkv, dy), (y, lse2, dqkv) in zip(ins, outs):
         _check(qkv, dy, y, lse2, dqkv, H, H, window, sinks)
+
+
+@pytest.mark.parametrize("T,H,Hkv,window,sinks", [(3000, 4, 1, 3000, 0), (2500, 3, 1, 100, 300), (4000, 2, 2, 2000, 4)])
+def test_shared_key_tiles(gpt_lib, T, H, Hkv, window, sinks):
+    # few heads and long windows or sinks: a key tile's query tiles are cut into segments of several CTAs
+    _case(1, T, H, Hkv, 64, window, sinks, seed=T)
