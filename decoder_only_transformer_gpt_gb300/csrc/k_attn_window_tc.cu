@@ -51,6 +51,9 @@ constexpr float kSumLimit = 65536.0f;   // recompute a tile against its exact ma
 constexpr int NS = 4;                   // K/U ring depth; the MMA warp's look-ahead needs at least 4
 constexpr int NSB = 3;                  // score buffers
 constexpr uint32_t kColO = 128 * NSB;   // O_g at kColO + 64 g
+constexpr int SR = 4;                   // items announced ahead by the producer
+constexpr int CH = 64;                  // keys that a softmax warp handles at a time
+constexpr int kConsumers = 10;          // warps that read each announced item: 2 MMA issuers + 8 softmax
 
 template <int D>
 struct AttnCfg {
@@ -69,15 +72,17 @@ struct AttnCfg {
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-struct __align__(8) AttnBars {
+struct __align__(16) AttnBars {
   uint64_t q_empty[2];      // every S of the item that used Q buffer k has been computed
   uint64_t kv_full[NS];     // ring stage holds K_j, U_j (and, for an item's first tile, its query tiles)
   uint64_t kv_empty[NS];
   uint64_t s_full[2][NSB];  // score buffer b holds a new score tile of group g (that group's uses of b, in order)
-  uint64_t p_full[NSB][2];  // score buffer b holds that tile's probabilities of keys [64 h, 64 h + 64) (4 warps)
+  uint64_t p_full[NSB];     // score buffer b holds that tile's probabilities (4 warps)
   uint64_t pv_done[NSB];    // the P U that read buffer b has completed (the buffer may take new scores)
-  uint64_t o_full[2][3];    // group g's P U number i (its own count) has completed: barrier i % 3
   uint64_t drain[2];        // the issuing warps' own MMAs have completed (exit)
+  uint64_t item_full[SR];   // slot r % SR holds this CTA's r-th item (from the producer)
+  uint64_t item_empty[SR];  // every other warp has read it
+  __align__(16) int item[SR][8];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -88,25 +93,54 @@ static_assert(sizeof(AttnBars) <= 512, "barrier block");
 // plain add of bytes >> 4 to its base descriptor.
 __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
+// The products of one step by one elected lane of the converged warp: a single election for all of them (and the
+// commit), as the issuing warps' own instructions are part of every score buffer's round.
 template <int D>
-__device__ __forceinline__ void issue_s(uint32_t tS, uint64_t q_desc, uint64_t k_desc) {
+__device__ __forceinline__ void issue_s(uint32_t tS, uint64_t q_desc, uint64_t k_desc, uint64_t* full) {
   constexpr uint32_t idesc = idesc_bf16_f32(BQ, BKV, false);
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k)          // K-major: a K step of 16 bf16 is 32 bytes along the swizzled row
-    tc_mma_bf16_warp(tS, desc_add(q_desc, k * 32), desc_add(k_desc, k * 32), idesc, k > 0 ? 1u : 0u);
+  // K-major: a K step of 16 bf16 is 32 bytes (2 descriptor units) along the swizzled row
+  if constexpr (D == 64) {
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 b1, %2, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 b2, %2, 4;\n\t"
+        "add.s64 a3, %1, 6;\n\tadd.s64 b3, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}\n"
+        :: "r"(tS), "l"(q_desc), "l"(k_desc), "r"(idesc), "r"(smem_u32(full)) : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a1, b1;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 b1, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}\n"
+        :: "r"(tS), "l"(q_desc), "l"(k_desc), "r"(idesc), "r"(smem_u32(full)) : "memory");
+  }
 }
 
 // O += P_h U_h for keys [64 h, 64 h + 64) of a tile: P lies in TMEM over the first 64
-// columns of its score buffer (two bf16 per column, row = lane; keys 64 h.. at column 32 h),
-// U is MN-major in shared memory (D contiguous per key).
+// columns of its score buffer (two bf16 per column, row = lane; keys 64 h.. at column 32 h; a K step of 16 keys: 8
+// columns), U is MN-major in shared memory (D contiguous per key; a K step: 16 rows, D * 2 descriptor units).
 template <int D>
 __device__ __forceinline__ void issue_pv_half(uint32_t tO, uint32_t tP, uint64_t u_desc, int h, bool accumulate) {
   using Cfg = AttnCfg<D>;
   constexpr uint32_t idesc = idesc_bf16_f32(BQ, D, true);     // U is MN-major (D contiguous)
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk)            // a K step of 16 keys: 8 TMEM columns of P, 16 rows of U
-    tc_mma_bf16_ts_warp(tO, tP + 32 * h + 8 * kk, desc_add(u_desc, (64 * h + 16 * kk) * Cfg::ROWB), idesc,
-                        (accumulate || kk > 0) ? 1u : 0u);
+  asm volatile(
+      "{\n\t.reg .pred e, f, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, %5;\n\tadd.s64 b2, b1, %5;\n\tadd.s64 b3, b2, %5;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}\n"
+      :: "r"(tO), "r"(tP + 32 * h), "l"(desc_add(u_desc, 64 * h * Cfg::ROWB)), "r"(idesc), "r"(accumulate ? 1u : 0u),
+         "n"(16 * Cfg::ROWB / 16) : "memory");
 }
 
 // What a launch computes, and how its items are cut.
@@ -132,7 +166,7 @@ __device__ __forceinline__ int item_of(const WinShape& w, int r) {
 // (its own window starts one tile later and that tile holds no sink).
 struct Item {
   int b, h, qt0, a, j0, n0, n;
-  bool two, skip;
+  int two, skip;
   __device__ __forceinline__ int tile(int i) const { return i < a ? i : j0 + (i - a); }
   __device__ __forceinline__ bool has1(int i) const { return two && !(skip && i == a); }
   __device__ __forceinline__ int first1() const { return skip && a == 0 ? 1 : 0; }
@@ -161,33 +195,37 @@ __device__ __forceinline__ Item decode_item(const WinShape& w, int item) {
   return x;
 }
 
-// Walks the score-tile sequence of one CTA for an issuing warp: item r, entry i, group g, with the ring position
-// of the item's entry 0.
-struct Cursor {
-  Item w;
-  int r, i, g;
-  uint32_t kvb;
-  bool valid;
-  __device__ __forceinline__ void load(const WinShape& s) {
-    const int item = item_of(s, r);
-    valid = item >= 0;
-    if (valid) w = decode_item(s, item);
-  }
-  __device__ __forceinline__ void advance(const WinShape& s) {
-    if (g == 0 && w.has1(i)) { g = 1; return; }
-    if (++i < w.n) { g = (i < w.n0) ? 0 : 1; return; }
-    kvb += w.n;
-    ++r;
-    i = 0;
-    g = 0;
-    load(s);
-  }
-  __device__ __forceinline__ uint32_t pos() const { return kvb + i; }
-  __device__ __forceinline__ bool first_of_group() const { return g == 0 ? i == 0 : i == w.first1(); }
-  // the element is the last MMA reader of its ring position / the item's last score tile
-  __device__ __forceinline__ bool last_of_pos() const { return g == 1 || !w.has1(i); }
-  __device__ __forceinline__ bool last_of_item() const { return i == w.n - 1 && last_of_pos(); }
-};
+// The CTA's r-th item from the producer, which decodes it (a chain of divisions that the other warps would wait for)
+// and announces it through a ring of SR slots; n = 0 ends the list.
+__device__ __forceinline__ bool next_item(AttnBars* bars, int r, Item& x, volatile int* abort_flag, int* err, int lane) {
+  const int slot = r % SR;
+  if (!mbar_wait_warp(&bars->item_full[slot], static_cast<uint32_t>(r / SR) & 1u, abort_flag, err)) return false;
+  const int4* v = reinterpret_cast<const int4*>(bars->item[slot]);
+  const int4 p = v[0], q = v[1];
+  x.b = p.x;
+  x.h = p.y;
+  x.qt0 = p.z;
+  x.a = p.w;
+  x.j0 = q.x;
+  x.n0 = q.y;
+  x.n = q.z;
+  x.two = q.w & 1;
+  x.skip = q.w >> 1;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
+  return x.n > 0;
+}
+
+__device__ __forceinline__ void load_chunk(uint32_t col, uint32_t (&v)[64]) {
+  tmem_ld_32x32b_x64(col, v);
+  tmem_ld_wait();
+}
+__device__ __forceinline__ void load_chunk(uint32_t col, uint32_t (&v)[32]) {
+  tmem_ld_32x32b_x32(col, v);
+  tmem_ld_wait();
+}
+__device__ __forceinline__ void store_chunk(uint32_t col, const uint32_t (&v)[32]) { tmem_st_32x32b_x32(col, v); }
+__device__ __forceinline__ void store_chunk(uint32_t col, const uint32_t (&v)[16]) { tmem_st_32x32b_x16(col, v); }
 
 // 16-byte unit u of row r of a staging box (rows of ROWB bytes) in the TMA swizzle of that width.
 template <int ROWB>
@@ -217,23 +255,24 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
   const int kcol = H * D, ucol = (H + H / w.G) * D;    // first key and value columns of a row
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->q_empty[i], 1);
-      for (int k = 0; k < 3; ++k) mbar_init(&bars->o_full[i][k], 1);
-    }
+    mbar_init(&bars->q_empty[0], 1);
+    mbar_init(&bars->q_empty[1], 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bars->kv_full[i], 1);
-      mbar_init(&bars->kv_empty[i], 2);                // K read by the score warp, U by the P U warp
+      mbar_init(&bars->kv_empty[i], 1);
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&bars->s_full[0][i], 1);
       mbar_init(&bars->s_full[1][i], 1);
-      mbar_init(&bars->p_full[i][0], 4);
-      mbar_init(&bars->p_full[i][1], 4);
+      mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->pv_done[i], 1);
     }
     mbar_init(&bars->drain[0], 1);
     mbar_init(&bars->drain[1], 1);
+    for (int i = 0; i < SR; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], kConsumers);
+    }
     bars->abort_flag = 0;
     fence_barrier_init();
   }
@@ -257,8 +296,15 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       bool ok = true;
       for (int r = 0; ok; ++r) {
         const int item = item_of(w, r);
+        const int slot = r % SR;
+        if (r >= SR && !mbar_wait(&bars->item_empty[slot], static_cast<uint32_t>(r / SR - 1) & 1u, abort_flag, err)) break;
+        Item x = {};
+        if (item >= 0) x = decode_item(w, item);
+        int4* v = reinterpret_cast<int4*>(bars->item[slot]);
+        v[0] = make_int4(x.b, x.h, x.qt0, x.a);
+        v[1] = make_int4(x.j0, x.n0, x.n, x.two | (x.skip << 1));
+        mbar_arrive(&bars->item_full[slot]);
         if (item < 0) break;
-        const Item x = decode_item(w, item);
         const int kh = x.h / w.G;                    // key head
         const int qb = r & 1;                        // Q buffer of this item; its previous user was item r - 2
         if (r >= 2 && !mbar_wait(&bars->q_empty[qb], static_cast<uint32_t>((r >> 1) - 1) & 1u, abort_flag, err)) break;
@@ -297,62 +343,57 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       const uint64_t dq0 = smem_desc(smem_u32(sQ), 16, 8 * Cfg::ROWB, Cfg::SWZ);
       const uint64_t dk0 = smem_desc(smem_u32(sK), 16, 8 * Cfg::ROWB, Cfg::SWZ);
       const uint64_t du0 = smem_desc(smem_u32(sU), Cfg::TILE, 8 * Cfg::ROWB, Cfg::SWZ);
-      Cursor c;
-      c.r = 0;
-      c.i = 0;
-      c.g = 0;
-      c.kvb = 0;
-      c.load(w);
+      Item x;
       uint32_t b = 0;                                // buffer of number k (k % 3)
       uint32_t bits = 0;                             // phase per buffer of the barrier this warp waits on
+      uint32_t pos = 0;                              // ring position
+      bool ok = true;
       if (pv_warp) {
-        uint32_t oi0 = 0, oi1 = 0;                   // next o_full barrier per group (P U count % 3)
-        while (c.valid) {
-          const uint32_t st = c.pos() % NS;
-          const uint32_t tOg = tmem_base + kColO + 64 * c.g;
-          // keys [0, 64) as soon as the group releases them, then keys [64, 128)
-          if (!mbar_wait_warp(&bars->p_full[b][0], (bits >> b) & 1u, abort_flag, err)) break;
-          tc_fence_after();
-          issue_pv_half<D>(tOg, tmem_base + 128 * b, desc_add(du0, st * Cfg::TILE), 0, !c.first_of_group());
-          if (!mbar_wait_warp(&bars->p_full[b][1], (bits >> b) & 1u, abort_flag, err)) break;
-          bits ^= 1u << b;
-          tc_fence_after();
-          issue_pv_half<D>(tOg, tmem_base + 128 * b, desc_add(du0, st * Cfg::TILE), 1, true);
-          tc_commit_warp(&bars->pv_done[b]);
-          if (c.g) {
-            tc_commit_warp(&bars->o_full[1][oi1]);
-            oi1 = oi1 == 2 ? 0 : oi1 + 1;
-          } else {
-            tc_commit_warp(&bars->o_full[0][oi0]);
-            oi0 = oi0 == 2 ? 0 : oi0 + 1;
+        for (int r = 0; ok && next_item(bars, r, x, abort_flag, err, lane); ++r) {
+          const int first1 = x.first1();
+          for (int i = 0; i < x.n && ok; ++i, ++pos) {
+            const uint32_t st = pos % NS;
+            const uint64_t du = desc_add(du0, st * Cfg::TILE);
+            const int g_end = x.has1(i) ? 2 : 1;
+#pragma unroll 1
+            for (int g = i < x.n0 ? 0 : 1; g < g_end; ++g) {
+              const uint32_t tOg = tmem_base + kColO + 64 * g, tP = tmem_base + 128 * b;
+              const bool more = i > (g ? first1 : 0);
+              if (!mbar_wait_warp(&bars->p_full[b], (bits >> b) & 1u, abort_flag, err)) { ok = false; break; }
+              bits ^= 1u << b;
+              tc_fence_after();
+              issue_pv_half<D>(tOg, tP, du, 0, more);
+              issue_pv_half<D>(tOg, tP, du, 1, true);
+              tc_commit_warp(&bars->pv_done[b]);
+              b = b == NSB - 1 ? 0 : b + 1;
+            }
+            // U_j is consumed, and K_j: every P was made of a score
+            if (ok) tc_commit_warp(&bars->kv_empty[st]);
           }
-          if (c.last_of_pos()) tc_commit_warp(&bars->kv_empty[st]);   // U_j is consumed
-          c.advance(w);
-          b = b == NSB - 1 ? 0 : b + 1;
         }
       } else {
-        uint32_t n = 0;                              // score number
-        uint32_t waited = 0xffffffffu;               // ring position whose K/U (and Q) was last waited for
-        while (c.valid) {
-          if (n >= NSB) {                            // the P U that read this buffer has completed
-            if (!mbar_wait_warp(&bars->pv_done[b], (bits >> b) & 1u, abort_flag, err)) break;
-            bits ^= 1u << b;
+        uint32_t n = 0;                              // scores so far, up to NSB
+        for (int r = 0; ok && next_item(bars, r, x, abort_flag, err, lane); ++r) {
+          const uint32_t qb = static_cast<uint32_t>(r) & 1u;
+          for (int i = 0; i < x.n && ok; ++i, ++pos) {
+            const uint32_t st = pos % NS;
+            if (!mbar_wait_warp(&bars->kv_full[st], (pos / NS) & 1u, abort_flag, err)) { ok = false; break; }
+            const uint64_t dk = desc_add(dk0, st * Cfg::TILE);
+            const int g_end = x.has1(i) ? 2 : 1;
+#pragma unroll 1
+            for (int g = i < x.n0 ? 0 : 1; g < g_end; ++g) {
+              if (n == NSB) {                        // the P U that read this buffer has completed
+                if (!mbar_wait_warp(&bars->pv_done[b], (bits >> b) & 1u, abort_flag, err)) { ok = false; break; }
+                bits ^= 1u << b;
+              } else {
+                ++n;
+              }
+              tc_fence_after();
+              issue_s<D>(tmem_base + 128 * b, desc_add(dq0, (2 * qb + g) * Cfg::TILE), dk, &bars->s_full[g][b]);
+              b = b == NSB - 1 ? 0 : b + 1;
+            }
           }
-          const uint32_t pos = c.pos();
-          const uint32_t st = pos % NS;
-          if (pos != waited) {
-            if (!mbar_wait_warp(&bars->kv_full[st], (pos / NS) & 1u, abort_flag, err)) break;
-            waited = pos;
-          }
-          tc_fence_after();
-          const uint32_t qb = static_cast<uint32_t>(c.r) & 1u;
-          issue_s<D>(tmem_base + 128 * b, desc_add(dq0, (2 * qb + c.g) * Cfg::TILE), desc_add(dk0, st * Cfg::TILE));
-          tc_commit_warp(c.g ? &bars->s_full[1][b] : &bars->s_full[0][b]);
-          if (c.last_of_pos()) tc_commit_warp(&bars->kv_empty[st]);   // K_j is consumed
-          if (c.last_of_item()) tc_commit_warp(&bars->q_empty[qb]);   // every S of the item has read its Q
-          c.advance(w);
-          b = b == NSB - 1 ? 0 : b + 1;
-          ++n;
+          if (ok) tc_commit_warp(&bars->q_empty[qb]);   // every S of the item has read its Q
         }
       }
       uint64_t* dr = &bars->drain[pv_warp ? 0 : 1];
@@ -368,7 +409,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
     const uint32_t tO = tmem_base + kColO + 64 * g + lane_off;
     uint8_t* stg = smem_raw + Cfg::OFF_STG + (warp - 2) * Cfg::STG;
     uint32_t kbase = 0;                               // score number of the item's first tile
-    uint32_t tiles = 0;                               // this group's tiles so far (its P U numbering)
+    uint32_t last = 0;                                // the number of this group's previous score tile
     uint32_t used0 = 0, used1 = 0, used2 = 0;         // this group's score tiles so far in buffers 0, 1, 2
     bool ok = true;
     const float2 sc2 = make_float2(scale_log2, scale_log2);
@@ -379,9 +420,9 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
     float pl = 0.0f;                                  // the pending item's running sum
     float pm = 0.0f;                                  // and its running max (log2 units)
     int pb = 0, ph = 0, pqt = 0;                      // its batch row, head and query tile
-    uint32_t plast = 0;                               // its last tile (this group's numbering)
+    uint32_t plast = 0;                               // the number of its last score tile
     auto write_out = [&]() -> bool {
-      if (!mbar_wait_warp(&bars->o_full[g][plast % 3], (plast / 3) & 1u, abort_flag, err)) return false;
+      if (!mbar_wait_warp(&bars->pv_done[plast % NSB], (plast / NSB) & 1u, abort_flag, err)) return false;
       tc_fence_after();
       const float inv = 1.0f / pl;
       uint32_t ov[D];
@@ -421,9 +462,8 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
     };
     const int wrow = sub * 32;                        // first row of this warp within the tile
     for (int r = 0; ok; ++r) {
-      const int item = item_of(w, r);
-      if (item < 0) break;
-      const Item x = decode_item(w, item);
+      Item x;
+      if (!next_item(bars, r, x, abort_flag, err, lane)) break;
       const uint32_t knext = kbase + x.total();
       if (g == 1 && !x.two) { kbase = knext; continue; }   // group 1 without a query tile
       const int qt = x.qt0 + g;
@@ -432,6 +472,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       const int i0 = g == 0 ? 0 : x.first1(), i1 = g == 0 ? x.n0 : x.n;
       float mr = -INFINITY;                           // running (lazily raised) reference, log2 units
       float l = 0.0f;                                 // running sum of 2^(s - mr)
+      bool ready = false;                             // every row of the warp has a reference
       for (int i = i0; i < i1 && ok; ++i) {
         if (g == 1 && !x.has1(i)) continue;
         const bool first = i == i0;
@@ -443,150 +484,183 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
         tc_fence_after();
         const uint32_t tS = tmem_base + 128 * b + lane_off;
         const int kb = x.tile(i) * BKV;               // first key of the tile
-        // bit n set: this row sees key kb_half + n
-        auto seen_bits = [&](int kb_half) -> uint64_t {
-          const int hi = t - kb_half;                 // last key of the row
+        // bit n set: this row sees key k0 + n
+        auto seen_bits = [&](int k0) -> uint32_t {
+          const int hi = t - k0;                      // last key of the row
           const int lo = hi - w.window + 1;           // first key of its window
-          const uint64_t to_hi = hi < 0 ? 0ull : (hi >= 63 ? ~0ull : (2ull << hi) - 1ull);
-          const uint64_t from_lo = lo <= 0 ? ~0ull : (lo >= 64 ? 0ull : ~0ull << lo);
-          const int ns = w.sinks - kb_half;
-          const uint64_t sinks = ns <= 0 ? 0ull : (ns >= 64 ? ~0ull : (1ull << ns) - 1ull);
+          const uint32_t to_hi = hi < 0 ? 0u : (hi >= 31 ? ~0u : (2u << hi) - 1u);
+          const uint32_t from_lo = lo <= 0 ? ~0u : (lo >= 32 ? 0u : ~0u << lo);
+          const int ns = w.sinks - k0;
+          const uint32_t sinks = ns <= 0 ? 0u : (ns >= 32 ? ~0u : (1u << ns) - 1u);
           return to_hi & (from_lo | sinks);
         };
-        // pv = 2^(s*scale - mr) in place of the scores, two keys per f32x2 instruction; 0 for the keys that the
-        // row does not see (masked: some row of the warp misses some key of the half); returns the sum
-        auto probs = [&](uint32_t (&v)[64], bool masked, uint64_t seen) -> float {
-          const float nm = mr == -INFINITY ? 0.0f : -mr;      // no key seen yet: every probability is masked to 0
-          const float2 nm2 = make_float2(nm, nm);
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
-              const uint32_t word = i < 32 ? static_cast<uint32_t>(seen) : static_cast<uint32_t>(seen >> 32);
-              v[i] = (word >> (i & 31)) & 1u ? __float_as_uint(ex2_approx(e.x)) : 0u;
-              v[i + 1] = (word >> ((i + 1) & 31)) & 1u ? __float_as_uint(ex2_approx(e.y)) : 0u;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
-              v[i] = __float_as_uint(ex2_approx(e.x));
-              v[i + 1] = __float_as_uint(ex2_approx(e.y));
-            }
-          }
-          float2 ls[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) ls[q] = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int i = 0; i < 64; i += 2)
-            ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-          const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
-          return l2.x + l2.y;
-        };
-        // exact maximum of the seen keys of one half, eight independent chains (-inf: none)
-        auto half_max = [&](const uint32_t (&v)[64], uint64_t seen) -> float {
-          float mx8[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) mx8[q] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float lo = (static_cast<uint32_t>(seen) >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY;
-            const float hi = (static_cast<uint32_t>(seen >> 32) >> i) & 1u ? __uint_as_float(v[32 + i]) : -INFINITY;
-            mx8[i & 7] = fmax3(mx8[i & 7], lo, hi);
-          }
-          return fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-        };
-        // The two 64-key halves in turn. A half's probabilities are final once its sum is checked
-        // (and, rarely, recomputed against a raised max); they are then stored as bf16 pairs over
-        // columns [32 hf, 32 hf + 32) of the buffer, whose scores are already in registers.
+        // some row of the warp (tw .. tw + 31) misses some of keys k .. k + 31 (warp-uniform)
+        auto crossed = [&](int k) { return k + 31 > tw || (k <= tw + 31 - w.window && k + 32 > w.sinks); };
+        // The tile's keys, CH at a time. A chunk's probabilities are final once its sum is checked (and, rarely,
+        // recomputed against a raised reference); they are then stored as bf16 pairs over the buffer's first
+        // columns, whose scores have been read. One copy of each loop: the warps' code has to fit the
+        // instruction cache.
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t tSh = tS + 64 * hf;
-          const int kbh = kb + 64 * hf;
-          // what the warp's rows tw .. tw + 31 see of keys kbh .. kbh + 63 (warp-uniform)
-          const bool dead = kbh > tw + 31 || (kbh + 63 <= tw - w.window && kbh >= w.sinks);
-          uint32_t pk[32];
-          if (!dead) {
-          const bool masked = kbh + 63 > tw || (kbh <= tw + 31 - w.window && kbh + 64 > w.sinks);
-          const uint64_t seen = masked ? seen_bits(kbh) : ~0ull;
-          uint32_t sv[64];
-          tmem_ld_32x32b_x64(tSh, sv);
-          tmem_ld_wait();
-          if (first && hf == 0 && kb == 0 && (w.sinks > 0 || tw + 31 < w.window)) {
-            mr = __uint_as_float(sv[0]) * scale_log2;         // key 0 is seen by every row of the warp
-          } else if (__any_sync(0xffffffffu, mr == -INFINITY)) {
-            const float m0 = half_max(sv, seen) * scale_log2;
-            if (mr == -INFINITY) mr = m0;
-          }
-          float lt = probs(sv, masked, seen);
-          if (__any_sync(0xffffffffu, !(lt <= kSumLimit))) {
-            // rare: this half's exact maximum, a rescale of the running output and sum (and of
-            // the first half's stored probabilities) where the max grew by more than 2^8, and
-            // the half again against the new reference
-            tmem_ld_32x32b_x64(tSh, sv);
-            tmem_ld_wait();
-            const float m_new = fmaxf(mr, half_max(sv, seen) * scale_log2);
-            const bool need = m_new > mr + kRescaleLog2;
-            if (__any_sync(0xffffffffu, need)) {
-              const float alpha = need ? ex2_approx(mr - m_new) : 1.0f;
-              if (need) mr = m_new;
-              l *= alpha;
-              if (!first) {
-                // every earlier P U of the group has completed (its own numbering, barrier i % 3)
-                const uint32_t last = tiles - 1;
-                if (!mbar_wait_warp(&bars->o_full[g][last % 3], (last / 3) & 1u, abort_flag, err)) { ok = false; break; }
-                tc_fence_after();
+        for (int c = 0; c < BKV / CH; ++c) {
+          const int k0 = kb + CH * c;
+          uint32_t pk[CH / 2];
+          // what the warp's rows tw .. tw + 31 see of the chunk: nothing; not everything (both warp-uniform)
+          const bool dead = k0 > tw + 31 || (k0 + CH - 1 <= tw - w.window && k0 >= w.sinks);
+          if (dead) {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                  uint32_t o[32];
-                  tmem_ld_32x32b_x32(tO + c * 32, o);
+            for (int i = 0; i < CH / 2; ++i) pk[i] = 0u;
+          } else {
+            const bool masked = k0 + CH - 1 > tw || (k0 <= tw + 31 - w.window && k0 + CH > w.sinks);
+            float lt;
+            bool plain = ready;
+            if (plain) {
+              // every key is seen and every row has its reference: the score's whole way to a bf16 probability in one
+              // run of independent steps (with the mask's branch in the middle of it the exponentials, sums and
+              // roundings ran one after the other: 179 against 143 us for 12,001 tokens, W = 1500)
+              uint32_t v[CH];
+              load_chunk(tS + CH * c, v);
+              const float2 nm2 = make_float2(-mr, -mr);
+              float2 ls[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) ls[q] = make_float2(0.0f, 0.0f);
+              if (!masked) {
+#pragma unroll
+              for (int i = 0; i < CH; i += 2) {
+                const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
+                const float2 pr = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], pr);
+                pk[i / 2] = pack_bf16x2(pr.x, pr.y);
+              }
+              } else {
+                uint32_t seen[CH / 32];
+#pragma unroll
+                for (int q = 0; q < CH / 32; ++q) seen[q] = seen_bits(k0 + 32 * q);
+#pragma unroll
+                for (int i = 0; i < CH; i += 2) {
+                  const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
+                  const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+                  const float2 pr = make_float2((seen[i / 32] >> (i & 31)) & 1u ? p0 : 0.0f,
+                                                (seen[i / 32] >> ((i + 1) & 31)) & 1u ? p1 : 0.0f);
+                  ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], pr);
+                  pk[i / 2] = pack_bf16x2(pr.x, pr.y);
+                }
+              }
+              const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
+              lt = l2.x + l2.y;
+              plain = !__any_sync(0xffffffffu, !(lt <= kSumLimit));
+            }
+            if (!plain) {
+            uint32_t v[CH];
+#pragma unroll 1
+            for (bool again = false;;) {
+              load_chunk(tS + CH * c, v);
+              if (first && k0 == 0 && !again && (w.sinks > 0 || tw + 31 < w.window))
+                mr = __uint_as_float(v[0]) * scale_log2;      // key 0 is seen by every row of the warp
+              bool full = __any_sync(0xffffffffu, mr == -INFINITY) && !again;   // a row without a key so far
+              if (!full) {
+                // 2^(s*scale - mr) in place of the scores, two keys per f32x2 instruction; 0 for the keys that the
+                // row does not see (mr = -inf: none so far, nor here); their sum
+                const float nm = mr == -INFINITY ? 0.0f : -mr;
+                const float2 nm2 = make_float2(nm, nm);
+#pragma unroll
+                for (int i = 0; i < CH; i += 2) {
+                  const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
+                  v[i] = __float_as_uint(ex2_approx(e.x));
+                  v[i + 1] = __float_as_uint(ex2_approx(e.y));
+                }
+                if (masked) {
+#pragma unroll
+                  for (int q = 0; q < CH / 32; ++q) {
+                    if (!crossed(k0 + 32 * q)) continue;
+                    const uint32_t seen = seen_bits(k0 + 32 * q);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[32 * q + i] = (seen >> i) & 1u ? v[32 * q + i] : 0u;
+                  }
+                }
+                float2 ls[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ls[q] = make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
+#pragma unroll
+                for (int i = 8; i < CH; i += 2)
+                  ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
+                lt = l2.x + l2.y;
+                full = __any_sync(0xffffffffu, !(lt <= kSumLimit)) && !again;
+                if (!full) break;
+                load_chunk(tS + CH * c, v);                   // rare: the chunk again, against a raised reference
+              }
+              // the chunk's exact maximum; a rescale of the running output and sum (and of the tile's probabilities
+              // so far) where it passes the reference by more than 2^8
+              again = true;
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int q = 0; q < CH / 32; ++q) {
+                const uint32_t seen = masked ? seen_bits(k0 + 32 * q) : ~0u;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                  mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], (seen >> i) & 1u ? __uint_as_float(v[32 * q + i]) : -INFINITY,
+                                           (seen >> (i + 1)) & 1u ? __uint_as_float(v[32 * q + i + 1]) : -INFINITY);
+              }
+              const float m_new = fmaxf(mr, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2);
+              const bool fresh = mr == -INFINITY;             // l and the row's outputs are zero
+              const bool need = m_new > mr + kRescaleLog2;    // (true for a fresh row that sees a key here)
+              if (need) {
+                const float alpha = fresh ? 1.0f : ex2_approx(mr - m_new);
+                mr = m_new;
+                l *= alpha;
+                mx[0] = alpha;
+              } else {
+                mx[0] = 1.0f;
+              }
+              if (__any_sync(0xffffffffu, need && !fresh)) {
+                const float alpha = mx[0];
+                if (!first) {
+                  // every earlier P U of the group has completed
+                  if (!mbar_wait_warp(&bars->pv_done[last % NSB], (last / NSB) & 1u, abort_flag, err)) { ok = false; break; }
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int cc = 0; cc < D / 16; ++cc) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(tO + cc * 16, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                    tmem_st_32x32b_x16(tO + cc * 16, o);
+                  }
+                }
+                tmem_st_wait();
+#pragma unroll 1
+                for (int cc = 0; cc < c * (CH / 32); ++cc) {
+                  uint32_t q[16];
+                  tmem_ld_32x32b_x16(tS + 16 * cc, q);
                   tmem_ld_wait();
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                  tmem_st_32x32b_x32(tO + c * 32, o);
+                  for (int i = 0; i < 16; ++i) {
+                    const float2 f = unpack_bf16x2(q[i]);
+                    q[i] = pack_bf16x2(f.x * alpha, f.y * alpha);
+                  }
+                  tmem_st_32x32b_x16(tS + 16 * cc, q);
                 }
-              }
-              if (hf == 1) {                          // the first half's probabilities, already stored
                 tmem_st_wait();
-                uint32_t q[32];
-                tmem_ld_32x32b_x32(tS, q);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float2 f = unpack_bf16x2(q[i]);
-                  q[i] = pack_bf16x2(f.x * alpha, f.y * alpha);
-                }
-                tmem_st_32x32b_x32(tS, q);
               }
-              tmem_st_wait();
             }
-            tmem_ld_32x32b_x64(tSh, sv);
-            tmem_ld_wait();
-            lt = probs(sv, masked, seen);
-          }
-          l += lt;
+            if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) pk[i] = 0u;
+            for (int i = 0; i < CH / 2; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            ready = __all_sync(0xffffffffu, mr != -INFINITY);
+            }
+            l += lt;
           }
-          if (hf == 1) {
-            // the previous item's output leaves the accumulator before this item's first P U
-            if (first && pend && !write_out()) { ok = false; break; }
-            tmem_st_wait();                           // keys [0, 64) are final: hand them to the P U warp
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[b][0]);
-          }
-          tmem_st_32x32b_x32(tS + 32 * hf, pk);
+          // the previous item's output leaves the accumulator before this item's first P U
+          if (c == BKV / CH - 1 && first && pend && !write_out()) { ok = false; break; }
+          store_chunk(tS + CH / 2 * c, pk);
         }
         if (!ok) break;
         tmem_st_wait();
         tc_fence_before();                      // our TMEM reads of S and writes of P precede the next MMA
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[b][1]);
-        ++tiles;
+        if (lane == 0) mbar_arrive(&bars->p_full[b]);
+        last = k;
       }
       if (!ok) break;
       // the item's output is written during the group's next tile (or after the last item)
@@ -596,7 +670,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       pb = x.b;
       ph = x.h;
       pqt = qt;
-      plast = tiles - 1;
+      plast = last;
       kbase = knext;
     }
     if (ok && pend) write_out();
