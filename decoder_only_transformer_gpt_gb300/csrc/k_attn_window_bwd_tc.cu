@@ -809,8 +809,7 @@ bool plan_bwd(int B, int T, int H, int Hkv, int window, int sinks, int num_sms, 
 
 int sm_count() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
+  return device_sms(&dev, &n) == cudaSuccess ? n : 0;
 }
 
 template <int D>
@@ -820,7 +819,10 @@ cudaError_t launch_bwd_d(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, co
                          cudaStream_t s) {
   using Cfg = BwdCfg<D>;
   const WinBwdShape& w = plan.w;
-  cudaError_t e = cudaFuncSetAttribute(attn_window_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  static SmemLimit limit;
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e == cudaSuccess) e = limit.raise(attn_window_bwd_tc_kernel<D>, dev, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const int M = B * w.T, C = w.H * D;
   const float rsd = 1.0f / sqrtf(static_cast<float>(D));

@@ -689,11 +689,10 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tm, const CUtensorMap& tm_y, WinShape w, int* err, float* lse2, cudaStream_t s) {
   using Cfg = AttnCfg<D>;
+  static SmemLimit limit;
   int dev = 0, num_sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_window_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  cudaError_t e = device_sms(&dev, &num_sms);
+  if (e == cudaSuccess) e = limit.raise(attn_window_tc_kernel<D>, dev, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   // pairs of query tiles halve the K/U traffic; single tiles where pairs would leave SMs idle
   const long long pairs = static_cast<long long>((w.n_qtiles + 1) / 2) * w.BH;

@@ -871,16 +871,16 @@ template <int D, int QR>
 cudaError_t launch_decode(const PagedCache& c, const __nv_bfloat16* qkv, const int32_t* lens, __nv_bfloat16* y, float* lse2,
                           DecShape w, int* err, cudaStream_t s) {
   using Cfg = DecCfg<D, QR>;
+  static SmemLimit limit;
   int dev = 0, num_sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device_sms(&dev, &num_sms);
   if (e != cudaSuccess) return e;
   // one block per SM with as many warps (rings) as its shared memory holds beside the lists, 8 at most
   const size_t lists = (2 * static_cast<size_t>(w.B) + 1) * sizeof(int);
   const size_t room = 232448 - 256 - lists;
   const int warps = room / Cfg::WARP < 8 ? static_cast<int>(room / Cfg::WARP) : 8;
   const size_t smem = static_cast<size_t>(warps) * Cfg::WARP + lists;
-  e = cudaFuncSetAttribute(paged_split_kernel<D, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  e = limit.raise(paged_split_kernel<D, QR>, dev, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int NW = num_sms * warps;
   long long seen_max = static_cast<long long>(c.max_pages) << c.page_log2;
@@ -943,7 +943,10 @@ cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const i
   // 46.7 and 32.7 us (48 lists)
   const int nt = rows <= 4096 ? 512 : 1024;
   auto choose = nt == 512 ? paged_choose_kernel<512> : paged_choose_kernel<1024>;
-  cudaError_t e = cudaFuncSetAttribute(choose, cudaFuncAttributeMaxDynamicSharedMemorySize, room * 4);
+  static SmemLimit limit[2];
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e == cudaSuccess) e = limit[nt == 512 ? 0 : 1].raise(choose, dev, room * 4);
   if (e != cudaSuccess) return e;
   e = launch_k(choose, lists, dim3(nt), static_cast<size_t>(room) * 4, s, c, lens, new_lens, kept, budget, sinks, recent,
                room, err);
