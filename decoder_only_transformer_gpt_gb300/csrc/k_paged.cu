@@ -8,6 +8,7 @@
 #include "kernels.h"
 #include "launch.h"
 
+#include <cooperative_groups.h>
 #include <math.h>
 
 namespace gptgb {
@@ -636,85 +637,118 @@ __device__ __forceinline__ uint32_t weight_rank(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Two kernels. The first chooses the rows of one (sequence, key head) per block: it turns the weights into ranks in
-// shared memory once (through the table, all loads independent; lists that do not fit are read again by each pass),
-// finds the rank of the smallest kept weight by three passes over 11, 11 and 10 bits (a histogram of the rows that
-// agree so far), and writes the kept rows in order: every warp counts its own stretch of rows, then places them
-// behind the stretches before. Equal weights are kept from the lowest row on. The second moves the rows.
+// Two kernels. The first chooses the rows of one (sequence, key head): a cluster of NC blocks holds the weights between
+// the sinks and the recent rows as ranks in shared memory, a stretch each (read once, through the table, all loads
+// independent; a list that does not fit is read again by each pass). Three passes over 11, 11 and 10 bits find the
+// rank of the smallest kept weight: a histogram of the rows that agree so far, summed over the blocks, whose bins are
+// scanned from the top. Then every warp counts its stretch of rows, and places them behind the stretches before it.
+// Equal weights are kept from the lowest row on. Bound by issuing about 200 instructions a row, so long lists are
+// spread over four SMs (10,000 to 20,000 rows, 48 lists: 24 us with one block of 1024 threads each).
+constexpr int kEvThreads = 512;
+constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
 
-template <int kEvThreads>
+template <int NC>
 __global__ void __launch_bounds__(kEvThreads)
 paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __restrict__ new_lens,
                     int32_t* __restrict__ kept, int budget, int sinks, int recent, int room, int* err) {
+  namespace cg = cooperative_groups;
   pdl_wait();
   pdl_trigger();
-  constexpr int kEvWarps = kEvThreads / 32;
-  extern __shared__ uint32_t s_rank[];               // [room] ranks of rows sinks, sinks + 1, ..
+  extern __shared__ uint32_t s_rank[];               // [room] ranks of this block's stretch
   __shared__ int hist[kEvBins];
-  __shared__ int s_sum[kEvWarps], s_tie[kEvWarps], pick[2];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int s_sum[kEvWarps], s_tie[kEvWarps], pick[2], s_total[2];
+  const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC), h = static_cast<int>(blockIdx.x / NC), b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pmask = (1 << c.page_log2) - 1;
   const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
   int32_t* out = kept + (static_cast<size_t>(b) * c.Hkv + h) * budget;
+  auto sync_all = [&]() {
+    if constexpr (NC == 1) __syncthreads();
+    else cg::this_cluster().sync();
+  };
   int n = __ldg(lens + b);
   if (n > static_cast<long long>(c.max_pages) << c.page_log2) {
     if (tid == 0) record_error(err, GPT_DEV_EPAGE);
     n = 0;
   }
   const int m = min(n, budget);                      // rows kept
-  if (h == 0 && tid == 0) new_lens[b] = m;
-  for (int i = max(m, 0) + tid; i < budget; i += kEvThreads) out[i] = -1;
-  if (n <= budget) {
-    for (int i = tid; i < m; i += kEvThreads) out[i] = i;
+  const int me = part * kEvThreads + tid;            // thread of the cluster
+  if (h == 0 && me == 0) new_lens[b] = m;
+  for (int i = max(m, 0) + me; i < budget; i += NC * kEvThreads) out[i] = -1;
+  if (n <= budget) {                                 // (the same for the whole cluster)
+    for (int i = me; i < m; i += NC * kEvThreads) out[i] = i;
     return;
   }
   const int lo = sinks, mid = n - recent - sinks;    // rows chosen by weight: lo .. lo + mid - 1
+  for (int i = me; i < sinks; i += NC * kEvThreads) out[i] = i;
+  for (int i = me; i < recent; i += NC * kEvThreads) out[budget - recent + i] = n - recent + i;
   int want = budget - sinks - recent;                // how many of them
-  const bool any = want > 0, fits = mid <= room;
+  if (want == 0) return;
+  const int each = ((mid + NC - 1) / NC + 31) / 32 * 32;
+  const int base = min(mid, part * each), size = min(mid - base, each);   // this block's stretch
+  const bool fits = each <= room;
   auto load = [&](int i) -> uint32_t {
-    const int r = lo + i, pg = page_of(c, trow, r, err);
+    const int r = lo + base + i, pg = page_of(c, trow, r, err);
     return pg < 0 ? 0u : weight_rank(__ldg(c.weight + weight_at(c, pg, h, r & pmask)));
   };
-  if (any && fits) {
+  for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
+  __syncthreads();
+  if (fits) {
     // K pages, then K weights in flight per thread: bad pages are looked at behind the loads (a branch between them
-    // had every load wait for the one before: 49 us instead of 20 for 15,000 rows)
-    constexpr int K = 4;
-    for (int i0 = tid; i0 < mid; i0 += K * kEvThreads) {
+    // had every load wait for the one before)
+    constexpr int K = 8;
+    for (int i0 = tid; i0 < size; i0 += K * kEvThreads) {
       int pg[K];
       float wt[K];
 #pragma unroll
-      for (int j = 0; j < K; ++j) pg[j] = __ldg(trow + ((lo + min(i0 + j * kEvThreads, mid - 1)) >> c.page_log2));
+      for (int j = 0; j < K; ++j) pg[j] = __ldg(trow + ((lo + base + min(i0 + j * kEvThreads, size - 1)) >> c.page_log2));
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         const int p = static_cast<unsigned>(pg[j]) < static_cast<unsigned>(c.pages) ? pg[j] : 0;
-        wt[j] = __ldg(c.weight + weight_at(c, p, h, (lo + min(i0 + j * kEvThreads, mid - 1)) & pmask));
+        wt[j] = __ldg(c.weight + weight_at(c, p, h, (lo + base + min(i0 + j * kEvThreads, size - 1)) & pmask));
       }
 #pragma unroll
       for (int j = 0; j < K; ++j) {
+        if (i0 + j * kEvThreads >= size) break;
         const bool ok = static_cast<unsigned>(pg[j]) < static_cast<unsigned>(c.pages);
         if (!ok) record_error(err, GPT_DEV_EPAGE);
-        if (i0 + j * kEvThreads < mid) s_rank[i0 + j * kEvThreads] = ok ? weight_rank(wt[j]) : 0u;
+        const uint32_t k = ok ? weight_rank(wt[j]) : 0u;
+        s_rank[i0 + j * kEvThreads] = k;
+        atomicAdd(&hist[k >> 21], 1);                // the first pass
       }
     }
+  } else {
+    for (int i = tid; i < size; i += kEvThreads) atomicAdd(&hist[load(i) >> 21], 1);
   }
-  auto rank = [&](int i) { return fits ? s_rank[i] : load(i); };
   uint32_t prefix = 0;                               // the leading bits of the smallest kept rank
   int low = 32;                                      // bits below them
-  for (int pass = 0; pass < 3 && any; ++pass) {
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass == 2 ? 10 : 11, shift = low - bits;
-    for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < mid; i += kEvThreads) {
-      const uint32_t k = rank(i);
-      if (low == 32 || (k >> low) == (prefix >> low)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+    if (pass > 0) {
+      for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < size; i += kEvThreads) {
+        const uint32_t k = fits ? s_rank[i] : load(i);
+        if ((k >> low) == (prefix >> low)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+      }
     }
-    __syncthreads();
+    sync_all();                                      // every block's histogram is complete
     // the bin where the count from the top reaches `want`: thread t sums bins 4 t .. 4 t + 3
     constexpr int BPT = kEvBins / kEvThreads;
-    int c4[BPT], own = 0;
+    static_assert(BPT == 4, "one 16-byte load per histogram");
+    int c4[BPT] = {};
 #pragma unroll
-    for (int j = 0; j < BPT; ++j) own += c4[j] = hist[tid * BPT + j];
+    for (int k = 0; k < NC; ++k) {
+      const int* other = NC == 1 ? hist : cg::this_cluster().map_shared_rank(hist, k);
+      const int4 x = *reinterpret_cast<const int4*>(other + tid * BPT);
+      c4[0] += x.x;
+      c4[1] += x.y;
+      c4[2] += x.z;
+      c4[3] += x.w;
+    }
+    const int own = c4[0] + c4[1] + c4[2] + c4[3];
     int above = own;                                 // counts of this and the later lanes
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
@@ -722,10 +756,10 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
       if (lane + k < 32) above += v;
     }
     if (lane == 0) s_sum[warp] = above;
-    __syncthreads();
+    sync_all();                                      // sums are written, and no block reads another's histogram any more
     for (int w = warp + 1; w < kEvWarps; ++w) above += s_sum[w];
     above -= own;                                    // rows in bins behind this thread's
-    if (above < want && above + own >= want) {       // one thread
+    if (above < want && above + own >= want) {       // one thread of each block
       int left = want - above, j = BPT - 1;
 #pragma unroll
       for (int k = BPT - 1; k > 0; --k)
@@ -738,22 +772,15 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
     want = pick[1];
     low = shift;
   }
-  // kept: every row of a rank above prefix, the first `want` of rank prefix, and the rows outside [lo, lo + mid)
-  const int per = ((n + kEvWarps - 1) / kEvWarps + 31) / 32 * 32;   // rows of a warp's stretch
-  const int first = min(n, warp * per), end = min(n, first + per);
-  auto kind = [&](int r) -> int {                    // 2 kept, 1 of rank prefix, 0 gone
-    const int i = r - lo;
-    if (r >= end) return 0;
-    if (i < 0 || i >= mid) return 2;
-    if (!any) return 0;
-    const uint32_t k = rank(i);
-    return k > prefix ? 2 : (k == prefix ? 1 : 0);
-  };
+  // kept: every row of a rank above prefix and the first `want` of rank prefix
+  const int per = ((size + kEvWarps - 1) / kEvWarps + 31) / 32 * 32;   // rows of a warp's stretch
+  const int first = min(size, warp * per), end = min(size, first + per);
   int sure = 0, ties = 0;
-  for (int r0 = first; r0 < end; r0 += 32) {
-    const int k = kind(r0 + lane);
-    sure += __popc(__ballot_sync(0xffffffffu, k == 2));
-    ties += __popc(__ballot_sync(0xffffffffu, k == 1));
+  for (int i0 = first; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < end ? (fits ? s_rank[i] : load(i)) : 0u;
+    sure += __popc(__ballot_sync(0xffffffffu, i < end && k > prefix));
+    ties += __popc(__ballot_sync(0xffffffffu, i < end && k == prefix));
   }
   __syncthreads();
   if (lane == 0) {
@@ -761,21 +788,39 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
     s_tie[warp] = ties;
   }
   __syncthreads();
-  int at = 0, seen_ties = 0;
-  for (int w = 0; w < warp; ++w) {
-    at += s_sum[w];
-    seen_ties += s_tie[w];
+  int at = 0, seen_ties = 0, all = 0, all_ties = 0;
+  for (int w = 0; w < kEvWarps; ++w) {
+    if (w == warp) {
+      at = all;
+      seen_ties = all_ties;
+    }
+    all += s_sum[w];
+    all_ties += s_tie[w];
   }
-  at += min(seen_ties, want);                        // ties before this stretch that are kept
-  for (int r0 = first; r0 < end; r0 += 32) {
-    const int r = r0 + lane, k = kind(r);
-    const uint32_t tie = __ballot_sync(0xffffffffu, k == 1), below = (1u << lane) - 1u;
-    const bool keep = k == 2 || (k == 1 && seen_ties + __popc(tie & below) < want);
-    const uint32_t all = __ballot_sync(0xffffffffu, keep);
-    if (keep) out[at + __popc(all & below)] = r;
-    at += __popc(all);
+  if constexpr (NC > 1) {
+    if (tid == 0) {
+      s_total[0] = all;
+      s_total[1] = all_ties;
+    }
+    sync_all();
+    for (int k = 0; k < part; ++k) {
+      const int* other = cg::this_cluster().map_shared_rank(s_total, k);
+      at += other[0];
+      seen_ties += other[1];
+    }
+  }
+  at += lo + min(seen_ties, want);                   // sinks, rows kept before, and the kept ties among them
+  for (int i0 = first; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < end ? (fits ? s_rank[i] : load(i)) : 0u;
+    const uint32_t tie = __ballot_sync(0xffffffffu, i < end && k == prefix), below = (1u << lane) - 1u;
+    const bool keep = i < end && (k > prefix || (k == prefix && seen_ties + __popc(tie & below) < want));
+    const uint32_t mask = __ballot_sync(0xffffffffu, keep);
+    if (keep) out[at + __popc(mask & below)] = lo + base + i;
+    at += __popc(mask);
     seen_ties += __popc(tie);
   }
+  if constexpr (NC > 1) sync_all();                  // no block leaves while another reads its totals
 }
 
 // Moves the kept rows of one (sequence, key head), a cluster of blocks each: 8 D bytes per row, bound by memory. Row i
@@ -802,12 +847,8 @@ paged_move_kernel(PagedCache c, const int32_t* __restrict__ dst_table, int dst_m
   const bool in_place = __ldg(trow) == __ldg(drow);
   uint4* pool = static_cast<uint4*>(c.pool);
   const size_t vstep = (static_cast<size_t>(c.Hkv) << c.page_log2) * U;   // from a page's keys to its values
-  for (int i0 = 0; i0 < budget; i0 += CHUNK) {
-    if (__ldg(rows + i0) < 0) break;                 // behind the last row (the same for the whole cluster)
-    uint4 kx[K], vx[K];
-    float wx[K];
-    int r[K], src[K], dst[K];
-    // all row numbers, then all pages, then all rows in flight; page 0 stands in for a bad page until the check
+  int r[K], src[K], dst[K];
+  auto look_up = [&](int i0) {                       // the chunk's row numbers, then their pages, K in flight
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = i0 + (k * kMoveBlocks + part) * ROWS + threadIdx.x / U;
@@ -819,8 +860,18 @@ paged_move_kernel(PagedCache c, const int32_t* __restrict__ dst_table, int dst_m
       src[k] = __ldg(trow + (max(r[k], 0) >> c.page_log2));
       dst[k] = __ldg(drow + (min(i, budget - 1) >> c.page_log2));
     }
+  };
+  look_up(0);
+  for (int i0 = 0; i0 < budget; i0 += CHUNK) {
+    if (__ldg(rows + i0) < 0) break;                 // behind the last row (the same for the whole cluster)
+    uint4 kx[K], vx[K];
+    float wx[K];
+    size_t to[K], wto[K];
+    bool go[K];
+    // page 0 stands in for a bad page until the check behind the loads
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      const int i = i0 + (k * kMoveBlocks + part) * ROWS + threadIdx.x / U;
       const bool ok = static_cast<unsigned>(src[k]) < static_cast<unsigned>(c.pages);
       const int pg = ok ? src[k] : 0, slot = max(r[k], 0) & pmask;
       const uint4* from = pool + row_at(c, pg, 0, h, slot) * U + u;
@@ -829,28 +880,22 @@ paged_move_kernel(PagedCache c, const int32_t* __restrict__ dst_table, int dst_m
         vx[k] = from[vstep];
         if (u == 0) wx[k] = c.weight[weight_at(c, pg, h, slot)];
       }
+      go[k] = r[k] >= 0 && ok && static_cast<unsigned>(dst[k]) < static_cast<unsigned>(c.pages);
+      if (r[k] >= 0 && !go[k]) record_error(err, GPT_DEV_EPAGE);
+      to[k] = row_at(c, go[k] ? dst[k] : 0, 0, h, i & pmask) * U + u;
+      wto[k] = weight_at(c, go[k] ? dst[k] : 0, h, i & pmask);
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (r[k] < 0) continue;
-      if (static_cast<unsigned>(src[k]) >= static_cast<unsigned>(c.pages) ||
-          static_cast<unsigned>(dst[k]) >= static_cast<unsigned>(c.pages)) {
-        record_error(err, GPT_DEV_EPAGE);
-        r[k] = -1;
-      }
-    }
+    if (i0 + CHUNK < budget) look_up(i0 + CHUNK);    // while the rows travel
     if (in_place) {
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (r[k] < 0) continue;
-      const int i = i0 + (k * kMoveBlocks + part) * ROWS + threadIdx.x / U;
-      uint4* to = pool + row_at(c, dst[k], 0, h, i & pmask) * U + u;
-      to[0] = kx[k];
-      to[vstep] = vx[k];
-      if (u == 0) c.weight[weight_at(c, dst[k], h, i & pmask)] = wx[k];
+      if (!go[k]) continue;
+      pool[to[k]] = kx[k];
+      pool[to[k] + vstep] = vx[k];
+      if (u == 0) c.weight[wto[k]] = wx[k];
     }
   }
 }
@@ -934,22 +979,31 @@ cudaError_t launch_paged_attention(const PagedCache& c, const void* qkv, const i
 cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const int32_t* dst_table, int dst_max_pages,
                                int32_t* new_lens, int32_t* kept, int B, int D, int budget, int sinks, int recent,
                                int* err, cudaStream_t s) {
-  // ranks for the longest list that the table allows, as far as shared memory goes
+  // one block per list up to 4,096 rows, clusters of four for longer lists; ranks for the longest stretch that the
+  // table allows, as far as shared memory goes
   const long long rows = (static_cast<long long>(c.max_pages) << c.page_log2) - sinks - recent;
-  const long long most = (232448 - 16384) / 4;
-  const int room = static_cast<int>(rows < 0 ? 0 : (rows < most ? rows : most));
-  const dim3 lists(static_cast<unsigned>(c.Hkv), static_cast<unsigned>(B));
-  // threads per list: 1,024 rows take 15.2 us with 512 threads and 20.7 with 1024 (192 lists); 10,000 to 20,000 rows
-  // 46.7 and 32.7 us (48 lists)
-  const int nt = rows <= 4096 ? 512 : 1024;
-  auto choose = nt == 512 ? paged_choose_kernel<512> : paged_choose_kernel<1024>;
+  const int nc = rows <= 4096 ? 1 : 4;
+  const long long most = (232448 - 16384) / 4, stretch = rows < 0 ? 0 : ((rows + nc - 1) / nc + 31) / 32 * 32;
+  const int room = static_cast<int>(stretch < most ? stretch : most);
+  auto choose = nc == 1 ? paged_choose_kernel<1> : paged_choose_kernel<4>;
   static SmemLimit limit[2];
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
-  if (e == cudaSuccess) e = limit[nt == 512 ? 0 : 1].raise(choose, dev, room * 4);
+  if (e == cudaSuccess) e = limit[nc == 1 ? 0 : 1].raise(choose, dev, room * 4);
   if (e != cudaSuccess) return e;
-  e = launch_k(choose, lists, dim3(nt), static_cast<size_t>(room) * 4, s, c, lens, new_lens, kept, budget, sinks, recent,
-               room, err);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(c.Hkv) * nc, static_cast<unsigned>(B));
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(room) * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(nc), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, choose, c, lens, new_lens, kept, budget, sinks, recent, room, err);
   if (e != cudaSuccess) return e;
   const dim3 grid(kMoveBlocks, static_cast<unsigned>(c.Hkv), static_cast<unsigned>(B));
   if (D == 64)

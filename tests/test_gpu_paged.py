@@ -351,7 +351,7 @@ def _evict_run(pool, weight, table, lens, dst, budget, sinks, recent):
 @pytest.mark.parametrize("lens,Hkv,D,page,budget,sinks,recent", [
     ([1], 1, 32, 8, 1, 0, 0), ([2, 3, 9], 2, 64, 8, 2, 0, 1), ([0, -1, 5, 40], 2, 32, 8, 4, 4, 0),
     ([100, 64, 63, 65, 700], 3, 64, 16, 64, 4, 16), ([100, 200], 1, 64, 32, 40, 10, 30), ([513, 1025, 2000], 2, 64, 64, 600, 0, 0),
-    ([5000], 1, 32, 256, 4999, 1, 1), ([60000, 100], 1, 32, 256, 700, 4, 64), ([3000, 20], 12, 64, 16, 1024, 16, 512)])
+    ([5000], 1, 32, 256, 4999, 1, 1), ([60000, 100], 1, 32, 256, 700, 4, 64), ([230000], 1, 32, 256, 900, 4, 64), ([3000, 20], 12, 64, 16, 1024, 16, 512)])
 @pytest.mark.parametrize("kind", ["plain", "ties", "nan"])
 def test_evict(gpt_lib, lens, Hkv, D, page, budget, sinks, recent, kind):
     case = _evict_case(len(lens) + budget, lens, Hkv, D, page, budget, kind == "ties", kind == "nan")
