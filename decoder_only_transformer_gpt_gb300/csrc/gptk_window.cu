@@ -57,18 +57,18 @@ int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, co
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int C = H * D, row = (H + 2 * Hkv) * D;
   const size_t M = static_cast<size_t>(B) * T;
-  // scratch on the stream: the fp32 dQ accumulator, Dsum, and the sums of key tiles that several CTAs share
-  const size_t acc_b = (M * C * sizeof(float) + 255) / 256 * 256, dsum_b = (M * H * sizeof(float) + 255) / 256 * 256;
+  // scratch on the stream: the fp32 dQ accumulator, the rows' values, and the sums of key tiles that several CTAs share
+  const size_t acc_b = (M * C * sizeof(float) + 255) / 256 * 256, row_b = attention_window_bwd_row_bytes(B, T, H);
   const size_t slab_b = attention_window_bwd_slab_bytes(B, T, H, Hkv, D, window, sinks);
   uint8_t* ws = nullptr;
-  cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&ws), acc_b + dsum_b + slab_b, s);
+  cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&ws), acc_b + row_b + slab_b, s);
   if (e != cudaSuccess) {
     set_detail("window attention derivative scratch", e);
     return e == cudaErrorMemoryAllocation ? GPT_ENOMEM : GPT_ECUDA;
   }
   float* dqacc = reinterpret_cast<float*>(ws);
-  float* dsum = reinterpret_cast<float*>(ws + acc_b);
-  float* slabs = reinterpret_cast<float*>(ws + acc_b + dsum_b);
+  float* rows = reinterpret_cast<float*>(ws + acc_b);
+  float* slabs = reinterpret_cast<float*>(ws + acc_b + row_b);
   CUtensorMap tq, tdy, tdkv, tdq;
   if (!(make_tmap_qkv(&tq, qkv, B, T, row, D) && make_tmap_qkv(&tdy, dy, B, T, C, D) &&
         make_tmap_attn_out(&tdkv, dqkv, B, T, row, D) && make_tmap_bt_f32(&tdq, dqacc, B, T, C))) {
@@ -76,7 +76,7 @@ int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, co
     set_detail_text("window attention derivative tensor maps");
     return GPT_ECUDA;
   }
-  e = launch_attention_window_bwd_tc(tq, tdy, tdkv, tdq, y, dy, lse2, dsum, dqacc, slabs, dqkv, B, T, H, Hkv, D, window, sinks,
+  e = launch_attention_window_bwd_tc(tq, tdy, tdkv, tdq, y, dy, lse2, rows, dqacc, slabs, dqkv, B, T, H, Hkv, D, window, sinks,
                                      err, s);
   scratch_free(ws, s);
   if (e != cudaSuccess) {

@@ -40,7 +40,7 @@ constexpr int BT = 128;                 // rows per key or query tile
 constexpr int HQ = 64;                  // queries per half tile
 constexpr int THREADS = 448;
 constexpr int TMEM_COLS = 512;
-constexpr int NQ = 2;                   // query-tile ring stages
+constexpr int NQ = 3;                   // query-tile ring stages
 constexpr int SR = 4;                   // items announced ahead
 constexpr int kConsumers = 13;          // warps that read each announced item: MMA, 8 derivative, 4 output
 constexpr float kLog2e = 1.4426950408889634f;
@@ -53,22 +53,22 @@ struct BwdCfg {
   static constexpr uint32_t SWZ = (ROWB == 128) ? SWZ_128B : SWZ_64B;
   static constexpr int TILE = BT * ROWB;
   static constexpr int OFF_K = 0;                                   // [2] item buffers
-  static constexpr int OFF_U = 2 * TILE;                            // [2]
-  static constexpr int OFF_Q = 4 * TILE;                            // [NQ]
+  static constexpr int OFF_U = 2 * TILE;                            // one: read once, into tensor memory
+  static constexpr int OFF_Q = 3 * TILE;                            // [NQ]
   static constexpr int OFF_DY = OFF_Q + NQ * TILE;                  // [NQ]
-  static constexpr int OFF_LD = OFF_DY + NQ * TILE;                 // [NQ][64 pairs] {-lse2 x2, -Dsum x2}
-  static constexpr int OFF_DS = (OFF_LD + NQ * BT * 8 + 1023) / 1024 * 1024;
+  static constexpr int OFF_LD = OFF_DY + NQ * TILE;                 // [2][64 pairs] {-lse2 x2, -Dsum x2}
+  static constexpr int OFF_DS = (OFF_LD + 2 * BT * 8 + 1023) / 1024 * 1024;
   static constexpr int DS_BUF = 2 * BT * 128;                       // one tile's dS: 2 atoms x 128 keys x 128 B
-  static constexpr int OFF_STG = OFF_DS + 2 * DS_BUF;               // 4 output warps x 2 boxes of 4 KB
-  static constexpr int OFF_BAR = OFF_STG + 4 * 8192;
+  static constexpr int OFF_STG = OFF_DS + 2 * DS_BUF;               // 4 output warps x one box of 4 KB
+  static constexpr int OFF_BAR = OFF_STG + 4 * 4096;
   static constexpr int SMEM = OFF_BAR + 512;
   static_assert(D == 32 || D == 64, "head width");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct __align__(16) BwdBars {
-  uint64_t kv_full[2], kv_empty[2];     // K_j, U_j of an item (buffer r % 2)
-  uint64_t q_full[NQ], q_empty[NQ];     // Q_i, dY_i, -lse2 and -Dsum of a query tile
+  uint64_t kv_full[2], kv_empty[2];     // K_j (buffer r % 2) and U_j of an item
+  uint64_t q_full[NQ], q_empty[NQ];     // Q_i, dY_i of a query tile (and its rows' -lse2 and -Dsum: two arrivals)
   uint64_t s_full[2];                   // S^T and dP^T of half g are in tensor memory
   uint64_t p_full[2];                   // the derivative warps wrote half g (4 warps)
   uint64_t dq_full;                     // the current tile's dQ product has completed
@@ -168,6 +168,12 @@ __device__ __forceinline__ int swz_unit(int rowb, int r, int u) {
   return (rowb == 128) ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
 }
 
+// `bytes` contiguous bytes into shared memory (both 16-byte aligned), counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
 // One half tile of the softmax derivative for this thread's key row: reads S^T and dP^T (64 queries
 // each) from columns [col, col + 64) and [col + 64, col + 128), writes P^T and dS^T as bf16 pairs
 // over [col, col + 32) and [col + 64, col + 96), and dS^T into the row's 128-byte slot `ds_row` of a
@@ -179,6 +185,7 @@ __device__ __forceinline__ void derivative_half(uint32_t col, const float4* __re
   const float2 sl2v = make_float2(sl2, sl2);
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {                      // 32 queries at a time
+    const uint32_t word = c == 0 ? static_cast<uint32_t>(keep) : static_cast<uint32_t>(keep >> 32);
     uint32_t sv[32], dv[32];
     tmem_ld_32x32b_x32(col + 32 * c, sv);
     tmem_ld_32x32b_x32(col + 64 + 32 * c, dv);
@@ -191,8 +198,8 @@ __device__ __forceinline__ void derivative_half(uint32_t col, const float4* __re
                                make_float2(L.x, L.y));
       float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
       if (kMasked) {
-        p0 = ((keep >> (32 * c + 2 * e)) & 1u) ? p0 : 0.0f;
-        p1 = ((keep >> (32 * c + 2 * e + 1)) & 1u) ? p1 : 0.0f;
+        p0 = ((word >> (2 * e)) & 1u) ? p0 : 0.0f;
+        p1 = ((word >> (2 * e + 1)) & 1u) ? p1 : 0.0f;
       }
       const float2 d = mul2_rn(make_float2(p0, p1),
                                add2_rn(make_float2(__uint_as_float(dv[2 * e]), __uint_as_float(dv[2 * e + 1])),
@@ -227,7 +234,7 @@ template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
 attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_dy,
                    const __grid_constant__ CUtensorMap tm_dkv, const __grid_constant__ CUtensorMap tm_dq,
-                   const float* __restrict__ lse2, const float* __restrict__ dsum, const WinBwdShape w, float sl2,
+                   const float* __restrict__ rows, const WinBwdShape w, float sl2,
                    float rsd, float* slabs, int* err) {
   using Cfg = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -250,7 +257,7 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       mbar_init(&bars->p_full[i], 4);
     }
     for (int i = 0; i < NQ; ++i) {
-      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_full[i], 2);
       mbar_init(&bars->q_empty[i], 1);
     }
     mbar_init(&bars->dq_full, 1);
@@ -309,40 +316,20 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       if (!have) break;
       const int kb = r & 1;
       if (r >= 2 && !mbar_wait_warp(&bars->kv_empty[kb], static_cast<uint32_t>((r >> 1) - 1) & 1u, abort_flag, err)) break;
+      // the previous item's U has gone to tensor memory
+      if (r >= 1 && !mbar_wait_warp(&bars->kvt_full, static_cast<uint32_t>(r - 1) & 1u, abort_flag, err)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars->kv_full[kb], 2 * Cfg::TILE);
         tma_load_3d(sK + kb * Cfg::TILE, &tm_qkv, &bars->kv_full[kb], kcol + x.kh * D, x.j * BT, x.b);
-        tma_load_3d(sU + kb * Cfg::TILE, &tm_qkv, &bars->kv_full[kb], ucol + x.kh * D, x.j * BT, x.b);
+        tma_load_3d(sU, &tm_qkv, &bars->kv_full[kb], ucol + x.kh * D, x.j * BT, x.b);
       }
       issued_kv |= 1u << kb;
       par_kv = (par_kv & ~(1u << kb)) | (static_cast<uint32_t>((r >> 1) & 1) << kb);
-      // the rows' -lse2 and -Dsum by query pair (plain loads; rows past T read nothing), each tile's
-      // fetched one tile ahead so that their latency passes while the producer waits for a free slot
-      float nl[BT / 32], nd[BT / 32];
-      int head = x.first_head(w.G), i = x.first_tile();   // query head and tile of the step to fetch
-      auto fetch_rows = [&]() {
-        const size_t row = (static_cast<size_t>(x.b) * H + head) * T;
-#pragma unroll
-        for (int e = 0; e < BT / 32; ++e) {
-          const int t = i * BT + e * 32 + lane;
-          nl[e] = t < T ? -__ldg(lse2 + row + t) : 0.0f;
-          nd[e] = t < T ? -__ldg(dsum + row + t) : 0.0f;
-        }
-      };
-      fetch_rows();
+      int head = x.first_head(w.G), i = x.first_tile();   // query head and tile of the step
       for (int e = 0; e < x.steps; ++e, ++qcount) {
+        // Q and dY three steps ahead of the last one done, the rows' values (two slots) two
         const uint32_t qs = qcount % NQ;
         if (qcount >= NQ && !mbar_wait_warp(&bars->q_empty[qs], (qcount / NQ - 1) & 1u, abort_flag, err)) { ok = false; break; }
-        float* ld = sLD + qs * (2 * BT);
-#pragma unroll
-        for (int e4 = 0; e4 < BT / 32; ++e4) {
-          const int ql = e4 * 32 + lane;
-          const int o = (ql >> 1) * 4 + (ql & 1);
-          ld[o] = nl[e4];
-          ld[o + 2] = nd[e4];
-        }
-        __threadfence_block();
-        __syncwarp();
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars->q_full[qs], 2 * Cfg::TILE);
           tma_load_3d(sQ + qs * Cfg::TILE, &tm_qkv, &bars->q_full[qs], head * D, i * BT, x.b);
@@ -350,11 +337,20 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
         }
         issued_q |= 1u << qs;
         par_q = (par_q & ~(1u << qs)) | (((qcount / NQ) & 1u) << qs);
+        if (qcount >= 2 && !mbar_wait_warp(&bars->q_empty[(qcount - 2) % NQ], ((qcount - 2) / NQ) & 1u, abort_flag, err)) {
+          ok = false;
+          if (lane == 0) mbar_arrive(&bars->q_full[qs]);   // the copies' phase completes for the drain below
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[qs], 2 * BT * sizeof(float));
+          bulk_load(sLD + (qcount & 1u) * (2 * BT), rows + ((static_cast<size_t>(x.b) * H + head) * w.n_qt + i) * (2 * BT),
+                    2 * BT * sizeof(float), &bars->q_full[qs]);
+        }
         if (++i == x.j + x.cnt) {
           i = x.j;
           ++head;
         }
-        if (e + 1 < x.steps) fetch_rows();
       }
     }
     // never leave with copies in flight into this CTA's shared memory
@@ -490,7 +486,7 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       for (int e = 0; e < x.steps; ++e, ++tiles) {
         const uint32_t qs = tiles % NQ;
         if (!mbar_wait_warp(&bars->q_full[qs], (tiles / NQ) & 1u, abort_flag, err)) { ok = false; break; }
-        const float4* ld = reinterpret_cast<const float4*>(sLD + qs * (2 * BT)) + 32 * g;
+        const float4* ld = reinterpret_cast<const float4*>(sLD + (tiles & 1u) * (2 * BT)) + 32 * g;
         uint8_t* ds_row = sDS + (tiles & 1u) * Cfg::DS_BUF + g * (BT * 128) + kr * 128;
         if (!mbar_wait_warp(&bars->s_full[g], tiles & 1u, abort_flag, err)) { ok = false; break; }
         tc_fence_after();
@@ -519,14 +515,14 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
     // ------------------------------------------------ output: dQ reduce-adds and conversion, dK and dU stores
     const int sub = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(sub * 32) << 16;
-    uint8_t* stg = smem_raw + Cfg::OFF_STG + (warp - 10) * 8192;
+    uint8_t* stg = smem_raw + Cfg::OFF_STG + (warp - 10) * 4096;
     // K_j and U_j (item buffer kb) into tensor memory as the scores' A operands: this warp's 32 key rows,
     // each row's D values as bf16 pairs
     auto stage_kv = [&](int kb) {
       constexpr int ROWB = Cfg::ROWB;
       const int kr = sub * 32 + lane;
       const uint8_t* krow = sK + kb * Cfg::TILE + kr * ROWB;
-      const uint8_t* urow = sU + kb * Cfg::TILE + kr * ROWB;
+      const uint8_t* urow = sU + kr * ROWB;
       uint32_t kw[D / 2], uw[D / 2];
 #pragma unroll
       for (int u = 0; u < ROWB / 16; ++u) {
@@ -612,20 +608,21 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->acc_free);
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
 #pragma unroll
-            for (int u = 0; u < ROWB / 16; ++u) {    // box 0, box 1
-              const int at = lane * ROWB + (swz_unit(ROWB, lane, u) << 4);
-              *reinterpret_cast<uint4*>(stg + at) = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-              *reinterpret_cast<uint4*>(stg + 4096 + at) = make_uint4(pu[4 * u], pu[4 * u + 1], pu[4 * u + 2], pu[4 * u + 3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&tm_dkv, stg, kcol + x.kh * D, x.j * BT + sub * 32, x.b);
-              tma_store_3d(&tm_dkv, stg + 4096, ucol + x.kh * D, x.j * BT + sub * 32, x.b);
-              bulk_commit();
+            for (int which = 0; which < 2; ++which) {
+              if (lane == 0) bulk_wait_read_all();   // the previous copy has read the box
+              __syncwarp();
+#pragma unroll
+              for (int u = 0; u < ROWB / 16; ++u)
+                *reinterpret_cast<uint4*>(stg + lane * ROWB + (swz_unit(ROWB, lane, u) << 4)) =
+                    which ? make_uint4(pu[4 * u], pu[4 * u + 1], pu[4 * u + 2], pu[4 * u + 3])
+                          : make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&tm_dkv, stg, (which ? ucol : kcol) + x.kh * D, x.j * BT + sub * 32, x.b);
+                bulk_commit();
+              }
             }
           }
         }
@@ -641,23 +638,20 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->dq_free);
-        if (lane == 0) bulk_wait_read_all();         // the previous copies have read the staging boxes
-        __syncwarp();
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {        // 32 fp32 columns (128 bytes) per box row
-          uint8_t* box = stg + cc * 4096 + lane * 128;
+          if (lane == 0) bulk_wait_read_all();       // the previous copy has read the box
+          __syncwarp();
 #pragma unroll
           for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4*>(box + (swz_unit(128, lane, u) << 4)) =
+            *reinterpret_cast<uint4*>(stg + lane * 128 + (swz_unit(128, lane, u) << 4)) =
                 make_uint4(v[32 * cc + 4 * u], v[32 * cc + 4 * u + 1], v[32 * cc + 4 * u + 2], v[32 * cc + 4 * u + 3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc)
-            tma_reduce_add_3d(&tm_dq, stg + cc * 4096, head * D + 32 * cc, i * BT + sub * 32, x.b);
-          bulk_commit();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_reduce_add_3d(&tm_dq, stg, head * D + 32 * cc, i * BT + sub * 32, x.b);
+            bulk_commit();
+          }
         }
         if (++i == x.end) {
           i = x.j;
@@ -680,13 +674,17 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
   }
 }
 
-// Dsum[(b H + h) T + t] = sum_d dY[b, t, h D + d] Y[b, t, h D + d]: one warp per row, D / 8 lanes per
-// head with 16-byte loads, so each load instruction of the warp reads 512 contiguous bytes of the row. It also clears
-// the row of the dQ accumulator (a memset of its own took a launch and as long again).
+// What the derivative reads of every query row, in its order: per (b, h), tile of 128 rows (the last one filled up with
+// zeros) and pair of rows {-lse2, -lse2, -Dsum, -Dsum}, with Dsum[t] = sum_d dY[t,d] Y[t,d], so that a tile's kilobyte is
+// one bulk copy (read by the derivative's producer with plain loads they were its longest wait: 0.85 us a step without
+// any product). One warp per row, D / 8 lanes per head with 16-byte loads, so each load instruction of the warp reads
+// 512 contiguous bytes of the row. It also clears the row of the dQ accumulator (a memset of its own took a launch and
+// as long again).
 template <int D>
 __global__ void __launch_bounds__(256)
-attn_window_dsum_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16* __restrict__ dy, float* __restrict__ dsum,
-                        float* __restrict__ dqacc, int M, int T, int H) {
+attn_window_rows_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16* __restrict__ dy,
+                        const float* __restrict__ lse2, float* __restrict__ rows, float* __restrict__ dqacc, int M, int T,
+                        int H, int n_qt) {
   pdl_wait();
   pdl_trigger();
   const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -697,9 +695,13 @@ attn_window_dsum_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16
   const uint4* a4 = reinterpret_cast<const uint4*>(dy + static_cast<size_t>(row) * C);
   const uint4* o4 = reinterpret_cast<const uint4*>(y + static_cast<size_t>(row) * C);
   const int b = static_cast<int>(row / T), t = static_cast<int>(row - static_cast<long long>(b) * T);
+  const size_t tp = static_cast<size_t>(n_qt) * BT;  // padded rows
   for (int v0 = 0; v0 < nv; v0 += 32) {            // nv is a multiple of LPH: a head's lanes are all in or all out
     const int v = v0 + lane;
-    float acc = 0.0f;
+    float acc = 0.0f, ls = 0.0f;
+    const size_t bh = static_cast<size_t>(b) * H + v / LPH;
+    const bool writer = v < nv && (lane % LPH) == 0;
+    if (writer) ls = __ldg(lse2 + bh * T + t);
     if (v < nv) {
       const uint4 a = __ldg(a4 + v), o = __ldg(o4 + v);
       float4* z = reinterpret_cast<float4*>(dqacc + static_cast<size_t>(row) * C) + 2 * v;
@@ -707,13 +709,21 @@ attn_window_dsum_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, ow[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 x = unpack_bf16x2(aw[k]), z = unpack_bf16x2(ow[k]);
-        acc = fmaf(x.x, z.x, fmaf(x.y, z.y, acc));
+        const float2 x = unpack_bf16x2(aw[k]), z2 = unpack_bf16x2(ow[k]);
+        acc = fmaf(x.x, z2.x, fmaf(x.y, z2.y, acc));
       }
     }
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (v < nv && (lane % LPH) == 0) dsum[(static_cast<size_t>(b) * H + v / LPH) * T + t] = acc;
+    if (writer) {
+      float* dst = rows + (bh * tp + (t & ~1)) * 2 + (t & 1);
+      dst[0] = -ls;
+      dst[2] = -acc;
+      if (t == T - 1) {                              // the last tile's missing rows
+        if ((t & 1) == 0) dst[1] = dst[3] = 0.0f;
+        for (size_t f = (bh * tp + ((t | 1) + 1)) * 2; f < (bh + 1) * tp * 2; ++f) rows[f] = 0.0f;
+      }
+    }
   }
 }
 
@@ -814,7 +824,7 @@ int sm_count() {
 
 template <int D>
 cudaError_t launch_bwd_d(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
-                         const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2, float* dsum,
+                         const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2, float* rows,
                          float* dqacc, float* slabs, void* dqkv, int B, const WinBwdPlan& plan, int num_sms, int* err,
                          cudaStream_t s) {
   using Cfg = BwdCfg<D>;
@@ -827,12 +837,13 @@ cudaError_t launch_bwd_d(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, co
   const int M = B * w.T, C = w.H * D;
   const float rsd = 1.0f / sqrtf(static_cast<float>(D));
   const float sl2 = rsd * kLog2e;
-  e = launch_k(attn_window_dsum_kernel<D>, dim3(static_cast<unsigned>((M - 1) / 8 + 1)), dim3(256), 0, s,
-               static_cast<const __nv_bfloat16*>(y), static_cast<const __nv_bfloat16*>(dy), dsum, dqacc, M, w.T, w.H);
+  e = launch_k(attn_window_rows_kernel<D>, dim3(static_cast<unsigned>((M - 1) / 8 + 1)), dim3(256), 0, s,
+               static_cast<const __nv_bfloat16*>(y), static_cast<const __nv_bfloat16*>(dy), lse2, rows, dqacc, M, w.T, w.H,
+               w.n_qt);
   if (e != cudaSuccess) return e;
   const int grid = w.n_items < num_sms ? w.n_items : num_sms;
   e = launch_k(attn_window_bwd_tc_kernel<D>, dim3(grid), dim3(THREADS), static_cast<size_t>(Cfg::SMEM), s, tm_qkv, tm_dy,
-               tm_dkv, tm_dq, lse2, static_cast<const float*>(dsum), w, sl2, rsd, slabs, err);
+               tm_dkv, tm_dq, static_cast<const float*>(rows), w, sl2, rsd, slabs, err);
   if (e != cudaSuccess) return e;
   const long long n4 = static_cast<long long>(M) * (C / 4);
   const long long cblocks = (n4 + 255) / 256;
@@ -843,6 +854,10 @@ cudaError_t launch_bwd_d(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, co
 
 }  // namespace
 
+size_t attention_window_bwd_row_bytes(int B, int T, int H) {
+  return static_cast<size_t>(B) * H * ((T + BT - 1) / BT) * (2 * BT) * sizeof(float);
+}
+
 size_t attention_window_bwd_slab_bytes(int B, int T, int H, int Hkv, int D, int window, int sinks) {
   WinBwdPlan p;
   const int num_sms = sm_count();
@@ -852,15 +867,15 @@ size_t attention_window_bwd_slab_bytes(int B, int T, int H, int Hkv, int D, int 
 
 cudaError_t launch_attention_window_bwd_tc(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
                                            const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2,
-                                           float* dsum, float* dqacc, float* slabs, void* dqkv, int B, int T, int H,
+                                           float* rows, float* dqacc, float* slabs, void* dqkv, int B, int T, int H,
                                            int Hkv, int D, int window, int sinks, int* err, cudaStream_t s) {
   WinBwdPlan p;
   const int num_sms = sm_count();
   if (num_sms <= 0 || !plan_bwd(B, T, H, Hkv, window, sinks, num_sms, &p)) return cudaErrorInvalidValue;
   if (D == 64)
-    return launch_bwd_d<64>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, dsum, dqacc, slabs, dqkv, B, p, num_sms, err, s);
+    return launch_bwd_d<64>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, rows, dqacc, slabs, dqkv, B, p, num_sms, err, s);
   if (D == 32)
-    return launch_bwd_d<32>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, dsum, dqacc, slabs, dqkv, B, p, num_sms, err, s);
+    return launch_bwd_d<32>(tm_qkv, tm_dy, tm_dkv, tm_dq, y, dy, lse2, rows, dqacc, slabs, dqkv, B, p, num_sms, err, s);
   return cudaErrorInvalidValue;
 }
 

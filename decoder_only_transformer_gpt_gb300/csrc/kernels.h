@@ -164,12 +164,14 @@ cudaError_t launch_attention_bwd_tc(const CUtensorMap& tm_qkv, const CUtensorMap
 cudaError_t launch_attention_window_tc(const CUtensorMap& tm_qkv, const CUtensorMap& tm_y, int B, int T, int H, int Hkv,
                                        int D, int window, int sinks, int* err, float* lse2, cudaStream_t s);
 // Its derivative: maps and scratch as for launch_attention_bwd_tc (tm_dkv over dqkv's rows), and
-// attention_window_bwd_slab_bytes of fp32 sums for key tiles that several CTAs share. Three kernels: Dsum and the
-// cleared dqacc, the derivative, dQ to bf16 and the shared tiles' sums.
+// attention_window_bwd_row_bytes for the rows' lse2 and Dsum (256-byte aligned) instead of dsum, and
+// attention_window_bwd_slab_bytes of fp32 sums for key tiles that several CTAs share. Three kernels: the rows' values and
+// the cleared dqacc, the derivative, dQ to bf16 and the shared tiles' sums.
+size_t attention_window_bwd_row_bytes(int B, int T, int H);
 size_t attention_window_bwd_slab_bytes(int B, int T, int H, int Hkv, int D, int window, int sinks);
 cudaError_t launch_attention_window_bwd_tc(const CUtensorMap& tm_qkv, const CUtensorMap& tm_dy, const CUtensorMap& tm_dkv,
                                            const CUtensorMap& tm_dq, const void* y, const void* dy, const float* lse2,
-                                           float* dsum, float* dqacc, float* slabs, void* dqkv, int B, int T, int H,
+                                           float* rows, float* dqacc, float* slabs, void* dqkv, int B, int T, int H,
                                            int Hkv, int D, int window, int sinks, int* err, cudaStream_t s);
 
 // One parameter tensor for the optimiser: values [off, off + n) of the flat gradient, master and

@@ -100,7 +100,7 @@ int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int3
 /*
  * Its derivative: from qkv, y and lse2 of gptk_attention_window (the same window and sinks) and dy [B, T, H D], writes
  * dqkv [B, T, (H + 2 Hkv) D]: dQ, and dK and dU summed over the H / Hkv query heads of a key head. Rows behind a
- * padded sequence's end take no part where their dy is zero. Scratch (4 B T H (D + 1) bytes, and
+ * padded sequence's end take no part where their dy is zero. Scratch (4 B T H (D + 2) bytes and a little, and
  * 1 KB x D for each part of a key tile that several CTAs share, a few hundred at most) is taken on the stream from a
  * pool that the library keeps; make a process's first call before any stream capture. dQ's fp32 additions come in an order that varies between runs.
  */
