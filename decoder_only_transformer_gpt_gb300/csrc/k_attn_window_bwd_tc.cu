@@ -168,6 +168,17 @@ __device__ __forceinline__ int swz_unit(int rowb, int r, int u) {
   return (rowb == 128) ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // `bytes` contiguous bytes into shared memory (both 16-byte aligned), counted on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -412,12 +423,21 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       issue_scores(1, qs);
       if (steps == 1) tc_commit_warp(&bars->kvt_free);   // the item's last reads of K_j, U_j in TMEM
     }
+    // A wait costs about 90 cycles even where the phase is complete, and the issue of 40 products a step (30 to 44 cycles
+    // each) leaves this warp no time for four of them: each barrier is tested ahead of a run of products, whose issue
+    // hides the answer's latency, and waited for only where the answer was no.
+    auto settled = [&](bool early, uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, early) || mbar_wait_warp(bar, parity, abort_flag, err);
+    };
+    bool early_p0 = false;
     while (ok) {
       const bool first = e == 0, last = e == steps - 1;
-      if (!mbar_wait_warp(&bars->p_full[0], tiles & 1u, abort_flag, err)) break;
+      if (!settled(early_p0, &bars->p_full[0], tiles & 1u)) break;
       // the previous item's dK and dU have been read out of the accumulators
       if (first && r > 0 && !mbar_wait_warp(&bars->acc_free, static_cast<uint32_t>(r - 1) & 1u, abort_flag, err)) break;
       tc_fence_after();
+      const uint32_t qcount2 = qcount + 1, qs2 = qcount2 % NQ;
+      const bool early_q = mbar_test(&bars->q_full[qs2], (qcount2 / NQ) & 1u);
       issue_acc(0, qs, first);
       // the next step: the same item's, or the first of the next item
       bool has_next = !last;
@@ -433,18 +453,25 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
           if (!mbar_wait_warp(&bars->kvt_full, static_cast<uint32_t>(r2) & 1u, abort_flag, err)) break;
         }
       }
-      const uint32_t qcount2 = qcount + 1, qs2 = qcount2 % NQ;
+      if (has_next && !settled(early_q, &bars->q_full[qs2], (qcount2 / NQ) & 1u)) break;
+      const bool early_p1 = mbar_test(&bars->p_full[1], tiles & 1u);
       if (has_next) {
-        if (!mbar_wait_warp(&bars->q_full[qs2], (qcount2 / NQ) & 1u, abort_flag, err)) break;
         tc_fence_after();
         issue_scores(0, qs2);
       }
-      if (!mbar_wait_warp(&bars->p_full[1], tiles & 1u, abort_flag, err)) break;
+      if (!settled(early_p1, &bars->p_full[1], tiles & 1u)) break;
       tc_fence_after();
+      const bool early_dq = tiles == 0 || mbar_test(&bars->dq_free, (tiles - 1) & 1u);
       issue_acc(1, qs, false);
       tc_commit_warp(&bars->q_empty[qs]);            // Q_i and dY_i are consumed
       if (last) tc_commit_warp(&bars->acc_full);
-      if (tiles > 0 && !mbar_wait_warp(&bars->dq_free, (tiles - 1) & 1u, abort_flag, err)) break;
+      // the next scores before dQ: the derivative warps wait for them, nothing waits for dQ
+      if (has_next) {
+        issue_scores(1, qs2);
+        if (e2 == steps2 - 1) tc_commit_warp(&bars->kvt_free);
+      }
+      if (!settled(early_dq, &bars->dq_free, (tiles - 1) & 1u)) break;
+      early_p0 = mbar_test(&bars->p_full[0], (tiles + 1) & 1u);
       tc_fence_after();
       const uint32_t dsoff = (tiles & 1u) * Cfg::DS_BUF;
 #pragma unroll
@@ -454,8 +481,6 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       tc_commit_warp(&bars->dq_full);
       if (last) tc_commit_warp(&bars->kv_empty[kb]);   // K_j and U_j are consumed
       if (!has_next) break;
-      issue_scores(1, qs2);
-      if (e2 == steps2 - 1) tc_commit_warp(&bars->kvt_free);
       r = r2;
       e = e2;
       steps = steps2;
