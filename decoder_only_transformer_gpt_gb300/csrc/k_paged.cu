@@ -128,7 +128,7 @@ paged_store_kernel(PagedCache c, const uint4* __restrict__ qkv, const int32_t* _
 //    that holds all units of a (sequence, head group) writes its output; the others write a partial result (maximum,
 //    sum, unnormalised output), at most two per warp, which a second kernel joins in a fixed order.
 //  * A warp streams its units through its own ring of kStages stages of shared memory (cp.async, 16 bytes a lane,
-//    whole rows), with no barrier across warps; the page numbers of a unit are loaded one unit before its rows. Rows
+//    whole rows), with no barrier across warps; the page numbers of a unit are loaded two units before its rows. Rows
 //    are found through the table one by one, so windows, sinks and pages may end anywhere in a unit. Rows that are
 //    not seen are not read (their shared memory is filled with zeros).
 //  * The scores and the product with the values are mma.sync m16n8k16 with the query heads of the group as the 16
@@ -163,10 +163,29 @@ struct DecShape {
   float scale_log2;
 };
 
-// First unit of warp g's range of `total` units dealt to n warps.
-__device__ __forceinline__ long long range_start(long long total, int g, int n) { return total * g / n; }
-// Warps that take part: every range holds a unit at least.
-__device__ __forceinline__ int active_warps(long long total, int n) { return total < n ? static_cast<int>(total) : n; }
+// `total` units dealt to n warps (every warp gets one at least): the first `rem` warps take q + 1, the others q. Written
+// so that a range's start costs a multiplication and a unit's warp one division, of 32 bits where the numbers allow: the
+// joining blocks ask several times before their first load.
+struct Deal {
+  long long q;
+  int n, rem;
+  __device__ __forceinline__ Deal(long long total, int warps) {
+    n = total < warps ? static_cast<int>(total) : warps;
+    if (total <= 0x7fffffffLL) {
+      q = n ? static_cast<int>(total) / n : 0;
+    } else {
+      q = total / n;
+    }
+    rem = static_cast<int>(total - q * n);
+  }
+  __device__ __forceinline__ long long start(int g) const { return g * q + min(g, rem); }
+  __device__ __forceinline__ int warp_of(long long u) const {
+    const long long split = rem * (q + 1);           // the first unit of the shorter ranges
+    if (u < split) return u <= 0x7fffffffLL ? static_cast<int>(u) / static_cast<int>(q + 1) : static_cast<int>(u / (q + 1));
+    const long long v = u - split;
+    return rem + (v <= 0x7fffffffLL && q <= 0x7fffffffLL ? static_cast<int>(v) / static_cast<int>(q) : static_cast<int>(v / q));
+  }
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool copy) {
   const int n = copy ? 16 : 0;                       // 0: the 16 bytes are zeros, src is not read
@@ -252,11 +271,11 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
 
   const int HM = c.Hkv * w.mg;
   const long long total = static_cast<long long>(carry) * HM;
-  const int NW = active_warps(total, static_cast<int>(gridDim.x) * nwarps);
+  const Deal deal(total, static_cast<int>(gridDim.x) * nwarps);
   const int gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-  if (gw >= NW) return;                              // no barrier of the block follows
-  const long long u0 = range_start(total, gw, NW);
-  const int count = static_cast<int>(range_start(total, gw + 1, NW) - u0);
+  if (gw >= deal.n) return;                          // no barrier of the block follows
+  const long long u0 = deal.start(gw);
+  const int count = static_cast<int>(deal.start(gw + 1) - u0);
 
   uint8_t* ring = smem + warp * Cfg::WARP;
   const uint32_t ring_a = smem_u32(ring);
@@ -294,15 +313,17 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
     at.hm = static_cast<int>(r / at.nt);
     at.tile = static_cast<int>(r - static_cast<long long>(at.hm) * at.nt);
   }
-  Unit next = at;                                    // the unit whose rows are copied next
-  int page = -1;                                     // its row's page, this lane
-  auto look_up = [&]() {
-    const int v = next.tile * kUnit + lane;
-    page = -1;
-    if (v < next.seen.n)
-      page = __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (seen_row(next.seen, v) >> c.page_log2));
+  Unit next = at, ahead = at;                        // the unit whose rows are copied next, and the one after it
+  auto look_up = [&](const Unit& x) -> int {         // the page of its row, this lane
+    const int v = x.tile * kUnit + lane;
+    return v < x.seen.n ? __ldg(c.table + static_cast<size_t>(x.b) * c.max_pages + (seen_row(x.seen, v) >> c.page_log2)) : -1;
   };
+  int page = look_up(next), page_ahead = -1;
   int issued = 0;
+  if (count > 1) {
+    advance(ahead);
+    page_ahead = look_up(ahead);
+  }
   auto issue = [&]() {                               // copies unit `next` into stage issued % kStages, steps on
     const int st = issued % kStages;
     const uint32_t sk = ring_a + st * Cfg::STAGE, sv = sk + Cfg::TILE, sq = sv + Cfg::TILE;
@@ -347,15 +368,16 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
       }
     }
     ++issued;
-    advance(next);
+    next = ahead;
+    page = page_ahead;
+    if (issued + 1 < count) {
+      advance(ahead);
+      page_ahead = look_up(ahead);
+    }
   };
-  look_up();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    if (issued < count) {
-      issue();
-      if (issued < count) look_up();
-    }
+    if (issued < count) issue();
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
 
@@ -366,10 +388,7 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
   int piece0 = 0;                                    // the segment's first unit in this warp's range
   const int qrow = lane >> 2, qcol = 2 * (lane & 3);
   for (int n = 0; n < count; ++n) {
-    if (issued < count) {
-      issue();
-      if (issued < count) look_up();
-    }
+    if (issued < count) issue();
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
@@ -538,20 +557,15 @@ paged_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16*
   if (nt == 0 || (blockIdx.y > 0 && static_cast<long long>(blockIdx.y) * kJoinRows >= static_cast<long long>(nt) * kUnit)) return;
   const int HM = c.Hkv * w.mg;
   const long long total = static_cast<long long>(ws.prefix[w.B]) * HM;
-  const int NW = active_warps(total, warps);
+  const Deal deal(total, warps);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int mt = 0; mt < w.mg; ++mt) {
     const long long t0 = static_cast<long long>(p0) * HM + static_cast<long long>(kh * w.mg + mt) * nt, t1 = t0 + nt;
-    int g1 = static_cast<int>(t0 * NW / total);      // the warp that holds the first unit
-    while (range_start(total, g1, NW) > t0) --g1;
-    while (range_start(total, g1 + 1, NW) <= t0) ++g1;
-    int g2 = static_cast<int>((t1 - 1) * NW / total);   // and the last
-    while (range_start(total, g2, NW) > t1 - 1) --g2;
-    while (range_start(total, g2 + 1, NW) <= t1 - 1) ++g2;
+    const int g1 = deal.warp_of(t0), g2 = deal.warp_of(t1 - 1);   // the warps that hold the first unit and the last
     const int gn = min(w.G - mt * 16, 16);
     const size_t head0 = static_cast<size_t>(b) * w.H + kh * w.G + mt * 16;
     // a piece is its warp's first (slot 0) unless its segment starts behind the warp's start: only g1's can
-    const size_t slot1 = static_cast<size_t>(g1) * 2 + (range_start(total, g1, NW) == t0 ? 0 : 1);
+    const size_t slot1 = static_cast<size_t>(g1) * 2 + (deal.start(g1) == t0 ? 0 : 1);
     auto slot_of = [&](int g) { return g == g1 ? slot1 : static_cast<size_t>(g) * 2; };
     if (g1 == g2) {                                  // one warp held it all and wrote the output
       if (tid < gn) s_lse[mt * 16 + tid] = ws.lse[head0 + tid];
