@@ -549,16 +549,34 @@ paged_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16*
                   DecShape w, DecScratch ws, int warps, int* err) {
   pdl_wait();
   pdl_trigger();
-  constexpr int P = kJoinThreads / D;                // pieces summed side by side
+  constexpr int P = kJoinThreads / D;                // rows, or shares of a row's pieces, side by side
+  constexpr int K = kJoinRows / kJoinThreads;
   __shared__ float s_lse[kPagedMaxGroup];
-  __shared__ float s_o[P][D];
+  __shared__ float s_o[P][D], s_m[P], s_l[P];
   const int kh = blockIdx.x, b = blockIdx.z;
-  const int p0 = ws.prefix[b], nt = ws.prefix[b + 1] - p0;
+  const int p0 = ws.prefix[b], nt = ws.prefix[b + 1] - p0, last = __ldg(lens + b);
+  const long long total = static_cast<long long>(ws.prefix[w.B]) * (c.Hkv * w.mg);
   if (nt == 0 || (blockIdx.y > 0 && static_cast<long long>(blockIdx.y) * kJoinRows >= static_cast<long long>(nt) * kUnit)) return;
   const int HM = c.Hkv * w.mg;
-  const long long total = static_cast<long long>(ws.prefix[w.B]) * HM;
   const Deal deal(total, warps);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, d = tid % D, part = tid / D;
+  const Seen sn = seen_rows(last + 1, w.window, w.sinks);
+  const int pmask = (1 << c.page_log2) - 1;
+  const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
+  const float* score = ws.score ? ws.score + (static_cast<size_t>(b) * w.H + kh * w.G) * ws.score_ld : nullptr;
+  const long long v0 = static_cast<long long>(blockIdx.y) * kJoinRows;
+  // the pages, and the first head's scores, of the rows whose weights this block adds to: on their way early
+  int pg[K];
+  float sc[K];
+  auto fetch = [&](long long first) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const long long v = min(first + tid + k * kJoinThreads, static_cast<long long>(sn.n) - 1);
+      pg[k] = __ldg(trow + (seen_row(sn, static_cast<int>(v)) >> c.page_log2));
+      sc[k] = score[v];
+    }
+  };
+  if (score) fetch(v0);
   for (int mt = 0; mt < w.mg; ++mt) {
     const long long t0 = static_cast<long long>(p0) * HM + static_cast<long long>(kh * w.mg + mt) * nt, t1 = t0 + nt;
     const int g1 = deal.warp_of(t0), g2 = deal.warp_of(t1 - 1);   // the warps that hold the first unit and the last
@@ -566,74 +584,72 @@ paged_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16*
     const size_t head0 = static_cast<size_t>(b) * w.H + kh * w.G + mt * 16;
     // a piece is its warp's first (slot 0) unless its segment starts behind the warp's start: only g1's can
     const size_t slot1 = static_cast<size_t>(g1) * 2 + (deal.start(g1) == t0 ? 0 : 1);
-    auto slot_of = [&](int g) { return g == g1 ? slot1 : static_cast<size_t>(g) * 2; };
     if (g1 == g2) {                                  // one warp held it all and wrote the output
       if (tid < gn) s_lse[mt * 16 + tid] = ws.lse[head0 + tid];
       __syncthreads();
       continue;
     }
-    for (int r = warp; r < gn; r += kJoinThreads / 32) {   // log-sum-exp: one warp per row
-      float mx = -INFINITY;
-      for (int g = g1 + lane; g <= g2; g += 32) mx = fmaxf(mx, ws.ml[slot_of(g) * QR + r].x);
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-      float lt = 0.0f;
-      for (int g = g1 + lane; g <= g2; g += 32) {
-        const float2 x = ws.ml[slot_of(g) * QR + r];
-        if (x.x != -INFINITY) lt += x.y * exp2f(x.x - mx);
-      }
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
-      if (lane == 0) s_lse[mt * 16 + r] = mx + log2f(lt);
-    }
-    __syncthreads();
-    if (blockIdx.y > 0) continue;
-    const int d = tid % D, part = tid / D;
-    for (int r = 0; r < gn; ++r) {
-      const float lse = s_lse[mt * 16 + r];
-      float acc = 0.0f;
+    // maxima, sums and outputs in one walk over the pieces; the pieces of one or two rows are shared by the parts
+    const int share = gn >= P ? 1 : (gn >= 2 && P >= 4 ? P / 2 : P);
+    for (int r0 = 0; r0 < gn; r0 += P / share) {
+      const int r = r0 + part / share, sub = part % share;
+      float m = -INFINITY, l = 0.0f, acc = 0.0f;
+      if (r < gn) {
 #pragma unroll 4
-      for (int g = g1 + part; g <= g2; g += P) {
-        const size_t sl = slot_of(g) * QR + r;
-        const float m = ws.ml[sl].x;
-        const float x = ws.o[sl * D + d];
-        acc = fmaf(x, m == -INFINITY ? 0.0f : exp2f(m - lse), acc);
+        for (int g = g1 + sub; g <= g2; g += share) {
+          const size_t sl = (g == g1 ? slot1 : static_cast<size_t>(g) * 2) * QR + r;
+          const float2 x = ws.ml[sl];
+          const float o = ws.o[sl * D + d];
+          const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.0f : mn;
+          const float f = ex2_approx(m - ref), h = ex2_approx(x.x - ref);
+          m = mn;
+          l = l * f + x.y * h;
+          acc = acc * f + o * h;
+        }
       }
       s_o[part][d] = acc;
+      if (d == 0) {
+        s_m[part] = m;
+        s_l[part] = l;
+      }
       __syncthreads();
-      if (part == 0) {
-#pragma unroll
-        for (int k = 1; k < P; ++k) acc += s_o[k][d];
-        y[(head0 + r) * D + d] = __float2bfloat16(acc);
-        if (lse2 && d == 0) lse2[head0 + r] = lse;
+      if (sub == 0 && r < gn) {
+        float mx = m;
+        for (int k = 1; k < share; ++k) mx = fmaxf(mx, s_m[part + k]);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        float lt = 0.0f, at = 0.0f;
+        for (int k = 0; k < share; ++k) {
+          const float f = ex2_approx(s_m[part + k] - ref);
+          lt += s_l[part + k] * f;
+          at += s_o[part + k][d] * f;
+        }
+        if (blockIdx.y == 0) y[(head0 + r) * D + d] = __float2bfloat16(lt > 0.0f ? at / lt : 0.0f);
+        if (d == 0) {
+          const float lse = mx + log2f(lt);
+          s_lse[mt * 16 + r] = lse;
+          if (lse2 && blockIdx.y == 0) lse2[head0 + r] = lse;
+        }
       }
       __syncthreads();
     }
   }
-  if (ws.score == nullptr) return;
-  const int last = __ldg(lens + b);
-  const Seen sn = seen_rows(last + 1, w.window, w.sinks);
-  const int pmask = (1 << c.page_log2) - 1;
-  const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
-  const float* score = ws.score + (static_cast<size_t>(b) * w.H + kh * w.G) * ws.score_ld;
-  for (long long v0 = static_cast<long long>(blockIdx.y) * kJoinRows; v0 < sn.n; v0 += static_cast<long long>(gridDim.y) * kJoinRows) {
-    constexpr int K = kJoinRows / kJoinThreads;
-    float sum[K] = {};
-    int pg[K];
+  if (!score) return;
+  for (long long first = v0; first < sn.n; first += static_cast<long long>(gridDim.y) * kJoinRows) {
+    if (first != v0) fetch(first);
+    float sum[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      pg[k] = __ldg(trow + (seen_row(sn, static_cast<int>(min(v0 + tid + k * kJoinThreads, static_cast<long long>(sn.n) - 1))) >> c.page_log2));
-    for (int r = 0; r < w.G; ++r) {
+    for (int k = 0; k < K; ++k) sum[k] = exp2f(sc[k] - s_lse[0]);
+    for (int r = 1; r < w.G; ++r) {
       const float lse = s_lse[r];
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (v0 + tid + k * kJoinThreads < sn.n)
-          sum[k] += exp2f(score[static_cast<size_t>(r) * ws.score_ld + v0 + tid + k * kJoinThreads] - lse);
+        if (first + tid + k * kJoinThreads < sn.n)
+          sum[k] += exp2f(score[static_cast<size_t>(r) * ws.score_ld + first + tid + k * kJoinThreads] - lse);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (v0 + tid + k * kJoinThreads >= sn.n) continue;
-      const int row = seen_row(sn, static_cast<int>(v0) + tid + k * kJoinThreads);
+      if (first + tid + k * kJoinThreads >= sn.n) continue;
+      const int row = seen_row(sn, static_cast<int>(first) + tid + k * kJoinThreads);
       // atomic: sequences may share a page (each adds to a row once, so a page of one sequence has one order)
       if (static_cast<unsigned>(pg[k]) < static_cast<unsigned>(c.pages))
         atomicAdd(c.weight + weight_at(c, pg[k], kh, row & pmask), sum[k]);
