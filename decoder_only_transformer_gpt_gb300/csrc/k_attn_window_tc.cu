@@ -227,6 +227,17 @@ __device__ __forceinline__ void load_chunk(uint32_t col, uint32_t (&v)[32]) {
 __device__ __forceinline__ void store_chunk(uint32_t col, const uint32_t (&v)[32]) { tmem_st_32x32b_x32(col, v); }
 __device__ __forceinline__ void store_chunk(uint32_t col, const uint32_t (&v)[16]) { tmem_st_32x32b_x16(col, v); }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // 16-byte unit u of row r of a staging box (rows of ROWB bytes) in the TMA swizzle of that width.
 template <int ROWB>
 __device__ __forceinline__ int swz_unit(int r, int u) {
@@ -410,7 +421,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
     uint8_t* stg = smem_raw + Cfg::OFF_STG + (warp - 2) * Cfg::STG;
     uint32_t kbase = 0;                               // score number of the item's first tile
     uint32_t last = 0;                                // the number of this group's previous score tile
-    uint32_t used0 = 0, used1 = 0, used2 = 0;         // this group's score tiles so far in buffers 0, 1, 2
+    uint32_t bits = 0;                                // per buffer: the phase of this group's next tile there
     bool ok = true;
     const float2 sc2 = make_float2(scale_log2, scale_log2);
     // An item's output is written during the group's next tile, just before that tile's first
@@ -473,17 +484,19 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       float mr = -INFINITY;                           // running (lazily raised) reference, log2 units
       float l = 0.0f;                                 // running sum of 2^(s - mr)
       bool ready = false;                             // every row of the warp has a reference
-      for (int i = i0; i < i1 && ok; ++i) {
-        if (g == 1 && !x.has1(i)) continue;
+      uint32_t k = kbase + x.number(i0, g);           // the tile's score number, and its buffer
+      uint32_t b = k % NSB;
+      int kb = x.tile(i0) * BKV;                      // the tile's first key
+      bool early = false;                             // the tile's scores were there when the last one was handed over
+      for (int i = i0; i < i1;) {
         const bool first = i == i0;
-        // this tile's score number and buffer
-        const uint32_t k = kbase + x.number(i, g);
-        const uint32_t b = k % NSB;
-        const uint32_t use = b == 0 ? used0++ : (b == 1 ? used1++ : used2++);
-        if (!mbar_wait_warp(&bars->s_full[g][b], use & 1u, abort_flag, err)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, early) && !mbar_wait_warp(&bars->s_full[g][b], (bits >> b) & 1u, abort_flag, err)) {
+          ok = false;
+          break;
+        }
+        bits ^= 1u << b;
         tc_fence_after();
         const uint32_t tS = tmem_base + 128 * b + lane_off;
-        const int kb = x.tile(i) * BKV;               // first key of the tile
         // bit n set: this row sees key k0 + n
         auto seen_bits = [&](int k0) -> uint32_t {
           const int hi = t - k0;                      // last key of the row
@@ -656,11 +669,23 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
           store_chunk(tS + CH / 2 * c, pk);
         }
         if (!ok) break;
+        // the group's next entry: its number, buffer and first key, and whether its scores are there (a wait costs 90
+        // cycles even then; the answer to the test comes while the probabilities are stored)
+        uint64_t* const full = &bars->p_full[b];
+        last = k;
+        do {
+          const uint32_t step = (g == 0 ? 1 : (x.has1(i) ? 1 : 0)) + (g == 0 ? (x.has1(i) ? 1 : 0) : (i + 1 < x.n0 ? 1 : 0));
+          ++i;
+          k += step;
+          b += step;
+          b = b >= NSB ? b - NSB : b;
+          kb = i == x.a ? x.j0 * BKV : kb + BKV;
+        } while (g == 1 && i < i1 && !x.has1(i));
+        early = i < i1 && mbar_test(&bars->s_full[g][b], (bits >> b) & 1u);
         tmem_st_wait();
         tc_fence_before();                      // our TMEM reads of S and writes of P precede the next MMA
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[b]);
-        last = k;
+        if (lane == 0) mbar_arrive(full);
       }
       if (!ok) break;
       // the item's output is written during the group's next tile (or after the last item)
