@@ -1,0 +1,49 @@
+// Helpers that the sliding-window attention kernels share beyond common.cuh.
+#pragma once
+
+#include "common.cuh"
+
+namespace gptgb {
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
+// `bytes` contiguous bytes into shared memory (both 16-byte aligned), counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// Waits for this thread's tensor-memory loads; the registers are not read before.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&v)[N]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
+
+// 32 lanes x 8 consecutive columns into tensor memory.
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// The start-address field is the low 14 bits of a descriptor (address >> 4), and every operand here lies below
+// 256 KB, so advancing an operand by `bytes` is a plain add of bytes >> 4 to its base descriptor.
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+// 16-byte unit u of row r of a staging box (rows of `rowb` bytes) in the TMA swizzle of that width.
+__device__ __forceinline__ int swz_unit(int rowb, int r, int u) {
+  return (rowb == 128) ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
+}
+
+}  // namespace gptgb

@@ -26,7 +26,7 @@
 // and dU_j by TMA. A last kernel rounds dQ to bf16.
 // Warps (448 threads, one persistent CTA per SM): 0 producer; 1 TMEM allocator and MMA issuer; 2-5 and 6-9 softmax
 // derivative of half 0 and 1 (thread = key row); 10-13 output.
-#include "common.cuh"
+#include "attn_window.cuh"
 #include "kernels.h"
 #include "launch.h"
 
@@ -86,7 +86,6 @@ struct __align__(16) BwdBars {
 };
 static_assert(sizeof(BwdBars) <= 512, "barrier block");
 
-__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
 // What a launch computes, and how it is cut. Items: one (b, key head), one key tile j, and a segment of that tile's
 // steps. The tiles with sinks see every later query tile and would keep one CTA busy long after the others (and a few
@@ -161,28 +160,6 @@ __device__ __forceinline__ bool next_item(BwdBars* bars, int r, Step0& x, volati
   __syncwarp();
   if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
   return x.steps > 0;
-}
-
-// 16-byte unit u of row r of a staging box (rows of `rowb` bytes) in the TMA swizzle of that width.
-__device__ __forceinline__ int swz_unit(int rowb, int r, int u) {
-  return (rowb == 128) ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
-}
-
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
-}
-
-// `bytes` contiguous bytes into shared memory (both 16-byte aligned), counted on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
 // One half tile of the softmax derivative for this thread's key row: reads S^T and dP^T (64 queries

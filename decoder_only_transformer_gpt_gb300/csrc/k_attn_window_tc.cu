@@ -31,7 +31,7 @@
 //
 // Tensor memory (512 columns): score buffers at 0, 128, 256; O_g at 384 + 64 g.
 // Warps: 0 TMA producer; 1 TMEM allocator and P U issuer; 2-5 softmax group 0; 6-9 group 1; 10 score issuer.
-#include "common.cuh"
+#include "attn_window.cuh"
 #include "kernels.h"
 #include "launch.h"
 
@@ -88,10 +88,6 @@ struct __align__(16) AttnBars {
 };
 static_assert(sizeof(AttnBars) <= 512, "barrier block");
 
-// The start-address field is the low 14 bits of a descriptor (address >> 4), and
-// every operand here lies below 256 KB, so advancing an operand by `bytes` is a
-// plain add of bytes >> 4 to its base descriptor.
-__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
 // The products of one step by one elected lane of the converged warp: a single election for all of them (and the
 // commit), as the issuing warps' own instructions are part of every score buffer's round.
@@ -220,28 +216,106 @@ __device__ __forceinline__ void load_chunk(uint32_t col, uint32_t (&v)[64]) {
   tmem_ld_32x32b_x64(col, v);
   tmem_ld_wait();
 }
-__device__ __forceinline__ void load_chunk(uint32_t col, uint32_t (&v)[32]) {
-  tmem_ld_32x32b_x32(col, v);
-  tmem_ld_wait();
-}
-__device__ __forceinline__ void store_chunk(uint32_t col, const uint32_t (&v)[32]) { tmem_st_32x32b_x32(col, v); }
-__device__ __forceinline__ void store_chunk(uint32_t col, const uint32_t (&v)[16]) { tmem_st_32x32b_x16(col, v); }
+// The two rare steps of a softmax warp, out of line: inlined they took the registers and the instruction cache of the
+// loop that turns scores into probabilities.
 
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
+// Row references: the exact maximum of a chunk's seen keys becomes the reference of a row that had none, or that it
+// passes by more than 2^8; then the running sum, the output so far (unless the item starts here) and the tile's
+// probabilities so far (n_p columns of 16 at tS) are rescaled. `prev`: the group's previous score tile.
+struct RowRef {
+  float mr, l;
+  bool ok;
+};
+template <int D>
+__device__ __noinline__ RowRef raise_reference(AttnBars* bars, uint32_t tSc, uint32_t tS, uint32_t tO, int n_p, float mr,
+                                               float l, float scale_log2, uint32_t seen0, uint32_t seen1, bool first,
+                                               uint32_t prev, volatile int* abort_flag, int* err) {
+  uint32_t v[CH];
+  load_chunk(tSc, v);
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < CH; i += 2) {
+    const uint32_t seen = i < 32 ? seen0 : seen1;
+    mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], (seen >> (i & 31)) & 1u ? __uint_as_float(v[i]) : -INFINITY,
+                             (seen >> ((i + 1) & 31)) & 1u ? __uint_as_float(v[i + 1]) : -INFINITY);
+  }
+  const float m_new = fmaxf(mr, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2);
+  const bool fresh = mr == -INFINITY;                // l and the row's outputs are zero
+  const bool need = m_new > mr + kRescaleLog2;       // (true for a fresh row that sees a key here)
+  const float alpha = need && !fresh ? ex2_approx(mr - m_new) : 1.0f;
+  RowRef out = {need ? m_new : mr, l * alpha, true};
+  if (__any_sync(0xffffffffu, need && !fresh)) {
+    if (!first) {
+      // every earlier P U of the group has completed
+      if (!mbar_wait_warp(&bars->pv_done[prev % NSB], (prev / NSB) & 1u, abort_flag, err)) {
+        out.ok = false;
+        return out;
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(tO + c * 16, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        tmem_st_32x32b_x16(tO + c * 16, o);
+      }
+    }
+    tmem_st_wait();
+#pragma unroll 1
+    for (int c = 0; c < n_p; ++c) {
+      uint32_t q[16];
+      tmem_ld_32x32b_x16(tS + 16 * c, q);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = unpack_bf16x2(q[i]);
+        q[i] = pack_bf16x2(f.x * alpha, f.y * alpha);
+      }
+      tmem_st_32x32b_x16(tS + 16 * c, q);
+    }
+    tmem_st_wait();
+  }
+  return out;
 }
 
-// 16-byte unit u of row r of a staging box (rows of ROWB bytes) in the TMA swizzle of that width.
-template <int ROWB>
-__device__ __forceinline__ int swz_unit(int r, int u) {
-  return (ROWB == 128) ? (u ^ (r & 7)) : (u ^ ((r >> 1) & 3));
+// An item's output: this warp's 32 rows, normalised, staged and stored by TMA; the rows' log-sum-exp (`lse` nullable).
+template <int D>
+__device__ __noinline__ bool write_rows(AttnBars* bars, uint32_t prev, uint32_t tO, uint8_t* stg, const CUtensorMap* tm_y,
+                                        int col, int row, int b, float l, float m, float* lse, volatile int* abort_flag,
+                                        int* err) {
+  using Cfg = AttnCfg<D>;
+  const int lane = threadIdx.x & 31;
+  if (!mbar_wait_warp(&bars->pv_done[prev % NSB], (prev / NSB) & 1u, abort_flag, err)) return false;
+  tc_fence_after();
+  const float inv = 1.0f / l;
+  if (lane == 0) bulk_wait_read_all();               // this warp's previous store has read its staging box
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld_32x32b_x32(tO + 32 * c, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint4 v;
+      v.x = pack_bf16x2(__uint_as_float(o[8 * u + 0]) * inv, __uint_as_float(o[8 * u + 1]) * inv);
+      v.y = pack_bf16x2(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv);
+      v.z = pack_bf16x2(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv);
+      v.w = pack_bf16x2(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv);
+      *reinterpret_cast<uint4*>(stg + lane * Cfg::ROWB + (swz_unit(Cfg::ROWB, lane, 4 * c + u) << 4)) = v;
+    }
+  }
+  tc_fence_before();                                 // the accumulator may be overwritten after this
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(tm_y, stg, col, row, b);
+    bulk_commit();
+  }
+  if (lse != nullptr) *lse = m + log2f(l);
+  return true;
 }
 
 template <int D>
@@ -433,43 +507,10 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
     int pb = 0, ph = 0, pqt = 0;                      // its batch row, head and query tile
     uint32_t plast = 0;                               // the number of its last score tile
     auto write_out = [&]() -> bool {
-      if (!mbar_wait_warp(&bars->pv_done[plast % NSB], (plast / NSB) & 1u, abort_flag, err)) return false;
-      tc_fence_after();
-      const float inv = 1.0f / pl;
-      uint32_t ov[D];
-      if constexpr (D == 64) {
-        uint32_t (&o64)[64] = *reinterpret_cast<uint32_t (*)[64]>(ov);
-        tmem_ld_32x32b_x64(tO, o64);
-      } else {
-        uint32_t (&o32)[32] = *reinterpret_cast<uint32_t (*)[32]>(ov);
-        tmem_ld_32x32b_x32(tO, o32);
-      }
-      tmem_ld_wait();
-      tc_fence_before();                        // the accumulator may be overwritten after this
-      if (lane == 0) bulk_wait_read_all();      // this warp's previous store has read its staging box
-      __syncwarp();
-      uint8_t* row = stg + lane * Cfg::ROWB;
-#pragma unroll
-      for (int u = 0; u < Cfg::ROWB / 16; ++u) {
-        uint4 v;
-        v.x = pack_bf16x2(__uint_as_float(ov[8 * u + 0]) * inv, __uint_as_float(ov[8 * u + 1]) * inv);
-        v.y = pack_bf16x2(__uint_as_float(ov[8 * u + 2]) * inv, __uint_as_float(ov[8 * u + 3]) * inv);
-        v.z = pack_bf16x2(__uint_as_float(ov[8 * u + 4]) * inv, __uint_as_float(ov[8 * u + 5]) * inv);
-        v.w = pack_bf16x2(__uint_as_float(ov[8 * u + 6]) * inv, __uint_as_float(ov[8 * u + 7]) * inv);
-        *reinterpret_cast<uint4*>(row + (swz_unit<Cfg::ROWB>(lane, u) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(&tm_y, stg, ph * D, pqt * BQ + sub * 32, pb);
-        bulk_commit();
-      }
-      if (lse2 != nullptr) {                      // the row's base-2 log-sum-exp of the scaled scores
-        const int t = pqt * BQ + r_row;
-        if (t < T) lse2[(static_cast<size_t>(pb) * H + ph) * T + t] = pm + log2f(pl);
-      }
+      const int t = pqt * BQ + r_row;
+      float* lse = lse2 != nullptr && t < T ? lse2 + (static_cast<size_t>(pb) * H + ph) * T + t : nullptr;
       pend = false;
-      return true;
+      return write_rows<D>(bars, plast, tO, stg, &tm_y, ph * D, pqt * BQ + sub * 32, pb, pl, pm, lse, abort_flag, err);
     };
     const int wrow = sub * 32;                        // first row of this warp within the tile
     for (int r = 0; ok; ++r) {
@@ -507,14 +548,49 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
           const uint32_t sinks = ns <= 0 ? 0u : (ns >= 32 ? ~0u : (1u << ns) - 1u);
           return to_hi & (from_lo | sinks);
         };
-        // some row of the warp (tw .. tw + 31) misses some of keys k .. k + 31 (warp-uniform)
-        auto crossed = [&](int k) { return k + 31 > tw || (k <= tw + 31 - w.window && k + 32 > w.sinks); };
         // The tile's keys, CH at a time. A chunk's probabilities are final once its sum is checked (and, rarely,
         // recomputed against a raised reference); they are then stored as bf16 pairs over the buffer's first
         // columns, whose scores have been read. One copy of each loop: the warps' code has to fit the
         // instruction cache.
+        int c0 = 0;
+        // Every row sees the whole tile and has its reference: 32 keys at a time, the next 32 scores on their way from
+        // tensor memory while these are worked on.
+        if (ready && kb + BKV - 1 <= tw && (kb > tw + 31 - w.window || kb + BKV <= w.sinks)) {
+          const float2 nm2 = make_float2(-mr, -mr);
+          uint32_t va[32], vb[32], pk[CH / 2];
+          float2 ls[4];
+          auto stream = [&](const uint32_t (&v)[32], int at) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
+              const float2 pr = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], pr);
+              pk[at + i / 2] = pack_bf16x2(pr.x, pr.y);
+            }
+          };
+          tmem_ld_32x32b_x32(tS, va);
+          tmem_loaded(va);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld_32x32b_x32(tS + 64 * c + 32, vb);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ls[q] = make_float2(0.0f, 0.0f);
+            stream(va, 0);
+            tmem_loaded(vb);
+            if (c == 0) tmem_ld_32x32b_x32(tS + 64, va);
+            stream(vb, 16);
+            const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
+            const float lt = l2.x + l2.y;
+            const bool over = __any_sync(0xffffffffu, !(lt <= kSumLimit));
+            if (c == 0) tmem_loaded(va);
+            if (over) break;
+            l += lt;
+            tmem_st_32x32b_x32(tS + 32 * c, pk);
+            c0 = c + 1;
+          }
+        }
 #pragma unroll 1
-        for (int c = 0; c < BKV / CH; ++c) {
+        for (int c = c0; c < BKV / CH; ++c) {
           const int k0 = kb + CH * c;
           uint32_t pk[CH / 2];
           // what the warp's rows tw .. tw + 31 see of the chunk: nothing; not everything (both warp-uniform)
@@ -523,150 +599,55 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) pk[i] = 0u;
           } else {
-            const bool masked = k0 + CH - 1 > tw || (k0 <= tw + 31 - w.window && k0 + CH > w.sinks);
-            float lt;
-            bool plain = ready;
-            if (plain) {
-              // every key is seen and every row has its reference: the score's whole way to a bf16 probability in one
-              // run of independent steps (with the mask's branch in the middle of it the exponentials, sums and
-              // roundings ran one after the other: 179 against 143 us for 12,001 tokens, W = 1500)
+            const bool at_key0 = first && k0 == 0 && (w.sinks > 0 || tw + 31 < w.window);   // all rows see key 0
+            float lt;                                 // the row's sum over the chunk
+#pragma unroll 1
+            for (bool raise = !ready && !at_key0;; raise = true) {
+              if (raise) {
+                const RowRef rr = raise_reference<D>(bars, tS + CH * c, tS, tO, c * (CH / 32), mr, l, scale_log2,
+                                                     seen_bits(k0), seen_bits(k0 + 32), first, last, abort_flag, err);
+                mr = rr.mr;
+                l = rr.l;
+                ok = rr.ok;
+                if (!ok) break;
+                ready = __all_sync(0xffffffffu, mr != -INFINITY);
+              }
               uint32_t v[CH];
               load_chunk(tS + CH * c, v);
-              const float2 nm2 = make_float2(-mr, -mr);
+              if (at_key0 && !raise) {
+                mr = __uint_as_float(v[0]) * scale_log2;
+                ready = true;
+              }
+              // A score's whole way to a bf16 probability, 2^(s scale - mr), and into the sum, in one run of
+              // independent steps, two keys per f32x2 instruction (with the mask as a branch in the middle the
+              // exponentials, sums and roundings ran one after the other: 179 against 156 us for 12,001 tokens).
               float2 ls[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) ls[q] = make_float2(0.0f, 0.0f);
-              if (!masked) {
-#pragma unroll
-              for (int i = 0; i < CH; i += 2) {
-                const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
-                const float2 pr = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], pr);
-                pk[i / 2] = pack_bf16x2(pr.x, pr.y);
-              }
-              } else {
-                uint32_t seen[CH / 32];
-#pragma unroll
-                for (int q = 0; q < CH / 32; ++q) seen[q] = seen_bits(k0 + 32 * q);
+              {                                       // 0 for the keys that the row does not see
+                const float nm = mr == -INFINITY ? 0.0f : -mr;
+                const float2 nm2 = make_float2(nm, nm);
+                const uint32_t seen0 = seen_bits(k0), seen1 = seen_bits(k0 + 32);
 #pragma unroll
                 for (int i = 0; i < CH; i += 2) {
+                  const uint32_t seen = i < 32 ? seen0 : seen1;
                   const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
                   const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
-                  const float2 pr = make_float2((seen[i / 32] >> (i & 31)) & 1u ? p0 : 0.0f,
-                                                (seen[i / 32] >> ((i + 1) & 31)) & 1u ? p1 : 0.0f);
+                  const float2 pr = make_float2((seen >> (i & 31)) & 1u ? p0 : 0.0f, (seen >> ((i + 1) & 31)) & 1u ? p1 : 0.0f);
                   ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], pr);
                   pk[i / 2] = pack_bf16x2(pr.x, pr.y);
                 }
               }
               const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
               lt = l2.x + l2.y;
-              plain = !__any_sync(0xffffffffu, !(lt <= kSumLimit));
-            }
-            if (!plain) {
-            uint32_t v[CH];
-#pragma unroll 1
-            for (bool again = false;;) {
-              load_chunk(tS + CH * c, v);
-              if (first && k0 == 0 && !again && (w.sinks > 0 || tw + 31 < w.window))
-                mr = __uint_as_float(v[0]) * scale_log2;      // key 0 is seen by every row of the warp
-              bool full = __any_sync(0xffffffffu, mr == -INFINITY) && !again;   // a row without a key so far
-              if (!full) {
-                // 2^(s*scale - mr) in place of the scores, two keys per f32x2 instruction; 0 for the keys that the
-                // row does not see (mr = -inf: none so far, nor here); their sum
-                const float nm = mr == -INFINITY ? 0.0f : -mr;
-                const float2 nm2 = make_float2(nm, nm);
-#pragma unroll
-                for (int i = 0; i < CH; i += 2) {
-                  const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
-                  v[i] = __float_as_uint(ex2_approx(e.x));
-                  v[i + 1] = __float_as_uint(ex2_approx(e.y));
-                }
-                if (masked) {
-#pragma unroll
-                  for (int q = 0; q < CH / 32; ++q) {
-                    if (!crossed(k0 + 32 * q)) continue;
-                    const uint32_t seen = seen_bits(k0 + 32 * q);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[32 * q + i] = (seen >> i) & 1u ? v[32 * q + i] : 0u;
-                  }
-                }
-                float2 ls[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) ls[q] = make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
-#pragma unroll
-                for (int i = 8; i < CH; i += 2)
-                  ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-                const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
-                lt = l2.x + l2.y;
-                full = __any_sync(0xffffffffu, !(lt <= kSumLimit)) && !again;
-                if (!full) break;
-                load_chunk(tS + CH * c, v);                   // rare: the chunk again, against a raised reference
-              }
-              // the chunk's exact maximum; a rescale of the running output and sum (and of the tile's probabilities
-              // so far) where it passes the reference by more than 2^8
-              again = true;
-              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int q = 0; q < CH / 32; ++q) {
-                const uint32_t seen = masked ? seen_bits(k0 + 32 * q) : ~0u;
-#pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                  mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], (seen >> i) & 1u ? __uint_as_float(v[32 * q + i]) : -INFINITY,
-                                           (seen >> (i + 1)) & 1u ? __uint_as_float(v[32 * q + i + 1]) : -INFINITY);
-              }
-              const float m_new = fmaxf(mr, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2);
-              const bool fresh = mr == -INFINITY;             // l and the row's outputs are zero
-              const bool need = m_new > mr + kRescaleLog2;    // (true for a fresh row that sees a key here)
-              if (need) {
-                const float alpha = fresh ? 1.0f : ex2_approx(mr - m_new);
-                mr = m_new;
-                l *= alpha;
-                mx[0] = alpha;
-              } else {
-                mx[0] = 1.0f;
-              }
-              if (__any_sync(0xffffffffu, need && !fresh)) {
-                const float alpha = mx[0];
-                if (!first) {
-                  // every earlier P U of the group has completed
-                  if (!mbar_wait_warp(&bars->pv_done[last % NSB], (last / NSB) & 1u, abort_flag, err)) { ok = false; break; }
-                  tc_fence_after();
-#pragma unroll 1
-                  for (int cc = 0; cc < D / 16; ++cc) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(tO + cc * 16, o);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tmem_st_32x32b_x16(tO + cc * 16, o);
-                  }
-                }
-                tmem_st_wait();
-#pragma unroll 1
-                for (int cc = 0; cc < c * (CH / 32); ++cc) {
-                  uint32_t q[16];
-                  tmem_ld_32x32b_x16(tS + 16 * cc, q);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const float2 f = unpack_bf16x2(q[i]);
-                    q[i] = pack_bf16x2(f.x * alpha, f.y * alpha);
-                  }
-                  tmem_st_32x32b_x16(tS + 16 * cc, q);
-                }
-                tmem_st_wait();
-              }
+              if (raise || !__any_sync(0xffffffffu, !(lt <= kSumLimit))) break;
             }
             if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            ready = __all_sync(0xffffffffu, mr != -INFINITY);
-            }
             l += lt;
           }
           // the previous item's output leaves the accumulator before this item's first P U
           if (c == BKV / CH - 1 && first && pend && !write_out()) { ok = false; break; }
-          store_chunk(tS + CH / 2 * c, pk);
+          tmem_st_32x32b_x32(tS + CH / 2 * c, pk);
         }
         if (!ok) break;
         // the group's next entry: its number, buffer and first key, and whether its scores are there (a wait costs 90
