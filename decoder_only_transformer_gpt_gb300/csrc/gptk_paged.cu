@@ -34,6 +34,7 @@ int paged_cache(PagedCache* c, const void* pool, const float* weight, const int3
 
 int finish(const char* what, cudaError_t e) {
   if (e == cudaSuccess) return GPT_OK;
+  cudaGetLastError();                                // reported here, and not again by the caller's next check
   set_detail(what, e);
   return e == cudaErrorMemoryAllocation ? GPT_ENOMEM : GPT_ECUDA;
 }

@@ -10,6 +10,12 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+int failed(const char* what, cudaError_t e) {
+  cudaGetLastError();                                // reported here, and not again by the caller's next check
+  set_detail(what, e);
+  return e == cudaErrorMemoryAllocation ? GPT_ENOMEM : GPT_ECUDA;
+}
+
 int window_shape(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t D, int32_t window, int32_t sinks) {
   if (B < 1 || T < 1 || H < 1 || Hkv < 1 || D < 1 || window < 1 || sinks < 0) return GPT_EINVAL;
   // the kernels number rows, heads and row elements with 32 bits
@@ -39,11 +45,7 @@ int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int3
   }
   const cudaError_t e = launch_attention_window_tc(tm, tm_y, B, T, H, Hkv, D, window, sinks, err, lse2,
                                                    reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) {
-    set_detail("window attention", e);
-    return GPT_ECUDA;
-  }
-  return GPT_OK;
+  return e == cudaSuccess ? GPT_OK : failed("window attention", e);
 }
 
 int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, const float* lse2, void* dqkv, int32_t B,
@@ -62,10 +64,7 @@ int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, co
   const size_t slab_b = attention_window_bwd_slab_bytes(B, T, H, Hkv, D, window, sinks);
   uint8_t* ws = nullptr;
   cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&ws), acc_b + row_b + slab_b, s);
-  if (e != cudaSuccess) {
-    set_detail("window attention derivative scratch", e);
-    return e == cudaErrorMemoryAllocation ? GPT_ENOMEM : GPT_ECUDA;
-  }
+  if (e != cudaSuccess) return failed("window attention derivative scratch", e);
   float* dqacc = reinterpret_cast<float*>(ws);
   float* rows = reinterpret_cast<float*>(ws + acc_b);
   float* slabs = reinterpret_cast<float*>(ws + acc_b + row_b);
@@ -79,11 +78,7 @@ int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, co
   e = launch_attention_window_bwd_tc(tq, tdy, tdkv, tdq, y, dy, lse2, rows, dqacc, slabs, dqkv, B, T, H, Hkv, D, window, sinks,
                                      err, s);
   scratch_free(ws, s);
-  if (e != cudaSuccess) {
-    set_detail("window attention derivative", e);
-    return GPT_ECUDA;
-  }
-  return GPT_OK;
+  return e == cudaSuccess ? GPT_OK : failed("window attention derivative", e);
 }
 
 }  // extern "C"

@@ -91,7 +91,7 @@ int gptk_attention_bwd(const void* qkv, const void* y, const void* dy, const flo
  * reads key head h / (H / Hkv). y [B, T, H D], heads merged; lse2 fp32 [B, H, T] or NULL: each row's base-2
  * log-sum-exp of its seen scaled scores, as for gptk_attention_lse. fp32 scores and sums; the probabilities are
  * rounded to bf16 for the product with the values. A sequence shorter than T is padded behind its end (rows of finite
- * numbers): no real token sees the padding. D in {32, 64}, H a multiple of Hkv, 16-byte aligned arrays
+ * numbers): no real token sees the padding. y overlaps no input. D in {32, 64}, H a multiple of Hkv, 16-byte aligned arrays
  * (GPT_ECONFIG otherwise), T < 2^30, B T < 2^31.
  */
 int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t D,
@@ -100,7 +100,7 @@ int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int3
 /*
  * Its derivative: from qkv, y and lse2 of gptk_attention_window (the same window and sinks) and dy [B, T, H D], writes
  * dqkv [B, T, (H + 2 Hkv) D]: dQ, and dK and dU summed over the H / Hkv query heads of a key head. Rows behind a
- * padded sequence's end take no part where their dy is zero. Scratch (4 B T H (D + 2) bytes and a little, and
+ * padded sequence's end take no part where their dy is zero. dqkv overlaps no input. Scratch (4 B T H (D + 2) bytes and a little, and
  * 1 KB x D for each part of a key tile that several CTAs share, a few hundred at most) is taken on the stream from a
  * pool that the library keeps; make a process's first call before any stream capture. dQ's fp32 additions come in an order that varies between runs.
  */
@@ -190,7 +190,7 @@ int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* 
  * that the table has room for) is taken on the stream from a pool that the library keeps; make a process's first call
  * before any stream capture. The caller counts lens up (one cache per layer
  * shares one lens). Sequences may share the pages of rows below their own; the new rows' pages are their own. fp32
- * scores and sums; the probabilities are rounded to bf16 for the product with the values.
+ * scores and sums; the probabilities are rounded to bf16 for the product with the values. y overlaps no input.
  */
 int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32_t* table, const int32_t* lens, void* y,
                          float* lse2, int32_t B, int32_t H, int32_t Hkv, int32_t D, int32_t pages, int32_t page,
