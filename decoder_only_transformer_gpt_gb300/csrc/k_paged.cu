@@ -855,9 +855,11 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
 
 // Moves the kept rows of one (sequence, key head), a cluster of blocks each: 8 D bytes per row, bound by memory. Row i
 // comes from a row at or behind i, so in place a chunk's rows are all read before any of them is written (a cluster
-// barrier between), and no later chunk reads what this one wrote. Into other pages no order is needed.
+// barrier between), and no later chunk reads what this one wrote. Into other pages no order is needed, and each of the
+// list's clusters takes its share of the chunks (in place the first cluster takes all).
 constexpr int kMoveBlocks = 8;
 constexpr int kMoveThreads = 256;
+constexpr int kMoveDepth = 2;
 
 template <int D>
 __global__ void __cluster_dims__(kMoveBlocks, 1, 1) __launch_bounds__(kMoveThreads)
@@ -867,14 +869,17 @@ paged_move_kernel(PagedCache c, const int32_t* __restrict__ dst_table, int dst_m
   pdl_trigger();
   constexpr int U = D / 8;
   constexpr int ROWS = kMoveThreads / U;             // rows a block copies at once
-  constexpr int K = 4;                               // times that, in flight
+  constexpr int K = kMoveDepth;                      // times that, in flight
   constexpr int CHUNK = kMoveBlocks * ROWS * K;
-  const int h = blockIdx.y, b = blockIdx.z, part = blockIdx.x, u = threadIdx.x % U;
+  const int h = blockIdx.y, b = blockIdx.z, u = threadIdx.x % U;
+  const int part = static_cast<int>(blockIdx.x) % kMoveBlocks, share = static_cast<int>(blockIdx.x) / kMoveBlocks;
   const int pmask = (1 << c.page_log2) - 1;
   const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
   const int32_t* drow = dst_table + static_cast<size_t>(b) * dst_max_pages;
   const int32_t* rows = kept + (static_cast<size_t>(b) * c.Hkv + h) * budget;
   const bool in_place = __ldg(trow) == __ldg(drow);
+  if (in_place && share > 0) return;                 // (the whole cluster)
+  const long long step = in_place ? CHUNK : static_cast<long long>(gridDim.x / kMoveBlocks) * CHUNK;
   uint4* pool = static_cast<uint4*>(c.pool);
   const size_t vstep = (static_cast<size_t>(c.Hkv) << c.page_log2) * U;   // from a page's keys to its values
   int r[K], src[K], dst[K];
@@ -891,8 +896,10 @@ paged_move_kernel(PagedCache c, const int32_t* __restrict__ dst_table, int dst_m
       dst[k] = __ldg(drow + (min(i, budget - 1) >> c.page_log2));
     }
   };
-  look_up(0);
-  for (int i0 = 0; i0 < budget; i0 += CHUNK) {
+  if (share * static_cast<long long>(CHUNK) >= budget) return;
+  look_up(share * CHUNK);
+  for (long long first = share * static_cast<long long>(CHUNK); first < budget; first += step) {
+    const int i0 = static_cast<int>(first);
     if (__ldg(rows + i0) < 0) break;                 // behind the last row (the same for the whole cluster)
     uint4 kx[K], vx[K];
     float wx[K];
@@ -915,7 +922,7 @@ paged_move_kernel(PagedCache c, const int32_t* __restrict__ dst_table, int dst_m
       to[k] = row_at(c, go[k] ? dst[k] : 0, 0, h, i & pmask) * U + u;
       wto[k] = weight_at(c, go[k] ? dst[k] : 0, h, i & pmask);
     }
-    if (i0 + CHUNK < budget) look_up(i0 + CHUNK);    // while the rows travel
+    if (first + step < budget) look_up(static_cast<int>(first + step));   // while the rows travel
     if (in_place) {
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1035,7 +1042,9 @@ cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const i
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, choose, c, lens, new_lens, kept, budget, sinks, recent, room, err);
   if (e != cudaSuccess) return e;
-  const dim3 grid(kMoveBlocks, static_cast<unsigned>(c.Hkv), static_cast<unsigned>(B));
+  const int chunk = kMoveBlocks * (kMoveThreads / (D / 8)) * kMoveDepth, chunks = (budget - 1) / chunk + 1;
+  const dim3 grid(static_cast<unsigned>(kMoveBlocks * (chunks < 8 ? chunks : 8)), static_cast<unsigned>(c.Hkv),
+                  static_cast<unsigned>(B));
   if (D == 64)
     return launch_k(paged_move_kernel<64>, grid, dim3(kMoveThreads), 0, s, c, dst_table, dst_max_pages,
                     static_cast<const int32_t*>(kept), budget, err);
