@@ -538,6 +538,256 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// The same attention where the rows that can be seen fit the warps of one cluster (UPW units per warp): one launch, no
+// scratch. Warp w of block `rank` takes units (j * 8 + w) * NC + rank, all of whose rows are copied at once;
+// it holds its scores in registers, so there is one maximum and no rescaling, and the attention weights follow from the
+// registers once the cluster's maxima and sums are known. Each block adds up its warps' outputs in shared memory and
+// pushes them to the block that joins that query row, and its maxima and sums to every block; one cluster barrier.
+// Bound by latency: the length and the page numbers, then the rows, then the barrier: 4.0 us for 600 rows x 12 heads,
+// where the two launches of the general form take 7.0.
+template <int D, int QR, int UPW>
+struct ShortCfg {
+  static constexpr int TILE = kUnit * D * 2;
+  static constexpr int WARP = UPW * 2 * TILE;
+  static constexpr int SMEM = 8 * WARP;
+};
+
+template <int D, int QR, int UPW>
+__global__ void __launch_bounds__(256, UPW == 1 ? 3 : 1)
+paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const int32_t* __restrict__ lens,
+                   __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, DecShape w, int* err) {
+  using Cfg = ShortCfg<D, QR, UPW>;
+  constexpr int U = D / 8, RPI = 32 / U, NT = D / 8, RH = QR == 16 ? 2 : 1;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[8][QR];                     // the warps' maxima and sums
+  __shared__ float2 s_all[8][QR];                    // the blocks', pushed by each of them
+  __shared__ float s_o[QR][D];                       // pushed outputs: [row / NC * NC + block][D]
+  auto cluster = cooperative_groups::this_cluster();
+  const int NC = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // every block has started (awaited below)
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y, hm = static_cast<int>(blockIdx.x) / NC;
+  const int kh = hm / w.mg, g0 = (hm - kh * w.mg) * 16, gn = min(w.G - g0, 16);
+  const int row = w.H + 2 * c.Hkv, pmask = (1 << c.page_log2) - 1;
+  const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
+  const __nv_bfloat16* tok = qkv + static_cast<size_t>(b) * row * D;
+  int last = __ldg(lens + b);
+  int page[UPW];                                     // on its way before the length is known: right unless a window cuts
+#pragma unroll
+  for (int j = 0; j < UPW; ++j)
+    page[j] = __ldg(trow + min((((j * 8 + warp) * NC + rank) * kUnit + lane) >> c.page_log2, c.max_pages - 1));
+  const int qrow = lane >> 2, qcol = 2 * (lane & 3);
+  uint32_t qf[D / 16][4];                            // A operand: the group's queries, zeros behind them
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = qrow + 8 * (i & 1);
+      qf[k][i] = (i & 1) < RH && r < gn
+          ? __ldg(reinterpret_cast<const uint32_t*>(tok + static_cast<size_t>(kh * w.G + g0 + r) * D + 16 * k + 8 * (i >> 1) + qcol))
+          : 0u;
+    }
+  if (last >= static_cast<long long>(c.max_pages) << c.page_log2) {
+    if (tid == 0) record_error(err, GPT_DEV_EPAGE);
+    last = -1;
+  }
+  const Seen seen = seen_rows(last + 1, w.window, w.sinks);
+  uint8_t* ring = smem + warp * Cfg::WARP;
+  const uint32_t ring_a = smem_u32(ring);
+  const size_t vstep = (static_cast<size_t>(c.Hkv) << c.page_log2) * D;
+  const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(c.pool);
+  uint32_t mask[UPW];
+#pragma unroll
+  for (int j = 0; j < UPW; ++j) {
+    const int v = ((j * 8 + warp) * NC + rank) * kUnit + lane, r = seen_row(seen, v);
+    bool ok = v < seen.n;
+    if (ok && r != v) page[j] = __ldg(trow + (r >> c.page_log2));
+    const __nv_bfloat16* kp = pool;
+    size_t dv = vstep;
+    if (ok && static_cast<unsigned>(page[j]) >= static_cast<unsigned>(c.pages)) record_error(err, GPT_DEV_EPAGE);
+    if (ok && r == last) {                           // the new token's own row comes from qkv
+      kp = tok + static_cast<size_t>(w.H + kh) * D;
+      dv = static_cast<size_t>(c.Hkv) * D;
+    } else {
+      ok = ok && static_cast<unsigned>(page[j]) < static_cast<unsigned>(c.pages);
+      if (ok) kp = pool + row_at(c, page[j], 0, kh, r & pmask) * D;
+    }
+    mask[j] = __ballot_sync(0xffffffffu, ok);
+    const unsigned long long ka = reinterpret_cast<unsigned long long>(kp);
+    const unsigned long long va = reinterpret_cast<unsigned long long>(kp + (ok ? dv : 0));
+    const uint32_t sk = ring_a + j * 2 * Cfg::TILE, sv = sk + Cfg::TILE;
+    const int u = lane % U;
+    if (mask[j])
+#pragma unroll
+      for (int i = 0; i < kUnit / RPI; ++i) {
+        const int rr = i * RPI + lane / U;
+        const bool have = (mask[j] >> rr) & 1u;
+        const unsigned long long k = __shfl_sync(0xffffffffu, ka, rr), x = __shfl_sync(0xffffffffu, va, rr);
+        cp_async16(sk + tile_at<D>(rr, u), reinterpret_cast<const uint8_t*>(k) + 16 * u, have);
+        cp_async16(sv + tile_at<D>(rr, u), reinterpret_cast<const uint8_t*>(x) + 16 * u, have);
+      }
+  }
+  // the newest row into the cache, by the warp whose unit holds it
+  const int ntail = (seen.n - 1) / kUnit;            // its unit
+  if (last >= 0 && g0 == 0 && ntail % NC == rank && (ntail / NC) % 8 == warp) {
+    const int pg = __ldg(trow + (last >> c.page_log2));
+    if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages) && lane < 2 * U) {
+      const int which = lane / U, u = lane % U;
+      reinterpret_cast<uint4*>(c.pool)[row_at(c, pg, which, kh, last & pmask) * U + u] =
+          __ldg(reinterpret_cast<const uint4*>(tok + static_cast<size_t>(w.H + which * c.Hkv + kh) * D) + u);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+
+  float s[4 * UPW][4];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  float o[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < UPW; ++t) {
+    const uint32_t sk = ring_a + t * 2 * Cfg::TILE;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float (&x)[4] = s[4 * t + j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = 0.0f;
+      if (mask[t])
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t f[4];
+          ldmatrix4(f, sk + tile_at<D>(8 * j + (lane & 7), 4 * k + (lane >> 3)));
+          mma_16816(x, qf[2 * k], f[0], f[1]);
+          mma_16816(x, qf[2 * k + 1], f[2], f[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < 2 * RH; ++i) {
+        x[i] = (mask[t] >> (8 * j + qcol + (i & 1))) & 1u ? x[i] * w.scale_log2 : -INFINITY;
+        m[i >> 1] = fmaxf(m[i >> 1], x[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int rh = 0; rh < RH; ++rh) {
+    m[rh] = fmaxf(m[rh], __shfl_xor_sync(0xffffffffu, m[rh], 1));
+    m[rh] = fmaxf(m[rh], __shfl_xor_sync(0xffffffffu, m[rh], 2));
+    const float ref = m[rh] == -INFINITY ? 0.0f : m[rh];   // nothing seen: every term is 2^-inf
+#pragma unroll
+    for (int j = 0; j < 4 * UPW; ++j) {
+      s[j][2 * rh] = ex2_approx(s[j][2 * rh] - ref);
+      s[j][2 * rh + 1] = ex2_approx(s[j][2 * rh + 1] - ref);
+      l[rh] += s[j][2 * rh] + s[j][2 * rh + 1];
+    }
+    l[rh] += __shfl_xor_sync(0xffffffffu, l[rh], 1);
+    l[rh] += __shfl_xor_sync(0xffffffffu, l[rh], 2);
+  }
+#pragma unroll
+  for (int k = 0; k < 2 * UPW; ++k) {
+    if (!mask[k >> 1]) continue;
+    const uint32_t sv = ring_a + (k >> 1) * 2 * Cfg::TILE + Cfg::TILE;
+    uint32_t p[4];
+    p[0] = pack_bf16x2(s[2 * k][0], s[2 * k][1]);
+    p[2] = pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]);
+    p[1] = RH == 2 ? pack_bf16x2(s[2 * k][2], s[2 * k][3]) : 0u;
+    p[3] = RH == 2 ? pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3]) : 0u;
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j) {
+      uint32_t f[4];
+      ldmatrix4_trans(f, sv + tile_at<D>(16 * (k & 1) + (lane & 15), 2 * j + (lane >> 4)));
+      mma_16816(o[2 * j], p, f[0], f[1]);
+      mma_16816(o[2 * j + 1], p, f[2], f[3]);
+    }
+  }
+  __syncwarp();                                      // the warp's tiles are read: its outputs take their place
+  float* own = reinterpret_cast<float*>(ring);       // [QR][D]
+#pragma unroll
+  for (int rh = 0; rh < RH; ++rh) {
+    const int r = qrow + 8 * rh;
+    if (r >= gn) continue;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(own + r * D + 8 * j + qcol) = make_float2(o[j][2 * rh], o[j][2 * rh + 1]);
+    if ((lane & 3) == 0) s_ml[warp][r] = make_float2(m[rh], l[rh]);
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  // this block's maximum, sum and output of each row, to the blocks that want them
+  for (int i = tid; i < gn * D; i += 256) {
+    const int r = i / D, d = i % D;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, s_ml[k][r].x);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    float lt = 0.0f, acc = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = ex2_approx(s_ml[k][r].x - ref);
+      lt += s_ml[k][r].y * f;
+      acc += reinterpret_cast<const float*>(smem + k * Cfg::WARP)[r * D + d] * f;
+    }
+    cluster.map_shared_rank(&s_o[0][0], r % NC)[(r / NC * NC + rank) * D + d] = acc;
+    if (d < NC) cluster.map_shared_rank(&s_all[0][0], d)[rank * QR + r] = make_float2(mx, lt);
+  }
+  cluster.sync();
+  auto joined = [&](int r, float* sum) -> float {    // a row's maximum and sum over all blocks
+    float mx = -INFINITY;
+    for (int k = 0; k < NC; ++k) mx = fmaxf(mx, s_all[k][r].x);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    float lt = 0.0f;
+    for (int k = 0; k < NC; ++k) lt += s_all[k][r].y * ex2_approx(s_all[k][r].x - ref);
+    *sum = lt;
+    return mx;
+  };
+  if (last >= 0)
+    for (int i = tid; i < (gn + NC - 1) / NC * D; i += 256) {
+      const int r = i / D * NC + rank, d = i % D;
+      if (r >= gn) continue;
+      float lt;
+      const float mx = joined(r, &lt), ref = mx == -INFINITY ? 0.0f : mx;
+      float acc = 0.0f;
+      for (int k = 0; k < NC; ++k) acc += s_o[r / NC * NC + k][d] * ex2_approx(s_all[k][r].x - ref);
+      const size_t head = static_cast<size_t>(b) * w.H + kh * w.G + g0 + r;
+      y[head * D + d] = __float2bfloat16(lt == 0.0f ? 0.0f : acc / lt);
+      if (d == 0 && lse2) lse2[head] = mx + log2f(lt);
+    }
+  if (!c.weight) return;
+  // the weights: a row's probabilities summed over the group's heads, one row per lane
+  float f[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int rh = 0; rh < RH; ++rh)
+    if (qrow + 8 * rh < gn) {
+      float lt;
+      const float mx = joined(qrow + 8 * rh, &lt);
+      f[rh] = m[rh] == -INFINITY ? 0.0f : ex2_approx(m[rh] - mx) / lt;
+    }
+#pragma unroll
+  for (int t = 0; t < UPW; ++t) {
+    if (!mask[t]) continue;
+    float mine = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = qrow < gn ? s[4 * t + j][i] * f[0] : 0.0f;   // (rows behind the group may hold NaN)
+        if (RH == 2 && qrow + 8 < gn) x += s[4 * t + j][2 + i] * f[1];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (qrow == 2 * j + i) mine = x;
+      }
+    const int at = 8 * (qrow >> 1) + qcol + (qrow & 1), v = ((t * 8 + warp) * NC + rank) * kUnit + at, r = seen_row(seen, v);
+    const int pg = __shfl_sync(0xffffffffu, page[t], at);
+    if (v >= seen.n || static_cast<unsigned>(pg) >= static_cast<unsigned>(c.pages)) continue;
+    float* dst = c.weight + weight_at(c, pg, kh, r & pmask);
+    if (r == last) *dst = mine;
+    else atomicAdd(dst, mine);                       // sequences may share a page
+  }
+}
+
 // Joins the partial results of a (sequence, key head), and adds the attention weights of its seen rows: block
 // (key head, z, sequence) takes rows z kJoinRows, + kJoinRows, then on in steps of the grid; blocks z > 0 only that.
 constexpr int kJoinThreads = 256;
@@ -623,7 +873,7 @@ paged_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16*
           lt += s_l[part + k] * f;
           at += s_o[part + k][d] * f;
         }
-        if (blockIdx.y == 0) y[(head0 + r) * D + d] = __float2bfloat16(lt > 0.0f ? at / lt : 0.0f);
+        if (blockIdx.y == 0) y[(head0 + r) * D + d] = __float2bfloat16(lt == 0.0f ? 0.0f : at / lt);
         if (d == 0) {
           const float lse = mx + log2f(lt);
           s_lse[mt * 16 + r] = lse;
@@ -949,6 +1199,28 @@ cudaError_t launch_paged_store(const PagedCache& c, const void* qkv, const int32
 
 namespace {
 
+template <int D, int QR, int UPW>
+cudaError_t launch_short(const PagedCache& c, const __nv_bfloat16* qkv, const int32_t* lens, __nv_bfloat16* y, float* lse2,
+                         const DecShape& w, int nc, int dev, int* err, cudaStream_t s) {
+  static SmemLimit limit;
+  constexpr int smem = ShortCfg<D, QR, UPW>::SMEM;
+  const cudaError_t e = limit.raise(paged_short_kernel<D, QR, UPW>, dev, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(nc) * c.Hkv * w.mg, static_cast<unsigned>(w.B));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(nc), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, paged_short_kernel<D, QR, UPW>, c, qkv, lens, y, lse2, w, err);
+}
+
 template <int D, int QR>
 cudaError_t launch_decode(const PagedCache& c, const __nv_bfloat16* qkv, const int32_t* lens, __nv_bfloat16* y, float* lse2,
                           DecShape w, int* err, cudaStream_t s) {
@@ -957,16 +1229,28 @@ cudaError_t launch_decode(const PagedCache& c, const __nv_bfloat16* qkv, const i
   int dev = 0, num_sms = 0;
   cudaError_t e = device_sms(&dev, &num_sms);
   if (e != cudaSuccess) return e;
-  // one block per SM with as many warps (rings) as its shared memory holds beside the lists, 8 at most
-  const size_t lists = (2 * static_cast<size_t>(w.B) + 1) * sizeof(int);
-  const size_t room = 232448 - 256 - lists;
+  long long seen_max = static_cast<long long>(c.max_pages) << c.page_log2;
+  if (w.window > 0 && static_cast<long long>(w.window) + w.sinks < seen_max) seen_max = w.window + w.sinks;
+  // Few rows in sight: one launch of clusters (8 NC warps of UPW units). It pays for blocks that a short sequence leaves
+  // idle, so it is taken up to 12 blocks per SM with one unit per warp (2,048 rows: 16 sequences x 12 heads of up to
+  // 1,023 rows 9.9 against 13.0 us, of 2,047 rows 16.7 against 17.6; 64 sequences of 1,023, 20 blocks per SM, 36.8
+  // against 33.4), and with two units while all blocks run at once (one per SM; 4,095 rows: one sequence 4.9 against
+  // 13.2 us, four of them, 2.5 blocks per SM, 14.3 against 13.2).
+  const long long units = (seen_max + kUnit - 1) / kUnit, lists = static_cast<long long>(w.B) * c.Hkv * w.mg;
+  if (units <= 128 && (!c.weight || w.mg == 1)) {
+    int nc = 1;
+    while (nc < 8 && nc * 8 < units) nc *= 2;
+    if (units <= 64 && nc * lists <= 12LL * num_sms) return launch_short<D, QR, 1>(c, qkv, lens, y, lse2, w, nc, dev, err, s);
+    if (units > 64 && nc * lists <= num_sms) return launch_short<D, QR, 2>(c, qkv, lens, y, lse2, w, nc, dev, err, s);
+  }
+  // one block per SM with as many warps (rings) as its shared memory holds beside the sequences' lengths, 8 at most
+  const size_t head = (2 * static_cast<size_t>(w.B) + 1) * sizeof(int);
+  const size_t room = 232448 - 256 - head;
   const int warps = room / Cfg::WARP < 8 ? static_cast<int>(room / Cfg::WARP) : 8;
-  const size_t smem = static_cast<size_t>(warps) * Cfg::WARP + lists;
+  const size_t smem = static_cast<size_t>(warps) * Cfg::WARP + head;
   e = limit.raise(paged_split_kernel<D, QR>, dev, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int NW = num_sms * warps;
-  long long seen_max = static_cast<long long>(c.max_pages) << c.page_log2;
-  if (w.window > 0 && static_cast<long long>(w.window) + w.sinks < seen_max) seen_max = w.window + w.sinks;
   const int score_ld = static_cast<int>((seen_max + kUnit - 1) / kUnit * kUnit);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t pre_b = up((w.B + 1) * sizeof(int)), o_b = up(static_cast<size_t>(NW) * 2 * QR * D * sizeof(float)),

@@ -1,0 +1,99 @@
+"""Attention of one new token on the GPU: the form for few rows in sight (one launch of clusters, one or two units of 32
+rows per warp) and the general one, chosen by the page table's width, at the sizes where the choice turns.
+
+The cases, the reference and the tolerances are those of test_gpu_paged.py: both forms take the same roundings, and the
+form for few rows one more factor 2^(m - M) per weight, whose 2^-22 the doubled bound of that file covers.
+"""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from gpu_util import host  # noqa: E402
+from test_gpu_paged import Case  # noqa: E402
+
+
+def widened(c, rows):
+    """A page table for `rows` rows: the entries behind the sequences' pages name no page, and are not used."""
+    more = rows // c.page - c.table.shape[1]
+    assert more >= 0
+    c.table = np.concatenate([c.table, np.full((c.table.shape[0], more), 10 ** 9, np.int32)], axis=1)
+    return c.device()
+
+
+def run(c):
+    from decoder_only_transformer_gpt_gb300 import binding
+    c.call()
+    binding.status()
+    c.check()
+
+
+@pytest.mark.parametrize("rows", [1024, 2048, 4096, 65536])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 4, 64), (8, 1, 32), (12, 1, 64), (16, 1, 32), (9, 3, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (33, 2), (500, 7)])
+def test_every_form_at_every_length(gpt_lib, rows, H, Hkv, D, window, sinks):
+    for lens in ([0], [1], [30, 31, 32], [-1, 255, 256, 257], [600, -1]):
+        run(widened(Case(H, Hkv, D, 16, lens, window, sinks, seed=rows + sum(lens)), rows))
+
+
+@pytest.mark.parametrize("rows", [2047, 2048, 2049, 4095, 4096, 4097])
+@pytest.mark.parametrize("weights", [False, True])
+def test_full_tables_where_the_form_turns(gpt_lib, rows, weights):
+    # the new token's row is the last that the table has room for, or near it
+    run(Case(2, 2, 64, 8, [rows - 1], seed=rows, weights=weights).device())
+    run(Case(4, 2, 32, 64, [rows - 1, 5], seed=rows, weights=weights).device())
+
+
+@pytest.mark.parametrize("lists", [12 * 152 - 2, 12 * 152, 12 * 152 + 2])
+def test_batches_where_the_form_turns(gpt_lib, lists):
+    rng = np.random.default_rng(lists)
+    run(Case(2, 2, 32, 8, rng.integers(-1, 255, lists // 2).tolist(), seed=lists).device())
+
+
+@pytest.mark.parametrize("rows", [1024, 4096, 65536])
+@pytest.mark.parametrize("weights", [False, True])
+def test_more_query_heads_than_a_tile(gpt_lib, rows, weights):
+    run(widened(Case(40, 2, 64, 16, [700, 3, 64], seed=rows, weights=weights), rows))
+
+
+@pytest.mark.parametrize("rows", [1024, 4096, 65536])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3)])
+def test_a_nan_in_sight_shows(gpt_lib, rows, window, sinks):
+    # a NaN in a seen key or value makes the outputs of its key head's queries NaN, and no other's
+    from decoder_only_transformer_gpt_gb300 import binding
+    for which in (0, 1):
+        c = Case(6, 2, 64, 16, [400, 90], window, sinks, seed=rows, weights=False)
+        p, s = c.table[0, 380 // 16], 380 % 16
+        c.pool[p, which, 1, s, 5 if which == 0 else slice(None)] = np.nan
+        widened(c, rows)
+        c.call()
+        binding.status()
+        y = host(c.d_y).reshape(2, 6, 64)
+        assert np.isnan(y[0, 3:]).all() and np.isfinite(y[0, :3]).all() and np.isfinite(y[1]).all()
+
+
+@pytest.mark.parametrize("rows", [1024, 4096, 65536])
+def test_bad_pages_in_every_form(gpt_lib, rows):
+    # rows of a page outside the pool are left out and reported; the other sequences are right
+    from decoder_only_transformer_gpt_gb300 import binding
+    for bad in (-1, 10 ** 9):
+        c = widened(Case(4, 2, 64, 16, [100, 50], seed=14, weights=False), rows)
+        c.d_table[0, 2] = bad
+        c.call()
+        with pytest.raises(binding.GptError) as e:
+            binding.status()
+        assert e.value.code == binding.GPT_EPAGE
+        binding.status()
+        c.check(skip=(0,))
+
+
+def test_one_result_bit_for_bit_in_every_form(gpt_lib):
+    for rows in (1024, 4096, 65536):
+        c = widened(Case(8, 2, 64, 16, [900, 20, 333], seed=6), rows)
+        c.call()
+        y, lse2, w0 = c.d_y.clone(), c.d_lse2.clone(), c.d_weight.clone()
+        c.device()
+        c.call()
+        assert torch.equal(y, c.d_y) and torch.equal(lse2, c.d_lse2) and torch.equal(w0, c.d_weight)
