@@ -936,8 +936,8 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
   pdl_wait();
   pdl_trigger();
   extern __shared__ uint32_t s_rank[];               // [room] ranks of this block's stretch
-  __shared__ int hist[kEvBins];
-  __shared__ int s_sum[kEvWarps], s_tie[kEvWarps], pick[2], s_total[2];
+  __shared__ __align__(16) int hists[3][kEvBins];    // one per pass: another block may still read the last one's
+  __shared__ int s_sum[kEvWarps], s_tie[kEvWarps], pick[3], s_total[2];
   const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC), h = static_cast<int>(blockIdx.x / NC), b = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pmask = (1 << c.page_log2) - 1;
@@ -972,7 +972,7 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
     const int r = lo + base + i, pg = page_of(c, trow, r, err);
     return pg < 0 ? 0u : weight_rank(__ldg(c.weight + weight_at(c, pg, h, r & pmask)));
   };
-  for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
+  for (int i = tid; i < 3 * kEvBins; i += kEvThreads) hists[0][i] = 0;
   __syncthreads();
   if (fits) {
     // K pages, then K weights in flight per thread: bad pages are looked at behind the loads (a branch between them
@@ -995,20 +995,19 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
         if (!ok) record_error(err, GPT_DEV_EPAGE);
         const uint32_t k = ok ? weight_rank(wt[j]) : 0u;
         s_rank[i0 + j * kEvThreads] = k;
-        atomicAdd(&hist[k >> 21], 1);                // the first pass
+        atomicAdd(&hists[0][k >> 21], 1);            // the first pass
       }
     }
   } else {
-    for (int i = tid; i < size; i += kEvThreads) atomicAdd(&hist[load(i) >> 21], 1);
+    for (int i = tid; i < size; i += kEvThreads) atomicAdd(&hists[0][load(i) >> 21], 1);
   }
   uint32_t prefix = 0;                               // the leading bits of the smallest kept rank
   int low = 32;                                      // bits below them
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass == 2 ? 10 : 11, shift = low - bits;
+    int* hist = hists[pass];
     if (pass > 0) {
-      for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
-      __syncthreads();
       for (int i = tid; i < size; i += kEvThreads) {
         const uint32_t k = fits ? s_rank[i] : load(i);
         if ((k >> low) == (prefix >> low)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
@@ -1036,7 +1035,7 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
       if (lane + k < 32) above += v;
     }
     if (lane == 0) s_sum[warp] = above;
-    sync_all();                                      // sums are written, and no block reads another's histogram any more
+    __syncthreads();
     for (int w = warp + 1; w < kEvWarps; ++w) above += s_sum[w];
     above -= own;                                    // rows in bins behind this thread's
     if (above < want && above + own >= want) {       // one thread of each block
@@ -1046,21 +1045,28 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
         if (j == k && c4[k] < left) { left -= c4[k]; --j; }
       pick[0] = tid * BPT + j;
       pick[1] = left;                                // still to take among the rows of that bin
+      int bin = c4[0];
+#pragma unroll
+      for (int k = 1; k < BPT; ++k)
+        if (j == k) bin = c4[k];
+      pick[2] = bin;
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(pick[0]) << shift;
     want = pick[1];
     low = shift;
+    if (want == pick[2]) break;                      // all of that bin are kept: no need to order them
   }
-  // kept: every row of a rank above prefix and the first `want` of rank prefix
+  // kept: every row whose leading bits are above prefix and the first `want` where they are equal
+  prefix >>= low;
   const int per = ((size + kEvWarps - 1) / kEvWarps + 31) / 32 * 32;   // rows of a warp's stretch
   const int first = min(size, warp * per), end = min(size, first + per);
   int sure = 0, ties = 0;
   for (int i0 = first; i0 < end; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < end ? (fits ? s_rank[i] : load(i)) : 0u;
-    sure += __popc(__ballot_sync(0xffffffffu, i < end && k > prefix));
-    ties += __popc(__ballot_sync(0xffffffffu, i < end && k == prefix));
+    sure += __popc(__ballot_sync(0xffffffffu, i < end && (k >> low) > prefix));
+    ties += __popc(__ballot_sync(0xffffffffu, i < end && (k >> low) == prefix));
   }
   __syncthreads();
   if (lane == 0) {
@@ -1093,8 +1099,8 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
   for (int i0 = first; i0 < end; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < end ? (fits ? s_rank[i] : load(i)) : 0u;
-    const uint32_t tie = __ballot_sync(0xffffffffu, i < end && k == prefix), below = (1u << lane) - 1u;
-    const bool keep = i < end && (k > prefix || (k == prefix && seen_ties + __popc(tie & below) < want));
+    const uint32_t tie = __ballot_sync(0xffffffffu, i < end && (k >> low) == prefix), below = (1u << lane) - 1u;
+    const bool keep = i < end && ((k >> low) > prefix || ((k >> low) == prefix && seen_ties + __popc(tie & below) < want));
     const uint32_t mask = __ballot_sync(0xffffffffu, keep);
     if (keep) out[at + __popc(mask & below)] = lo + base + i;
     at += __popc(mask);
@@ -1304,7 +1310,7 @@ cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const i
   // table allows, as far as shared memory goes
   const long long rows = (static_cast<long long>(c.max_pages) << c.page_log2) - sinks - recent;
   const int nc = rows <= 4096 ? 1 : 4;
-  const long long most = (232448 - 16384) / 4, stretch = rows < 0 ? 0 : ((rows + nc - 1) / nc + 31) / 32 * 32;
+  const long long most = (232448 - 28672) / 4, stretch = rows < 0 ? 0 : ((rows + nc - 1) / nc + 31) / 32 * 32;
   const int room = static_cast<int>(stretch < most ? stretch : most);
   auto choose = nc == 1 ? paged_choose_kernel<1> : paged_choose_kernel<4>;
   static SmemLimit limit[2];
