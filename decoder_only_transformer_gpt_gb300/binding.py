@@ -399,6 +399,12 @@ def _arg(name: str, t, dtype, shape, dev) -> int:
     return t.data_ptr()
 
 
+def _int32(**numbers) -> None:
+    for name, n in numbers.items():
+        if not -2 ** 31 <= n < 2 ** 31:              # ctypes would pass its low 32 bits
+            raise ValueError(f"{name}: {n}, needs an int32")
+
+
 def _qkv_dims(qkv, H: int, Hkv: int):
     """(B, T, D) of fused rows [B, T, (H + 2 Hkv) D]."""
     shape = qkv.shape
@@ -411,6 +417,8 @@ def _qkv_dims(qkv, H: int, Hkv: int):
 def attention_window(qkv, y, H: int, Hkv: int, window: int, sinks: int = 0, lse2=None, stream=None):
     """Causal attention over the last `window` keys and the first `sinks`: qkv [B, T, (H + 2 Hkv) D] -> y [B, T, H D];
     lse2 [B, H, T] (optional, needed by the derivative) takes each row's base-2 log-sum-exp."""
+    if (window | sinks) >> 31 not in (0, -1):
+        _int32(window=window, sinks=sinks)
     lib = _LIB or load()
     torch, dev, s = _cuda(stream)
     B, T, D = _qkv_dims(qkv, H, Hkv)
@@ -425,6 +433,8 @@ def attention_window(qkv, y, H: int, Hkv: int, window: int, sinks: int = 0, lse2
 
 def attention_window_bwd(qkv, y, dy, lse2, dqkv, H: int, Hkv: int, window: int, sinks: int = 0, stream=None):
     """dqkv of attention_window from its input, output, log-sum-exp and the output's gradient dy [B, T, H D]."""
+    if (window | sinks) >> 31 not in (0, -1):
+        _int32(window=window, sinks=sinks)
     lib = _LIB or load()
     torch, dev, s = _cuda(stream)
     B, T, D = _qkv_dims(qkv, H, Hkv)
@@ -471,6 +481,8 @@ def paged_attention(qkv, pool, table, lens, y, H: int, lse2=None, weight=None, w
 
     window 0 sees every cached row, else the last `window` rows and the first `sinks`; weight (optional) sums
     each row's attention weight, lse2 [B, H] (optional) takes the log-sum-exp. lens[b] < 0 skips row b."""
+    if (window | sinks) >> 31 not in (0, -1):
+        _int32(window=window, sinks=sinks)
     lib = _LIB or load()
     torch, dev, s = _cuda(stream)
     pages, Hkv, page, D, B, max_pages, p, w, tb = _cache(torch, pool, weight, table, dev)
@@ -487,6 +499,8 @@ def paged_evict(pool, weight, table, lens, dst_table, new_lens, kept, budget: in
                 stream=None):
     """Keep budget rows per sequence and key head (first `sinks`, last `recent`, largest weights between), in order,
     in the pages of dst_table (`table` itself: in place); kept [B, Hkv, budget] names them, -1 behind the last."""
+    if (budget | sinks | recent) >> 31 not in (0, -1):
+        _int32(budget=budget, sinks=sinks, recent=recent)
     lib = _LIB or load()
     torch, dev, s = _cuda(stream)
     pages, Hkv, page, D, B, max_pages, p, w, tb = _cache(torch, pool, weight, table, dev)

@@ -51,6 +51,7 @@ int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* 
   const int rc = paged_cache(&c, pool, weight, table, B, Hkv, D, pages, page, max_pages);
   if (rc != GPT_OK) return rc;
   if (H % Hkv || !aligned16(qkv)) return GPT_ECONFIG;
+  if ((static_cast<int64_t>(H) + 2LL * Hkv) * D > 0x3fffffffLL) return GPT_EINVAL;   // a row's elements: 32 bits
   if (T == 0) return GPT_OK;
   int* err = step_err_word();
   if (!err) return GPT_ENOMEM;

@@ -91,8 +91,10 @@ int gptk_attention_bwd(const void* qkv, const void* y, const void* dy, const flo
  * reads key head h / (H / Hkv). y [B, T, H D], heads merged; lse2 fp32 [B, H, T] or NULL: each row's base-2
  * log-sum-exp of its seen scaled scores, as for gptk_attention_lse. fp32 scores and sums; the probabilities are
  * rounded to bf16 for the product with the values. A sequence shorter than T is padded behind its end (rows of finite
- * numbers): no real token sees the padding. y overlaps no input. D in {32, 64}, H a multiple of Hkv, 16-byte aligned arrays
- * (GPT_ECONFIG otherwise), T < 2^30, B T < 2^31.
+ * numbers): no real token sees the padding. A value that is not finite makes the outputs of the queries that see it NaN,
+ * and may make those of others of its tile of 128 tokens and the tiles that read it so. y overlaps no input. D in {32, 64},
+ * H a multiple of Hkv, 16-byte aligned arrays (GPT_ECONFIG otherwise), T < 2^30, B T < 2^31, rows of less than 2^30
+ * elements.
  */
 int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t D,
                           int32_t window, int32_t sinks, void* stream);
@@ -100,9 +102,10 @@ int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int3
 /*
  * Its derivative: from qkv, y and lse2 of gptk_attention_window (the same window and sinks) and dy [B, T, H D], writes
  * dqkv [B, T, (H + 2 Hkv) D]: dQ, and dK and dU summed over the H / Hkv query heads of a key head. Rows behind a
- * padded sequence's end take no part where their dy is zero. dqkv overlaps no input. Scratch (4 B T H (D + 2) bytes and a little, and
- * 1 KB x D for each part of a key tile that several CTAs share, a few hundred at most) is taken on the stream from a
- * pool that the library keeps; make a process's first call before any stream capture. dQ's fp32 additions come in an order that varies between runs.
+ * padded sequence's end take no part where their dy is zero. dqkv overlaps no input. Scratch (4 B T H (D + 2) bytes and
+ * a little, and 1 KB x D for each part of a key tile that several CTAs share, a few hundred at most) is taken on the
+ * stream from a pool that the library keeps; make a process's first call before any stream capture. dQ's fp32 additions
+ * come in an order that varies between runs.
  */
 int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, const float* lse2, void* dqkv, int32_t B,
                               int32_t T, int32_t H, int32_t Hkv, int32_t D, int32_t window, int32_t sinks, void* stream);
@@ -164,7 +167,8 @@ int gptk_lmhead_ce_noalloc(const void* h, const void* wte, const int32_t* target
  *   weight  [pages][Hkv][page] fp32 or NULL: per cached row and key head, the attention weight it has received
  *   table   [B][max_pages] int32: row r of sequence b lies in page table[b][r / page] at slot r % page
  * page is a power of two, 8..256. H query heads share Hkv key heads (H a multiple of Hkv): query head h reads key
- * head h / (H / Hkv), H / Hkv <= 128 for the attention. A token's qkv row holds H D queries, Hkv D keys, Hkv D values, as the output of one product.
+ * head h / (H / Hkv), H / Hkv <= 128 for the attention. A token's qkv row holds H D queries, Hkv D keys, Hkv D values,
+ * as the output of one product (less than 2^30 elements).
  * All arrays are device memory of the current device, pool, qkv and y 16-byte aligned. B <= 8192.
  * GPT_EINVAL: null pointers or sizes; GPT_ECONFIG: D, H % Hkv or alignment. Checked on the device: a page number
  * outside [0, pages) or a row past max_pages * page is neither read nor written, and gptk_status() then returns
@@ -186,8 +190,8 @@ int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* 
  *   lse2[b, h] = log2 sum_r 2^(q_h . k_r log2(e) / sqrt(D))         fp32 [B, H], NULL: not wanted
  *   weight(r, key head) += the sum of a_r over the head's H / Hkv queries (r < n); = that sum for row n
  * lens[b] < 0: no sequence; nothing of row b is read or written. B max_pages page / 32 < 2^31, and times Hkv
- * <= 2^40 (GPT_EINVAL otherwise). Scratch (about 10 MB at most, and with weights 4 bytes per query head and seen row
- * that the table has room for) is taken on the stream from a pool that the library keeps; make a process's first call
+ * <= 2^40 (GPT_EINVAL otherwise). Scratch (none where the table, or the window and sinks, hold few rows; else about
+ * 10 MB at most, and with weights 4 bytes per query head and seen row that the table has room for) is taken on the stream from a pool that the library keeps; make a process's first call
  * before any stream capture. The caller counts lens up (one cache per layer
  * shares one lens). Sequences may share the pages of rows below their own; the new rows' pages are their own. fp32
  * scores and sums; the probabilities are rounded to bf16 for the product with the values. y overlaps no input.
@@ -204,7 +208,7 @@ int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32
  * kept[b][head][i] (int32 [B, Hkv, budget]) is the row that row i was, -1 behind the last; new_lens[b] =
  * min(lens[b], budget) (lens[b] itself where it is negative; new_lens must not be lens). dst_table either is
  * `table`, or starts every sequence with the same pages (in place), or names pages that no sequence of `table`
- * holds, each once; the old rows then stay as they were.
+ * holds, each once; the old rows then stay as they were. In place no page may be held by two sequences.
  */
 int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int32_t* lens, const int32_t* dst_table,
                      int32_t* new_lens, int32_t* kept, int32_t B, int32_t Hkv, int32_t D, int32_t pages, int32_t page,

@@ -122,3 +122,24 @@ def test_the_plain_forms_agree_with_a_direct_count():
     weight[1, 0, :6] = [0.0, 2.0, 5.0, 2.0, np.nan, 0.0]
     _, w, n, kept = paged_ref.evict(pool, weight, np.array([[1]]), np.array([6]), np.array([[0]]), 4, 1, 1)
     assert n.tolist() == [4] and kept[0, 0].tolist() == [0, 1, 2, 5] and w[0, 0, :4].tolist() == [0.0, 2.0, 5.0, 0.0]
+
+
+def test_numbers_past_32_bits_are_refused(lib):
+    from decoder_only_transformer_gpt_gb300 import binding
+    x = torch.zeros(1)
+    assert _store(lib, H=2 ** 31 - 2, T=1) == binding.GPT_EINVAL
+    for n in (2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5):
+        for k in ("window", "sinks"):
+            a = dict(window=8, sinks=0)
+            a[k] = n
+            with pytest.raises(ValueError, match=k):
+                binding.attention_window(x, x, 4, 4, **a)
+            with pytest.raises(ValueError, match=k):
+                binding.attention_window_bwd(x, x, x, x, x, 4, 4, **a)
+            with pytest.raises(ValueError, match=k):
+                binding.paged_attention(x, x, x, x, x, 4, **a)
+        for k in ("budget", "sinks", "recent"):
+            a = dict(budget=8, sinks=0, recent=0)
+            a[k] = n
+            with pytest.raises(ValueError, match=k):
+                binding.paged_evict(x, x, x, x, x, x, x, **a)
