@@ -16,14 +16,23 @@
 // Four derivative warps per half (one thread per key) turn it into P^T = 2^(S^T log2(e)/sqrt(D) - lse2[q]) and
 // dS^T = P^T (dP^T - Dsum[q]), rounded to bf16 for the products below (the type the tensor core multiplies: 2^-8
 // of each term) while the tensor core and the other four work on the other half (with one set of four warps
-// for both halves a step took 1.8 us: each scheduler had one warp, whose waits nothing covered); a warp writes plain zeros for a half of which its
-// 32 keys are not seen. dS^T also goes to shared memory (the MN-major A operand of dQ). Then
+// for both halves a step took 1.8 us, now 1.5: each scheduler had one warp, whose waits nothing covered); a warp writes
+// plain zeros for a half of which its 32 keys are not seen. dS^T also goes to shared memory (the MN-major A operand of dQ). Then
 //   dU_j += P^T_g dY_{i,g}     A from tensor memory, B = dY rows read MN-major    columns [256, 256 + D)
 //   dK_j += dS^T_g Q_{i,g}     A from tensor memory, B = Q rows read MN-major     columns [320, 320 + D)
 //   dQ_i  = dS_i K_j           after both halves: A = dS (shared memory), B = K_j  columns [384, 384 + D)
 // Four output warps add each dQ_i tile into an fp32 [B][T][H D] buffer with TMA reduce-adds (the order of a query
 // tile's few additions varies, below a bf16 step of the result) and, at the end of an item, store dK_j / sqrt(D)
-// and dU_j by TMA. A last kernel rounds dQ to bf16.
+// and dU_j by TMA. Rows of -lse2 and -Dsum are laid out by a first kernel; a last one rounds dQ to bf16 and sums segments.
+//
+// Bound by shared memory: a step (128 keys x 128 queries) moves about 270 KB through it (operand reads of five products,
+// the dS tile written and read, copies in, dQ out), 2,100 of its 2,850 cycles at 128 bytes each; the derivative's chain
+// on one half takes about 1,270. A deeper ring of query tiles, or the scores read 16 queries ahead, changed nothing.
+// Measured (with the forward, calls back to back): 8,192 tokens, 16 heads on 4, D 64, W 1024: 182 us, 620 TFLOP/s; with
+// 12 heads, 8 x 1,000 tokens, W 250: 84 us.
+//
+// Error of dqkv against 64 bits, relative to its norm: 2.3e-3 to 2.7e-3 on normal inputs, where rounding the result
+// alone is 1.7e-3; P and dS rounded to bf16 bring 2.3e-3, the rest is Dsum from the bf16 rows of y.
 // Warps (448 threads, one persistent CTA per SM): 0 producer; 1 TMEM allocator and MMA issuer; 2-5 and 6-9 softmax
 // derivative of half 0 and 1 (thread = key row); 10-13 output.
 #include "attn_window.cuh"
@@ -400,9 +409,8 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       issue_scores(1, qs);
       if (steps == 1) tc_commit_warp(&bars->kvt_free);   // the item's last reads of K_j, U_j in TMEM
     }
-    // A wait costs about 90 cycles even where the phase is complete, and the issue of 40 products a step (30 to 44 cycles
-    // each) leaves this warp no time for four of them: each barrier is tested ahead of a run of products, whose issue
-    // hides the answer's latency, and waited for only where the answer was no.
+    // A wait costs about 90 cycles even where the phase is complete: each barrier is tested ahead of a run of products,
+    // whose issue hides the answer's latency, and waited for only where the answer was no.
     auto settled = [&](bool early, uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, early) || mbar_wait_warp(bar, parity, abort_flag, err);
     };
@@ -678,8 +686,7 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
 
 // What the derivative reads of every query row, in its order: per (b, h), tile of 128 rows (the last one filled up with
 // zeros) and pair of rows {-lse2, -lse2, -Dsum, -Dsum}, with Dsum[t] = sum_d dY[t,d] Y[t,d], so that a tile's kilobyte is
-// one bulk copy (read by the derivative's producer with plain loads they were its longest wait: 0.85 us a step without
-// any product). One warp per row, D / 8 lanes per head with 16-byte loads, so each load instruction of the warp reads
+// one bulk copy, which waits for nothing else (the producer's plain loads of them waited with every step). One warp per row, D / 8 lanes per head with 16-byte loads, so each load instruction of the warp reads
 // 512 contiguous bytes of the row. It also clears the row of the dQ accumulator (a memset of its own took a launch and
 // as long again).
 template <int D>
