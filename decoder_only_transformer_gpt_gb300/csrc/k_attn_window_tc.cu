@@ -62,6 +62,7 @@ constexpr int NSB = 3;                  // score buffers
 constexpr uint32_t kColO = 128 * NSB;   // O_g at kColO + 64 g
 constexpr int SR = 4;                   // items announced ahead by the producer
 constexpr int CH = 64;                  // keys that a softmax warp handles at a time
+constexpr int kFewSinks = 16;           // sinks that are taken as one step of 16 keys
 constexpr int kConsumers = 10;          // warps that read each announced item: 2 MMA issuers + 8 softmax
 
 template <int D>
@@ -146,6 +147,17 @@ __device__ __forceinline__ void issue_pv_half(uint32_t tO, uint32_t tP, uint64_t
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}\n"
       :: "r"(tO), "r"(tP + 32 * h), "l"(desc_add(u_desc, 64 * h * Cfg::ROWB)), "r"(idesc), "r"(accumulate ? 1u : 0u),
          "n"(16 * Cfg::ROWB / 16) : "memory");
+}
+
+// The same for the first 16 keys of a tile alone (those after the sinks of a sink tile have no probability).
+template <int D>
+__device__ __forceinline__ void issue_pv_sinks(uint32_t tO, uint32_t tP, uint64_t u_desc, bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(BQ, D, true);
+  asm volatile(
+      "{\n\t.reg .pred e, f;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 f, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t}\n"
+      :: "r"(tO), "r"(tP), "l"(u_desc), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
 }
 
 // What a launch computes, and how its items are cut.
@@ -456,8 +468,12 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
               if (!mbar_wait_warp(&bars->p_full[b], (bits >> b) & 1u, abort_flag, err)) { ok = false; break; }
               bits ^= 1u << b;
               tc_fence_after();
-              issue_pv_half<D>(tOg, tP, du, 0, more);
-              issue_pv_half<D>(tOg, tP, du, 1, true);
+              if (i < x.a && w.sinks <= kFewSinks) {
+                issue_pv_sinks<D>(tOg, tP, du, more);
+              } else {
+                issue_pv_half<D>(tOg, tP, du, 0, more);
+                issue_pv_half<D>(tOg, tP, du, 1, true);
+              }
               tc_commit_warp(&bars->pv_done[b]);
               b = b == NSB - 1 ? 0 : b + 1;
             }
@@ -562,6 +578,32 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
         // columns, whose scores have been read. One copy of each loop: the warps' code has to fit the
         // instruction cache.
         int c0 = 0;
+        if (i < x.a && w.sinks <= kFewSinks) {
+          // A sink tile before the window with few sinks: its first 16 keys alone. Every row sees key 0, whose score is
+          // the reference (the tile is the item's first).
+          uint32_t v[16], pk[8];
+          tmem_ld_32x32b_x16(tS, v);
+          tmem_ld_wait();
+          const float m0 = __uint_as_float(v[0]) * scale_log2;
+          const float2 nm2 = make_float2(-m0, -m0);
+          float2 ls = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int q = 0; q < 16; q += 2) {
+            const float2 e = fma2_rn(make_float2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])), sc2, nm2);
+            const float2 pr = make_float2(q < w.sinks ? ex2_approx(e.x) : 0.0f, q + 1 < w.sinks ? ex2_approx(e.y) : 0.0f);
+            ls = add2_rn(ls, pr);
+            pk[q / 2] = pack_bf16x2(pr.x, pr.y);
+          }
+          const float lt = ls.x + ls.y;
+          if (!__any_sync(0xffffffffu, !(lt <= kSumLimit))) {
+            mr = m0;
+            l = lt;
+            ready = true;
+            c0 = BKV / CH;
+            tmem_st_32x32b_x8(tS, pk);
+            if (pend && !write_out()) { ok = false; break; }
+          }
+        } else
         // Every row sees the whole tile and has its reference: 32 keys at a time, the next 32 scores on their way from
         // tensor memory while these are worked on.
         if (ready && kb + BKV - 1 <= tw && (kb > tw + 31 - w.window || kb + BKV <= w.sinks)) {
@@ -588,6 +630,48 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
             tmem_loaded(vb);
             if (c == 0) tmem_ld_32x32b_x32(tS + 64, va);
             stream(vb, 16);
+            const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
+            const float lt = l2.x + l2.y;
+            const bool over = __any_sync(0xffffffffu, !(lt <= kSumLimit));
+            if (c == 0) tmem_loaded(va);
+            if (over) break;
+            l += lt;
+            tmem_st_32x32b_x32(tS + 32 * c, pk);
+            c0 = c + 1;
+          }
+        } else if (ready) {
+          // the same where a border crosses the tile: 0 for the keys that a row does not see, and 32 keys of which the
+          // warp's rows see nothing are left out
+          const float2 nm2 = make_float2(-mr, -mr);
+          uint32_t va[32], vb[32], pk[CH / 2];
+          float2 ls[4];
+          auto stream = [&](const uint32_t (&v)[32], int at, int k0) {
+            if (k0 > tw + 31 || (k0 + 31 <= tw - w.window && k0 >= w.sinks)) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[at + i] = 0u;
+              return;
+            }
+            const uint32_t seen = seen_bits(k0);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 e = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
+              const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+              const float2 pr = make_float2((seen >> i) & 1u ? p0 : 0.0f, (seen >> (i + 1)) & 1u ? p1 : 0.0f);
+              ls[(i >> 1) & 3] = add2_rn(ls[(i >> 1) & 3], pr);
+              pk[at + i / 2] = pack_bf16x2(pr.x, pr.y);
+            }
+          };
+          tmem_ld_32x32b_x32(tS, va);
+          tmem_loaded(va);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld_32x32b_x32(tS + 64 * c + 32, vb);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ls[q] = make_float2(0.0f, 0.0f);
+            stream(va, 0, kb + CH * c);
+            tmem_loaded(vb);
+            if (c == 0) tmem_ld_32x32b_x32(tS + 64, va);
+            stream(vb, 16, kb + CH * c + 32);
             const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
             const float lt = l2.x + l2.y;
             const bool over = __any_sync(0xffffffffu, !(lt <= kSumLimit));
