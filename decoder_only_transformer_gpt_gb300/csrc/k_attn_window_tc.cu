@@ -30,9 +30,11 @@
 // two, a 64-key half each, cost more in waits than their earlier start gave) and issues O_g += P(k) U_j with the A
 // operand in tensor memory.
 //
-// Softmax: per row one running reference m and sum. The reference starts as the score of key 0 where every row of
-// the tile sees it, else as the exact maximum of the first half tile in which the row sees a key; it is raised only
-// when a half tile's sum passes 2^16 and the maximum grew by more than 2^8. Sums are fp32; P is rounded to bf16 for
+// An item's key tiles come from the diagonal down, the sinks last, so that every row sees a key of its first tile.
+//
+// Softmax: per row one running reference m and sum. The reference starts as the score of the warp's first diagonal key
+// where all its rows see that (W >= 32), else as the exact maximum of the first half tile in which the row sees a key;
+// it is raised only when a half tile's sum passes 2^16 and the maximum grew by more than 2^8. Sums are fp32; P is rounded to bf16 for
 // the second product (the type the tensor core multiplies), which costs at most 2^-8 of sum a |u|.
 //
 // Taken back, at the 12,001 tokens above as they were then: tiles of 64 keys in six score buffers (157 us against 151),
@@ -177,21 +179,21 @@ __device__ __forceinline__ int item_of(const WinShape& w, int r) {
   return i < w.n_items ? static_cast<int>(i) : -1;
 }
 
-// One item: query tiles qt0 (group 0) and, if `two`, qt0 + 1 (group 1), and the list of key tiles they share:
-// entries [0, a) are the sink tiles before the window, entries a.. the tiles from j0 (the window start of qt0's
-// first row) to the last diagonal. Group 0 takes entries [0, n0); group 1 takes all but entry a where `skip`
-// (its own window starts one tile later and that tile holds no sink).
+// One item: query tiles qt0 (group 0) and, if `two`, qt0 + 1 (group 1), and the list of key tiles they share: entries
+// [0, m) are the tiles of the window from the last diagonal (tile `top`) down to the window start of qt0's first row,
+// entries [m, m + a) the sink tiles before those. Group 0 takes all but the other's diagonal; group 1 takes all but
+// entry m - 1 where `skip` (its own window starts one tile later and that tile holds no sink).
 struct Item {
-  int b, h, qt0, a, j0, n0, n;
+  int b, h, qt0, a, top, m, n;
   int two, skip;
-  __device__ __forceinline__ int tile(int i) const { return i < a ? i : j0 + (i - a); }
-  __device__ __forceinline__ bool has1(int i) const { return two && !(skip && i == a); }
-  __device__ __forceinline__ int first1() const { return skip && a == 0 ? 1 : 0; }
-  // group 1's entries before i
-  __device__ __forceinline__ int count1(int i) const { return two ? i - (skip && i > a ? 1 : 0) : 0; }
+  __device__ __forceinline__ int tile(int i) const { return i < m ? top - i : a - 1 - (i - m); }
+  __device__ __forceinline__ int first0() const { return two; }
+  __device__ __forceinline__ bool has1(int i) const { return two && !(skip && i == m - 1); }
   // position of (entry i, group g) in the item's score sequence, and the sequence's length
-  __device__ __forceinline__ int number(int i, int g) const { return (g ? min(i + 1, n0) : i) + count1(i); }
-  __device__ __forceinline__ int total() const { return n0 + count1(n); }
+  __device__ __forceinline__ int number(int i, int g) const {
+    return max(i + g - two, 0) + (two ? i - (skip && i >= m ? 1 : 0) : 0);
+  }
+  __device__ __forceinline__ int total() const { return number(n, 0); }
 };
 
 __device__ __forceinline__ Item decode_item(const WinShape& w, int item) {
@@ -203,12 +205,13 @@ __device__ __forceinline__ Item decode_item(const WinShape& w, int item) {
   x.qt0 = w.per_item * p;
   x.two = w.per_item == 2 && x.qt0 + 1 < w.n_qtiles;
   const int first = x.qt0 * BQ - w.window + 1;       // window start of the first row (window < 2^30: no overflow)
-  x.j0 = first > 0 ? first / BKV : 0;
-  x.a = min(w.sink_tiles, x.j0);
+  const int j0 = first > 0 ? first / BKV : 0;
+  x.a = min(w.sink_tiles, j0);
   const int j1 = first + BQ > 0 ? (first + BQ) / BKV : 0;
-  x.skip = x.two && j1 > x.j0 && x.j0 >= w.sink_tiles;
-  x.n0 = x.a + (x.qt0 - x.j0) + 1;
-  x.n = x.n0 + (x.two ? 1 : 0);
+  x.skip = x.two && j1 > j0 && j0 >= w.sink_tiles;
+  x.top = x.qt0 + x.two;
+  x.m = x.top - j0 + 1;
+  x.n = x.m + x.a;
   return x;
 }
 
@@ -223,8 +226,8 @@ __device__ __forceinline__ bool next_item(AttnBars* bars, int r, Item& x, volati
   x.h = p.y;
   x.qt0 = p.z;
   x.a = p.w;
-  x.j0 = q.x;
-  x.n0 = q.y;
+  x.top = q.x;
+  x.m = q.y;
   x.n = q.z;
   x.two = q.w & 1;
   x.skip = q.w >> 1;
@@ -408,7 +411,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
         if (item >= 0) x = decode_item(w, item);
         int4* v = reinterpret_cast<int4*>(bars->item[slot]);
         v[0] = make_int4(x.b, x.h, x.qt0, x.a);
-        v[1] = make_int4(x.j0, x.n0, x.n, x.two | (x.skip << 1));
+        v[1] = make_int4(x.top, x.m, x.n, x.two | (x.skip << 1));
         mbar_arrive(&bars->item_full[slot]);
         if (item < 0) break;
         const int kh = x.h / w.G;                    // key head
@@ -456,19 +459,18 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       bool ok = true;
       if (pv_warp) {
         for (int r = 0; ok && next_item(bars, r, x, abort_flag, err, lane); ++r) {
-          const int first1 = x.first1();
           for (int i = 0; i < x.n && ok; ++i, ++pos) {
             const uint32_t st = pos % NS;
             const uint64_t du = desc_add(du0, st * Cfg::TILE);
             const int g_end = x.has1(i) ? 2 : 1;
 #pragma unroll 1
-            for (int g = i < x.n0 ? 0 : 1; g < g_end; ++g) {
+            for (int g = i >= x.first0() ? 0 : 1; g < g_end; ++g) {
               const uint32_t tOg = tmem_base + kColO + 64 * g, tP = tmem_base + 128 * b;
-              const bool more = i > (g ? first1 : 0);
+              const bool more = i > (g ? 0 : x.first0());
               if (!mbar_wait_warp(&bars->p_full[b], (bits >> b) & 1u, abort_flag, err)) { ok = false; break; }
               bits ^= 1u << b;
               tc_fence_after();
-              if (i < x.a && w.sinks <= kFewSinks) {
+              if (i >= x.m && w.sinks <= kFewSinks) {
                 issue_pv_sinks<D>(tOg, tP, du, more);
               } else {
                 issue_pv_half<D>(tOg, tP, du, 0, more);
@@ -491,7 +493,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
             const uint64_t dk = desc_add(dk0, st * Cfg::TILE);
             const int g_end = x.has1(i) ? 2 : 1;
 #pragma unroll 1
-            for (int g = i < x.n0 ? 0 : 1; g < g_end; ++g) {
+            for (int g = i >= x.first0() ? 0 : 1; g < g_end; ++g) {
               if (n == NSB) {                        // the P U that read this buffer has completed
                 if (!mbar_wait_warp(&bars->pv_done[b], (bits >> b) & 1u, abort_flag, err)) { ok = false; break; }
                 bits ^= 1u << b;
@@ -546,7 +548,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       const int qt = x.qt0 + g;
       const int t = qt * BQ + r_row;                  // query position
       const int tw = qt * BQ + wrow;                  // the warp's first query
-      const int i0 = g == 0 ? 0 : x.first1(), i1 = g == 0 ? x.n0 : x.n;
+      const int i0 = g == 0 ? x.first0() : 0;
       float mr = -INFINITY;                           // running (lazily raised) reference, log2 units
       float l = 0.0f;                                 // running sum of 2^(s - mr)
       bool ready = false;                             // every row of the warp has a reference
@@ -554,7 +556,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
       uint32_t b = k % NSB;
       int kb = x.tile(i0) * BKV;                      // the tile's first key
       bool early = false;                             // the tile's scores were there when the last one was handed over
-      for (int i = i0; i < i1;) {
+      for (int i = i0; i < x.n;) {
         const bool first = i == i0;
         if (!__all_sync(0xffffffffu, early) && !mbar_wait_warp(&bars->s_full[g][b], (bits >> b) & 1u, abort_flag, err)) {
           ok = false;
@@ -578,14 +580,12 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
         // columns, whose scores have been read. One copy of each loop: the warps' code has to fit the
         // instruction cache.
         int c0 = 0;
-        if (i < x.a && w.sinks <= kFewSinks) {
-          // A sink tile before the window with few sinks: its first 16 keys alone. Every row sees key 0, whose score is
-          // the reference (the tile is the item's first).
+        if (ready && i >= x.m && w.sinks <= kFewSinks) {
+          // a sink tile before the window with few sinks: its first 16 keys alone
+          const float2 nm2 = make_float2(-mr, -mr);
           uint32_t v[16], pk[8];
           tmem_ld_32x32b_x16(tS, v);
-          tmem_ld_wait();
-          const float m0 = __uint_as_float(v[0]) * scale_log2;
-          const float2 nm2 = make_float2(-m0, -m0);
+          tmem_loaded(v);
           float2 ls = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int q = 0; q < 16; q += 2) {
@@ -596,17 +596,13 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
           }
           const float lt = ls.x + ls.y;
           if (!__any_sync(0xffffffffu, !(lt <= kSumLimit))) {
-            mr = m0;
-            l = lt;
-            ready = true;
+            l += lt;
             c0 = BKV / CH;
             tmem_st_32x32b_x8(tS, pk);
-            if (pend && !write_out()) { ok = false; break; }
           }
-        } else
-        // Every row sees the whole tile and has its reference: 32 keys at a time, the next 32 scores on their way from
-        // tensor memory while these are worked on.
-        if (ready && kb + BKV - 1 <= tw && (kb > tw + 31 - w.window || kb + BKV <= w.sinks)) {
+        } else if (ready && kb + BKV - 1 <= tw && (kb > tw + 31 - w.window || kb + BKV <= w.sinks)) {
+          // every row sees the whole tile and has its reference: 32 keys at a time, the next 32 scores on their way from
+          // tensor memory while these are worked on
           const float2 nm2 = make_float2(-mr, -mr);
           uint32_t va[32], vb[32], pk[CH / 2];
           float2 ls[4];
@@ -639,13 +635,13 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
             tmem_st_32x32b_x32(tS + 32 * c, pk);
             c0 = c + 1;
           }
-        } else if (ready) {
+        } else if (ready || (first && w.window >= 32)) {
           // the same where a border crosses the tile: 0 for the keys that a row does not see, and 32 keys of which the
-          // warp's rows see nothing are left out
-          const float2 nm2 = make_float2(-mr, -mr);
+          // warp's rows see nothing are left out. In the first tile, the diagonal, all rows of the warp see the key of
+          // the first of them: its score is their reference.
           uint32_t va[32], vb[32], pk[CH / 2];
           float2 ls[4];
-          auto stream = [&](const uint32_t (&v)[32], int at, int k0) {
+          auto stream = [&](const uint32_t (&v)[32], int at, int k0, float2 nm2) {
             if (k0 > tw + 31 || (k0 + 31 <= tw - w.window && k0 >= w.sinks)) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) pk[at + i] = 0u;
@@ -662,16 +658,24 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
             }
           };
           tmem_ld_32x32b_x32(tS, va);
+          if (!ready) {
+            uint32_t own[1];
+            tmem_ld_32x32b_x1(tS + wrow, own);
+            tmem_loaded(own);
+            mr = __uint_as_float(own[0]) * scale_log2;
+            ready = true;
+          }
+          const float2 nm2 = make_float2(-mr, -mr);
           tmem_loaded(va);
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             tmem_ld_32x32b_x32(tS + 64 * c + 32, vb);
 #pragma unroll
             for (int q = 0; q < 4; ++q) ls[q] = make_float2(0.0f, 0.0f);
-            stream(va, 0, kb + CH * c);
+            stream(va, 0, kb + CH * c, nm2);
             tmem_loaded(vb);
             if (c == 0) tmem_ld_32x32b_x32(tS + 64, va);
-            stream(vb, 16, kb + CH * c + 32);
+            stream(vb, 16, kb + CH * c + 32, nm2);
             const float2 l2 = add2_rn(add2_rn(ls[0], ls[1]), add2_rn(ls[2], ls[3]));
             const float lt = l2.x + l2.y;
             const bool over = __any_sync(0xffffffffu, !(lt <= kSumLimit));
@@ -692,10 +696,9 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) pk[i] = 0u;
           } else {
-            const bool at_key0 = first && k0 == 0 && (w.sinks > 0 || tw + 31 < w.window);   // all rows see key 0
             float lt;                                 // the row's sum over the chunk
 #pragma unroll 1
-            for (bool raise = !ready && !at_key0;; raise = true) {
+            for (bool raise = !ready;; raise = true) {
               if (raise) {
                 const RowRef rr = raise_reference<D>(bars, tS + CH * c, tS, tO, c * (CH / 32), mr, l, scale_log2,
                                                      seen_bits(k0), seen_bits(k0 + 32), first, last, abort_flag, err);
@@ -707,10 +710,6 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
               }
               uint32_t v[CH];
               load_chunk(tS + CH * c, v);
-              if (at_key0 && !raise) {
-                mr = __uint_as_float(v[0]) * scale_log2;
-                ready = true;
-              }
               // A score's whole way to a bf16 probability, 2^(s scale - mr), and into the sum, in one run of
               // independent steps, two keys per f32x2 instruction (with the mask as a branch in the middle the
               // exponentials, sums and roundings ran one after the other: 179 against 156 us for 12,001 tokens).
@@ -738,24 +737,23 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
             if (!ok) break;
             l += lt;
           }
-          // the previous item's output leaves the accumulator before this item's first P U
-          if (c == BKV / CH - 1 && first && pend && !write_out()) { ok = false; break; }
           tmem_st_32x32b_x32(tS + CH / 2 * c, pk);
         }
-        if (!ok) break;
+        // the previous item's output leaves the accumulator before this item's first P U
+        if (!ok || (first && pend && !write_out())) { ok = false; break; }
         // the group's next entry: its number, buffer and first key, and whether its scores are there (a wait costs 90
         // cycles even then; the answer to the test comes while the probabilities are stored)
         uint64_t* const full = &bars->p_full[b];
         last = k;
         do {
-          const uint32_t step = (g == 0 ? 1 : (x.has1(i) ? 1 : 0)) + (g == 0 ? (x.has1(i) ? 1 : 0) : (i + 1 < x.n0 ? 1 : 0));
+          const uint32_t step = x.has1(i) ? 2 : 1;
           ++i;
           k += step;
           b += step;
           b = b >= NSB ? b - NSB : b;
-          kb = i == x.a ? x.j0 * BKV : kb + BKV;
-        } while (g == 1 && i < i1 && !x.has1(i));
-        early = i < i1 && mbar_test(&bars->s_full[g][b], (bits >> b) & 1u);
+          kb = (i == x.m ? x.a * BKV : kb) - BKV;
+        } while (g == 1 && i < x.n && !x.has1(i));
+        early = i < x.n && mbar_test(&bars->s_full[g][b], (bits >> b) & 1u);
         tmem_st_wait();
         tc_fence_before();                      // our TMEM reads of S and writes of P precede the next MMA
         __syncwarp();
