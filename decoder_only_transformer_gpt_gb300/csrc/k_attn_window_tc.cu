@@ -17,7 +17,7 @@
 // 12 heads, W 256: 38 us, 2.7 TB/s of rows.
 //
 // Pipeline (one persistent CTA per SM, 352 threads): as in the full causal kernel, a work item is one (b, h) and a
-// PAIR of consecutive query tiles that share one stream of 128-key K/U tiles through a four-stage TMA ring; two
+// PAIR of consecutive query tiles that share one stream of 128-key tiles, K and U through a four-stage TMA ring each; two
 // softmax groups of four warps (thread = query row = TMEM lane) own one query tile each and run out of phase.
 // Where the pairs would leave SMs without work an item is one query tile. Items are dealt statically, the long
 // ones first, forwards and backwards in turn (item r of CTA c: r grid + c, or r grid + grid - 1 - c for odd r):
@@ -59,7 +59,7 @@ constexpr int TMEM_COLS = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;    // rescale O only when the max grows by more than this
 constexpr float kSumLimit = 65536.0f;   // recompute a tile against its exact max past this sum
-constexpr int NS = 4;                   // K/U ring depth; the MMA warp's look-ahead needs at least 4
+constexpr int NS = 4;                   // ring depth of K and of U
 constexpr int NSB = 3;                  // score buffers
 constexpr uint32_t kColO = 128 * NSB;   // O_g at kColO + 64 g
 constexpr int SR = 4;                   // items announced ahead by the producer
@@ -86,8 +86,10 @@ struct AttnCfg {
 
 struct __align__(16) AttnBars {
   uint64_t q_empty[2];      // every S of the item that used Q buffer k has been computed
-  uint64_t kv_full[NS];     // ring stage holds K_j, U_j (and, for an item's first tile, its query tiles)
-  uint64_t kv_empty[NS];
+  uint64_t k_full[NS];      // ring stage holds K_j (and, for an item's first tile, its query tiles)
+  uint64_t k_empty[NS];     // every S of that tile has been computed
+  uint64_t u_full[NS];      // ring stage holds U_j
+  uint64_t u_empty[NS];     // every P U of that tile has been computed
   uint64_t s_full[2][NSB];  // score buffer b holds a new score tile of group g (that group's uses of b, in order)
   uint64_t p_full[NSB];     // score buffer b holds that tile's probabilities (4 warps)
   uint64_t pv_done[NSB];    // the P U that read buffer b has completed (the buffer may take new scores)
@@ -367,8 +369,10 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
     mbar_init(&bars->q_empty[0], 1);
     mbar_init(&bars->q_empty[1], 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&bars->kv_full[i], 1);
-      mbar_init(&bars->kv_empty[i], 1);
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->u_full[i], 1);
+      mbar_init(&bars->u_empty[i], 1);
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&bars->s_full[0][i], 1);
@@ -398,10 +402,19 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
   pdl_trigger();
 
   if (warp == 0) {
-    // ------------------------------------------------ TMA producer
+    // ------------------------------------------------ producer of items and copies
     if (lane == 0) {
-      uint32_t issued = 0, last_par = 0;
-      uint32_t kv_it = 0;                            // K/U tiles loaded so far (ring position)
+      uint32_t pos = 0, u_pos = 0;                   // K and U tiles loaded so far (ring positions)
+      int ux = 0, u_row = 0, ub = 0;                 // where the next U lies
+      // U one tile behind K: its stage is released later, and K's copy does not wait for that
+      auto load_u = [&]() -> bool {
+        const int s = u_pos % NS;
+        if (!mbar_wait(&bars->u_empty[s], ((u_pos / NS) & 1u) ^ 1u, abort_flag, err)) return false;
+        mbar_arrive_expect_tx(&bars->u_full[s], Cfg::TILE);
+        tma_load_3d(sU + s * Cfg::TILE, &tm, &bars->u_full[s], ux, u_row, ub);
+        ++u_pos;
+        return true;
+      };
       bool ok = true;
       for (int r = 0; ok; ++r) {
         const int item = item_of(w, r);
@@ -417,34 +430,36 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
         const int kh = x.h / w.G;                    // key head
         const int qb = r & 1;                        // Q buffer of this item; its previous user was item r - 2
         if (r >= 2 && !mbar_wait(&bars->q_empty[qb], static_cast<uint32_t>((r >> 1) - 1) & 1u, abort_flag, err)) break;
-        for (int i = 0; i < x.n; ++i, ++kv_it) {
-          const int s = kv_it % NS;
-          const uint32_t use_par = (kv_it / NS) & 1u;
-          if (!mbar_wait(&bars->kv_empty[s], use_par ^ 1u, abort_flag, err)) { ok = false; break; }
-          // the item's query tiles complete on the barrier of its first K/U tile
+        for (int i = 0; i < x.n; ++i) {
+          const int s = pos % NS;
+          if (!mbar_wait(&bars->k_empty[s], ((pos / NS) & 1u) ^ 1u, abort_flag, err)) { ok = false; break; }
+          // the item's query tiles complete on the barrier of its first K tile
           const int nq = (i == 0) ? (x.two ? 2 : 1) : 0;
           const int row = x.tile(i) * BKV;
-          mbar_arrive_expect_tx(&bars->kv_full[s], (2 + nq) * Cfg::TILE);
-          if (nq > 0) tma_load_3d(sQ + (2 * qb) * Cfg::TILE, &tm, &bars->kv_full[s], x.h * D, x.qt0 * BQ, x.b);
-          if (nq > 1) tma_load_3d(sQ + (2 * qb + 1) * Cfg::TILE, &tm, &bars->kv_full[s], x.h * D, (x.qt0 + 1) * BQ, x.b);
-          tma_load_3d(sK + s * Cfg::TILE, &tm, &bars->kv_full[s], kcol + kh * D, row, x.b);
-          tma_load_3d(sU + s * Cfg::TILE, &tm, &bars->kv_full[s], ucol + kh * D, row, x.b);
-          issued |= 1u << s;
-          last_par = (last_par & ~(1u << s)) | (use_par << s);
+          mbar_arrive_expect_tx(&bars->k_full[s], (1 + nq) * Cfg::TILE);
+          if (nq > 0) tma_load_3d(sQ + (2 * qb) * Cfg::TILE, &tm, &bars->k_full[s], x.h * D, x.qt0 * BQ, x.b);
+          if (nq > 1) tma_load_3d(sQ + (2 * qb + 1) * Cfg::TILE, &tm, &bars->k_full[s], x.h * D, (x.qt0 + 1) * BQ, x.b);
+          tma_load_3d(sK + s * Cfg::TILE, &tm, &bars->k_full[s], kcol + kh * D, row, x.b);
+          ++pos;
+          if (pos > 1 && !load_u()) { ok = false; break; }
+          ux = ucol + kh * D;
+          u_row = row;
+          ub = x.b;
         }
       }
-      // never leave with copies in flight into this CTA's shared memory
-      for (int s = 0; s < NS; ++s)
-        if (issued & (1u << s)) mbar_wait_drain(&bars->kv_full[s], (last_par >> s) & 1u);
+      if (ok && u_pos < pos) load_u();
+      // never leave with copies in flight into this CTA's shared memory: the last ones into each stage
+      for (uint32_t q = pos > NS ? pos - NS : 0; q < pos; ++q) mbar_wait_drain(&bars->k_full[q % NS], (q / NS) & 1u);
+      for (uint32_t q = u_pos > NS ? u_pos - NS : 0; q < u_pos; ++q) mbar_wait_drain(&bars->u_full[q % NS], (q / NS) & 1u);
     }
   } else if (warp == 1 || warp == 10) {
     // ------------------------------------------------ MMA issuers (whole warp; one elected lane issues)
     // Two warps on different sub-partitions share the issue work, each walking the same
     // sequence of score numbers: warp 1 waits for P(k) and issues O_g += P(k) U_j; warp 10
     // issues S(k) = Q K_j^T into buffer k % 3 once the P U of number k - 3 (which read that
-    // buffer) has completed. A ring stage is released by the last P U reading its U (its K has been
-    // read by then: the probabilities were made of those scores); S(k) lies at most three ring
-    // positions past the oldest unreleased stage, so four stages never wait on each other.
+    // buffer) has completed. K's ring stage is released by the tile's last S, U's by its last P U,
+    // which comes up to two tiles later: with one stage for both, K's loads had that much less time
+    // (64 x 1,024 tokens, 12 heads, W 256: 118 us against 109).
     {
       const bool pv_warp = warp == 1;
       // base descriptors: Q and K K-major (8-row groups ROWB*8 apart), U MN-major (K-direction
@@ -461,6 +476,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
         for (int r = 0; ok && next_item(bars, r, x, abort_flag, err, lane); ++r) {
           for (int i = 0; i < x.n && ok; ++i, ++pos) {
             const uint32_t st = pos % NS;
+            if (!mbar_wait_warp(&bars->u_full[st], (pos / NS) & 1u, abort_flag, err)) { ok = false; break; }
             const uint64_t du = desc_add(du0, st * Cfg::TILE);
             const int g_end = x.has1(i) ? 2 : 1;
 #pragma unroll 1
@@ -479,8 +495,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
               tc_commit_warp(&bars->pv_done[b]);
               b = b == NSB - 1 ? 0 : b + 1;
             }
-            // U_j is consumed, and K_j: every P was made of a score
-            if (ok) tc_commit_warp(&bars->kv_empty[st]);
+            if (ok) tc_commit_warp(&bars->u_empty[st]);
           }
         }
       } else {
@@ -489,7 +504,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
           const uint32_t qb = static_cast<uint32_t>(r) & 1u;
           for (int i = 0; i < x.n && ok; ++i, ++pos) {
             const uint32_t st = pos % NS;
-            if (!mbar_wait_warp(&bars->kv_full[st], (pos / NS) & 1u, abort_flag, err)) { ok = false; break; }
+            if (!mbar_wait_warp(&bars->k_full[st], (pos / NS) & 1u, abort_flag, err)) { ok = false; break; }
             const uint64_t dk = desc_add(dk0, st * Cfg::TILE);
             const int g_end = x.has1(i) ? 2 : 1;
 #pragma unroll 1
@@ -504,6 +519,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
               issue_s<D>(tmem_base + 128 * b, desc_add(dq0, (2 * qb + g) * Cfg::TILE), dk, &bars->s_full[g][b]);
               b = b == NSB - 1 ? 0 : b + 1;
             }
+            if (ok) tc_commit_warp(&bars->k_empty[st]);
           }
           if (ok) tc_commit_warp(&bars->q_empty[qb]);   // every S of the item has read its Q
         }
