@@ -9,12 +9,12 @@
 // diagonal, and the tiles that hold sinks, so work and traffic grow with T (W + S), not T^2 / 2. The kernel is
 // bound by the softmax warps, not by the tensor core: a 128-key tile takes them about 2,000 cycles, of which the
 // exponentials are 1,024 (one per score on a quarter-rate unit, two warps per scheduler) and the rest waits between
-// dependent instructions and for tensor memory; the tile's two products take 540. So a warp leaves out every 64-key
-// half tile of which its 32 rows see nothing (beyond the diagonal, before the window, after the sinks), masks only
-// the half tiles that a border crosses, and takes tiles that all its rows see whole by the shortest path: 32 keys at
-// a time, the next scores on their way out of tensor memory meanwhile.
-// Measured (calls back to back): 12,001 tokens, 25 heads on 5, D 64, W 1500: 130 us, 830 TFLOP/s; 16 x 1,024 tokens,
-// 12 heads, W 256: 38 us, 2.7 TB/s of rows.
+// dependent instructions and for tensor memory; the tile's two products take 540. So a warp leaves out the 32-key
+// parts of a tile of which its rows see nothing (beyond the diagonal, before the window, after the sinks), masks only
+// tiles that a border crosses, takes few sinks (up to 16) as one step of 16 keys, and works 32 keys at a time with the
+// next scores on their way out of tensor memory meanwhile.
+// Measured (calls back to back): 12,001 tokens, 25 heads on 5, D 64, W 1500: 126 us, 860 TFLOP/s; 16 x 1,024 tokens,
+// 12 heads, W 256: 35 us, 2.9 TB/s of rows.
 //
 // Pipeline (one persistent CTA per SM, 352 threads): as in the full causal kernel, a work item is one (b, h) and a
 // PAIR of consecutive query tiles that share one stream of 128-key tiles, K and U through a four-stage TMA ring each; two
