@@ -541,7 +541,8 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
 }
 
 // The same attention where the rows that can be seen fit the warps of one cluster (UPW units per warp): one launch, no
-// scratch. Warp w of block `rank` takes units (j * 8 + w) * NC + rank, all of whose rows are copied at once;
+// scratch. A block takes 8 UPW consecutive units, and blocks behind the last leave at once (the table's room
+// is the most a sequence can hold, not what it holds); a warp's rows are all copied at once and
 // it holds its scores in registers, so there is one maximum and no rescaling, and the attention weights follow from the
 // registers once the cluster's maxima and sums are known. Each block adds up its warps' outputs in shared memory and
 // pushes them to the block that joins that query row, and its maxima and sums to every block; one cluster barrier.
@@ -563,7 +564,7 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[8][QR];                     // the warps' maxima and sums
   __shared__ float2 s_all[8][QR];                    // the blocks', pushed by each of them
-  __shared__ float s_o[QR][D];                       // pushed outputs: [row / NC * NC + block][D]
+  __shared__ float s_o[QR + 7][D];                   // pushed outputs: [row / NB * NB + block][D]
   auto cluster = cooperative_groups::this_cluster();
   const int NC = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -579,7 +580,7 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
   int page[UPW];                                     // on its way before the length is known: right unless a window cuts
 #pragma unroll
   for (int j = 0; j < UPW; ++j)
-    page[j] = __ldg(trow + min((((j * 8 + warp) * NC + rank) * kUnit + lane) >> c.page_log2, c.max_pages - 1));
+    page[j] = __ldg(trow + min((((rank * UPW + j) * 8 + warp) * kUnit + lane) >> c.page_log2, c.max_pages - 1));
   const int qrow = lane >> 2, qcol = 2 * (lane & 3);
   uint32_t qf[D / 16][4];                            // A operand: the group's queries, zeros behind them
 #pragma unroll
@@ -596,6 +597,8 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
     last = -1;
   }
   const Seen seen = seen_rows(last + 1, w.window, w.sinks);
+  const int NB = (seen.n + 8 * UPW * kUnit - 1) / (8 * UPW * kUnit);   // blocks that hold units
+  if (rank >= NB) return;                            // (whole blocks: barriers wait for the others only)
   uint8_t* ring = smem + warp * Cfg::WARP;
   const uint32_t ring_a = smem_u32(ring);
   const size_t vstep = (static_cast<size_t>(c.Hkv) << c.page_log2) * D;
@@ -603,7 +606,7 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
   uint32_t mask[UPW];
 #pragma unroll
   for (int j = 0; j < UPW; ++j) {
-    const int v = ((j * 8 + warp) * NC + rank) * kUnit + lane, r = seen_row(seen, v);
+    const int v = ((rank * UPW + j) * 8 + warp) * kUnit + lane, r = seen_row(seen, v);
     bool ok = v < seen.n;
     if (ok && r != v) page[j] = __ldg(trow + (r >> c.page_log2));
     const __nv_bfloat16* kp = pool;
@@ -633,7 +636,7 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
   }
   // the newest row into the cache, by the warp whose unit holds it
   const int ntail = (seen.n - 1) / kUnit;            // its unit
-  if (last >= 0 && g0 == 0 && ntail % NC == rank && (ntail / NC) % 8 == warp) {
+  if (g0 == 0 && ntail / (8 * UPW) == rank && ntail % 8 == warp) {
     const int pg = __ldg(trow + (last >> c.page_log2));
     if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages) && lane < 2 * U) {
       const int which = lane / U, u = lane % U;
@@ -731,31 +734,30 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
       lt += s_ml[k][r].y * f;
       acc += reinterpret_cast<const float*>(smem + k * Cfg::WARP)[r * D + d] * f;
     }
-    cluster.map_shared_rank(&s_o[0][0], r % NC)[(r / NC * NC + rank) * D + d] = acc;
-    if (d < NC) cluster.map_shared_rank(&s_all[0][0], d)[rank * QR + r] = make_float2(mx, lt);
+    cluster.map_shared_rank(&s_o[0][0], r % NB)[(r / NB * NB + rank) * D + d] = acc;
+    if (d < NB) cluster.map_shared_rank(&s_all[0][0], d)[rank * QR + r] = make_float2(mx, lt);
   }
   cluster.sync();
   auto joined = [&](int r, float* sum) -> float {    // a row's maximum and sum over all blocks
     float mx = -INFINITY;
-    for (int k = 0; k < NC; ++k) mx = fmaxf(mx, s_all[k][r].x);
+    for (int k = 0; k < NB; ++k) mx = fmaxf(mx, s_all[k][r].x);
     const float ref = mx == -INFINITY ? 0.0f : mx;
     float lt = 0.0f;
-    for (int k = 0; k < NC; ++k) lt += s_all[k][r].y * ex2_approx(s_all[k][r].x - ref);
+    for (int k = 0; k < NB; ++k) lt += s_all[k][r].y * ex2_approx(s_all[k][r].x - ref);
     *sum = lt;
     return mx;
   };
-  if (last >= 0)
-    for (int i = tid; i < (gn + NC - 1) / NC * D; i += 256) {
-      const int r = i / D * NC + rank, d = i % D;
-      if (r >= gn) continue;
-      float lt;
-      const float mx = joined(r, &lt), ref = mx == -INFINITY ? 0.0f : mx;
-      float acc = 0.0f;
-      for (int k = 0; k < NC; ++k) acc += s_o[r / NC * NC + k][d] * ex2_approx(s_all[k][r].x - ref);
-      const size_t head = static_cast<size_t>(b) * w.H + kh * w.G + g0 + r;
-      y[head * D + d] = __float2bfloat16(lt == 0.0f ? 0.0f : acc / lt);
-      if (d == 0 && lse2) lse2[head] = mx + log2f(lt);
-    }
+  for (int i = tid; i < (gn + NB - 1) / NB * D; i += 256) {
+    const int r = i / D * NB + rank, d = i % D;
+    if (r >= gn) continue;
+    float lt;
+    const float mx = joined(r, &lt), ref = mx == -INFINITY ? 0.0f : mx;
+    float acc = 0.0f;
+    for (int k = 0; k < NB; ++k) acc += s_o[r / NB * NB + k][d] * ex2_approx(s_all[k][r].x - ref);
+    const size_t head = static_cast<size_t>(b) * w.H + kh * w.G + g0 + r;
+    y[head * D + d] = __float2bfloat16(lt == 0.0f ? 0.0f : acc / lt);
+    if (d == 0 && lse2) lse2[head] = mx + log2f(lt);
+  }
   if (!c.weight) return;
   // the weights: a row's probabilities summed over the group's heads, one row per lane
   float f[2] = {0.0f, 0.0f};
@@ -781,7 +783,7 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (qrow == 2 * j + i) mine = x;
       }
-    const int at = 8 * (qrow >> 1) + qcol + (qrow & 1), v = ((t * 8 + warp) * NC + rank) * kUnit + at, r = seen_row(seen, v);
+    const int at = 8 * (qrow >> 1) + qcol + (qrow & 1), v = ((rank * UPW + t) * 8 + warp) * kUnit + at, r = seen_row(seen, v);
     const int pg = __shfl_sync(0xffffffffu, page[t], at);
     if (v >= seen.n || static_cast<unsigned>(pg) >= static_cast<unsigned>(c.pages)) continue;
     float* dst = c.weight + weight_at(c, pg, kh, r & pmask);
