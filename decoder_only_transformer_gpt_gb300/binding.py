@@ -368,18 +368,21 @@ def lmhead_ce_noalloc(h, wte, targets, nll, err=None, stream=None):
 # tensor; 8 us of the call's host time went to them and the stream object in a first form).
 
 _torch = None
+_cuda_up = False
 
 
 def _cuda(stream):
     """(torch, the current device's index, the stream to launch on as an integer)."""
-    global _torch
-    if _torch is None:
+    global _torch, _cuda_up
+    if not _cuda_up:
         import torch
         _torch = torch
-    if not _torch.cuda.is_initialized():             # no tensor can be on a GPU yet
-        return _torch, 0, 0
-    dev = _torch.cuda.current_device()
-    return _torch, dev, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        _cuda_up = torch.cuda.is_initialized()
+        if not _cuda_up:                             # no tensor can be on a GPU yet
+            return torch, 0, 0
+    c = _torch._C
+    dev = c._cuda_getDevice()
+    return _torch, dev, c._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _refuse(name: str, t, dtype, shape, dev) -> None:
@@ -396,6 +399,13 @@ def _arg(name: str, t, dtype, shape, dev) -> int:
     """The address of a tensor whose type, shape, layout and device the kernels can take; ValueError otherwise."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _addr(name: str, t, dtype, dev) -> int:
+    """_arg for a tensor whose shape has been read and is right."""
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(name, t, dtype, t.shape, dev)
     return t.data_ptr()
 
 
@@ -423,7 +433,7 @@ def attention_window(qkv, y, H: int, Hkv: int, window: int, sinks: int = 0, lse2
     torch, dev, s = _cuda(stream)
     B, T, D = _qkv_dims(qkv, H, Hkv)
     bf16 = torch.bfloat16
-    rc = lib.gptk_attention_window(_arg("qkv", qkv, bf16, (B, T, (H + 2 * Hkv) * D), dev),
+    rc = lib.gptk_attention_window(_addr("qkv", qkv, bf16, dev),
                                    _arg("y", y, bf16, (B, T, H * D), dev),
                                    None if lse2 is None else _arg("lse2", lse2, torch.float32, (B, H, T), dev),
                                    B, T, H, Hkv, D, window, sinks, s)
@@ -439,7 +449,7 @@ def attention_window_bwd(qkv, y, dy, lse2, dqkv, H: int, Hkv: int, window: int, 
     torch, dev, s = _cuda(stream)
     B, T, D = _qkv_dims(qkv, H, Hkv)
     bf16, rows, out = torch.bfloat16, (B, T, (H + 2 * Hkv) * D), (B, T, H * D)
-    rc = lib.gptk_attention_window_bwd(_arg("qkv", qkv, bf16, rows, dev), _arg("y", y, bf16, out, dev),
+    rc = lib.gptk_attention_window_bwd(_addr("qkv", qkv, bf16, dev), _arg("y", y, bf16, out, dev),
                                        _arg("dy", dy, bf16, out, dev),
                                        _arg("lse2", lse2, torch.float32, (B, H, T), dev),
                                        _arg("dqkv", dqkv, bf16, rows, dev), B, T, H, Hkv, D, window, sinks, s)
@@ -455,9 +465,9 @@ def _cache(torch, pool, weight, table, dev):
     if len(tshape) != 2:
         raise ValueError(f"table: shape {tuple(tshape)}, needs [B, max_pages]")
     pages, _, Hkv, page, D = shape
-    return (pages, Hkv, page, D, tshape[0], tshape[1], _arg("pool", pool, torch.bfloat16, shape, dev),
+    return (pages, Hkv, page, D, tshape[0], tshape[1], _addr("pool", pool, torch.bfloat16, dev),
             None if weight is None else _arg("weight", weight, torch.float32, (pages, Hkv, page), dev),
-            _arg("table", table, torch.int32, tshape, dev))
+            _addr("table", table, torch.int32, dev))
 
 
 def paged_store(qkv, pool, table, H: int, start=None, count=None, weight=None, stream=None):
@@ -467,7 +477,9 @@ def paged_store(qkv, pool, table, H: int, start=None, count=None, weight=None, s
     pages, Hkv, page, D, B, max_pages, p, w, tb = _cache(torch, pool, weight, table, dev)
     i32, shape = torch.int32, qkv.shape
     T = shape[1] if len(shape) == 3 else 0
-    rc = lib.gptk_paged_store(_arg("qkv", qkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D), dev), p, w, tb,
+    if shape != (B, T, (H + 2 * Hkv) * D):
+        _refuse("qkv", qkv, torch.bfloat16, (B, T, (H + 2 * Hkv) * D), dev)
+    rc = lib.gptk_paged_store(_addr("qkv", qkv, torch.bfloat16, dev), p, w, tb,
                               None if start is None else _arg("start", start, i32, (B,), dev),
                               None if count is None else _arg("count", count, i32, (B,), dev),
                               B, T, H, Hkv, D, pages, page, max_pages, s)
