@@ -934,14 +934,62 @@ constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
 
-template <int NC>
-__global__ void __launch_bounds__(kEvThreads)
+// Copies the m kept rows (s_keep) of one key head and sequence by the block that chose them: a batch of rows is read
+// whole before any of it is written, as row i comes from a row at or behind i (no later batch reads what one wrote).
+template <int D>
+__device__ __forceinline__ void copy_kept(const PagedCache& c, const int32_t* trow, const int32_t* drow, const int* s_keep,
+                                          int m, int h, int* err) {
+  constexpr int U = D / 8, ROWS = kEvThreads / U, K = 4;
+  const int u = threadIdx.x % U, pmask = (1 << c.page_log2) - 1;
+  uint4* pool = static_cast<uint4*>(c.pool);
+  const size_t vstep = (static_cast<size_t>(c.Hkv) << c.page_log2) * U;
+  for (int i0 = threadIdx.x / U; i0 - static_cast<int>(threadIdx.x) / U < m; i0 += ROWS * K) {
+    uint4 kx[K], vx[K];
+    float wx[K];
+    int src[K], dst[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = min(i0 + k * ROWS, m - 1);
+      src[k] = __ldg(trow + (s_keep[i] >> c.page_log2));
+      dst[k] = __ldg(drow + (i >> c.page_log2));
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int i = i0 + k * ROWS, slot = s_keep[min(i, m - 1)] & pmask;
+      const bool ok = static_cast<unsigned>(src[k]) < static_cast<unsigned>(c.pages) &&
+                      static_cast<unsigned>(dst[k]) < static_cast<unsigned>(c.pages);
+      if (!ok) record_error(err, GPT_DEV_EPAGE);
+      if (!ok || i >= m) dst[k] = -1;                // nothing to write; the loads go to page 0
+      const int pg = ok ? src[k] : 0;
+      const uint4* from = pool + row_at(c, pg, 0, h, slot) * U + u;
+      kx[k] = from[0];
+      vx[k] = from[vstep];
+      wx[k] = c.weight[weight_at(c, pg, h, slot)];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (dst[k] < 0) continue;
+      const int slot = (i0 + k * ROWS) & pmask;
+      uint4* to = pool + row_at(c, dst[k], 0, h, slot) * U + u;
+      to[0] = kx[k];
+      to[vstep] = vx[k];
+      if (u == 0) c.weight[weight_at(c, dst[k], h, slot)] = wx[k];
+    }
+  }
+}
+
+// D = 0: the chosen rows are named in `kept` for the kernel that moves them; else the block moves them itself.
+template <int NC, int D>
+__global__ void __launch_bounds__(kEvThreads, 2)
 paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __restrict__ new_lens,
-                    int32_t* __restrict__ kept, int budget, int sinks, int recent, int room, int* err) {
+                    int32_t* __restrict__ kept, const int32_t* __restrict__ dst_table, int dst_max_pages, int budget,
+                    int sinks, int recent, int room, int* err) {
   namespace cg = cooperative_groups;
   pdl_wait();
   pdl_trigger();
-  extern __shared__ uint32_t s_rank[];               // [room] ranks of this block's stretch
+  extern __shared__ uint32_t s_rank[];               // [room] ranks of this block's stretch, then the kept rows
+  int* s_keep = reinterpret_cast<int*>(s_rank + room);
   __shared__ __align__(16) int hists[3][kEvBins];    // one per pass: another block may still read the last one's
   __shared__ int s_sum[kEvWarps], s_tie[kEvWarps], pick[3], s_total[2];
   const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC), h = static_cast<int>(blockIdx.x / NC), b = blockIdx.y;
@@ -962,15 +1010,27 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
   const int me = part * kEvThreads + tid;            // thread of the cluster
   if (h == 0 && me == 0) new_lens[b] = m;
   for (int i = max(m, 0) + me; i < budget; i += NC * kEvThreads) out[i] = -1;
+  const int32_t* drow = dst_table + static_cast<size_t>(b) * dst_max_pages;
+  auto keep_row = [&](int i, int r) {
+    out[i] = r;
+    if constexpr (D > 0) s_keep[i] = r;
+  };
+  auto finish = [&]() {
+    if constexpr (D > 0) {
+      __syncthreads();
+      copy_kept<D>(c, trow, drow, s_keep, m, h, err);
+    }
+  };
   if (n <= budget) {                                 // (the same for the whole cluster)
-    for (int i = me; i < m; i += NC * kEvThreads) out[i] = i;
+    for (int i = me; i < m; i += NC * kEvThreads) keep_row(i, i);
+    if (n > 0) finish();
     return;
   }
   const int lo = sinks, mid = n - recent - sinks;    // rows chosen by weight: lo .. lo + mid - 1
-  for (int i = me; i < sinks; i += NC * kEvThreads) out[i] = i;
-  for (int i = me; i < recent; i += NC * kEvThreads) out[budget - recent + i] = n - recent + i;
+  for (int i = me; i < sinks; i += NC * kEvThreads) keep_row(i, i);
+  for (int i = me; i < recent; i += NC * kEvThreads) keep_row(budget - recent + i, n - recent + i);
   int want = budget - sinks - recent;                // how many of them
-  if (want == 0) return;
+  if (want == 0) return finish();
   const int each = ((mid + NC - 1) / NC + 31) / 32 * 32;
   const int base = min(mid, part * each), size = min(mid - base, each);   // this block's stretch
   const bool fits = each <= room;
@@ -1108,11 +1168,12 @@ paged_choose_kernel(PagedCache c, const int32_t* __restrict__ lens, int32_t* __r
     const uint32_t tie = __ballot_sync(0xffffffffu, i < end && (k >> low) == prefix), below = (1u << lane) - 1u;
     const bool keep = i < end && ((k >> low) > prefix || ((k >> low) == prefix && seen_ties + __popc(tie & below) < want));
     const uint32_t mask = __ballot_sync(0xffffffffu, keep);
-    if (keep) out[at + __popc(mask & below)] = lo + base + i;
+    if (keep) keep_row(at + __popc(mask & below), lo + base + i);
     at += __popc(mask);
     seen_ties += __popc(tie);
   }
   if constexpr (NC > 1) sync_all();                  // no block leaves while another reads its totals
+  finish();
 }
 
 // Moves the kept rows of one (sequence, key head), a cluster of blocks each: 8 D bytes per row, bound by memory. Row i
@@ -1314,20 +1375,31 @@ cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const i
                                int* err, cudaStream_t s) {
   // one block per list up to 4,096 rows, clusters of four for longer lists; ranks for the longest stretch that the
   // table allows, as far as shared memory goes
-  const long long rows = (static_cast<long long>(c.max_pages) << c.page_log2) - sinks - recent;
+  const long long all = static_cast<long long>(c.max_pages) << c.page_log2, rows = all - sinks - recent;
   const int nc = rows <= 4096 ? 1 : 4;
-  const long long most = (232448 - 28672) / 4, stretch = rows < 0 ? 0 : ((rows + nc - 1) / nc + 31) / 32 * 32;
-  const int room = static_cast<int>(stretch < most ? stretch : most);
-  auto choose = nc == 1 ? paged_choose_kernel<1> : paged_choose_kernel<4>;
-  static SmemLimit limit[2];
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
-  if (e == cudaSuccess) e = limit[nc == 1 ? 0 : 1].raise(choose, dev, room * 4);
+  if (e != cudaSuccess) return e;
+  // One launch where the choosing blocks copy as well: a block copies 256 rows in about 1.9 us, a second launch takes 2.5
+  // and then has the whole machine. 64 sequences x 12 heads of up to 1,024 rows to 512: 44.6 us in one, 53.3 in two
+  // launches, 16 sequences 12.8 and 13.3; 48 lists to 512 rows 8.5 and 9.3, to 900 rows 12.1 and 11.0; 12 lists to 128
+  // rows 6.3 and 6.5, to 512 rows 8.4 and 6.6.
+  const long long lists = static_cast<long long>(B) * c.Hkv;
+  const int held = static_cast<int>(budget < all ? budget : all);      // rows that a list can keep
+  const bool one = nc == 1 && held <= 4096 && (lists >= sms || held <= 14 * lists);
+  const long long most = (232448 - 28672) / 4, stretch = rows < 0 ? 0 : ((rows + nc - 1) / nc + 31) / 32 * 32;
+  const int room = static_cast<int>(stretch < most ? stretch : most);
+  const int form = nc == 4 ? 0 : !one ? 1 : D == 64 ? 2 : 3;
+  const int smem = 4 * (room + (one ? held : 0));
+  auto choose = form == 0 ? paged_choose_kernel<4, 0> : form == 1 ? paged_choose_kernel<1, 0>
+      : form == 2 ? paged_choose_kernel<1, 64> : paged_choose_kernel<1, 32>;
+  static SmemLimit limit[4];
+  e = limit[form].raise(choose, dev, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(c.Hkv) * nc, static_cast<unsigned>(B));
   cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(room) * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1336,8 +1408,8 @@ cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const i
   attr[1].val.clusterDim = {static_cast<unsigned>(nc), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, choose, c, lens, new_lens, kept, budget, sinks, recent, room, err);
-  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, choose, c, lens, new_lens, kept, dst_table, dst_max_pages, budget, sinks, recent, room, err);
+  if (e != cudaSuccess || one) return e;
   const int chunk = kMoveBlocks * (kMoveThreads / (D / 8)) * kMoveDepth, chunks = (budget - 1) / chunk + 1;
   const dim3 grid(static_cast<unsigned>(kMoveBlocks * (chunks < 8 ? chunks : 8)), static_cast<unsigned>(c.Hkv),
                   static_cast<unsigned>(B));

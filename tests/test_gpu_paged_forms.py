@@ -1,5 +1,8 @@
-"""Attention of one new token on the GPU: the form for few rows in sight (one launch of clusters, one or two units of 32
-rows per warp) and the general one, chosen by the page table's width, at the sizes where the choice turns.
+"""The paged operators' forms on the GPU, at the sizes where the choice between them turns.
+
+Attention of one new token: the form for few rows in sight (one launch of clusters, one or two units of 32
+rows per warp) and the general one, chosen by the page table's width. Eviction: in one launch, whose choosing blocks
+copy as well, or in two, chosen by the lists and the rows that they keep; copies, so equal bit for bit.
 
 The cases, the reference and the tolerances are those of test_gpu_paged.py: both forms take the same roundings, and the
 form for few rows one more factor 2^(m - M) per weight, whose 2^-22 the doubled bound of that file covers.
@@ -12,7 +15,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from gpu_util import host  # noqa: E402
-from test_gpu_paged import Case  # noqa: E402
+from test_gpu_paged import Case, _evict_case, _evict_run  # noqa: E402
 
 
 def widened(c, rows):
@@ -97,3 +100,46 @@ def test_one_result_bit_for_bit_in_every_form(gpt_lib):
         c.device()
         c.call()
         assert torch.equal(y, c.d_y) and torch.equal(lse2, c.d_lse2) and torch.equal(w0, c.d_weight)
+
+
+@pytest.mark.parametrize("B,Hkv,D,page,rows,budget,sinks,recent", [
+    (20, 8, 64, 16, 300, 100, 4, 30), (20, 8, 32, 8, 300, 257, 0, 0), (77, 2, 64, 64, 700, 600, 16, 100),   # 152 lists and more
+    (4, 12, 64, 16, 900, 672, 4, 64), (4, 12, 64, 16, 900, 673, 4, 64),          # 48 lists: up to 672 rows in one launch
+    (1, 12, 64, 16, 700, 168, 0, 168), (1, 12, 32, 16, 700, 169, 169, 0),        # 12 lists: up to 168; nothing to choose
+    (1, 1, 64, 8, 40, 14, 2, 3), (1, 1, 64, 8, 40, 15, 2, 3),
+    (80, 2, 32, 64, 4400, 4096, 4, 300), (80, 2, 32, 64, 4400, 4097, 4, 300),    # kept rows past the shared list
+    (10, 16, 32, 16, 200, 5000, 0, 0)])                                         # all are kept
+def test_evict_in_one_launch_and_in_two(gpt_lib, B, Hkv, D, page, rows, budget, sinks, recent):
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(-1, rows + 1, B).tolist()
+    lens[0] = rows
+    for kind in ("plain", "ties", "nan"):
+        pool, weight, table, n, dst = _evict_case(budget, lens, Hkv, D, page, budget, kind == "ties", kind == "nan")
+        _evict_run(pool, weight, table, n, dst, budget, sinks, recent)
+        if table.shape[1] * page >= budget:
+            _evict_run(pool, weight, table, n, table, budget, sinks, recent)
+
+
+def test_evict_in_one_launch_reports_bad_pages(gpt_lib):
+    # rows of a page outside the pool are neither read nor written; the other sequences are right
+    from decoder_only_transformer_gpt_gb300 import binding
+    import paged_ref
+    from gpu_util import dev_bf16, dev_f32, dev_i32
+    pool, weight, table, lens, dst = _evict_case(9, [300] * 20, 8, 64, 16, 100)
+    for bad in (-1, 10 ** 9):
+        for where in ("source", "target"):
+            t, d = table.copy(), dst.copy()
+            (t if where == "source" else d)[0, 3] = bad
+            d_pool, d_weight = dev_bf16(pool), dev_f32(weight)
+            new = torch.full((20,), 99, dtype=torch.int32, device="cuda")
+            kept = torch.full((20, 8, 100), 99, dtype=torch.int32, device="cuda")
+            binding.paged_evict(d_pool, d_weight, dev_i32(t), dev_i32(lens), dev_i32(d), new, kept, 100, 4, 30)
+            with pytest.raises(binding.GptError) as e:
+                binding.status()
+            assert e.value.code == binding.GPT_EPAGE
+            want = paged_ref.evict(pool.astype(np.float64), weight, table, lens, dst, 100, 4, 30)
+            np.testing.assert_array_equal(host(new), want[2])
+            np.testing.assert_array_equal(host(kept)[1:], want[3][1:])
+            mine = np.concatenate([table[1:].ravel(), dst[1:].ravel()])  # the other sequences' pages
+            np.testing.assert_array_equal(host(d_pool)[mine], want[0][mine])
+            np.testing.assert_array_equal(host(d_weight)[mine], want[1][mine])
