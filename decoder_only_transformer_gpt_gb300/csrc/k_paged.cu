@@ -921,15 +921,18 @@ __device__ __forceinline__ uint32_t weight_rank(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Two kernels. The first chooses the rows of one (sequence, key head): a cluster of NC blocks holds the weights between
-// the sinks and the recent rows as ranks in shared memory, a stretch each (read once, through the table, all loads
-// independent; a list that does not fit is read again by each pass). Three passes over 11, 11 and 10 bits find the
-// rank of the smallest kept weight: a histogram of the rows that agree so far, summed over the blocks, whose bins are
-// scanned from the top. Then every warp counts its stretch of rows, and places them behind the stretches before it.
-// Equal weights are kept from the lowest row on. Bound by issuing about 200 instructions a row and
-// by the passes' barriers, so long lists are spread over four SMs (10,000 to 20,000 rows, 48 lists: 24 us with one block
-// of 1024 threads each; in clusters of eight both kernels took 65 us against 32), and lists of up to 4,096 rows are not
-// (500 to 1,024 rows, 192 lists: clusters of two 28 against 18.5). Both kernels: 28 us and 17.7 us, 2.3 and 2.9 TB/s.
+// One kernel chooses the rows of each (sequence, key head), and for short lists copies them too; for the others a second
+// one does. The choice: a cluster of NC blocks holds the weights between the sinks and the recent rows as ranks in shared
+// memory, a stretch each (read once, through the table, all loads independent; a list that does not fit is read again by
+// each pass). Up to three passes over 11, 11 and 10 bits find the rank of the smallest kept weight: a histogram of the
+// rows that agree so far, summed over the blocks, whose bins are scanned from the top; a bin that is kept whole ends them.
+// Then every warp counts its stretch of rows, and places them behind the stretches before it. Equal weights are kept
+// from the lowest row on.
+// Bound by issuing about 200 instructions a row and by the passes' barriers, so long lists are spread over four SMs
+// (10,000 to 20,000 rows, 48 lists: 24 us with one block of 1024 threads each; in clusters of eight both kernels took
+// 65 us against 32), and lists of up to 4,096 rows are not (500 to 1,024 rows, 192 lists: clusters of two 28 against
+// 18.5). Measured: 4 x 12 lists of 10,000 to 20,000 rows to 2,500 28 us, 16 x 12 of 500 to 1,024 to 512 15 us. Clusters
+// of four that copy as well were slower than the second launch (25.2 against 23.6 us, graph replays).
 constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
