@@ -143,3 +143,93 @@ def test_evict_in_one_launch_reports_bad_pages(gpt_lib):
             mine = np.concatenate([table[1:].ravel(), dst[1:].ravel()])  # the other sequences' pages
             np.testing.assert_array_equal(host(d_pool)[mine], want[0][mine])
             np.testing.assert_array_equal(host(d_weight)[mine], want[1][mine])
+
+
+WIDE = 65536                                         # a table this wide takes the general form
+
+
+@pytest.mark.parametrize("rows", [1024, WIDE])
+@pytest.mark.parametrize("weights", [False, True])
+def test_two_streams_and_two_graphs_at_once(gpt_lib, rows, weights):
+    # two caches: eager calls on two streams, then a graph of each, replayed together
+    a = widened(Case(12, 12, 64, 16, [700] * 8, seed=12, weights=weights), rows)
+    b = widened(Case(6, 2, 32, 16, [650, 1, -1, 500], 300, 4, seed=13, weights=weights), rows)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a.call(stream=s)
+    b.call(stream=t)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+    graphs = []
+    for c in (a, b):
+        c.device()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.call()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graphs[0].replay()
+    with torch.cuda.stream(t):
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+
+
+@pytest.mark.parametrize("rows", [1024, WIDE])
+def test_a_graph_with_other_lengths(gpt_lib, rows):
+    # captured with short sequences, replayed with longer ones and one that has ended
+    c = widened(Case(8, 2, 64, 16, [0, 3, 900], seed=9), rows)
+    g = torch.cuda.CUDAGraph()
+    c.call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        c.call()
+    d = widened(Case(8, 2, 64, 16, [900, -1, 17], seed=10), rows)
+    for x, v in ((c.d_qkv, d.d_qkv), (c.d_pool, d.d_pool), (c.d_table, d.d_table), (c.d_lens, d.d_lens), (c.d_weight, d.d_weight)):
+        x.copy_(v)
+    c.d_y.fill_(7.0)
+    c.d_lse2.fill_(7.0)
+    g.replay()
+    torch.cuda.synchronize()
+    d.d_y, d.d_lse2, d.d_pool, d.d_weight = c.d_y, c.d_lse2, c.d_pool, c.d_weight
+    d.check()
+
+
+@pytest.mark.parametrize("rows", [1024, WIDE])
+def test_sequences_that_share_pages(gpt_lib, rows):
+    c = Case(4, 2, 64, 16, [40, 40, 25], seed=7)
+    c.table[1, :2] = c.table[0, :2]
+    run(widened(c, rows))
+
+
+@pytest.mark.parametrize("rows", [1024, WIDE])
+def test_peaked_scores(gpt_lib, rows):
+    # one row takes nearly all the weight, the rest underflow
+    run(widened(Case(4, 4, 64, 16, [500, 40], seed=4, scale=24.0), rows))
+
+
+@pytest.mark.parametrize("budget", [60, 400])
+def test_evictions_on_two_streams(gpt_lib, budget):
+    # the form with one launch and the one with two, each on two caches at once
+    from decoder_only_transformer_gpt_gb300 import binding
+    import paged_ref
+    from gpu_util import dev_bf16, dev_f32, dev_i32
+    runs = []
+    for seed in (1, 2):
+        pool, weight, table, lens, dst = _evict_case(seed, [500, 450, 480], 2, 64, 16, budget)
+        d = [dev_bf16(pool), dev_f32(weight), dev_i32(table), dev_i32(lens), dev_i32(dst),
+             torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty(3, 2, budget, dtype=torch.int32, device="cuda")]
+        runs.append((torch.cuda.Stream(), d, paged_ref.evict(pool.astype(np.float64), weight, table, lens, dst, budget, 4, 20)))
+    torch.cuda.synchronize()
+    for s, d, _ in runs:
+        binding.paged_evict(*d, budget, 4, 20, stream=s)
+    torch.cuda.synchronize()
+    binding.status()
+    for _, d, want in runs:
+        np.testing.assert_array_equal(host(d[5]), want[2])
+        np.testing.assert_array_equal(host(d[6]), want[3])
+        np.testing.assert_array_equal(host(d[1]), want[1])
+        np.testing.assert_array_equal(host(d[0]), want[0])
