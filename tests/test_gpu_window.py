@@ -248,3 +248,28 @@ def test_two_calls_at_once(gpt_lib):
 def test_shared_key_tiles(gpt_lib, T, H, Hkv, window, sinks):
     # few heads and long windows or sinks: a key tile's query tiles are cut into segments of several CTAs
     _case(1, T, H, Hkv, 64, window, sinks, seed=T)
+
+
+@pytest.mark.parametrize("window", [31, 32, 33, 127, 128, 129, 256, 300])
+@pytest.mark.parametrize("sinks", [0, 1, 15, 16, 17, 31, 129])
+def test_borders_in_pairs_of_tiles(gpt_lib, window, sinks):
+    # several items per CTA; sinks as one step of 16 keys and as whole tiles; every 32-key part of a tile as a border
+    _case(10, 900, 4, 2, 64, window, sinks, seed=window + sinks, only={(0, 0), (9, 1)})
+    _case(10, 900, 4, 2, 32, window, sinks, seed=window + sinks, only={(4, 1)})
+
+
+@pytest.mark.parametrize("B,T", [(1, 700), (12, 700)])
+@pytest.mark.parametrize("what", ["sinks high", "sinks low", "first of 32 high", "first of 32 low"])
+def test_references_far_from_the_rest(gpt_lib, B, T, what):
+    # scores around 0 but for the sinks, or every 32nd key (a warp's reference in its first tile), hundreds above or below
+    H, D, window, sinks = 4, 64, 200, 6
+    qkv, dy = _inputs(B, T, H, H, D, seed=T)
+    q, k = qkv[..., :H * D], qkv[..., H * D:2 * H * D]
+    q[...] = np.abs(q)
+    rows = slice(0, sinks) if what.startswith("sinks") else slice(0, T, 32)
+    k[:, rows] = np.abs(k[:, rows]) * (8.0 if what.endswith("high") else -8.0)
+    qkv = host(dev_bf16(qkv)).astype(np.float32)
+    y, lse2 = _forward(dev_bf16(qkv), H, H, window, sinks)
+    from decoder_only_transformer_gpt_gb300 import binding
+    binding.status()
+    _check(qkv, dy, y, lse2, None, H, H, window, sinks, only={(0, 0), (B - 1, 3)})
