@@ -373,27 +373,16 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
     // of 16 dimensions: 8 columns)
     auto issue_scores = [&](int g, uint32_t qs) {
       const uint32_t qoff = qs * Cfg::TILE + g * HQ * Cfg::ROWB;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc_mma_bf16_ts_warp(tmem_base + 128 * g, tmem_base + kColK + 8 * k, desc_add(dq0, qoff + k * 32), id_s,
-                            k > 0 ? 1u : 0u);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc_mma_bf16_ts_warp(tmem_base + 128 * g + 64, tmem_base + kColK + D / 2 + 8 * k, desc_add(dy0, qoff + k * 32),
-                            id_s, k > 0 ? 1u : 0u);
+      mma_ts_run<D / 16, 2>(tmem_base + 128 * g, tmem_base + kColK, desc_add(dq0, qoff), id_s, false);
+      mma_ts_run<D / 16, 2>(tmem_base + 128 * g + 64, tmem_base + kColK + D / 2, desc_add(dy0, qoff), id_s, false);
       tc_commit_warp(&bars->s_full[g]);
     };
     // dU += P^T_g dY_g and dK += dS^T_g Q_g (a K step of 16 queries: 8 TMEM columns, 16 rows of dY / Q)
     auto issue_acc = [&](int g, uint32_t qs, bool first) {
       const uint32_t qoff = qs * Cfg::TILE + g * HQ * Cfg::ROWB;
-#pragma unroll
-      for (int kk = 0; kk < HQ / 16; ++kk)
-        tc_mma_bf16_ts_warp(tmem_base + kColDU, tmem_base + 128 * g + 8 * kk, desc_add(dymn0, qoff + kk * 16 * Cfg::ROWB),
-                            id_acc, (first && kk == 0) ? 0u : 1u);
-#pragma unroll
-      for (int kk = 0; kk < HQ / 16; ++kk)
-        tc_mma_bf16_ts_warp(tmem_base + kColDK, tmem_base + 128 * g + 64 + 8 * kk,
-                            desc_add(qmn0, qoff + kk * 16 * Cfg::ROWB), id_acc, (first && kk == 0) ? 0u : 1u);
+      static_assert(HQ / 16 == 4, "K steps of a half");
+      mma_ts_run<4, Cfg::ROWB>(tmem_base + kColDU, tmem_base + 128 * g, desc_add(dymn0, qoff), id_acc, !first);
+      mma_ts_run<4, Cfg::ROWB>(tmem_base + kColDK, tmem_base + 128 * g + 64, desc_add(qmn0, qoff), id_acc, !first);
     };
     int r = 0;
     Step0 x;
@@ -460,9 +449,9 @@ attn_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __gr
       tc_fence_after();
       const uint32_t dsoff = (tiles & 1u) * Cfg::DS_BUF;
 #pragma unroll
-      for (int kk = 0; kk < BT / 16; ++kk)           // a K step of 16 keys: 16 rows of dS and of K_j
-        tc_mma_bf16_warp(tmem_base + kColDQ, desc_add(ds0, dsoff + kk * 16 * 128),
-                         desc_add(kmn0, kb * Cfg::TILE + kk * 16 * Cfg::ROWB), id_dq, kk > 0 ? 1u : 0u);
+      for (int kk = 0; kk < BT / 64; ++kk)           // a K step of 16 keys: 16 rows of dS and of K_j
+        mma_ss_run4<128, Cfg::ROWB>(tmem_base + kColDQ, desc_add(ds0, dsoff + kk * 64 * 128),
+                                    desc_add(kmn0, kb * Cfg::TILE + kk * 64 * Cfg::ROWB), id_dq, kk > 0);
       tc_commit_warp(&bars->dq_full);
       if (last) tc_commit_warp(&bars->kv_empty[kb]);   // K_j and U_j are consumed
       if (!has_next) break;
