@@ -28,8 +28,8 @@
 // Bound by shared memory: a step (128 keys x 128 queries) moves about 270 KB through it (operand reads of five products,
 // the dS tile written and read, copies in, dQ out), 2,100 of its 2,850 cycles at 128 bytes each; the derivative's chain
 // on one half takes about 1,270. A deeper ring of query tiles, or the scores read 16 queries ahead, changed nothing.
-// Measured (with the forward, calls back to back): 8,192 tokens, 16 heads on 4, D 64, W 1024: 179 us, 630 TFLOP/s; with
-// 12 heads, 8 x 1,000 tokens, W 250: 81 us.
+// Measured (with the forward, calls back to back): 8,192 tokens, 16 heads on 4, D 64, W 1024: 183 us, 620 TFLOP/s; with
+// 12 heads, 8 x 1,000 tokens, W 250: 78 us.
 //
 // Error of dqkv against 64 bits, relative to its norm: 2.3e-3 to 2.7e-3 on normal inputs, where rounding the result
 // alone is 1.7e-3; P and dS rounded to bf16 bring 2.3e-3, the rest is Dsum from the bf16 rows of y.
