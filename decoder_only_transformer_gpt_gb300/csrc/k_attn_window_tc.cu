@@ -34,8 +34,8 @@
 //
 // Softmax: per row one running reference m and sum. The reference starts as the score of the warp's first diagonal key
 // where all its rows see that (W >= 32), else as the exact maximum of the first half tile in which the row sees a key;
-// it is raised only when a half tile's sum passes 2^16 and the maximum grew by more than 2^8. Sums are fp32; P is rounded to bf16 for
-// the second product (the type the tensor core multiplies), which costs at most 2^-8 of sum a |u|.
+// it is raised only when a half tile's sum passes 2^16 and the maximum grew by more than 2^8. Sums are fp32; P is rounded
+// to bf16 for the second product (the type the tensor core multiplies), which costs at most 2^-8 of sum a |u|.
 //
 // Taken back, at the 12,001 tokens above as they were then: tiles of 64 keys in six score buffers (157 us against 151),
 // a third softmax group (194 against 151), more registers for the softmax warps by setmaxnreg (207 against 185).
