@@ -133,8 +133,8 @@ paged_store_kernel(PagedCache c, const uint4* __restrict__ qkv, const int32_t* _
 //    not seen are not read (their shared memory is filled with zeros).
 //  * The scores and the product with the values are mma.sync m16n8k16 with the query heads of the group as the 16
 //    rows: with at most 16 rows of queries per key head the tensor core's rate does not matter (a tcgen05 tile
-//    would have 128), but shared keys and values are unpacked once for all heads. P is rounded to bf16 for that
-//    product (2^-8 of sum a |u| at most); scores, maxima, sums and outputs stay fp32.
+//    would have 128), but shared keys and values are unpacked once for all heads. P enters that product in two bf16
+//    parts; scores, maxima, sums and outputs stay fp32.
 // Measured: 16 sequences of 9,000 to 32,000 rows x 12 heads 160 us, 6.3 TB/s. Units of 16 rows were slower (16 sequences
 // of up to 1,023 rows: 15.6 against 14.5 us).
 constexpr int kStages = 3;
@@ -213,6 +213,51 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 template <int D>
 __device__ __forceinline__ uint32_t tile_at(int r, int u) {
   return D == 64 ? r * 128 + ((u ^ (r & 7)) << 4) : r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+}
+
+// O += P U for 16 cached rows (a, b: the score tiles of eight each, now probabilities; u0: their first value row's place in
+// shared memory), P in two bf16 parts: hi is p rounded, lo is p - hi rounded, so p - hi - lo is at most 2^-16 of p (one
+// part alone made the outputs' error 2.0e-3 of their norm where their own rounding makes 1.6e-3). Of up to eight query
+// heads lo takes the operand's other eight rows, its products o[][2] and o[][3] (joined_parts adds them): the second
+// product of their own took 16 sequences of up to 1,023 rows from 10.6 to 11.7 us. Of 9 to 16 heads it is a product of its
+// own (16 sequences of 9,000 to 32,000 rows, 12 key heads of 16 heads: 185 us, with one part 168).
+template <int D, int RH>
+__device__ __forceinline__ void add_values(float (&o)[D / 8][4], const float (&a)[4], const float (&b)[4], uint32_t u0, int lane) {
+  uint32_t p[4], q[4];
+#pragma unroll
+  for (int i = 0; i < 2 * RH; ++i) {                 // heads lane / 4 (i even) and lane / 4 + 8, columns of a, then of b
+    const float x = i < RH ? a[2 * i] : b[2 * (i - RH)], y = i < RH ? a[2 * i + 1] : b[2 * (i - RH) + 1];
+    const int at = RH == 2 ? i : 2 * i;              // a: registers 0 and 1, b: 2 and 3
+    p[at] = pack_bf16x2(x, y);
+    const float2 f = unpack_bf16x2(p[at]);
+    const uint32_t lo = pack_bf16x2(x - f.x, y - f.y);
+    if (RH == 2) q[at] = lo;
+    else p[at + 1] = lo;
+  }
+  uint32_t f[D / 16][4];
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    ldmatrix4_trans(f[j], u0 + tile_at<D>(lane & 15, 2 * j + (lane >> 4)));
+    mma_16816(o[2 * j], p, f[j][0], f[j][1]);
+    mma_16816(o[2 * j + 1], p, f[j][2], f[j][3]);
+  }
+  if constexpr (RH == 2) {
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      mma_16816(o[2 * j], q, f[j][0], f[j][1]);
+      mma_16816(o[2 * j + 1], q, f[j][2], f[j][3]);
+    }
+  }
+}
+template <int NT, int RH>
+__device__ __forceinline__ void joined_parts(float (&o)[NT][4]) {
+  if constexpr (RH == 1) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      o[j][0] += o[j][2];
+      o[j][1] += o[j][3];
+    }
+  }
 }
 
 // The list position of a unit: sequence, head group (key head * mg + group), tile of the sequence's seen rows.
@@ -476,24 +521,15 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
       for (int j = 0; j < NT; ++j) {
         o[j][2 * rh] *= a;
         o[j][2 * rh + 1] *= a;
+        if (RH == 1) {                               // the second part's
+          o[j][2] *= a;
+          o[j][3] *= a;
+        }
       }
     }
-    // O += P U: two steps of 16 rows
+    // O += P U: two steps of 16 rows (a step's offset keeps tile_at's permutation: it is a multiple of eight rows)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t p[4];
-      p[0] = pack_bf16x2(s[2 * k][0], s[2 * k][1]);
-      p[2] = pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]);
-      p[1] = RH == 2 ? pack_bf16x2(s[2 * k][2], s[2 * k][3]) : 0u;
-      p[3] = RH == 2 ? pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3]) : 0u;
-#pragma unroll
-      for (int j = 0; j < NT / 2; ++j) {
-        uint32_t f[4];
-        ldmatrix4_trans(f, sv + tile_at<D>(16 * k + (lane & 15), 2 * j + (lane >> 4)));
-        mma_16816(o[2 * j], p, f[0], f[1]);
-        mma_16816(o[2 * j + 1], p, f[2], f[3]);
-      }
-    }
+    for (int k = 0; k < 2; ++k) add_values<D, RH>(o, s[2 * k], s[2 * k + 1], sv + 16 * k * Cfg::ROWB, lane);
     const bool ends = at.tile == at.nt - 1;
     if (ends && g0 == 0) {                           // the sequence's newest row: into the cache
       const int pg = __ldg(c.table + static_cast<size_t>(at.b) * c.max_pages + (at.last >> c.page_log2));
@@ -508,6 +544,7 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
     if (ends || n == count - 1) {                    // the piece is done
       const bool whole = ends && piece0 + at.nt == n + 1;   // it holds all of the segment's units
       const size_t slot = static_cast<size_t>(gw) * 2 + (piece0 == 0 ? 0 : 1);
+      joined_parts<NT, RH>(o);
 #pragma unroll
       for (int rh = 0; rh < RH; ++rh) {
         float lt = l[rh];
@@ -695,19 +732,9 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
   for (int k = 0; k < 2 * UPW; ++k) {
     if (!mask[k >> 1]) continue;
     const uint32_t sv = ring_a + (k >> 1) * 2 * Cfg::TILE + Cfg::TILE;
-    uint32_t p[4];
-    p[0] = pack_bf16x2(s[2 * k][0], s[2 * k][1]);
-    p[2] = pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]);
-    p[1] = RH == 2 ? pack_bf16x2(s[2 * k][2], s[2 * k][3]) : 0u;
-    p[3] = RH == 2 ? pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3]) : 0u;
-#pragma unroll
-    for (int j = 0; j < NT / 2; ++j) {
-      uint32_t f[4];
-      ldmatrix4_trans(f, sv + tile_at<D>(16 * (k & 1) + (lane & 15), 2 * j + (lane >> 4)));
-      mma_16816(o[2 * j], p, f[0], f[1]);
-      mma_16816(o[2 * j + 1], p, f[2], f[3]);
-    }
+    add_values<D, RH>(o, s[2 * k], s[2 * k + 1], sv + 16 * (k & 1) * D * 2, lane);
   }
+  joined_parts<NT, RH>(o);
   __syncwarp();                                      // the warp's tiles are read: its outputs take their place
   float* own = reinterpret_cast<float*>(ring);       // [QR][D]
 #pragma unroll

@@ -194,7 +194,8 @@ int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* 
  * 10 MB at most, and with weights 4 bytes per query head and seen row that the table has room for) is taken on the stream from a pool that the library keeps; make a process's first call
  * before any stream capture. The caller counts lens up (one cache per layer
  * shares one lens). Sequences may share the pages of rows below their own; the new rows' pages are their own. fp32
- * scores and sums; the probabilities are rounded to bf16 for the product with the values. y overlaps no input.
+ * scores and sums; the probabilities enter the product with the values in two bf16 parts (2^-16 of each at most is
+ * lost). y overlaps no input.
  */
 int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32_t* table, const int32_t* lens, void* y,
                          float* lse2, int32_t B, int32_t H, int32_t Hkv, int32_t D, int32_t pages, int32_t page,
