@@ -13,6 +13,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 import paged_ref  # noqa: E402
+import test_gpu_window as gw  # noqa: E402
 from gpu_util import dev_bf16, host  # noqa: E402
 from test_gpu_paged import LOG2E, Case  # noqa: E402
 from test_gpu_paged_forms import widened  # noqa: E402
@@ -40,3 +41,27 @@ def test_decode_rounds_its_output_alone(gpt_lib, rows, H, Hkv, D):
             tol = (2.0 ** -16 + 2 * d + (ln + 1) * 2.0 ** -24) * (a @ np.abs(u)) + 2.0 ** -8 * np.abs(y[b, at]) * (1 + 2.0 ** -7)
             err = np.abs(gy[b, at] - y[b, at])
             assert np.all(err <= tol), (b, h, err.max(), tol[err.argmax()])
+
+
+@pytest.mark.parametrize("D", [32, 64])
+@pytest.mark.parametrize("B", [1, 8])
+def test_raised_reference_keeps_probabilities(gpt_lib, B, D):
+    # Key 64 of every tile of 128 scores 14 to 25 nats above the rest, so the queries behind it raise their reference
+    # after the tile's first 64 probabilities were rounded. Each output column reads one of those keys alone, whose value
+    # is large: an output is one probability, rounded once, times its value, and is rounded once itself.
+    H, T, window = 24, 256, 256
+    rng = np.random.default_rng(D + B)
+    qkv = np.zeros((B, T, 3, H, D), np.float32)
+    qkv[:, :, 0] = rng.standard_normal((B, T, H, D)) * 0.3
+    qkv[:, :, 1] = rng.standard_normal((B, T, H, D)) * 0.5
+    qkv[:, :, 0, :, 0] = rng.uniform(4, 7, (B, T, H))
+    qkv[:, :, 1, :, 0] = 0.0
+    qkv[:, 64::128, 1, :, 0] = 3.5 * math.sqrt(D)
+    for t in range(T):
+        if t % 128 < 64:
+            qkv[:, t, 2, :, t % D] = 2.0 ** 20 * rng.uniform(1, 2, (B, H))
+    qkv = host(dev_bf16(qkv.reshape(B, T, 3 * H * D))).astype(np.float32)
+    y, lse2 = gw._forward(dev_bf16(qkv), H, H, window, 0)
+    from decoder_only_transformer_gpt_gb300 import binding
+    binding.status()
+    gw._check(qkv, np.zeros((B, T, H * D), np.float32), y, lse2, None, H, H, window, 0, only=None if B == 1 else {(7, h) for h in range(H)})
