@@ -8,9 +8,10 @@
 // so results are unchanged. Set GPT_GB300_NO_PDL=1 to launch without overlap.
 #pragma once
 
+#include "device_state.h"
+
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdlib>
 #include <utility>
 
@@ -33,35 +34,6 @@ inline bool pair_enabled() {
   }();
   return on;
 }
-
-// What a launcher asks of the device at every call, asked once per device (each question costs the host about half a
-// microsecond, which counts where a whole step takes ten).
-constexpr int kMaxLaunchDevices = 64;
-
-// The current device's number and its SM count.
-inline cudaError_t device_sms(int* dev, int* sms) {
-  static std::atomic<int> known[kMaxLaunchDevices];
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return e;
-  if (*dev < 0 || *dev >= kMaxLaunchDevices) return cudaErrorInvalidDevice;
-  *sms = known[*dev].load(std::memory_order_relaxed);
-  if (*sms > 0) return cudaSuccess;
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
-  if (e == cudaSuccess) known[*dev].store(*sms, std::memory_order_relaxed);
-  return e;
-}
-
-// Largest dynamic shared memory that a kernel has been allowed on each device.
-struct SmemLimit {
-  std::atomic<int> bytes[kMaxLaunchDevices];
-  template <typename K>
-  cudaError_t raise(K kernel, int dev, int want) {
-    if (want <= bytes[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
-    if (e == cudaSuccess) bytes[dev].store(want, std::memory_order_relaxed);
-    return e;
-  }
-};
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args&&... args) {
