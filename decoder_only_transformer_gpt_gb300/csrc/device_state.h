@@ -42,4 +42,33 @@ struct SmemLimit {
   }
 };
 
+// One int of device memory per device, 0 when it is made, which the kernels launched there may write. The first caller on
+// a device makes it; nullptr (and no CUDA error left behind) where that fails.
+struct DeviceWord {
+  std::atomic<int*> word[kMaxLaunchDevices];
+  std::mutex mu;
+  int* get() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return failed();
+    if (dev < 0 || dev >= kMaxLaunchDevices) return nullptr;
+    if (int* p = word[dev].load(std::memory_order_acquire)) return p;
+    std::lock_guard<std::mutex> lk(mu);
+    if (int* p = word[dev].load(std::memory_order_relaxed)) return p;
+    void* p = nullptr;
+    if (cudaMalloc(&p, sizeof(int)) != cudaSuccess) return failed();
+    if (cudaMemset(p, 0, sizeof(int)) != cudaSuccess) {
+      cudaFree(p);
+      return failed();
+    }
+    word[dev].store(static_cast<int*>(p), std::memory_order_release);
+    return static_cast<int*>(p);
+  }
+
+ private:
+  static int* failed() {
+    cudaGetLastError();
+    return nullptr;
+  }
+};
+
 }  // namespace gptgb

@@ -1,6 +1,7 @@
 // Per-step entry points (include/gpt_kernels.h): one kernel of the forward pass
 // on caller-owned device buffers.
 #include "../../include/gpt_kernels.h"
+#include "device_state.h"
 #include "model.h"
 
 #include <cuda_runtime.h>
@@ -11,17 +12,9 @@ using namespace gptgb;
 
 namespace {
 
-int* g_err = nullptr;
-std::mutex g_err_mu;
+DeviceWord g_err;   // the current device's error word: kernels of several devices may run at once
 
-int* err_word() {
-  std::lock_guard<std::mutex> lk(g_err_mu);
-  if (!g_err) {
-    if (cudaMalloc(&g_err, sizeof(int)) != cudaSuccess) { g_err = nullptr; return nullptr; }
-    if (cudaMemset(g_err, 0, sizeof(int)) != cudaSuccess) return nullptr;
-  }
-  return g_err;
-}
+int* err_word() { return g_err.get(); }
 
 int num_sms() {
   int dev = 0, n = 0;
@@ -38,8 +31,7 @@ int* gptgb::step_err_word() { return err_word(); }
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-cudaMemPool_t g_pools[kMaxDevices] = {};
+cudaMemPool_t g_pools[kMaxLaunchDevices] = {};
 std::mutex g_pool_mu;
 
 // The current device's scratch pool, made by its first user.
@@ -47,7 +39,7 @@ cudaError_t scratch_pool(cudaMemPool_t* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= kMaxLaunchDevices) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(g_pool_mu);
   if (!g_pools[dev]) {
     cudaMemPoolProps props = {};

@@ -5,8 +5,9 @@
  * launches) on caller-owned device buffers, so that every step can be checked
  * on its own against the definitions it implements. All pointers are device
  * pointers, 16-byte aligned; all calls are stream-ordered and asynchronous.
- * Device-side errors (out-of-range ids, expired waits) are recorded in a
- * library-wide device error word that gptk_status() reads and clears.
+ * Device-side errors (out-of-range ids, expired waits) are recorded in an error
+ * word of the current device, which gptk_status() reads and clears with that
+ * device current.
  *
  * dtype selects the arithmetic: 0 = fp32 SIMT kernels (fp32 operands),
  * 1 = bf16 operands on the tcgen05 tensor-core kernels with fp32 accumulation.
@@ -104,7 +105,7 @@ int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int3
  * dqkv [B, T, (H + 2 Hkv) D]: dQ, and dK and dU summed over the H / Hkv query heads of a key head. Rows behind a
  * padded sequence's end take no part where their dy is zero. dqkv overlaps no input. Scratch (4 B T H (D + 2) bytes and
  * a little, and 1 KB x D for each part of a key tile that several CTAs share, a few hundred at most) is taken on the
- * stream from a pool that the library keeps; make a process's first call before any stream capture. dQ's fp32 additions
+ * stream from a pool that the library keeps; make a process's first call on a device before any stream capture. dQ's fp32 additions
  * come in an order that varies between runs.
  */
 int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, const float* lse2, void* dqkv, int32_t B,
@@ -219,7 +220,7 @@ int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int3
 /* Deterministic mean of nll[0..M) into *loss (device fp32). */
 int gptk_mean(const float* nll, int32_t M, float* loss, void* stream);
 
-/* Synchronise the stream, then read and clear the per-step device error word. */
+/* Synchronise the stream, then read and clear the current device's per-step error word. */
 int gptk_status(void* stream);
 
 #ifdef __cplusplus

@@ -96,3 +96,64 @@ int main() {
   need(device_sms(&dev, &n) == cudaErrorInvalidDevice, "device past the table");
 }
 """)
+
+
+def test_every_device_has_its_own_word(tmp_path):
+    # a kernel that runs on one device must not be given another device's memory, however many threads ask first; what
+    # cannot be made whole is asked for again by the next caller
+    _run(tmp_path, r"""
+#include <set>
+#include <vector>
+struct Piece { int dev, value; };
+static std::mutex m;
+static std::set<Piece*> pieces;
+static int fail_malloc = 0, fail_memset = 0, errors = 0;
+extern "C" cudaError_t cudaMalloc(void** p, size_t n) {
+  std::lock_guard<std::mutex> lk(m);
+  if (fail_malloc && fail_malloc--) { ++errors; return cudaErrorMemoryAllocation; }
+  need(n == sizeof(int), "size");
+  Piece* x = new Piece{t_dev, 77};
+  pieces.insert(x);
+  *p = x;
+  return cudaSuccess;
+}
+extern "C" cudaError_t cudaMemset(void* p, int v, size_t n) {
+  std::lock_guard<std::mutex> lk(m);
+  if (fail_memset && fail_memset--) { ++errors; return cudaErrorInvalidValue; }
+  need(v == 0 && n == sizeof(int), "cleared");
+  static_cast<Piece*>(p)->value = 0;
+  return cudaSuccess;
+}
+extern "C" cudaError_t cudaFree(void* p) {
+  std::lock_guard<std::mutex> lk(m);
+  need(pieces.erase(static_cast<Piece*>(p)) == 1, "freed twice");
+  return cudaSuccess;
+}
+extern "C" cudaError_t cudaGetLastError() { errors = 0; return cudaSuccess; }
+int main() {
+  static DeviceWord word;
+  fail_malloc = fail_memset = 1;
+  need(word.get() == nullptr && errors == 0 && pieces.empty(), "no memory");
+  need(word.get() == nullptr && errors == 0 && pieces.empty(), "not cleared");
+  std::vector<std::thread> threads;
+  std::vector<int*> got(32);
+  for (int i = 0; i < 32; ++i)
+    threads.emplace_back([&got, i] { t_dev = i % 2 ? 5 : 0; got[i] = word.get(); });
+  for (auto& t : threads) t.join();
+  for (int i = 0; i < 32; ++i) {
+    const Piece* p = reinterpret_cast<const Piece*>(got[i]);
+    need(p && p->dev == (i % 2 ? 5 : 0) && p->value == 0 && got[i] == got[i % 2], "this device's word");
+  }
+  need(pieces.size() == 2, "one per device");
+  t_dev = 64;
+  need(word.get() == nullptr, "device past the table");
+}
+""")
+
+
+def test_the_library_takes_its_error_word_by_device():
+    # the per-step entries have no word of their own beside it
+    import re
+    from decoder_only_transformer_gpt_gb300 import build
+    text = open(os.path.join(build.CSRC, "gptk.cu")).read()
+    assert re.search(r"DeviceWord g_err;", text) and "cudaMalloc(&g_err" not in text
