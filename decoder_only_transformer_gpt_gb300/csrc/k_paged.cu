@@ -71,7 +71,7 @@ paged_store_kernel(PagedCache c, const uint4* __restrict__ qkv, const int32_t* _
   __shared__ long long s_row[kStoreTokens];          // row (of D elements) of the token's key of head 0; -1: nowhere
   __shared__ long long s_weight[kStoreTokens];
   const int b = blockIdx.y, t0 = blockIdx.x * kStoreTokens;
-  const int n = (count ? min(__ldg(count + b), T) : T) - t0;          // tokens from t0 on
+  const int n = (count ? min(max(__ldg(count + b), 0), T) : T) - t0;  // tokens from t0 on; a count below 0 is 0
   if (n <= 0) return;
   if (threadIdx.x < kStoreTokens) {
     long long row = -1, weight = 0;

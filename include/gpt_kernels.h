@@ -176,8 +176,8 @@ int gptk_lmhead_ce_noalloc(const void* h, const void* wte, const int32_t* target
  * GPT_EPAGE (what the call wrote for that sequence is unspecified).
  *
  * gptk_paged_store: rows start[b] + t of sequence b take the keys and values of qkv[b][t] ([B, T, (H + 2 Hkv) D])
- * for t < count[b]; their weights become 0. start NULL: 0; count NULL: T (more than T counts as T). No two of the
- * stored rows may share a place.
+ * for t < count[b]; their weights become 0. start NULL: 0; count NULL: T (more than T counts as T, less than 0 as 0).
+ * No two of the stored rows may share a place.
  */
 int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* table, const int32_t* start,
                      const int32_t* count, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t D, int32_t pages,

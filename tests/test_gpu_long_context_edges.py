@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 
 import paged_ref  # noqa: E402
 import test_gpu_window as gw  # noqa: E402
-from gpu_util import dev_bf16, host  # noqa: E402
+from gpu_util import dev_bf16, dev_i32, host  # noqa: E402
 from test_gpu_paged import LOG2E, Case  # noqa: E402
 from test_gpu_paged_forms import widened  # noqa: E402
 
@@ -65,3 +65,16 @@ def test_raised_reference_keeps_probabilities(gpt_lib, B, D):
     from decoder_only_transformer_gpt_gb300 import binding
     binding.status()
     gw._check(qkv, np.zeros((B, T, H * D), np.float32), y, lse2, None, H, H, window, 0, only=None if B == 1 else {(7, h) for h in range(H)})
+
+
+def test_store_of_counts_far_below_zero(gpt_lib):
+    # a count below zero stores nothing, the lowest int32 too: count - 16, for a block's first token, would wrap around
+    from decoder_only_transformer_gpt_gb300 import binding
+    B, T, H, D, page = 4, 77, 2, 32, 8
+    pool = torch.full((B * 10, 2, 1, page, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    weight = torch.ones(B * 10, 1, page, device="cuda")
+    qkv = torch.ones(B, T, (H + 2) * D, dtype=torch.bfloat16, device="cuda")
+    count = dev_i32(np.array([-2 ** 31, -2 ** 31 + 20, -1, -2 ** 31], np.int32))
+    binding.paged_store(qkv, pool, dev_i32(np.arange(B * 10).reshape(B, 10)), H, count=count, weight=weight)
+    binding.status()
+    assert torch.all(pool == 3.0) and torch.all(weight == 1.0)
