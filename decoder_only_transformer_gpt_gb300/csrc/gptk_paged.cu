@@ -17,7 +17,7 @@ int paged_cache(PagedCache* c, const void* pool, const float* weight, const int3
                 int32_t D, int32_t pages, int32_t page, int32_t max_pages) {
   if (!pool || !table || B < 1 || Hkv < 1 || D < 1 || pages < 1 || max_pages < 1) return GPT_EINVAL;
   if (page < 8 || page > 256 || (page & (page - 1))) return GPT_EINVAL;
-  if (static_cast<int64_t>(max_pages) * page > 0x7fffffffLL - 1) return GPT_EINVAL;
+  if (static_cast<int64_t>(max_pages) * page > kPagedMaxRows) return GPT_EINVAL;
   if (B > kPagedMaxB || Hkv > 65535) return GPT_EINVAL;
   if ((D != 32 && D != 64) || !aligned16(pool)) return GPT_ECONFIG;
   int lg = 0;
@@ -81,7 +81,7 @@ int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int3
                      int32_t max_pages, int32_t dst_max_pages, int32_t budget, int32_t sinks, int32_t recent,
                      void* stream) {
   if (!weight || !lens || !dst_table || !new_lens || !kept || new_lens == lens) return GPT_EINVAL;
-  if (dst_max_pages < 1 || budget < 1 || sinks < 0 || recent < 0) return GPT_EINVAL;
+  if (dst_max_pages < 1 || budget < 1 || budget > kPagedMaxRows || sinks < 0 || recent < 0) return GPT_EINVAL;
   if (static_cast<int64_t>(sinks) + recent > budget) return GPT_EINVAL;
   PagedCache c;
   const int rc = paged_cache(&c, pool, weight, table, B, Hkv, D, pages, page, max_pages);

@@ -232,6 +232,9 @@ cudaError_t scratch_free(void* p, cudaStream_t s);
 // [pages][Hkv][page]: one running sum of attention weight per cached row and key head.
 constexpr int kPagedMaxB = 8192;       // sequences of a call (their lengths are held in shared memory)
 constexpr int kPagedMaxGroup = 128;    // query heads per key head of paged attention
+// Rows that a table may have room for, and rows that an eviction may keep: the kernels number rows with 32 bits and step
+// up to 4,095 beyond the last one before they compare.
+constexpr int64_t kPagedMaxRows = 0x7fffffff - 4095;
 struct PagedCache {
   void* pool;
   float* weight;

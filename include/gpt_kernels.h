@@ -170,7 +170,8 @@ int gptk_lmhead_ce_noalloc(const void* h, const void* wte, const int32_t* target
  * page is a power of two, 8..256. H query heads share Hkv key heads (H a multiple of Hkv): query head h reads key
  * head h / (H / Hkv), H / Hkv <= 128 for the attention. A token's qkv row holds H D queries, Hkv D keys, Hkv D values,
  * as the output of one product (less than 2^30 elements).
- * All arrays are device memory of the current device, pool, qkv and y 16-byte aligned. B <= 8192.
+ * All arrays are device memory of the current device, pool, qkv and y 16-byte aligned. B <= 8192, max_pages * page <=
+ * 2^31 - 4096.
  * GPT_EINVAL: null pointers or sizes; GPT_ECONFIG: D, H % Hkv or alignment. Checked on the device: a page number
  * outside [0, pages) or a row past max_pages * page is neither read nor written, and gptk_status() then returns
  * GPT_EPAGE (what the call wrote for that sequence is unspecified).
@@ -206,7 +207,7 @@ int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32
  * Eviction by summed attention weight, for every sequence and key head by itself: of rows 0..lens[b]-1 keeps the
  * first `sinks`, the last `recent`, and between them the rows of the largest weight, budget rows in all (every row
  * where lens[b] <= budget; equal weights: the lowest rows; a NaN weight counts as the smallest; sinks + recent <=
- * budget). The kept rows, their weights with them, become rows 0.. of dst_table [B][dst_max_pages] in their order;
+ * budget <= 2^31 - 4096). The kept rows, their weights with them, become rows 0.. of dst_table [B][dst_max_pages] in their order;
  * kept[b][head][i] (int32 [B, Hkv, budget]) is the row that row i was, -1 behind the last; new_lens[b] =
  * min(lens[b], budget) (lens[b] itself where it is negative; new_lens must not be lens). dst_table either is
  * `table`, or starts every sequence with the same pages (in place), or names pages that no sequence of `table`
