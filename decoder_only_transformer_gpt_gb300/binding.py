@@ -103,6 +103,7 @@ def load(path: str = LIB_PATH):
         "gptk_paged_attention": (ctypes.c_int, [vp] * 7 + [i32] * 9 + [vp]),
         "gptk_paged_evict": (ctypes.c_int, [vp] * 7 + [i32] * 10 + [vp]),
         "gptk_mean": (ctypes.c_int, [vp, i32, vp, vp]),
+        "gptk_scratch_trim": (ctypes.c_int, [ctypes.c_uint64]),
         "gptk_status": (ctypes.c_int, [vp]),
     }
     for name, (res, args) in sigs.items():
@@ -524,6 +525,13 @@ def paged_evict(pool, weight, table, lens, dst_table, new_lens, kept, budget: in
                               B, Hkv, D, pages, page, max_pages, dst_pages, budget, sinks, recent, s)
     if rc:
         _check(rc, "gptk_paged_evict")
+
+
+def scratch_trim(keep: int = 0) -> None:
+    """Give the current device's scratch of finished calls back, down to `keep` bytes (synchronise first)."""
+    if not 0 <= keep < 2 ** 64:
+        raise ValueError(f"keep: {keep}, needs a number of bytes")
+    _check(load().gptk_scratch_trim(keep), "gptk_scratch_trim")
 
 
 def mean(nll, loss, stream=None):

@@ -34,7 +34,9 @@ namespace {
 cudaMemPool_t g_pools[kMaxLaunchDevices] = {};
 std::mutex g_pool_mu;
 
-// The current device's scratch pool, made by its first user.
+// The current device's scratch pool, made by its first user. It keeps what is freed until gptk_scratch_trim(): a call that
+// takes 2 GiB and is waited for lasted 0.56 ms, and 2.9 ms with a pool that gave all but a gibibyte back at every
+// synchronisation.
 cudaError_t scratch_pool(cudaMemPool_t* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -336,6 +338,16 @@ int gptk_lmhead_ce(const void* h, const void* wte, const int32_t* targets, float
 int gptk_mean(const float* nll, int32_t M, float* loss, void* stream) {
   if (!nll || !loss || M < 1) return GPT_EINVAL;
   GPT_CUDA(launch_mean(nll, M, M, loss, reinterpret_cast<cudaStream_t>(stream)));
+  return GPT_OK;
+}
+
+int gptk_scratch_trim(uint64_t keep) {
+  int dev = 0;
+  GPT_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= kMaxLaunchDevices) return GPT_EINVAL;
+  std::lock_guard<std::mutex> lk(g_pool_mu);
+  if (!g_pools[dev]) return GPT_OK;
+  GPT_CUDA(cudaMemPoolTrimTo(g_pools[dev], static_cast<size_t>(keep)));
   return GPT_OK;
 }
 

@@ -221,6 +221,14 @@ int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int3
 /* Deterministic mean of nll[0..M) into *loss (device fp32). */
 int gptk_mean(const float* nll, int32_t M, float* loss, void* stream);
 
+/*
+ * Gives memory of the current device's scratch pool back to the device, down to `keep` bytes. The pool serves the calls
+ * above whose comments name it and keeps what they have freed, so that the next call does not map it anew; the largest
+ * call's scratch therefore stays with the process until this is called. Only memory of calls that have been waited for
+ * is given back (synchronise first); a captured graph's scratch is the graph's own. GPT_OK also where there is no pool.
+ */
+int gptk_scratch_trim(uint64_t keep);
+
 /* Synchronise the stream, then read and clear the current device's per-step error word. */
 int gptk_status(void* stream);
 

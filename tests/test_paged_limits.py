@@ -24,3 +24,10 @@ def test_rows_that_an_eviction_keeps(lib):  # noqa: F811
     from decoder_only_transformer_gpt_gb300 import binding
     for budget in (2 ** 31 - 1, 2 ** 31 - 2048, MOST + 1):
         assert _evict(lib, budget=budget, dst_max_pages=2 ** 27, sinks=0, recent=0) == binding.GPT_EINVAL, budget
+
+
+def test_scratch_is_trimmed_to_a_number_of_bytes(lib):  # noqa: F811
+    from decoder_only_transformer_gpt_gb300 import binding
+    for keep in (-1, 2 ** 64):
+        with pytest.raises(ValueError, match="keep"):
+            binding.scratch_trim(keep)
