@@ -554,7 +554,7 @@ paged_split_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
         if (r >= gn) continue;
         if (whole) {
           const size_t head = static_cast<size_t>(at.b) * w.H + kh * w.G + g0 + r;
-          const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+          const float inv = 1.0f / lt;               // (a sum of 0, every score -inf, gives NaN)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
             *reinterpret_cast<uint32_t*>(y + head * D + 8 * j + qcol) = pack_bf16x2(o[j][2 * rh] * inv, o[j][2 * rh + 1] * inv);
@@ -782,7 +782,7 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
     float acc = 0.0f;
     for (int k = 0; k < NB; ++k) acc += s_o[r / NB * NB + k][d] * ex2_approx(s_all[k][r].x - ref);
     const size_t head = static_cast<size_t>(b) * w.H + kh * w.G + g0 + r;
-    y[head * D + d] = __float2bfloat16(lt == 0.0f ? 0.0f : acc / lt);
+    y[head * D + d] = __float2bfloat16(acc / lt);
     if (d == 0 && lse2) lse2[head] = mx + log2f(lt);
   }
   if (!c.weight) return;
@@ -793,7 +793,7 @@ paged_short_kernel(PagedCache c, const __nv_bfloat16* __restrict__ qkv, const in
     if (qrow + 8 * rh < gn) {
       float lt;
       const float mx = joined(qrow + 8 * rh, &lt);
-      f[rh] = m[rh] == -INFINITY ? 0.0f : ex2_approx(m[rh] - mx) / lt;
+      f[rh] = ex2_approx(m[rh] - mx) / lt;
     }
 #pragma unroll
   for (int t = 0; t < UPW; ++t) {
@@ -904,7 +904,7 @@ paged_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16*
           lt += s_l[part + k] * f;
           at += s_o[part + k][d] * f;
         }
-        if (blockIdx.y == 0) y[(head0 + r) * D + d] = __float2bfloat16(lt == 0.0f ? 0.0f : at / lt);
+        if (blockIdx.y == 0) y[(head0 + r) * D + d] = __float2bfloat16(at / lt);
         if (d == 0) {
           const float lse = mx + log2f(lt);
           s_lse[mt * 16 + r] = lse;

@@ -197,7 +197,8 @@ int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* 
  * before any stream capture. The caller counts lens up (one cache per layer
  * shares one lens). Sequences may share the pages of rows below their own; the new rows' pages are their own. fp32
  * scores and sums; the probabilities enter the product with the values in two bf16 parts (2^-16 of each at most is
- * lost). y overlaps no input.
+ * lost). A NaN in sight makes the outputs and weights of its queries NaN, and so do scores that are all -inf (products past
+ * fp32's range; lse2 is -inf then). y overlaps no input.
  */
 int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32_t* table, const int32_t* lens, void* y,
                          float* lse2, int32_t B, int32_t H, int32_t Hkv, int32_t D, int32_t pages, int32_t page,

@@ -78,3 +78,25 @@ def test_store_of_counts_far_below_zero(gpt_lib):
     binding.paged_store(qkv, pool, dev_i32(np.arange(B * 10).reshape(B, 10)), H, count=count, weight=weight)
     binding.status()
     assert torch.all(pool == 3.0) and torch.all(weight == 1.0)
+
+
+@pytest.mark.parametrize("rows", [1024, 4096, 65536])
+@pytest.mark.parametrize("H,Hkv,length", [(2, 2, 700), (12, 1, 700), (40, 2, 700), (2, 2, 20)])
+def test_scores_of_minus_infinity(gpt_lib, rows, H, Hkv, length):
+    # products past fp32's range: every score of the first key head's queries is -inf, their softmax 0 / 0
+    from decoder_only_transformer_gpt_gb300 import binding
+    D, G = 64, H // Hkv
+    c = Case(H, Hkv, D, 16, [length, 40], seed=rows)
+    x = c.qkv.reshape(2, H + 2 * Hkv, D)
+    x[0, :G], x[0, H] = 3e38, -3e38
+    for r in range(length):
+        p, s = c.table[0, r // 16], r % 16
+        c.pool[p, 0, 0, s] = -3e38
+    widened(c, rows)
+    c.call()
+    binding.status()
+    y, lse2, w = host(c.d_y).reshape(2, H, D), host(c.d_lse2), host(c.d_weight)
+    assert np.isnan(y[0, :G]).all() and np.isfinite(y[0, G:]).all() and np.isfinite(y[1]).all()
+    assert np.all(lse2[0, :G] == -np.inf) and np.isfinite(lse2[0, G:]).all() and np.isfinite(lse2[1]).all()
+    seen = np.stack([w[c.table[0, r // 16], :, r % 16] for r in range(length + 1)])
+    assert np.isnan(seen[:, 0]).all() and np.isfinite(seen[:, 1:]).all()
