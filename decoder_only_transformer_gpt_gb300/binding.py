@@ -368,22 +368,28 @@ def lmhead_ce_noalloc(h, wte, targets, nll, err=None, stream=None):
 # The operators below are called per layer and token, so their checks are kept to attribute reads (about 0.4 us a
 # tensor; 8 us of the call's host time went to them and the stream object in a first form).
 
-_torch = None
+_torch = _device = _raw_stream = None
 _cuda_up = False
 
 
 def _cuda(stream):
     """(torch, the current device's index, the stream to launch on as an integer)."""
-    global _torch, _cuda_up
+    global _torch, _device, _raw_stream, _cuda_up
     if not _cuda_up:
         import torch
         _torch = torch
+        # what the public functions call, without the objects that they make; they themselves where torch has no such name
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
         _cuda_up = torch.cuda.is_initialized()
         if not _cuda_up:                             # no tensor can be on a GPU yet
             return torch, 0, 0
-    c = _torch._C
-    dev = c._cuda_getDevice()
-    return _torch, dev, c._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    dev = _device()
+    if stream is None:
+        return _torch, dev, _raw_stream(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream: of device {stream.device_index}, needs one of the current device {dev}")
+    return _torch, dev, stream.cuda_stream
 
 
 def _refuse(name: str, t, dtype, shape, dev) -> None:
