@@ -14,7 +14,7 @@ def cuda(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 7, raising=False)
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
-    monkeypatch.setattr(binding, "_cuda_up", False)
+    binding._cuda_up = False                                             # asks torch again, here and after the test
     yield binding._cuda
     binding._cuda_up = False
 
