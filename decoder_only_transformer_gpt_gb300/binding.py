@@ -498,8 +498,9 @@ def paged_attention(qkv, pool, table, lens, y, H: int, lse2=None, weight=None, w
                     stream=None):
     """One new token per sequence, qkv [B, (H + 2 Hkv) D]: stored at row lens[b], its attention in y [B, H D].
 
-    window 0 sees every cached row, else the last `window` rows and the first `sinks`; weight (optional) sums
-    each row's attention weight, lse2 [B, H] (optional) takes the log-sum-exp. lens[b] < 0 skips row b."""
+    window 0 sees every cached row, else the last `window` rows and the first `sinks` (rows as the cache holds them: after
+    an eviction they reach further back in the text); weight (optional) sums each row's attention weight, lse2 [B, H]
+    (optional) takes the log-sum-exp. lens[b] < 0: the outputs, cache and weights of row b stay as they were."""
     if (window | sinks) >> 31 not in (0, -1):
         _int32(window=window, sinks=sinks)
     lib = _LIB or load()

@@ -103,10 +103,10 @@ int gptk_attention_window(const void* qkv, void* y, float* lse2, int32_t B, int3
 /*
  * Its derivative: from qkv, y and lse2 of gptk_attention_window (the same window and sinks) and dy [B, T, H D], writes
  * dqkv [B, T, (H + 2 Hkv) D]: dQ, and dK and dU summed over the H / Hkv query heads of a key head. Rows behind a
- * padded sequence's end take no part where their dy is zero. dqkv overlaps no input. Scratch (4 B T H (D + 2) bytes and
- * a little, and 1 KB x D for each part of a key tile that several CTAs share, a few hundred at most) is taken on the
- * stream from a pool that the library keeps; make a process's first call on a device before any stream capture. dQ's fp32 additions
- * come in an order that varies between runs.
+ * padded sequence's end take no part where their dy is zero. dqkv overlaps no input. Scratch (4 B T H D bytes, 1,024 B H
+ * for each 128 rows of T or part of them, and 1,024 D for each part of a key tile that several CTAs share, a few hundred at
+ * most) is taken on the stream from a pool that the library keeps; make a process's first call on a device before any
+ * stream capture. dQ's fp32 additions come in an order that varies between runs.
  */
 int gptk_attention_window_bwd(const void* qkv, const void* y, const void* dy, const float* lse2, void* dqkv, int32_t B,
                               int32_t T, int32_t H, int32_t Hkv, int32_t D, int32_t window, int32_t sinks, void* stream);
@@ -191,14 +191,17 @@ int gptk_paged_store(const void* qkv, void* pool, float* weight, const int32_t* 
  *   y[b, h] = sum_r a_r u_r,  a = softmax(q_h . k_r / sqrt(D))     bf16 [B, H D]
  *   lse2[b, h] = log2 sum_r 2^(q_h . k_r log2(e) / sqrt(D))         fp32 [B, H], NULL: not wanted
  *   weight(r, key head) += the sum of a_r over the head's H / Hkv queries (r < n); = that sum for row n
- * lens[b] < 0: no sequence; nothing of row b is read or written. B max_pages page / 32 < 2^31, and times Hkv
- * <= 2^40 (GPT_EINVAL otherwise). Scratch (none where the table, or the window and sinks, hold few rows; else about
- * 10 MB at most, and with weights 4 bytes per query head and seen row that the table has room for) is taken on the stream from a pool that the library keeps; make a process's first call
- * before any stream capture. The caller counts lens up (one cache per layer
- * shares one lens). Sequences may share the pages of rows below their own; the new rows' pages are their own. fp32
- * scores and sums; the probabilities enter the product with the values in two bf16 parts (2^-16 of each at most is
- * lost). A NaN in sight makes the outputs and weights of its queries NaN, and so do scores that are all -inf (products past
- * fp32's range; lse2 is -inf then). y overlaps no input.
+ * lens[b] < 0: no sequence; row b of the outputs, the cache and the weights stay as they were (qkv[b] and the entries of
+ * table[b] may be read, and count for nothing). B max_pages page / 32 < 2^31, and times Hkv <= 2^40 (GPT_EINVAL otherwise).
+ * The window counts cached rows. An eviction numbers the rows that it keeps anew, so a window over such a cache reaches
+ * further back in the text than over a whole one.
+ * Scratch (none where the table, or the window and sinks, hold few rows; else about 10 MB and 4 B (H + 1) bytes at most,
+ * and with weights 4 B H bytes for each row that the table, or the window and sinks, have room for, whatever the lengths)
+ * is taken on the stream from a pool that the library keeps; make a process's first call on a device before any stream
+ * capture. The caller counts lens up (one cache per layer shares one lens). Sequences may share the pages of rows below
+ * their own; the new rows' pages are their own. fp32 scores and sums; the probabilities enter the product with the values
+ * in two bf16 parts (2^-16 of each at most is lost). A NaN in sight makes the outputs and weights of its queries NaN, and
+ * so do scores that are all -inf (products past fp32's range; lse2 is -inf then). y overlaps no input.
  */
 int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32_t* table, const int32_t* lens, void* y,
                          float* lse2, int32_t B, int32_t H, int32_t Hkv, int32_t D, int32_t pages, int32_t page,
@@ -207,12 +210,12 @@ int gptk_paged_attention(const void* qkv, void* pool, float* weight, const int32
 /*
  * Eviction by summed attention weight, for every sequence and key head by itself: of rows 0..lens[b]-1 keeps the
  * first `sinks`, the last `recent`, and between them the rows of the largest weight, budget rows in all (every row
- * where lens[b] <= budget; equal weights: the lowest rows; a NaN weight counts as the smallest; sinks + recent <=
- * budget <= 2^31 - 4096). The kept rows, their weights with them, become rows 0.. of dst_table [B][dst_max_pages] in their order;
- * kept[b][head][i] (int32 [B, Hkv, budget]) is the row that row i was, -1 behind the last; new_lens[b] =
- * min(lens[b], budget) (lens[b] itself where it is negative; new_lens must not be lens). dst_table either is
- * `table`, or starts every sequence with the same pages (in place), or names pages that no sequence of `table`
- * holds, each once; the old rows then stay as they were. In place no page may be held by two sequences.
+ * where lens[b] <= budget; sinks + recent <= budget <= 2^31 - 4096). Equal weights, as after a store alone, which sets
+ * them to 0: the lowest rows are kept; a NaN weight counts as the smallest. The kept rows, their weights with them, become
+ * rows 0.. of dst_table [B][dst_max_pages] in their order; kept[b][head][i] (int32 [B, Hkv, budget]) is the row that row i
+ * was, -1 behind the last; new_lens[b] = min(lens[b], budget) (lens[b] itself where it is negative; new_lens must not be
+ * lens). dst_table either is `table`, or starts every sequence with the same pages (in place), or names pages that no
+ * sequence of `table` holds, each once; the old rows then stay as they were. In place no page may be held by two sequences.
  */
 int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int32_t* lens, const int32_t* dst_table,
                      int32_t* new_lens, int32_t* kept, int32_t B, int32_t Hkv, int32_t D, int32_t pages, int32_t page,
