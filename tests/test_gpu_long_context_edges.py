@@ -100,3 +100,23 @@ def test_scores_of_minus_infinity(gpt_lib, rows, H, Hkv, length):
     assert np.all(lse2[0, :G] == -np.inf) and np.isfinite(lse2[0, G:]).all() and np.isfinite(lse2[1]).all()
     seen = np.stack([w[c.table[0, r // 16], :, r % 16] for r in range(length + 1)])
     assert np.isnan(seen[:, 0]).all() and np.isfinite(seen[:, 1:]).all()
+
+
+@pytest.mark.parametrize("B,T", [(1, 700), (12, 700)])
+@pytest.mark.parametrize("what", ["sinks high", "sinks low", "first of 32 high", "first of 32 low"])
+@pytest.mark.parametrize("D", [32, 64])
+def test_derivative_with_scores_far_from_the_rest(gpt_lib, B, T, what, D):
+    # the inputs of the forward's test: log-sum-exps of hundreds, from which the derivative makes the probabilities again
+    H, window, sinks = 4, 200, 6
+    qkv, dy = gw._inputs(B, T, H, H, D, seed=T)
+    q, k = qkv[..., :H * D], qkv[..., H * D:2 * H * D]
+    q[...] = np.abs(q)
+    rows = slice(0, sinks) if what.startswith("sinks") else slice(0, T, 32)
+    k[:, rows] = np.abs(k[:, rows]) * (8.0 if what.endswith("high") else -8.0)
+    qkv = host(dev_bf16(qkv)).astype(np.float32)
+    x = dev_bf16(qkv)
+    y, lse2 = gw._forward(x, H, H, window, sinks)
+    dqkv = gw._backward(x, y, dev_bf16(dy), lse2, H, H, window, sinks)
+    from decoder_only_transformer_gpt_gb300 import binding
+    binding.status()
+    gw._check(qkv, dy, y, lse2, dqkv, H, H, window, sinks, only={(0, 0), (B - 1, 3)})
