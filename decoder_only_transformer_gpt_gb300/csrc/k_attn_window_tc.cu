@@ -34,9 +34,9 @@
 //
 // Softmax: per row one running reference m and sum. The reference starts as the score of the warp's first diagonal key
 // where all its rows see that (W >= 32), else as the exact maximum of the first half tile in which the row sees a key;
-// it is raised only when a half tile's sum passes 2^16 and the maximum grew by more than 2^8. References are whole numbers,
-// so a raise rescales sum, output and the tile's rounded probabilities by a power of two, which is exact. Sums are fp32; P
-// is rounded to bf16 once, for the second product (the type the tensor core multiplies), which costs at most 2^-8 of
+// it is raised only when a half tile's sum passes 2^16 and the maximum grew by more than 2^8, and by a whole number, so that
+// sum, output and the tile's rounded probabilities are rescaled by a power of two, which is exact. Sums are fp32; P is
+// rounded to bf16 once, for the second product (the type the tensor core multiplies), which costs at most 2^-8 of
 // sum a |u|.
 //
 // Taken back, at the 12,001 tokens above as they were then: tiles of 64 keys in six score buffers (157 us against 151),
@@ -247,10 +247,10 @@ __device__ __forceinline__ void load_chunk(uint32_t col, uint32_t (&v)[64]) {
 // The two rare steps of a softmax warp, out of line: inlined they took the registers and the instruction cache of the
 // loop that turns scores into probabilities.
 
-// Row references: the maximum of a chunk's seen keys, rounded to a whole number, becomes the reference of a row that had
-// none, or that it passes by more than 2^8; then the running sum, the output so far (unless the item starts here) and the
-// tile's probabilities so far (n_p columns of 16 at tS) are rescaled, by a power of two. `prev`: the group's previous
-// score tile.
+// Row references: the exact maximum of a chunk's seen keys becomes the reference of a row that had none. A reference that
+// it passes by more than 2^8 rises by the next whole number of steps (to the rounding of the fp32 sum, as that of a score
+// of its size); the running sum, the output so far (unless the item starts here) and the tile's probabilities so far (n_p
+// columns of 16 at tS) are rescaled, by a power of two. `prev`: the group's previous score tile.
 struct RowRef {
   float mr, l;
   bool ok;
@@ -268,12 +268,12 @@ __device__ __noinline__ RowRef raise_reference(AttnBars* bars, uint32_t tSc, uin
     mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], (seen >> (i & 31)) & 1u ? __uint_as_float(v[i]) : -INFINITY,
                              (seen >> ((i + 1) & 31)) & 1u ? __uint_as_float(v[i + 1]) : -INFINITY);
   }
-  const float m_max = fmaxf(mr, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2), m_new = rintf(m_max);
+  const float m_max = fmaxf(mr, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2);
   const bool fresh = mr == -INFINITY;                // l and the row's outputs are zero
   const bool need = m_max > mr + kRescaleLog2;       // (true for a fresh row that sees a key here)
-  const float drop = mr - m_new;                     // whole; 2^drop from its exponent bits
-  const float alpha = !need || fresh ? 1.0f : drop < -126.0f ? 0.0f : __int_as_float((127 + static_cast<int>(drop)) << 23);
-  RowRef out = {need ? m_new : mr, l * alpha, true};
+  const float up = need && !fresh ? ceilf(m_max - mr) : 0.0f;
+  const float alpha = up > 126.0f ? 0.0f : __int_as_float((127 - static_cast<int>(up)) << 23);   // 2^-up
+  RowRef out = {!need ? mr : fresh ? m_max : mr + up, l * alpha, true};
   if (__any_sync(0xffffffffu, need && !fresh)) {
     if (!first) {
       // every earlier P U of the group has completed
@@ -682,7 +682,7 @@ attn_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_const
             uint32_t own[1];
             tmem_ld_32x32b_x1(tS + wrow, own);
             tmem_loaded(own);
-            mr = rintf(__uint_as_float(own[0]) * scale_log2);
+            mr = __uint_as_float(own[0]) * scale_log2;
             ready = true;
           }
           const float2 nm2 = make_float2(-mr, -mr);

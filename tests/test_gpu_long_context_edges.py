@@ -67,6 +67,21 @@ def test_raised_reference_keeps_probabilities(gpt_lib, B, D):
     gw._check(qkv, np.zeros((B, T, H * D), np.float32), y, lse2, None, H, H, window, 0, only=None if B == 1 else {(7, h) for h in range(H)})
 
 
+@pytest.mark.parametrize("D", [32, 64])
+@pytest.mark.parametrize("B,T,window", [(1, 300, 1), (40, 300, 1), (3, 5, 64), (40, 129, 40)])
+def test_a_row_that_sees_one_key_copies_its_value(gpt_lib, B, T, window, D):
+    # its probability is 1 in every type, and the sum it is divided by
+    H = 4
+    qkv, _ = gw._inputs(B, T, H, H, D, seed=T)
+    y, lse2 = gw._forward(dev_bf16(qkv), H, H, window, 0)
+    n = T if window == 1 else 1
+    assert torch.equal(y[:, :n], dev_bf16(qkv)[:, :n, 2 * H * D:])
+    x = qkv.astype(np.float64).reshape(B, T, 3, H, D)[:, :n]
+    s = np.einsum("bthd,bthd->bht", x[:, :, 0], x[:, :, 1]) / math.sqrt(D) * LOG2E
+    tol = 2 * (D + 2) * 2.0 ** -24 * np.einsum("bthd,bthd->bht", abs(x[:, :, 0]), abs(x[:, :, 1])) + 2.0 ** -22 * (1 + abs(s))
+    assert np.all(np.abs(host(lse2)[:, :, :n] - s) <= tol)
+
+
 def test_store_of_counts_far_below_zero(gpt_lib):
     # a count below zero stores nothing, the lowest int32 too: count - 16, for a block's first token, would wrap around
     from decoder_only_transformer_gpt_gb300 import binding
