@@ -136,7 +136,7 @@ paged_store_kernel(PagedCache c, const uint4* __restrict__ qkv, const int32_t* _
 //    would have 128), but shared keys and values are unpacked once for all heads. P enters that product in two bf16
 //    parts; scores, maxima, sums and outputs stay fp32.
 // Measured: 16 sequences of 9,000 to 32,000 rows x 12 heads 160 us, 6.3 TB/s. Units of 16 rows were slower (16 sequences
-// of up to 1,023 rows: 15.6 against 14.5 us).
+// of up to 1,023 rows, as this form was then: 15.6 against 14.5 us).
 constexpr int kStages = 3;
 constexpr int kUnit = 32;                 // seen rows per unit
 
@@ -1335,10 +1335,10 @@ cudaError_t launch_decode(const PagedCache& c, const __nv_bfloat16* qkv, const i
   long long seen_max = static_cast<long long>(c.max_pages) << c.page_log2;
   if (w.window > 0 && static_cast<long long>(w.window) + w.sinks < seen_max) seen_max = w.window + w.sinks;
   // Few rows in sight: one launch of clusters (8 NC warps of UPW units). It pays for blocks that a short sequence leaves
-  // idle, so it is taken up to 12 blocks per SM with one unit per warp (2,048 rows: 16 sequences x 12 heads of up to
-  // 1,023 rows 9.9 against 13.0 us, of 2,047 rows 16.7 against 17.6; 64 sequences of 1,023, 20 blocks per SM, 36.8
-  // against 33.4), and with two units while all blocks run at once (one per SM; 4,095 rows: one sequence 4.9 against
-  // 13.2 us, four of them, 2.5 blocks per SM, 14.3 against 13.2).
+  // idle, so it is taken up to 12 blocks per SM with one unit per warp (2,048 rows; 12 heads, graph replays: 16 sequences of
+  // up to 1,023 rows 10.2 against 13.1 us, of up to 2,047 15.9 against 16.9; 64 sequences of up to 1,023, 20 blocks per
+  // SM, 32.5 against 30.1), and with two units while all blocks run at once (one per SM; 4,095 rows: one sequence 5.1
+  // against 13.2 us, four of them, 2.5 blocks per SM, 16.4 against 14.5).
   const long long units = (seen_max + kUnit - 1) / kUnit, lists = static_cast<long long>(w.B) * c.Hkv * w.mg;
   if (units <= 128 && (!c.weight || w.mg == 1)) {
     int nc = 1;
