@@ -1,10 +1,12 @@
-// Entry points of the paged key/value cache (include/gpt_kernels.h): argument checks, then the kernels of
-// k_paged.cu. Everything that the host can check is refused before any device call; page numbers and lengths
+// Entry points of the paged key/value caches and the position rotation (include/gpt_kernels.h): argument checks, then the
+// kernels of k_paged.cu, k_append.cu and k_paged4.cu. Everything that the host can check is refused before any device call; page numbers and lengths
 // live on the device and are checked there (an access they would lead out of bounds is skipped and recorded).
 #include "../../include/gpt_kernels.h"
 #include "model.h"
 
 #include <cuda_runtime.h>
+
+#include <cmath>
 
 using namespace gptgb;
 
@@ -29,6 +31,19 @@ int paged_cache(PagedCache* c, const void* pool, const float* weight, const int3
   c->page_log2 = lg;
   c->max_pages = max_pages;
   c->Hkv = Hkv;
+  return GPT_OK;
+}
+
+// Fused rows and their rotation. GPT_OK fills *x.
+int rotary_rows(RotaryRows* x, const void* qkv, void* out, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T,
+                int32_t H, int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t inverse) {
+  if (!qkv || B < 1 || T < 0 || H < 1 || Hkv < 1 || D < 1 || rot < 0) return GPT_EINVAL;
+  if (static_cast<int64_t>(B) * T > 0x7fffffffLL) return GPT_EINVAL;
+  if ((static_cast<int64_t>(H) + 2LL * Hkv) * D > 0x3fffffffLL) return GPT_EINVAL;   // a row's elements: 32 bits
+  if ((rot > 0) != (turns != nullptr) || (interleaved & ~1) || (inverse & ~1)) return GPT_EINVAL;
+  if ((D != 32 && D != 64) || H % Hkv || rot % 16 || rot > D || !aligned16(qkv) || !aligned16(out)) return GPT_ECONFIG;
+  if (reinterpret_cast<uintptr_t>(turns) & 7u) return GPT_ECONFIG;
+  *x = {qkv, out, pos, turns, B, T, H, Hkv, D, rot, interleaved, inverse};
   return GPT_OK;
 }
 
@@ -91,6 +106,104 @@ int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int3
   if (!err) return GPT_ENOMEM;
   return finish("paged evict", launch_paged_evict(c, lens, dst_table, dst_max_pages, new_lens, kept, B, D, budget, sinks,
                                                   recent, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gptk_rotary_turns(const double* freq, uint64_t* turns, int32_t n) {
+  if (!freq || !turns || n < 0) return GPT_EINVAL;
+  // 1 / (2 pi) in two doubles, and the product with the first in two as well: turns to about 2^-100 of themselves
+  const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
+  for (int32_t i = 0; i < n; ++i) {
+    const double f = freq[i];
+    if (!(std::fabs(f) <= 1e12)) return GPT_EINVAL;
+    const volatile double product = f * hi;          // rounded here, whatever the compiler would join it with
+    const double p = product, e = std::fma(f, hi, -p) + f * lo;
+    const double frac = p - std::trunc(p);           // exact; below a turn either way
+    const uint64_t whole = static_cast<uint64_t>(std::nearbyint(std::ldexp(std::fabs(frac), 64)));
+    const int64_t rest = static_cast<int64_t>(std::nearbyint(std::ldexp(e, 64)));   // |e| <= 2^-16 turns
+    turns[i] = (frac < 0 ? 0 - whole : whole) + static_cast<uint64_t>(rest);
+  }
+  return GPT_OK;
+}
+
+int gptk_rotary(const void* qkv, void* out, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
+                int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t inverse, void* stream) {
+  if (!out || !turns) return GPT_EINVAL;
+  RotaryRows x;
+  const int rc = rotary_rows(&x, qkv, out, pos, turns, B, T, H, Hkv, D, rot, interleaved, inverse);
+  if (rc != GPT_OK) return rc;
+  if (T == 0) return GPT_OK;
+  return finish("rotary", launch_rotary(x, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gptk_paged_append(const void* qkv, void* out, void* pool, float* weight, const int32_t* table, const int32_t* start,
+                      const int32_t* count, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
+                      int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t pages, int32_t page,
+                      int32_t max_pages, void* stream) {
+  RotaryRows x;
+  int rc = rotary_rows(&x, qkv, out, pos, turns, B, T, H, Hkv, D, rot, interleaved, 0);
+  if (rc != GPT_OK) return rc;
+  PagedCache c;
+  rc = paged_cache(&c, pool, weight, table, B, Hkv, D, pages, page, max_pages);
+  if (rc != GPT_OK) return rc;
+  if (T == 0) return GPT_OK;
+  int* err = step_err_word();
+  if (!err) return GPT_ENOMEM;
+  return finish("paged append", launch_paged_append(c, x, start, count, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gptk_paged_append4(const void* qkv, void* out, void* codes, void* ranges, const int32_t* table, const int32_t* start,
+                       const int32_t* count, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
+                       int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t pages, int32_t page,
+                       int32_t max_pages, void* stream) {
+  if (!ranges) return GPT_EINVAL;
+  RotaryRows x;
+  int rc = rotary_rows(&x, qkv, out, pos, turns, B, T, H, Hkv, D, rot, interleaved, 0);
+  if (rc != GPT_OK) return rc;
+  PagedCache c;
+  rc = paged_cache(&c, codes, nullptr, table, B, Hkv, D, pages, page, max_pages);
+  if (rc != GPT_OK) return rc;
+  if (!aligned16(ranges)) return GPT_ECONFIG;
+  if (T == 0) return GPT_OK;
+  int* err = step_err_word();
+  if (!err) return GPT_ENOMEM;
+  return finish("paged append in 4 bits",
+                launch_paged_append4(c, ranges, x, start, count, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gptk_paged_load4(const void* codes, const void* ranges, const int32_t* table, const int32_t* start,
+                     const int32_t* count, void* rows, int32_t B, int32_t T, int32_t Hkv, int32_t D, int32_t pages,
+                     int32_t page, int32_t max_pages, void* stream) {
+  if (!ranges || !rows || T < 0 || static_cast<int64_t>(B) * T > 0x7fffffffLL) return GPT_EINVAL;
+  PagedCache c;
+  const int rc = paged_cache(&c, codes, nullptr, table, B, Hkv, D, pages, page, max_pages);
+  if (rc != GPT_OK) return rc;
+  if (!aligned16(ranges) || !aligned16(rows)) return GPT_ECONFIG;
+  if (T == 0) return GPT_OK;
+  int* err = step_err_word();
+  if (!err) return GPT_ENOMEM;
+  return finish("paged load of 4 bits", launch_paged_load4(c, ranges, start, count, rows, B, T, D, err,
+                                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gptk_paged_attention4(const void* qkv, const void* codes, const void* ranges, const int32_t* table,
+                          const int32_t* lens, void* y, float* lse2, int32_t B, int32_t H, int32_t Hkv, int32_t D,
+                          int32_t pages, int32_t page, int32_t max_pages, int32_t window, int32_t sinks, int32_t added,
+                          void* stream) {
+  if (!qkv || !ranges || !lens || !y || H < 1 || window < 0 || sinks < 0 || added < 0) return GPT_EINVAL;
+  PagedCache c;
+  const int rc = paged_cache(&c, codes, nullptr, table, B, Hkv, D, pages, page, max_pages);
+  if (rc != GPT_OK) return rc;
+  if (added > static_cast<int64_t>(max_pages) * page) return GPT_EINVAL;
+  if ((static_cast<int64_t>(H) + 2LL * Hkv) * D > 0x3fffffffLL) return GPT_EINVAL;
+  if (H % Hkv || H / Hkv > kPagedMaxGroup || !aligned16(qkv) || !aligned16(y) || !aligned16(ranges)) return GPT_ECONFIG;
+  // the units of 32 rows are numbered with 32 bits, and with 64 over all heads
+  const int64_t units = static_cast<int64_t>(B) * ((static_cast<int64_t>(max_pages) * page + 31) / 32);
+  if (units > 0x7fffffffLL || units * Hkv > (1LL << 40)) return GPT_EINVAL;
+  int* err = step_err_word();
+  if (!err) return GPT_ENOMEM;
+  return finish("paged attention over 4 bits",
+                launch_paged_attention4(c, ranges, qkv, lens, added, y, lse2, B, H, D, window, sinks, err,
+                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,346 @@
+// Position rotation of fused rows, alone or on the way into a paged cache of 16-bit or 4-bit rows, and 4-bit rows read back.
+//
+// Rotation: pair i of the first `rot` values of every query and key head turns by n f_i at position n. Phases are counted
+// in turns as 64-bit fractions: turns[i] = f_i / (2 pi) * 2^64 (mod 2^64), so n turns[i] mod 2^64 is the phase of any
+// position without rounding (one fp32 product n f_i is off by 2^-25 n f_i: 0.03 rad at position 1,000,000), and 32 bits
+// of it go through sincospif. The map is orthogonal: its gradient is the rotation back (sin of the other sign).
+//
+// A 4-bit row: of its D values the lowest (bf16) and scale = bf16((highest - lowest) / 15), and a code
+// min(15, round((x - lowest) / scale)) per value, value 2 j low in byte j. Every step is one rounding in fp32 (1 / scale
+// and the products included), so that the same row always gives the same codes. Codes [pages][2][Hkv][page][D / 2] bytes,
+// ranges [pages][2][Hkv][page] pairs (scale, lowest).
+//
+// All three kernels are bound by memory and give a warp one token (or part of one): a lane holds 16 values of a head, two
+// 16-byte units that contain each other's pair partners, D / 16 lanes a head, so a load instruction of the warp covers
+// 1 KB of the token's row. A lane computes the sine and cosine of one pair for the whole warp, once per token.
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.h"
+#include "paged.cuh"
+
+#include <math.h>
+
+namespace gptgb {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kAppendWarps = 8;
+
+// min and max that pass a NaN on
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+struct Row16 {          // 16 values of a head: units u0 and u1
+  uint4 a, b;
+};
+
+__device__ __forceinline__ void turn16(Row16& x, const float (&cs)[8], const float (&sn)[8], bool interleaved) {
+  uint32_t* a = &x.a.x;
+  uint32_t* b = &x.b.x;
+  if (interleaved) {                                 // pairs side by side: four in each unit
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 p = unpack_bf16x2(a[k]), q = unpack_bf16x2(b[k]);
+      a[k] = pack_bf16x2(p.x * cs[k] - p.y * sn[k], p.y * cs[k] + p.x * sn[k]);
+      b[k] = pack_bf16x2(q.x * cs[4 + k] - q.y * sn[4 + k], q.y * cs[4 + k] + q.x * sn[4 + k]);
+    }
+  } else {                                           // unit a's values pair with unit b's
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 p = unpack_bf16x2(a[k]), q = unpack_bf16x2(b[k]);
+      a[k] = pack_bf16x2(p.x * cs[2 * k] - q.x * sn[2 * k], p.y * cs[2 * k + 1] - q.y * sn[2 * k + 1]);
+      b[k] = pack_bf16x2(q.x * cs[2 * k] + p.x * sn[2 * k], q.y * cs[2 * k + 1] + p.y * sn[2 * k + 1]);
+    }
+  }
+}
+
+// The codes of a unit's eight values. v * inv + 2^23 leaves the rounded code in the low bits of the sum (ties to even, as
+// rintf); the bits above it cancel in the subtraction.
+__device__ __forceinline__ uint32_t codes8(const uint4& x, float low, float inv) {
+  const uint32_t* a = &x.x;
+  uint32_t w = 0u - 0xfb000000u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 p = unpack_bf16x2(a[k]);
+    const float m = 8388608.0f;
+    const float lo = fminf(__fadd_rn(__fmul_rn(p.x - low, inv), m), m + 15.0f);
+    const float hi = fminf(__fadd_rn(__fmul_rn(p.y - low, inv), m), m + 15.0f);
+    w += (__float_as_uint(lo) << (8 * k)) + (__float_as_uint(hi) << (8 * k + 4));
+  }
+  return w;
+}
+
+// Scale and lowest value of a row whose values lie in the LANES lanes around this one (bf16 pair), and 1 / scale; a row
+// with a value that is not finite, or a range past fp32, is NaN throughout. A scale below the normal numbers counts as 0.
+template <int LANES>
+__device__ __forceinline__ uint32_t range_of(const Row16& x, float* low, float* inv) {
+  const uint32_t* a = &x.a.x;
+  const uint32_t* b = &x.b.x;
+  float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 p = unpack_bf16x2(a[k]), q = unpack_bf16x2(b[k]);
+    lo = min_nan(lo, min_nan(min_nan(p.x, p.y), min_nan(q.x, q.y)));
+    hi = max_nan(hi, max_nan(max_nan(p.x, p.y), max_nan(q.x, q.y)));
+  }
+#pragma unroll
+  for (int k = 1; k < LANES; k <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(kAll, lo, k));
+    hi = max_nan(hi, __shfl_xor_sync(kAll, hi, k));
+  }
+  const float range = hi - lo;
+  float scale = __bfloat162float(__float2bfloat16(__fmul_rn(range, 1.0f / 15.0f)));
+  *low = lo;
+  *inv = 0.0f;
+  if (!(range <= 3.402823466e38f)) return 0x7fff7fffu;
+  if (scale < 1.17549435e-38f) scale = 0.0f;
+  else *inv = __frcp_rn(scale);
+  return pack_bf16x2(scale, lo);
+}
+
+struct AppendArgs {
+  const uint4* qkv;       // [B, T, (H + 2 Hkv) D] bf16
+  uint4* out;             // the same, rotated; qkv itself: in place; nullptr: not wanted
+  const int32_t *start, *count, *pos;
+  const unsigned long long* turns;   // [rot / 2]; nullptr: no rotation
+  uint32_t* ranges;       // 4-bit rows' (scale, lowest)
+  long long tokens;       // B T
+  int T, H, Hkv, rot, interleaved, inverse;
+  int parts;              // warps that share a token
+};
+
+// MODE 0: rotation alone; 1: keys and values into c.pool (bf16); 2: into c.pool (codes) and a.ranges.
+template <int D, int MODE>
+__global__ void __launch_bounds__(kAppendWarps * 32)
+append_kernel(PagedCache c, AppendArgs a, int* err) {
+  constexpr int U = D / 8, LANES = D / 16, HEADS = 32 / LANES;   // units and lanes of a head, heads side by side
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned w = blockIdx.x * kAppendWarps + warp;
+  const unsigned tok = w / static_cast<unsigned>(a.parts), part = w - tok * a.parts;
+  if (tok >= a.tokens) return;
+  const int b = static_cast<int>(tok / static_cast<unsigned>(a.T)), t = static_cast<int>(tok - static_cast<unsigned>(b) * a.T);
+  if (MODE != 0 && a.count && t >= __ldg(a.count + b)) return;
+  const long long first = MODE != 0 && a.start ? __ldg(a.start + b) : 0;
+  if (first < 0) return;                             // no sequence
+  const long long r = first + t;
+  long long row = -1;                                // of the key of head 0 in the pool
+  size_t weight = 0;
+  if (MODE != 0) {
+    if (r >= static_cast<long long>(c.max_pages) << c.page_log2) {
+      record_error(err, GPT_DEV_EPAGE);
+    } else {
+      const int pg = page_of(c, c.table + static_cast<size_t>(b) * c.max_pages, static_cast<int>(r), err);
+      const int slot = static_cast<int>(r) & ((1 << c.page_log2) - 1);
+      if (pg >= 0) {
+        row = static_cast<long long>(row_at(c, pg, 0, 0, slot));
+        weight = weight_at(c, pg, 0, slot);
+      }
+    }
+  }
+  // this lane's head (of HEADS side by side) and its two units
+  const int i = lane % LANES, hh = lane / LANES, pairs = a.rot / 2;
+  const bool turns = 8 * i < pairs;
+  const int u0 = turns && !a.interleaved ? i : 2 * i, u1 = turns && !a.interleaved ? i + a.rot / 16 : 2 * i + 1;
+  const int NH = a.H + 2 * a.Hkv, heads = a.H + a.Hkv;
+  const size_t base = static_cast<size_t>(tok) * NH * U;
+  const uint4* src = a.qkv + base;
+  uint4* dst = a.out ? a.out + base : nullptr;
+  const bool in_place = a.out == a.qkv;
+  float cs[8], sn[8];
+  if (pairs) {
+    float s = 0.0f, co = 1.0f;
+    if (lane < pairs) {
+      const long long n = (a.pos ? static_cast<long long>(__ldg(a.pos + b)) : first) + t;
+      const unsigned long long phase = static_cast<unsigned long long>(n) * __ldg(a.turns + lane);
+      sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &co);   // 2 / 2^32 half turns
+      if (a.inverse) s = -s;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      cs[k] = __shfl_sync(kAll, co, (8 * i + k) & 31);
+      sn[k] = __shfl_sync(kAll, s, (8 * i + k) & 31);
+    }
+  }
+  // without an output the queries are not needed
+  const int skip = dst ? 0 : a.H;
+  for (int h0 = skip + static_cast<int>(part) * HEADS; h0 < NH; h0 += 2 * HEADS * a.parts) {
+    Row16 x[2];
+    int hd[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {                    // two heads' loads in flight
+      hd[k] = h0 + k * HEADS * a.parts + hh;
+      const int at = min(hd[k], NH - 1);
+      x[k].a = src[static_cast<size_t>(at) * U + u0];
+      x[k].b = src[static_cast<size_t>(at) * U + u1];
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool ok = hd[k] < NH, moved = turns && hd[k] < heads;
+      if (moved) turn16(x[k], cs, sn, a.interleaved);
+      if (ok && dst && (moved || !in_place)) {
+        dst[static_cast<size_t>(hd[k]) * U + u0] = x[k].a;
+        dst[static_cast<size_t>(hd[k]) * U + u1] = x[k].b;
+      }
+      if (MODE == 0) continue;
+      const int e = hd[k] - a.H;                     // key head, or Hkv + value head
+      const bool stored = ok && e >= 0 && row >= 0;
+      const long long to = row + (static_cast<long long>(e) << c.page_log2);
+      if (MODE == 1 && stored) {
+        uint4* pool = static_cast<uint4*>(c.pool);
+        pool[to * U + u0] = x[k].a;
+        pool[to * U + u1] = x[k].b;
+        if (c.weight && i == 0 && e < a.Hkv) c.weight[weight + (static_cast<size_t>(e) << c.page_log2)] = 0.0f;
+      }
+      if (MODE == 2) {
+        float low, inv;
+        const uint32_t range = range_of<LANES>(x[k], &low, &inv);
+        if (stored) {
+          uint32_t* codes = static_cast<uint32_t*>(c.pool) + to * U;
+          const uint32_t ca = range == 0x7fff7fffu ? 0u : codes8(x[k].a, low, inv), cb = range == 0x7fff7fffu ? 0u : codes8(x[k].b, low, inv);
+          if (u1 == u0 + 1) {
+            *reinterpret_cast<uint2*>(codes + u0) = make_uint2(ca, cb);
+          } else {
+            codes[u0] = ca;
+            codes[u1] = cb;
+          }
+          if (i == 0) a.ranges[to] = range;
+        }
+      }
+    }
+  }
+}
+
+// Rows start[b] + t (t < count[b]) of a 4-bit cache as bf16 rows of Hkv keys, then Hkv values.
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32)
+load4_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const int32_t* __restrict__ start,
+             const int32_t* __restrict__ count, uint4* __restrict__ rows, long long tokens, int T, int parts, int* err) {
+  constexpr int U = D / 8, LANES = D / 16, HEADS = 32 / LANES;
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned w = blockIdx.x * kAppendWarps + warp;
+  const unsigned tok = w / static_cast<unsigned>(parts), part = w - tok * parts;
+  if (tok >= tokens) return;
+  const int b = static_cast<int>(tok / static_cast<unsigned>(T)), t = static_cast<int>(tok - static_cast<unsigned>(b) * T);
+  if (count && t >= __ldg(count + b)) return;
+  const long long first = start ? __ldg(start + b) : 0, r = first + t;
+  if (first < 0) return;                             // no sequence
+  if (r >= static_cast<long long>(c.max_pages) << c.page_log2) {
+    record_error(err, GPT_DEV_EPAGE);
+    return;
+  }
+  const int pg = page_of(c, c.table + static_cast<size_t>(b) * c.max_pages, static_cast<int>(r), err);
+  if (pg < 0) return;
+  const size_t row = row_at(c, pg, 0, 0, static_cast<int>(r) & ((1 << c.page_log2) - 1));
+  const int i = lane % LANES, hh = lane / LANES, NH = 2 * c.Hkv;
+  const uint2* codes = static_cast<const uint2*>(c.pool);
+  uint4* dst = rows + static_cast<size_t>(tok) * NH * U;
+  for (int h0 = static_cast<int>(part) * HEADS; h0 < NH; h0 += 2 * HEADS * parts) {
+    uint2 x[2];
+    uint32_t range[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const size_t from = row + (static_cast<size_t>(min(h0 + k * HEADS * parts + hh, NH - 1)) << c.page_log2);
+      x[k] = __ldg(codes + from * LANES + i);
+      range[k] = __ldg(ranges + from);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int hd = h0 + k * HEADS * parts + hh;
+      if (hd >= NH) continue;
+      const float2 f = unpack_bf16x2(range[k]);      // scale, lowest
+      const uint32_t words[2] = {x[k].x, x[k].y};
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t n = words[j >> 2] >> (8 * (j & 3));
+        v[j] = pack_bf16x2(fmaf(f.x, static_cast<float>(n & 15u), f.y), fmaf(f.x, static_cast<float>((n >> 4) & 15u), f.y));
+      }
+      dst[static_cast<size_t>(hd) * U + 2 * i] = make_uint4(v[0], v[1], v[2], v[3]);
+      dst[static_cast<size_t>(hd) * U + 2 * i + 1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+  }
+}
+
+// Warps that share a token: one where the tokens alone give every SM eight warps and more, else as many as there are
+// groups of heads, so that a step of a few tokens is one group a warp.
+int parts_of(long long tokens, int heads, int side_by_side, int sms) {
+  const int most = (heads + side_by_side - 1) / side_by_side;
+  const long long want = (8LL * sms + tokens - 1) / tokens;
+  return want < most ? static_cast<int>(want) : most;
+}
+
+template <int MODE>
+cudaError_t launch_append(const PagedCache& c, AppendArgs a, int D, int* err, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  const cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  const int heads = (a.out ? a.H : 0) + 2 * a.Hkv;
+  a.parts = parts_of(a.tokens, heads, 512 / D, sms);
+  const dim3 grid(static_cast<unsigned>((a.tokens * a.parts + kAppendWarps - 1) / kAppendWarps)), block(32 * kAppendWarps);
+  if (D == 64) return launch_k(append_kernel<64, MODE>, grid, block, 0, s, c, a, err);
+  return launch_k(append_kernel<32, MODE>, grid, block, 0, s, c, a, err);
+}
+
+AppendArgs append_args(const RotaryRows& x, const int32_t* start, const int32_t* count, void* ranges) {
+  AppendArgs a = {};
+  a.qkv = static_cast<const uint4*>(x.qkv);
+  a.out = static_cast<uint4*>(x.out);
+  a.start = start;
+  a.count = count;
+  a.pos = x.pos;
+  a.turns = reinterpret_cast<const unsigned long long*>(x.turns);
+  a.ranges = static_cast<uint32_t*>(ranges);
+  a.tokens = static_cast<long long>(x.B) * x.T;
+  a.T = x.T;
+  a.H = x.H;
+  a.Hkv = x.Hkv;
+  a.rot = x.turns ? x.rot : 0;
+  a.interleaved = x.interleaved;
+  a.inverse = x.inverse;
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryRows& x, cudaStream_t s) {
+  return launch_append<0>(PagedCache{}, append_args(x, nullptr, nullptr, nullptr), x.D, nullptr, s);
+}
+
+cudaError_t launch_paged_append(const PagedCache& c, const RotaryRows& x, const int32_t* start, const int32_t* count,
+                                int* err, cudaStream_t s) {
+  return launch_append<1>(c, append_args(x, start, count, nullptr), x.D, err, s);
+}
+
+cudaError_t launch_paged_append4(const PagedCache& c, void* ranges, const RotaryRows& x, const int32_t* start,
+                                 const int32_t* count, int* err, cudaStream_t s) {
+  return launch_append<2>(c, append_args(x, start, count, ranges), x.D, err, s);
+}
+
+cudaError_t launch_paged_load4(const PagedCache& c, const void* ranges, const int32_t* start, const int32_t* count,
+                               void* rows, int B, int T, int D, int* err, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  const cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  const long long tokens = static_cast<long long>(B) * T;
+  const int parts = parts_of(tokens, 2 * c.Hkv, 512 / D, sms);
+  const dim3 grid(static_cast<unsigned>((tokens * parts + kAppendWarps - 1) / kAppendWarps)), block(32 * kAppendWarps);
+  const uint32_t* r = static_cast<const uint32_t*>(ranges);
+  uint4* out = static_cast<uint4*>(rows);
+  if (D == 64) return launch_k(load4_kernel<64>, grid, block, 0, s, c, r, start, count, out, tokens, T, parts, err);
+  return launch_k(load4_kernel<32>, grid, block, 0, s, c, r, start, count, out, tokens, T, parts, err);
+}
+
+}  // namespace gptgb

@@ -1,0 +1,458 @@
+// Log probabilities of given tokens under logits, with entropy and the most probable tokens, and their gradient.
+//
+// With m the row's largest logit and d = z - m: S = sum e^d, A = sum d e^d, ln p = d - ln S, entropy = ln S - A / S. One pass
+// keeps m, S and A per lane against a running maximum (a chunk's maximum first, so S and A are rescaled once a chunk:
+// S' = f S, A' = f (A + (m - m') S), f = e^(m - m')). All in fp32, d as a difference, never through a rounded log-sum-exp:
+// the gradient gets (m, S), as e^(z - lse) would carry the rounding of lse, 2^-24 |lse| of every probability.
+//
+// The most probable tokens: every warp keeps its best 32 in order, one a lane, as 64-bit keys (logit, then lowest index),
+// and passes over a chunk none of whose lanes reaches the K-th of them, or of any other warp of the block. Lists are joined
+// two by two: the larger of each pair of opposite ends is a bitonic sequence of the best 32, sorted in five steps.
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.h"
+
+#include <cooperative_groups.h>
+#include <math.h>
+
+namespace gptgb {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kL2E = 1.4426950408889634f;
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kFar = -1e20f;           // stands for differences of -inf in products with 0 (times 2^31 it is finite)
+constexpr int kLpWarps = 8;
+constexpr int kLpVecs = 4;               // 16-byte vectors a lane and chunk
+constexpr int kLpChunk = 32 * kLpVecs;   // vectors a warp and chunk
+
+using Key = unsigned long long;
+
+// Larger logit, larger key; equal logits: lower index, larger key. Never 0. (-0 equals +0.)
+__device__ __forceinline__ Key key_of(float v, int index) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (static_cast<Key>(o) << 32) | static_cast<uint32_t>(~index);
+}
+__device__ __forceinline__ float value_of(Key k) {
+  const uint32_t o = static_cast<uint32_t>(k >> 32);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ int index_of(Key k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
+
+// The 32 best of two lists in descending order.
+__device__ __forceinline__ Key join_lists(Key a, Key b, int lane) {
+  const Key r = __shfl_sync(kAll, b, 31 - lane);
+  Key x = a > r ? a : r;
+#pragma unroll
+  for (int k = 16; k; k >>= 1) {
+    const Key y = __shfl_xor_sync(kAll, x, k);
+    x = ((lane & k) == 0) == (x > y) ? x : y;
+  }
+  return x;
+}
+
+// The K-th largest of the lanes' values.
+__device__ __forceinline__ float kth_largest(float v, int K, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int k = size >> 1; k; k >>= 1) {
+      const float y = __shfl_xor_sync(kAll, v, k);
+      const bool down = (lane & size) == 0 || size == 32;   // this run is sorted in descending order
+      const bool upper = (lane & k) == 0;
+      v = upper == down ? fmaxf(v, y) : fminf(v, y);
+    }
+  return __shfl_sync(kAll, v, K - 1);
+}
+
+struct Sums {
+  float m, s, a;
+};
+__device__ __forceinline__ Sums joined_sums(const Sums& x, const Sums& y) {
+  const float m = fmaxf(x.m, y.m);
+  const float dx = fmaxf(x.m - m, kFar), dy = fmaxf(y.m - m, kFar);
+  const float fx = ex2_approx(dx * kL2E), fy = ex2_approx(dy * kL2E);
+  return {m, x.s * fx + y.s * fy, fx * (x.a + x.s * dx) + fy * (y.a + y.s * dy)};
+}
+
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ float2 pair(const uint4& v, int k) {
+    const uint32_t* w = &v.x;
+    return make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+  static __device__ __forceinline__ void put(float* p, float x) { *p = x; }
+  static constexpr uint32_t kNone = 0xff800000u;     // -inf
+  static __device__ __forceinline__ float largest(const uint4 (&v)[kLpVecs]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kLpVecs; ++k) {
+      const float2 a = pair(v[k], 0), b = pair(v[k], 1);
+      m = fmax3(m, fmax3(a.x, a.y, b.x), b.y);
+    }
+    return m;
+  }
+};
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ float2 pair(const uint4& v, int k) { return unpack_bf16x2((&v.x)[k]); }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ float largest(const uint4 (&v)[kLpVecs]) {
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
+    __nv_bfloat162 m = w[0];
+#pragma unroll
+    for (int k = 1; k < 4 * kLpVecs; ++k) m = __hmax2(m, w[k]);   // (a NaN is passed over here and shows in the sums)
+    const float2 f = __bfloat1622float2(m);
+    return fmaxf(f.x, f.y);
+  }
+};
+
+struct LpArgs {
+  const void* z;
+  const int32_t* targets;
+  float *logp, *entropy, *stats, *top_logp;
+  int32_t* top_ids;
+  long long ld;
+  int V, K;
+};
+
+// A row, or a stretch of it, as seen by one warp.
+template <typename T>
+struct Row {
+  const T* z;
+  int head, nvec;      // values before the first 16-byte boundary, then whole vectors
+  __device__ __forceinline__ Row(const void* base, long long ld, int V, long long m) {
+    z = static_cast<const T*>(base) + m * ld;
+    const int to = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / static_cast<int>(sizeof(T));
+    head = min(V, to);
+    nvec = (V - head) / Vec<T>::N;
+  }
+};
+
+// One block per row, or a cluster of NC blocks: the row's chunks go round the warps of all of them.
+template <typename T, int NC>
+__global__ void __launch_bounds__(kLpWarps * 32)
+logprobs_kernel(LpArgs a, int* err) {
+  using W = Vec<T>;
+  constexpr int N = W::N, VALUES = kLpVecs * N;      // values a lane and chunk
+  namespace cg = cooperative_groups;
+  __shared__ __align__(16) uint4 s_stage[kLpWarps][32][kLpVecs + 1];
+  __shared__ Key s_floor;                            // a K-th best of one of the warps: nothing below it is wanted
+  __shared__ Key s_list[8][32];                      // the warps' lists, then the blocks'
+  __shared__ Sums s_sums[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC);
+  const long long m = blockIdx.x / NC;
+  if (threadIdx.x == 0) s_floor = 0;
+  pdl_wait();
+  pdl_trigger();
+  const Row<T> row(a.z, a.ld, a.V, m);
+  const uint4* vecs = reinterpret_cast<const uint4*>(row.z + row.head);
+  const int K = a.K;
+  int target = -1;
+  float zt = 0.0f;
+  if (part == 0 && threadIdx.x == 0 && a.targets) {
+    target = __ldg(a.targets + m);
+    if (static_cast<unsigned>(target) < static_cast<unsigned>(a.V)) {
+      zt = W::get(row.z + target);
+    } else {
+      if (target != -1) record_error(err, GPT_DEV_ETARGET);
+      target = -1;
+    }
+  }
+  Sums sum = {kLowest, 0.0f, 0.0f};
+  Key best = 0;                                      // this warp's list, one a lane
+  Key floor_key = 0;                                 // what a token has to pass
+  if (K) __syncthreads();                            // s_floor
+
+  auto load = [&](int chunk, uint4 (&v)[kLpVecs]) {
+#pragma unroll
+    for (int k = 0; k < kLpVecs; ++k) {
+      const long long i = static_cast<long long>(chunk) * kLpChunk + k * 32 + lane;
+      v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+      if (i < row.nvec) v[k] = __ldg(vecs + i);
+    }
+  };
+  auto add = [&](float cm, const uint4 (&v)[kLpVecs]) {
+    const float mn = fmaxf(sum.m, cm), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E);
+    float2 s = make_float2(sum.s * f, 0.0f), e2 = make_float2(f * (sum.a + sum.s * dm), 0.0f);
+    const float2 neg = make_float2(-mn, -mn), l2e = make_float2(kL2E, kL2E);
+#pragma unroll
+    for (int k = 0; k < kLpVecs; ++k)
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 d = add2_rn(W::pair(v[k], j), neg), x = mul2_rn(d, l2e);
+        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        s = add2_rn(s, e);
+        e2 = fma2_rn(e, make_float2(fmaxf(d.x, kFar), fmaxf(d.y, kFar)), e2);
+      }
+    sum = {mn, s.x + s.y, e2.x + e2.y};
+  };
+  // Puts the lanes' keys that pass into the list, one by one.
+  auto insert = [&](Key key) {
+    unsigned who = __ballot_sync(kAll, key > floor_key);
+    while (who) {
+      const Key k = __shfl_sync(kAll, key, __ffs(who) - 1);
+      const int n = __popc(__ballot_sync(kAll, best > k));
+      const Key up = __shfl_up_sync(kAll, best, 1);
+      best = lane > n ? up : lane == n ? k : best;
+      const Key last = __shfl_sync(kAll, best, K - 1);
+      if (last > floor_key) floor_key = last;
+      who &= who - 1;
+      who &= __ballot_sync(kAll, key > floor_key);
+    }
+  };
+  auto may_pass = [&](float v) { return floor_key == 0 || v >= value_of(floor_key); };
+  // The chunk's tokens that pass. cm: the largest value of this lane's.
+  auto take = [&](int chunk, float cm, const uint4 (&v)[kLpVecs]) {
+    const Key shared = *static_cast<volatile Key*>(&s_floor);
+    if (shared > floor_key) floor_key = shared;
+    unsigned who = __ballot_sync(kAll, may_pass(cm));
+    if (!who) return;
+    if (__popc(who) > K) {
+      // K lanes have a value at least as large as the K-th of their largest ones: nothing below it is wanted
+      const Key k = (key_of(kth_largest(cm, K, lane), 0) >> 32) << 32;
+      if (k > floor_key) floor_key = k;
+      who = __ballot_sync(kAll, may_pass(cm));
+    }
+#pragma unroll
+    for (int k = 0; k < kLpVecs; ++k) s_stage[warp][lane][k] = v[k];
+    __syncwarp();
+    while (who) {
+      const int from = __ffs(who) - 1;
+      who &= who - 1;
+      const int j = lane % VALUES;                   // this lane's value of the candidate lane's
+      const T x = reinterpret_cast<const T*>(&s_stage[warp][from][0])[j];
+      const long long vec = static_cast<long long>(chunk) * kLpChunk + (j / N) * 32 + from;
+      const int index = row.head + static_cast<int>(vec) * N + j % N;
+      insert(lane < VALUES && vec < row.nvec ? key_of(W::get(&x), index) : 0);
+      who &= __ballot_sync(kAll, may_pass(cm));
+    }
+    __syncwarp();                                    // the stage is read before it is filled again
+    if (lane == 0 && floor_key > *static_cast<volatile Key*>(&s_floor)) atomicMax(&s_floor, floor_key);
+  };
+
+  const int chunks = (row.nvec + kLpChunk - 1) / kLpChunk, step = NC * kLpWarps, first = part * kLpWarps + warp;
+  uint4 v[kLpVecs], next[kLpVecs];
+  if (first < chunks) load(first, v);
+  for (int c = first; c < chunks; c += step) {
+    if (c + step < chunks) load(c + step, next);
+    const float cm = W::largest(v);
+    add(cm, v);
+    if (K) take(c, cm, v);
+#pragma unroll
+    for (int k = 0; k < kLpVecs; ++k) v[k] = next[k];
+  }
+  if (part == 0 && warp == 0) {                      // the values before and behind the vectors
+    const int tail = row.head + row.nvec * N;
+    const int index = lane < 16 ? (lane < row.head ? lane : -1) : (tail + lane - 16 < a.V ? tail + lane - 16 : -1);
+    const float z = index >= 0 ? W::get(row.z + index) : -INFINITY;
+    const float mn = fmaxf(sum.m, z), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E), d = z - mn, e = ex2_approx(d * kL2E);
+    sum = {mn, sum.s * f + e, f * (sum.a + sum.s * dm) + e * fmaxf(d, kFar)};
+    if (K) insert(index >= 0 ? key_of(z, index) : 0);
+  }
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1)
+    sum = joined_sums(sum, {__shfl_xor_sync(kAll, sum.m, k), __shfl_xor_sync(kAll, sum.s, k), __shfl_xor_sync(kAll, sum.a, k)});
+  if (lane == 0) s_sums[warp] = sum;
+  if (K) s_list[warp][lane] = best;
+  __syncthreads();
+  auto join8 = [&](int n) {                          // the n lists and sums in shared memory, to warp 0's registers
+    if (K) {
+#pragma unroll
+      for (int half = 4; half; half >>= 1) {
+        if (n > half) {
+          if (warp < half && warp + half < n) s_list[warp][lane] = join_lists(s_list[warp][lane], s_list[warp + half][lane], lane);
+          __syncthreads();
+        }
+      }
+      best = s_list[0][lane];
+    }
+    sum = s_sums[0];
+    for (int i = 1; i < n; ++i) sum = joined_sums(sum, s_sums[i]);
+  };
+  join8(kLpWarps);
+  if constexpr (NC > 1) {
+    auto cluster = cg::this_cluster();
+    cluster.sync();                                  // every block has read its own lists, before rank 0's are replaced
+    if (warp == 0) {
+      if (K) *cluster.map_shared_rank(&s_list[part][lane], 0) = best;
+      if (lane == 0) *cluster.map_shared_rank(&s_sums[part], 0) = sum;
+    }
+    cluster.sync();
+    if (part) return;
+    join8(NC);
+  }
+  if (warp) return;
+  const bool fine = sum.s > 0.0f && sum.s < INFINITY;   // a finite log-sum-exp
+  const float ln_s = logf(sum.s), nan = __int_as_float(0x7fffffff);
+  if (lane == 0) {
+    if (a.logp) a.logp[m] = target < 0 && fine ? 0.0f : fine ? (zt - sum.m) - ln_s : nan;
+    if (a.entropy) a.entropy[m] = fine ? ln_s - sum.a / sum.s : nan;
+    if (a.stats) *reinterpret_cast<float2*>(a.stats + 2 * m) = fine ? make_float2(sum.m, sum.s) : make_float2(nan, nan);
+  }
+  if (lane < K) {
+    a.top_ids[m * K + lane] = fine ? index_of(best) : -1;
+    a.top_logp[m * K + lane] = fine ? (value_of(best) - sum.m) - ln_s : nan;
+  }
+}
+
+// dz = dlogp (1[j = t] - p) - dentropy p (ln p + entropy), from (m, S): p = e^d / S. Bound by memory: the logits once in,
+// once out. A block takes 256 x kGradVecs vectors of a row.
+constexpr int kGradVecs = 4;
+
+struct LpGrad {
+  const void* z;
+  const int32_t* targets;
+  const float *stats, *entropy, *dlogp, *dentropy;
+  void* dz;
+  long long ld, dld, M;
+  int V, segments;     // blocks a row
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+logprobs_grad_kernel(LpGrad a) {
+  using W = Vec<T>;
+  constexpr int N = W::N;
+  pdl_wait();
+  pdl_trigger();
+  for (long long u = blockIdx.x; u < a.M * a.segments; u += gridDim.x) {
+    const long long m = u / a.segments;
+    const int seg = static_cast<int>(u - m * a.segments);
+    const Row<T> row(a.z, a.ld, a.V, m);
+    T* out = static_cast<T*>(a.dz) + m * a.dld;
+    const uint4* vecs = reinterpret_cast<const uint4*>(row.z + row.head);
+    const long long v0 = static_cast<long long>(seg) * 256 * kGradVecs + threadIdx.x;
+    uint4 v[kGradVecs];
+#pragma unroll
+    for (int k = 0; k < kGradVecs; ++k)
+      if (v0 + k * 256 < row.nvec) v[k] = vecs[v0 + k * 256];
+    const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * m);
+    const float h = a.entropy ? __ldg(a.entropy + m) : 0.0f, ge = a.dentropy ? __ldg(a.dentropy + m) : 0.0f;
+    int t = a.targets ? __ldg(a.targets + m) : -1;
+    if (static_cast<unsigned>(t) >= static_cast<unsigned>(a.V)) t = -1;
+    const float g = t >= 0 && a.dlogp ? __ldg(a.dlogp + m) : 0.0f;
+    // dz = p (c - ge d) with c = -g - ge (entropy - ln S), p = e^d / S
+    const float inv = 1.0f / st.y, c = -g - ge * (h - logf(st.y));
+    auto grad = [&](float z) {
+      const float d = z - st.x;
+      return ex2_approx(d * kL2E) * inv * (c - ge * fmaxf(d, kFar));
+    };
+    const bool same = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+#pragma unroll
+    for (int k = 0; k < kGradVecs; ++k) {
+      const long long i = v0 + k * 256;
+      if (i >= row.nvec) continue;
+      const int index = row.head + static_cast<int>(i) * N;
+      float x[N];
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 p = W::pair(v[k], j);
+        x[2 * j] = grad(p.x);
+        x[2 * j + 1] = grad(p.y);
+      }
+      if (static_cast<unsigned>(t - index) < static_cast<unsigned>(N) && t >= 0) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (t - index == j) x[j] += g;
+      }
+      if (same) {
+        *reinterpret_cast<uint4*>(out + index) = W::pack(x);
+      } else {                                       // rows of the gradient that start elsewhere in their 16 bytes
+#pragma unroll
+        for (int j = 0; j < N; ++j) W::put(out + index + j, x[j]);
+      }
+    }
+    if (seg == 0 && threadIdx.x < 32) {              // the values before and behind the vectors
+      const int lane = threadIdx.x, tail = row.head + row.nvec * N;
+      const int index = lane < 16 ? (lane < row.head ? lane : -1) : (tail + lane - 16 < a.V ? tail + lane - 16 : -1);
+      if (index >= 0) W::put(out + index, grad(W::get(row.z + index)) + (index == t ? g : 0.0f));
+    }
+  }
+}
+
+template <typename T, int NC>
+cudaError_t launch_nc(const LpArgs& a, int M, int* err, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(M) * NC);
+  cfg.blockDim = dim3(32 * kLpWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {NC, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = NC > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NC>, a, err);
+}
+
+template <typename T>
+cudaError_t launch_logprobs_of(const LpArgs& a, int M, int* err, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  const cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  const long long chunks = (static_cast<long long>(a.V) / Vec<T>::N + kLpChunk - 1) / kLpChunk;
+  if (8LL * M <= 2 * sms && chunks > 4 * kLpWarps) return launch_nc<T, 8>(a, M, err, s);
+  if (2LL * M <= 2 * sms && chunks > kLpWarps) return launch_nc<T, 2>(a, M, err, s);
+  return launch_nc<T, 1>(a, M, err, s);
+}
+
+template <typename T>
+cudaError_t launch_grad_of(LpGrad a, cudaStream_t s) {
+  a.segments = (a.V / Vec<T>::N + 256 * kGradVecs - 1) / (256 * kGradVecs);
+  if (a.segments < 1) a.segments = 1;
+  const long long units = a.M * a.segments;
+  return launch_k(logprobs_grad_kernel<T>, dim3(static_cast<unsigned>(units < 0x7fffffffLL ? units : 0x7fffffffLL)), dim3(256),
+                  0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const LogprobRows& x, float* logp, float* entropy, float* stats, int32_t* top_ids,
+                            float* top_logp, int K, int* err, cudaStream_t s) {
+  LpArgs a = {};
+  a.z = x.logits;
+  a.targets = x.targets;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.stats = stats;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  a.ld = x.ld;
+  a.V = x.V;
+  a.K = K;
+  return x.bf16 ? launch_logprobs_of<__nv_bfloat16>(a, x.M, err, s) : launch_logprobs_of<float>(a, x.M, err, s);
+}
+
+cudaError_t launch_logprobs_bwd(const LogprobRows& x, const float* stats, const float* entropy, const float* dlogp,
+                                const float* dentropy, void* dlogits, int64_t dld, cudaStream_t s) {
+  LpGrad a = {};
+  a.z = x.logits;
+  a.targets = x.targets;
+  a.stats = stats;
+  a.entropy = entropy;
+  a.dlogp = dlogp;
+  a.dentropy = dentropy;
+  a.dz = dlogits;
+  a.ld = x.ld;
+  a.dld = dld;
+  a.M = x.M;
+  a.V = x.V;
+  return x.bf16 ? launch_grad_of<__nv_bfloat16>(a, s) : launch_grad_of<float>(a, s);
+}
+
+}  // namespace gptgb

@@ -221,6 +221,20 @@ cudaError_t launch_set_int(int* p, int v, cudaStream_t s);
 constexpr int kSampleMaxV = 55296;
 cudaError_t launch_sample(const float* logits, int B, int V, float temperature, int top_k, float top_p,
                           const float* uniform, int32_t* out, cudaStream_t s);
+// Rows of logits [M, V] (row stride ld elements; fp32, or bf16) and one given token each (nullable; -1: none).
+struct LogprobRows {
+  const void* logits;
+  const int32_t* targets;
+  int M, V;
+  int64_t ld;
+  int bf16;
+};
+// ln p of the given tokens, entropy, (largest logit, sum of exponentials) and the K most probable tokens (each nullable).
+cudaError_t launch_logprobs(const LogprobRows& x, float* logp, float* entropy, float* stats, int32_t* top_ids,
+                            float* top_logp, int K, int* err, cudaStream_t s);
+// The logits' gradient from those of logp and entropy (nullable, with what it needs).
+cudaError_t launch_logprobs_bwd(const LogprobRows& x, const float* stats, const float* entropy, const float* dlogp,
+                                const float* dentropy, void* dlogits, int64_t dld, cudaStream_t s);
 // Scratch on a stream from a pool that the library keeps per device (gptk.cu): as cudaMallocAsync / cudaFreeAsync,
 // but freed memory stays with the library, so that a call after a synchronisation does not map it anew.
 cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t s);
@@ -249,6 +263,31 @@ cudaError_t launch_paged_store(const PagedCache& c, const void* qkv, const int32
 // (window 0: all; else those less than window rows back, and the first `sinks`).
 cudaError_t launch_paged_attention(const PagedCache& c, const void* qkv, const int32_t* lens, void* y, float* lse2,
                                    int B, int H, int D, int window, int sinks, int* err, cudaStream_t s);
+// Fused rows [B, T, (H + 2 Hkv) D] whose queries and keys turn by their positions: pos[b] + t (nullable: the row's own
+// number) times turns[i] / 2^64 turns for pair i of the first rot values (turns nullable: no rotation). out: the rotated
+// rows (qkv itself: in place).
+struct RotaryRows {
+  const void* qkv;
+  void* out;
+  const int32_t* pos;
+  const uint64_t* turns;
+  int B, T, H, Hkv, D, rot, interleaved, inverse;
+};
+cudaError_t launch_rotary(const RotaryRows& x, cudaStream_t s);
+// Rows start[b] + t (start nullable: 0; below 0: no sequence) = keys and values of the rotated rows, t < count[b]
+// (nullable: T); weights 0. out nullable.
+cudaError_t launch_paged_append(const PagedCache& c, const RotaryRows& x, const int32_t* start, const int32_t* count,
+                                int* err, cudaStream_t s);
+// The 4-bit cache: c.pool holds codes [pages][2][Hkv][page][D / 2] bytes, ranges [pages][2][Hkv][page][2] bf16.
+cudaError_t launch_paged_append4(const PagedCache& c, void* ranges, const RotaryRows& x, const int32_t* start,
+                                 const int32_t* count, int* err, cudaStream_t s);
+// Its rows start[b] + t as bf16 [B, T, 2 Hkv D].
+cudaError_t launch_paged_load4(const PagedCache& c, const void* ranges, const int32_t* start, const int32_t* count,
+                               void* rows, int B, int T, int D, int* err, cudaStream_t s);
+// Attention of one query row per sequence (the queries of qkv [B, (H + 2 Hkv) D]) over rows 0 .. lens[b] + added - 1.
+cudaError_t launch_paged_attention4(const PagedCache& c, const void* ranges, const void* qkv, const int32_t* lens, int added,
+                                    void* y, float* lse2, int B, int H, int D, int window, int sinks, int* err,
+                                    cudaStream_t s);
 // Keeps budget rows per sequence and key head (the first `sinks`, the last `recent`, the largest weights
 // between) in order, in the pages of dst_table.
 cudaError_t launch_paged_evict(const PagedCache& c, const int32_t* lens, const int32_t* dst_table, int dst_max_pages,

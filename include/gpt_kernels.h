@@ -222,6 +222,101 @@ int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int3
                      int32_t max_pages, int32_t dst_max_pages, int32_t budget, int32_t sinks, int32_t recent,
                      void* stream);
 
+/*
+ * Position rotation of fused rows (bf16, D in {32, 64}; the source pages' models learn their positions, this is the
+ * library's extension for those that turn them): at position n, pair i of the first rot values (a multiple of 16, at most
+ * D) of every query and key head turns by the angle n f_i:  a' = a cos - b sin,  b' = b cos + a sin.  The pair is values
+ * i and i + rot / 2, or 2 i and 2 i + 1 where interleaved is 1. Values behind rot, and value heads, stay as they are.
+ * turns [rot / 2] uint64 holds the frequencies in turns, turns[i] = f_i / (2 pi) 2^64 modulo 2^64, so that the phase of
+ * every 32-bit position is exact (gptk_rotary_turns makes it); sine and cosine are fp32, the results rounded once.
+ *
+ * gptk_rotary_turns: host arrays. freq [n] in radians per position, |freq| <= 1e12 (GPT_EINVAL otherwise, NaN included).
+ *
+ * gptk_rotary: qkv [B, T, (H + 2 Hkv) D] -> out, row t of sequence b at position pos[b] + t (pos int32 [B] or NULL: 0).
+ * out is qkv itself (in place; the values are then not written) or does not overlap it. inverse 1 turns back: the
+ * derivative of the rotation, from the gradient of its output to that of its input. B T < 2^31, 16-byte aligned rows.
+ */
+int gptk_rotary_turns(const double* freq, uint64_t* turns, int32_t n);
+int gptk_rotary(const void* qkv, void* out, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
+                int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t inverse, void* stream);
+
+/*
+ * gptk_paged_store with the rotation applied on the way: rows start[b] + t of sequence b take the rotated keys, and the
+ * values, of qkv[b][t] for t < count[b]; their weights become 0. They stand at positions pos[b] + t (pos NULL: start[b] + t,
+ * the rows' own numbers; an eviction numbers rows anew, so behind one pos is the caller's). turns NULL with rot 0: no
+ * rotation. out [B, T, (H + 2 Hkv) D] or NULL takes the rotated rows, whose queries the attention wants; it may be qkv
+ * itself. Rows t >= count[b] of out stay as they were. start[b] < 0: no sequence, nothing is written for it. What else
+ * holds for gptk_paged_store holds here.
+ */
+int gptk_paged_append(const void* qkv, void* out, void* pool, float* weight, const int32_t* table, const int32_t* start,
+                      const int32_t* count, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
+                      int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t pages, int32_t page,
+                      int32_t max_pages, void* stream);
+
+/*
+ * The paged cache in 4 bits (D in {32, 64}), laid out as the one above:
+ *   codes   [pages][2][Hkv][page][D / 2] uint8: value 2 j of a row in the low half of byte j, value 2 j + 1 in the high one
+ *   ranges  [pages][2][Hkv][page][2] bf16: per row its scale and its lowest value
+ * A row stands for lowest + scale * code. Storing takes lowest = its smallest value, scale = (largest - smallest) / 15
+ * rounded to bf16 (one below 2^-126 becomes 0), code = min(15, round((x - lowest) / scale)), half to even, 0 where the
+ * scale is 0; each step (the products with fp32 1 / 15 and 1 / scale) is one fp32 rounding. So a value is off by half a
+ * scale, 1 / 30 of its row's range, and the scale's rounding. A row with a value that is not finite, or whose range passes
+ * fp32, is held as NaN throughout (codes 0). Keys are rounded to bf16 after their rotation, then to 4 bits.
+ * codes and ranges 16-byte aligned; tables, pages, errors and limits as for the 16-bit cache.
+ *
+ * gptk_paged_append4: gptk_paged_append into this cache.
+ *
+ * gptk_paged_load4: rows start[b] + t, t < count[b], of sequence b as bf16: rows [B, T, 2 Hkv D], a token's Hkv keys, then
+ * its Hkv values. start NULL: 0, count NULL: T; start[b] < 0 or t >= count[b]: the row stays as it was.
+ *
+ * gptk_paged_attention4: attention of one query row per sequence over its cached rows 0 .. n - 1, n = lens[b] + added (the
+ * newest token is in the cache already; with added 1, lens can still be the numbers that its append started from). Only
+ * the queries of qkv [B, (H + 2 Hkv) D] are read; they see rows r with n - 1 - r < window or r < sinks (window 0: all).
+ *   y[b, h] = sum_r a_r u_r,  a = softmax(q_h . k_r / sqrt(D))     bf16 [B, H D]
+ *   lse2[b, h] = log2 sum_r 2^(q_h . k_r log2(e) / sqrt(D))         fp32 [B, H], NULL: not wanted
+ * n = 0: y 0, lse2 -inf. lens[b] < 0: no sequence, row b of the outputs stays as it was. fp32 scores and sums; the
+ * probabilities enter the product with the values in two bf16 parts (2^-16 of each at most is lost). Scores are taken as
+ * scale * (q . codes) + lowest * sum(q), whose terms have to stay within fp32. A NaN in sight makes its queries' outputs
+ * NaN, and so do scores that are all -inf. Rows out of sight are not read. Scratch (none where the table, or the window
+ * and sinks, hold few rows; else about 10 MB and 4 B bytes) is taken on the stream as for gptk_paged_attention; make a
+ * process's first call on a device before any stream capture.
+ */
+int gptk_paged_append4(const void* qkv, void* out, void* codes, void* ranges, const int32_t* table, const int32_t* start,
+                       const int32_t* count, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
+                       int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t pages, int32_t page,
+                       int32_t max_pages, void* stream);
+int gptk_paged_load4(const void* codes, const void* ranges, const int32_t* table, const int32_t* start,
+                     const int32_t* count, void* rows, int32_t B, int32_t T, int32_t Hkv, int32_t D, int32_t pages,
+                     int32_t page, int32_t max_pages, void* stream);
+int gptk_paged_attention4(const void* qkv, const void* codes, const void* ranges, const int32_t* table,
+                          const int32_t* lens, void* y, float* lse2, int32_t B, int32_t H, int32_t Hkv, int32_t D,
+                          int32_t pages, int32_t page, int32_t max_pages, int32_t window, int32_t sinks, int32_t added,
+                          void* stream);
+
+/*
+ * Log probabilities of given tokens under logits [M, V] (dtype 0: fp32, 1: bf16; row stride ld >= V elements), with
+ * p = softmax of a row ("第 25 章" §25.7 per token, without the mean; the alternatives are what gpt_sample draws from):
+ *   logp[m] = ln p[targets[m]]                 fp32 [M]; targets int32 [M] or NULL (then logp is NULL too); a target of -1:
+ *                                              none, logp 0; any other outside [0, V): 0, and gptk_status() says GPT_ETOKEN
+ *   entropy[m] = - sum_j p_j ln p_j            fp32 [M] or NULL; 0 ln 0 = 0
+ *   stats[m] = largest logit, and S = sum of e^(logit - largest)   fp32 [M, 2] or NULL: for the gradient
+ *   top_ids, top_logp [M, K], 0 <= K <= min(V, 32): the K most probable tokens and their ln p, the most probable first,
+ *                                              the lowest index first among equal logits
+ * A logit of -inf has no probability (its ln p is -inf). A row with a NaN, with +inf, or of -inf alone gives NaN
+ * everywhere, and ids of -1. fp32 sums; M, V >= 1. logits need only their type's alignment.
+ *
+ * gptk_logprobs_bwd: from logits, targets, stats and entropy of the call above and the gradients dlogp and dentropy (fp32
+ * [M]; dentropy NULL with entropy NULL: none; dlogp NULL with targets NULL: none), the gradient of the logits
+ *   dlogits[m, j] = dlogp (1[j = target] - p_j) - dentropy p_j (ln p_j + entropy)
+ * in the logits' type, row stride dld >= V; it is logits itself (with the same stride) or does not overlap them. A row whose target is -1 (or
+ * outside [0, V)) takes no part with its dlogp. Rows without a finite log-sum-exp give NaN.
+ */
+int gptk_logprobs(const void* logits, const int32_t* targets, float* logp, float* entropy, float* stats, int32_t* top_ids,
+                  float* top_logp, int32_t M, int32_t V, int64_t ld, int32_t K, int32_t dtype, void* stream);
+int gptk_logprobs_bwd(const void* logits, const int32_t* targets, const float* stats, const float* entropy,
+                      const float* dlogp, const float* dentropy, void* dlogits, int32_t M, int32_t V, int64_t ld,
+                      int64_t dld, int32_t dtype, void* stream);
+
 /* Deterministic mean of nll[0..M) into *loss (device fp32). */
 int gptk_mean(const float* nll, int32_t M, float* loss, void* stream);
 
