@@ -1,15 +1,22 @@
 // Attention of one query row per sequence over the paged cache in 4 bits (layout: k_append.cu).
 //
 // A row stands for low + scale * code, so with Q = sum of a query's values
-//   q . k_r = scale_r (q . code_r) + low_r Q,    sum_r p_r u_r = sum_r (p_r scale_r) code_r + sum_r p_r low_r,
-// and codes enter the products as they are: a 4-bit code placed in a bf16 number's upper four mantissa bits, with the
-// exponent of 16, is the number 16 + code: one shift and one logical operation make two operands. The 16 is taken back
-// where it costs nothing: the score products start from -16 Q, and low - 16 scale stands for low in the second sum.
+//   q . k_r = scale_r (q . code_r) + low_r Q,    sum_r p_r u_r = sum_r (p_r scale_r) (code_r - 8) + sum_r p_r (low_r + 8 scale_r),
+// and codes enter the products as they are, as fp16 numbers code - 8: a code in the low four bits of a half with the
+// exponent of 1024 is 1024 + code, one in bits 4 to 7 with the exponent of 64 is 64 + code, so a shift serves four operand
+// registers and each takes one logical operation and one packed subtraction, which is exact. (In bf16, whose seven bits of
+// mantissa hold one code, every register takes its own shift, and a code comes out as 16 + code: taking the 16 back from the
+// finished sums left the outputs of 20,000 rows 1.8e-3 of their norm off, where their own rounding makes 1.6e-3.)
+// fp16 has few exponents: queries enter it times a power of two, exactly (largest value in [2^14, 2^15); what is below 2^-38
+// of that is lost), and p_r scale_r times 2^(15 - E) with 2^E above every scale and lowest value of the rows so far: 11
+// bits (2^-12 of a term is lost; one bf16 part would lose 2^-9, as much as the output's own rounding), and whole multiples of
+// 2^-39 of 2^E for the smallest.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
 #include "paged.cuh"
 
+#include <cuda_fp16.h>
 #include <math.h>
 
 namespace gptgb {
@@ -19,25 +26,32 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kUnit4 = 32;                // seen rows per unit
 
-// Bound by reading the cache (D + 8 bytes per seen row and key head) and, nearly as much, by issuing instructions: a byte of
-// codes takes a warp four times the unpacking and products of a byte of bf16. Work is dealt as in the 16-bit cache's
-// kernel (k_paged.cu): units of 32 seen rows of one (sequence, key head, group of up to 16 query heads), equal contiguous
-// ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
+// Bound by issuing instructions, about 400 for a unit: a byte of codes takes a warp four times the unpacking and products of
+// a byte of bf16, and the integer unit takes a warp's instruction only every other cycle. Work is dealt as in the 16-bit
+// cache's kernel (k_paged.cu): units of 32 seen rows of one (sequence, key head, group of up to 16 query heads), equal
+// contiguous ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
 //    memory as they lie there, without ldmatrix: a lane takes a quarter of a key row (8 bytes: its codes are the lane's
 //    operands of four products), and of value rows the same byte column of four rows, two of which are interleaved by one
 //    byte permutation into eight operands. Column 2 q + i of score tile j is row 16 (j / 2) + 8 (j % 2) + 4 i + q; output
 //    tile i holds value 8 n + i (D = 64; 4 n + i for 32) in column n, so a lane ends with D / 4 consecutive values.
-//  * 16 warps per SM with a ring of their own each.
+//  * A row's scales and lowest values are made into fp32 factors once, by the lane of its number.
+//  * Units are whole 32-row tiles of the sequence, so a page's share of one is contiguous and starts on a 16-byte boundary:
+//    a few bulk copies, a lane each, bring codes and ranges into the warp's own ring (16 warps per SM), counted by an
+//    mbarrier per stage. (Copies of 16 bytes by every lane took 250 of 680 instructions a unit to find their addresses, and 131
+//    us for 16 sequences of 9,000 to 32,000 rows.) Rows of a tile that are not seen are masked: their codes are numbers whatever
+//    they hold, their factors are set to 0.
 template <int D, int QR>
 struct Dec4Cfg {
   static constexpr int ROWB = D / 2;                              // bytes of a row's codes
   static constexpr int TILE = kUnit4 * ROWB;                      // keys, or values, of a unit
-  static constexpr int RANGES = 2 * TILE;                         // offset of the pairs (key range, value range)
+  static constexpr int RANGES = 2 * TILE;                         // offset of the keys' ranges, then the values'
   static constexpr int QUERIES = RANGES + kUnit4 * 8;             // offset of the query rows (where a unit starts a segment)
   static constexpr int STAGE = QUERIES + QR * D * 2;
   static constexpr int STAGES = QR == 8 ? 4 : 3;
-  static constexpr int WARP = STAGES * STAGE;
+  static constexpr int FACTORS = STAGES * STAGE;                  // the rows' factors: behind the stages
+  static constexpr int BARS = FACTORS + kUnit4 * 16;              // the stages' mbarriers
+  static constexpr int WARP = BARS + 64;
   static constexpr int WARPS = 16;
 };
 
@@ -53,10 +67,6 @@ struct Dec4Shape {
   float scale_log2;
 };
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool copy) {
-  const int n = copy ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -77,23 +87,50 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-// d = a b + c
-__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128f(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+// fp16 products: d = a b + (c0, c0, c1, c1), and d += a b
+__device__ __forceinline__ void mma16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%10, %10, %11, %11};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
-// Codes p of both halves of w as the bf16 pair (16 + low half's, 16 + high half's).
-template <int p>
-__device__ __forceinline__ uint32_t pair16(uint32_t w) {
-  const uint32_t x = p == 0 ? w << 3 : w >> (4 * p - 3);
-  return (x & 0x00780078u) | 0x41804180u;
+// The eight codes of a word, less 8, as fp16 pairs (code p, code p + 4).
+__device__ __forceinline__ void unpack8(uint32_t (&r)[4], uint32_t w) {
+  auto less = [](uint32_t x, uint32_t y) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&d);
+  };
+  const uint32_t h = w >> 8;
+  r[0] = less((w & 0x000f000fu) | 0x64006400u, 0x64086408u);    // 1024 + code - 1032
+  r[1] = less((w & 0x00f000f0u) | 0x54005400u, 0x54805480u);    // 64 + code - 72
+  r[2] = less((h & 0x000f000fu) | 0x64006400u, 0x64086408u);
+  r[3] = less((h & 0x00f000f0u) | 0x54005400u, 0x54805480u);
 }
 
 __device__ __forceinline__ float scale_of(uint32_t range) { return __uint_as_float(range << 16); }
 __device__ __forceinline__ float low_of(uint32_t range) { return __uint_as_float(range & 0xffff0000u); }
+// 2^e for -126 <= e <= 127, and the e with 2^e <= x < 2^(e + 1) (of a normal number's size; -127 below)
+__device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 
 // The rows that a sequence's query sees, from its length (-1: none to compute).
 __device__ __forceinline__ int rows_of(const PagedCache& c, const Dec4Shape& w, int len) {
@@ -101,29 +138,54 @@ __device__ __forceinline__ int rows_of(const PagedCache& c, const Dec4Shape& w, 
                                                                                                                       : len + w.added;
 }
 
-// A group's queries as the products' A operands, and the sum of each row's values.
-// rows: QR rows of D bf16 at shared address sq (zeros behind the group).
+// A group's queries as the products' A operands, times 2^(14 - e) for 2^e <= the row's largest value < 2^(e + 1): q are the
+// rows' sums, c the factors from a product to the softmax's base-2 exponent. gn rows of D bf16 at shared address sq, zeros
+// behind them.
 template <int D, int QR>
-__device__ __forceinline__ void take_queries(uint32_t (&f)[D / 16][4], float (&q)[2], uint32_t sq, int lane) {
+__device__ __forceinline__ void take_queries(uint32_t (&f)[D / 16][4], float (&q)[2], float (&c)[2], float scale_log2,
+                                             uint32_t sq, int gn, int lane) {
   constexpr int C = D / 4;                           // values of a lane: its codes' places
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
-    float sum = 0.0f;
+    if (rh == 1 && QR == 8) {
+      q[1] = c[1] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < D / 16; ++w) f[w][1] = f[w][3] = 0u;
+      continue;
+    }
+    float v[C], top = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (rh == 0 || QR == 16) x = lds128(sq + ((lane >> 2) + 8 * rh) * D * 2 + ((lane & 3) * C + 8 * w) * 2);
-      const float2 a = unpack_bf16x2(x.x), b = unpack_bf16x2(x.y), c = unpack_bf16x2(x.z), d = unpack_bf16x2(x.w);
-      sum += ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y));
-      // pairs (0, 4), (1, 5), (2, 6), (3, 7): as a word of codes unpacks
-      f[2 * w][rh] = __byte_perm(x.x, x.z, 0x5410);
-      f[2 * w][2 + rh] = __byte_perm(x.x, x.z, 0x7632);
-      f[2 * w + 1][rh] = __byte_perm(x.y, x.w, 0x5410);
-      f[2 * w + 1][2 + rh] = __byte_perm(x.y, x.w, 0x7632);
+      uint4 x = lds128(sq + ((lane >> 2) + 8 * rh) * D * 2 + ((lane & 3) * C + 8 * w) * 2);
+      if ((lane >> 2) + 8 * rh >= gn) x = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 p = unpack_bf16x2((&x.x)[k]);
+        v[8 * w + 2 * k] = p.x;
+        v[8 * w + 2 * k + 1] = p.y;
+        top = fmax3(top, fabsf(p.x), fabsf(p.y));
+      }
+    }
+    top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+    const int e = max(exponent_of(top), -100);
+    const float factor = exp2_of(14 - e);
+    c[rh] = scale_log2 * exp2_of(e - 14);
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      v[k] *= factor;
+      sum += v[k];
     }
     sum += __shfl_xor_sync(kAll, sum, 1);
     sum += __shfl_xor_sync(kAll, sum, 2);
     q[rh] = sum;
+#pragma unroll
+    for (int w = 0; w < C / 8; ++w) {                // pairs (0, 4), (1, 5), (2, 6), (3, 7): as a word of codes unpacks
+      f[2 * w][rh] = pack_half2(v[8 * w], v[8 * w + 4]);
+      f[2 * w][2 + rh] = pack_half2(v[8 * w + 1], v[8 * w + 5]);
+      f[2 * w + 1][rh] = pack_half2(v[8 * w + 2], v[8 * w + 6]);
+      f[2 * w + 1][2 + rh] = pack_half2(v[8 * w + 3], v[8 * w + 7]);
+    }
   }
 }
 
@@ -133,43 +195,32 @@ __device__ __forceinline__ void code_scores(float (&s)[4][4], const uint32_t (&f
                                             int lane) {
   const int c = lane >> 2;
   const uint32_t at = sk + ((c & 1) * 4 + (c >> 1)) * (D / 2) + (lane & 3) * (D / 8);
-  const float c0 = -16.0f * q[0], c1 = -16.0f * q[1];
+  const float c0 = 8.0f * q[0], c1 = 8.0f * q[1];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t w[2];
+    uint32_t r[4];
     if constexpr (D == 64) {
       const uint2 x = lds64(at + 8 * j * (D / 2));
-      w[0] = x.x;
-      w[1] = x.y;
+      unpack8(r, x.x);
+      mma16_from(s[j], f[0], r[0], r[1], c0, c1);
+      mma16(s[j], f[1], r[2], r[3]);
+      unpack8(r, x.y);
+      mma16(s[j], f[2], r[0], r[1]);
+      mma16(s[j], f[3], r[2], r[3]);
     } else {
-      w[0] = lds32(at + 8 * j * (D / 2));
-      w[1] = 0u;
-    }
-    mma_from(s[j], f[0], pair16<0>(w[0]), pair16<1>(w[0]), c0, c1);
-    mma_16816(s[j], f[1], pair16<2>(w[0]), pair16<3>(w[0]));
-    if constexpr (D == 64) {
-      mma_16816(s[j], f[2], pair16<0>(w[1]), pair16<1>(w[1]));
-      mma_16816(s[j], f[3], pair16<2>(w[1]), pair16<3>(w[1]));
+      unpack8(r, lds32(at + 8 * j * (D / 2)));
+      mma16_from(s[j], f[0], r[0], r[1], c0, c1);
+      mma16(s[j], f[1], r[2], r[3]);
     }
   }
 }
 
-// O += P (16 + code) for the 16 value rows at sv (rows of half a unit): a, b are the score tiles of eight each, now p times
-// the rows' scales, in two bf16 parts as in k_paged.cu: of up to eight query heads the second part takes the operand's other
-// eight rows.
+// O += P (code - 8) for the 16 value rows at sv (rows of half a unit): a, b are the score tiles of eight each, now p times
+// the rows' scales. The tiles of up to eight heads take the upper half of the operand's rows only.
 template <int D, int RH>
 __device__ __forceinline__ void add_codes(float (&o)[D / 8][4], const float (&a)[4], const float (&b)[4], uint32_t sv, int lane) {
-  uint32_t p[4], q[4];
-#pragma unroll
-  for (int i = 0; i < 2 * RH; ++i) {                 // heads lane / 4 (i even) and lane / 4 + 8, columns of a, then of b
-    const float x = i < RH ? a[2 * i] : b[2 * (i - RH)], y = i < RH ? a[2 * i + 1] : b[2 * (i - RH) + 1];
-    const int at = RH == 2 ? i : 2 * i;
-    p[at] = pack_bf16x2(x, y);
-    const float2 f = unpack_bf16x2(p[at]);
-    const uint32_t lo = pack_bf16x2(x - f.x, y - f.y);
-    if (RH == 2) q[at] = lo;
-    else p[at + 1] = lo;
-  }
+  const uint32_t p[4] = {pack_half2(a[0], a[1]), RH == 2 ? pack_half2(a[2], a[3]) : 0u, pack_half2(b[0], b[1]),
+                         RH == 2 ? pack_half2(b[2], b[3]) : 0u};
   constexpr int ROWB = D / 2;
   uint32_t x[2], y[2];                               // rows (0, 4) and (8, 12) + q: codes 0-3 and, of D = 64, 4-7 of a word
 #pragma unroll
@@ -181,30 +232,52 @@ __device__ __forceinline__ void add_codes(float (&o)[D / 8][4], const float (&a)
       y[h] = __byte_perm(w0, w1, 0x7632);
     } else {
       x[h] = lds16(at) | (lds16(at + 4 * ROWB) << 16);
-      y[h] = 0u;
     }
   }
-  auto step = [&](const uint32_t (&t)[4]) {
-    mma_16816(o[0], t, pair16<0>(x[0]), pair16<0>(x[1]));
-    mma_16816(o[1], t, pair16<1>(x[0]), pair16<1>(x[1]));
-    mma_16816(o[2], t, pair16<2>(x[0]), pair16<2>(x[1]));
-    mma_16816(o[3], t, pair16<3>(x[0]), pair16<3>(x[1]));
-    if constexpr (D == 64) {
-      mma_16816(o[4], t, pair16<0>(y[0]), pair16<0>(y[1]));
-      mma_16816(o[5], t, pair16<1>(y[0]), pair16<1>(y[1]));
-      mma_16816(o[6], t, pair16<2>(y[0]), pair16<2>(y[1]));
-      mma_16816(o[7], t, pair16<3>(y[0]), pair16<3>(y[1]));
-    }
-  };
-  step(p);
-  if constexpr (RH == 2) step(q);
+  uint32_t r[4], t[4];
+  unpack8(r, x[0]);
+  unpack8(t, x[1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mma16(o[i], p, r[i], t[i]);
+  if constexpr (D == 64) {
+    unpack8(r, y[0]);
+    unpack8(t, y[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mma16(o[4 + i], p, r[i], t[i]);
+  }
 }
 
-// The list position of a unit: sequence, head group (key head * mg + group), tile of the sequence's seen rows.
-struct Unit4 {
-  int b, hm, tile, nt;
-  Seen seen;
+// The tiles of 32 rows that hold the rows which a sequence's query sees, of n rows: v < head at the start, then from `gap`
+// tiles on.
+struct Tiles {
+  int n, head, gap, count;
 };
+__device__ __forceinline__ Tiles tiles_of(int n, int window, int sinks) {
+  Tiles t;
+  t.n = n;
+  t.count = (n + kUnit4 - 1) / kUnit4;
+  t.head = t.count;
+  t.gap = 0;
+  if (window > 0 && window < n) {
+    const int first = n - window, from = first / kUnit4;   // the first row of the window, and its tile
+    t.head = min((min(sinks, first) + kUnit4 - 1) / kUnit4, from);
+    t.gap = from - t.head;
+    t.count -= t.gap;
+  }
+  return t;
+}
+__device__ __forceinline__ int first_row(const Tiles& t, int v) { return (v < t.head ? v : v + t.gap) * kUnit4; }
+
+// The list position of a unit: sequence, key head, group of its query heads, tile of the sequence's seen rows.
+struct Unit4 {
+  int b, kh, mt, tile;
+  Tiles t;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
 
 template <int D, int QR>
 __global__ void __launch_bounds__(512, 1)
@@ -212,12 +285,14 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
                     const int32_t* __restrict__ lens, __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, Dec4Shape w,
                     Dec4Scratch ws, int* err) {
   using Cfg = Dec4Cfg<D, QR>;
-  constexpr int ROWB = Cfg::ROWB, UNITS = ROWB / 16, NT = D / 8, RH = QR == 16 ? 2 : 1;
+  constexpr int ROWB = Cfg::ROWB, NT = D / 8, RH = QR == 16 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
   int* s_prefix = reinterpret_cast<int*>(smem + nwarps * Cfg::WARP);     // [B + 1]
   int* s_rows = s_prefix + w.B + 1;                                      // [B]
   __shared__ int s_sum[16];
+  __shared__ int s_abort;
+  if (threadIdx.x == 0) s_abort = 0;
   pdl_wait();
   pdl_trigger();
 
@@ -231,7 +306,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       rows = rows_of(c, w, __ldg(lens + b));
       if (rows == -2) record_error(err, GPT_DEV_EPAGE);
       rows = max(rows, 0);
-      x = (seen_rows(rows, w.window, w.sinks).n + kUnit4 - 1) / kUnit4;
+      x = tiles_of(rows, w.window, w.sinks).count;
       s_rows[b] = rows;
     }
     int incl = x;
@@ -261,21 +336,26 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const long long u0 = deal.start(gw);
   const int count = static_cast<int>(deal.start(gw + 1) - u0);
 
-  const uint32_t ring = smem_u32(smem + warp * Cfg::WARP);
+  uint8_t* own = smem + warp * Cfg::WARP;
+  const uint32_t ring = smem_u32(own);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(own + Cfg::BARS);
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < Cfg::STAGES; ++k) mbar_init(bars + k, 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
   const int row = w.H + 2 * c.Hkv;                   // heads of a token's row
-  const int pmask = (1 << c.page_log2) - 1;
-  const size_t vrows = static_cast<size_t>(c.Hkv) << c.page_log2;        // rows from a page's keys to its values
-  const uint8_t* pool = static_cast<const uint8_t*>(c.pool);
 
-  auto set_seq = [&](Unit4& x) {                     // the sequence's lengths (b has units)
-    x.nt = s_prefix[x.b + 1] - s_prefix[x.b];
-    x.seen = seen_rows(s_rows[x.b], w.window, w.sinks);
-  };
+  auto set_seq = [&](Unit4& x) { x.t = tiles_of(s_rows[x.b], w.window, w.sinks); };   // (b has units)
   auto advance = [&](Unit4& x) {
-    if (++x.tile < x.nt) return;
+    if (++x.tile < x.t.count) return;
     x.tile = 0;
-    if (++x.hm < HM) return;
-    x.hm = 0;
+    if (++x.mt < w.mg) return;
+    x.mt = 0;
+    if (++x.kh < c.Hkv) return;
+    x.kh = 0;
     do ++x.b; while (x.b < w.B && s_prefix[x.b + 1] == s_prefix[x.b]);
     if (x.b < w.B) set_seq(x);
   };
@@ -291,76 +371,83 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     at.b = lo;
     set_seq(at);
     const long long r = u0 - static_cast<long long>(s_prefix[lo]) * HM;
-    at.hm = static_cast<int>(r / at.nt);
-    at.tile = static_cast<int>(r - static_cast<long long>(at.hm) * at.nt);
+    const int hm = static_cast<int>(r / at.t.count);
+    at.kh = hm / w.mg;
+    at.mt = hm - at.kh * w.mg;
+    at.tile = static_cast<int>(r - static_cast<long long>(hm) * at.t.count);
   }
-  // A lane copies of rows lane / 2 and 16 + lane / 2 of a unit: half `part` of their codes (all of the keys', or the values',
-  // where D = 32) and the range of the key (part 0) or the value. Their pages are looked up one unit ahead.
-  const int part = lane & 1;
+  // A tile lies in 32 / page pages, or in part of one: runs of rows. Lane 4 run + kind copies the run's key codes (kind 0),
+  // value codes (1), key ranges (2) or value ranges (3). Its page is looked up one unit ahead.
+  const int run_log2 = min(c.page_log2, 5), kind = lane & 3, run0 = (lane >> 2) << run_log2;   // run0: the run's first row
+  const uint32_t rowb = kind < 2 ? ROWB : 4, bytes = rowb << run_log2;
+  const uint32_t to = (kind < 2 ? kind * Cfg::TILE : Cfg::RANGES + (kind - 2) * kUnit4 * 4) + run0 * rowb;
+  const uint32_t pageb = (2u * static_cast<uint32_t>(c.Hkv) << c.page_log2) * rowb;   // a page's codes, or ranges
+  const uint8_t* from = (kind < 2 ? static_cast<const uint8_t*>(c.pool) : reinterpret_cast<const uint8_t*>(ranges)) + (kind & 1) * (pageb / 2);
+  const uint32_t in_page = static_cast<uint32_t>(run0 & ((1 << c.page_log2) - 1)) * rowb, headb = rowb << c.page_log2;
+  const uint32_t tile_mask = ((1u << c.page_log2) - 1u) & ~31u;   // of a tile's first row: where in its page
   Unit4 next = at;                                   // the unit whose rows are copied next
-  int pg[2];
+  int pg, r0;                                        // the run's page; -2: nothing to copy. The tile's first row
   auto look_up = [&]() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int v = next.tile * kUnit4 + 16 * i + (lane >> 1);
-      pg[i] = v < next.seen.n ? __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (seen_row(next.seen, v) >> c.page_log2)) : -1;
-    }
+    r0 = first_row(next.t, next.tile);
+    const int r = r0 + run0;
+    pg = run0 < kUnit4 && r < next.t.n ? __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (r >> c.page_log2)) : -2;
   };
   look_up();
-  int issued = 0;
-  auto issue = [&]() {                               // copies unit `next` into stage issued % STAGES, steps on
-    const uint32_t st = ring + (issued % Cfg::STAGES) * Cfg::STAGE;
-    const int kh = next.hm / w.mg, g0 = (next.hm - kh * w.mg) * 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = 16 * i + (lane >> 1), v = next.tile * kUnit4 + rr;
-      const bool seen = v < next.seen.n, ok = seen && static_cast<unsigned>(pg[i]) < static_cast<unsigned>(c.pages);
-      if (seen && !ok) record_error(err, GPT_DEV_EPAGE);
-      const size_t key = ok ? row_at(c, pg[i], 0, kh, seen_row(next.seen, v) & pmask) : 0, value = key + (ok ? vrows : 0);
-      if constexpr (UNITS == 2) {
-        cp_async16(st + rr * ROWB + 16 * part, pool + key * ROWB + 16 * part, ok);
-        cp_async16(st + Cfg::TILE + rr * ROWB + 16 * part, pool + value * ROWB + 16 * part, ok);
-      } else {
-        cp_async16(st + part * Cfg::TILE + rr * ROWB, pool + (part ? value : key) * ROWB, ok);
-      }
-      cp_async4(st + Cfg::RANGES + 8 * rr + 4 * part, ranges + (part ? value : key), ok);
-    }
-    if (issued == 0 || next.tile == 0) {             // a segment starts: its queries (rows past the group: zeros)
-      const int gn = min(w.G - g0, 16);
-      const __nv_bfloat16* tok = qkv + (static_cast<size_t>(next.b) * row + kh * w.G + g0) * D;
-#pragma unroll
-      for (int i = 0; i < QR * D / 256; ++i) {
-        const int e = 32 * i + lane, rr = e / (D / 8), u = e % (D / 8);
-        cp_async16(st + Cfg::QUERIES + e * 16, tok + static_cast<size_t>(min(rr, gn - 1)) * D + 8 * u, rr < gn);
-      }
-    }
-    ++issued;
-    if (issued < count) {
+  int issued = 0, fill = 0;                          // fill: the stage that is filled next
+  auto issue = [&]() {                               // copies unit `next`, steps on
+    const bool ok = static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages);
+    if (!ok && pg != -2) record_error(err, GPT_DEV_EPAGE);
+    const bool starts = issued == 0 || next.tile == 0;   // a segment starts: its queries
+    const int gn = min(w.G - next.mt * 16, 16);
+    const uint32_t who = __ballot_sync(kAll, ok), bar = smem_u32(bars + fill), dst = ring + fill * Cfg::STAGE;
+    if (lane == 0)
+      mbar_arrive_expect_tx(bars + fill, ((__popc(who & 0x33333333u) * ROWB + __popc(who & 0xccccccccu) * 4) << run_log2) +
+                                             (starts ? gn * D * 2 : 0));
+    __syncwarp();
+    if (ok)
+      bulk_load(dst + to, from + static_cast<size_t>(static_cast<uint32_t>(pg)) * pageb +
+                              (static_cast<uint32_t>(next.kh) * headb + (r0 & tile_mask) * rowb + in_page), bytes, bar);
+    if (starts && lane == 0)
+      bulk_load(dst + Cfg::QUERIES, qkv + (static_cast<size_t>(next.b) * row + next.kh * w.G + next.mt * 16) * D, gn * D * 2, bar);
+    fill = fill == Cfg::STAGES - 1 ? 0 : fill + 1;
+    if (++issued < count) {
       advance(next);
       look_up();
     }
   };
 #pragma unroll
-  for (int s = 0; s < Cfg::STAGES - 1; ++s) {
+  for (int s = 0; s < Cfg::STAGES - 1; ++s)
     if (issued < count) issue();
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
 
-  float o[NT][4];
+  float o[NT][4];                                    // times 2^(15 - e)
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, off[2] = {0.0f, 0.0f};   // rows lane / 4 and lane / 4 + 8
   uint32_t qf[D / 16][4];
-  float qsum[2] = {0.0f, 0.0f};
-  int piece0 = 0;                                    // the segment's first unit in this warp's range
+  float qsum[2] = {0.0f, 0.0f}, qc[2] = {0.0f, 0.0f};
+  int e = 0;                                         // 2^e is above every scale and lowest value of the segment's rows
+  float into = 0.0f;                                 // 2^(15 - e)
+  bool whole = false;                                // the segment's units so far are all in this warp's range
+  uint32_t slot0 = 0;                                // of the two places for partial results
   const int qrow = lane >> 2, q4 = lane & 3;
+  const uint32_t factors = ring + Cfg::FACTORS;
+  int stage = 0;                                     // that is read
+  uint32_t phase = 0;
   for (int n = 0; n < count; ++n) {
     if (issued < count) issue();
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::STAGES - 1) : "memory");
-    __syncwarp();
-    const uint32_t st = ring + (n % Cfg::STAGES) * Cfg::STAGE;
-    const int kh = at.hm / w.mg, g0 = (at.hm - kh * w.mg) * 16, gn = min(w.G - g0, 16);
+    if (!mbar_wait_warp(bars + stage, phase, &s_abort, err)) {   // reported; the copies under way end in this block's memory
+      for (int k = n; k < issued; ++k) {
+        mbar_wait_drain(bars + stage, phase);
+        stage = stage == Cfg::STAGES - 1 ? 0 : stage + 1;
+        if (stage == 0) phase ^= 1;
+      }
+      return;
+    }
+    const uint32_t st = ring + stage * Cfg::STAGE;
+    const int gn = min(w.G - at.mt * 16, 16);
     if (n == 0 || at.tile == 0) {
-      piece0 = n;
+      whole = at.tile == 0;
+      slot0 = n == 0 ? 0 : 1;
+      e = -111;
+      into = exp2_of(15 - e);
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh) {
         m[rh] = -INFINITY;
@@ -370,71 +457,96 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-      take_queries<D, QR>(qf, qsum, st + Cfg::QUERIES, lane);
+      take_queries<D, QR>(qf, qsum, qc, w.scale_log2, st + Cfg::QUERIES, gn, lane);
+    }
+    uint32_t seen = kAll;                            // the tile's rows that are
+    {                                                // row `lane`'s factors
+      const uint32_t kr = lds32(st + Cfg::RANGES + 4 * lane);
+      uint32_t vr = lds32(st + Cfg::RANGES + kUnit4 * 4 + 4 * lane);
+      const int f = first_row(at.t, at.tile), after = at.t.n - w.window;   // the window's first row
+      if (f + kUnit4 > at.t.n || (w.window > 0 && f < after && f + kUnit4 > w.sinks)) {
+        const bool mine = f + lane < at.t.n && (w.window == 0 || f + lane >= after || f + lane < w.sinks);
+        seen = __ballot_sync(kAll, mine);
+        if (!mine) vr = 0u;
+      }
+      const float vs = scale_of(vr), vl = low_of(vr);
+      const float size = fmaxf(vs, fabsf(vl));
+      if (__any_sync(kAll, size * into >= 32768.0f)) {   // (rarely: 2^e has to grow, and o and off with it)
+        const uint32_t top = __reduce_max_sync(kAll, __float_as_uint(size) & 0x7fffffffu);
+        const int up = min(exponent_of(__uint_as_float(top)) + 1, 128);
+        const float less = up - e > 126 ? 0.0f : exp2_of(e - up);
+        e = up;
+        into = exp2_of(15 - e);
+#pragma unroll
+        for (int rh = 0; rh < RH; ++rh) {
+          off[rh] *= less;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            o[j][2 * rh] *= less;
+            o[j][2 * rh + 1] *= less;
+          }
+        }
+      }
+      sts128f(factors + 16 * lane, scale_of(kr), low_of(kr), vs * into, fmaf(8.0f, vs, vl) * into);
     }
     float s[4][4];
     code_scores<D>(s, qf, qsum, st, lane);
-    // scores scale (q . code) + low Q, in units of the softmax's base-2 exponent over scale_log2
-    uint32_t vr[4][2];                               // the value rows' ranges
+    __syncwarp();
+    float2 vf[4][2];                                 // the value rows' factors
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint2 r = lds64(st + Cfg::RANGES + 8 * (16 * (j >> 1) + 8 * (j & 1) + 4 * i + q4));
-        vr[j][i] = r.y;
-        const float sc = scale_of(r.x), lo = low_of(r.x);
-        s[j][i] = fmaf(sc, s[j][i], lo * qsum[0]);
-        if (RH == 2) s[j][2 + i] = fmaf(sc, s[j][2 + i], lo * qsum[1]);
+        const float4 f = lds128f(factors + 16 * (16 * (j >> 1) + 8 * (j & 1) + 4 * i + q4));
+        vf[j][i] = make_float2(f.z, f.w);
+        s[j][i] = fmaf(f.x, s[j][i], f.y * qsum[0]);
+        if (RH == 2) s[j][2 + i] = fmaf(f.x, s[j][2 + i], f.y * qsum[1]);
       }
-    const int left = at.seen.n - at.tile * kUnit4;
-    if (left < kUnit4) {                             // rows behind the last: not seen
+    if (seen != kAll) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 2 * RH; ++i)
-          if (16 * (j >> 1) + 8 * (j & 1) + 4 * (i & 1) + q4 >= left) s[j][i] = -INFINITY;
+          if (!((seen >> (16 * (j >> 1) + 8 * (j & 1) + 4 * (i & 1) + q4)) & 1u)) s[j][i] = -INFINITY;
     }
 #pragma unroll
     for (int rh = 0; rh < RH; ++rh) {
       float mx = fmax3(s[0][2 * rh], s[0][2 * rh + 1], s[1][2 * rh]);
       mx = fmax3(mx, s[1][2 * rh + 1], s[2][2 * rh]);
       mx = fmax3(mx, s[2][2 * rh + 1], s[3][2 * rh]);
-      mx = fmaxf(mx, s[3][2 * rh + 1]) * w.scale_log2;
+      mx = fmaxf(mx, s[3][2 * rh + 1]) * qc[rh];
       mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
       mx = fmaxf(mx, m[rh]);
       const float ref = mx == -INFINITY ? 0.0f : mx;   // every score so far -inf: every term is 2^-inf
-      const float a = ex2_approx(m[rh] - ref);
-      m[rh] = mx;
-      float sum = 0.0f, low = 0.0f;
+      if (__any_sync(kAll, mx > m[rh])) {            // a new maximum
+        const float a = ex2_approx(m[rh] - ref);
+        m[rh] = mx;
+        l[rh] *= a;
+        off[rh] *= a;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][2 * rh] *= a;
+          o[j][2 * rh + 1] *= a;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float p = ex2_approx(fmaf(s[j][2 * rh + i], w.scale_log2, -ref));
-          const float sc = scale_of(vr[j][i]);
-          sum += p;
-          low = fmaf(p, fmaf(-16.0f, sc, low_of(vr[j][i])), low);
-          s[j][2 * rh + i] = p * sc;
+          const float p = ex2_approx(fmaf(s[j][2 * rh + i], qc[rh], -ref));
+          l[rh] += p;
+          off[rh] = fmaf(p, vf[j][i].y, off[rh]);
+          s[j][2 * rh + i] = p * vf[j][i].x;
         }
-      l[rh] = l[rh] * a + sum;
-      off[rh] = off[rh] * a + low;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        o[j][2 * rh] *= a;
-        o[j][2 * rh + 1] *= a;
-        if (RH == 1) {                               // the second part's
-          o[j][2] *= a;
-          o[j][3] *= a;
-        }
-      }
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) add_codes<D, RH>(o, s[2 * k], s[2 * k + 1], st + Cfg::TILE + 16 * k * ROWB, lane);
-    const bool ends = at.tile == at.nt - 1;
+    const bool ends = at.tile == at.t.count - 1;
     if (ends || n == count - 1) {                    // the piece is done
-      const bool whole = ends && piece0 + at.nt == n + 1;   // it holds all of the segment's units
-      const size_t slot = static_cast<size_t>(gw) * 2 + (piece0 == 0 ? 0 : 1);
+      whole = whole && ends;                         // it holds all of the segment's units
+      const size_t slot = static_cast<size_t>(gw) * 2 + slot0;
+      const float back = exp2_of((e - 15) / 2), rest = exp2_of(e - 15 - (e - 15) / 2);   // 2^(e - 15) in two steps
 #pragma unroll
       for (int rh = 0; rh < RH; ++rh) {
         float lt = l[rh], ot = off[rh];
@@ -448,9 +560,9 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) v[i * NT + j] = o[j][2 * rh + i] + (RH == 1 ? o[j][2 + i] : 0.0f) + ot;
+          for (int i = 0; i < 2; ++i) v[i * NT + j] = (o[j][2 * rh + i] + ot) * back * rest;
         if (whole) {
-          const size_t head = static_cast<size_t>(at.b) * w.H + kh * w.G + g0 + r;
+          const size_t head = static_cast<size_t>(at.b) * w.H + at.kh * w.G + at.mt * 16 + r;
           const float inv = 1.0f / lt;               // (a sum of 0, every score -inf, gives NaN)
           uint4* dst = reinterpret_cast<uint4*>(y + head * D + q4 * (D / 4));
 #pragma unroll
@@ -467,9 +579,10 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       }
     }
     advance(at);
-    __syncwarp();                                    // the stage is read before it is filled again
+    stage = stage == Cfg::STAGES - 1 ? 0 : stage + 1;
+    if (stage == 0) phase ^= 1;
+    __syncwarp();                                    // the stage and the factors are read before they are filled again
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Joins the partial results of a (sequence, key head) in a fixed order; sequences of no rows get zeros and -inf.
