@@ -33,8 +33,9 @@ constexpr int kUnit4 = 32;                // seen rows per unit
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
 //    memory as they lie there, without ldmatrix: a lane takes a quarter of a key row (8 bytes: its codes are the lane's
 //    operands of four products), and of value rows the same byte column of four rows, two of which are interleaved by one
-//    byte permutation into eight operands. Column 2 q + i of score tile j is row 16 (j / 2) + 8 (j % 2) + 4 i + q; output
-//    tile i holds value 8 n + i (D = 64; 4 n + i for 32) in column n, so a lane ends with D / 4 consecutive values.
+//    byte permutation into eight operands. The cached rows, and the values, are the 16 rows of a product, the heads its eight
+//    columns, so that one key head for each query head wastes half as much as with the heads as rows; the probabilities are
+//    turned over by movmatrix.
 //  * A row's scales and lowest values are made into fp32 factors once, by the lane of its number.
 //  * Units are whole 32-row tiles of the sequence, so a page's share of one is contiguous and starts on a 16-byte boundary:
 //    a few bulk copies, a lane each, bring codes and ranges into the warp's own ring (16 warps per SM), counted by an
@@ -95,12 +96,12 @@ __device__ __forceinline__ float4 lds128f(uint32_t a) {
 __device__ __forceinline__ void sts128f(uint32_t a, float x, float y, float z, float w) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
-// fp16 products: d = a b + (c0, c0, c1, c1), and d += a b
-__device__ __forceinline__ void mma16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
+// fp16 products: d = a b + c, and c += a b
+__device__ __forceinline__ void mma16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%10, %10, %11, %11};"
+               "{%10, %11, %12, %13};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -113,17 +114,38 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The eight codes of a word, less 8, as fp16 pairs (code p, code p + 4).
-__device__ __forceinline__ void unpack8(uint32_t (&r)[4], uint32_t w) {
+// An 8 x 8 matrix of 16-bit numbers, a row of pairs to four lanes, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The eight codes of a word, less 8, as fp16 pairs (code p, code p + 4). exps: the two exponents, in registers that the
+// compiler takes for variables (it would make two logical operations of one with two constants).
+struct Exponents {
+  uint32_t e1024, e64;
+  __device__ __forceinline__ Exponents() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(e1024));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(e64));
+  }
+};
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t masked_or(uint32_t x, uint32_t y) {   // (x & MASK) | y
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack8(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t w, const Exponents& exps) {
   auto less = [](uint32_t x, uint32_t y) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
     return *reinterpret_cast<const uint32_t*>(&d);
   };
   const uint32_t h = w >> 8;
-  r[0] = less((w & 0x000f000fu) | 0x64006400u, 0x64086408u);    // 1024 + code - 1032
-  r[1] = less((w & 0x00f000f0u) | 0x54005400u, 0x54805480u);    // 64 + code - 72
-  r[2] = less((h & 0x000f000fu) | 0x64006400u, 0x64086408u);
-  r[3] = less((h & 0x00f000f0u) | 0x54005400u, 0x54805480u);
+  r0 = less(masked_or<0x000f000fu>(w, exps.e1024), 0x64086408u);    // 1024 + code - 1032
+  r1 = less(masked_or<0x00f000f0u>(w, exps.e64), 0x54805480u);      // 64 + code - 72
+  r2 = less(masked_or<0x000f000fu>(h, exps.e1024), 0x64086408u);
+  r3 = less(masked_or<0x00f000f0u>(h, exps.e64), 0x54805480u);
 }
 
 __device__ __forceinline__ float scale_of(uint32_t range) { return __uint_as_float(range << 16); }
@@ -138,26 +160,25 @@ __device__ __forceinline__ int rows_of(const PagedCache& c, const Dec4Shape& w, 
                                                                                                                       : len + w.added;
 }
 
-// A group's queries as the products' A operands, times 2^(14 - e) for 2^e <= the row's largest value < 2^(e + 1): q are the
-// rows' sums, c the factors from a product to the softmax's base-2 exponent. gn rows of D bf16 at shared address sq, zeros
-// behind them.
-template <int D, int QR>
-__device__ __forceinline__ void take_queries(uint32_t (&f)[D / 16][4], float (&q)[2], float (&c)[2], float scale_log2,
-                                             uint32_t sq, int gn, int lane) {
-  constexpr int C = D / 4;                           // values of a lane: its codes' places
-#pragma unroll
-  for (int rh = 0; rh < 2; ++rh) {
-    if (rh == 1 && QR == 8) {
-      q[1] = c[1] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < D / 16; ++w) f[w][1] = f[w][3] = 0u;
-      continue;
-    }
-    float v[C], top = 0.0f, sum = 0.0f;
+// A unit's products have the cached rows, or the value columns, as the 16 rows of their first operand, and eight query heads
+// as the columns (twice for 9 to 16 heads): lane 4 n + q holds, of every tile of scores, rows n and n + 8 under heads 2 q and
+// 2 q + 1. Row n of a tile is row 4 (n % 2) + n / 2 of its eight rows in the cache.
+__device__ __forceinline__ int row_in_eight(int n) { return (n & 1) * 4 + (n >> 1); }
+
+// Eight heads' queries as second operands, times 2^(14 - e) for 2^e <= the head's largest value < 2^(e + 1). from: what the
+// score products start with, 8 times the sums of heads 2 q and 2 q + 1; sum: these sums; c: the factors from a product to the
+// softmax's base-2 exponent. gn rows of D bf16 at shared address sq, zeros behind them.
+template <int D>
+struct Queries {
+  uint32_t f[D / 16][2];
+  float from[4], sum[2], c[2];
+  __device__ __forceinline__ void take(float scale_log2, uint32_t sq, int gn, int lane) {
+    constexpr int C = D / 4;                         // values of a lane: its codes' places
+    float v[C], top = 0.0f, mine = 0.0f;
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {
-      uint4 x = lds128(sq + ((lane >> 2) + 8 * rh) * D * 2 + ((lane & 3) * C + 8 * w) * 2);
-      if ((lane >> 2) + 8 * rh >= gn) x = make_uint4(0u, 0u, 0u, 0u);
+      uint4 x = lds128(sq + (lane >> 2) * D * 2 + ((lane & 3) * C + 8 * w) * 2);
+      if ((lane >> 2) >= gn) x = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 p = unpack_bf16x2((&x.x)[k]);
@@ -169,81 +190,95 @@ __device__ __forceinline__ void take_queries(uint32_t (&f)[D / 16][4], float (&q
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
     const int e = max(exponent_of(top), -100);
-    const float factor = exp2_of(14 - e);
-    c[rh] = scale_log2 * exp2_of(e - 14);
+    const float factor = exp2_of(14 - e), back = scale_log2 * exp2_of(e - 14);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       v[k] *= factor;
-      sum += v[k];
+      mine += v[k];
     }
-    sum += __shfl_xor_sync(kAll, sum, 1);
-    sum += __shfl_xor_sync(kAll, sum, 2);
-    q[rh] = sum;
+    mine += __shfl_xor_sync(kAll, mine, 1);
+    mine += __shfl_xor_sync(kAll, mine, 2);
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {                // pairs (0, 4), (1, 5), (2, 6), (3, 7): as a word of codes unpacks
-      f[2 * w][rh] = pack_half2(v[8 * w], v[8 * w + 4]);
-      f[2 * w][2 + rh] = pack_half2(v[8 * w + 1], v[8 * w + 5]);
-      f[2 * w + 1][rh] = pack_half2(v[8 * w + 2], v[8 * w + 6]);
-      f[2 * w + 1][2 + rh] = pack_half2(v[8 * w + 3], v[8 * w + 7]);
+      f[2 * w][0] = pack_half2(v[8 * w], v[8 * w + 4]);
+      f[2 * w][1] = pack_half2(v[8 * w + 1], v[8 * w + 5]);
+      f[2 * w + 1][0] = pack_half2(v[8 * w + 2], v[8 * w + 6]);
+      f[2 * w + 1][1] = pack_half2(v[8 * w + 3], v[8 * w + 7]);
     }
-  }
-}
-
-// Products q . code of the 32 key rows at sk: tile j, column 2 q + i is row 16 (j / 2) + 8 (j % 2) + 4 i + q.
-template <int D>
-__device__ __forceinline__ void code_scores(float (&s)[4][4], const uint32_t (&f)[D / 16][4], const float (&q)[2], uint32_t sk,
-                                            int lane) {
-  const int c = lane >> 2;
-  const uint32_t at = sk + ((c & 1) * 4 + (c >> 1)) * (D / 2) + (lane & 3) * (D / 8);
-  const float c0 = 8.0f * q[0], c1 = 8.0f * q[1];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t r[4];
-    if constexpr (D == 64) {
-      const uint2 x = lds64(at + 8 * j * (D / 2));
-      unpack8(r, x.x);
-      mma16_from(s[j], f[0], r[0], r[1], c0, c1);
-      mma16(s[j], f[1], r[2], r[3]);
-      unpack8(r, x.y);
-      mma16(s[j], f[2], r[0], r[1]);
-      mma16(s[j], f[3], r[2], r[3]);
-    } else {
-      unpack8(r, lds32(at + 8 * j * (D / 2)));
-      mma16_from(s[j], f[0], r[0], r[1], c0, c1);
-      mma16(s[j], f[1], r[2], r[3]);
+    for (int i = 0; i < 2; ++i) {
+      sum[i] = __shfl_sync(kAll, mine, 8 * (lane & 3) + 4 * i);
+      c[i] = __shfl_sync(kAll, back, 8 * (lane & 3) + 4 * i);
+      from[i] = from[2 + i] = 8.0f * sum[i];
+    }
+  }
+};
+
+// Products q . code of the 32 key rows at sk, two tiles of 16.
+template <int D, int NQ>
+__device__ __forceinline__ void code_scores(float (&s)[NQ][2][4], const Queries<D> (&q)[NQ], uint32_t sk, int lane, const Exponents& exps) {
+  const uint32_t at = sk + row_in_eight(lane >> 2) * (D / 2) + (lane & 3) * (D / 8);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t w[2][2];                                // rows n and n + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (D == 64) {
+        const uint2 x = lds64(at + (16 * j + 8 * h) * (D / 2));
+        w[h][0] = x.x;
+        w[h][1] = x.y;
+      } else {
+        w[h][0] = lds32(at + (16 * j + 8 * h) * (D / 2));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      uint32_t a[4], b[4];
+      unpack8(a[0], a[2], b[0], b[2], w[0][k], exps);
+      unpack8(a[1], a[3], b[1], b[3], w[1][k], exps);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        if (k == 0) mma16_from(s[i][j], a, q[i].f[0][0], q[i].f[0][1], q[i].from);
+        else mma16(s[i][j], a, q[i].f[2 * k][0], q[i].f[2 * k][1]);
+        mma16(s[i][j], b, q[i].f[2 * k + 1][0], q[i].f[2 * k + 1][1]);
+      }
     }
   }
 }
 
-// O += P (code - 8) for the 16 value rows at sv (rows of half a unit): a, b are the score tiles of eight each, now p times
-// the rows' scales. The tiles of up to eight heads take the upper half of the operand's rows only.
-template <int D, int RH>
-__device__ __forceinline__ void add_codes(float (&o)[D / 8][4], const float (&a)[4], const float (&b)[4], uint32_t sv, int lane) {
-  const uint32_t p[4] = {pack_half2(a[0], a[1]), RH == 2 ? pack_half2(a[2], a[3]) : 0u, pack_half2(b[0], b[1]),
-                         RH == 2 ? pack_half2(b[2], b[3]) : 0u};
+// O += (code - 8) P for 16 value rows at sv; s: a tile of scores, now p times the rows' scales. Tile t of O has values
+// 8 n + 2 t and, in its lower half, 8 n + 2 t + 1 as rows (D = 32: 4 n + ..).
+template <int D, int NQ>
+__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const float (&s)[NQ][2][4], int j, uint32_t sv, int lane, const Exponents& exps) {
+  uint32_t p[NQ][2];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
+    p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
+  }
   constexpr int ROWB = D / 2;
-  uint32_t x[2], y[2];                               // rows (0, 4) and (8, 12) + q: codes 0-3 and, of D = 64, 4-7 of a word
+  uint32_t x[2][2];                                  // rows (0, 4) + q, then (8, 12) + q: codes 0-3 and, of D = 64, 4-7 of a word
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t at = sv + (8 * h + (lane & 3)) * ROWB + (lane >> 2) * (D / 16);
     if constexpr (D == 64) {
       const uint32_t w0 = lds32(at), w1 = lds32(at + 4 * ROWB);
-      x[h] = __byte_perm(w0, w1, 0x5410);
-      y[h] = __byte_perm(w0, w1, 0x7632);
+      x[0][h] = __byte_perm(w0, w1, 0x5410);
+      x[1][h] = __byte_perm(w0, w1, 0x7632);
     } else {
-      x[h] = lds16(at) | (lds16(at + 4 * ROWB) << 16);
+      x[0][h] = lds16(at) | (lds16(at + 4 * ROWB) << 16);
     }
   }
-  uint32_t r[4], t[4];
-  unpack8(r, x[0]);
-  unpack8(t, x[1]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) mma16(o[i], p, r[i], t[i]);
-  if constexpr (D == 64) {
-    unpack8(r, y[0]);
-    unpack8(t, y[1]);
+  for (int k = 0; k < D / 32; ++k) {
+    uint32_t a[4], b[4];
+    unpack8(a[0], a[1], b[0], b[1], x[k][0], exps);
+    unpack8(a[2], a[3], b[2], b[3], x[k][1], exps);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mma16(o[4 + i], p, r[i], t[i]);
+    for (int i = 0; i < NQ; ++i) {
+      mma16(o[i][2 * k], a, p[i][0], p[i][1]);
+      mma16(o[i][2 * k + 1], b, p[i][0], p[i][1]);
+    }
   }
 }
 
@@ -285,7 +320,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
                     const int32_t* __restrict__ lens, __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, Dec4Shape w,
                     Dec4Scratch ws, int* err) {
   using Cfg = Dec4Cfg<D, QR>;
-  constexpr int ROWB = Cfg::ROWB, NT = D / 8, RH = QR == 16 ? 2 : 1;
+  constexpr int ROWB = Cfg::ROWB, NT = D / 16, NQ = QR / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
   int* s_prefix = reinterpret_cast<int*>(smem + nwarps * Cfg::WARP);     // [B + 1]
@@ -419,15 +454,15 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   for (int s = 0; s < Cfg::STAGES - 1; ++s)
     if (issued < count) issue();
 
-  float o[NT][4];                                    // times 2^(15 - e)
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, off[2] = {0.0f, 0.0f};   // rows lane / 4 and lane / 4 + 8
-  uint32_t qf[D / 16][4];
-  float qsum[2] = {0.0f, 0.0f}, qc[2] = {0.0f, 0.0f};
+  const Exponents exps;
+  float o[NQ][NT][4];                                // times 2^(15 - e)
+  float m[NQ][2], l[NQ][2], off[NQ][2];              // of heads 8 i + 2 q and the next
+  Queries<D> qs[NQ];
   int e = 0;                                         // 2^e is above every scale and lowest value of the segment's rows
   float into = 0.0f;                                 // 2^(15 - e)
   bool whole = false;                                // the segment's units so far are all in this warp's range
   uint32_t slot0 = 0;                                // of the two places for partial results
-  const int qrow = lane >> 2, q4 = lane & 3;
+  const int n8 = lane >> 2, q4 = lane & 3;
   const uint32_t factors = ring + Cfg::FACTORS;
   int stage = 0;                                     // that is read
   uint32_t phase = 0;
@@ -442,22 +477,24 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       return;
     }
     const uint32_t st = ring + stage * Cfg::STAGE;
-    const int gn = min(w.G - at.mt * 16, 16);
     if (n == 0 || at.tile == 0) {
       whole = at.tile == 0;
       slot0 = n == 0 ? 0 : 1;
       e = -111;
       into = exp2_of(15 - e);
 #pragma unroll
-      for (int rh = 0; rh < 2; ++rh) {
-        m[rh] = -INFINITY;
-        l[rh] = off[rh] = 0.0f;
+      for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          m[i][k] = -INFINITY;
+          l[i][k] = off[i][k] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][j][k] = 0.0f;
+        qs[i].take(w.scale_log2, st + Cfg::QUERIES + i * 16 * D, w.G - at.mt * 16 - 8 * i, lane);
       }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-      take_queries<D, QR>(qf, qsum, qc, w.scale_log2, st + Cfg::QUERIES, gn, lane);
     }
     uint32_t seen = kAll;                            // the tile's rows that are
     {                                                // row `lane`'s factors
@@ -478,105 +515,120 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         e = up;
         into = exp2_of(15 - e);
 #pragma unroll
-        for (int rh = 0; rh < RH; ++rh) {
-          off[rh] *= less;
+        for (int i = 0; i < NQ; ++i) {
+          off[i][0] *= less;
+          off[i][1] *= less;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[j][2 * rh] *= less;
-            o[j][2 * rh + 1] *= less;
-          }
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][j][k] *= less;
         }
       }
       sts128f(factors + 16 * lane, scale_of(kr), low_of(kr), vs * into, fmaf(8.0f, vs, vl) * into);
     }
-    float s[4][4];
-    code_scores<D>(s, qf, qsum, st, lane);
+    float s[NQ][2][4];
+    code_scores<D, NQ>(s, qs, st, lane, exps);
     __syncwarp();
-    float2 vf[4][2];                                 // the value rows' factors
+    float2 vf[4];                                    // the value rows' factors, of rows 8 r + row_in_eight(n8)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int r = 0; r < 4; ++r) {
+      const float4 f = lds128f(factors + 16 * (8 * r + row_in_eight(n8)));
+      vf[r] = make_float2(f.z, f.w);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 f = lds128f(factors + 16 * (16 * (j >> 1) + 8 * (j & 1) + 4 * i + q4));
-        vf[j][i] = make_float2(f.z, f.w);
-        s[j][i] = fmaf(f.x, s[j][i], f.y * qsum[0]);
-        if (RH == 2) s[j][2 + i] = fmaf(f.x, s[j][2 + i], f.y * qsum[1]);
-      }
+      for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float& x = s[i][r >> 1][2 * (r & 1) + k];
+          x = fmaf(f.x, x, f.y * qs[i].sum[k]);
+        }
+    }
     if (seen != kAll) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int r = 0; r < 4; ++r)
+        if (!((seen >> (8 * r + row_in_eight(n8))) & 1u))
 #pragma unroll
-        for (int i = 0; i < 2 * RH; ++i)
-          if (!((seen >> (16 * (j >> 1) + 8 * (j & 1) + 4 * (i & 1) + q4)) & 1u)) s[j][i] = -INFINITY;
+          for (int i = 0; i < NQ; ++i) s[i][r >> 1][2 * (r & 1)] = s[i][r >> 1][2 * (r & 1) + 1] = -INFINITY;
     }
 #pragma unroll
-    for (int rh = 0; rh < RH; ++rh) {
-      float mx = fmax3(s[0][2 * rh], s[0][2 * rh + 1], s[1][2 * rh]);
-      mx = fmax3(mx, s[1][2 * rh + 1], s[2][2 * rh]);
-      mx = fmax3(mx, s[2][2 * rh + 1], s[3][2 * rh]);
-      mx = fmaxf(mx, s[3][2 * rh + 1]) * qc[rh];
-      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
-      mx = fmaxf(mx, m[rh]);
-      const float ref = mx == -INFINITY ? 0.0f : mx;   // every score so far -inf: every term is 2^-inf
-      if (__any_sync(kAll, mx > m[rh])) {            // a new maximum
-        const float a = ex2_approx(m[rh] - ref);
-        m[rh] = mx;
-        l[rh] *= a;
-        off[rh] *= a;
+    for (int i = 0; i < NQ; ++i) {
+      float mx[2], ref[2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          o[j][2 * rh] *= a;
-          o[j][2 * rh + 1] *= a;
+      for (int k = 0; k < 2; ++k) {
+        float x = fmax3(s[i][0][k], s[i][0][2 + k], s[i][1][k]);
+        x = fmaxf(x, s[i][1][2 + k]) * qs[i].c[k];
+        x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+        mx[k] = fmaxf(x, m[i][k]);
+        ref[k] = mx[k] == -INFINITY ? 0.0f : mx[k];  // every score so far -inf: every term is 2^-inf
+      }
+      if (__any_sync(kAll, mx[0] > m[i][0] || mx[1] > m[i][1])) {   // a new maximum
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float a = ex2_approx(m[i][k] - ref[k]);
+          m[i][k] = mx[k];
+          l[i][k] *= a;
+          off[i][k] *= a;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            o[i][j][k] *= a;
+            o[i][j][2 + k] *= a;
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float p = ex2_approx(fmaf(s[j][2 * rh + i], qc[rh], -ref));
-          l[rh] += p;
-          off[rh] = fmaf(p, vf[j][i].y, off[rh]);
-          s[j][2 * rh + i] = p * vf[j][i].x;
+        for (int k = 0; k < 2; ++k) {
+          float& x = s[i][r >> 1][2 * (r & 1) + k];
+          const float p = ex2_approx(fmaf(x, qs[i].c[k], -ref[k]));
+          l[i][k] += p;
+          off[i][k] = fmaf(p, vf[r].y, off[i][k]);
+          x = p * vf[r].x;
         }
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) add_codes<D, RH>(o, s[2 * k], s[2 * k + 1], st + Cfg::TILE + 16 * k * ROWB, lane);
+    for (int j = 0; j < 2; ++j) add_codes<D, NQ>(o, s, j, st + Cfg::TILE + 16 * j * ROWB, lane, exps);
     const bool ends = at.tile == at.t.count - 1;
     if (ends || n == count - 1) {                    // the piece is done
       whole = whole && ends;                         // it holds all of the segment's units
       const size_t slot = static_cast<size_t>(gw) * 2 + slot0;
       const float back = exp2_of((e - 15) / 2), rest = exp2_of(e - 15 - (e - 15) / 2);   // 2^(e - 15) in two steps
+      const int gn = min(w.G - at.mt * 16, 16);
 #pragma unroll
-      for (int rh = 0; rh < RH; ++rh) {
-        float lt = l[rh], ot = off[rh];
-        lt += __shfl_xor_sync(kAll, lt, 1);
-        lt += __shfl_xor_sync(kAll, lt, 2);
-        ot += __shfl_xor_sync(kAll, ot, 1);
-        ot += __shfl_xor_sync(kAll, ot, 2);
-        const int r = qrow + 8 * rh;
-        if (r >= gn) continue;
-        float v[D / 4];                              // values D / 4 q4 .. of the head
+      for (int i = 0; i < NQ; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int k = 0; k < 2; ++k) {
+          float lt = l[i][k], ot = off[i][k];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) v[i * NT + j] = (o[j][2 * rh + i] + ot) * back * rest;
-        if (whole) {
-          const size_t head = static_cast<size_t>(at.b) * w.H + at.kh * w.G + at.mt * 16 + r;
-          const float inv = 1.0f / lt;               // (a sum of 0, every score -inf, gives NaN)
-          uint4* dst = reinterpret_cast<uint4*>(y + head * D + q4 * (D / 4));
+          for (int x = 4; x < 32; x <<= 1) {
+            lt += __shfl_xor_sync(kAll, lt, x);
+            ot += __shfl_xor_sync(kAll, ot, x);
+          }
+          const int r = 8 * i + 2 * q4 + k;
+          if (r >= gn) continue;
+          float v[D / 8];                            // values D / 8 n8 .. of the head
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            dst[k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv), pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                                pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv), pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
-          if (q4 == 0 && lse2) lse2[head] = m[rh] + log2f(lt);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(ws.o + (slot * QR + r) * D + q4 * (D / 4));
+          for (int j = 0; j < NT; ++j) {
+            v[2 * j] = (o[i][j][k] + ot) * back * rest;
+            v[2 * j + 1] = (o[i][j][2 + k] + ot) * back * rest;
+          }
+          if (whole) {
+            const size_t head = static_cast<size_t>(at.b) * w.H + at.kh * w.G + at.mt * 16 + r;
+            const float inv = 1.0f / lt;             // (a sum of 0, every score -inf, gives NaN)
+            uint32_t h[D / 16];
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          if (q4 == 0) ws.ml[slot * QR + r] = make_float2(m[rh], lt);
+            for (int j = 0; j < NT; ++j) h[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+            if constexpr (D == 64) *reinterpret_cast<uint4*>(y + head * D + 8 * n8) = make_uint4(h[0], h[1], h[2], h[3]);
+            else *reinterpret_cast<uint2*>(y + head * D + 4 * n8) = make_uint2(h[0], h[1]);
+            if (n8 == 0 && lse2) lse2[head] = m[i][k] + log2f(lt);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(ws.o + (slot * QR + r) * D + n8 * (D / 8));
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            if (n8 == 0) ws.ml[slot * QR + r] = make_float2(m[i][k], lt);
+          }
         }
-      }
     }
     advance(at);
     stage = stage == Cfg::STAGES - 1 ? 0 : stage + 1;
