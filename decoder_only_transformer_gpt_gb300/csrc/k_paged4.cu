@@ -24,11 +24,10 @@ namespace gptgb {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kUnit4 = 32;                // seen rows per unit
 
 // Bound by issuing instructions, about 400 for a unit: a byte of codes takes a warp four times the unpacking and products of
 // a byte of bf16, and the integer unit takes a warp's instruction only every other cycle. Work is dealt as in the 16-bit
-// cache's kernel (k_paged.cu): units of 32 seen rows of one (sequence, key head, group of up to 16 query heads), equal
+// cache's kernel (k_paged.cu): units of 64 rows (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal
 // contiguous ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
 //    memory as they lie there, without ldmatrix: a lane takes a quarter of a key row (8 bytes: its codes are the lane's
@@ -37,21 +36,22 @@ constexpr int kUnit4 = 32;                // seen rows per unit
 //    columns, so that one key head for each query head wastes half as much as with the heads as rows; the probabilities are
 //    turned over by movmatrix.
 //  * A row's scales and lowest values are made into fp32 factors once, by the lane of its number.
-//  * Units are whole 32-row tiles of the sequence, so a page's share of one is contiguous and starts on a 16-byte boundary:
+//  * Units are whole tiles of the sequence, so a page's share of one is contiguous and starts on a 16-byte boundary:
 //    a few bulk copies, a lane each, bring codes and ranges into the warp's own ring (16 warps per SM), counted by an
 //    mbarrier per stage. (Copies of 16 bytes by every lane took 250 of 680 instructions a unit to find their addresses, and 131
 //    us for 16 sequences of 9,000 to 32,000 rows.) Rows of a tile that are not seen are masked: their codes are numbers whatever
 //    they hold, their factors are set to 0.
 template <int D, int QR>
 struct Dec4Cfg {
+  static constexpr int UNIT = QR == 8 ? 64 : 32;                  // rows of a unit
   static constexpr int ROWB = D / 2;                              // bytes of a row's codes
-  static constexpr int TILE = kUnit4 * ROWB;                      // keys, or values, of a unit
+  static constexpr int TILE = UNIT * ROWB;                        // keys, or values, of a unit
   static constexpr int RANGES = 2 * TILE;                         // offset of the keys' ranges, then the values'
-  static constexpr int QUERIES = RANGES + kUnit4 * 8;             // offset of the query rows (where a unit starts a segment)
+  static constexpr int QUERIES = RANGES + UNIT * 8;               // offset of the query rows (where a unit starts a segment)
   static constexpr int STAGE = QUERIES + QR * D * 2;
-  static constexpr int STAGES = QR == 8 ? 4 : 3;
+  static constexpr int STAGES = QR == 8 ? 2 : 3;
   static constexpr int FACTORS = STAGES * STAGE;                  // the rows' factors: behind the stages
-  static constexpr int BARS = FACTORS + kUnit4 * 16;              // the stages' mbarriers
+  static constexpr int BARS = FACTORS + UNIT * 16;                // the stages' mbarriers
   static constexpr int WARP = BARS + 64;
   static constexpr int WARPS = 16;
 };
@@ -214,12 +214,12 @@ struct Queries {
   }
 };
 
-// Products q . code of the 32 key rows at sk, two tiles of 16.
-template <int D, int NQ>
-__device__ __forceinline__ void code_scores(float (&s)[NQ][2][4], const Queries<D> (&q)[NQ], uint32_t sk, int lane, const Exponents& exps) {
+// Products q . code of the key rows at sk, NJ tiles of 16.
+template <int D, int NQ, int NJ>
+__device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], const Queries<D> (&q)[NQ], uint32_t sk, int lane, const Exponents& exps) {
   const uint32_t at = sk + row_in_eight(lane >> 2) * (D / 2) + (lane & 3) * (D / 8);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < NJ; ++j) {
     uint32_t w[2][2];                                // rows n and n + 8
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -248,8 +248,8 @@ __device__ __forceinline__ void code_scores(float (&s)[NQ][2][4], const Queries<
 
 // O += (code - 8) P for 16 value rows at sv; s: a tile of scores, now p times the rows' scales. Tile t of O has values
 // 8 n + 2 t and, in its lower half, 8 n + 2 t + 1 as rows (D = 32: 4 n + ..).
-template <int D, int NQ>
-__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const float (&s)[NQ][2][4], int j, uint32_t sv, int lane, const Exponents& exps) {
+template <int D, int NQ, int NJ>
+__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const float (&s)[NQ][NJ][4], int j, uint32_t sv, int lane, const Exponents& exps) {
   uint32_t p[NQ][2];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
@@ -282,26 +282,28 @@ __device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const float
   }
 }
 
-// The tiles of 32 rows that hold the rows which a sequence's query sees, of n rows: v < head at the start, then from `gap`
+// The tiles of UNIT rows that hold the rows which a sequence's query sees, of n rows: v < head at the start, then from `gap`
 // tiles on.
 struct Tiles {
   int n, head, gap, count;
 };
+template <int UNIT>
 __device__ __forceinline__ Tiles tiles_of(int n, int window, int sinks) {
   Tiles t;
   t.n = n;
-  t.count = (n + kUnit4 - 1) / kUnit4;
+  t.count = (n + UNIT - 1) / UNIT;
   t.head = t.count;
   t.gap = 0;
   if (window > 0 && window < n) {
-    const int first = n - window, from = first / kUnit4;   // the first row of the window, and its tile
-    t.head = min((min(sinks, first) + kUnit4 - 1) / kUnit4, from);
+    const int first = n - window, from = first / UNIT;   // the first row of the window, and its tile
+    t.head = min((min(sinks, first) + UNIT - 1) / UNIT, from);
     t.gap = from - t.head;
     t.count -= t.gap;
   }
   return t;
 }
-__device__ __forceinline__ int first_row(const Tiles& t, int v) { return (v < t.head ? v : v + t.gap) * kUnit4; }
+template <int UNIT>
+__device__ __forceinline__ int first_row(const Tiles& t, int v) { return (v < t.head ? v : v + t.gap) * UNIT; }
 
 // The list position of a unit: sequence, key head, group of its query heads, tile of the sequence's seen rows.
 struct Unit4 {
@@ -320,7 +322,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
                     const int32_t* __restrict__ lens, __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, Dec4Shape w,
                     Dec4Scratch ws, int* err) {
   using Cfg = Dec4Cfg<D, QR>;
-  constexpr int ROWB = Cfg::ROWB, NT = D / 16, NQ = QR / 8;
+  constexpr int ROWB = Cfg::ROWB, UNIT = Cfg::UNIT, NT = D / 16, NQ = QR / 8, NJ = UNIT / 16, NH = UNIT / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
   int* s_prefix = reinterpret_cast<int*>(smem + nwarps * Cfg::WARP);     // [B + 1]
@@ -341,7 +343,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       rows = rows_of(c, w, __ldg(lens + b));
       if (rows == -2) record_error(err, GPT_DEV_EPAGE);
       rows = max(rows, 0);
-      x = tiles_of(rows, w.window, w.sinks).count;
+      x = tiles_of<UNIT>(rows, w.window, w.sinks).count;
       s_rows[b] = rows;
     }
     int incl = x;
@@ -383,7 +385,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   __syncwarp();
   const int row = w.H + 2 * c.Hkv;                   // heads of a token's row
 
-  auto set_seq = [&](Unit4& x) { x.t = tiles_of(s_rows[x.b], w.window, w.sinks); };   // (b has units)
+  auto set_seq = [&](Unit4& x) { x.t = tiles_of<UNIT>(s_rows[x.b], w.window, w.sinks); };   // (b has units)
   auto advance = [&](Unit4& x) {
     if (++x.tile < x.t.count) return;
     x.tile = 0;
@@ -411,21 +413,21 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     at.mt = hm - at.kh * w.mg;
     at.tile = static_cast<int>(r - static_cast<long long>(hm) * at.t.count);
   }
-  // A tile lies in 32 / page pages, or in part of one: runs of rows. Lane 4 run + kind copies the run's key codes (kind 0),
+  // A tile lies in UNIT / page pages, or in part of one: runs of rows. Lane 4 run + kind copies the run's key codes (kind 0),
   // value codes (1), key ranges (2) or value ranges (3). Its page is looked up one unit ahead.
-  const int run_log2 = min(c.page_log2, 5), kind = lane & 3, run0 = (lane >> 2) << run_log2;   // run0: the run's first row
+  const int run_log2 = min(c.page_log2, UNIT == 64 ? 6 : 5), kind = lane & 3, run0 = (lane >> 2) << run_log2;   // run0: the run's first row
   const uint32_t rowb = kind < 2 ? ROWB : 4, bytes = rowb << run_log2;
-  const uint32_t to = (kind < 2 ? kind * Cfg::TILE : Cfg::RANGES + (kind - 2) * kUnit4 * 4) + run0 * rowb;
+  const uint32_t to = (kind < 2 ? kind * Cfg::TILE : Cfg::RANGES + (kind - 2) * UNIT * 4) + run0 * rowb;
   const uint32_t pageb = (2u * static_cast<uint32_t>(c.Hkv) << c.page_log2) * rowb;   // a page's codes, or ranges
   const uint8_t* from = (kind < 2 ? static_cast<const uint8_t*>(c.pool) : reinterpret_cast<const uint8_t*>(ranges)) + (kind & 1) * (pageb / 2);
   const uint32_t in_page = static_cast<uint32_t>(run0 & ((1 << c.page_log2) - 1)) * rowb, headb = rowb << c.page_log2;
-  const uint32_t tile_mask = ((1u << c.page_log2) - 1u) & ~31u;   // of a tile's first row: where in its page
+  const uint32_t tile_mask = ((1u << c.page_log2) - 1u) & ~(UNIT - 1u);   // of a tile's first row: where in its page
   Unit4 next = at;                                   // the unit whose rows are copied next
   int pg, r0;                                        // the run's page; -2: nothing to copy. The tile's first row
   auto look_up = [&]() {
-    r0 = first_row(next.t, next.tile);
+    r0 = first_row<UNIT>(next.t, next.tile);
     const int r = r0 + run0;
-    pg = run0 < kUnit4 && r < next.t.n ? __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (r >> c.page_log2)) : -2;
+    pg = run0 < UNIT && r < next.t.n ? __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (r >> c.page_log2)) : -2;
   };
   look_up();
   int issued = 0, fill = 0;                          // fill: the stage that is filled next
@@ -496,18 +498,29 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         qs[i].take(w.scale_log2, st + Cfg::QUERIES + i * 16 * D, w.G - at.mt * 16 - 8 * i, lane);
       }
     }
-    uint32_t seen = kAll;                            // the tile's rows that are
-    {                                                // row `lane`'s factors
-      const uint32_t kr = lds32(st + Cfg::RANGES + 4 * lane);
-      uint32_t vr = lds32(st + Cfg::RANGES + kUnit4 * 4 + 4 * lane);
-      const int f = first_row(at.t, at.tile), after = at.t.n - w.window;   // the window's first row
-      if (f + kUnit4 > at.t.n || (w.window > 0 && f < after && f + kUnit4 > w.sinks)) {
-        const bool mine = f + lane < at.t.n && (w.window == 0 || f + lane >= after || f + lane < w.sinks);
-        seen = __ballot_sync(kAll, mine);
-        if (!mine) vr = 0u;
+    uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
+    {                                                // the factors of rows `lane` and, of a unit of 64, 32 + lane
+      const int f = first_row<UNIT>(at.t, at.tile), after = at.t.n - w.window;   // the window's first row
+      const bool cut = f + UNIT > at.t.n || (w.window > 0 && f < after && f + UNIT > w.sinks);
+      float ks[NH], kl[NH], vs[NH], vl[NH], size = 0.0f;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const uint32_t kr = lds32(st + Cfg::RANGES + 4 * (32 * h + lane));
+        uint32_t vr = lds32(st + Cfg::RANGES + 4 * (UNIT + 32 * h + lane));
+        seen[h] = kAll;
+        if (cut) {
+          const int r = f + 32 * h + lane;
+          const bool mine = r < at.t.n && (w.window == 0 || r >= after || r < w.sinks);
+          seen[h] = __ballot_sync(kAll, mine);
+          if (!mine) vr = 0u;
+        }
+        unseen |= ~seen[h];
+        ks[h] = scale_of(kr);
+        kl[h] = low_of(kr);
+        vs[h] = scale_of(vr);
+        vl[h] = low_of(vr);
+        size = fmax3(size, vs[h], fabsf(vl[h]));
       }
-      const float vs = scale_of(vr), vl = low_of(vr);
-      const float size = fmaxf(vs, fabsf(vl));
       if (__any_sync(kAll, size * into >= 32768.0f)) {   // (rarely: 2^e has to grow, and o and off with it)
         const uint32_t top = __reduce_max_sync(kAll, __float_as_uint(size) & 0x7fffffffu);
         const int up = min(exponent_of(__uint_as_float(top)) + 1, 128);
@@ -524,14 +537,16 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
             for (int k = 0; k < 4; ++k) o[i][j][k] *= less;
         }
       }
-      sts128f(factors + 16 * lane, scale_of(kr), low_of(kr), vs * into, fmaf(8.0f, vs, vl) * into);
-    }
-    float s[NQ][2][4];
-    code_scores<D, NQ>(s, qs, st, lane, exps);
-    __syncwarp();
-    float2 vf[4];                                    // the value rows' factors, of rows 8 r + row_in_eight(n8)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+      for (int h = 0; h < NH; ++h)
+        sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h] * into, fmaf(8.0f, vs[h], vl[h]) * into);
+    }
+    float s[NQ][NJ][4];
+    code_scores<D, NQ, NJ>(s, qs, st, lane, exps);
+    __syncwarp();
+    float2 vf[2 * NJ];                               // the value rows' factors, of rows 8 r + row_in_eight(n8)
+#pragma unroll
+    for (int r = 0; r < 2 * NJ; ++r) {
       const float4 f = lds128f(factors + 16 * (8 * r + row_in_eight(n8)));
       vf[r] = make_float2(f.z, f.w);
 #pragma unroll
@@ -542,10 +557,10 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
           x = fmaf(f.x, x, f.y * qs[i].sum[k]);
         }
     }
-    if (seen != kAll) {
+    if (unseen) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (!((seen >> (8 * r + row_in_eight(n8))) & 1u))
+      for (int r = 0; r < 2 * NJ; ++r)
+        if (!((seen[r >> 2] >> (8 * (r & 3) + row_in_eight(n8))) & 1u))
 #pragma unroll
           for (int i = 0; i < NQ; ++i) s[i][r >> 1][2 * (r & 1)] = s[i][r >> 1][2 * (r & 1) + 1] = -INFINITY;
     }
@@ -554,8 +569,10 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       float mx[2], ref[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float x = fmax3(s[i][0][k], s[i][0][2 + k], s[i][1][k]);
-        x = fmaxf(x, s[i][1][2 + k]) * qs[i].c[k];
+        float x = s[i][0][k];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) x = j ? fmax3(x, s[i][j][k], s[i][j][2 + k]) : fmaxf(x, s[i][j][2 + k]);
+        x *= qs[i].c[k];
         x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
         x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
         x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
@@ -577,7 +594,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 2 * NJ; ++r)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float& x = s[i][r >> 1][2 * (r & 1) + k];
@@ -588,7 +605,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) add_codes<D, NQ>(o, s, j, st + Cfg::TILE + 16 * j * ROWB, lane, exps);
+    for (int j = 0; j < NJ; ++j) add_codes<D, NQ, NJ>(o, s, j, st + Cfg::TILE + 16 * j * ROWB, lane, exps);
     const bool ends = at.tile == at.t.count - 1;
     if (ends || n == count - 1) {                    // the piece is done
       whole = whole && ends;                         // it holds all of the segment's units
