@@ -43,17 +43,18 @@ constexpr unsigned kAll = 0xffffffffu;
 //    they hold, their factors are set to 0.
 template <int D, int QR>
 struct Dec4Cfg {
-  static constexpr int UNIT = QR == 8 ? 64 : 32;                  // rows of a unit
+  static constexpr int UNIT = QR == 16 ? 32 : 64;                 // rows of a unit
   static constexpr int ROWB = D / 2;                              // bytes of a row's codes
   static constexpr int TILE = UNIT * ROWB;                        // keys, or values, of a unit
   static constexpr int RANGES = 2 * TILE;                         // offset of the keys' ranges, then the values'
   static constexpr int QUERIES = RANGES + UNIT * 8;               // offset of the query rows (where a unit starts a segment)
   static constexpr int STAGE = QUERIES + QR * D * 2;
-  static constexpr int STAGES = QR == 8 ? 2 : 3;
+  static constexpr int STAGES = QR == 16 ? 3 : 2;
   static constexpr int FACTORS = STAGES * STAGE;                  // the rows' factors: behind the stages
-  static constexpr int BARS = FACTORS + UNIT * 16;                // the stages' mbarriers
-  static constexpr int WARP = BARS + 64;
-  static constexpr int WARPS = 16;
+  // one head a key head: its scores of 64 rows, its factors as fp16, zeros for the products' other columns
+  static constexpr int BARS = FACTORS + (QR == 1 ? 256 + 128 + 32 : UNIT * 16);   // the stages' mbarriers
+  static constexpr int WARP = BARS + 32;
+  static constexpr int WARPS = QR == 1 ? 20 : 16;
 };
 
 struct Dec4Scratch {
@@ -108,6 +109,9 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
                "{%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void sts16(uint32_t a, float x) {   // as fp16
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(__half_as_ushort(__float2half_rn(x))) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -177,7 +181,7 @@ struct Queries {
     float v[C], top = 0.0f, mine = 0.0f;
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {
-      uint4 x = lds128(sq + (lane >> 2) * D * 2 + ((lane & 3) * C + 8 * w) * 2);
+      uint4 x = lds128(sq + min(lane >> 2, max(gn - 1, 0)) * D * 2 + ((lane & 3) * C + 8 * w) * 2);
       if ((lane >> 2) >= gn) x = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -246,16 +250,10 @@ __device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], const Queries
   }
 }
 
-// O += (code - 8) P for 16 value rows at sv; s: a tile of scores, now p times the rows' scales. Tile t of O has values
-// 8 n + 2 t and, in its lower half, 8 n + 2 t + 1 as rows (D = 32: 4 n + ..).
-template <int D, int NQ, int NJ>
-__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const float (&s)[NQ][NJ][4], int j, uint32_t sv, int lane, const Exponents& exps) {
-  uint32_t p[NQ][2];
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
-    p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
-  }
+// O += (code - 8) P for 16 value rows at sv; p: probabilities times the rows' scales, as second operands. Tile t of O has
+// values 8 n + 2 t and, in its lower half, 8 n + 2 t + 1 as rows (D = 32: 4 n + ..).
+template <int D, int NQ>
+__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint32_t (&p)[NQ][2], uint32_t sv, int lane, const Exponents& exps) {
   constexpr int ROWB = D / 2;
   uint32_t x[2][2];                                  // rows (0, 4) + q, then (8, 12) + q: codes 0-3 and, of D = 64, 4-7 of a word
 #pragma unroll
@@ -317,17 +315,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 template <int D, int QR>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(32 * Dec4Cfg<D, QR>::WARPS, 1)
 paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __nv_bfloat16* __restrict__ qkv,
                     const int32_t* __restrict__ lens, __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, Dec4Shape w,
                     Dec4Scratch ws, int* err) {
   using Cfg = Dec4Cfg<D, QR>;
-  constexpr int ROWB = Cfg::ROWB, UNIT = Cfg::UNIT, NT = D / 16, NQ = QR / 8, NJ = UNIT / 16, NH = UNIT / 32;
+  constexpr int ROWB = Cfg::ROWB, UNIT = Cfg::UNIT, NT = D / 16, NQ = (QR + 7) / 8, NJ = UNIT / 16, NH = UNIT / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
   int* s_prefix = reinterpret_cast<int*>(smem + nwarps * Cfg::WARP);     // [B + 1]
   int* s_rows = s_prefix + w.B + 1;                                      // [B]
-  __shared__ int s_sum[16];
+  __shared__ int s_sum[Cfg::WARPS];
   __shared__ int s_abort;
   if (threadIdx.x == 0) s_abort = 0;
   pdl_wait();
@@ -456,6 +454,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   for (int s = 0; s < Cfg::STAGES - 1; ++s)
     if (issued < count) issue();
 
+  constexpr bool ONE = QR == 1;
   const Exponents exps;
   float o[NQ][NT][4];                                // times 2^(15 - e)
   float m[NQ][2], l[NQ][2], off[NQ][2];              // of heads 8 i + 2 q and the next
@@ -466,6 +465,9 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   uint32_t slot0 = 0;                                // of the two places for partial results
   const int n8 = lane >> 2, q4 = lane & 3;
   const uint32_t factors = ring + Cfg::FACTORS;
+  if constexpr (ONE) {
+    if (lane < 2) sts128f(factors + 256 + 128 + 16 * lane, 0.0f, 0.0f, 0.0f, 0.0f);
+  }
   int stage = 0;                                     // that is read
   uint32_t phase = 0;
   for (int n = 0; n < count; ++n) {
@@ -497,12 +499,17 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
           for (int k = 0; k < 4; ++k) o[i][j][k] = 0.0f;
         qs[i].take(w.scale_log2, st + Cfg::QUERIES + i * 16 * D, w.G - at.mt * 16 - 8 * i, lane);
       }
+      if constexpr (ONE) {                           // every lane has rows of the one head
+        qs[0].sum[0] = __shfl_sync(kAll, qs[0].sum[0], 0);
+        qs[0].c[0] = __shfl_sync(kAll, qs[0].c[0], 0);
+      }
     }
     uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
-    {                                                // the factors of rows `lane` and, of a unit of 64, 32 + lane
+    float ks[NH], kl[NH], vs[NH], vl[NH];            // the factors of rows `lane` and, of a unit of 64, 32 + lane
+    {
       const int f = first_row<UNIT>(at.t, at.tile), after = at.t.n - w.window;   // the window's first row
       const bool cut = f + UNIT > at.t.n || (w.window > 0 && f < after && f + UNIT > w.sinks);
-      float ks[NH], kl[NH], vs[NH], vl[NH], size = 0.0f;
+      float size = 0.0f;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         const uint32_t kr = lds32(st + Cfg::RANGES + 4 * (32 * h + lane));
@@ -538,11 +545,65 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         }
       }
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
-        sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h] * into, fmaf(8.0f, vs[h], vl[h]) * into);
+      for (int h = 0; h < NH; ++h) {
+        vl[h] = fmaf(8.0f, vs[h], vl[h]) * into;
+        vs[h] *= into;
+        if constexpr (!ONE) sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h], vl[h]);
+      }
     }
     float s[NQ][NJ][4];
     code_scores<D, NQ, NJ>(s, qs, st, lane, exps);
+    if constexpr (ONE) {
+      // One head: lanes 4 n have its 64 products, which go round the warp, two rows a lane.
+      if (q4 == 0) {
+        sts128f(factors + 32 * n8, s[0][0][0], s[0][0][2], s[0][1][0], s[0][1][2]);
+        sts128f(factors + 32 * n8 + 16, s[0][2][0], s[0][2][2], s[0][3][0], s[0][3][2]);
+      }
+      __syncwarp();
+      float x[2];
+      // row 8 v + i of the tile is value v of lane 4 n with row_in_eight(n) = i
+      const uint32_t mine = factors + 32 * (2 * (lane & 3) + ((lane >> 2) & 1)) + 4 * (lane >> 3);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        x[h] = fmaf(ks[h], __uint_as_float(lds32(mine + 16 * h)), kl[h] * qs[0].sum[0]);
+        if (!((seen[h] >> lane) & 1u)) x[h] = -INFINITY;
+      }
+      float mx = fmaxf(x[0], x[1]) * qs[0].c[0];
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, k));
+      mx = fmaxf(mx, m[0][0]);
+      const float ref = mx == -INFINITY ? 0.0f : mx;   // every score so far -inf: every term is 2^-inf
+      if (mx > m[0][0]) {                            // a new maximum (the same for all lanes)
+        const float a = ex2_approx(m[0][0] - ref);
+        m[0][0] = mx;
+        l[0][0] *= a;
+        off[0][0] *= a;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[0][j][0] *= a;
+          o[0][j][2] *= a;
+        }
+      }
+      // as second operands: lane q of head 0 takes of rows 8 v the rows q and q + 4, eight words of fp16 pairs
+      const uint32_t weights = factors + 256;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p = ex2_approx(fmaf(x[h], qs[0].c[0], -ref));
+        l[0][0] += p;
+        off[0][0] = fmaf(p, vl[h], off[0][0]);
+        sts16(weights + 32 * (lane & 3) + 16 * h + 4 * (lane >> 3) + 2 * ((lane >> 2) & 1), p * vs[h]);
+      }
+      __syncwarp();
+      const uint32_t pa = n8 == 0 ? weights + 32 * q4 : weights + 128;   // other columns: zeros
+      const uint32_t step = n8 == 0 ? 16 : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 w4 = lds128(pa + step * h);
+        const uint32_t p0[1][2] = {{w4.x, w4.y}}, p1[1][2] = {{w4.z, w4.w}};
+        add_codes<D, NQ>(o, p0, st + Cfg::TILE + 32 * h * ROWB, lane, exps);
+        add_codes<D, NQ>(o, p1, st + Cfg::TILE + (32 * h + 16) * ROWB, lane, exps);
+      }
+    } else {
     __syncwarp();
     float2 vf[2 * NJ];                               // the value rows' factors, of rows 8 r + row_in_eight(n8)
 #pragma unroll
@@ -605,7 +666,16 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         }
     }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) add_codes<D, NQ, NJ>(o, s, j, st + Cfg::TILE + 16 * j * ROWB, lane, exps);
+    for (int j = 0; j < NJ; ++j) {
+      uint32_t p[NQ][2];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
+        p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
+      }
+      add_codes<D, NQ>(o, p, st + Cfg::TILE + 16 * j * ROWB, lane, exps);
+    }
+    }
     const bool ends = at.tile == at.t.count - 1;
     if (ends || n == count - 1) {                    // the piece is done
       whole = whole && ends;                         // it holds all of the segment's units
@@ -618,7 +688,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         for (int k = 0; k < 2; ++k) {
           float lt = l[i][k], ot = off[i][k];
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) {
+          for (int x = ONE ? 1 : 4; x < 32; x <<= 1) {
             lt += __shfl_xor_sync(kAll, lt, x);
             ot += __shfl_xor_sync(kAll, ot, x);
           }
@@ -779,10 +849,10 @@ cudaError_t launch_paged_attention4(const PagedCache& c, const void* ranges, con
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(qkv);
   const uint32_t* r = static_cast<const uint32_t*>(ranges);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(y);
-  // up to 8 query heads per key head need half of the 16 query rows in shared memory and registers
-  if (D == 64)
-    return w.G <= 8 ? launch_decode4<64, 8>(c, r, x, lens, o, lse2, w, err, s) : launch_decode4<64, 16>(c, r, x, lens, o, lse2, w, err, s);
-  return w.G <= 8 ? launch_decode4<32, 8>(c, r, x, lens, o, lse2, w, err, s) : launch_decode4<32, 16>(c, r, x, lens, o, lse2, w, err, s);
+  const int qr = w.G == 1 ? 1 : w.G <= 8 ? 8 : 16;
+  auto launch = D == 64 ? (qr == 1 ? launch_decode4<64, 1> : qr == 8 ? launch_decode4<64, 8> : launch_decode4<64, 16>)
+                        : (qr == 1 ? launch_decode4<32, 1> : qr == 8 ? launch_decode4<32, 8> : launch_decode4<32, 16>);
+  return launch(c, r, x, lens, o, lse2, w, err, s);
 }
 
 }  // namespace gptgb
