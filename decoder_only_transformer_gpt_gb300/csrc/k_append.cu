@@ -27,18 +27,6 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kAppendWarps = 8;
 
-// min and max that pass a NaN on
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 struct Row16 {          // 16 values of a head: units u0 and u1
   uint4 a, b;
 };
@@ -64,17 +52,18 @@ __device__ __forceinline__ void turn16(Row16& x, const float (&cs)[8], const flo
 }
 
 // The codes of a unit's eight values. v * inv + 2^23 leaves the rounded code in the low bits of the sum (ties to even, as
-// rintf); the bits above it cancel in the subtraction.
+// rintf); the bits above it cancel in the subtraction. (The largest value's code is 15: its quotient is off by the scale's
+// rounding, 15 (1 + 2^-8) at most.)
 __device__ __forceinline__ uint32_t codes8(const uint4& x, float low, float inv) {
   const uint32_t* a = &x.x;
+  const float2 neg = make_float2(-low, -low), by = make_float2(inv, inv);
+  const float m = 8388608.0f;
   uint32_t w = 0u - 0xfb000000u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float2 p = unpack_bf16x2(a[k]);
-    const float m = 8388608.0f;
-    const float lo = fminf(__fadd_rn(__fmul_rn(p.x - low, inv), m), m + 15.0f);
-    const float hi = fminf(__fadd_rn(__fmul_rn(p.y - low, inv), m), m + 15.0f);
-    w += (__float_as_uint(lo) << (8 * k)) + (__float_as_uint(hi) << (8 * k + 4));
+    const float2 n = mul2_rn(add2_rn(unpack_bf16x2(a[k]), neg), by);
+    // (a packed sum here would be joined with the product, and the product not rounded)
+    w += __float_as_uint(__fadd_rn(n.x, m)) * (1u << (8 * k)) + __float_as_uint(__fadd_rn(n.y, m)) * (16u << (8 * k));
   }
   return w;
 }
@@ -83,20 +72,20 @@ __device__ __forceinline__ uint32_t codes8(const uint4& x, float low, float inv)
 // with a value that is not finite, or a range past fp32, is NaN throughout. A scale below the normal numbers counts as 0.
 template <int LANES>
 __device__ __forceinline__ uint32_t range_of(const Row16& x, float* low, float* inv) {
-  const uint32_t* a = &x.a.x;
-  const uint32_t* b = &x.b.x;
-  float lo = INFINITY, hi = -INFINITY;
+  const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x.a.x);
+  const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&x.b.x);
+  __nv_bfloat162 mn = __hmin2_nan(a[0], b[0]), mx = __hmax2_nan(a[0], b[0]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 p = unpack_bf16x2(a[k]), q = unpack_bf16x2(b[k]);
-    lo = min_nan(lo, min_nan(min_nan(p.x, p.y), min_nan(q.x, q.y)));
-    hi = max_nan(hi, max_nan(max_nan(p.x, p.y), max_nan(q.x, q.y)));
+  for (int k = 1; k < 4; ++k) {
+    mn = __hmin2_nan(mn, __hmin2_nan(a[k], b[k]));
+    mx = __hmax2_nan(mx, __hmax2_nan(a[k], b[k]));
   }
+  // (largest, -lowest) side by side
+  __nv_bfloat162 both = __hmax2_nan(__halves2bfloat162(__low2bfloat16(mx), __hneg(__low2bfloat16(mn))),
+                                    __halves2bfloat162(__high2bfloat16(mx), __hneg(__high2bfloat16(mn))));
 #pragma unroll
-  for (int k = 1; k < LANES; k <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(kAll, lo, k));
-    hi = max_nan(hi, __shfl_xor_sync(kAll, hi, k));
-  }
+  for (int k = 1; k < LANES; k <<= 1) both = __hmax2_nan(both, __shfl_xor_sync(kAll, both, k));
+  const float hi = __low2float(both), lo = -__high2float(both);
   const float range = hi - lo;
   float scale = __bfloat162float(__float2bfloat16(__fmul_rn(range, 1.0f / 15.0f)));
   *low = lo;
@@ -172,53 +161,65 @@ append_kernel(PagedCache c, AppendArgs a, int* err) {
       sn[k] = __shfl_sync(kAll, s, (8 * i + k) & 31);
     }
   }
-  // without an output the queries are not needed
-  const int skip = dst ? 0 : a.H;
-  for (int h0 = skip + static_cast<int>(part) * HEADS; h0 < NH; h0 += 2 * HEADS * a.parts) {
-    Row16 x[2];
-    int hd[2];
+  // Heads [h0, h1), HEADS side by side in a step of the warp, two steps' loads in flight.
+  auto walk = [&](int h0, int h1, auto&& use) {
+    for (h0 += static_cast<int>(part) * HEADS; h0 < h1; h0 += 2 * HEADS * a.parts) {
+      Row16 x[2];
+      int hd[2];
+      const bool two = h0 + HEADS * a.parts < h1;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {                    // two heads' loads in flight
-      hd[k] = h0 + k * HEADS * a.parts + hh;
-      const int at = min(hd[k], NH - 1);
-      x[k].a = src[static_cast<size_t>(at) * U + u0];
-      x[k].b = src[static_cast<size_t>(at) * U + u1];
+      for (int k = 0; k < 2; ++k) {
+        hd[k] = h0 + k * HEADS * a.parts + hh;
+        if (k && !two) break;
+        const size_t at = static_cast<size_t>(min(hd[k], h1 - 1)) * U;
+        x[k].a = src[at + u0];
+        x[k].b = src[at + u1];
+      }
+      use(x[0], hd[0], hd[0] < h1);
+      if (two) use(x[1], hd[1], hd[1] < h1);
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const bool ok = hd[k] < NH, moved = turns && hd[k] < heads;
-      if (moved) turn16(x[k], cs, sn, a.interleaved);
-      if (ok && dst && (moved || !in_place)) {
-        dst[static_cast<size_t>(hd[k]) * U + u0] = x[k].a;
-        dst[static_cast<size_t>(hd[k]) * U + u1] = x[k].b;
-      }
-      if (MODE == 0) continue;
-      const int e = hd[k] - a.H;                     // key head, or Hkv + value head
-      const bool stored = ok && e >= 0 && row >= 0;
-      const long long to = row + (static_cast<long long>(e) << c.page_log2);
-      if (MODE == 1 && stored) {
-        uint4* pool = static_cast<uint4*>(c.pool);
-        pool[to * U + u0] = x[k].a;
-        pool[to * U + u1] = x[k].b;
-        if (c.weight && i == 0 && e < a.Hkv) c.weight[weight + (static_cast<size_t>(e) << c.page_log2)] = 0.0f;
-      }
-      if (MODE == 2) {
-        float low, inv;
-        const uint32_t range = range_of<LANES>(x[k], &low, &inv);
-        if (stored) {
-          uint32_t* codes = static_cast<uint32_t*>(c.pool) + to * U;
-          const uint32_t ca = range == 0x7fff7fffu ? 0u : codes8(x[k].a, low, inv), cb = range == 0x7fff7fffu ? 0u : codes8(x[k].b, low, inv);
-          if (u1 == u0 + 1) {
-            *reinterpret_cast<uint2*>(codes + u0) = make_uint2(ca, cb);
-          } else {
-            codes[u0] = ca;
-            codes[u1] = cb;
-          }
-          if (i == 0) a.ranges[to] = range;
+  };
+  auto put = [&](const Row16& x, int hd) {
+    dst[static_cast<size_t>(hd) * U + u0] = x.a;
+    dst[static_cast<size_t>(hd) * U + u1] = x.b;
+  };
+  if (dst)                                           // without an output the queries are not needed
+    walk(0, a.H, [&](Row16& x, int hd, bool ok) {
+      if (turns) turn16(x, cs, sn, a.interleaved);
+      if (ok && (turns || !in_place)) put(x, hd);
+    });
+  if (MODE == 0 && in_place && !pairs) return;
+  walk(a.H, MODE == 0 && in_place ? heads : NH, [&](Row16& x, int hd, bool ok) {
+    const bool moved = turns && hd < heads;
+    if (moved) turn16(x, cs, sn, a.interleaved);
+    if (ok && dst && (moved || !in_place)) put(x, hd);
+    if (MODE == 0) return;
+    const int e = hd - a.H;                          // key head, or Hkv + value head
+    const bool stored = ok && row >= 0;
+    const long long to = row + (static_cast<long long>(e) << c.page_log2);
+    if (MODE == 1 && stored) {
+      uint4* pool = static_cast<uint4*>(c.pool);
+      pool[to * U + u0] = x.a;
+      pool[to * U + u1] = x.b;
+      if (c.weight && i == 0 && e < a.Hkv) c.weight[weight + (static_cast<size_t>(e) << c.page_log2)] = 0.0f;
+    }
+    if (MODE == 2) {
+      float low, inv;
+      const uint32_t range = range_of<LANES>(x, &low, &inv);
+      if (stored) {
+        uint32_t* codes = static_cast<uint32_t*>(c.pool) + to * U;
+        const bool bad = range == 0x7fff7fffu;
+        const uint32_t ca = bad ? 0u : codes8(x.a, low, inv), cb = bad ? 0u : codes8(x.b, low, inv);
+        if (u1 == u0 + 1) {
+          *reinterpret_cast<uint2*>(codes + u0) = make_uint2(ca, cb);
+        } else {
+          codes[u0] = ca;
+          codes[u1] = cb;
         }
+        if (i == 0) a.ranges[to] = range;
       }
     }
-  }
+  });
 }
 
 // Rows start[b] + t (t < count[b]) of a 4-bit cache as bf16 rows of Hkv keys, then Hkv values.

@@ -6,8 +6,11 @@
 // the gradient gets (m, S), as e^(z - lse) would carry the rounding of lse, 2^-24 |lse| of every probability.
 //
 // The most probable tokens: every warp keeps its best 32 in order, one a lane, as 64-bit keys (logit, then lowest index),
-// and passes over a chunk none of whose lanes reaches the K-th of them, or of any other warp of the block. Lists are joined
-// two by two: the larger of each pair of opposite ends is a bitonic sequence of the best 32, sorted in five steps.
+// and passes over a chunk none of whose lanes reaches a floor that K tokens of the row are known to reach: the K-th of its
+// list, or the least of what each of the block's W warps says that J = ceil(K / W) of its tokens reach (of the first chunk
+// the J-th largest of the lanes' maxima, then the J-th of its list). With the warps' own K-th alone a row of 50,257 logits
+// and K = 8 took 24 instructions for every 32 logits. Lists are joined two by two: the larger of each pair of opposite
+// ends is a bitonic sequence of the best 32, sorted in five steps.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -149,13 +152,12 @@ logprobs_kernel(LpArgs a, int* err) {
   constexpr int N = W::N, VALUES = kLpVecs * N;      // values a lane and chunk
   namespace cg = cooperative_groups;
   __shared__ __align__(16) uint4 s_stage[kLpWarps][32][kLpVecs + 1];
-  __shared__ Key s_floor;                            // a K-th best of one of the warps: nothing below it is wanted
+  __shared__ __align__(16) float s_reach[kLpWarps];  // what J tokens of each warp reach
   __shared__ Key s_list[8][32];                      // the warps' lists, then the blocks'
   __shared__ Sums s_sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC);
   const long long m = blockIdx.x / NC;
-  if (threadIdx.x == 0) s_floor = 0;
   pdl_wait();
   pdl_trigger();
   const Row<T> row(a.z, a.ld, a.V, m);
@@ -175,7 +177,6 @@ logprobs_kernel(LpArgs a, int* err) {
   Sums sum = {kLowest, 0.0f, 0.0f};
   Key best = 0;                                      // this warp's list, one a lane
   Key floor_key = 0;                                 // what a token has to pass
-  if (K) __syncthreads();                            // s_floor
 
   auto load = [&](int chunk, uint4 (&v)[kLpVecs]) {
 #pragma unroll
@@ -214,12 +215,25 @@ logprobs_kernel(LpArgs a, int* err) {
       who &= __ballot_sync(kAll, key > floor_key);
     }
   };
+  const int chunks = (row.nvec + kLpChunk - 1) / kLpChunk, step = NC * kLpWarps, first = part * kLpWarps + warp;
+  const int busy = min(max(chunks - part * kLpWarps, 0), kLpWarps);   // this block's warps that have chunks
+  const int J = busy ? (K + busy - 1) / busy : 0;
+  float reach = INFINITY;                            // what J tokens of this warp reach (of warps without chunks: no say)
   auto may_pass = [&](float v) { return floor_key == 0 || v >= value_of(floor_key); };
+  // The floor from what every warp says.
+  auto raise_floor = [&]() {
+    float x = *static_cast<volatile float*>(&s_reach[lane & (kLpWarps - 1)]);
+#pragma unroll
+    for (int k = 1; k < kLpWarps; k <<= 1) x = fminf(x, __shfl_xor_sync(kAll, x, k));
+    const Key f = (key_of(x, 0) >> 32) << 32;
+    if (x < INFINITY && f > floor_key) floor_key = f;
+  };
   // The chunk's tokens that pass. cm: the largest value of this lane's.
   auto take = [&](int chunk, float cm, const uint4 (&v)[kLpVecs]) {
-    const Key shared = *static_cast<volatile Key*>(&s_floor);
-    if (shared > floor_key) floor_key = shared;
     unsigned who = __ballot_sync(kAll, may_pass(cm));
+    if (!who) return;
+    raise_floor();
+    who = __ballot_sync(kAll, may_pass(cm));
     if (!who) return;
     if (__popc(who) > K) {
       // K lanes have a value at least as large as the K-th of their largest ones: nothing below it is wanted
@@ -240,13 +254,22 @@ logprobs_kernel(LpArgs a, int* err) {
       insert(lane < VALUES && vec < row.nvec ? key_of(W::get(&x), index) : 0);
       who &= __ballot_sync(kAll, may_pass(cm));
     }
+    const Key mine = __shfl_sync(kAll, best, J - 1);
+    if (mine && value_of(mine) > reach) {
+      reach = value_of(mine);
+      if (lane == 0) *static_cast<volatile float*>(&s_reach[warp]) = reach;
+    }
     __syncwarp();                                    // the stage is read before it is filled again
-    if (lane == 0 && floor_key > *static_cast<volatile Key*>(&s_floor)) atomicMax(&s_floor, floor_key);
   };
 
-  const int chunks = (row.nvec + kLpChunk - 1) / kLpChunk, step = NC * kLpWarps, first = part * kLpWarps + warp;
   uint4 v[kLpVecs], next[kLpVecs];
   if (first < chunks) load(first, v);
+  if (K) {                                           // what each warp's first chunk reaches
+    if (first < chunks) reach = kth_largest(W::largest(v), J, lane);
+    if (lane == 0) s_reach[warp] = reach;
+    __syncthreads();
+    raise_floor();
+  }
   for (int c = first; c < chunks; c += step) {
     if (c + step < chunks) load(c + step, next);
     const float cm = W::largest(v);
