@@ -178,14 +178,6 @@ logprobs_kernel(LpArgs a, int* err) {
   Key best = 0;                                      // this warp's list, one a lane
   Key floor_key = 0;                                 // what a token has to pass
 
-  auto load = [&](int chunk, uint4 (&v)[kLpVecs]) {
-#pragma unroll
-    for (int k = 0; k < kLpVecs; ++k) {
-      const long long i = static_cast<long long>(chunk) * kLpChunk + k * 32 + lane;
-      v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-      if (i < row.nvec) v[k] = __ldg(vecs + i);
-    }
-  };
   auto add = [&](float cm, const uint4 (&v)[kLpVecs]) {
     const float mn = fmaxf(sum.m, cm), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E);
     float2 s = make_float2(sum.s * f, 0.0f), e2 = make_float2(f * (sum.a + sum.s * dm), 0.0f);
@@ -215,8 +207,8 @@ logprobs_kernel(LpArgs a, int* err) {
       who &= __ballot_sync(kAll, key > floor_key);
     }
   };
-  const int chunks = (row.nvec + kLpChunk - 1) / kLpChunk, step = NC * kLpWarps, first = part * kLpWarps + warp;
-  const int busy = min(max(chunks - part * kLpWarps, 0), kLpWarps);   // this block's warps that have chunks
+  const int full = row.nvec / kLpChunk, step = NC * kLpWarps, first = part * kLpWarps + warp;   // chunks without a gap
+  const int busy = min(max(full - part * kLpWarps, 0), kLpWarps);   // this block's warps that have such chunks
   const int J = busy ? (K + busy - 1) / busy : 0;
   float reach = INFINITY;                            // what J tokens of this warp reach (of warps without chunks: no say)
   auto may_pass = [&](float v) { return floor_key == 0 || v >= value_of(floor_key); };
@@ -254,29 +246,51 @@ logprobs_kernel(LpArgs a, int* err) {
       insert(lane < VALUES && vec < row.nvec ? key_of(W::get(&x), index) : 0);
       who &= __ballot_sync(kAll, may_pass(cm));
     }
-    const Key mine = __shfl_sync(kAll, best, J - 1);
-    if (mine && value_of(mine) > reach) {
-      reach = value_of(mine);
-      if (lane == 0) *static_cast<volatile float*>(&s_reach[warp]) = reach;
+    if (J) {
+      const Key mine = __shfl_sync(kAll, best, J - 1);
+      if (mine && value_of(mine) > reach) {
+        reach = value_of(mine);
+        if (lane == 0) *static_cast<volatile float*>(&s_reach[warp]) = reach;
+      }
     }
     __syncwarp();                                    // the stage is read before it is filled again
   };
+  auto use = [&](int chunk, const uint4 (&v)[kLpVecs]) {
+    const float cm = W::largest(v);
+    add(cm, v);
+    if (K) take(chunk, cm, v);
+  };
 
+  const uint4* at = vecs + static_cast<long long>(first) * kLpChunk + lane;
+  auto load = [&](uint4 (&v)[kLpVecs]) {             // the chunk at `at`, which moves on
+#pragma unroll
+    for (int k = 0; k < kLpVecs; ++k) v[k] = __ldg(at + 32 * k);
+    at += static_cast<long long>(step) * kLpChunk;
+  };
   uint4 v[kLpVecs], next[kLpVecs];
-  if (first < chunks) load(first, v);
+  if (first < full) load(v);
   if (K) {                                           // what each warp's first chunk reaches
-    if (first < chunks) reach = kth_largest(W::largest(v), J, lane);
+    if (first < full) reach = kth_largest(W::largest(v), J, lane);
     if (lane == 0) s_reach[warp] = reach;
     __syncthreads();
     raise_floor();
   }
-  for (int c = first; c < chunks; c += step) {
-    if (c + step < chunks) load(c + step, next);
-    const float cm = W::largest(v);
-    add(cm, v);
-    if (K) take(c, cm, v);
+  for (int c = first; c < full; c += 2 * step) {     // the next chunk on its way while one is used
+    const bool two = c + step < full;
+    if (two) load(next);
+    use(c, v);
+    if (!two) break;
+    if (c + 2 * step < full) load(v);
+    use(c + step, next);
+  }
+  if (full % step == first && row.nvec > full * kLpChunk) {   // the vectors behind the last whole chunk
 #pragma unroll
-    for (int k = 0; k < kLpVecs; ++k) v[k] = next[k];
+    for (int k = 0; k < kLpVecs; ++k) {
+      const int i = full * kLpChunk + k * 32 + lane;
+      v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+      if (i < row.nvec) v[k] = __ldg(vecs + i);
+    }
+    use(full, v);
   }
   if (part == 0 && warp == 0) {                      // the values before and behind the vectors
     const int tail = row.head + row.nvec * N;
@@ -286,13 +300,15 @@ logprobs_kernel(LpArgs a, int* err) {
     sum = {mn, sum.s * f + e, f * (sum.a + sum.s * dm) + e * fmaxf(d, kFar)};
     if (K) insert(index >= 0 ? key_of(z, index) : 0);
   }
+  auto shuffled = [&](const Sums& x, int k) {
+    return joined_sums(x, {__shfl_xor_sync(kAll, x.m, k), __shfl_xor_sync(kAll, x.s, k), __shfl_xor_sync(kAll, x.a, k)});
+  };
 #pragma unroll
-  for (int k = 1; k < 32; k <<= 1)
-    sum = joined_sums(sum, {__shfl_xor_sync(kAll, sum.m, k), __shfl_xor_sync(kAll, sum.s, k), __shfl_xor_sync(kAll, sum.a, k)});
+  for (int k = 1; k < 32; k <<= 1) sum = shuffled(sum, k);
   if (lane == 0) s_sums[warp] = sum;
   if (K) s_list[warp][lane] = best;
   __syncthreads();
-  auto join8 = [&](int n) {                          // the n lists and sums in shared memory, to warp 0's registers
+  auto join8 = [&](int n) {                          // the n <= 8 lists and sums in shared memory, to warp 0
     if (K) {
 #pragma unroll
       for (int half = 4; half; half >>= 1) {
@@ -303,8 +319,10 @@ logprobs_kernel(LpArgs a, int* err) {
       }
       best = s_list[0][lane];
     }
-    sum = s_sums[0];
-    for (int i = 1; i < n; ++i) sum = joined_sums(sum, s_sums[i]);
+    if (warp) return;
+    sum = (lane & 7) < n ? s_sums[lane & 7] : Sums{kLowest, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 1; k < 8; k <<= 1) sum = shuffled(sum, k);
   };
   join8(kLpWarps);
   if constexpr (NC > 1) {
