@@ -5,12 +5,12 @@
 // S' = f S, A' = f (A + (m - m') S), f = e^(m - m')). All in fp32, d as a difference, never through a rounded log-sum-exp:
 // the gradient gets (m, S), as e^(z - lse) would carry the rounding of lse, 2^-24 |lse| of every probability.
 //
-// The most probable tokens: every warp keeps its best 32 in order, one a lane, as 64-bit keys (logit, then lowest index),
-// and passes over a chunk none of whose lanes reaches a floor that K tokens of the row are known to reach: the K-th of its
-// list, or the least of what each of the block's W warps says that J = ceil(K / W) of its tokens reach (of the first chunk
-// the J-th largest of the lanes' maxima, then the J-th of its list). With the warps' own K-th alone a row of 50,257 logits
-// and K = 8 took 24 instructions for every 32 logits. Lists are joined two by two: the larger of each pair of opposite
-// ends is a bitonic sequence of the best 32, sorted in five steps.
+// The most probable tokens, behind the sums: every thread has noted the largest logit of each of its chunks. The K-th largest
+// of the 256 threads' maxima is a floor that K tokens reach, and few others: only the chunks of threads that reach it are read
+// again (out of L2). A warp keeps the best 32 tokens that it finds there in order, one a lane, as 64-bit keys (logit, then
+// lowest index); lists are joined two by two: the larger of each pair of opposite ends is a bitonic sequence of the best
+// 32, sorted in five steps. (Lists kept up to date while the row went by took 8 to 16 instructions for every 32 logits, as
+// many as the sums: 4,096 rows of 50,257 with K = 8 took 151 us in fp32 and 124 in bf16, and 128 and 77 with K = 0.)
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -29,6 +29,7 @@ constexpr float kFar = -1e20f;           // stands for differences of -inf in pr
 constexpr int kLpWarps = 8;
 constexpr int kLpVecs = 4;               // 16-byte vectors a lane and chunk
 constexpr int kLpChunk = 32 * kLpVecs;   // vectors a warp and chunk
+constexpr int kLpGroups = 16;            // maxima that a thread notes: of a chunk each, or of as many as it takes
 
 using Key = unsigned long long;
 
@@ -56,8 +57,19 @@ __device__ __forceinline__ Key join_lists(Key a, Key b, int lane) {
   return x;
 }
 
-// The K-th largest of the lanes' values.
-__device__ __forceinline__ float kth_largest(float v, int K, int lane) {
+// The same of values.
+__device__ __forceinline__ float join_values(float a, float b, int lane) {
+  float x = fmaxf(a, __shfl_sync(kAll, b, 31 - lane));
+#pragma unroll
+  for (int k = 16; k; k >>= 1) {
+    const float y = __shfl_xor_sync(kAll, x, k);
+    x = (lane & k) == 0 ? fmaxf(x, y) : fminf(x, y);
+  }
+  return x;
+}
+
+// The lanes' values in descending order.
+__device__ __forceinline__ float sorted_values(float v, int lane) {
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
@@ -67,7 +79,7 @@ __device__ __forceinline__ float kth_largest(float v, int K, int lane) {
       const bool upper = (lane & k) == 0;
       v = upper == down ? fmaxf(v, y) : fminf(v, y);
     }
-  return __shfl_sync(kAll, v, K - 1);
+  return v;
 }
 
 struct Sums {
@@ -152,7 +164,8 @@ logprobs_kernel(LpArgs a, int* err) {
   constexpr int N = W::N, VALUES = kLpVecs * N;      // values a lane and chunk
   namespace cg = cooperative_groups;
   __shared__ __align__(16) uint4 s_stage[kLpWarps][32][kLpVecs + 1];
-  __shared__ __align__(16) float s_reach[kLpWarps];  // what J tokens of each warp reach
+  __shared__ float s_max[kLpGroups][kLpWarps * 32];  // the threads' largest logits, by group of chunks
+  __shared__ float s_order[kLpWarps][32];            // and over all groups, in order
   __shared__ Key s_list[8][32];                      // the warps' lists, then the blocks'
   __shared__ Sums s_sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -176,7 +189,6 @@ logprobs_kernel(LpArgs a, int* err) {
   }
   Sums sum = {kLowest, 0.0f, 0.0f};
   Key best = 0;                                      // this warp's list, one a lane
-  Key floor_key = 0;                                 // what a token has to pass
 
   auto add = [&](float cm, const uint4 (&v)[kLpVecs]) {
     const float mn = fmaxf(sum.m, cm), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E);
@@ -193,72 +205,23 @@ logprobs_kernel(LpArgs a, int* err) {
       }
     sum = {mn, s.x + s.y, e2.x + e2.y};
   };
-  // Puts the lanes' keys that pass into the list, one by one.
-  auto insert = [&](Key key) {
-    unsigned who = __ballot_sync(kAll, key > floor_key);
-    while (who) {
-      const Key k = __shfl_sync(kAll, key, __ffs(who) - 1);
-      const int n = __popc(__ballot_sync(kAll, best > k));
-      const Key up = __shfl_up_sync(kAll, best, 1);
-      best = lane > n ? up : lane == n ? k : best;
-      const Key last = __shfl_sync(kAll, best, K - 1);
-      if (last > floor_key) floor_key = last;
-      who &= who - 1;
-      who &= __ballot_sync(kAll, key > floor_key);
-    }
-  };
   const int full = row.nvec / kLpChunk, step = NC * kLpWarps, first = part * kLpWarps + warp;   // chunks without a gap
-  const int busy = min(max(full - part * kLpWarps, 0), kLpWarps);   // this block's warps that have such chunks
-  const int J = busy ? (K + busy - 1) / busy : 0;
-  float reach = INFINITY;                            // what J tokens of this warp reach (of warps without chunks: no say)
-  auto may_pass = [&](float v) { return floor_key == 0 || v >= value_of(floor_key); };
-  // The floor from what every warp says.
-  auto raise_floor = [&]() {
-    float x = *static_cast<volatile float*>(&s_reach[lane & (kLpWarps - 1)]);
-#pragma unroll
-    for (int k = 1; k < kLpWarps; k <<= 1) x = fminf(x, __shfl_xor_sync(kAll, x, k));
-    const Key f = (key_of(x, 0) >> 32) << 32;
-    if (x < INFINITY && f > floor_key) floor_key = f;
-  };
-  // The chunk's tokens that pass. cm: the largest value of this lane's.
-  auto take = [&](int chunk, float cm, const uint4 (&v)[kLpVecs]) {
-    unsigned who = __ballot_sync(kAll, may_pass(cm));
-    if (!who) return;
-    raise_floor();
-    who = __ballot_sync(kAll, may_pass(cm));
-    if (!who) return;
-    if (__popc(who) > K) {
-      // K lanes have a value at least as large as the K-th of their largest ones: nothing below it is wanted
-      const Key k = (key_of(kth_largest(cm, K, lane), 0) >> 32) << 32;
-      if (k > floor_key) floor_key = k;
-      who = __ballot_sync(kAll, may_pass(cm));
-    }
-#pragma unroll
-    for (int k = 0; k < kLpVecs; ++k) s_stage[warp][lane][k] = v[k];
-    __syncwarp();
-    while (who) {
-      const int from = __ffs(who) - 1;
-      who &= who - 1;
-      const int j = lane % VALUES;                   // this lane's value of the candidate lane's
-      const T x = reinterpret_cast<const T*>(&s_stage[warp][from][0])[j];
-      const long long vec = static_cast<long long>(chunk) * kLpChunk + (j / N) * 32 + from;
-      const int index = row.head + static_cast<int>(vec) * N + j % N;
-      insert(lane < VALUES && vec < row.nvec ? key_of(W::get(&x), index) : 0);
-      who &= __ballot_sync(kAll, may_pass(cm));
-    }
-    if (J) {
-      const Key mine = __shfl_sync(kAll, best, J - 1);
-      if (mine && value_of(mine) > reach) {
-        reach = value_of(mine);
-        if (lane == 0) *static_cast<volatile float*>(&s_reach[warp]) = reach;
-      }
-    }
-    __syncwarp();                                    // the stage is read before it is filled again
-  };
-  auto use = [&](int chunk, const uint4 (&v)[kLpVecs]) {
+  const int chunks = (row.nvec + kLpChunk - 1) / kLpChunk;
+  const int per = ((chunks + step - 1) / step + kLpGroups - 1) / kLpGroups;   // chunks of a group
+  float top = -INFINITY, noted = -INFINITY;          // this thread's largest logit, and of the group
+  int group = 0, in_group = 0;
+  auto use = [&](const uint4 (&v)[kLpVecs]) {
     const float cm = W::largest(v);
     add(cm, v);
-    if (K) take(chunk, cm, v);
+    if (K) {
+      noted = fmaxf(noted, cm);
+      if (++in_group == per) {
+        s_max[group++][threadIdx.x] = noted;
+        top = fmaxf(top, noted);
+        noted = -INFINITY;
+        in_group = 0;
+      }
+    }
   };
 
   const uint4* at = vecs + static_cast<long long>(first) * kLpChunk + lane;
@@ -267,38 +230,105 @@ logprobs_kernel(LpArgs a, int* err) {
     for (int k = 0; k < kLpVecs; ++k) v[k] = __ldg(at + 32 * k);
     at += static_cast<long long>(step) * kLpChunk;
   };
-  uint4 v[kLpVecs], next[kLpVecs];
-  if (first < full) load(v);
-  if (K) {                                           // what each warp's first chunk reaches
-    if (first < full) reach = kth_largest(W::largest(v), J, lane);
-    if (lane == 0) s_reach[warp] = reach;
-    __syncthreads();
-    raise_floor();
-  }
-  for (int c = first; c < full; c += 2 * step) {     // the next chunk on its way while one is used
-    const bool two = c + step < full;
-    if (two) load(next);
-    use(c, v);
-    if (!two) break;
-    if (c + 2 * step < full) load(v);
-    use(c + step, next);
-  }
-  if (full % step == first && row.nvec > full * kLpChunk) {   // the vectors behind the last whole chunk
+  auto load_last = [&](int chunk, uint4 (&v)[kLpVecs]) {   // a chunk that the row's last vector may end
 #pragma unroll
     for (int k = 0; k < kLpVecs; ++k) {
-      const int i = full * kLpChunk + k * 32 + lane;
+      const int i = chunk * kLpChunk + k * 32 + lane;
       v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
       if (i < row.nvec) v[k] = __ldg(vecs + i);
     }
-    use(full, v);
+  };
+  uint4 v[kLpVecs], next[kLpVecs];
+  if (first < full) load(v);
+  for (int c = first; c < full; c += 2 * step) {     // the next chunk on its way while one is used
+    const bool two = c + step < full;
+    if (two) load(next);
+    use(v);
+    if (!two) break;
+    if (c + 2 * step < full) load(v);
+    use(next);
   }
-  if (part == 0 && warp == 0) {                      // the values before and behind the vectors
+  if (full % step == first && row.nvec > full * kLpChunk) {   // the vectors behind the last whole chunk
+    load_last(full, v);
+    use(v);
+  }
+  float ze = -INFINITY;                              // the values before and behind the vectors
+  int edge = -1;
+  if (part == 0 && warp == 0) {
     const int tail = row.head + row.nvec * N;
-    const int index = lane < 16 ? (lane < row.head ? lane : -1) : (tail + lane - 16 < a.V ? tail + lane - 16 : -1);
-    const float z = index >= 0 ? W::get(row.z + index) : -INFINITY;
-    const float mn = fmaxf(sum.m, z), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E), d = z - mn, e = ex2_approx(d * kL2E);
+    edge = lane < 16 ? (lane < row.head ? lane : -1) : (tail + lane - 16 < a.V ? tail + lane - 16 : -1);
+    if (edge >= 0) ze = W::get(row.z + edge);
+    const float mn = fmaxf(sum.m, ze), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E), d = ze - mn, e = ex2_approx(d * kL2E);
     sum = {mn, sum.s * f + e, f * (sum.a + sum.s * dm) + e * fmaxf(d, kFar)};
-    if (K) insert(index >= 0 ? key_of(z, index) : 0);
+  }
+  if (K) {
+    if (in_group) {
+      s_max[group++][threadIdx.x] = noted;
+      top = fmaxf(top, noted);
+    }
+    float order = sorted_values(top, lane);
+    s_order[warp][lane] = order;
+    __syncthreads();
+#pragma unroll
+    for (int half = kLpWarps / 2; half; half >>= 1) {
+      if (warp < half) s_order[warp][lane] = order = join_values(order, s_order[warp + half][lane], lane);
+      __syncthreads();
+    }
+    const float reached = s_order[0][K - 1];         // by K threads' largest logits
+    Key floor_key = (key_of(reached, 0) >> 32) << 32;   // what a token has to pass
+    // Puts the lanes' keys that pass into the list, one by one.
+    auto insert = [&](Key key) {
+      unsigned who = __ballot_sync(kAll, key > floor_key);
+      while (who) {
+        const Key k = __shfl_sync(kAll, key, __ffs(who) - 1);
+        const int n = __popc(__ballot_sync(kAll, best > k));
+        const Key up = __shfl_up_sync(kAll, best, 1);
+        best = lane > n ? up : lane == n ? k : best;
+        const Key last = __shfl_sync(kAll, best, K - 1);
+        if (last > floor_key) floor_key = last;
+        who &= who - 1;
+        who &= __ballot_sync(kAll, key > floor_key);
+      }
+    };
+    if (__any_sync(kAll, top >= reached)) {
+      for (int g = 0; g < group; ++g) {
+        const float most = s_max[g][threadIdx.x];
+        if (!__any_sync(kAll, most >= reached)) continue;
+        for (int c = first + g * per * step; c < min(chunks, first + (g + 1) * per * step); c += step) {
+          // lanes whose largest logit, at their first index of the chunk, would pass
+          const int at0 = row.head + (c * kLpChunk + lane) * N;
+          const bool mine = key_of(most, at0) > floor_key;
+          if (!__any_sync(kAll, mine)) continue;
+#pragma unroll
+          for (int k = 0; k < kLpVecs; ++k) v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+          if (mine) load_last(c, v);
+          const float cm = W::largest(v);
+          const Key best_here = key_of(cm, at0);
+          unsigned who = __ballot_sync(kAll, mine && best_here > floor_key);
+          if (__popc(who) > K) {
+            // K lanes have a value at least as large as the K-th of their largest ones: nothing below it is wanted
+            const float x = __shfl_sync(kAll, sorted_values(mine ? cm : -INFINITY, lane), K - 1);
+            const Key k = (key_of(x, 0) >> 32) << 32;
+            if (k > floor_key) floor_key = k;
+            who &= __ballot_sync(kAll, best_here > floor_key);
+          }
+#pragma unroll
+          for (int k = 0; k < kLpVecs; ++k) s_stage[warp][lane][k] = v[k];
+          __syncwarp();
+          while (who) {
+            const int from = __ffs(who) - 1;
+            who &= who - 1;
+            const int j = lane % VALUES;             // this lane's value of the candidate lane's
+            const float x = W::get(reinterpret_cast<const T*>(&s_stage[warp][from][0]) + j);
+            const int vec = c * kLpChunk + (j / N) * 32 + from;
+            insert(lane < VALUES && vec < row.nvec ? key_of(x, row.head + vec * N + j % N) : 0);
+            who &= __ballot_sync(kAll, best_here > floor_key);
+          }
+          __syncwarp();                              // the stage is read before it is filled again
+        }
+      }
+    }
+    if (part == 0 && warp == 0) insert(edge >= 0 ? key_of(ze, edge) : 0);
   }
   auto shuffled = [&](const Sums& x, int k) {
     return joined_sums(x, {__shfl_xor_sync(kAll, x.m, k), __shfl_xor_sync(kAll, x.s, k), __shfl_xor_sync(kAll, x.a, k)});

@@ -146,6 +146,22 @@ def test_rows_of_a_large_vocabulary(gpt_lib, dtype, M):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [65536, 65541, 131075, 300007])
+def test_vocabularies_of_several_chunks_a_note(gpt_lib, dtype, V):
+    # a thread notes the largest logit of several chunks; the best tokens next to each other, or all equal
+    for M in (2, 40):
+        z = np.zeros((M, V))
+        z[0] = logits(1, V, V)[0]
+        z[0, 1000:1040] = 30.0 + np.arange(40) % 7
+        z[1, 5:V:3] = -1.0
+        t = some_targets(M, V, V)
+        d, zd, _ = run(z, t, 32, dtype)
+        check({k: None if v is None else v[:2] for k, v in d.items()}, zd[:2], t[:2], 32)
+        for i in range(2, M):
+            assert d["top_ids"][i].tolist() == list(range(32))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("kind", ["masked", "lowest", "ties", "rising", "far"])
 def test_kinds_of_logits(gpt_lib, dtype, kind):
     for M, V in ((3, 700), (2, 9000), (40, 3001)):
