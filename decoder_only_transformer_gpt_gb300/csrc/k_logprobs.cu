@@ -82,6 +82,10 @@ __device__ __forceinline__ float sorted_values(float v, int lane) {
   return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 struct Sums {
   float m, s, a;
 };
@@ -139,8 +143,8 @@ struct LpArgs {
   const int32_t* targets;
   float *logp, *entropy, *stats, *top_logp;
   int32_t* top_ids;
-  long long ld;
-  int V, K;
+  long long ld, M;
+  int V, K, ahead;     // ahead: rows from one that is worked on to one that is not yet
 };
 
 // A row, or a stretch of it, as seen by one warp.
@@ -262,6 +266,13 @@ logprobs_kernel(LpArgs a, int* err) {
     sum = {mn, sum.s * f + e, f * (sum.a + sum.s * dm) + e * fmaxf(d, kFar)};
   }
   if (K) {
+    // Blocks take the same time for their rows and so come to this part together, in which nothing is read: the first
+    // chunks of a row that comes next are fetched into L2 meanwhile.
+    if (NC == 1 && lane < 2 && m + a.ahead < a.M) {
+      const Row<T> later(a.z, a.ld, a.V, m + a.ahead);
+      const int c = first + lane * step;
+      if (c < later.nvec / kLpChunk) prefetch_l2(reinterpret_cast<const uint4*>(later.z + later.head) + static_cast<long long>(c) * kLpChunk, kLpChunk * 16);
+    }
     if (in_group) {
       s_max[group++][threadIdx.x] = noted;
       top = fmaxf(top, noted);
@@ -472,13 +483,14 @@ cudaError_t launch_nc(const LpArgs& a, int M, int* err, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_logprobs_of(const LpArgs& a, int M, int* err, cudaStream_t s) {
+cudaError_t launch_logprobs_of(LpArgs a, int M, int* err, cudaStream_t s) {
   int dev = 0, sms = 0;
   const cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   const long long chunks = (static_cast<long long>(a.V) / Vec<T>::N + kLpChunk - 1) / kLpChunk;
   if (8LL * M <= 2 * sms && chunks > 4 * kLpWarps) return launch_nc<T, 8>(a, M, err, s);
   if (2LL * M <= 2 * sms && chunks > kLpWarps) return launch_nc<T, 2>(a, M, err, s);
+  a.ahead = 4 * sms;                                 // (four blocks an SM)
   return launch_nc<T, 1>(a, M, err, s);
 }
 
@@ -504,6 +516,7 @@ cudaError_t launch_logprobs(const LogprobRows& x, float* logp, float* entropy, f
   a.top_ids = top_ids;
   a.top_logp = top_logp;
   a.ld = x.ld;
+  a.M = x.M;
   a.V = x.V;
   a.K = K;
   return x.bf16 ? launch_logprobs_of<__nv_bfloat16>(a, x.M, err, s) : launch_logprobs_of<float>(a, x.M, err, s);
