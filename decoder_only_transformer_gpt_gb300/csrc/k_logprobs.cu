@@ -268,7 +268,7 @@ logprobs_kernel(LpArgs a, int* err) {
   if (K) {
     // Blocks take the same time for their rows and so come to this part together, in which nothing is read: the first
     // chunks of a row that comes next are fetched into L2 meanwhile.
-    if (NC == 1 && lane < 2 && m + a.ahead < a.M) {
+    if (NC == 1 && lane < 4 && m + a.ahead < a.M) {
       const Row<T> later(a.z, a.ld, a.V, m + a.ahead);
       const int c = first + lane * step;
       if (c < later.nvec / kLpChunk) prefetch_l2(reinterpret_cast<const uint4*>(later.z + later.head) + static_cast<long long>(c) * kLpChunk, kLpChunk * 16);
@@ -301,43 +301,56 @@ logprobs_kernel(LpArgs a, int* err) {
         who &= __ballot_sync(kAll, key > floor_key);
       }
     };
+    // What is read again: a chunk of one thread a lane, as many as there are at once, so that they travel together.
+    int items = 0, item_chunk = 0, item_lane = 0;
+    auto look = [&]() {
+      const int at0 = row.head + (item_chunk * kLpChunk + item_lane) * N;
+#pragma unroll
+      for (int k = 0; k < kLpVecs; ++k) {
+        const int i = item_chunk * kLpChunk + k * 32 + item_lane;
+        v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+        if (lane < items && i < row.nvec) v[k] = __ldg(vecs + i);
+        s_stage[warp][lane][k] = v[k];
+      }
+      const float cm = lane < items ? W::largest(v) : -INFINITY;
+      const Key best_here = lane < items ? key_of(cm, at0) : 0;
+      if (items > K) {
+        // K of them have a value at least as large as the K-th of their largest ones: nothing below it is wanted
+        const Key k = (key_of(__shfl_sync(kAll, sorted_values(cm, lane), K - 1), 0) >> 32) << 32;
+        if (k > floor_key) floor_key = k;
+      }
+      unsigned who = __ballot_sync(kAll, best_here > floor_key);
+      __syncwarp();
+      while (who) {
+        const int from = __ffs(who) - 1;
+        who &= who - 1;
+        const int j = lane % VALUES;                 // this lane's value of that chunk's
+        const float x = W::get(reinterpret_cast<const T*>(&s_stage[warp][from][0]) + j);
+        const int vec = __shfl_sync(kAll, item_chunk, from) * kLpChunk + (j / N) * 32 + __shfl_sync(kAll, item_lane, from);
+        insert(lane < VALUES && vec < row.nvec ? key_of(x, row.head + vec * N + j % N) : 0);
+        who &= __ballot_sync(kAll, best_here > floor_key);
+      }
+      __syncwarp();                                  // the stage is read before it is filled again
+      items = 0;
+    };
     if (__any_sync(kAll, top >= reached)) {
       for (int g = 0; g < group; ++g) {
         const float most = s_max[g][threadIdx.x];
         if (!__any_sync(kAll, most >= reached)) continue;
         for (int c = first + g * per * step; c < min(chunks, first + (g + 1) * per * step); c += step) {
           // lanes whose largest logit, at their first index of the chunk, would pass
-          const int at0 = row.head + (c * kLpChunk + lane) * N;
-          const bool mine = key_of(most, at0) > floor_key;
-          if (!__any_sync(kAll, mine)) continue;
-#pragma unroll
-          for (int k = 0; k < kLpVecs; ++k) v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-          if (mine) load_last(c, v);
-          const float cm = W::largest(v);
-          const Key best_here = key_of(cm, at0);
-          unsigned who = __ballot_sync(kAll, mine && best_here > floor_key);
-          if (__popc(who) > K) {
-            // K lanes have a value at least as large as the K-th of their largest ones: nothing below it is wanted
-            const float x = __shfl_sync(kAll, sorted_values(mine ? cm : -INFINITY, lane), K - 1);
-            const Key k = (key_of(x, 0) >> 32) << 32;
-            if (k > floor_key) floor_key = k;
-            who &= __ballot_sync(kAll, best_here > floor_key);
-          }
-#pragma unroll
-          for (int k = 0; k < kLpVecs; ++k) s_stage[warp][lane][k] = v[k];
-          __syncwarp();
+          unsigned who = __ballot_sync(kAll, key_of(most, row.head + (c * kLpChunk + lane) * N) > floor_key);
           while (who) {
-            const int from = __ffs(who) - 1;
+            if (lane == items) {
+              item_chunk = c;
+              item_lane = __ffs(who) - 1;
+            }
             who &= who - 1;
-            const int j = lane % VALUES;             // this lane's value of the candidate lane's
-            const float x = W::get(reinterpret_cast<const T*>(&s_stage[warp][from][0]) + j);
-            const int vec = c * kLpChunk + (j / N) * 32 + from;
-            insert(lane < VALUES && vec < row.nvec ? key_of(x, row.head + vec * N + j % N) : 0);
-            who &= __ballot_sync(kAll, best_here > floor_key);
+            if (++items == 32) look();
           }
-          __syncwarp();                              // the stage is read before it is filled again
         }
       }
+      if (items) look();
     }
     if (part == 0 && warp == 0) insert(edge >= 0 ? key_of(ze, edge) : 0);
   }
