@@ -16,6 +16,7 @@
 #include "launch.h"
 #include "paged.cuh"
 
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -171,17 +172,18 @@ __device__ __forceinline__ int row_in_eight(int n) { return (n & 1) * 4 + (n >> 
 
 // Eight heads' queries as second operands, times 2^(14 - e) for 2^e <= the head's largest value < 2^(e + 1). from: what the
 // score products start with, 8 times the sums of heads 2 q and 2 q + 1; sum: these sums; c: the factors from a product to the
-// softmax's base-2 exponent. gn rows of D bf16 at shared address sq, zeros behind them.
+// softmax's base-2 exponent. load(row, i): values 8 i of one of the gn heads; zeros behind them.
 template <int D>
 struct Queries {
   uint32_t f[D / 16][2];
   float from[4], sum[2], c[2];
-  __device__ __forceinline__ void take(float scale_log2, uint32_t sq, int gn, int lane) {
+  template <typename Load>
+  __device__ __forceinline__ void take(float scale_log2, int gn, int lane, Load&& load) {
     constexpr int C = D / 4;                         // values of a lane: its codes' places
     float v[C], top = 0.0f, mine = 0.0f;
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {
-      uint4 x = lds128(sq + min(lane >> 2, max(gn - 1, 0)) * D * 2 + ((lane & 3) * C + 8 * w) * 2);
+      uint4 x = load(min(lane >> 2, max(gn - 1, 0)), (lane & 3) * (C / 8) + w);
       if ((lane >> 2) >= gn) x = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -218,54 +220,34 @@ struct Queries {
   }
 };
 
-// Products q . code of the key rows at sk, NJ tiles of 16.
+// Products q . code of 16 key rows, tile j of s; w: this lane's quarter of rows n and n + 8.
 template <int D, int NQ, int NJ>
-__device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], const Queries<D> (&q)[NQ], uint32_t sk, int lane, const Exponents& exps) {
-  const uint32_t at = sk + row_in_eight(lane >> 2) * (D / 2) + (lane & 3) * (D / 8);
+__device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], int j, const Queries<D> (&q)[NQ], const uint32_t (&w)[2][D / 32],
+                                            const Exponents& exps) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    uint32_t w[2][2];                                // rows n and n + 8
+  for (int k = 0; k < D / 32; ++k) {
+    uint32_t a[4], b[4];
+    unpack8(a[0], a[2], b[0], b[2], w[0][k], exps);
+    unpack8(a[1], a[3], b[1], b[3], w[1][k], exps);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (D == 64) {
-        const uint2 x = lds64(at + (16 * j + 8 * h) * (D / 2));
-        w[h][0] = x.x;
-        w[h][1] = x.y;
-      } else {
-        w[h][0] = lds32(at + (16 * j + 8 * h) * (D / 2));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-      uint32_t a[4], b[4];
-      unpack8(a[0], a[2], b[0], b[2], w[0][k], exps);
-      unpack8(a[1], a[3], b[1], b[3], w[1][k], exps);
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        if (k == 0) mma16_from(s[i][j], a, q[i].f[0][0], q[i].f[0][1], q[i].from);
-        else mma16(s[i][j], a, q[i].f[2 * k][0], q[i].f[2 * k][1]);
-        mma16(s[i][j], b, q[i].f[2 * k + 1][0], q[i].f[2 * k + 1][1]);
-      }
+    for (int i = 0; i < NQ; ++i) {
+      if (k == 0) mma16_from(s[i][j], a, q[i].f[0][0], q[i].f[0][1], q[i].from);
+      else mma16(s[i][j], a, q[i].f[2 * k][0], q[i].f[2 * k][1]);
+      mma16(s[i][j], b, q[i].f[2 * k + 1][0], q[i].f[2 * k + 1][1]);
     }
   }
 }
 
-// O += (code - 8) P for 16 value rows at sv; p: probabilities times the rows' scales, as second operands. Tile t of O has
-// values 8 n + 2 t and, in its lower half, 8 n + 2 t + 1 as rows (D = 32: 4 n + ..).
+// O += (code - 8) P for 16 value rows; w: byte columns (of D = 64 words, else half words) of rows q, q + 4, q + 8, q + 12; p:
+// probabilities times the rows' scales, as second operands. Tile t of O has values 8 n + 2 t and, in its lower half, 8 n + 2 t + 1
+// as rows (D = 32: 4 n + ..).
 template <int D, int NQ>
-__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint32_t (&p)[NQ][2], uint32_t sv, int lane, const Exponents& exps) {
-  constexpr int ROWB = D / 2;
-  uint32_t x[2][2];                                  // rows (0, 4) + q, then (8, 12) + q: codes 0-3 and, of D = 64, 4-7 of a word
+__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint32_t (&p)[NQ][2], const uint32_t (&w)[4], const Exponents& exps) {
+  uint32_t x[2][2];                                  // codes 0-3 and, of D = 64, 4-7 of two rows each, side by side
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t at = sv + (8 * h + (lane & 3)) * ROWB + (lane >> 2) * (D / 16);
-    if constexpr (D == 64) {
-      const uint32_t w0 = lds32(at), w1 = lds32(at + 4 * ROWB);
-      x[0][h] = __byte_perm(w0, w1, 0x5410);
-      x[1][h] = __byte_perm(w0, w1, 0x7632);
-    } else {
-      x[0][h] = lds16(at) | (lds16(at + 4 * ROWB) << 16);
-    }
+    x[0][h] = __byte_perm(w[2 * h], w[2 * h + 1], 0x5410);
+    if (D == 64) x[1][h] = __byte_perm(w[2 * h], w[2 * h + 1], 0x7632);
   }
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
@@ -278,6 +260,197 @@ __device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint3
       mma16(o[i][2 * k + 1], b, p[i][0], p[i][1]);
     }
   }
+}
+
+// What a warp holds of a segment: up to QR heads of one key head. Lane 4 n + q has heads 8 i + 2 q and the next, and of every
+// lane's rows its own share of the sums l and off; with one head (QR = 1) all lanes have rows of it.
+template <int D, int QR>
+struct Segment {
+  static constexpr int NQ = (QR + 7) / 8, NT = D / 16;
+  static constexpr bool ONE = QR == 1;
+  Queries<D> qs[NQ];
+  float o[NQ][NT][4];                                // times 2^(15 - e)
+  float m[NQ][2], l[NQ][2], off[NQ][2];
+  int e;                                             // 2^e is above every scale and lowest value of the rows so far
+  float into;                                        // 2^(15 - e)
+
+  template <typename Load>
+  __device__ __forceinline__ void start(float scale_log2, int gn, int lane, Load&& load) {
+    e = -111;
+    into = exp2_of(15 - e);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[i][k] = -INFINITY;
+        l[i][k] = off[i][k] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][j][k] = 0.0f;
+      qs[i].take(scale_log2, gn - 8 * i, lane, [&](int r, int u) { return load(8 * i + r, u); });
+    }
+    if constexpr (ONE) {                             // every lane has rows of the one head
+      qs[0].sum[0] = __shfl_sync(kAll, qs[0].sum[0], 0);
+      qs[0].c[0] = __shfl_sync(kAll, qs[0].c[0], 0);
+    }
+  }
+
+  // Makes room for rows with scales and lowest values of this size (rarely: then 2^e grows, and o and off with it).
+  __device__ __forceinline__ void fit(float size) {
+    if (!__any_sync(kAll, size * into >= 32768.0f)) return;
+    const uint32_t top = __reduce_max_sync(kAll, __float_as_uint(size) & 0x7fffffffu);
+    const int up = min(exponent_of(__uint_as_float(top)) + 1, 128);
+    const float less = up - e > 126 ? 0.0f : exp2_of(e - up);
+    e = up;
+    into = exp2_of(15 - e);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      off[i][0] *= less;
+      off[i][1] *= less;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][j][k] *= less;
+    }
+  }
+
+  // Scores of the tiles into probabilities times the rows' scales. factors: shared address of the rows' (key scale, key
+  // lowest, value scale 2^(15 - e), (value lowest + 8 value scale) 2^(15 - e)).
+  template <int NJ>
+  __device__ __forceinline__ void weigh(float (&s)[NQ][NJ][4], uint32_t factors, const uint32_t (&seen)[NJ / 2], uint32_t unseen, int lane) {
+    const int n8 = lane >> 2;
+    float2 vf[2 * NJ];                               // the value rows' factors, of rows 8 r + row_in_eight(n8)
+#pragma unroll
+    for (int r = 0; r < 2 * NJ; ++r) {
+      const float4 f = lds128f(factors + 16 * (8 * r + row_in_eight(n8)));
+      vf[r] = make_float2(f.z, f.w);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float& x = s[i][r >> 1][2 * (r & 1) + k];
+          x = fmaf(f.x, x, f.y * qs[i].sum[k]);
+        }
+    }
+    if (unseen) {
+#pragma unroll
+      for (int r = 0; r < 2 * NJ; ++r)
+        if (!((seen[r >> 2] >> (8 * (r & 3) + row_in_eight(n8))) & 1u))
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) s[i][r >> 1][2 * (r & 1)] = s[i][r >> 1][2 * (r & 1) + 1] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float mx[2], ref[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x = s[i][0][k];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) x = j ? fmax3(x, s[i][j][k], s[i][j][2 + k]) : fmaxf(x, s[i][j][2 + k]);
+        x *= qs[i].c[k];
+        x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+        mx[k] = fmaxf(x, m[i][k]);
+        ref[k] = mx[k] == -INFINITY ? 0.0f : mx[k];  // every score so far -inf: every term is 2^-inf
+      }
+      if (__any_sync(kAll, mx[0] > m[i][0] || mx[1] > m[i][1])) {   // a new maximum
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float a = ex2_approx(m[i][k] - ref[k]);
+          m[i][k] = mx[k];
+          l[i][k] *= a;
+          off[i][k] *= a;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            o[i][j][k] *= a;
+            o[i][j][2 + k] *= a;
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2 * NJ; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float& x = s[i][r >> 1][2 * (r & 1) + k];
+          const float p = ex2_approx(fmaf(x, qs[i].c[k], -ref[k]));
+          l[i][k] += p;
+          off[i][k] = fmaf(p, vf[r].y, off[i][k]);
+          x = p * vf[r].x;
+        }
+    }
+  }
+
+  // The same of one head: s has the products in lanes 4 n, which go round the warp in shared memory (128 NH bytes at `room`),
+  // 32 rows to a value of x and of the rows' factors; x becomes the rows' probabilities times their scales.
+  template <int NH, int NJ>
+  __device__ __forceinline__ void weigh_one(const float (&s)[1][NJ][4], float (&x)[NH], uint32_t room, const float (&ks)[NH], const float (&kl)[NH],
+                                            const float (&vs)[NH], const float (&vl)[NH], const uint32_t (&seen)[NH], int lane) {
+    if ((lane & 3) == 0) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+        sts128f(room + NH * 4 * lane + 16 * h, s[0][2 * h][0], s[0][2 * h][2], s[0][2 * h + 1][0], s[0][2 * h + 1][2]);
+    }
+    __syncwarp();
+    // row 8 v + i of the tile is value v of lane 4 n with row_in_eight(n) = i
+    const uint32_t mine = room + NH * 16 * (2 * (lane & 3) + ((lane >> 2) & 1)) + 4 * (lane >> 3);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      x[h] = fmaf(ks[h], __uint_as_float(lds32(mine + 16 * h)), kl[h] * qs[0].sum[0]);
+      if (!((seen[h] >> lane) & 1u)) x[h] = -INFINITY;
+      mx = fmaxf(mx, x[h]);
+    }
+    mx *= qs[0].c[0];
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, k));
+    mx = fmaxf(mx, m[0][0]);
+    const float ref = mx == -INFINITY ? 0.0f : mx;   // every score so far -inf: every term is 2^-inf
+    if (mx > m[0][0]) {                              // a new maximum (the same for all lanes)
+      const float a = ex2_approx(m[0][0] - ref);
+      m[0][0] = mx;
+      l[0][0] *= a;
+      off[0][0] *= a;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        o[0][j][0] *= a;
+        o[0][j][2] *= a;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const float p = ex2_approx(fmaf(x[h], qs[0].c[0], -ref));
+      l[0][0] += p;
+      off[0][0] = fmaf(p, vl[h], off[0][0]);
+      x[h] = p * vs[h];
+    }
+  }
+
+  // The lane's values D / 8 n .. of head 8 i + 2 q + k, not divided by the sum, which is returned.
+  __device__ __forceinline__ float values(int i, int k, float (&v)[D / 8]) const {
+    float lt = l[i][k], ot = off[i][k];
+#pragma unroll
+    for (int x = ONE ? 1 : 4; x < 32; x <<= 1) {
+      lt += __shfl_xor_sync(kAll, lt, x);
+      ot += __shfl_xor_sync(kAll, ot, x);
+    }
+    const float back = exp2_of((e - 15) / 2), rest = exp2_of(e - 15 - (e - 15) / 2);   // 2^(e - 15) in two steps
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      v[2 * j] = (o[i][j][k] + ot) * back * rest;
+      v[2 * j + 1] = (o[i][j][2 + k] + ot) * back * rest;
+    }
+    return lt;
+  }
+};
+
+// A row's probability times its scale as part of a second operand: lane q of head 0 takes of the rows 8 v the rows q and q + 4
+// of every v, NV words of fp16 pairs at `weights`.
+template <int NV>
+__device__ __forceinline__ uint32_t weight_place(int row) {
+  return 4 * (NV * (row & 3) + (row >> 3)) + 2 * ((row >> 2) & 1);
 }
 
 // The tiles of UNIT rows that hold the rows which a sequence's query sees, of n rows: v < head at the start, then from `gap`
@@ -456,11 +629,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
 
   constexpr bool ONE = QR == 1;
   const Exponents exps;
-  float o[NQ][NT][4];                                // times 2^(15 - e)
-  float m[NQ][2], l[NQ][2], off[NQ][2];              // of heads 8 i + 2 q and the next
-  Queries<D> qs[NQ];
-  int e = 0;                                         // 2^e is above every scale and lowest value of the segment's rows
-  float into = 0.0f;                                 // 2^(15 - e)
+  Segment<D, QR> g;
   bool whole = false;                                // the segment's units so far are all in this warp's range
   uint32_t slot0 = 0;                                // of the two places for partial results
   const int n8 = lane >> 2, q4 = lane & 3;
@@ -484,25 +653,8 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     if (n == 0 || at.tile == 0) {
       whole = at.tile == 0;
       slot0 = n == 0 ? 0 : 1;
-      e = -111;
-      into = exp2_of(15 - e);
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          m[i][k] = -INFINITY;
-          l[i][k] = off[i][k] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[i][j][k] = 0.0f;
-        qs[i].take(w.scale_log2, st + Cfg::QUERIES + i * 16 * D, w.G - at.mt * 16 - 8 * i, lane);
-      }
-      if constexpr (ONE) {                           // every lane has rows of the one head
-        qs[0].sum[0] = __shfl_sync(kAll, qs[0].sum[0], 0);
-        qs[0].c[0] = __shfl_sync(kAll, qs[0].c[0], 0);
-      }
+      g.start(w.scale_log2, min(w.G - at.mt * 16, 16), lane,
+              [&](int r, int u) { return lds128(st + Cfg::QUERIES + (r * (D / 8) + u) * 16); });
     }
     uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
     float ks[NH], kl[NH], vs[NH], vl[NH];            // the factors of rows `lane` and, of a unit of 64, 32 + lane
@@ -528,178 +680,85 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         vl[h] = low_of(vr);
         size = fmax3(size, vs[h], fabsf(vl[h]));
       }
-      if (__any_sync(kAll, size * into >= 32768.0f)) {   // (rarely: 2^e has to grow, and o and off with it)
-        const uint32_t top = __reduce_max_sync(kAll, __float_as_uint(size) & 0x7fffffffu);
-        const int up = min(exponent_of(__uint_as_float(top)) + 1, 128);
-        const float less = up - e > 126 ? 0.0f : exp2_of(e - up);
-        e = up;
-        into = exp2_of(15 - e);
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          off[i][0] *= less;
-          off[i][1] *= less;
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[i][j][k] *= less;
-        }
-      }
+      g.fit(size);
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        vl[h] = fmaf(8.0f, vs[h], vl[h]) * into;
-        vs[h] *= into;
+        vl[h] = fmaf(8.0f, vs[h], vl[h]) * g.into;
+        vs[h] *= g.into;
         if constexpr (!ONE) sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h], vl[h]);
       }
     }
     float s[NQ][NJ][4];
-    code_scores<D, NQ, NJ>(s, qs, st, lane, exps);
-    if constexpr (ONE) {
-      // One head: lanes 4 n have its 64 products, which go round the warp, two rows a lane.
-      if (q4 == 0) {
-        sts128f(factors + 32 * n8, s[0][0][0], s[0][0][2], s[0][1][0], s[0][1][2]);
-        sts128f(factors + 32 * n8 + 16, s[0][2][0], s[0][2][2], s[0][3][0], s[0][3][2]);
-      }
-      __syncwarp();
-      float x[2];
-      // row 8 v + i of the tile is value v of lane 4 n with row_in_eight(n) = i
-      const uint32_t mine = factors + 32 * (2 * (lane & 3) + ((lane >> 2) & 1)) + 4 * (lane >> 3);
+    const uint32_t krow = st + row_in_eight(n8) * ROWB + q4 * (D / 8), vcol = st + Cfg::TILE + q4 * ROWB + n8 * (D / 16);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      uint32_t x[2][D / 32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        x[h] = fmaf(ks[h], __uint_as_float(lds32(mine + 16 * h)), kl[h] * qs[0].sum[0]);
-        if (!((seen[h] >> lane) & 1u)) x[h] = -INFINITY;
-      }
-      float mx = fmaxf(x[0], x[1]) * qs[0].c[0];
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, k));
-      mx = fmaxf(mx, m[0][0]);
-      const float ref = mx == -INFINITY ? 0.0f : mx;   // every score so far -inf: every term is 2^-inf
-      if (mx > m[0][0]) {                            // a new maximum (the same for all lanes)
-        const float a = ex2_approx(m[0][0] - ref);
-        m[0][0] = mx;
-        l[0][0] *= a;
-        off[0][0] *= a;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          o[0][j][0] *= a;
-          o[0][j][2] *= a;
+        if constexpr (D == 64) {
+          const uint2 u = lds64(krow + (16 * j + 8 * h) * ROWB);
+          x[h][0] = u.x;
+          x[h][1] = u.y;
+        } else {
+          x[h][0] = lds32(krow + (16 * j + 8 * h) * ROWB);
         }
       }
-      // as second operands: lane q of head 0 takes of rows 8 v the rows q and q + 4, eight words of fp16 pairs
+      code_scores<D, NQ, NJ>(s, j, g.qs, x, exps);
+    }
+    auto value_words = [&](uint32_t (&x)[4], int j) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if constexpr (D == 64) x[h] = lds32(vcol + (16 * j + 4 * h) * ROWB);
+        else x[h] = lds16(vcol + (16 * j + 4 * h) * ROWB);
+      }
+    };
+    if constexpr (ONE) {
+      float x[NH];
+      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, lane);
       const uint32_t weights = factors + 256;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float p = ex2_approx(fmaf(x[h], qs[0].c[0], -ref));
-        l[0][0] += p;
-        off[0][0] = fmaf(p, vl[h], off[0][0]);
-        sts16(weights + 32 * (lane & 3) + 16 * h + 4 * (lane >> 3) + 2 * ((lane >> 2) & 1), p * vs[h]);
-      }
+      for (int h = 0; h < NH; ++h) sts16(weights + weight_place<2 * NJ>(32 * h + lane), x[h]);
       __syncwarp();
       const uint32_t pa = n8 == 0 ? weights + 32 * q4 : weights + 128;   // other columns: zeros
       const uint32_t step = n8 == 0 ? 16 : 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < NH; ++h) {
         const uint4 w4 = lds128(pa + step * h);
         const uint32_t p0[1][2] = {{w4.x, w4.y}}, p1[1][2] = {{w4.z, w4.w}};
-        add_codes<D, NQ>(o, p0, st + Cfg::TILE + 32 * h * ROWB, lane, exps);
-        add_codes<D, NQ>(o, p1, st + Cfg::TILE + (32 * h + 16) * ROWB, lane, exps);
+        uint32_t u[4];
+        value_words(u, 2 * h);
+        add_codes<D, NQ>(g.o, p0, u, exps);
+        value_words(u, 2 * h + 1);
+        add_codes<D, NQ>(g.o, p1, u, exps);
       }
     } else {
-    __syncwarp();
-    float2 vf[2 * NJ];                               // the value rows' factors, of rows 8 r + row_in_eight(n8)
+      __syncwarp();
+      g.weigh(s, factors, seen, unseen, lane);
 #pragma unroll
-    for (int r = 0; r < 2 * NJ; ++r) {
-      const float4 f = lds128f(factors + 16 * (8 * r + row_in_eight(n8)));
-      vf[r] = make_float2(f.z, f.w);
+      for (int j = 0; j < NJ; ++j) {
+        uint32_t p[NQ][2], u[4];
 #pragma unroll
-      for (int i = 0; i < NQ; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float& x = s[i][r >> 1][2 * (r & 1) + k];
-          x = fmaf(f.x, x, f.y * qs[i].sum[k]);
+        for (int i = 0; i < NQ; ++i) {
+          p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
+          p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
         }
-    }
-    if (unseen) {
-#pragma unroll
-      for (int r = 0; r < 2 * NJ; ++r)
-        if (!((seen[r >> 2] >> (8 * (r & 3) + row_in_eight(n8))) & 1u))
-#pragma unroll
-          for (int i = 0; i < NQ; ++i) s[i][r >> 1][2 * (r & 1)] = s[i][r >> 1][2 * (r & 1) + 1] = -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      float mx[2], ref[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x = s[i][0][k];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) x = j ? fmax3(x, s[i][j][k], s[i][j][2 + k]) : fmaxf(x, s[i][j][2 + k]);
-        x *= qs[i].c[k];
-        x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
-        mx[k] = fmaxf(x, m[i][k]);
-        ref[k] = mx[k] == -INFINITY ? 0.0f : mx[k];  // every score so far -inf: every term is 2^-inf
+        value_words(u, j);
+        add_codes<D, NQ>(g.o, p, u, exps);
       }
-      if (__any_sync(kAll, mx[0] > m[i][0] || mx[1] > m[i][1])) {   // a new maximum
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float a = ex2_approx(m[i][k] - ref[k]);
-          m[i][k] = mx[k];
-          l[i][k] *= a;
-          off[i][k] *= a;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[i][j][k] *= a;
-            o[i][j][2 + k] *= a;
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 2 * NJ; ++r)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float& x = s[i][r >> 1][2 * (r & 1) + k];
-          const float p = ex2_approx(fmaf(x, qs[i].c[k], -ref[k]));
-          l[i][k] += p;
-          off[i][k] = fmaf(p, vf[r].y, off[i][k]);
-          x = p * vf[r].x;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      uint32_t p[NQ][2];
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
-        p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
-      }
-      add_codes<D, NQ>(o, p, st + Cfg::TILE + 16 * j * ROWB, lane, exps);
-    }
     }
     const bool ends = at.tile == at.t.count - 1;
     if (ends || n == count - 1) {                    // the piece is done
       whole = whole && ends;                         // it holds all of the segment's units
       const size_t slot = static_cast<size_t>(gw) * 2 + slot0;
-      const float back = exp2_of((e - 15) / 2), rest = exp2_of(e - 15 - (e - 15) / 2);   // 2^(e - 15) in two steps
       const int gn = min(w.G - at.mt * 16, 16);
 #pragma unroll
       for (int i = 0; i < NQ; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float lt = l[i][k], ot = off[i][k];
-#pragma unroll
-          for (int x = ONE ? 1 : 4; x < 32; x <<= 1) {
-            lt += __shfl_xor_sync(kAll, lt, x);
-            ot += __shfl_xor_sync(kAll, ot, x);
-          }
+          float v[D / 8];                            // values D / 8 n8 .. of the head
+          const float lt = g.values(i, k, v);
           const int r = 8 * i + 2 * q4 + k;
           if (r >= gn) continue;
-          float v[D / 8];                            // values D / 8 n8 .. of the head
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            v[2 * j] = (o[i][j][k] + ot) * back * rest;
-            v[2 * j + 1] = (o[i][j][2 + k] + ot) * back * rest;
-          }
           if (whole) {
             const size_t head = static_cast<size_t>(at.b) * w.H + at.kh * w.G + at.mt * 16 + r;
             const float inv = 1.0f / lt;             // (a sum of 0, every score -inf, gives NaN)
@@ -708,12 +767,12 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
             for (int j = 0; j < NT; ++j) h[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
             if constexpr (D == 64) *reinterpret_cast<uint4*>(y + head * D + 8 * n8) = make_uint4(h[0], h[1], h[2], h[3]);
             else *reinterpret_cast<uint2*>(y + head * D + 4 * n8) = make_uint2(h[0], h[1]);
-            if (n8 == 0 && lse2) lse2[head] = m[i][k] + log2f(lt);
+            if (n8 == 0 && lse2) lse2[head] = g.m[i][k] + log2f(lt);
           } else {
             float4* dst = reinterpret_cast<float4*>(ws.o + (slot * QR + r) * D + n8 * (D / 8));
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-            if (n8 == 0) ws.ml[slot * QR + r] = make_float2(m[i][k], lt);
+            if (n8 == 0) ws.ml[slot * QR + r] = make_float2(g.m[i][k], lt);
           }
         }
     }
@@ -721,6 +780,195 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     stage = stage == Cfg::STAGES - 1 ? 0 : stage + 1;
     if (stage == 0) phase ^= 1;
     __syncwarp();                                    // the stage and the factors are read before they are filled again
+  }
+}
+
+// The same attention where the rows that can be seen fit the warps of one cluster, UPW units of 32 rows a warp: one launch, no
+// scratch. Blocks behind a sequence's last unit leave at once. Codes and ranges go from the cache straight into the lanes
+// that use them, all at once; each block adds up its warps' outputs in shared memory and pushes them to the block that joins
+// that query row, and its maxima and sums to every block; one cluster barrier. Bound by latency.
+template <int D, int QR>
+__global__ void __launch_bounds__(256, QR == 16 ? 1 : 2)
+paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __nv_bfloat16* __restrict__ qkv,
+                    const int32_t* __restrict__ lens, __nv_bfloat16* __restrict__ y, float* __restrict__ lse2, Dec4Shape w, int upw,
+                    int* err) {
+  constexpr int ROWB = D / 2, NQ = (QR + 7) / 8, UNIT = 32;
+  constexpr bool ONE = QR == 1;
+  __shared__ __align__(16) float s_own[8][QR][D];    // the warps' outputs, and before them what a unit's rows need
+  __shared__ __align__(16) float s_factors[8][ONE ? 32 + 16 + 4 : UNIT * 4];
+  __shared__ float2 s_ml[8][QR];                     // the warps' maxima and sums
+  __shared__ float2 s_all[8][QR];                    // the blocks', pushed by each of them
+  __shared__ float s_o[QR + 7][D];                   // pushed outputs: [row / NB * NB + block][D]
+  auto cluster = cooperative_groups::this_cluster();
+  const int NC = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n8 = lane >> 2, q4 = lane & 3;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // every block has started (awaited below)
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y, hm = static_cast<int>(blockIdx.x) / NC;
+  const int kh = hm / w.mg, g0 = (hm - kh * w.mg) * 16, gn = min(w.G - g0, 16);
+  const int pmask = (1 << c.page_log2) - 1;
+  const int32_t* trow = c.table + static_cast<size_t>(b) * c.max_pages;
+  const __nv_bfloat16* tok = qkv + (static_cast<size_t>(b) * (w.H + 2 * c.Hkv) + kh * w.G + g0) * D;
+  const size_t head0 = static_cast<size_t>(b) * w.H + kh * w.G + g0;
+  const int len = __ldg(lens + b);
+  // the first unit's pages, on their way before the length is known: right unless a window cuts
+  const int guess = (rank * upw * 8 + warp) * UNIT;
+  int page = __ldg(trow + min((guess + lane) >> c.page_log2, c.max_pages - 1));
+  const Exponents exps;
+  Segment<D, QR> g;
+  g.start(w.scale_log2, gn, lane, [&](int r, int u) { return __ldg(reinterpret_cast<const uint4*>(tok + static_cast<size_t>(r) * D) + u); });
+  const int n = rows_of(c, w, len);
+  if (n <= 0) {                                      // (the same for the whole cluster)
+    if (n == -2 && rank == 0 && tid == 0) record_error(err, GPT_DEV_EPAGE);
+    if (n == 0 && rank == 0) {
+      for (int i = tid; i < gn * D; i += 256) y[head0 * D + i] = __float2bfloat16(0.0f);
+      if (lse2 && tid < gn) lse2[head0 + tid] = -INFINITY;
+    }
+    return;
+  }
+  const Tiles t = tiles_of<UNIT>(n, w.window, w.sinks);
+  const int NB = (t.count + 8 * upw - 1) / (8 * upw);   // blocks that hold units
+  if (rank >= NB) return;                            // (whole blocks: barriers wait for the others only)
+  const size_t prows = static_cast<size_t>(2 * c.Hkv) << c.page_log2, vrows = prows / 2;
+  const uint8_t* codes = static_cast<const uint8_t*>(c.pool);
+  const uint32_t factors = smem_u32(&s_factors[warp][0]);
+  if constexpr (ONE) {
+    if (lane == 0) sts128f(factors + 192, 0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  for (int u = 0; u < upw; ++u) {
+    const int unit = (rank * upw + u) * 8 + warp;
+    if (unit >= t.count) break;
+    const int r0 = first_row<UNIT>(t, unit), mine = r0 + lane;
+    if (r0 != guess) page = mine < n ? __ldg(trow + (mine >> c.page_log2)) : 0;
+    const bool there = mine < n && static_cast<unsigned>(page) < static_cast<unsigned>(c.pages);
+    if (mine < n && !there) record_error(err, GPT_DEV_EPAGE);
+    // eight rows lie in one page: theirs, from the lane of the first one
+    const uint32_t have = __ballot_sync(kAll, there);
+    uint32_t kw[4][D / 32], vw[8];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const size_t row = static_cast<size_t>(static_cast<uint32_t>(__shfl_sync(kAll, page, 8 * r))) * prows +
+                         (static_cast<size_t>(kh) << c.page_log2) + ((r0 + 8 * r) & pmask);
+      const bool ok = (have >> (8 * r)) & 1u;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) kw[r][k] = 0u;
+      vw[2 * r] = vw[2 * r + 1] = 0u;
+      if (!ok) continue;
+      const uint8_t* k8 = codes + (row + row_in_eight(n8)) * ROWB + q4 * (D / 8);
+      const uint8_t* v8 = codes + (row + vrows + q4) * ROWB + n8 * (D / 16);
+      if constexpr (D == 64) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(k8));
+        kw[r][0] = x.x;
+        kw[r][1] = x.y;
+        vw[2 * r] = __ldg(reinterpret_cast<const uint32_t*>(v8));
+        vw[2 * r + 1] = __ldg(reinterpret_cast<const uint32_t*>(v8 + 4 * ROWB));
+      } else {
+        kw[r][0] = __ldg(reinterpret_cast<const uint32_t*>(k8));
+        vw[2 * r] = __ldg(reinterpret_cast<const uint16_t*>(v8));
+        vw[2 * r + 1] = __ldg(reinterpret_cast<const uint16_t*>(v8 + 4 * ROWB));
+      }
+    }
+    const bool is_seen = there && (w.window == 0 || mine >= n - w.window || mine < w.sinks);
+    uint32_t kr = 0u, vr = 0u;                       // row `lane`'s ranges
+    if (is_seen) {
+      const size_t row = static_cast<size_t>(static_cast<uint32_t>(page)) * prows + (static_cast<size_t>(kh) << c.page_log2) + (mine & pmask);
+      kr = __ldg(ranges + row);
+      vr = __ldg(ranges + row + vrows);
+    }
+    const uint32_t seen[1] = {__ballot_sync(kAll, is_seen)};
+    float ks[1] = {scale_of(kr)}, kl[1] = {low_of(kr)}, vs[1] = {scale_of(vr)}, vl[1] = {low_of(vr)};
+    g.fit(fmaxf(vs[0], fabsf(vl[0])));
+    vl[0] = fmaf(8.0f, vs[0], vl[0]) * g.into;
+    vs[0] *= g.into;
+    float s[NQ][2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t x[2][D / 32];
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        x[0][k] = kw[2 * j][k];
+        x[1][k] = kw[2 * j + 1][k];
+      }
+      code_scores<D, NQ, 2>(s, j, g.qs, x, exps);
+    }
+    uint32_t p[2][NQ][2];
+    if constexpr (ONE) {
+      float x[1];
+      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, lane);
+      sts16(factors + 128 + weight_place<4>(lane), x[0]);
+      __syncwarp();
+      const uint4 w4 = lds128(factors + 128 + (n8 == 0 ? 16 * q4 : 64));   // other columns: zeros
+      p[0][0][0] = w4.x;
+      p[0][0][1] = w4.y;
+      p[1][0][0] = w4.z;
+      p[1][0][1] = w4.w;
+    } else {
+      sts128f(factors + 16 * lane, ks[0], kl[0], vs[0], vl[0]);
+      __syncwarp();
+      g.weigh(s, factors, seen, ~seen[0], lane);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          p[j][i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
+          p[j][i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t x[4] = {vw[4 * j], vw[4 * j + 1], vw[4 * j + 2], vw[4 * j + 3]};
+      add_codes<D, NQ>(g.o, p[j], x, exps);
+    }
+    __syncwarp();                                    // the factors are read before they are written again
+  }
+#pragma unroll
+  for (int i = 0; i < NQ; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float v[D / 8];
+      const float lt = g.values(i, k, v);
+      const int r = 8 * i + 2 * q4 + k;
+      if (r >= gn) continue;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+        *reinterpret_cast<float4*>(&s_own[warp][r][n8 * (D / 8) + 4 * x]) = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+      if (n8 == 0) s_ml[warp][r] = make_float2(g.m[i][k], lt);
+    }
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  // this block's maximum, sum and output of each row, to the blocks that want them
+  for (int i = tid; i < gn * D; i += 256) {
+    const int r = i / D, d = i % D;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, s_ml[k][r].x);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    float lt = 0.0f, acc = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = ex2_approx(s_ml[k][r].x - ref);
+      lt += s_ml[k][r].y * f;
+      acc += s_own[k][r][d] * f;
+    }
+    cluster.map_shared_rank(&s_o[0][0], r % NB)[(r / NB * NB + rank) * D + d] = acc;
+    if (d < NB) cluster.map_shared_rank(&s_all[0][0], d)[rank * QR + r] = make_float2(mx, lt);
+  }
+  cluster.sync();
+  for (int i = tid; i < (gn + NB - 1) / NB * D; i += 256) {
+    const int r = i / D * NB + rank, d = i % D;
+    if (r >= gn) continue;
+    float mx = -INFINITY;
+    for (int k = 0; k < NB; ++k) mx = fmaxf(mx, s_all[k][r].x);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    float lt = 0.0f, acc = 0.0f;
+    for (int k = 0; k < NB; ++k) {
+      const float f = ex2_approx(s_all[k][r].x - ref);
+      lt += s_all[k][r].y * f;
+      acc += s_o[r / NB * NB + k][d] * f;
+    }
+    y[(head0 + r) * D + d] = __float2bfloat16(acc / lt);
+    if (d == 0 && lse2) lse2[head0 + r] = mx + log2f(lt);
   }
 }
 
@@ -806,6 +1054,32 @@ cudaError_t launch_decode4(const PagedCache& c, const uint32_t* ranges, const __
   int dev = 0, num_sms = 0;
   cudaError_t e = device_sms(&dev, &num_sms);
   if (e != cudaSuccess) return e;
+  // few rows in sight: one launch of clusters
+  long long units = ((static_cast<long long>(c.max_pages) << c.page_log2) + 31) / 32;
+  if (w.window > 0) {
+    const long long cut = (w.window + 31LL) / 32 + 1 + (w.sinks + 31LL) / 32;
+    if (cut < units) units = cut;
+  }
+  const long long lists = static_cast<long long>(w.B) * c.Hkv * w.mg;
+  if (units <= 128) {
+    int nc = 1;
+    while (nc < 8 && nc * 8 < units) nc *= 2;
+    const int upw = units > 64 ? 2 : 1;
+    if (nc * lists <= (upw == 1 ? 12LL : 1LL) * num_sms) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(nc) * c.Hkv * w.mg, static_cast<unsigned>(w.B));
+      cfg.blockDim = dim3(256);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim = {static_cast<unsigned>(nc), 1, 1};
+      cfg.attrs = attr;
+      cfg.numAttrs = 2;
+      return cudaLaunchKernelEx(&cfg, paged4_short_kernel<D, QR>, c, ranges, qkv, lens, y, lse2, w, upw, err);
+    }
+  }
   // one block per SM with as many warps (rings) as its shared memory holds beside the sequences' lengths, 16 at most
   const size_t head = (2 * static_cast<size_t>(w.B) + 1) * sizeof(int);
   const size_t room = 232448 - 256 - head;
