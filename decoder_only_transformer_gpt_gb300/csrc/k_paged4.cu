@@ -1044,18 +1044,22 @@ cudaError_t launch_decode4(const PagedCache& c, const uint32_t* ranges, const __
   int dev = 0, num_sms = 0;
   cudaError_t e = device_sms(&dev, &num_sms);
   if (e != cudaSuccess) return e;
-  // few rows in sight: one launch of clusters
+  // Few rows in sight: one launch of clusters, eight blocks at most, with as many units a warp as that takes. It pays while
+  // there are not many more blocks than run at once, and not many units behind each other (graph replays, 12 heads unless
+  // stated, against the general form): 16 sequences of 1,000 rows 12.6 and 13.9 us, 32 23.5 and 17.2; 8 of 4,000 rows 17.2 and
+  // 16.9; one of 16,000 13.2 and 26.9, four 32.6 and 27.5; of 12 heads on one, where a block takes more registers, 16 sequences
+  // of 1,000 rows and 4 key heads 10.4 and 13.4, of 2,040 rows 24.8 and 19.2.
   long long units = ((static_cast<long long>(c.max_pages) << c.page_log2) + 31) / 32;
   if (w.window > 0) {
     const long long cut = (w.window + 31LL) / 32 + 1 + (w.sinks + 31LL) / 32;
     if (cut < units) units = cut;
   }
   const long long lists = static_cast<long long>(w.B) * c.Hkv * w.mg;
-  if (units <= 128) {
+  if (units <= 512) {
     int nc = 1;
     while (nc < 8 && nc * 8 < units) nc *= 2;
-    const int upw = units > 64 ? 2 : 1;
-    if (nc * lists <= (upw == 1 ? 12LL : 1LL) * num_sms) {
+    const int upw = static_cast<int>((units + 8 * nc - 1) / (8 * nc));
+    if (nc * lists <= (QR == 16 ? 2LL : 6LL) * num_sms && nc * lists * upw <= 12LL * num_sms) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(nc) * c.Hkv * w.mg, static_cast<unsigned>(w.B));
       cfg.blockDim = dim3(256);

@@ -67,7 +67,7 @@ class Case:
         return self
 
 
-FORMS = [None, 1024, 4096, 65536]          # room of the page table, by which the form is chosen
+FORMS = [None, 1024, 4096, 16384, 65536]          # room of the page table, by which the form is chosen
 
 
 @pytest.mark.parametrize("rows", FORMS)
@@ -79,7 +79,7 @@ def test_lengths_heads_and_windows(gpt_lib, rows, H, Hkv, D, page, window, sinks
         Case(H, Hkv, D, page, lens, window, sinks, seed=sum(lens), rows=rows).run()
 
 
-@pytest.mark.parametrize("rows", [2047, 2048, 2049, 4095, 4096, 4097, 9000])
+@pytest.mark.parametrize("rows", [2047, 2048, 2049, 4095, 4096, 4097, 9000, 16384, 16385])
 def test_full_tables(gpt_lib, rows):
     Case(2, 2, 64, 8, [rows], seed=rows).run()
     Case(4, 2, 32, 64, [rows, 5], seed=rows).run()
