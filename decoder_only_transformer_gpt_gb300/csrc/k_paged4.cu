@@ -37,11 +37,10 @@ constexpr unsigned kAll = 0xffffffffu;
 //    columns, so that one key head for each query head wastes half as much as with the heads as rows; the probabilities are
 //    turned over by movmatrix.
 //  * A row's scales and lowest values are made into fp32 factors once, by the lane of its number.
-//  * Units are whole tiles of the sequence, so a page's share of one is contiguous and starts on a 16-byte boundary:
-//    a few bulk copies, a lane each, bring codes and ranges into the warp's own ring (16 warps per SM), counted by an
-//    mbarrier per stage. (Copies of 16 bytes by every lane took 250 of 680 instructions a unit to find their addresses, and 131
-//    us for 16 sequences of 9,000 to 32,000 rows.) Rows of a tile that are not seen are masked: their codes are numbers whatever
-//    they hold, their factors are set to 0.
+//  * Units are whole tiles of the sequence, so every eight rows of one lie in one page and start on a 16-byte boundary: the
+//    tile's pages, one to a lane, are looked up once, and every lane copies 16 bytes at a time (cp.async) into the warp's own
+//    ring. (A few bulk copies by as many lanes, counted by an mbarrier, cost more: each lane's copy is issued by itself.) Rows
+//    of a tile that are not seen are masked: their codes are numbers whatever they hold, their factors are set to 0.
 template <int D, int QR>
 struct Dec4Cfg {
   static constexpr int UNIT = QR == 16 ? 32 : 64;                 // rows of a unit
@@ -53,9 +52,8 @@ struct Dec4Cfg {
   static constexpr int STAGES = QR == 16 ? 3 : 2;
   static constexpr int FACTORS = STAGES * STAGE;                  // the rows' factors: behind the stages
   // one head a key head: its scores of 64 rows, its factors as fp16, zeros for the products' other columns
-  static constexpr int BARS = FACTORS + (QR == 1 ? 256 + 128 + 32 : UNIT * 16);   // the stages' mbarriers
-  static constexpr int WARP = BARS + 32;
-  static constexpr int WARPS = QR == 1 ? 20 : 16;
+  static constexpr int WARP = FACTORS + (QR == 1 ? 256 + 128 + 32 : UNIT * 16);
+  static constexpr int WARPS = 16;
 };
 
 struct Dec4Scratch {
@@ -70,6 +68,15 @@ struct Dec4Shape {
   float scale_log2;
 };
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The largest of the lanes' values, in all of them (a NaN is passed over).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -387,7 +394,7 @@ struct Segment {
   // 32 rows to a value of x and of the rows' factors; x becomes the rows' probabilities times their scales.
   template <int NH, int NJ>
   __device__ __forceinline__ void weigh_one(const float (&s)[1][NJ][4], float (&x)[NH], uint32_t room, const float (&ks)[NH], const float (&kl)[NH],
-                                            const float (&vs)[NH], const float (&vl)[NH], const uint32_t (&seen)[NH], int lane) {
+                                            const float (&vs)[NH], const float (&vl)[NH], const uint32_t (&seen)[NH], uint32_t unseen, int lane) {
     if ((lane & 3) == 0) {
 #pragma unroll
       for (int h = 0; h < NH; ++h)
@@ -400,13 +407,11 @@ struct Segment {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       x[h] = fmaf(ks[h], __uint_as_float(lds32(mine + 16 * h)), kl[h] * qs[0].sum[0]);
-      if (!((seen[h] >> lane) & 1u)) x[h] = -INFINITY;
+      if (unseen && !((seen[h] >> lane) & 1u)) x[h] = -INFINITY;
       mx = fmaxf(mx, x[h]);
     }
     mx *= qs[0].c[0];
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, k));
-    mx = fmaxf(mx, m[0][0]);
+    mx = fmaxf(warp_max(mx), m[0][0]);
     const float ref = mx == -INFINITY ? 0.0f : mx;   // every score so far -inf: every term is 2^-inf
     if (mx > m[0][0]) {                              // a new maximum (the same for all lanes)
       const float a = ex2_approx(m[0][0] - ref);
@@ -482,11 +487,6 @@ struct Unit4 {
   Tiles t;
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-
 template <int D, int QR>
 __global__ void __launch_bounds__(32 * Dec4Cfg<D, QR>::WARPS, 1)
 paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __nv_bfloat16* __restrict__ qkv,
@@ -499,8 +499,6 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   int* s_prefix = reinterpret_cast<int*>(smem + nwarps * Cfg::WARP);     // [B + 1]
   int* s_rows = s_prefix + w.B + 1;                                      // [B]
   __shared__ int s_sum[Cfg::WARPS];
-  __shared__ int s_abort;
-  if (threadIdx.x == 0) s_abort = 0;
   pdl_wait();
   pdl_trigger();
 
@@ -544,16 +542,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const long long u0 = deal.start(gw);
   const int count = static_cast<int>(deal.start(gw + 1) - u0);
 
-  uint8_t* own = smem + warp * Cfg::WARP;
-  const uint32_t ring = smem_u32(own);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(own + Cfg::BARS);
-  if (lane == 0) {
-#pragma unroll
-    for (int k = 0; k < Cfg::STAGES; ++k) mbar_init(bars + k, 1);
-    fence_barrier_init();
-    fence_proxy_async_smem();
-  }
-  __syncwarp();
+  const uint32_t ring = smem_u32(smem + warp * Cfg::WARP);
   const int row = w.H + 2 * c.Hkv;                   // heads of a token's row
 
   auto set_seq = [&](Unit4& x) { x.t = tiles_of<UNIT>(s_rows[x.b], w.window, w.sinks); };   // (b has units)
@@ -584,48 +573,65 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     at.mt = hm - at.kh * w.mg;
     at.tile = static_cast<int>(r - static_cast<long long>(hm) * at.t.count);
   }
-  // A tile lies in UNIT / page pages, or in part of one: runs of rows. Lane 4 run + kind copies the run's key codes (kind 0),
-  // value codes (1), key ranges (2) or value ranges (3). Its page is looked up one unit ahead.
-  const int run_log2 = min(c.page_log2, UNIT == 64 ? 6 : 5), kind = lane & 3, run0 = (lane >> 2) << run_log2;   // run0: the run's first row
-  const uint32_t rowb = kind < 2 ? ROWB : 4, bytes = rowb << run_log2;
-  const uint32_t to = (kind < 2 ? kind * Cfg::TILE : Cfg::RANGES + (kind - 2) * UNIT * 4) + run0 * rowb;
-  const uint32_t pageb = (2u * static_cast<uint32_t>(c.Hkv) << c.page_log2) * rowb;   // a page's codes, or ranges
-  const uint8_t* from = (kind < 2 ? static_cast<const uint8_t*>(c.pool) : reinterpret_cast<const uint8_t*>(ranges)) + (kind & 1) * (pageb / 2);
-  const uint32_t in_page = static_cast<uint32_t>(run0 & ((1 << c.page_log2) - 1)) * rowb, headb = rowb << c.page_log2;
-  const uint32_t tile_mask = ((1u << c.page_log2) - 1u) & ~(UNIT - 1u);   // of a tile's first row: where in its page
+  // A copy of the warp takes 512 bytes: RPC rows' codes. This lane's 16 bytes are of eight rows whose page lane `block` (of the
+  // first copy; RPC / 8 on for each further one) has looked up; of the ranges it copies four rows' of the keys (lanes below
+  // UNIT / 4) or of the values.
+  constexpr int RPC = 512 / ROWB, COPIES = UNIT / RPC, PER8 = ROWB / 2;   // PER8: lanes that copy eight rows' codes
+  const int block = lane / PER8, pmask = (1 << c.page_log2) - 1;
+  const uint32_t pageb = (2u * static_cast<uint32_t>(c.Hkv) << c.page_log2) * ROWB, rpageb = pageb / ROWB * 4;   // a page's codes, and ranges
+  const uint32_t lo = (lane % PER8) * 16;
+  const uint8_t* pool = static_cast<const uint8_t*>(c.pool);
+  const int rrow = 4 * (lane % (UNIT / 4)), rwhich = lane / (UNIT / 4);
+  const uint8_t* rfrom = reinterpret_cast<const uint8_t*>(ranges) + rwhich * (rpageb / 2);
   Unit4 next = at;                                   // the unit whose rows are copied next
-  int pg, r0;                                        // the run's page; -2: nothing to copy. The tile's first row
+  int pg = -2, r0 = 0;                               // page of eight rows (of lanes below UNIT / 8; -2: none), the tile's first row
   auto look_up = [&]() {
     r0 = first_row<UNIT>(next.t, next.tile);
-    const int r = r0 + run0;
-    pg = run0 < UNIT && r < next.t.n ? __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (r >> c.page_log2)) : -2;
+    const int r = r0 + 8 * lane;
+    pg = lane < UNIT / 8 && r < next.t.n ? __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (r >> c.page_log2)) : -2;
   };
   look_up();
-  int issued = 0, fill = 0;                          // fill: the stage that is filled next
+  int issued = 0;
+  uint32_t fill = ring;                              // the stage that is filled next
   auto issue = [&]() {                               // copies unit `next`, steps on
-    const bool ok = static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages);
-    if (!ok && pg != -2) record_error(err, GPT_DEV_EPAGE);
-    const bool starts = issued == 0 || next.tile == 0;   // a segment starts: its queries
-    const int gn = min(w.G - next.mt * 16, 16);
-    const uint32_t who = __ballot_sync(kAll, ok), bar = smem_u32(bars + fill), dst = ring + fill * Cfg::STAGE;
-    if (lane == 0)
-      mbar_arrive_expect_tx(bars + fill, ((__popc(who & 0x33333333u) * ROWB + __popc(who & 0xccccccccu) * 4) << run_log2) +
-                                             (starts ? gn * D * 2 : 0));
-    __syncwarp();
-    if (ok)
-      bulk_load(dst + to, from + static_cast<size_t>(static_cast<uint32_t>(pg)) * pageb +
-                              (static_cast<uint32_t>(next.kh) * headb + (r0 & tile_mask) * rowb + in_page), bytes, bar);
-    if (starts && lane == 0)
-      bulk_load(dst + Cfg::QUERIES, qkv + (static_cast<size_t>(next.b) * row + next.kh * w.G + next.mt * 16) * D, gn * D * 2, bar);
-    fill = fill == Cfg::STAGES - 1 ? 0 : fill + 1;
+    if (static_cast<unsigned>(pg) >= static_cast<unsigned>(c.pages) && pg != -2) {
+      record_error(err, GPT_DEV_EPAGE);
+      pg = -2;
+    }
+    const uint32_t khrows = static_cast<uint32_t>(next.kh) << c.page_log2;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+      const int mine = __shfl_sync(kAll, pg, block + i * (RPC / 8));
+      const uint32_t in_page = (khrows + ((r0 + 8 * block + i * RPC) & pmask)) * ROWB + lo;
+      if (mine >= 0) {
+        const uint8_t* src = pool + static_cast<size_t>(static_cast<uint32_t>(mine)) * pageb + in_page;
+        copy16(fill + lane * 16 + i * 512, src);
+        copy16(fill + Cfg::TILE + lane * 16 + i * 512, src + pageb / 2);
+      }
+    }
+    {
+      const int mine = __shfl_sync(kAll, pg, rrow / 8);
+      if (mine >= 0 && lane < UNIT / 2)
+        copy16(fill + Cfg::RANGES + lane * 16, rfrom + static_cast<size_t>(static_cast<uint32_t>(mine)) * rpageb + (khrows + ((r0 + rrow) & pmask)) * 4);
+    }
+    if (issued == 0 || next.tile == 0) {             // a segment starts: its queries
+      const int gn = min(w.G - next.mt * 16, 16);
+      const __nv_bfloat16* tok = qkv + (static_cast<size_t>(next.b) * row + next.kh * w.G + next.mt * 16) * D;
+#pragma unroll
+      for (int i = 0; i < (QR * D + 255) / 256; ++i)
+        if (32 * i + lane < gn * (D / 8)) copy16(fill + Cfg::QUERIES + (32 * i + lane) * 16, tok + 8 * (32 * i + lane));
+    }
+    fill = fill == ring + (Cfg::STAGES - 1) * Cfg::STAGE ? ring : fill + Cfg::STAGE;
     if (++issued < count) {
       advance(next);
       look_up();
     }
   };
 #pragma unroll
-  for (int s = 0; s < Cfg::STAGES - 1; ++s)
+  for (int s = 0; s < Cfg::STAGES - 1; ++s) {
     if (issued < count) issue();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
 
   constexpr bool ONE = QR == 1;
   const Exponents exps;
@@ -637,19 +643,12 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   if constexpr (ONE) {
     if (lane < 2) sts128f(factors + 256 + 128 + 16 * lane, 0.0f, 0.0f, 0.0f, 0.0f);
   }
-  int stage = 0;                                     // that is read
-  uint32_t phase = 0;
+  uint32_t st = ring;                                // the stage that is read
   for (int n = 0; n < count; ++n) {
     if (issued < count) issue();
-    if (!mbar_wait_warp(bars + stage, phase, &s_abort, err)) {   // reported; the copies under way end in this block's memory
-      for (int k = n; k < issued; ++k) {
-        mbar_wait_drain(bars + stage, phase);
-        stage = stage == Cfg::STAGES - 1 ? 0 : stage + 1;
-        if (stage == 0) phase ^= 1;
-      }
-      return;
-    }
-    const uint32_t st = ring + stage * Cfg::STAGE;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::STAGES - 1) : "memory");
+    __syncwarp();
     if (n == 0 || at.tile == 0) {
       whole = at.tile == 0;
       slot0 = n == 0 ? 0 : 1;
@@ -714,7 +713,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     };
     if constexpr (ONE) {
       float x[NH];
-      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, lane);
+      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, unseen, lane);
       const uint32_t weights = factors + 256;
 #pragma unroll
       for (int h = 0; h < NH; ++h) sts16(weights + weight_place<2 * NJ>(32 * h + lane), x[h]);
@@ -777,8 +776,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         }
     }
     advance(at);
-    stage = stage == Cfg::STAGES - 1 ? 0 : stage + 1;
-    if (stage == 0) phase ^= 1;
+    st = st == ring + (Cfg::STAGES - 1) * Cfg::STAGE ? ring : st + Cfg::STAGE;
     __syncwarp();                                    // the stage and the factors are read before they are filled again
   }
 }
@@ -895,7 +893,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     uint32_t p[2][NQ][2];
     if constexpr (ONE) {
       float x[1];
-      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, lane);
+      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, ~seen[0], lane);
       sts16(factors + 128 + weight_place<4>(lane), x[0]);
       __syncwarp();
       const uint4 w4 = lds128(factors + 128 + (n8 == 0 ? 16 * q4 : 64));   // other columns: zeros
