@@ -11,8 +11,10 @@
 // ranges [pages][2][Hkv][page] pairs (scale, lowest).
 //
 // All three kernels are bound by memory and give a warp one token (or part of one): a lane holds 16 values of a head, two
-// 16-byte units that contain each other's pair partners, D / 16 lanes a head, so a load instruction of the warp covers
-// 1 KB of the token's row. A lane computes the sine and cosine of one pair for the whole warp, once per token.
+// 16-byte units that contain each other's pair partners, D / 16 lanes a head. Neighbouring lanes hold neighbouring units, so
+// that each load and store covers whole 32-byte sectors (with units 2 i and 2 i + 1 in lane i the L2 moved 1.6 times the bytes:
+// 16 x up to 1,024 tokens into 4 bits and back 41 us). A lane computes the sine and cosine of one pair for the whole warp,
+// once per token.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -25,23 +27,25 @@ namespace gptgb {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
 
 struct Row16 {          // 16 values of a head: units u0 and u1
   uint4 a, b;
 };
 
-__device__ __forceinline__ void turn16(Row16& x, const float (&cs)[8], const float (&sn)[8], bool interleaved) {
+// cs, sn: of pairs 0-3 of unit a and of unit b where they lie side by side, else of the eight pairs that a's values form with b's.
+// ta, tb: whether unit a, or b, is turned (apart, only where pairs lie side by side).
+__device__ __forceinline__ void turn16(Row16& x, const float (&cs)[8], const float (&sn)[8], bool interleaved, bool ta, bool tb) {
   uint32_t* a = &x.a.x;
   uint32_t* b = &x.b.x;
-  if (interleaved) {                                 // pairs side by side: four in each unit
+  if (interleaved) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 p = unpack_bf16x2(a[k]), q = unpack_bf16x2(b[k]);
-      a[k] = pack_bf16x2(p.x * cs[k] - p.y * sn[k], p.y * cs[k] + p.x * sn[k]);
-      b[k] = pack_bf16x2(q.x * cs[4 + k] - q.y * sn[4 + k], q.y * cs[4 + k] + q.x * sn[4 + k]);
+      if (ta) a[k] = pack_bf16x2(p.x * cs[k] - p.y * sn[k], p.y * cs[k] + p.x * sn[k]);
+      if (tb) b[k] = pack_bf16x2(q.x * cs[4 + k] - q.y * sn[4 + k], q.y * cs[4 + k] + q.x * sn[4 + k]);
     }
-  } else {                                           // unit a's values pair with unit b's
+  } else if (ta) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 p = unpack_bf16x2(a[k]), q = unpack_bf16x2(b[k]);
@@ -109,7 +113,7 @@ struct AppendArgs {
 
 // MODE 0: rotation alone; 1: keys and values into c.pool (bf16); 2: into c.pool (codes) and a.ranges.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kAppendWarps * 32)
+__global__ void __launch_bounds__(kAppendWarps * 32, 8)
 append_kernel(PagedCache c, AppendArgs a, int* err) {
   constexpr int U = D / 8, LANES = D / 16, HEADS = 32 / LANES;   // units and lanes of a head, heads side by side
   pdl_wait();
@@ -119,9 +123,26 @@ append_kernel(PagedCache c, AppendArgs a, int* err) {
   const unsigned tok = w / static_cast<unsigned>(a.parts), part = w - tok * a.parts;
   if (tok >= a.tokens) return;
   const int b = static_cast<int>(tok / static_cast<unsigned>(a.T)), t = static_cast<int>(tok - static_cast<unsigned>(b) * a.T);
-  if (MODE != 0 && a.count && t >= __ldg(a.count + b)) return;
+  // (on their way together)
+  const int count = MODE != 0 && a.count ? __ldg(a.count + b) : a.T;
   const long long first = MODE != 0 && a.start ? __ldg(a.start + b) : 0;
-  if (first < 0) return;                             // no sequence
+  const long long position = a.pos ? static_cast<long long>(__ldg(a.pos + b)) : first;
+  const unsigned long long turn = lane < a.rot / 2 ? __ldg(a.turns + lane) : 0;
+  if (t >= count || first < 0) return;               // behind the tokens; no sequence
+  // This lane's head (of HEADS side by side) and its two units: i and i + LANES, but of heads that are turned with partners
+  // rot / 2 apart, units i and i + rot / 16 in the first rot / 16 lanes, and those behind the first rot values in the others.
+  const int i = lane % LANES, hh = lane / LANES, pairs = a.rot / 2, apart = a.rot / 16;
+  const bool beyond = i >= apart;
+  const int u0 = i, u1 = i + LANES;
+  const int t0 = a.interleaved ? i : beyond ? i + apart : i;
+  const int t1 = a.interleaved ? u1 : beyond ? i + LANES : i + apart;
+  const int c0 = a.interleaved ? 4 * i : 8 * i, c1 = a.interleaved ? 4 * u1 : 8 * i + 4;   // pairs of the first four and the last
+  const bool ta = c0 < pairs, tb = c1 < pairs, turns = ta || tb;
+  const int NH = a.H + 2 * a.Hkv, heads = a.H + a.Hkv;
+  const size_t base = static_cast<size_t>(tok) * NH * U;
+  const uint4* src = a.qkv + base;
+  uint4* dst = a.out ? a.out + base : nullptr;
+  const bool in_place = a.out == a.qkv;
   const long long r = first + t;
   long long row = -1;                                // of the key of head 0 in the pool
   size_t weight = 0;
@@ -137,31 +158,20 @@ append_kernel(PagedCache c, AppendArgs a, int* err) {
       }
     }
   }
-  // this lane's head (of HEADS side by side) and its two units
-  const int i = lane % LANES, hh = lane / LANES, pairs = a.rot / 2;
-  const bool turns = 8 * i < pairs;
-  const int u0 = turns && !a.interleaved ? i : 2 * i, u1 = turns && !a.interleaved ? i + a.rot / 16 : 2 * i + 1;
-  const int NH = a.H + 2 * a.Hkv, heads = a.H + a.Hkv;
-  const size_t base = static_cast<size_t>(tok) * NH * U;
-  const uint4* src = a.qkv + base;
-  uint4* dst = a.out ? a.out + base : nullptr;
-  const bool in_place = a.out == a.qkv;
   float cs[8], sn[8];
   if (pairs) {
-    float s = 0.0f, co = 1.0f;
-    if (lane < pairs) {
-      const long long n = (a.pos ? static_cast<long long>(__ldg(a.pos + b)) : first) + t;
-      const unsigned long long phase = static_cast<unsigned long long>(n) * __ldg(a.turns + lane);
-      sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &co);   // 2 / 2^32 half turns
-      if (a.inverse) s = -s;
-    }
+    float s, co;
+    const unsigned long long phase = static_cast<unsigned long long>(position + t) * turn;
+    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &co);   // 2 / 2^32 half turns
+    if (a.inverse) s = -s;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      cs[k] = __shfl_sync(kAll, co, (8 * i + k) & 31);
-      sn[k] = __shfl_sync(kAll, s, (8 * i + k) & 31);
+      const int from = ((k < 4 ? c0 : c1) + (k & 3)) & 31;
+      cs[k] = __shfl_sync(kAll, co, from);
+      sn[k] = __shfl_sync(kAll, s, from);
     }
   }
-  // Heads [h0, h1), HEADS side by side in a step of the warp, two steps' loads in flight.
+  // Heads [h0, h1), HEADS side by side in a step of the warp, two steps' loads in flight; those below `heads` are turned.
   auto walk = [&](int h0, int h1, auto&& use) {
     for (h0 += static_cast<int>(part) * HEADS; h0 < h1; h0 += 2 * HEADS * a.parts) {
       Row16 x[2];
@@ -171,36 +181,36 @@ append_kernel(PagedCache c, AppendArgs a, int* err) {
       for (int k = 0; k < 2; ++k) {
         hd[k] = h0 + k * HEADS * a.parts + hh;
         if (k && !two) break;
-        const size_t at = static_cast<size_t>(min(hd[k], h1 - 1)) * U;
-        x[k].a = src[at + u0];
-        x[k].b = src[at + u1];
+        const int at = min(hd[k], h1 - 1);
+        x[k].a = src[static_cast<size_t>(at) * U + (at < heads ? t0 : u0)];
+        x[k].b = src[static_cast<size_t>(at) * U + (at < heads ? t1 : u1)];
       }
       use(x[0], hd[0], hd[0] < h1);
       if (two) use(x[1], hd[1], hd[1] < h1);
     }
   };
-  auto put = [&](const Row16& x, int hd) {
-    dst[static_cast<size_t>(hd) * U + u0] = x.a;
-    dst[static_cast<size_t>(hd) * U + u1] = x.b;
+  auto put = [&](const Row16& x, int hd, int at0, int at1) {
+    dst[static_cast<size_t>(hd) * U + at0] = x.a;
+    dst[static_cast<size_t>(hd) * U + at1] = x.b;
   };
   if (dst)                                           // without an output the queries are not needed
     walk(0, a.H, [&](Row16& x, int hd, bool ok) {
-      if (turns) turn16(x, cs, sn, a.interleaved);
-      if (ok && (turns || !in_place)) put(x, hd);
+      turn16(x, cs, sn, a.interleaved, ta, tb);
+      if (ok && (turns || !in_place)) put(x, hd, t0, t1);
     });
-  if (MODE == 0 && in_place && !pairs) return;
   walk(a.H, MODE == 0 && in_place ? heads : NH, [&](Row16& x, int hd, bool ok) {
-    const bool moved = turns && hd < heads;
-    if (moved) turn16(x, cs, sn, a.interleaved);
-    if (ok && dst && (moved || !in_place)) put(x, hd);
+    const bool key = hd < heads;
+    const int at0 = key ? t0 : u0, at1 = key ? t1 : u1;
+    if (key) turn16(x, cs, sn, a.interleaved, ta, tb);
+    if (ok && dst && ((key && turns) || !in_place)) put(x, hd, at0, at1);
     if (MODE == 0) return;
     const int e = hd - a.H;                          // key head, or Hkv + value head
     const bool stored = ok && row >= 0;
     const long long to = row + (static_cast<long long>(e) << c.page_log2);
     if (MODE == 1 && stored) {
       uint4* pool = static_cast<uint4*>(c.pool);
-      pool[to * U + u0] = x.a;
-      pool[to * U + u1] = x.b;
+      pool[to * U + at0] = x.a;
+      pool[to * U + at1] = x.b;
       if (c.weight && i == 0 && e < a.Hkv) c.weight[weight + (static_cast<size_t>(e) << c.page_log2)] = 0.0f;
     }
     if (MODE == 2) {
@@ -209,13 +219,8 @@ append_kernel(PagedCache c, AppendArgs a, int* err) {
       if (stored) {
         uint32_t* codes = static_cast<uint32_t*>(c.pool) + to * U;
         const bool bad = range == 0x7fff7fffu;
-        const uint32_t ca = bad ? 0u : codes8(x.a, low, inv), cb = bad ? 0u : codes8(x.b, low, inv);
-        if (u1 == u0 + 1) {
-          *reinterpret_cast<uint2*>(codes + u0) = make_uint2(ca, cb);
-        } else {
-          codes[u0] = ca;
-          codes[u1] = cb;
-        }
+        codes[at0] = bad ? 0u : codes8(x.a, low, inv);
+        codes[at1] = bad ? 0u : codes8(x.b, low, inv);
         if (i == 0) a.ranges[to] = range;
       }
     }
@@ -246,15 +251,15 @@ load4_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const int32_t* _
   if (pg < 0) return;
   const size_t row = row_at(c, pg, 0, 0, static_cast<int>(r) & ((1 << c.page_log2) - 1));
   const int i = lane % LANES, hh = lane / LANES, NH = 2 * c.Hkv;
-  const uint2* codes = static_cast<const uint2*>(c.pool);
+  const uint32_t* codes = static_cast<const uint32_t*>(c.pool);
   uint4* dst = rows + static_cast<size_t>(tok) * NH * U;
   for (int h0 = static_cast<int>(part) * HEADS; h0 < NH; h0 += 2 * HEADS * parts) {
-    uint2 x[2];
-    uint32_t range[2];
+    uint32_t x[2][2], range[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const size_t from = row + (static_cast<size_t>(min(h0 + k * HEADS * parts + hh, NH - 1)) << c.page_log2);
-      x[k] = __ldg(codes + from * LANES + i);
+      x[k][0] = __ldg(codes + from * U + i);
+      x[k][1] = __ldg(codes + from * U + i + LANES);
       range[k] = __ldg(ranges + from);
     }
 #pragma unroll
@@ -262,15 +267,16 @@ load4_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const int32_t* _
       const int hd = h0 + k * HEADS * parts + hh;
       if (hd >= NH) continue;
       const float2 f = unpack_bf16x2(range[k]);      // scale, lowest
-      const uint32_t words[2] = {x[k].x, x[k].y};
-      uint32_t v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t n = words[j >> 2] >> (8 * (j & 3));
-        v[j] = pack_bf16x2(fmaf(f.x, static_cast<float>(n & 15u), f.y), fmaf(f.x, static_cast<float>((n >> 4) & 15u), f.y));
+      for (int j = 0; j < 2; ++j) {
+        uint32_t v[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t two = x[k][j] >> (8 * n);
+          v[n] = pack_bf16x2(fmaf(f.x, static_cast<float>(two & 15u), f.y), fmaf(f.x, static_cast<float>((two >> 4) & 15u), f.y));
+        }
+        dst[static_cast<size_t>(hd) * U + i + j * LANES] = make_uint4(v[0], v[1], v[2], v[3]);
       }
-      dst[static_cast<size_t>(hd) * U + 2 * i] = make_uint4(v[0], v[1], v[2], v[3]);
-      dst[static_cast<size_t>(hd) * U + 2 * i + 1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
   }
 }
