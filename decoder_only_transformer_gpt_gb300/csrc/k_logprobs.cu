@@ -405,7 +405,8 @@ logprobs_kernel(LpArgs a, int* err) {
 }
 
 // dz = dlogp (1[j = t] - p) - dentropy p (ln p + entropy), from (m, S): p = e^d / S. Bound by memory: the logits once in,
-// once out. A block takes 256 x kGradVecs vectors of a row.
+// once out. A block takes 256 x kGradVecs vectors of a row. The last rows come first: they are what the call that made (m, S)
+// has left in L2 (4,096 x 50,257 in bf16, both calls: 198 us, in the other order 202; with streaming loads or stores more).
 constexpr int kGradVecs = 4;
 
 struct LpGrad {
@@ -425,8 +426,8 @@ logprobs_grad_kernel(LpGrad a) {
   pdl_wait();
   pdl_trigger();
   for (long long u = blockIdx.x; u < a.M * a.segments; u += gridDim.x) {
-    const long long m = u / a.segments;
-    const int seg = static_cast<int>(u - m * a.segments);
+    const long long up = u / a.segments, m = a.M - 1 - up;
+    const int seg = static_cast<int>(u - up * a.segments);
     const Row<T> row(a.z, a.ld, a.V, m);
     T* out = static_cast<T*>(a.dz) + m * a.dld;
     const uint4* vecs = reinterpret_cast<const uint4*>(row.z + row.head);
