@@ -1,7 +1,8 @@
 // Attention of one query row per sequence over the paged cache in 4 bits (layout: k_append.cu).
 //
 // A row stands for low + scale * code, so with Q = sum of a query's values
-//   q . k_r = scale_r (q . code_r) + low_r Q,    sum_r p_r u_r = sum_r (p_r scale_r) (code_r - 8) + sum_r p_r (low_r + 8 scale_r),
+//   q . k_r = scale_r (q . code_r) + low_r Q,
+//   sum_r p_r u_r = sum_r (p_r scale_r) (code_r - 8) + sum_r p_r (low_r + 8 scale_r),
 // and codes enter the products as they are, as fp16 numbers code - 8: a code in the low four bits of a half with the
 // exponent of 1024 is 1024 + code, one in bits 4 to 7 with the exponent of 64 is 64 + code, so a shift serves four operand
 // registers and each takes one logical operation and one packed subtraction, which is exact. (In bf16, whose seven bits of
@@ -26,9 +27,10 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// Bound by issuing instructions, about 400 for a unit: a byte of codes takes a warp four times the unpacking and products of
-// a byte of bf16, and the integer unit takes a warp's instruction only every other cycle. Work is dealt as in the 16-bit
-// cache's kernel (k_paged.cu): units of 64 rows (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal
+// Bound by issuing instructions, about 350 for 32 rows of a key head: a byte of codes takes a warp four times the unpacking
+// and products of a byte of bf16, and the integer unit takes a warp's instruction only every other cycle. Measured: 16
+// sequences of 9,000 to 32,000 rows x 12 heads 60.5 us, 4.7 TB/s. Work is dealt as in the 16-bit cache's kernel (k_paged.cu):
+// units of 64 rows (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal
 // contiguous ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
 //    memory as they lie there, without ldmatrix: a lane takes a quarter of a key row (8 bytes: its codes are the lane's
@@ -49,8 +51,7 @@ struct Dec4Cfg {
   static constexpr int RANGES = 2 * TILE;                         // offset of the keys' ranges, then the values'
   static constexpr int QUERIES = RANGES + UNIT * 8;               // offset of the query rows (where a unit starts a segment)
   static constexpr int STAGE = QUERIES + QR * D * 2;
-  static constexpr int STAGES = QR == 16 ? 3 : 2;
-  static constexpr int FACTORS = STAGES * STAGE;                  // the rows' factors: behind the stages
+  static constexpr int FACTORS = 2 * STAGE;                      // the rows' factors: behind two stages
   // one head a key head: its scores of 64 rows, its factors as fp16, zeros for the products' other columns
   static constexpr int WARP = FACTORS + (QR == 1 ? 256 + 128 + 32 : UNIT * 16);
   static constexpr int WARPS = 16;
@@ -106,7 +107,8 @@ __device__ __forceinline__ void sts128f(uint32_t a, float x, float y, float z, f
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 // fp16 products: d = a b + c, and c += a b
-__device__ __forceinline__ void mma16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+__device__ __forceinline__ void mma16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                           const float (&c)[4]) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%10, %11, %12, %13};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -148,7 +150,8 @@ __device__ __forceinline__ uint32_t masked_or(uint32_t x, uint32_t y) {   // (x 
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(y));
   return r;
 }
-__device__ __forceinline__ void unpack8(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t w, const Exponents& exps) {
+__device__ __forceinline__ void unpack8(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t w,
+                                        const Exponents& exps) {
   auto less = [](uint32_t x, uint32_t y) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
     return *reinterpret_cast<const uint32_t*>(&d);
@@ -166,10 +169,10 @@ __device__ __forceinline__ float low_of(uint32_t range) { return __uint_as_float
 __device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 
-// The rows that a sequence's query sees, from its length (-1: none to compute).
+// A sequence's rows, from its length (-1: no sequence, -2: more than its table has room for).
 __device__ __forceinline__ int rows_of(const PagedCache& c, const Dec4Shape& w, int len) {
-  return len < 0 ? -1 : static_cast<long long>(len) + w.added > (static_cast<long long>(c.max_pages) << c.page_log2) ? -2
-                                                                                                                      : len + w.added;
+  if (len < 0) return -1;
+  return static_cast<long long>(len) + w.added > (static_cast<long long>(c.max_pages) << c.page_log2) ? -2 : len + w.added;
 }
 
 // A unit's products have the cached rows, or the value columns, as the 16 rows of their first operand, and eight query heads
@@ -229,8 +232,8 @@ struct Queries {
 
 // Products q . code of 16 key rows, tile j of s; w: this lane's quarter of rows n and n + 8.
 template <int D, int NQ, int NJ>
-__device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], int j, const Queries<D> (&q)[NQ], const uint32_t (&w)[2][D / 32],
-                                            const Exponents& exps) {
+__device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], int j, const Queries<D> (&q)[NQ],
+                                            const uint32_t (&w)[2][D / 32], const Exponents& exps) {
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     uint32_t a[4], b[4];
@@ -246,10 +249,11 @@ __device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], int j, const 
 }
 
 // O += (code - 8) P for 16 value rows; w: byte columns (of D = 64 words, else half words) of rows q, q + 4, q + 8, q + 12; p:
-// probabilities times the rows' scales, as second operands. Tile t of O has values 8 n + 2 t and, in its lower half, 8 n + 2 t + 1
-// as rows (D = 32: 4 n + ..).
+// probabilities times the rows' scales, as second operands. Tile t of O has values 8 n + 2 t and, in its lower half,
+// 8 n + 2 t + 1 as rows (D = 32: 4 n + ..).
 template <int D, int NQ>
-__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint32_t (&p)[NQ][2], const uint32_t (&w)[4], const Exponents& exps) {
+__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint32_t (&p)[NQ][2], const uint32_t (&w)[4],
+                                          const Exponents& exps) {
   uint32_t x[2][2];                                  // codes 0-3 and, of D = 64, 4-7 of two rows each, side by side
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -326,7 +330,8 @@ struct Segment {
   // Scores of the tiles into probabilities times the rows' scales. factors: shared address of the rows' (key scale, key
   // lowest, value scale 2^(15 - e), (value lowest + 8 value scale) 2^(15 - e)).
   template <int NJ>
-  __device__ __forceinline__ void weigh(float (&s)[NQ][NJ][4], uint32_t factors, const uint32_t (&seen)[NJ / 2], uint32_t unseen, int lane) {
+  __device__ __forceinline__ void weigh(float (&s)[NQ][NJ][4], uint32_t factors, const uint32_t (&seen)[NJ / 2],
+                                        uint32_t unseen, int lane) {
     const int n8 = lane >> 2;
     float2 vf[2 * NJ];                               // the value rows' factors, of rows 8 r + row_in_eight(n8)
 #pragma unroll
@@ -393,8 +398,9 @@ struct Segment {
   // The same of one head: s has the products in lanes 4 n, which go round the warp in shared memory (128 NH bytes at `room`),
   // 32 rows to a value of x and of the rows' factors; x becomes the rows' probabilities times their scales.
   template <int NH, int NJ>
-  __device__ __forceinline__ void weigh_one(const float (&s)[1][NJ][4], float (&x)[NH], uint32_t room, const float (&ks)[NH], const float (&kl)[NH],
-                                            const float (&vs)[NH], const float (&vl)[NH], const uint32_t (&seen)[NH], uint32_t unseen, int lane) {
+  __device__ __forceinline__ void weigh_one(const float (&s)[1][NJ][4], float (&x)[NH], uint32_t room,
+                                            const float (&ks)[NH], const float (&kl)[NH], const float (&vs)[NH],
+                                            const float (&vl)[NH], const uint32_t (&seen)[NH], uint32_t unseen, int lane) {
     if ((lane & 3) == 0) {
 #pragma unroll
       for (int h = 0; h < NH; ++h)
@@ -481,9 +487,10 @@ __device__ __forceinline__ Tiles tiles_of(int n, int window, int sinks) {
 template <int UNIT>
 __device__ __forceinline__ int first_row(const Tiles& t, int v) { return (v < t.head ? v : v + t.gap) * UNIT; }
 
-// The list position of a unit: sequence, key head, group of its query heads, tile of the sequence's seen rows.
-struct Unit4 {
-  int b, kh, mt, tile;
+// A warp's part of a segment: tiles [t0, t1) of the rows that a sequence's query sees, of one key head and a group of its query
+// heads.
+struct Piece {
+  int b, kh, mt, t0, t1;
   Tiles t;
 };
 
@@ -545,18 +552,24 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const uint32_t ring = smem_u32(smem + warp * Cfg::WARP);
   const int row = w.H + 2 * c.Hkv;                   // heads of a token's row
 
-  auto set_seq = [&](Unit4& x) { x.t = tiles_of<UNIT>(s_rows[x.b], w.window, w.sinks); };   // (b has units)
-  auto advance = [&](Unit4& x) {
-    if (++x.tile < x.t.count) return;
-    x.tile = 0;
-    if (++x.mt < w.mg) return;
-    x.mt = 0;
-    if (++x.kh < c.Hkv) return;
-    x.kh = 0;
-    do ++x.b; while (x.b < w.B && s_prefix[x.b + 1] == s_prefix[x.b]);
-    if (x.b < w.B) set_seq(x);
+  int left = count;                                  // units behind the pieces made so far
+  auto cut_piece = [&](Piece& x) {
+    x.t1 = min(x.t.count, x.t0 + left);
+    left -= x.t1 - x.t0;
   };
-  Unit4 at;                                          // the unit that is computed next
+  auto next_piece = [&](Piece& x) {
+    x.t0 = 0;
+    if (++x.mt == w.mg) {
+      x.mt = 0;
+      if (++x.kh == c.Hkv) {
+        x.kh = 0;
+        do ++x.b; while (s_prefix[x.b + 1] == s_prefix[x.b]);   // (a sequence with units follows)
+        x.t = tiles_of<UNIT>(s_rows[x.b], w.window, w.sinks);
+      }
+    }
+    cut_piece(x);
+  };
+  Piece at;                                          // the piece that is computed
   {
     const int target = static_cast<int>(u0 / HM);    // the sequence with prefix[b] <= target < prefix[b + 1]
     int lo = 0, hi = w.B - 1;
@@ -566,13 +579,17 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       else lo = mid + 1;
     }
     at.b = lo;
-    set_seq(at);
+    at.t = tiles_of<UNIT>(s_rows[lo], w.window, w.sinks);
     const long long r = u0 - static_cast<long long>(s_prefix[lo]) * HM;
     const int hm = static_cast<int>(r / at.t.count);
     at.kh = hm / w.mg;
     at.mt = hm - at.kh * w.mg;
-    at.tile = static_cast<int>(r - static_cast<long long>(hm) * at.t.count);
+    at.t0 = static_cast<int>(r - static_cast<long long>(hm) * at.t.count);
+    cut_piece(at);
   }
+  Piece next = at;                                   // and the one behind it
+  bool more = left > 0;
+  if (more) next_piece(next);
   // A copy of the warp takes 512 bytes: RPC rows' codes. This lane's 16 bytes are of eight rows whose page lane `block` (of the
   // first copy; RPC / 8 on for each further one) has looked up; of the ranges it copies four rows' of the keys (lanes below
   // UNIT / 4) or of the values.
@@ -583,201 +600,201 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const uint8_t* pool = static_cast<const uint8_t*>(c.pool);
   const int rrow = 4 * (lane % (UNIT / 4)), rwhich = lane / (UNIT / 4);
   const uint8_t* rfrom = reinterpret_cast<const uint8_t*>(ranges) + rwhich * (rpageb / 2);
-  Unit4 next = at;                                   // the unit whose rows are copied next
-  int pg = -2, r0 = 0;                               // page of eight rows (of lanes below UNIT / 8; -2: none), the tile's first row
-  auto look_up = [&]() {
-    r0 = first_row<UNIT>(next.t, next.tile);
+  // of the unit that is copied next: page of eight rows (of lanes below UNIT / 8; -2: none), the tile's first row
+  int pg = -2, r0 = 0;
+  auto look_up = [&](const Piece& x, int tile) {
+    r0 = first_row<UNIT>(x.t, tile);
     const int r = r0 + 8 * lane;
-    pg = lane < UNIT / 8 && r < next.t.n ? __ldg(c.table + static_cast<size_t>(next.b) * c.max_pages + (r >> c.page_log2)) : -2;
+    pg = lane < UNIT / 8 && r < x.t.n ? __ldg(c.table + static_cast<size_t>(x.b) * c.max_pages + (r >> c.page_log2)) : -2;
   };
-  look_up();
-  int issued = 0;
-  uint32_t fill = ring;                              // the stage that is filled next
-  auto issue = [&]() {                               // copies unit `next`, steps on
+  auto copy_rows = [&](int kh, uint32_t to) {
     if (static_cast<unsigned>(pg) >= static_cast<unsigned>(c.pages) && pg != -2) {
       record_error(err, GPT_DEV_EPAGE);
       pg = -2;
     }
-    const uint32_t khrows = static_cast<uint32_t>(next.kh) << c.page_log2;
+    const uint32_t khrows = static_cast<uint32_t>(kh) << c.page_log2;
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
       const int mine = __shfl_sync(kAll, pg, block + i * (RPC / 8));
       const uint32_t in_page = (khrows + ((r0 + 8 * block + i * RPC) & pmask)) * ROWB + lo;
       if (mine >= 0) {
         const uint8_t* src = pool + static_cast<size_t>(static_cast<uint32_t>(mine)) * pageb + in_page;
-        copy16(fill + lane * 16 + i * 512, src);
-        copy16(fill + Cfg::TILE + lane * 16 + i * 512, src + pageb / 2);
+        copy16(to + lane * 16 + i * 512, src);
+        copy16(to + Cfg::TILE + lane * 16 + i * 512, src + pageb / 2);
       }
     }
-    {
-      const int mine = __shfl_sync(kAll, pg, rrow / 8);
-      if (mine >= 0 && lane < UNIT / 2)
-        copy16(fill + Cfg::RANGES + lane * 16, rfrom + static_cast<size_t>(static_cast<uint32_t>(mine)) * rpageb + (khrows + ((r0 + rrow) & pmask)) * 4);
-    }
-    if (issued == 0 || next.tile == 0) {             // a segment starts: its queries
-      const int gn = min(w.G - next.mt * 16, 16);
-      const __nv_bfloat16* tok = qkv + (static_cast<size_t>(next.b) * row + next.kh * w.G + next.mt * 16) * D;
-#pragma unroll
-      for (int i = 0; i < (QR * D + 255) / 256; ++i)
-        if (32 * i + lane < gn * (D / 8)) copy16(fill + Cfg::QUERIES + (32 * i + lane) * 16, tok + 8 * (32 * i + lane));
-    }
-    fill = fill == ring + (Cfg::STAGES - 1) * Cfg::STAGE ? ring : fill + Cfg::STAGE;
-    if (++issued < count) {
-      advance(next);
-      look_up();
-    }
+    const int mine = __shfl_sync(kAll, pg, rrow / 8);
+    if (mine >= 0 && lane < UNIT / 2)
+      copy16(to + Cfg::RANGES + lane * 16, rfrom + static_cast<size_t>(static_cast<uint32_t>(mine)) * rpageb + (khrows + ((r0 + rrow) & pmask)) * 4);
   };
+  auto copy_queries = [&](const Piece& x, uint32_t to) {
+    const int gn = min(w.G - x.mt * 16, 16);
+    const __nv_bfloat16* tok = qkv + (static_cast<size_t>(x.b) * row + x.kh * w.G + x.mt * 16) * D;
 #pragma unroll
-  for (int s = 0; s < Cfg::STAGES - 1; ++s) {
-    if (issued < count) issue();
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
+    for (int i = 0; i < (QR * D + 255) / 256; ++i)
+      if (32 * i + lane < gn * (D / 8)) copy16(to + Cfg::QUERIES + (32 * i + lane) * 16, tok + 8 * (32 * i + lane));
+  };
 
   constexpr bool ONE = QR == 1;
   const Exponents exps;
   Segment<D, QR> g;
-  bool whole = false;                                // the segment's units so far are all in this warp's range
-  uint32_t slot0 = 0;                                // of the two places for partial results
   const int n8 = lane >> 2, q4 = lane & 3;
   const uint32_t factors = ring + Cfg::FACTORS;
   if constexpr (ONE) {
     if (lane < 2) sts128f(factors + 256 + 128 + 16 * lane, 0.0f, 0.0f, 0.0f, 0.0f);
   }
-  uint32_t st = ring;                                // the stage that is read
-  for (int n = 0; n < count; ++n) {
-    if (issued < count) issue();
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::STAGES - 1) : "memory");
-    __syncwarp();
-    if (n == 0 || at.tile == 0) {
-      whole = at.tile == 0;
-      slot0 = n == 0 ? 0 : 1;
-      g.start(w.scale_log2, min(w.G - at.mt * 16, 16), lane,
-              [&](int r, int u) { return lds128(st + Cfg::QUERIES + (r * (D / 8) + u) * 16); });
-    }
-    uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
-    float ks[NH], kl[NH], vs[NH], vl[NH];            // the factors of rows `lane` and, of a unit of 64, 32 + lane
-    {
-      const int f = first_row<UNIT>(at.t, at.tile), after = at.t.n - w.window;   // the window's first row
-      const bool cut = f + UNIT > at.t.n || (w.window > 0 && f < after && f + UNIT > w.sinks);
-      float size = 0.0f;
+  uint32_t st = ring, other = ring + Cfg::STAGE;     // the stage that is read, and the one that is filled meanwhile
+  look_up(at, at.t0);
+  copy_rows(at.kh, st);
+  copy_queries(at, st);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if (at.t0 + 1 < at.t1) look_up(at, at.t0 + 1);
+  uint32_t slot0 = 0;                                // of the two places for partial results
+  while (true) {
+    for (int tile = at.t0; tile < at.t1; ++tile) {
+      if (tile + 1 < at.t1) {
+        copy_rows(at.kh, other);
+        if (tile + 2 < at.t1) look_up(at, tile + 2);
+        else if (more) look_up(next, 0);
+      } else if (more) {
+        if (at.t1 == at.t0 + 1) look_up(next, 0);      // (of pieces of one tile not before now)
+        copy_rows(next.kh, other);
+        copy_queries(next, other);
+        if (next.t1 > 1) look_up(next, 1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      if (tile == at.t0)
+        g.start(w.scale_log2, min(w.G - at.mt * 16, 16), lane,
+                [&](int r, int u) { return lds128(st + Cfg::QUERIES + (r * (D / 8) + u) * 16); });
+      const int f = first_row<UNIT>(at.t, tile), after = at.t.n - w.window;   // the window's first row
+      uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
+      float ks[NH], kl[NH], vs[NH], vl[NH];            // the factors of rows `lane` and, of a unit of 64, 32 + lane
+      {
+        const bool cut = f + UNIT > at.t.n || (w.window > 0 && f < after && f + UNIT > w.sinks);
+        float size = 0.0f;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const uint32_t kr = lds32(st + Cfg::RANGES + 4 * (32 * h + lane));
-        uint32_t vr = lds32(st + Cfg::RANGES + 4 * (UNIT + 32 * h + lane));
-        seen[h] = kAll;
-        if (cut) {
-          const int r = f + 32 * h + lane;
-          const bool mine = r < at.t.n && (w.window == 0 || r >= after || r < w.sinks);
-          seen[h] = __ballot_sync(kAll, mine);
-          if (!mine) vr = 0u;
+        for (int h = 0; h < NH; ++h) {
+          const uint32_t kr = lds32(st + Cfg::RANGES + 4 * (32 * h + lane));
+          uint32_t vr = lds32(st + Cfg::RANGES + 4 * (UNIT + 32 * h + lane));
+          seen[h] = kAll;
+          if (cut) {
+            const int r = f + 32 * h + lane;
+            const bool mine = r < at.t.n && (w.window == 0 || r >= after || r < w.sinks);
+            seen[h] = __ballot_sync(kAll, mine);
+            if (!mine) vr = 0u;
+          }
+          unseen |= ~seen[h];
+          ks[h] = scale_of(kr);
+          kl[h] = low_of(kr);
+          vs[h] = scale_of(vr);
+          vl[h] = low_of(vr);
+          size = fmax3(size, vs[h], fabsf(vl[h]));
         }
-        unseen |= ~seen[h];
-        ks[h] = scale_of(kr);
-        kl[h] = low_of(kr);
-        vs[h] = scale_of(vr);
-        vl[h] = low_of(vr);
-        size = fmax3(size, vs[h], fabsf(vl[h]));
-      }
-      g.fit(size);
+        g.fit(size);
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        vl[h] = fmaf(8.0f, vs[h], vl[h]) * g.into;
-        vs[h] *= g.into;
-        if constexpr (!ONE) sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h], vl[h]);
-      }
-    }
-    float s[NQ][NJ][4];
-    const uint32_t krow = st + row_in_eight(n8) * ROWB + q4 * (D / 8), vcol = st + Cfg::TILE + q4 * ROWB + n8 * (D / 16);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      uint32_t x[2][D / 32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (D == 64) {
-          const uint2 u = lds64(krow + (16 * j + 8 * h) * ROWB);
-          x[h][0] = u.x;
-          x[h][1] = u.y;
-        } else {
-          x[h][0] = lds32(krow + (16 * j + 8 * h) * ROWB);
+        for (int h = 0; h < NH; ++h) {
+          vl[h] = fmaf(8.0f, vs[h], vl[h]) * g.into;
+          vs[h] *= g.into;
+          if constexpr (!ONE) sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h], vl[h]);
         }
       }
-      code_scores<D, NQ, NJ>(s, j, g.qs, x, exps);
-    }
-    auto value_words = [&](uint32_t (&x)[4], int j) {
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        if constexpr (D == 64) x[h] = lds32(vcol + (16 * j + 4 * h) * ROWB);
-        else x[h] = lds16(vcol + (16 * j + 4 * h) * ROWB);
-      }
-    };
-    if constexpr (ONE) {
-      float x[NH];
-      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, unseen, lane);
-      const uint32_t weights = factors + 256;
-#pragma unroll
-      for (int h = 0; h < NH; ++h) sts16(weights + weight_place<2 * NJ>(32 * h + lane), x[h]);
-      __syncwarp();
-      const uint32_t pa = n8 == 0 ? weights + 32 * q4 : weights + 128;   // other columns: zeros
-      const uint32_t step = n8 == 0 ? 16 : 0;
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const uint4 w4 = lds128(pa + step * h);
-        const uint32_t p0[1][2] = {{w4.x, w4.y}}, p1[1][2] = {{w4.z, w4.w}};
-        uint32_t u[4];
-        value_words(u, 2 * h);
-        add_codes<D, NQ>(g.o, p0, u, exps);
-        value_words(u, 2 * h + 1);
-        add_codes<D, NQ>(g.o, p1, u, exps);
-      }
-    } else {
-      __syncwarp();
-      g.weigh(s, factors, seen, unseen, lane);
+      float s[NQ][NJ][4];
+      const uint32_t krow = st + row_in_eight(n8) * ROWB + q4 * (D / 8), vcol = st + Cfg::TILE + q4 * ROWB + n8 * (D / 16);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        uint32_t p[NQ][2], u[4];
+        uint32_t x[2][D / 32];
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
-          p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
-        }
-        value_words(u, j);
-        add_codes<D, NQ>(g.o, p, u, exps);
-      }
-    }
-    const bool ends = at.tile == at.t.count - 1;
-    if (ends || n == count - 1) {                    // the piece is done
-      whole = whole && ends;                         // it holds all of the segment's units
-      const size_t slot = static_cast<size_t>(gw) * 2 + slot0;
-      const int gn = min(w.G - at.mt * 16, 16);
-#pragma unroll
-      for (int i = 0; i < NQ; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float v[D / 8];                            // values D / 8 n8 .. of the head
-          const float lt = g.values(i, k, v);
-          const int r = 8 * i + 2 * q4 + k;
-          if (r >= gn) continue;
-          if (whole) {
-            const size_t head = static_cast<size_t>(at.b) * w.H + at.kh * w.G + at.mt * 16 + r;
-            const float inv = 1.0f / lt;             // (a sum of 0, every score -inf, gives NaN)
-            uint32_t h[D / 16];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) h[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
-            if constexpr (D == 64) *reinterpret_cast<uint4*>(y + head * D + 8 * n8) = make_uint4(h[0], h[1], h[2], h[3]);
-            else *reinterpret_cast<uint2*>(y + head * D + 4 * n8) = make_uint2(h[0], h[1]);
-            if (n8 == 0 && lse2) lse2[head] = g.m[i][k] + log2f(lt);
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (D == 64) {
+            const uint2 u = lds64(krow + (16 * j + 8 * h) * ROWB);
+            x[h][0] = u.x;
+            x[h][1] = u.y;
           } else {
-            float4* dst = reinterpret_cast<float4*>(ws.o + (slot * QR + r) * D + n8 * (D / 8));
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-            if (n8 == 0) ws.ml[slot * QR + r] = make_float2(g.m[i][k], lt);
+            x[h][0] = lds32(krow + (16 * j + 8 * h) * ROWB);
           }
         }
+        code_scores<D, NQ, NJ>(s, j, g.qs, x, exps);
+      }
+      auto value_words = [&](uint32_t (&x)[4], int j) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if constexpr (D == 64) x[h] = lds32(vcol + (16 * j + 4 * h) * ROWB);
+          else x[h] = lds16(vcol + (16 * j + 4 * h) * ROWB);
+        }
+      };
+      if constexpr (ONE) {
+        float x[NH];
+        g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, unseen, lane);
+        const uint32_t weights = factors + 256;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) sts16(weights + weight_place<2 * NJ>(32 * h + lane), x[h]);
+        __syncwarp();
+        const uint32_t pa = n8 == 0 ? weights + 32 * q4 : weights + 128;   // other columns: zeros
+        const uint32_t step = n8 == 0 ? 16 : 0;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const uint4 w4 = lds128(pa + step * h);
+          const uint32_t p0[1][2] = {{w4.x, w4.y}}, p1[1][2] = {{w4.z, w4.w}};
+          uint32_t u[4];
+          value_words(u, 2 * h);
+          add_codes<D, NQ>(g.o, p0, u, exps);
+          value_words(u, 2 * h + 1);
+          add_codes<D, NQ>(g.o, p1, u, exps);
+        }
+      } else {
+        __syncwarp();
+        g.weigh(s, factors, seen, unseen, lane);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          uint32_t p[NQ][2], u[4];
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
+            p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
+          }
+          value_words(u, j);
+          add_codes<D, NQ>(g.o, p, u, exps);
+        }
+      }
+      const uint32_t swap = st;
+      st = other;
+      other = swap;
+      __syncwarp();                                    // the stage and the factors are read before they are filled again
     }
-    advance(at);
-    st = st == ring + (Cfg::STAGES - 1) * Cfg::STAGE ? ring : st + Cfg::STAGE;
-    __syncwarp();                                    // the stage and the factors are read before they are filled again
+    const bool whole = at.t0 == 0 && at.t1 == at.t.count;   // the piece is the segment
+    const size_t slot = static_cast<size_t>(gw) * 2 + slot0;
+    const int gn = min(w.G - at.mt * 16, 16);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float v[D / 8];                               // values D / 8 n8 .. of the head
+        const float lt = g.values(i, k, v);
+        const int r = 8 * i + 2 * q4 + k;
+        if (r >= gn) continue;
+        if (whole) {
+          const size_t head = static_cast<size_t>(at.b) * w.H + at.kh * w.G + at.mt * 16 + r;
+          const float inv = 1.0f / lt;                // (a sum of 0, every score -inf, gives NaN)
+          uint32_t h[D / 16];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) h[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+          if constexpr (D == 64) *reinterpret_cast<uint4*>(y + head * D + 8 * n8) = make_uint4(h[0], h[1], h[2], h[3]);
+          else *reinterpret_cast<uint2*>(y + head * D + 4 * n8) = make_uint2(h[0], h[1]);
+          if (n8 == 0 && lse2) lse2[head] = g.m[i][k] + log2f(lt);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(ws.o + (slot * QR + r) * D + n8 * (D / 8));
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+          if (n8 == 0) ws.ml[slot * QR + r] = make_float2(g.m[i][k], lt);
+        }
+      }
+    if (!more) break;
+    at = next;
+    slot0 = 1;
+    more = left > 0;
+    if (more) next_piece(next);
   }
 }
 
