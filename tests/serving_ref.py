@@ -57,11 +57,13 @@ def values(codes, ranges):
 def attend4(qkv, codes, ranges, table, lens, H, window, sinks, added=0):
     """(y, lse2, bounds of y's and lse2's errors apart from y's rounding); rows of no sequence are NaN.
 
-    The bounds: a score is scale (q . (16 + code) - 16 Q) + low Q; sums of up to 64 terms of at most 31 |q_d| from 16 Q on, in
-    any order, are off by 2^-21 of sum |q| 47 at most (each of the 16 steps of a product's chain by 2^-24, or 2^-23 where an
-    adder cuts off), and scaling and the low term add three roundings. So the base-2 exponents are off by d, the weights
-    by the factor 2^(2 d), another 2^-21 for exponentials and sums; the weights enter the product in parts that keep 2^-16 of
-    them, times 16 + code (up to 31), and 16 is taken back (47 in all).
+    The bounds. A score is scale (8 Q + q . (code - 8)) + low Q: the products are exact (queries enter them times a power of two,
+    in fp16; what is below 2^-38 of its largest value is lost), and a chain of at most 16 sums of at most 16 sum |q| is off by
+    2^-24 of that at every step, or 2^-23 where an adder cuts off: 2^-19 16 sum |q|, times the scale; the low term adds three
+    roundings. So the base-2 exponents are off by d, the weights by the factor 2^(2 d), another 2^-20 for exponentials and sums.
+    A weight times its scale is rounded to fp16 once, 2^-12 of it, times |code - 8| <= 8; the smallest ones to whole multiples
+    of 2^-39 of 2^E, which is at most twice the largest scale or lowest value: 2^-40 8 of that for each row. The sum that
+    stands for low + 8 scale takes the weights as they are.
     """
     pages, _, Hkv, page, half = codes.shape
     D, B, G = 2 * half, len(lens), H // Hkv
@@ -90,9 +92,11 @@ def attend4(qkv, codes, ranges, table, lens, H, window, sinks, added=0):
                 a = e / e.sum()
                 y[b, h], lse2[b, h] = a @ u, m + math.log2(e.sum())
                 qa = np.abs(q).sum()
-                d = c * qa * 2.0 ** -21 * float((47 * kr[:, 0] + 2 * kr[:, 1]).max())
+                d = c * qa * float((2.0 ** -15 * kr[:, 0] + 2.0 ** -22 * (16 * kr[:, 0] + kr[:, 1])).max())
                 el[b, h] = d + 2.0 ** -20 + 2.0 ** -22 * abs(lse2[b, h])
-                ey[b, h] = float(a @ (47 * ur[:, 0] + ur[:, 1])) * (2.0 ** -16 + 2 * (2 * d * math.log(2.0) + 2.0 ** -20))
+                off = 2 * (2 * d * math.log(2.0) + 2.0 ** -20)
+                ey[b, h] = float(a @ (8 * ur[:, 0])) * 2.0 ** -12 + float(a @ (16 * ur[:, 0] + ur[:, 1])) * off + \
+                    len(seen) * 2.0 ** -36 * float(ur.max()) / float(e.sum())
     return y.reshape(B, H * D), lse2, ey.reshape(B, H * D), el
 
 

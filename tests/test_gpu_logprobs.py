@@ -339,3 +339,31 @@ def test_more_rows_than_a_wave_and_a_graph(gpt_lib):
     assert torch.equal(ids.long(), torch.sort(x, dim=-1, descending=True, stable=True).indices[:, :3])
     one = torch.nn.functional.one_hot(t.long(), V)
     assert torch.allclose(g.double(), dl.double()[:, None] * (one - want.exp()), atol=4e-6, rtol=0)
+
+
+def test_offsets_past_32_bits(gpt_lib):
+    # rows 2.4 GB apart, and one row of 270,000,001 logits
+    from decoder_only_transformer_gpt_gb300 import binding
+    ld, V = 1_200_000_001, 5000
+    flat = torch.empty(2 * ld + V, dtype=BF16, device="cuda")
+    z = torch.as_strided(flat, (3, V), (ld, 1))
+    z.copy_(torch.from_numpy(logits(3, V, 9)))
+    t, lp, st = dev_i32(np.array([0, 77, V - 1])), torch.zeros(3, device="cuda"), torch.zeros(3, 2, device="cuda")
+    ids, top = torch.zeros(3, 5, dtype=torch.int32, device="cuda"), torch.zeros(3, 5, device="cuda")
+    binding.logprobs(z, t, lp, stats=st, top_ids=ids, top_logp=top)
+    a, _, i, v, _, _ = ref.logprobs(host(z), [0, 77, V - 1], 5)
+    assert np.array_equal(ids.cpu().numpy(), i) and np.abs(host(lp) - a).max() < 8e-6 and np.abs(host(top) - v).max() < 8e-6
+    binding.logprobs_bwd(z, t, st, torch.ones(3, device="cuda"), z)
+    p = np.exp(ref.logprobs(host(z), None)[5])
+    assert np.isfinite(p).all() and abs(float(z[2, V - 1].float()) - (1 - np.exp(a[2]))) < 2.0 ** -8
+    del flat, z
+    V = 270_000_001
+    z = torch.randn(1, V, device="cuda")
+    z[0, [5, V - 1, V // 2]] = torch.tensor([9.0, 9.0, 11.0], device="cuda")
+    lp, en = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
+    ids, top = torch.zeros(1, 3, dtype=torch.int32, device="cuda"), torch.zeros(1, 3, device="cuda")
+    binding.logprobs(z, dev_i32(np.array([V - 1])), lp, entropy=en, top_ids=ids, top_logp=top)
+    assert ids[0].tolist() == [V // 2, 5, V - 1]
+    lse = float(torch.logsumexp(z.double(), -1))
+    # V / 2048 sums one after another in a lane of the eight blocks: 2^-24 each
+    assert abs(float(lp) - (9.0 - lse)) <= 2.0 ** -24 * V / 1024 and abs(float(top[0, 0]) - (11.0 - lse)) <= 2.0 ** -24 * V / 1024
