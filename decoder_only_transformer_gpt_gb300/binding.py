@@ -555,94 +555,53 @@ def rotary_turns(freq, device="cuda"):
     return torch.from_numpy(turns).to(device)
 
 
-def _turns(torch, turns, dev):
-    """(address, turned values) of the frequencies."""
-    if turns is None:
-        return None, 0
-    if len(turns.shape) != 1:
-        raise ValueError(f"turns: shape {tuple(turns.shape)}, needs [rot / 2]")
-    return _addr("turns", turns, torch.int64, dev), 2 * turns.shape[0]
+# The operators below are called per layer and token too, and most of their kernels run for a few microseconds: their checks
+# and marshalling are compiled (csrc/py_calls.cpp).
+
+_CALLS = None
+
+
+def _compiled():
+    """The compiled calls; raise if they have not been built (no fallback path exists)."""
+    global _CALLS
+    load()
+    if not os.path.exists(os.path.join(HERE, "_calls.so")):
+        raise RuntimeError("module not built: _calls.so is missing (run `python -c 'import __graft_entry__ as g; g.build()'`)")
+    import torch  # noqa: F401 (its libraries, which the module is linked against)
+    from . import _calls
+    _CALLS = _calls
+    return _calls
 
 
 def rotary(qkv, out, H: int, Hkv: int, turns, pos=None, interleaved: bool = False, inverse: bool = False, stream=None):
     """Queries and keys of qkv [B, T, (H + 2 Hkv) D] turned by their positions pos[b] + t (pos None: t) into out (qkv
     itself: in place). inverse: back, the derivative of the same rotation."""
-    lib = _LIB or load()
-    torch, dev, s = _cuda(stream)
-    B, T, D = _qkv_dims(qkv, H, Hkv)
-    bf16 = torch.bfloat16
-    tn, rot = _turns(torch, turns, dev)
-    rc = lib.gptk_rotary(_addr("qkv", qkv, bf16, dev), _arg("out", out, bf16, qkv.shape, dev),
-                         None if pos is None else _arg("pos", pos, torch.int32, (B,), dev),
-                         tn, B, T, H, Hkv, D, rot, int(interleaved), int(inverse), s)
+    rc = (_CALLS or _compiled()).rotary(qkv, out, H, Hkv, turns, pos, interleaved, inverse, stream)
     if rc:
         _check(rc, "gptk_rotary")
-
-
-def _rows_in(torch, qkv, out, start, count, pos, B, row, dev):
-    """(T, addresses of qkv, out, start, count, pos) of tokens that go into a paged cache."""
-    bf16, i32, shape = torch.bfloat16, torch.int32, qkv.shape
-    T = shape[1] if len(shape) == 3 else 0
-    if shape != (B, T, row):
-        _refuse("qkv", qkv, bf16, (B, T, row), dev)
-    return (T, _addr("qkv", qkv, bf16, dev), None if out is None else _arg("out", out, bf16, shape, dev),
-            None if start is None else _arg("start", start, i32, (B,), dev),
-            None if count is None else _arg("count", count, i32, (B,), dev),
-            None if pos is None else _arg("pos", pos, i32, (B,), dev))
 
 
 def paged_append(qkv, pool, table, H: int, turns=None, start=None, count=None, pos=None, weight=None, out=None,
                  interleaved: bool = False, stream=None):
     """paged_store with the keys turned by their positions pos[b] + t (None: start[b] + t); out (optional, may be qkv)
     takes the turned rows, for the attention. start[b] < 0: no sequence."""
-    lib = _LIB or load()
-    torch, dev, s = _cuda(stream)
-    pages, Hkv, page, D, B, max_pages, p, w, tb = _cache(torch, pool, weight, table, dev)
-    T, q, o, st, ct, ps = _rows_in(torch, qkv, out, start, count, pos, B, (H + 2 * Hkv) * D, dev)
-    tn, rot = _turns(torch, turns, dev)
-    rc = lib.gptk_paged_append(q, o, p, w, tb, st, ct, ps, tn, B, T, H, Hkv, D, rot, int(interleaved), pages, page,
-                               max_pages, s)
+    rc = (_CALLS or _compiled()).paged_append(qkv, pool, table, H, turns, start, count, pos, weight, out, interleaved, stream)
     if rc:
         _check(rc, "gptk_paged_append")
-
-
-def _cache4(torch, codes, ranges, table, dev):
-    """(pages, Hkv, page, D, B, max_pages, addresses of codes, ranges and table) of a paged cache in 4 bits."""
-    shape, tshape = codes.shape, table.shape
-    if len(shape) != 5 or shape[1] != 2:
-        raise ValueError(f"codes: shape {tuple(shape)}, needs [pages, 2, Hkv, page, D / 2]")
-    if len(tshape) != 2:
-        raise ValueError(f"table: shape {tuple(tshape)}, needs [B, max_pages]")
-    pages, _, Hkv, page, half = shape
-    return (pages, Hkv, page, 2 * half, tshape[0], tshape[1], _addr("codes", codes, torch.uint8, dev),
-            _arg("ranges", ranges, torch.bfloat16, (pages, 2, Hkv, page, 2), dev), _addr("table", table, torch.int32, dev))
 
 
 def paged_append4(qkv, codes, ranges, table, H: int, turns=None, start=None, count=None, pos=None, out=None,
                   interleaved: bool = False, stream=None):
     """paged_append into a cache of 4-bit rows: codes uint8 [pages, 2, Hkv, page, D / 2], ranges bf16
     [pages, 2, Hkv, page, 2] (scale, lowest)."""
-    lib = _LIB or load()
-    torch, dev, s = _cuda(stream)
-    pages, Hkv, page, D, B, max_pages, cd, rg, tb = _cache4(torch, codes, ranges, table, dev)
-    T, q, o, st, ct, ps = _rows_in(torch, qkv, out, start, count, pos, B, (H + 2 * Hkv) * D, dev)
-    tn, rot = _turns(torch, turns, dev)
-    rc = lib.gptk_paged_append4(q, o, cd, rg, tb, st, ct, ps, tn, B, T, H, Hkv, D, rot, int(interleaved), pages, page,
-                                max_pages, s)
+    rc = (_CALLS or _compiled()).paged_append4(qkv, codes, ranges, table, H, turns, start, count, pos, out, interleaved, stream)
     if rc:
         _check(rc, "gptk_paged_append4")
 
 
 def paged_load4(codes, ranges, table, rows, start=None, count=None, stream=None):
     """Rows start[b] + t (t < count[b]) of a 4-bit cache as bf16 rows [B, T, 2 Hkv D]: a token's keys, then its values."""
-    lib = _LIB or load()
-    torch, dev, s = _cuda(stream)
-    pages, Hkv, page, D, B, max_pages, cd, rg, tb = _cache4(torch, codes, ranges, table, dev)
-    T = rows.shape[1] if len(rows.shape) == 3 else 0
-    rc = lib.gptk_paged_load4(cd, rg, tb, None if start is None else _arg("start", start, torch.int32, (B,), dev),
-                              None if count is None else _arg("count", count, torch.int32, (B,), dev),
-                              _arg("rows", rows, torch.bfloat16, (B, T, 2 * Hkv * D), dev), B, T, Hkv, D, pages, page,
-                              max_pages, s)
+    rc = (_CALLS or _compiled()).paged_load4(codes, ranges, table, rows, start, count, stream)
     if rc:
         _check(rc, "gptk_paged_load4")
 
@@ -654,34 +613,9 @@ def paged_attention4(qkv, codes, ranges, table, lens, y, H: int, lse2=None, wind
 
     With added 1, lens can be the numbers that the token's paged_append4 started from. lens[b] < 0: row b of the outputs
     stays as it was."""
-    if (window | sinks | added) >> 31 not in (0, -1):
-        _int32(window=window, sinks=sinks, added=added)
-    lib = _LIB or load()
-    torch, dev, s = _cuda(stream)
-    pages, Hkv, page, D, B, max_pages, cd, rg, tb = _cache4(torch, codes, ranges, table, dev)
-    bf16 = torch.bfloat16
-    rc = lib.gptk_paged_attention4(_arg("qkv", qkv, bf16, (B, (H + 2 * Hkv) * D), dev), cd, rg, tb,
-                                   _arg("lens", lens, torch.int32, (B,), dev), _arg("y", y, bf16, (B, H * D), dev),
-                                   None if lse2 is None else _arg("lse2", lse2, torch.float32, (B, H), dev),
-                                   B, H, Hkv, D, pages, page, max_pages, window, sinks, added, s)
+    rc = (_CALLS or _compiled()).paged_attention4(qkv, codes, ranges, table, lens, y, H, lse2, window, sinks, added, stream)
     if rc:
         _check(rc, "gptk_paged_attention4")
-
-
-def _logits(torch, name, t, shape, dtype, dev):
-    """(address, row stride) of logits [M, V] whose rows are contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _refuse(name, t, dtype, shape, dev)
-    ld, one = t.stride()
-    if (one != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
-        raise ValueError(f"{name}: strides {t.stride()}, needs rows of contiguous values")
-    return t.data_ptr(), max(ld, shape[1])
-
-
-def _logit_type(torch, logits):
-    if len(logits.shape) != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"logits: {logits.dtype} of shape {tuple(logits.shape)}, needs float32 or bfloat16 [M, V]")
-    return logits.shape, logits.dtype, int(logits.dtype is torch.bfloat16)
 
 
 def logprobs(logits, targets, logp, entropy=None, stats=None, top_ids=None, top_logp=None, stream=None):
@@ -690,21 +624,7 @@ def logprobs(logits, targets, logp, entropy=None, stats=None, top_ids=None, top_
 
     entropy [M] (optional); stats [M, 2] (optional, needed by the gradient): the largest logit and the sum of exponentials
     against it; top_ids int32 and top_logp [M, K] (optional, K <= 32): the most probable tokens."""
-    lib = _LIB or load()
-    torch, dev, s = _cuda(stream)
-    shape, dtype, code = _logit_type(torch, logits)
-    M, f32 = shape[0], torch.float32
-    z, ld = _logits(torch, "logits", logits, shape, dtype, dev)
-    ids = K = None
-    if top_ids is not None:
-        K = top_ids.shape[1] if len(top_ids.shape) == 2 else 0
-        ids = _arg("top_ids", top_ids, torch.int32, (M, K), dev)
-    rc = lib.gptk_logprobs(z, None if targets is None else _arg("targets", targets, torch.int32, (M,), dev),
-                           None if logp is None else _arg("logp", logp, f32, (M,), dev),
-                           None if entropy is None else _arg("entropy", entropy, f32, (M,), dev),
-                           None if stats is None else _arg("stats", stats, f32, (M, 2), dev), ids,
-                           None if top_logp is None else _arg("top_logp", top_logp, f32, (M, K or 0), dev),
-                           M, shape[1], ld, K or 0, code, s)
+    rc = (_CALLS or _compiled()).logprobs(logits, targets, logp, entropy, stats, top_ids, top_logp, stream)
     if rc:
         _check(rc, "gptk_logprobs")
 
@@ -712,18 +632,7 @@ def logprobs(logits, targets, logp, entropy=None, stats=None, top_ids=None, top_
 def logprobs_bwd(logits, targets, stats, dlogp, dlogits, entropy=None, dentropy=None, stream=None):
     """dlogits [M, V] (may be logits) of logprobs from its logits, targets and stats and the gradient dlogp [M]; with
     dentropy [M] also the entropy's, which then is needed too."""
-    lib = _LIB or load()
-    torch, dev, s = _cuda(stream)
-    shape, dtype, code = _logit_type(torch, logits)
-    M, f32 = shape[0], torch.float32
-    z, ld = _logits(torch, "logits", logits, shape, dtype, dev)
-    dz, dld = _logits(torch, "dlogits", dlogits, shape, dtype, dev)
-    rc = lib.gptk_logprobs_bwd(z, None if targets is None else _arg("targets", targets, torch.int32, (M,), dev),
-                               _arg("stats", stats, f32, (M, 2), dev),
-                               None if entropy is None else _arg("entropy", entropy, f32, (M,), dev),
-                               None if dlogp is None else _arg("dlogp", dlogp, f32, (M,), dev),
-                               None if dentropy is None else _arg("dentropy", dentropy, f32, (M,), dev),
-                               dz, M, shape[1], ld, dld, code, s)
+    rc = (_CALLS or _compiled()).logprobs_bwd(logits, targets, stats, dlogp, dlogits, entropy, dentropy, stream)
     if rc:
         _check(rc, "gptk_logprobs_bwd")
 

@@ -1,8 +1,10 @@
-"""Build the CUDA library libgpt_gb300.so in-tree with nvcc for sm_103a.
+"""Build the CUDA library libgpt_gb300.so in-tree with nvcc for sm_103a, and the
+module _calls.so that calls it with torch's tensors.
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
-one shared library next to this file. Rebuilds only when a source or header is
-newer than the library (or when forced).
+one shared library next to this file; the module (csrc/py_calls.cpp, host code
+only) is compiled beside them. Rebuilds only when a source or header is newer
+than either (or when forced).
 
     python -m decoder_only_transformer_gpt_gb300.build [--force] [--verbose]
 """
@@ -18,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgpt_gb300.so")
+CALLS = os.path.join(HERE, "_calls.so")
 
 SOURCES = ["k_gemm_tc.cu", "k_attn_tc.cu", "k_rowwise.cu", "k_simt.cu", "k_decode.cu", "tmap.cu", "gpt_api.cu",
            "gpt_forward.cu", "gptk.cu", "gptk_noalloc.cu", "k_backward.cu", "k_attn_bwd_tc.cu", "gpt_backward.cu",
@@ -43,10 +46,42 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def compile_calls() -> str:
+    """The object file of the module, against this machine's Python, torch and CUDA headers."""
+    import sysconfig
+    import torch
+    obj = os.path.join(BUILD, "py_calls.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unknown-pragmas",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(_torch_dir(), "include"), "-isystem", cuda,
+           "-c", os.path.join(CSRC, "py_calls.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for py_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def link_calls(obj: str) -> None:
+    """_calls.so, which finds the library next to itself and torch's libraries where `import torch` has loaded them."""
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libgpt_gb300.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _calls.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -64,8 +99,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(compile_calls)
         results = list(ex.map(compile_one, SOURCES))
+        calls_obj = calls.result()
     if verbose or ptxas_verbose:
         for obj, log in results:
             if log.strip():
@@ -76,6 +113,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    link_calls(calls_obj)
     return LIB
 
 

@@ -260,3 +260,28 @@ def test_two_graphs_with_scratch_at_once(gpt_lib):
     torch.cuda.synchronize()
     for c in cases:
         c.check()
+
+
+def test_streams_given_and_refused(gpt_lib):
+    from decoder_only_transformer_gpt_gb300 import binding
+    z, lp = torch.randn(4, 5000, device="cuda"), torch.zeros(4, device="cuda")
+    t = torch.arange(4, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    binding.logprobs(z, t, lp, stream=side)
+    side.synchronize()
+    assert torch.allclose(lp, torch.log_softmax(z, -1)[t.long(), t.long()], atol=1e-5)
+
+    class Other:
+        device_index, cuda_stream = torch.cuda.current_device() + 1, 0
+    with pytest.raises(ValueError, match="stream"):
+        binding.logprobs(z, t, lp, stream=Other())
+    with pytest.raises(AttributeError):
+        binding.logprobs(z, t, lp, stream=object())
+    for bad in (z.cpu(), None, "z"):
+        with pytest.raises((ValueError, TypeError)):
+            binding.logprobs(bad, t, lp)
+    with pytest.raises(ValueError, match="targets"):
+        binding.logprobs(z, t.cpu(), lp)
+    with pytest.raises(ValueError, match="logp"):
+        binding.logprobs(z, t, lp[:3])

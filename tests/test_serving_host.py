@@ -156,6 +156,13 @@ def test_binding_refuses_what_the_kernels_cannot_take(lib):
             (lambda: binding.logprobs_bwd(torch.zeros(2, 5), None, torch.zeros(2, 2), None, torch.zeros(2, 5)), "device")):
         with pytest.raises(ValueError, match=word):
             call()
+    for call in (lambda: binding.rotary(None, qkv, 4, 2, turns), lambda: binding.rotary(qkv, qkv, "4", 2, turns),
+                 lambda: binding.paged_load4(codes, ranges, table, 5), lambda: binding.logprobs(None, None, None)):
+        with pytest.raises(TypeError):
+            call()
+    for H in (2 ** 31, 10 ** 30, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="needs an int32"):
+            binding.paged_append(qkv, pool, table, H)
     with pytest.raises(ValueError):
         binding.rotary_turns([[1.0]], device="cpu")
     for bad in (math.nan, math.inf, -2e12):
