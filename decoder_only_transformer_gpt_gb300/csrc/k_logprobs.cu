@@ -160,29 +160,33 @@ struct Row {
   }
 };
 
-// One block per row, or a cluster of NC blocks: the row's chunks go round the warps of all of them.
-template <typename T, int NC>
+// A warp takes a row (WR = 1; eight rows a block), or a block's eight warps do (WR = 8), or those of a cluster of NC blocks: the
+// row's chunks go round the warps. FEW: no warp has more than two, which then stay in its registers and are not read again.
+template <typename T, int NC, int WR, bool FEW>
 __global__ void __launch_bounds__(kLpWarps * 32)
 logprobs_kernel(LpArgs a, int* err) {
   using W = Vec<T>;
   constexpr int N = W::N, VALUES = kLpVecs * N;      // values a lane and chunk
   namespace cg = cooperative_groups;
   __shared__ __align__(16) uint4 s_stage[kLpWarps][32][kLpVecs + 1];
-  __shared__ float s_max[kLpGroups][kLpWarps * 32];  // the threads' largest logits, by group of chunks
+  __shared__ float s_max[FEW ? 1 : kLpGroups][kLpWarps * 32];   // the threads' largest logits, by group of chunks
   __shared__ float s_order[kLpWarps][32];            // and over all groups, in order
-  __shared__ Key s_list[8][32];                      // the warps' lists, then the blocks'
-  __shared__ Sums s_sums[8];
+  __shared__ Key s_list[kLpWarps][32], s_lists[NC][32];   // the warps' lists, and the blocks'
+  __shared__ Sums s_sums[8], s_parts[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC);
-  const long long m = blockIdx.x / NC;
+  const long long m = WR == 1 ? static_cast<long long>(blockIdx.x) * kLpWarps + warp : blockIdx.x / NC;
+  if constexpr (NC > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // every block has started
   pdl_wait();
   pdl_trigger();
+  if (WR == 1 && m >= a.M) return;
+  const bool lead = WR == 1 || (part == 0 && warp == 0);
   const Row<T> row(a.z, a.ld, a.V, m);
   const uint4* vecs = reinterpret_cast<const uint4*>(row.z + row.head);
   const int K = a.K;
   int target = -1;
   float zt = 0.0f;
-  if (part == 0 && threadIdx.x == 0 && a.targets) {
+  if (lead && lane == 0 && a.targets) {
     target = __ldg(a.targets + m);
     if (static_cast<unsigned>(target) < static_cast<unsigned>(a.V)) {
       zt = W::get(row.z + target);
@@ -209,7 +213,8 @@ logprobs_kernel(LpArgs a, int* err) {
       }
     sum = {mn, s.x + s.y, e2.x + e2.y};
   };
-  const int full = row.nvec / kLpChunk, step = NC * kLpWarps, first = part * kLpWarps + warp;   // chunks without a gap
+  const int full = row.nvec / kLpChunk;              // chunks without a gap
+  const int step = WR == 1 ? 1 : NC * kLpWarps, first = WR == 1 ? 0 : part * kLpWarps + warp;
   const int chunks = (row.nvec + kLpChunk - 1) / kLpChunk;
   const int per = ((chunks + step - 1) / step + kLpGroups - 1) / kLpGroups;   // chunks of a group
   float top = -INFINITY, noted = -INFINITY;          // this thread's largest logit, and of the group
@@ -243,22 +248,31 @@ logprobs_kernel(LpArgs a, int* err) {
     }
   };
   uint4 v[kLpVecs], next[kLpVecs];
-  if (first < full) load(v);
-  for (int c = first; c < full; c += 2 * step) {     // the next chunk on its way while one is used
-    const bool two = c + step < full;
-    if (two) load(next);
-    use(v);
-    if (!two) break;
-    if (c + 2 * step < full) load(v);
-    use(next);
-  }
-  if (full % step == first && row.nvec > full * kLpChunk) {   // the vectors behind the last whole chunk
-    load_last(full, v);
-    use(v);
+  float cm0 = -INFINITY, cm1 = -INFINITY;            // FEW: the lane's largest of each chunk
+  if constexpr (FEW) {
+    if (first < chunks) load_last(first, v);
+    if (first + step < chunks) load_last(first + step, next);
+    if (first < chunks) add(cm0 = W::largest(v), v);
+    if (first + step < chunks) add(cm1 = W::largest(next), next);
+    top = fmaxf(cm0, cm1);
+  } else {
+    if (first < full) load(v);
+    for (int c = first; c < full; c += 2 * step) {   // the next chunk on its way while one is used
+      const bool two = c + step < full;
+      if (two) load(next);
+      use(v);
+      if (!two) break;
+      if (c + 2 * step < full) load(v);
+      use(next);
+    }
+    if (full % step == first && row.nvec > full * kLpChunk) {   // the vectors behind the last whole chunk
+      load_last(full, v);
+      use(v);
+    }
   }
   float ze = -INFINITY;                              // the values before and behind the vectors
   int edge = -1;
-  if (part == 0 && warp == 0) {
+  if (lead) {
     const int tail = row.head + row.nvec * N;
     edge = lane < 16 ? (lane < row.head ? lane : -1) : (tail + lane - 16 < a.V ? tail + lane - 16 : -1);
     if (edge >= 0) ze = W::get(row.z + edge);
@@ -268,24 +282,28 @@ logprobs_kernel(LpArgs a, int* err) {
   if (K) {
     // Blocks take the same time for their rows and so come to this part together, in which nothing is read: the first
     // chunks of a row that comes next are fetched into L2 meanwhile.
-    if (NC == 1 && lane < 4 && m + a.ahead < a.M) {
+    if (NC == 1 && !FEW && lane < 4 && m + a.ahead < a.M) {
       const Row<T> later(a.z, a.ld, a.V, m + a.ahead);
       const int c = first + lane * step;
       if (c < later.nvec / kLpChunk) prefetch_l2(reinterpret_cast<const uint4*>(later.z + later.head) + static_cast<long long>(c) * kLpChunk, kLpChunk * 16);
     }
-    if (in_group) {
+    if (!FEW && in_group) {
       s_max[group++][threadIdx.x] = noted;
       top = fmaxf(top, noted);
     }
-    float order = sorted_values(top, lane);
-    s_order[warp][lane] = order;
-    __syncthreads();
-#pragma unroll
-    for (int half = kLpWarps / 2; half; half >>= 1) {
-      if (warp < half) s_order[warp][lane] = order = join_values(order, s_order[warp + half][lane], lane);
+    float order = sorted_values(top, lane), reached;   // reached: by K threads' largest logits
+    if constexpr (WR == 1) {
+      reached = __shfl_sync(kAll, order, K - 1);
+    } else {
+      s_order[warp][lane] = order;
       __syncthreads();
+#pragma unroll
+      for (int half = kLpWarps / 2; half; half >>= 1) {
+        if (warp < half) s_order[warp][lane] = order = join_values(order, s_order[warp + half][lane], lane);
+        __syncthreads();
+      }
+      reached = s_order[0][K - 1];
     }
-    const float reached = s_order[0][K - 1];         // by K threads' largest logits
     Key floor_key = (key_of(reached, 0) >> 32) << 32;   // what a token has to pass
     // Puts the lanes' keys that pass into the list, one by one.
     auto insert = [&](Key key) {
@@ -301,39 +319,48 @@ logprobs_kernel(LpArgs a, int* err) {
         who &= __ballot_sync(kAll, key > floor_key);
       }
     };
-    // What is read again: a chunk of one thread a lane, as many as there are at once, so that they travel together.
-    int items = 0, item_chunk = 0, item_lane = 0;
-    auto look = [&]() {
-      const int at0 = row.head + (item_chunk * kLpChunk + item_lane) * N;
-#pragma unroll
-      for (int k = 0; k < kLpVecs; ++k) {
-        const int i = item_chunk * kLpChunk + k * 32 + item_lane;
-        v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-        if (lane < items && i < row.nvec) v[k] = __ldg(vecs + i);
-        s_stage[warp][lane][k] = v[k];
-      }
-      const float cm = lane < items ? W::largest(v) : -INFINITY;
-      const Key best_here = lane < items ? key_of(cm, at0) : 0;
-      if (items > K) {
-        // K of them have a value at least as large as the K-th of their largest ones: nothing below it is wanted
-        const Key k = (key_of(__shfl_sync(kAll, sorted_values(cm, lane), K - 1), 0) >> 32) << 32;
-        if (k > floor_key) floor_key = k;
-      }
+    // Chunks of one thread each, a lane's own in x (its chunk's number, of that thread; cm: the largest value; none where `some`
+    // is false): the tokens that pass.
+    auto search = [&](const uint4 (&x)[kLpVecs], bool some, float cm, int chunk, int thread) {
+      const Key best_here = some ? key_of(cm, row.head + (chunk * kLpChunk + thread) * N) : 0;
       unsigned who = __ballot_sync(kAll, best_here > floor_key);
+      if (__popc(who) > K) {
+        // K of them have a value at least as large as the K-th of their largest ones: nothing below it is wanted
+        const Key k = (key_of(__shfl_sync(kAll, sorted_values(some ? cm : -INFINITY, lane), K - 1), 0) >> 32) << 32;
+        if (k > floor_key) floor_key = k;
+        who &= __ballot_sync(kAll, best_here > floor_key);
+      }
+      if (!who) return;
+#pragma unroll
+      for (int k = 0; k < kLpVecs; ++k) s_stage[warp][lane][k] = x[k];
       __syncwarp();
       while (who) {
         const int from = __ffs(who) - 1;
         who &= who - 1;
         const int j = lane % VALUES;                 // this lane's value of that chunk's
-        const float x = W::get(reinterpret_cast<const T*>(&s_stage[warp][from][0]) + j);
-        const int vec = __shfl_sync(kAll, item_chunk, from) * kLpChunk + (j / N) * 32 + __shfl_sync(kAll, item_lane, from);
-        insert(lane < VALUES && vec < row.nvec ? key_of(x, row.head + vec * N + j % N) : 0);
+        const float z = W::get(reinterpret_cast<const T*>(&s_stage[warp][from][0]) + j);
+        const int vec = __shfl_sync(kAll, chunk, from) * kLpChunk + (j / N) * 32 + __shfl_sync(kAll, thread, from);
+        insert(lane < VALUES && vec < row.nvec ? key_of(z, row.head + vec * N + j % N) : 0);
         who &= __ballot_sync(kAll, best_here > floor_key);
       }
       __syncwarp();                                  // the stage is read before it is filled again
-      items = 0;
     };
-    if (__any_sync(kAll, top >= reached)) {
+    if constexpr (FEW) {
+      if (__any_sync(kAll, cm0 >= reached)) search(v, first < chunks, cm0, first, lane);
+      if (__any_sync(kAll, cm1 >= reached)) search(next, first + step < chunks, cm1, first + step, lane);
+    } else if (__any_sync(kAll, top >= reached)) {
+      // what is read again: one thread's chunk a lane, as many as there are at once, so that they travel together
+      int items = 0, item_chunk = 0, item_lane = 0;
+      auto look = [&]() {
+#pragma unroll
+        for (int k = 0; k < kLpVecs; ++k) {
+          const int i = item_chunk * kLpChunk + k * 32 + item_lane;
+          v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+          if (lane < items && i < row.nvec) v[k] = __ldg(vecs + i);
+        }
+        search(v, lane < items, W::largest(v), item_chunk, item_lane);
+        items = 0;
+      };
       for (int g = 0; g < group; ++g) {
         const float most = s_max[g][threadIdx.x];
         if (!__any_sync(kAll, most >= reached)) continue;
@@ -352,45 +379,48 @@ logprobs_kernel(LpArgs a, int* err) {
       }
       if (items) look();
     }
-    if (part == 0 && warp == 0) insert(edge >= 0 ? key_of(ze, edge) : 0);
+    if (lead) insert(edge >= 0 ? key_of(ze, edge) : 0);
   }
   auto shuffled = [&](const Sums& x, int k) {
     return joined_sums(x, {__shfl_xor_sync(kAll, x.m, k), __shfl_xor_sync(kAll, x.s, k), __shfl_xor_sync(kAll, x.a, k)});
   };
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) sum = shuffled(sum, k);
-  if (lane == 0) s_sums[warp] = sum;
-  if (K) s_list[warp][lane] = best;
-  __syncthreads();
-  auto join8 = [&](int n) {                          // the n <= 8 lists and sums in shared memory, to warp 0
-    if (K) {
+  if constexpr (WR > 1) {
+    // n <= 8 lists and sums in shared memory, to warp 0
+    auto join8 = [&](Key (*list)[32], const Sums* sums, int n) {
+      if (K) {
 #pragma unroll
-      for (int half = 4; half; half >>= 1) {
-        if (n > half) {
-          if (warp < half && warp + half < n) s_list[warp][lane] = join_lists(s_list[warp][lane], s_list[warp + half][lane], lane);
-          __syncthreads();
+        for (int half = 4; half; half >>= 1) {
+          if (n > half) {
+            if (warp < half && warp + half < n) list[warp][lane] = join_lists(list[warp][lane], list[warp + half][lane], lane);
+            __syncthreads();
+          }
         }
+        best = list[0][lane];
       }
-      best = s_list[0][lane];
+      if (warp) return;
+      sum = (lane & 7) < n ? sums[lane & 7] : Sums{kLowest, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 1; k < 8; k <<= 1) sum = shuffled(sum, k);
+    };
+    if (lane == 0) s_sums[warp] = sum;
+    if (K) s_list[warp][lane] = best;
+    __syncthreads();
+    join8(s_list, s_sums, kLpWarps);
+    if constexpr (NC > 1) {
+      auto cluster = cg::this_cluster();
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (warp == 0) {
+        if (K) *cluster.map_shared_rank(&s_lists[part][lane], 0) = best;
+        if (lane == 0) *cluster.map_shared_rank(&s_parts[part], 0) = sum;
+      }
+      cluster.sync();
+      if (part) return;
+      join8(s_lists, s_parts, NC);
     }
     if (warp) return;
-    sum = (lane & 7) < n ? s_sums[lane & 7] : Sums{kLowest, 0.0f, 0.0f};
-#pragma unroll
-    for (int k = 1; k < 8; k <<= 1) sum = shuffled(sum, k);
-  };
-  join8(kLpWarps);
-  if constexpr (NC > 1) {
-    auto cluster = cg::this_cluster();
-    cluster.sync();                                  // every block has read its own lists, before rank 0's are replaced
-    if (warp == 0) {
-      if (K) *cluster.map_shared_rank(&s_list[part][lane], 0) = best;
-      if (lane == 0) *cluster.map_shared_rank(&s_sums[part], 0) = sum;
-    }
-    cluster.sync();
-    if (part) return;
-    join8(NC);
   }
-  if (warp) return;
   const bool fine = sum.s > 0.0f && sum.s < INFINITY;   // a finite log-sum-exp
   const float ln_s = logf(sum.s), nan = __int_as_float(0x7fffffff);
   if (lane == 0) {
@@ -480,10 +510,10 @@ logprobs_grad_kernel(LpGrad a) {
   }
 }
 
-template <typename T, int NC>
-cudaError_t launch_nc(const LpArgs& a, int M, int* err, cudaStream_t s) {
+template <typename T, int NC, int WR, bool FEW>
+cudaError_t launch_rows(const LpArgs& a, int* err, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(M) * NC);
+  cfg.gridDim = dim3(static_cast<unsigned>(WR == 1 ? (a.M + kLpWarps - 1) / kLpWarps : a.M * NC));
   cfg.blockDim = dim3(32 * kLpWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -493,19 +523,29 @@ cudaError_t launch_nc(const LpArgs& a, int M, int* err, cudaStream_t s) {
   attr[1].val.clusterDim = {NC, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = NC > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NC>, a, err);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NC, WR, FEW>, a, err);
+}
+
+template <typename T, int NC, int WR = kLpWarps>
+cudaError_t launch_form(const LpArgs& a, long long chunks, int* err, cudaStream_t s) {
+  return chunks <= 2 * NC * WR ? launch_rows<T, NC, WR, true>(a, err, s) : launch_rows<T, NC, WR, false>(a, err, s);
 }
 
 template <typename T>
-cudaError_t launch_logprobs_of(LpArgs a, int M, int* err, cudaStream_t s) {
+cudaError_t launch_logprobs_of(LpArgs a, int* err, cudaStream_t s) {
   int dev = 0, sms = 0;
   const cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   const long long chunks = (static_cast<long long>(a.V) / Vec<T>::N + kLpChunk - 1) / kLpChunk;
-  if (8LL * M <= 2 * sms && chunks > 4 * kLpWarps) return launch_nc<T, 8>(a, M, err, s);
-  if (2LL * M <= 2 * sms && chunks > kLpWarps) return launch_nc<T, 2>(a, M, err, s);
   a.ahead = 4 * sms;                                 // (four blocks an SM)
-  return launch_nc<T, 1>(a, M, err, s);
+  if (chunks <= 2 || (chunks <= 16 && a.M >= 4LL * sms)) {
+    a.ahead *= kLpWarps;
+    return launch_form<T, 1, 1>(a, chunks, err, s);
+  }
+  if (8 * a.M <= 2 * sms && chunks > 4 * kLpWarps) return launch_form<T, 8>(a, chunks, err, s);
+  if (4 * a.M <= 2 * sms && chunks > 2 * kLpWarps) return launch_form<T, 4>(a, chunks, err, s);
+  if (2 * a.M <= 2 * sms && chunks > kLpWarps) return launch_form<T, 2>(a, chunks, err, s);
+  return launch_form<T, 1>(a, chunks, err, s);
 }
 
 template <typename T>
@@ -533,7 +573,7 @@ cudaError_t launch_logprobs(const LogprobRows& x, float* logp, float* entropy, f
   a.M = x.M;
   a.V = x.V;
   a.K = K;
-  return x.bf16 ? launch_logprobs_of<__nv_bfloat16>(a, x.M, err, s) : launch_logprobs_of<float>(a, x.M, err, s);
+  return x.bf16 ? launch_logprobs_of<__nv_bfloat16>(a, err, s) : launch_logprobs_of<float>(a, err, s);
 }
 
 cudaError_t launch_logprobs_bwd(const LogprobRows& x, const float* stats, const float* entropy, const float* dlogp,

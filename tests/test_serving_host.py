@@ -157,7 +157,7 @@ def test_binding_refuses_what_the_kernels_cannot_take(lib):
         with pytest.raises(ValueError, match=word):
             call()
     for call in (lambda: binding.rotary(None, qkv, 4, 2, turns), lambda: binding.rotary(qkv, qkv, "4", 2, turns),
-                 lambda: binding.paged_load4(codes, ranges, table, 5), lambda: binding.logprobs(None, None, None)):
+                 lambda: binding.rotary(qkv, qkv, 4.5, 2, turns), lambda: binding.logprobs(None, None, None)):
         with pytest.raises(TypeError):
             call()
     for H in (2 ** 31, 10 ** 30, -2 ** 31 - 1):
