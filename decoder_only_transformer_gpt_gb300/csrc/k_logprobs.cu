@@ -538,7 +538,10 @@ cudaError_t launch_logprobs_of(LpArgs a, int* err, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long chunks = (static_cast<long long>(a.V) / Vec<T>::N + kLpChunk - 1) / kLpChunk;
   a.ahead = 4 * sms;                                 // (four blocks an SM)
-  if (chunks <= 2 || (chunks <= 16 && a.M >= 4LL * sms)) {
+  // A warp a row where its whole row is two chunks, or the rows are short and many: 4,096 x 500 with K = 5 6.1 us, a block a row
+  // 35; 2,500 x 5,000 16.6 and 21.5; but 1,500 x 8,000 17.1 and 14.8, 620 x 5,000 9.0 and 7.9 (graph replays). Clusters of as
+  // many blocks as keep all of them at work at once.
+  if (chunks <= 2 || (chunks <= 10 && a.M >= 8LL * sms)) {
     a.ahead *= kLpWarps;
     return launch_form<T, 1, 1>(a, chunks, err, s);
   }
