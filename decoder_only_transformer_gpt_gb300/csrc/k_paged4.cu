@@ -182,7 +182,8 @@ __device__ __forceinline__ int row_in_eight(int n) { return (n & 1) * 4 + (n >> 
 
 // Eight heads' queries as second operands, times 2^(14 - e) for 2^e <= the head's largest value < 2^(e + 1). from: what the
 // score products start with, 8 times the sums of heads 2 q and 2 q + 1; sum: these sums; c: the factors from a product to the
-// softmax's base-2 exponent. load(row, i): values 8 i of one of the gn heads; zeros behind them.
+// softmax's base-2 exponent. load(row, i): values 8 i .. of one of the gn heads (none where
+// gn <= 0); zeros behind them.
 template <int D>
 struct Queries {
   uint32_t f[D / 16][2];
@@ -193,8 +194,8 @@ struct Queries {
     float v[C], top = 0.0f, mine = 0.0f;
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {
-      uint4 x = load(min(lane >> 2, max(gn - 1, 0)), (lane & 3) * (C / 8) + w);
-      if ((lane >> 2) >= gn) x = make_uint4(0u, 0u, 0u, 0u);
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if ((lane >> 2) < gn) x = load(lane >> 2, (lane & 3) * (C / 8) + w);   // (no head behind the last one is read)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 p = unpack_bf16x2((&x.x)[k]);
