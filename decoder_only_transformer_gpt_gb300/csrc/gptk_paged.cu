@@ -1,6 +1,7 @@
 // Entry points of the paged key/value caches and the position rotation (include/gpt_kernels.h): argument checks, then the
-// kernels of k_paged.cu, k_append.cu and k_paged4.cu. Everything that the host can check is refused before any device call; page numbers and lengths
-// live on the device and are checked there (an access they would lead out of bounds is skipped and recorded).
+// kernels of k_paged.cu, k_append.cu and k_paged4.cu. Everything that the host can check is refused before any device call;
+// page numbers and lengths live on the device and are checked there (an access they would lead out of bounds is skipped and
+// recorded).
 #include "../../include/gpt_kernels.h"
 #include "model.h"
 
@@ -37,7 +38,7 @@ int paged_cache(PagedCache* c, const void* pool, const float* weight, const int3
 // Fused rows and their rotation. GPT_OK fills *x.
 int rotary_rows(RotaryRows* x, const void* qkv, void* out, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T,
                 int32_t H, int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t inverse) {
-  if (!qkv || B < 1 || T < 0 || H < 1 || Hkv < 1 || D < 1 || rot < 0) return GPT_EINVAL;
+  if ((!qkv && T) || B < 1 || T < 0 || H < 1 || Hkv < 1 || D < 1 || rot < 0) return GPT_EINVAL;   // (no rows: no address)
   if (static_cast<int64_t>(B) * T > 0x7fffffffLL) return GPT_EINVAL;
   if ((static_cast<int64_t>(H) + 2LL * Hkv) * D > 0x3fffffffLL) return GPT_EINVAL;   // a row's elements: 32 bits
   if ((rot > 0) != (turns != nullptr) || (interleaved & ~1) || (inverse & ~1)) return GPT_EINVAL;
@@ -127,7 +128,7 @@ int gptk_rotary_turns(const double* freq, uint64_t* turns, int32_t n) {
 
 int gptk_rotary(const void* qkv, void* out, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
                 int32_t Hkv, int32_t D, int32_t rot, int32_t interleaved, int32_t inverse, void* stream) {
-  if (!out || !turns) return GPT_EINVAL;
+  if ((!out && T) || !turns) return GPT_EINVAL;
   RotaryRows x;
   const int rc = rotary_rows(&x, qkv, out, pos, turns, B, T, H, Hkv, D, rot, interleaved, inverse);
   if (rc != GPT_OK) return rc;
@@ -173,7 +174,7 @@ int gptk_paged_append4(const void* qkv, void* out, void* codes, void* ranges, co
 int gptk_paged_load4(const void* codes, const void* ranges, const int32_t* table, const int32_t* start,
                      const int32_t* count, void* rows, int32_t B, int32_t T, int32_t Hkv, int32_t D, int32_t pages,
                      int32_t page, int32_t max_pages, void* stream) {
-  if (!ranges || !rows || T < 0 || static_cast<int64_t>(B) * T > 0x7fffffffLL) return GPT_EINVAL;
+  if (!ranges || (!rows && T) || T < 0 || static_cast<int64_t>(B) * T > 0x7fffffffLL) return GPT_EINVAL;
   PagedCache c;
   const int rc = paged_cache(&c, codes, nullptr, table, B, Hkv, D, pages, page, max_pages);
   if (rc != GPT_OK) return rc;

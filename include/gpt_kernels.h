@@ -234,7 +234,8 @@ int gptk_paged_evict(void* pool, float* weight, const int32_t* table, const int3
  *
  * gptk_rotary: qkv [B, T, (H + 2 Hkv) D] -> out, row t of sequence b at position pos[b] + t (pos int32 [B] or NULL: 0).
  * out is qkv itself (in place; the values are then not written) or does not overlap it. inverse 1 turns back: the
- * derivative of the rotation, from the gradient of its output to that of its input. B T < 2^31, 16-byte aligned rows.
+ * derivative of the rotation, from the gradient of its output to that of its input. B T < 2^31, 16-byte aligned rows. T 0:
+ * nothing to do, and qkv and out may be NULL (here and in the calls below).
  */
 int gptk_rotary_turns(const double* freq, uint64_t* turns, int32_t n);
 int gptk_rotary(const void* qkv, void* out, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,
@@ -310,8 +311,8 @@ int gptk_paged_attention4(const void* qkv, const void* codes, const void* ranges
  * gptk_logprobs_bwd: from logits, targets, stats and entropy of the call above and the gradients dlogp and dentropy (fp32
  * [M]; dentropy NULL with entropy NULL: none; dlogp NULL with targets NULL: none), the gradient of the logits
  *   dlogits[m, j] = dlogp (1[j = target] - p_j) - dentropy p_j (ln p_j + entropy)
- * in the logits' type, row stride dld >= V; it is logits itself (with the same stride) or does not overlap them. A row whose target is -1 (or
- * outside [0, V)) takes no part with its dlogp. Rows without a finite log-sum-exp give NaN.
+ * in the logits' type, row stride dld >= V; it is logits itself (with the same stride) or does not overlap them. A row
+ * whose target is -1 (or outside [0, V)) takes no part with its dlogp. Rows without a finite log-sum-exp give NaN.
  */
 int gptk_logprobs(const void* logits, const int32_t* targets, float* logp, float* entropy, float* stats, int32_t* top_ids,
                   float* top_logp, int32_t M, int32_t V, int64_t ld, int32_t K, int32_t dtype, void* stream);

@@ -285,3 +285,19 @@ def test_streams_given_and_refused(gpt_lib):
         binding.logprobs(z, t.cpu(), lp)
     with pytest.raises(ValueError, match="logp"):
         binding.logprobs(z, t, lp[:3])
+
+
+def test_calls_without_rows(gpt_lib):
+    # an empty chunk of a prompt: tensors without an address
+    from decoder_only_transformer_gpt_gb300 import binding
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    turns = binding.rotary_turns([10000.0 ** (-2.0 * i / 64) for i in range(32)])
+    none, out = torch.empty(2, 0, 6 * 64, **bf16), torch.empty(2, 0, 6 * 64, **bf16)
+    pool, table = torch.full((4, 2, 1, 16, 64), 3.0, **bf16), torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    codes, ranges = torch.full((4, 2, 1, 16, 32), 5, dtype=torch.uint8, device="cuda"), torch.full((4, 2, 1, 16, 2), 2.0, **bf16)
+    binding.rotary(none, out, 4, 1, turns)
+    binding.paged_append(none, pool, table, 4, turns=turns, out=out)
+    binding.paged_append4(none, codes, ranges, table, 4, turns=turns, out=out)
+    binding.paged_load4(codes, ranges, table, torch.empty(2, 0, 2 * 64, **bf16))
+    binding.status()
+    assert (pool == 3).all() and (codes == 5).all() and (ranges == 2).all()

@@ -95,6 +95,14 @@ def test_row_arguments(lib, call):
     assert call(lib, T=0) == binding.GPT_OK                                # nothing to do
 
 
+def test_no_rows_need_no_address(lib):
+    from decoder_only_transformer_gpt_gb300 import binding
+    for call in (_rotary, _append, _append4):
+        assert call(lib, T=0, qkv=None, out=None) == binding.GPT_OK
+    assert _load4(lib, T=0, rows=None) == binding.GPT_OK
+    assert _rotary(lib, T=0, qkv=None, out=None, turns=None) == binding.GPT_EINVAL
+
+
 def test_rotary_arguments(lib):
     from decoder_only_transformer_gpt_gb300 import binding
     for bad in (dict(out=None), dict(turns=None, rot=0), dict(inverse=2)):
