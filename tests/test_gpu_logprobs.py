@@ -146,6 +146,37 @@ def test_rows_of_a_large_vocabulary(gpt_lib, dtype, M):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,K", [(2049, 1), (3001, 5), (5003, 0), (5003, 32), (5120, 32)])
+@pytest.mark.parametrize("M", [1300, 2437])
+def test_many_short_rows(gpt_lib, dtype, V, K, M):
+    # rows of different shifts of nine, and single ones among them without a distribution or with one token left
+    from decoder_only_transformer_gpt_gb300 import binding
+    z = logits(9, V, V + K)[np.arange(M) % 9]
+    for i in range(9):
+        z[i::9] = np.roll(z[i::9], 13 * i, 1)
+    bad, alone = [11, 640, M - 2], [12, 641, M - 1]
+    z[bad[0], V // 2], z[bad[1], V - 1] = np.nan, np.inf
+    z[bad[2]] = -np.inf
+    for i in alone:
+        z[i] = -np.inf
+        z[i, (7 * i) % V] = -3.0
+    t = some_targets(M, V, M)
+    d, zd, _ = run(z, t, K, dtype, ld=V + 3, offset=1)
+    binding.status()
+    keep = sorted({0, 1, 7, 8, M // 2, M - 9} | set(bad) | set(alone) | {b - 1 for b in bad} | {a + 1 for a in alone[:2]})
+    check({k: None if v is None else v[keep] for k, v in d.items()}, zd[keep], [t[i] for i in keep], K)
+    want = np.array([torch.isfinite(d["entropy"][i]).item() for i in range(M)])
+    assert (want == ~np.isin(np.arange(M), bad)).all()
+    _, ent, _, _, p, lp = ref.logprobs(zd[:9], [0] * 9, 0)
+    _, ed, u, ua, ln_s = bounds(zd[:9], p, lp)       # (all rows of a shift have its entropy, to twice the bounds)
+    lim = 2.0 * (u * (1 + ed) + ua + 2.0 ** -22 * (1 + ln_s + ed))
+    got = host(d["entropy"])
+    for i in range(M):
+        if i not in bad and i not in alone:
+            assert abs(got[i] - ent[i % 9]) <= lim[i % 9]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("V", [65536, 65541, 131075, 300007])
 def test_vocabularies_of_several_chunks_a_note(gpt_lib, dtype, V):
     # a thread notes the largest logit of several chunks; the best tokens next to each other, or all equal
