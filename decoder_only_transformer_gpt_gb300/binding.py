@@ -1,8 +1,10 @@
-"""Thin ctypes binding of the C ABI (include/gpt.h, include/gpt_kernels.h).
+"""Thin binding of the C ABI (include/gpt.h, include/gpt_kernels.h).
 
 Argument marshalling only: every step of the forward pass runs in the CUDA
-library. PyTorch supplies device memory and streams. If the library has not
-been built, or a call fails, this module raises; there is no fallback.
+library. PyTorch supplies device memory and streams. Calls go through ctypes,
+those of the serving and scoring operators through a compiled module
+(csrc/py_calls.cpp). If the library or the module has not been built, or a call
+fails, this module raises; there is no fallback.
 """
 import ctypes
 import os

@@ -13,8 +13,10 @@
 // All three kernels are bound by memory and give a warp one token (or part of one): a lane holds 16 values of a head, two
 // 16-byte units that contain each other's pair partners, D / 16 lanes a head. Neighbouring lanes hold neighbouring units, so
 // that each load and store covers whole 32-byte sectors (with units 2 i and 2 i + 1 in lane i the L2 moved 1.6 times the bytes:
-// 16 x up to 1,024 tokens into 4 bits and back 41 us). A lane computes the sine and cosine of one pair for the whole warp,
-// once per token.
+// 16 x up to 1,024 tokens into 4 bits and back 41 us, now 35.8). A lane computes the sine and cosine of one pair for the whole
+// warp, once per token. Eight blocks an SM, with the loads of two steps of heads in flight: 16 x up to 1,024 tokens of 12 heads
+// into bf16 pages and rows 27.5 us (155 MB, 5.6 TB/s, 0.84 of a copy's rate); with 6 or 5 blocks 29.0 and 30.5, with 10, whose
+// registers spill, 32.8, with one step in flight 29.7. Into 4 bits the instructions count as much (63 % of the issue slots).
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"

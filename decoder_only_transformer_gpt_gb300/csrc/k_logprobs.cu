@@ -10,7 +10,11 @@
 // again (out of L2). A warp keeps the best 32 tokens that it finds there in order, one a lane, as 64-bit keys (logit, then
 // lowest index); lists are joined two by two: the larger of each pair of opposite ends is a bitonic sequence of the best
 // 32, sorted in five steps. (Lists kept up to date while the row went by took 8 to 16 instructions for every 32 logits, as
-// many as the sums: 4,096 rows of 50,257 with K = 8 took 151 us in fp32 and 124 in bf16, and 128 and 77 with K = 0.)
+// many as the sums: 4,096 rows of 50,257 with K = 8 took 151 us in fp32 and 124 in bf16.)
+//
+// Bound by memory where rows are many: 4,096 x 50,257 in fp32 123 us with K = 0, 6.7 TB/s, what a copy reaches, and 135 with
+// K = 8; in bf16 70 and 85, 5.9 TB/s, the exponentials' units and the sums' instructions close behind. The part after the
+// sums reads little and lets the memory rest: that is what K adds.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"

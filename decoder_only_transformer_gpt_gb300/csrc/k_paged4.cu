@@ -29,7 +29,8 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // Bound by issuing instructions, about 350 for 32 rows of a key head: a byte of codes takes a warp four times the unpacking
 // and products of a byte of bf16, and the integer unit takes a warp's instruction only every other cycle. Measured: 16
-// sequences of 9,000 to 32,000 rows x 12 heads 60.5 us, 4.7 TB/s. Work is dealt as in the 16-bit cache's kernel (k_paged.cu):
+// sequences of 9,000 to 32,000 rows x 12 heads 60.0 us, 4.7 TB/s, where the rows of a 16-bit cache take 160; with 8 query heads
+// on each of 4 key heads 34.5, with 12 50. Work is dealt as in the 16-bit cache's kernel (k_paged.cu):
 // units of 64 rows (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal
 // contiguous ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
