@@ -107,13 +107,12 @@ __device__ __forceinline__ float4 lds128f(uint32_t a) {
 __device__ __forceinline__ void sts128f(uint32_t a, float x, float y, float z, float w) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
-// fp16 products: d = a b + c, and c += a b
-__device__ __forceinline__ void mma16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                           const float (&c)[4]) {
+// fp16 products: d = a b, and c += a b
+__device__ __forceinline__ void mma16_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%10, %11, %12, %13};"
+               "{%10, %10, %10, %10};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -136,32 +135,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
-// The eight codes of a word, less 8, as fp16 pairs (code p, code p + 4). exps: the two exponents, in registers that the
-// compiler takes for variables (it would make two logical operations of one with two constants).
-struct Exponents {
-  uint32_t e1024, e64;
-  __device__ __forceinline__ Exponents() {
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(e1024));
-    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(e64));
-  }
-};
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t masked_or(uint32_t x, uint32_t y) {   // (x & MASK) | y
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(y));
-  return r;
-}
-__device__ __forceinline__ void unpack8(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t w,
-                                        const Exponents& exps) {
-  auto less = [](uint32_t x, uint32_t y) {
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&d);
-  };
+// The eight codes of a word as fp16 pairs (code p, code p + 4): r0 and r2 times 2^-24, r1 and r3 times 2^-20.
+__device__ __forceinline__ void unpack8(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t w) {
   const uint32_t h = w >> 8;
-  r0 = less(masked_or<0x000f000fu>(w, exps.e1024), 0x64086408u);    // 1024 + code - 1032
-  r1 = less(masked_or<0x00f000f0u>(w, exps.e64), 0x54805480u);      // 64 + code - 72
-  r2 = less(masked_or<0x000f000fu>(h, exps.e1024), 0x64086408u);
-  r3 = less(masked_or<0x00f000f0u>(h, exps.e64), 0x54805480u);
+  r0 = w & 0x000f000fu;
+  r1 = w & 0x00f000f0u;
+  r2 = h & 0x000f000fu;
+  r3 = h & 0x00f000f0u;
 }
 
 __device__ __forceinline__ float scale_of(uint32_t range) { return __uint_as_float(range << 16); }
@@ -188,7 +168,7 @@ __device__ __forceinline__ int row_in_eight(int n) { return (n & 1) * 4 + (n >> 
 template <int D>
 struct Queries {
   uint32_t f[D / 16][2];
-  float from[4], sum[2], c[2];
+  float sum[2], c[2];
   template <typename Load>
   __device__ __forceinline__ void take(float scale_log2, int gn, int lane, Load&& load) {
     constexpr int C = D / 4;                         // values of a lane: its codes' places
@@ -219,15 +199,14 @@ struct Queries {
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {                // pairs (0, 4), (1, 5), (2, 6), (3, 7): as a word of codes unpacks
       f[2 * w][0] = pack_half2(v[8 * w], v[8 * w + 4]);
-      f[2 * w][1] = pack_half2(v[8 * w + 1], v[8 * w + 5]);
+      f[2 * w][1] = pack_half2(v[8 * w + 1] * 0.0625f, v[8 * w + 5] * 0.0625f);
       f[2 * w + 1][0] = pack_half2(v[8 * w + 2], v[8 * w + 6]);
-      f[2 * w + 1][1] = pack_half2(v[8 * w + 3], v[8 * w + 7]);
+      f[2 * w + 1][1] = pack_half2(v[8 * w + 3] * 0.0625f, v[8 * w + 7] * 0.0625f);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       sum[i] = __shfl_sync(kAll, mine, 8 * (lane & 3) + 4 * i);
       c[i] = __shfl_sync(kAll, back, 8 * (lane & 3) + 4 * i);
-      from[i] = from[2 + i] = 8.0f * sum[i];
     }
   }
 };
@@ -235,15 +214,15 @@ struct Queries {
 // Products q . code of 16 key rows, tile j of s; w: this lane's quarter of rows n and n + 8.
 template <int D, int NQ, int NJ>
 __device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], int j, const Queries<D> (&q)[NQ],
-                                            const uint32_t (&w)[2][D / 32], const Exponents& exps) {
+                                            const uint32_t (&w)[2][D / 32]) {
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     uint32_t a[4], b[4];
-    unpack8(a[0], a[2], b[0], b[2], w[0][k], exps);
-    unpack8(a[1], a[3], b[1], b[3], w[1][k], exps);
+    unpack8(a[0], a[2], b[0], b[2], w[0][k]);
+    unpack8(a[1], a[3], b[1], b[3], w[1][k]);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      if (k == 0) mma16_from(s[i][j], a, q[i].f[0][0], q[i].f[0][1], q[i].from);
+      if (k == 0) mma16_new(s[i][j], a, q[i].f[0][0], q[i].f[0][1]);
       else mma16(s[i][j], a, q[i].f[2 * k][0], q[i].f[2 * k][1]);
       mma16(s[i][j], b, q[i].f[2 * k + 1][0], q[i].f[2 * k + 1][1]);
     }
@@ -253,9 +232,15 @@ __device__ __forceinline__ void code_scores(float (&s)[NQ][NJ][4], int j, const 
 // O += (code - 8) P for 16 value rows; w: byte columns (of D = 64 words, else half words) of rows q, q + 4, q + 8, q + 12; p:
 // probabilities times the rows' scales, as second operands. Tile t of O has values 8 n + 2 t and, in its lower half,
 // 8 n + 2 t + 1 as rows (D = 32: 4 n + ..).
-template <int D, int NQ>
-__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint32_t (&p)[NQ][2], const uint32_t (&w)[4],
-                                          const Exponents& exps) {
+template <bool FIRST, int D, int NQ>
+__device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], float (&eights)[NQ][4], const uint32_t (&p)[NQ][2],
+                                          const uint32_t (&w)[4]) {
+  const uint32_t less8[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    if (FIRST) mma16_new(eights[i], less8, p[i][0], p[i][1]);
+    else mma16(eights[i], less8, p[i][0], p[i][1]);
+  }
   uint32_t x[2][2];                                  // codes 0-3 and, of D = 64, 4-7 of two rows each, side by side
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -265,8 +250,8 @@ __device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], const uint3
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     uint32_t a[4], b[4];
-    unpack8(a[0], a[1], b[0], b[1], x[k][0], exps);
-    unpack8(a[2], a[3], b[2], b[3], x[k][1], exps);
+    unpack8(a[0], a[1], b[0], b[1], x[k][0]);
+    unpack8(a[2], a[3], b[2], b[3], x[k][1]);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       mma16(o[i][2 * k], a, p[i][0], p[i][1]);
@@ -327,6 +312,16 @@ struct Segment {
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][j][k] *= less;
     }
+  }
+
+  // Adds a unit's -8 sum P to its sums of code P.
+  __device__ __forceinline__ void centre(const float (&eights)[NQ][4]) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; k += ONE ? 2 : 1) o[i][j][k] += eights[i][k];
   }
 
   // Scores of the tiles into probabilities times the rows' scales. factors: shared address of the rows' (key scale, key
@@ -452,8 +447,8 @@ struct Segment {
     const float back = exp2_of((e - 15) / 2), rest = exp2_of(e - 15 - (e - 15) / 2);   // 2^(e - 15) in two steps
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      v[2 * j] = (o[i][j][k] + ot) * back * rest;
-      v[2 * j + 1] = (o[i][j][2 + k] + ot) * back * rest;
+      v[2 * j] = fmaf(o[i][j][k], 16777216.0f, ot) * back * rest;   // 2^24 and 2^20
+      v[2 * j + 1] = fmaf(o[i][j][2 + k], 1048576.0f, ot) * back * rest;
     }
     return lt;
   }
@@ -592,42 +587,39 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   Piece next = at;                                   // and the one behind it
   bool more = left > 0;
   if (more) next_piece(next);
-  // A copy of the warp takes 512 bytes: RPC rows' codes. This lane's 16 bytes are of eight rows whose page lane `block` (of the
-  // first copy; RPC / 8 on for each further one) has looked up; of the ranges it copies four rows' of the keys (lanes below
-  // UNIT / 4) or of the values.
-  constexpr int RPC = 512 / ROWB, COPIES = UNIT / RPC, PER8 = ROWB / 2;   // PER8: lanes that copy eight rows' codes
+  // A copy of the warp takes 512 bytes: RPC rows' codes. Eight rows of a head lie side by side, and the pool is counted in
+  // such blocks (32 bits: 2^32 of them are more than the memory holds): lanes below UNIT / 8 know those of the unit that is
+  // copied next, and every lane copies 16 bytes of block `block` (of the first copy; RPC / 8 on for each further one). Of the
+  // ranges it copies four rows' of the keys (lanes below UNIT / 4) or of the values.
+  constexpr int RPC = 512 / ROWB, COPIES = UNIT / RPC, PER8 = ROWB / 2;   // PER8: lanes that copy a block's codes
+  constexpr uint32_t kNoBlock = 0xffffffffu;
   const int block = lane / PER8, pmask = (1 << c.page_log2) - 1;
-  const uint32_t pageb = (2u * static_cast<uint32_t>(c.Hkv) << c.page_log2) * ROWB, rpageb = pageb / ROWB * 4;   // a page's codes, and ranges
-  const uint32_t lo = (lane % PER8) * 16;
-  const uint8_t* pool = static_cast<const uint8_t*>(c.pool);
-  const int rrow = 4 * (lane % (UNIT / 4)), rwhich = lane / (UNIT / 4);
-  const uint8_t* rfrom = reinterpret_cast<const uint8_t*>(ranges) + rwhich * (rpageb / 2);
-  // of the unit that is copied next: page of eight rows (of lanes below UNIT / 8; -2: none), the tile's first row
-  int pg = -2, r0 = 0;
+  const uint32_t page_blocks = static_cast<uint32_t>(c.Hkv) << (c.page_log2 - 2);   // of a page: keys, then values
+  const uint8_t* kfrom = static_cast<const uint8_t*>(c.pool) + (lane % PER8) * 16;
+  const uint8_t* vfrom = kfrom + static_cast<size_t>(page_blocks / 2) * (8 * ROWB);
+  const int rrow = 4 * (lane % (UNIT / 4));
+  const uint8_t* rfrom = reinterpret_cast<const uint8_t*>(ranges) + (lane / (UNIT / 4) ? page_blocks * 16 : 0u) + (rrow & 4) * 4;
+  int pg = -2;                                       // the page of this lane's eight rows; -2: none
+  uint32_t in_page = 0;                              // and their block in it
   auto look_up = [&](const Piece& x, int tile) {
-    r0 = first_row<UNIT>(x.t, tile);
-    const int r = r0 + 8 * lane;
+    const int r = first_row<UNIT>(x.t, tile) + 8 * lane;
     pg = lane < UNIT / 8 && r < x.t.n ? __ldg(c.table + static_cast<size_t>(x.b) * c.max_pages + (r >> c.page_log2)) : -2;
+    in_page = ((static_cast<uint32_t>(x.kh) << c.page_log2) + (r & pmask)) >> 3;
   };
-  auto copy_rows = [&](int kh, uint32_t to) {
-    if (static_cast<unsigned>(pg) >= static_cast<unsigned>(c.pages) && pg != -2) {
-      record_error(err, GPT_DEV_EPAGE);
-      pg = -2;
-    }
-    const uint32_t khrows = static_cast<uint32_t>(kh) << c.page_log2;
+  auto copy_rows = [&](uint32_t to) {
+    uint32_t blk = kNoBlock;
+    if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages)) blk = static_cast<uint32_t>(pg) * page_blocks + in_page;
+    else if (pg != -2) record_error(err, GPT_DEV_EPAGE);
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-      const int mine = __shfl_sync(kAll, pg, block + i * (RPC / 8));
-      const uint32_t in_page = (khrows + ((r0 + 8 * block + i * RPC) & pmask)) * ROWB + lo;
-      if (mine >= 0) {
-        const uint8_t* src = pool + static_cast<size_t>(static_cast<uint32_t>(mine)) * pageb + in_page;
-        copy16(to + lane * 16 + i * 512, src);
-        copy16(to + Cfg::TILE + lane * 16 + i * 512, src + pageb / 2);
+      const uint32_t mine = __shfl_sync(kAll, blk, block + i * (RPC / 8));
+      if (mine != kNoBlock) {
+        copy16(to + lane * 16 + i * 512, kfrom + static_cast<size_t>(mine) * (8 * ROWB));
+        copy16(to + Cfg::TILE + lane * 16 + i * 512, vfrom + static_cast<size_t>(mine) * (8 * ROWB));
       }
     }
-    const int mine = __shfl_sync(kAll, pg, rrow / 8);
-    if (mine >= 0 && lane < UNIT / 2)
-      copy16(to + Cfg::RANGES + lane * 16, rfrom + static_cast<size_t>(static_cast<uint32_t>(mine)) * rpageb + (khrows + ((r0 + rrow) & pmask)) * 4);
+    const uint32_t mine = __shfl_sync(kAll, blk, rrow / 8);
+    if (mine != kNoBlock && lane < UNIT / 2) copy16(to + Cfg::RANGES + lane * 16, rfrom + static_cast<size_t>(mine) * 32);
   };
   auto copy_queries = [&](const Piece& x, uint32_t to) {
     const int gn = min(w.G - x.mt * 16, 16);
@@ -638,7 +630,6 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   };
 
   constexpr bool ONE = QR == 1;
-  const Exponents exps;
   Segment<D, QR> g;
   const int n8 = lane >> 2, q4 = lane & 3;
   const uint32_t factors = ring + Cfg::FACTORS;
@@ -647,7 +638,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   }
   uint32_t st = ring, other = ring + Cfg::STAGE;     // the stage that is read, and the one that is filled meanwhile
   look_up(at, at.t0);
-  copy_rows(at.kh, st);
+  copy_rows(st);
   copy_queries(at, st);
   asm volatile("cp.async.commit_group;" ::: "memory");
   if (at.t0 + 1 < at.t1) look_up(at, at.t0 + 1);
@@ -655,12 +646,12 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   while (true) {
     for (int tile = at.t0; tile < at.t1; ++tile) {
       if (tile + 1 < at.t1) {
-        copy_rows(at.kh, other);
+        copy_rows(other);
         if (tile + 2 < at.t1) look_up(at, tile + 2);
         else if (more) look_up(next, 0);
       } else if (more) {
         if (at.t1 == at.t0 + 1) look_up(next, 0);      // (of pieces of one tile not before now)
-        copy_rows(next.kh, other);
+        copy_rows(other);
         copy_queries(next, other);
         if (next.t1 > 1) look_up(next, 1);
       }
@@ -688,7 +679,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
             if (!mine) vr = 0u;
           }
           unseen |= ~seen[h];
-          ks[h] = scale_of(kr);
+          ks[h] = scale_of(kr) * 16777216.0f;
           kl[h] = low_of(kr);
           vs[h] = scale_of(vr);
           vl[h] = low_of(vr);
@@ -702,7 +693,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
           if constexpr (!ONE) sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h], vl[h]);
         }
       }
-      float s[NQ][NJ][4];
+      float s[NQ][NJ][4], eights[NQ][4];
       const uint32_t krow = st + row_in_eight(n8) * ROWB + q4 * (D / 8), vcol = st + Cfg::TILE + q4 * ROWB + n8 * (D / 16);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -717,7 +708,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
             x[h][0] = lds32(krow + (16 * j + 8 * h) * ROWB);
           }
         }
-        code_scores<D, NQ, NJ>(s, j, g.qs, x, exps);
+        code_scores<D, NQ, NJ>(s, j, g.qs, x);
       }
       auto value_words = [&](uint32_t (&x)[4], int j) {
 #pragma unroll
@@ -741,9 +732,10 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
           const uint32_t p0[1][2] = {{w4.x, w4.y}}, p1[1][2] = {{w4.z, w4.w}};
           uint32_t u[4];
           value_words(u, 2 * h);
-          add_codes<D, NQ>(g.o, p0, u, exps);
+          if (h == 0) add_codes<true, D, NQ>(g.o, eights, p0, u);
+          else add_codes<false, D, NQ>(g.o, eights, p0, u);
           value_words(u, 2 * h + 1);
-          add_codes<D, NQ>(g.o, p1, u, exps);
+          add_codes<false, D, NQ>(g.o, eights, p1, u);
         }
       } else {
         __syncwarp();
@@ -757,9 +749,11 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
             p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
           }
           value_words(u, j);
-          add_codes<D, NQ>(g.o, p, u, exps);
+          if (j == 0) add_codes<true, D, NQ>(g.o, eights, p, u);
+          else add_codes<false, D, NQ>(g.o, eights, p, u);
         }
       }
+      g.centre(eights);
       const uint32_t swap = st;
       st = other;
       other = swap;
@@ -832,7 +826,6 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   // the first unit's pages, on their way before the length is known: right unless a window cuts
   const int guess = (rank * upw * 8 + warp) * UNIT;
   int page = __ldg(trow + min((guess + lane) >> c.page_log2, c.max_pages - 1));
-  const Exponents exps;
   Segment<D, QR> g;
   g.start(w.scale_log2, gn, lane, [&](int r, int u) { return __ldg(reinterpret_cast<const uint4*>(tok + static_cast<size_t>(r) * D) + u); });
   const int n = rows_of(c, w, len);
@@ -894,11 +887,11 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       vr = __ldg(ranges + row + vrows);
     }
     const uint32_t seen[1] = {__ballot_sync(kAll, is_seen)};
-    float ks[1] = {scale_of(kr)}, kl[1] = {low_of(kr)}, vs[1] = {scale_of(vr)}, vl[1] = {low_of(vr)};
+    float ks[1] = {scale_of(kr) * 16777216.0f}, kl[1] = {low_of(kr)}, vs[1] = {scale_of(vr)}, vl[1] = {low_of(vr)};
     g.fit(fmaxf(vs[0], fabsf(vl[0])));
     vl[0] = fmaf(8.0f, vs[0], vl[0]) * g.into;
     vs[0] *= g.into;
-    float s[NQ][2][4];
+    float s[NQ][2][4], eights[NQ][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t x[2][D / 32];
@@ -907,7 +900,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         x[0][k] = kw[2 * j][k];
         x[1][k] = kw[2 * j + 1][k];
       }
-      code_scores<D, NQ, 2>(s, j, g.qs, x, exps);
+      code_scores<D, NQ, 2>(s, j, g.qs, x);
     }
     uint32_t p[2][NQ][2];
     if constexpr (ONE) {
@@ -935,8 +928,10 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t x[4] = {vw[4 * j], vw[4 * j + 1], vw[4 * j + 2], vw[4 * j + 3]};
-      add_codes<D, NQ>(g.o, p[j], x, exps);
+      if (j == 0) add_codes<true, D, NQ>(g.o, eights, p[j], x);
+      else add_codes<false, D, NQ>(g.o, eights, p[j], x);
     }
+    g.centre(eights);
     __syncwarp();                                    // the factors are read before they are written again
   }
 #pragma unroll
