@@ -984,23 +984,25 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   }
 }
 
-// Joins the partial results of a (sequence, query head) in a fixed order, 256 / D parts of the pieces side by side; sequences
-// of no rows get zeros and -inf. (A block for all heads of a key head, one after another, took 126 of 133 us for one
-// sequence of 4,000 rows, 16 heads on one.)
-constexpr int kJoin4Threads = 256;
+// Joins the partial results of a (sequence, query head) in a fixed order, D / 4 threads to a piece, four pieces of a thread on
+// their way at once; sequences of no rows get zeros and -inf. (A block for all heads of a key head, one after another, took 126
+// of 133 us for one sequence of 4,000 rows, 16 heads on one.) Bound by latency: the lists' start, then the pieces.
+constexpr int kJoin4Pieces = 4;
 
 template <int D, int QR>
-__global__ void __launch_bounds__(kJoin4Threads)
+__global__ void __launch_bounds__(1024)
 paged4_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16* __restrict__ y, float* __restrict__ lse2,
                    Dec4Shape w, Dec4Scratch ws, int warps) {
   pdl_wait();
   pdl_trigger();
-  constexpr int P = kJoin4Threads / D;
-  __shared__ float s_o[P][D], s_m[P], s_l[P];
+  constexpr int LANES = D / 4;
+  __shared__ __align__(16) float s_o[32][D];
+  __shared__ float s_m[32], s_l[32];
+  const int P = static_cast<int>(blockDim.x) / LANES, W = static_cast<int>(blockDim.x) / 32;
   const int b = blockIdx.y, h = blockIdx.x, kh = h / w.G, mt = (h - kh * w.G) / 16, r = (h - kh * w.G) % 16;
   const int HM = c.Hkv * w.mg, p0 = ws.prefix[b], nt = ws.prefix[b + 1] - p0;
   const long long total = static_cast<long long>(ws.prefix[w.B]) * HM;
-  const int tid = threadIdx.x, d = tid % D, part = tid / D;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d4 = tid % LANES, part = tid / LANES;
   const size_t head = static_cast<size_t>(b) * w.H + h;
   if (nt == 0) {
     if (rows_of(c, w, __ldg(lens + b)) != 0) return;
@@ -1014,38 +1016,63 @@ paged4_join_kernel(PagedCache c, const int32_t* __restrict__ lens, __nv_bfloat16
   if (g1 == g2) return;                              // one warp held it all and wrote the output
   // a piece is its warp's first (slot 0) unless its segment starts behind the warp's start: only g1's can
   const size_t slot1 = static_cast<size_t>(g1) * 2 + (deal.start(g1) == t0 ? 0 : 1);
-  float m = -INFINITY, l = 0.0f, acc = 0.0f;
-#pragma unroll 8
-  for (int g = g1 + part; g <= g2; g += P) {
-    const size_t sl = (g == g1 ? slot1 : static_cast<size_t>(g) * 2) * QR + r;
-    const float2 x = ws.ml[sl];
-    const float o = ws.o[sl * D + d];
-    const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = ex2_approx(m - ref), e = ex2_approx(x.x - ref);
+  float m = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](float m2, float l2, const float4& o2) {
+    const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.0f : mn;
+    const float f = ex2_approx(m - ref), e = ex2_approx(m2 - ref);
     m = mn;
-    l = l * f + x.y * e;
-    acc = acc * f + o * e;
+    l = l * f + l2 * e;
+    acc[0] = acc[0] * f + o2.x * e;
+    acc[1] = acc[1] * f + o2.y * e;
+    acc[2] = acc[2] * f + o2.z * e;
+    acc[3] = acc[3] * f + o2.w * e;
+  };
+  for (int g0 = g1 + part; g0 <= g2; g0 += kJoin4Pieces * P) {
+    float2 x[kJoin4Pieces];
+    float4 o[kJoin4Pieces];
+#pragma unroll
+    for (int k = 0; k < kJoin4Pieces; ++k) {
+      const int g = g0 + k * P;
+      x[k] = make_float2(-INFINITY, 0.0f);
+      o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (g <= g2) {
+        const size_t sl = (g == g1 ? slot1 : static_cast<size_t>(g) * 2) * QR + r;
+        x[k] = ws.ml[sl];
+        o[k] = *reinterpret_cast<const float4*>(ws.o + sl * D + 4 * d4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kJoin4Pieces; ++k) add(x[k].x, x[k].y, o[k]);
   }
-  s_o[part][d] = acc;
-  if (d == 0) {
-    s_m[part] = m;
-    s_l[part] = l;
+#pragma unroll
+  for (int k = LANES; k < 32; k <<= 1) {             // the parts of a warp
+    const float m2 = __shfl_xor_sync(kAll, m, k), l2 = __shfl_xor_sync(kAll, l, k);
+    const float4 o2 = make_float4(__shfl_xor_sync(kAll, acc[0], k), __shfl_xor_sync(kAll, acc[1], k),
+                                  __shfl_xor_sync(kAll, acc[2], k), __shfl_xor_sync(kAll, acc[3], k));
+    add(m2, l2, o2);
+  }
+  if (lane < LANES) {
+    *reinterpret_cast<float4*>(&s_o[warp][4 * d4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
   }
   __syncthreads();
-  if (part) return;
-  float mx = m;
-#pragma unroll
-  for (int k = 1; k < P; ++k) mx = fmaxf(mx, s_m[k]);
+  if (tid >= D) return;
+  float mx = -INFINITY;
+#pragma unroll 8
+  for (int k = 0; k < W; ++k) mx = fmaxf(mx, s_m[k]);
   const float ref = mx == -INFINITY ? 0.0f : mx;
   float lt = 0.0f, at = 0.0f;
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
+#pragma unroll 8
+  for (int k = 0; k < W; ++k) {
     const float f = ex2_approx(s_m[k] - ref);
     lt += s_l[k] * f;
-    at += s_o[k][d] * f;
+    at += s_o[k][tid] * f;
   }
-  y[head * D + d] = __float2bfloat16(at / lt);
-  if (d == 0 && lse2) lse2[head] = mx + log2f(lt);
+  y[head * D + tid] = __float2bfloat16(at / lt);
+  if (tid == 0 && lse2) lse2[head] = mx + log2f(lt);
 }
 
 template <int D, int QR>
@@ -1105,9 +1132,13 @@ cudaError_t launch_decode4(const PagedCache& c, const uint32_t* ranges, const __
   ws.o = reinterpret_cast<float*>(p + pre_b);
   ws.ml = reinterpret_cast<float2*>(p + pre_b + o_b);
   e = launch_k(paged4_split_kernel<D, QR>, dim3(num_sms), dim3(32 * warps), smem, s, c, ranges, qkv, lens, y, lse2, w, ws, err);
+  // Blocks of 1,024 threads join where each has an SM and there are more pieces to a list than 256 take at once (graph replays,
+  // against 256): 12 heads on one, 200,000 rows 28.6 and 67.0 us; 16 x 20,000 rows, 4 key heads 23.5 and 24.5; but 192 lists of
+  // 13 pieces 53.1 and 50.7, 384 of 76 33.5 and 29.2.
+  const int join_threads = static_cast<long long>(w.B) * w.H <= num_sms && lists * (1024 / D) < NW ? 1024 : 256;
   if (e == cudaSuccess)
-    e = launch_k(paged4_join_kernel<D, QR>, dim3(static_cast<unsigned>(w.H), static_cast<unsigned>(w.B)), dim3(kJoin4Threads), 0,
-                 s, c, lens, y, lse2, w, ws, NW);
+    e = launch_k(paged4_join_kernel<D, QR>, dim3(static_cast<unsigned>(w.H), static_cast<unsigned>(w.B)), dim3(join_threads), 0, s,
+                 c, lens, y, lse2, w, ws, NW);
   const cudaError_t f = scratch_free(p, s);
   return e != cudaSuccess ? e : f;
 }
