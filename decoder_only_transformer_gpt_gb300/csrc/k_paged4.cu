@@ -3,12 +3,15 @@
 // A row stands for low + scale * code, so with Q = sum of a query's values
 //   q . k_r = scale_r (q . code_r) + low_r Q,
 //   sum_r p_r u_r = sum_r (p_r scale_r) (code_r - 8) + sum_r p_r (low_r + 8 scale_r),
-// and codes enter the products as they are, as fp16 numbers code - 8: a code in the low four bits of a half with the
-// exponent of 1024 is 1024 + code, one in bits 4 to 7 with the exponent of 64 is 64 + code, so a shift serves four operand
-// registers and each takes one logical operation and one packed subtraction, which is exact. (In bf16, whose seven bits of
-// mantissa hold one code, every register takes its own shift, and a code comes out as 16 + code: taking the 16 back from the
-// finished sums left the outputs of 20,000 rows 1.8e-3 of their norm off, where their own rounding makes 1.6e-3.)
-// fp16 has few exponents: queries enter it times a power of two, exactly (largest value in [2^14, 2^15); what is below 2^-38
+// and codes enter the products as the fp16 numbers that their bits are: in bits 0 to 3 of a half with nothing above them a
+// code is the subnormal code 2^-24, in bits 4 to 7 it is code 2^-20, so a word of eight codes takes one shift and four logical
+// operations. The powers of two are taken back with the keys' scales, with the queries (2^-4 for every other value) and in the
+// finished sums. The 8 is taken from the sums after every unit, by products of their own with -8: 64 rows' codes then add
+// up to no more than the fp32 sums can hold beside their centred values. (As 1024 + code and 64 + code, less 1032 and 72 by a
+// packed subtraction, an operand register took two instructions, and the long case below 59.8 us instead of 54.9. In bf16 every
+// register takes its own shift, and a code comes out as 16 + code: taking the 16 back from the finished sums left the outputs
+// of 20,000 rows 1.8e-3 of their norm off, where their own rounding makes 1.6e-3.)
+// fp16 has few exponents: queries enter it times a power of two, exactly (largest value in [2^14, 2^15); what is below 2^-34
 // of that is lost), and p_r scale_r times 2^(15 - E) with 2^E above every scale and lowest value of the rows so far: 11
 // bits (2^-12 of a term is lost; one bf16 part would lose 2^-9, as much as the output's own rounding), and whole multiples of
 // 2^-39 of 2^E for the smallest.
@@ -27,10 +30,12 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// Bound by issuing instructions, about 350 for 32 rows of a key head: a byte of codes takes a warp four times the unpacking
-// and products of a byte of bf16, and the integer unit takes a warp's instruction only every other cycle. Measured: 16
-// sequences of 9,000 to 32,000 rows x 12 heads 60.0 us, 4.7 TB/s, where the rows of a 16-bit cache take 160; with 8 query heads
-// on each of 4 key heads 34.5, with 12 50. Work is dealt as in the 16-bit cache's kernel (k_paged.cu):
+// Bound by memory once all warps are under way (8 sequences of 20,000 rows more take 19.3 us, 7.2 TB/s), with about 540
+// instructions for 64 rows of a key head close behind: a byte of codes takes a warp twice the unpacking and products of a byte
+// of bf16, and the integer unit takes a warp's instruction only every other cycle. Measured: 16 sequences of 9,000 to 32,000
+// rows x 12 heads 53.2 us, 5.3 TB/s, of which the first rows' chain of loads and the last units take 8 and the join 5; the rows
+// of a 16-bit cache take 160. With 8 query heads on each of 4 key heads 29.9, with 12 46. Work is dealt as in the 16-bit
+// cache's kernel (k_paged.cu):
 // units of 64 rows (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal
 // contiguous ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
@@ -41,9 +46,10 @@ constexpr unsigned kAll = 0xffffffffu;
 //    turned over by movmatrix.
 //  * A row's scales and lowest values are made into fp32 factors once, by the lane of its number.
 //  * Units are whole tiles of the sequence, so every eight rows of one lie in one page and start on a 16-byte boundary: the
-//    tile's pages, one to a lane, are looked up once, and every lane copies 16 bytes at a time (cp.async) into the warp's own
-//    ring. (A few bulk copies by as many lanes, counted by an mbarrier, cost more: each lane's copy is issued by itself.) Rows
-//    of a tile that are not seen are masked: their codes are numbers whatever they hold, their factors are set to 0.
+//    tile's pages, one to a lane, are looked up once and counted in blocks of eight rows, and every lane copies 16 bytes at a
+//    time (cp.async) into the warp's own ring. (A few bulk copies by as many lanes, counted by an mbarrier, cost more: each
+//    lane's copy is issued by itself.) Rows of a tile that are not seen are masked: their codes are numbers whatever they
+//    hold, their factors are set to 0.
 template <int D, int QR>
 struct Dec4Cfg {
   static constexpr int UNIT = QR == 16 ? 32 : 64;                 // rows of a unit
@@ -1084,21 +1090,23 @@ cudaError_t launch_decode4(const PagedCache& c, const uint32_t* ranges, const __
   cudaError_t e = device_sms(&dev, &num_sms);
   if (e != cudaSuccess) return e;
   // Few rows in sight: one launch of clusters, eight blocks at most, with as many units a warp as that takes. It pays while
-  // there are not many more blocks than run at once, and not many units behind each other (graph replays, 12 heads unless
-  // stated, against the general form): 16 sequences of 1,000 rows 12.6 and 13.9 us, 32 23.5 and 17.2; 8 of 4,000 rows 17.2 and
-  // 16.9; one of 16,000 13.2 and 26.9, four 32.6 and 27.5; of 12 heads on one, where a block takes more registers, 16 sequences
-  // of 1,000 rows and 4 key heads 10.4 and 13.4, of 2,040 rows 24.8 and 19.2.
+  // there are not many more blocks than run at once (of more than eight heads on one, whose blocks take more registers, one an
+  // SM), and not many units behind each other. Graph replays, against the general form: 12 heads, 12 sequences of 1,000 rows 8.7
+  // and 9.5 us, 14 11.6 and 11.2, 32 22.6 and 13.7; 4 of 4,000 rows 10.8 and 11.1, 8 16.1 and 12.5; one of 12,000 9.8 and 10.3, of
+  // 16,000 12.1 and 11.3; 16 heads on 4, 16 of 4,000 rows 12.8 and 13.7; 48 heads on 4, 16 of 1,000 rows 10.4 and 13.1, 8 of 2,000
+  // 14.8 and 12.7, 4 of 4,000 12.5 and 13.9, 8 of 4,000 18.7 and 16.2.
   long long units = ((static_cast<long long>(c.max_pages) << c.page_log2) + 31) / 32;
   if (w.window > 0) {
     const long long cut = (w.window + 31LL) / 32 + 1 + (w.sinks + 31LL) / 32;
     if (cut < units) units = cut;
   }
   const long long lists = static_cast<long long>(w.B) * c.Hkv * w.mg;
-  if (units <= 512) {
+  if (units <= 384) {
     int nc = 1;
     while (nc < 8 && nc * 8 < units) nc *= 2;
     const int upw = static_cast<int>((units + 8 * nc - 1) / (8 * nc));
-    if (nc * lists <= (QR == 16 ? 2LL : 6LL) * num_sms && nc * lists * upw <= 12LL * num_sms) {
+    const long long blocks = nc * lists, most = QR < 16 ? 4 : nc < 8 ? 2 : 1;
+    if (blocks <= most * num_sms && blocks * upw <= (QR < 16 ? 7LL : 2LL) * num_sms) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(nc) * c.Hkv * w.mg, static_cast<unsigned>(w.B));
       cfg.blockDim = dim3(256);

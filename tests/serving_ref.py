@@ -57,8 +57,8 @@ def values(codes, ranges):
 def attend4(qkv, codes, ranges, table, lens, H, window, sinks, added=0):
     """(y, lse2, bounds of y's and lse2's errors apart from y's rounding); rows of no sequence are NaN.
 
-    The bounds. A score is scale (8 Q + q . (code - 8)) + low Q: the products are exact (queries enter them times a power of two,
-    in fp16; what is below 2^-38 of its largest value is lost), and a chain of at most 16 sums of at most 16 sum |q| is off by
+    The bounds. A score is scale (q . code) + low Q: the products are exact (queries enter them times a power of two,
+    in fp16; what is below 2^-34 of its largest value is lost), and a chain of at most 16 sums of at most 16 sum |q| is off by
     2^-24 of that at every step, or 2^-23 where an adder cuts off: 2^-19 16 sum |q|, times the scale; the low term adds three
     roundings. So the base-2 exponents are off by d, the weights by the factor 2^(2 d), another 2^-20 for exponentials and sums.
     A weight times its scale is rounded to fp16 once, 2^-12 of it, times |code - 8| <= 8; the smallest ones to whole multiples
