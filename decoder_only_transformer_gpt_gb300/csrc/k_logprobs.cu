@@ -33,6 +33,8 @@ constexpr float kFar = -1e20f;           // stands for differences of -inf in pr
 constexpr int kLpWarps = 8;
 constexpr int kLpVecs = 4;               // 16-byte vectors a lane and chunk
 constexpr int kLpChunk = 32 * kLpVecs;   // vectors a warp and chunk
+constexpr int kLpFewTop = 16;
+constexpr int kLpPool = 64;              // tokens that are put in order at once
 constexpr int kLpGroups = 16;            // maxima that a thread notes: of a chunk each, or of as many as it takes
 
 using Key = unsigned long long;
@@ -86,6 +88,13 @@ __device__ __forceinline__ float sorted_values(float v, int lane) {
   return v;
 }
 
+// The largest of the lanes' values, in all of them (a NaN is passed over).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -113,6 +122,10 @@ template <> struct Vec<float> {
   }
   static __device__ __forceinline__ void put(float* p, float x) { *p = x; }
   static constexpr uint32_t kNone = 0xff800000u;     // -inf
+  static __device__ __forceinline__ float most(const uint4& v) {
+    const float2 a = pair(v, 0), b = pair(v, 1);
+    return fmaxf(fmax3(a.x, a.y, b.x), b.y);
+  }
   static __device__ __forceinline__ float largest(const uint4 (&v)[kLpVecs]) {
     float m = -INFINITY;
 #pragma unroll
@@ -132,6 +145,11 @@ template <> struct Vec<__nv_bfloat16> {
   }
   static __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
   static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __forceinline__ float most(const uint4& v) {
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v.x);
+    const float2 f = __bfloat1622float2(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
+    return fmaxf(f.x, f.y);
+  }
   static __device__ __forceinline__ float largest(const uint4 (&v)[kLpVecs]) {
     const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
     __nv_bfloat162 m = w[0];
@@ -174,8 +192,10 @@ logprobs_kernel(LpArgs a, int* err) {
   namespace cg = cooperative_groups;
   __shared__ __align__(16) uint4 s_stage[kLpWarps][32][kLpVecs + 1];
   __shared__ float s_max[FEW ? 1 : kLpGroups][kLpWarps * 32];   // the threads' largest logits, by group of chunks
-  __shared__ float s_order[kLpWarps][32];            // and over all groups, in order
+  __shared__ __align__(16) float s_order[kLpWarps][32];   // and over all groups, in order: all, or each warp's four largest
   __shared__ Key s_list[kLpWarps][32], s_lists[NC][32];   // the warps' lists, and the blocks'
+  __shared__ Key s_pool[2][kLpPool], s_best[32];     // the same without an order where they are few, and in order
+  __shared__ int s_count;
   __shared__ Sums s_sums[8], s_parts[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC);
@@ -283,6 +303,7 @@ logprobs_kernel(LpArgs a, int* err) {
     const float mn = fmaxf(sum.m, ze), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E), d = ze - mn, e = ex2_approx(d * kL2E);
     sum = {mn, sum.s * f + e, f * (sum.a + sum.s * dm) + e * fmaxf(d, kFar)};
   }
+  float reached = 0.0f;                              // by K threads' largest logits
   if (K) {
     // Blocks take the same time for their rows and so come to this part together, in which nothing is read: the first
     // chunks of a row that comes next are fetched into L2 meanwhile.
@@ -295,19 +316,81 @@ logprobs_kernel(LpArgs a, int* err) {
       s_max[group++][threadIdx.x] = noted;
       top = fmaxf(top, noted);
     }
-    float order = sorted_values(top, lane), reached;   // reached: by K threads' largest logits
     if constexpr (WR == 1) {
-      reached = __shfl_sync(kAll, order, K - 1);
+      reached = __shfl_sync(kAll, sorted_values(top, lane), K - 1);
     } else {
-      s_order[warp][lane] = order;
-      __syncthreads();
+      if (threadIdx.x == 0) s_count = 0;
+      if (K <= kLpFewTop) {
+        float left = top, mine = 0.0f;
 #pragma unroll
-      for (int half = kLpWarps / 2; half; half >>= 1) {
-        if (warp < half) s_order[warp][lane] = order = join_values(order, s_order[warp + half][lane], lane);
+        for (int k = 0; k < 4; ++k) {
+          const float most = warp_max(left);
+          if (lane == k) mine = most;
+          if (lane == __ffs(__ballot_sync(kAll, left == most)) - 1) left = -INFINITY;
+        }
+        if (lane < 4) s_order[0][4 * warp + lane] = mine;
         __syncthreads();
+        const float x = s_order[0][lane];
+        int at = 0;
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(&s_order[0][k]);
+          at += (y.x > x || (y.x == x && k < lane)) + (y.y > x || (y.y == x && k + 1 < lane)) +
+                (y.z > x || (y.z == x && k + 2 < lane)) + (y.w > x || (y.w == x && k + 3 < lane));
+        }
+        reached = __shfl_sync(kAll, x, __ffs(__ballot_sync(kAll, at == K - 1)) - 1);
+      } else {
+        float order = sorted_values(top, lane);
+        s_order[warp][lane] = order;
+        __syncthreads();
+#pragma unroll
+        for (int half = kLpWarps / 2; half; half >>= 1) {
+          if (warp < half) s_order[warp][lane] = order = join_values(order, s_order[warp + half][lane], lane);
+          __syncthreads();
+        }
+        reached = s_order[0][K - 1];
       }
-      reached = s_order[0][K - 1];
     }
+  }
+  // The chunks that may hold a token which passes: passes(a largest logit, the first index of its chunk), use(their 16-byte
+  // vectors, one thread's chunk a lane; whether there is one, its largest logit, its number and its thread).
+  auto each_chunk = [&](auto&& passes, auto&& use) {
+    if constexpr (FEW) {
+      if (__any_sync(kAll, cm0 >= reached)) use(v, first < chunks, cm0, first, lane);
+      if (__any_sync(kAll, cm1 >= reached)) use(next, first + step < chunks, cm1, first + step, lane);
+    } else if (__any_sync(kAll, top >= reached)) {
+      // what is read again: as many at once as there are lanes, so that they travel together
+      int items = 0, item_chunk = 0, item_lane = 0;
+      auto look = [&]() {
+#pragma unroll
+        for (int k = 0; k < kLpVecs; ++k) {
+          const int i = item_chunk * kLpChunk + k * 32 + item_lane;
+          v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
+          if (lane < items && i < row.nvec) v[k] = __ldg(vecs + i);
+        }
+        use(v, lane < items, W::largest(v), item_chunk, item_lane);
+        items = 0;
+      };
+      for (int g = 0; g < group; ++g) {
+        const float most = s_max[g][threadIdx.x];
+        if (!__any_sync(kAll, most >= reached)) continue;
+        for (int c = first + g * per * step; c < min(chunks, first + (g + 1) * per * step); c += step) {
+          unsigned who = __ballot_sync(kAll, passes(most, row.head + (c * kLpChunk + lane) * N));
+          while (who) {
+            if (lane == items) {
+              item_chunk = c;
+              item_lane = __ffs(who) - 1;
+            }
+            who &= who - 1;
+            if (++items == 32) look();
+          }
+        }
+      }
+      if (items) look();
+    }
+  };
+  // The warp's best tokens, in order, from its chunks.
+  auto search = [&]() {
     Key floor_key = (key_of(reached, 0) >> 32) << 32;   // what a token has to pass
     // Puts the lanes' keys that pass into the list, one by one.
     auto insert = [&](Key key) {
@@ -323,9 +406,8 @@ logprobs_kernel(LpArgs a, int* err) {
         who &= __ballot_sync(kAll, key > floor_key);
       }
     };
-    // Chunks of one thread each, a lane's own in x (its chunk's number, of that thread; cm: the largest value; none where `some`
-    // is false): the tokens that pass.
-    auto search = [&](const uint4 (&x)[kLpVecs], bool some, float cm, int chunk, int thread) {
+    each_chunk([&](float most, int index) { return key_of(most, index) > floor_key; },
+               [&](const uint4 (&x)[kLpVecs], bool some, float cm, int chunk, int thread) {
       const Key best_here = some ? key_of(cm, row.head + (chunk * kLpChunk + thread) * N) : 0;
       unsigned who = __ballot_sync(kAll, best_here > floor_key);
       if (__popc(who) > K) {
@@ -348,42 +430,45 @@ logprobs_kernel(LpArgs a, int* err) {
         who &= __ballot_sync(kAll, best_here > floor_key);
       }
       __syncwarp();                                  // the stage is read before it is filled again
-    };
-    if constexpr (FEW) {
-      if (__any_sync(kAll, cm0 >= reached)) search(v, first < chunks, cm0, first, lane);
-      if (__any_sync(kAll, cm1 >= reached)) search(next, first + step < chunks, cm1, first + step, lane);
-    } else if (__any_sync(kAll, top >= reached)) {
-      // what is read again: one thread's chunk a lane, as many as there are at once, so that they travel together
-      int items = 0, item_chunk = 0, item_lane = 0;
-      auto look = [&]() {
-#pragma unroll
-        for (int k = 0; k < kLpVecs; ++k) {
-          const int i = item_chunk * kLpChunk + k * 32 + item_lane;
-          v[k] = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-          if (lane < items && i < row.nvec) v[k] = __ldg(vecs + i);
-        }
-        search(v, lane < items, W::largest(v), item_chunk, item_lane);
-        items = 0;
-      };
-      for (int g = 0; g < group; ++g) {
-        const float most = s_max[g][threadIdx.x];
-        if (!__any_sync(kAll, most >= reached)) continue;
-        for (int c = first + g * per * step; c < min(chunks, first + (g + 1) * per * step); c += step) {
-          // lanes whose largest logit, at their first index of the chunk, would pass
-          unsigned who = __ballot_sync(kAll, key_of(most, row.head + (c * kLpChunk + lane) * N) > floor_key);
-          while (who) {
-            if (lane == items) {
-              item_chunk = c;
-              item_lane = __ffs(who) - 1;
-            }
-            who &= who - 1;
-            if (++items == 32) look();
-          }
-        }
-      }
-      if (items) look();
-    }
+    });
     if (lead) insert(edge >= 0 ? key_of(ze, edge) : 0);
+  };
+  if constexpr (WR == 1) {
+    if (K) search();
+  } else if (K) {
+    // Every token that reaches it, in any order: as a rule K of them and a few more.
+    auto put = [&](int place, float z, int index) {
+      if (place < kLpPool) s_pool[0][place] = key_of(z, index);
+    };
+    each_chunk([&](float most, int) { return most >= reached; },
+               [&](const uint4 (&x)[kLpVecs], bool some, float cm, int chunk, int thread) {
+      if (!some || !(cm >= reached)) return;
+      unsigned which = 0;                            // this lane's vectors with such a token
+#pragma unroll
+      for (int k = 0; k < kLpVecs; ++k)
+        if (chunk * kLpChunk + k * 32 + thread < row.nvec && W::most(x[k]) >= reached) which |= 1u << k;
+      while (which) {
+        const int k = __ffs(which) - 1, index = row.head + (chunk * kLpChunk + k * 32 + thread) * N;
+        which &= which - 1;
+        uint4 y = x[0];
+#pragma unroll
+        for (int i = 1; i < kLpVecs; ++i)
+          if (i == k) y = x[i];
+        unsigned hits = 0;
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          const float2 z = W::pair(y, j);
+          if (z.x >= reached) hits |= 1u << (2 * j);
+          if (z.y >= reached) hits |= 2u << (2 * j);
+        }
+        int place = atomicAdd(&s_count, __popc(hits));
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if ((hits >> j) & 1u) put(place++, j & 1 ? W::pair(y, j / 2).y : W::pair(y, j / 2).x, index + j);
+      }
+    });
+    if (edge >= 0 && ze >= reached) put(atomicAdd(&s_count, 1), ze, edge);
+    __syncwarp();
   }
   auto shuffled = [&](const Sums& x, int k) {
     return joined_sums(x, {__shfl_xor_sync(kAll, x.m, k), __shfl_xor_sync(kAll, x.s, k), __shfl_xor_sync(kAll, x.a, k)});
@@ -391,37 +476,71 @@ logprobs_kernel(LpArgs a, int* err) {
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) sum = shuffled(sum, k);
   if constexpr (WR > 1) {
-    // n <= 8 lists and sums in shared memory, to warp 0
-    auto join8 = [&](Key (*list)[32], const Sums* sums, int n) {
-      if (K) {
+    // Lists in shared memory to all warps, joined two by two: the larger of each pair of opposite ends is a bitonic sequence of
+    // the best 32, sorted in five steps.
+    auto join_all = [&](Key (*list)[32], int n) {
 #pragma unroll
-        for (int half = 4; half; half >>= 1) {
-          if (n > half) {
-            if (warp < half && warp + half < n) list[warp][lane] = join_lists(list[warp][lane], list[warp + half][lane], lane);
-            __syncthreads();
-          }
+      for (int half = 4; half; half >>= 1) {
+        if (n > half) {
+          if (warp < half && warp + half < n) list[warp][lane] = join_lists(list[warp][lane], list[warp + half][lane], lane);
+          __syncthreads();
         }
-        best = list[0][lane];
       }
-      if (warp) return;
+      best = list[0][lane];
+    };
+    // Up to kLpPool tokens in any order to one warp: each one's place is the number of larger ones. (Reading them all costs a
+    // third of joining eight lists, whose three steps wait for one another.)
+    auto ranked = [&](const Key* pool, int n) {
+      const Key x = lane < n ? pool[lane] : 0, y = lane + 32 < n ? pool[lane + 32] : 0;
+      int at_x = 0, at_y = 0;
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const Key z = pool[k];
+        at_x += z > x;
+        at_y += z > y;
+      }
+      s_best[lane] = 0;
+      __syncwarp();
+      if (x && at_x < 32) s_best[at_x] = x;
+      if (y && at_y < 32) s_best[at_y] = y;
+      __syncwarp();
+      best = s_best[lane];
+    };
+    auto join_sums = [&](const Sums* sums, int n) {
       sum = (lane & 7) < n ? sums[lane & 7] : Sums{kLowest, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 1; k < 8; k <<= 1) sum = shuffled(sum, k);
     };
     if (lane == 0) s_sums[warp] = sum;
-    if (K) s_list[warp][lane] = best;
     __syncthreads();
-    join8(s_list, s_sums, kLpWarps);
+    if (K) {
+      const int n = s_count;
+      if (n <= kLpPool) {
+        if (warp == 0) ranked(s_pool[0], n);
+      } else {                                       // (many equal ones, or many large ones in few threads)
+        search();
+        s_list[warp][lane] = best;
+        __syncthreads();
+        join_all(s_list, kLpWarps);
+      }
+    }
+    if (warp == 0) join_sums(s_sums, kLpWarps);
     if constexpr (NC > 1) {
+      const bool pool = NC * K <= kLpPool;
       auto cluster = cg::this_cluster();
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
       if (warp == 0) {
-        if (K) *cluster.map_shared_rank(&s_lists[part][lane], 0) = best;
+        if (K && !pool) *cluster.map_shared_rank(&s_lists[part][lane], 0) = best;
+        if (lane < K && pool) *cluster.map_shared_rank(&s_pool[1][part * K + lane], 0) = best;
         if (lane == 0) *cluster.map_shared_rank(&s_parts[part], 0) = sum;
       }
       cluster.sync();
       if (part) return;
-      join8(s_lists, s_parts, NC);
+      if (K) {
+        if (!pool) join_all(s_lists, NC);
+        else if (warp == 0) ranked(s_pool[1], NC * K);
+      }
+      if (warp == 0) join_sums(s_parts, NC);
     }
     if (warp) return;
   }
