@@ -185,7 +185,7 @@ struct Row {
 // A warp takes a row (WR = 1; eight rows a block), or a block's eight warps do (WR = 8), or those of a cluster of NC blocks: the
 // row's chunks go round the warps. FEW: no warp has more than two, which then stay in its registers and are not read again.
 template <typename T, int NC, int WR, bool FEW>
-__global__ void __launch_bounds__(kLpWarps * 32)
+__global__ void __launch_bounds__(kLpWarps * 32, NC > 1 ? 2 : 0)
 logprobs_kernel(LpArgs a, int* err) {
   using W = Vec<T>;
   constexpr int N = W::N, VALUES = kLpVecs * N;      // values a lane and chunk
@@ -238,7 +238,7 @@ logprobs_kernel(LpArgs a, int* err) {
     sum = {mn, s.x + s.y, e2.x + e2.y};
   };
   const int full = row.nvec / kLpChunk;              // chunks without a gap
-  const int step = WR == 1 ? 1 : NC * kLpWarps, first = WR == 1 ? 0 : part * kLpWarps + warp;
+  const int step = WR == 1 ? 1 : NC * kLpWarps, first = WR == 1 ? 0 : warp * NC + part;
   const int chunks = (row.nvec + kLpChunk - 1) / kLpChunk;
   const int per = ((chunks + step - 1) / step + kLpGroups - 1) / kLpGroups;   // chunks of a group
   float top = -INFINITY, noted = -INFINITY;          // this thread's largest logit, and of the group
