@@ -6,15 +6,17 @@
 // the gradient gets (m, S), as e^(z - lse) would carry the rounding of lse, 2^-24 |lse| of every probability.
 //
 // The most probable tokens, behind the sums: every thread has noted the largest logit of each of its chunks. The K-th largest
-// of the 256 threads' maxima is a floor that K tokens reach, and few others: only the chunks of threads that reach it are read
-// again (out of L2). A warp keeps the best 32 tokens that it finds there in order, one a lane, as 64-bit keys (logit, then
-// lowest index); lists are joined two by two: the larger of each pair of opposite ends is a bitonic sequence of the best
-// 32, sorted in five steps. (Lists kept up to date while the row went by took 8 to 16 instructions for every 32 logits, as
-// many as the sums: 4,096 rows of 50,257 with K = 8 took 151 us in fp32 and 124 in bf16.)
+// of the warps' four largest of those is a floor that K tokens reach, and few others: only the chunks of threads that reach it
+// are looked at again (out of L2, where they are not kept in registers), and what reaches it there goes into one pool of keys
+// (logit, then lowest index) in shared memory, in any order. A key's place is the number of larger ones, so the result does
+// not depend on that order. Where more tokens reach the floor than the pool holds (many equal ones), every warp keeps its best
+// 32 in order instead, one a lane, and the lists are joined. A warp that has a row to itself does so from the start. (Lists
+// kept up to date while the row went by took 8 to 16 instructions for every 32 logits, as many as the sums: 4,096 rows of
+// 50,257 with K = 8 took 151 us in fp32 and 124 in bf16; lists for every warp behind the sums 135 and 85.)
 //
-// Bound by memory where rows are many: 4,096 x 50,257 in fp32 123 us with K = 0, 6.7 TB/s, what a copy reaches, and 135 with
-// K = 8; in bf16 70 and 85, 5.9 TB/s, the exponentials' units and the sums' instructions close behind. The part after the
-// sums reads little and lets the memory rest: that is what K adds.
+// Bound by memory where rows are many: 4,096 x 50,257 in fp32 123 us with K = 0, 6.7 TB/s, what a copy reaches, and 128 with
+// K = 8; in bf16 70 and 81, 5.9 TB/s, the exponentials' units and the sums' instructions close behind. The part after the
+// sums reads little and lets the memory rest: that is what K adds. 16 rows with K = 5 4.6 us in a graph, 2.9 with K = 0.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -33,6 +35,8 @@ constexpr float kFar = -1e20f;           // stands for differences of -inf in pr
 constexpr int kLpWarps = 8;
 constexpr int kLpVecs = 4;               // 16-byte vectors a lane and chunk
 constexpr int kLpChunk = 32 * kLpVecs;   // vectors a warp and chunk
+// Up to this K the floor comes from the warps' four largest logits, else from all (16 rows of 50,257 with K = 20 5.2 and 5.3 us,
+// with K = 32 11.5 and 5.5, as the pool then holds too few for what reaches the lower floor).
 constexpr int kLpFewTop = 16;
 constexpr int kLpPool = 64;              // tokens that are put in order at once
 constexpr int kLpGroups = 16;            // maxima that a thread notes: of a chunk each, or of as many as it takes
@@ -661,10 +665,11 @@ cudaError_t launch_logprobs_of(LpArgs a, int* err, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long chunks = (static_cast<long long>(a.V) / Vec<T>::N + kLpChunk - 1) / kLpChunk;
   a.ahead = 4 * sms;                                 // (four blocks an SM)
-  // A warp a row where its whole row is two chunks, or the rows are short and many: 4,096 x 500 with K = 5 6.1 us, a block a row
-  // 35; 2,500 x 5,000 16.6 and 21.5; but 1,500 x 8,000 17.1 and 14.8, 620 x 5,000 9.0 and 7.9 (graph replays). Clusters of as
-  // many blocks as keep all of them at work at once.
-  if (chunks <= 2 || (chunks <= 10 && a.M >= 8LL * sms)) {
+  // A warp a row where its whole row is two chunks, or the rows are short and many and not too many tokens are wanted: 4,096 x
+  // 500 with K = 5 6.2 us, a block a row 42; 4,096 x 5,000 22.3 and 30.3, with K = 16 28.9 and 32.6, but with K = 32 62 and 36;
+  // 1,500 x 8,000 17.1 and 14.8, 620 x 5,000 9.0 and 7.9 (graph replays). Clusters of as many blocks as keep all of them at
+  // work at once.
+  if (chunks <= 2 || (chunks <= 10 && a.M >= 8LL * sms && a.K <= kLpFewTop)) {
     a.ahead *= kLpWarps;
     return launch_form<T, 1, 1>(a, chunks, err, s);
   }

@@ -146,6 +146,28 @@ def test_rows_of_a_large_vocabulary(gpt_lib, dtype, M):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,V", [(3, 50257), (20, 50257), (60, 20011), (130, 9001), (700, 2500), (200, 400)])
+@pytest.mark.parametrize("K", [1, 16, 17, 32])
+def test_more_equal_logits_than_are_wanted(gpt_lib, dtype, M, V, K):
+    # rows all equal; of two values, a few hundred of the larger; the larger ones side by side
+    from decoder_only_transformer_gpt_gb300 import binding
+    rng = np.random.default_rng(V + K)
+    z = np.full((M, V), -1.5)
+    for i in range(1, M, 3):
+        z[i, rng.permutation(V)[:300]] = 2.0
+    for i in range(2, M, 3):
+        at = int(rng.integers(0, V - 200))
+        z[i, at: at + 200] = 2.0 + np.arange(200) / 64.0
+    t = some_targets(M, V, K)
+    d, zd, _ = run(z, t, K, dtype)
+    binding.status()
+    keep = sorted({0, 1, 2, M // 2, M - 2, M - 1})
+    check({k: None if v is None else v[keep] for k, v in d.items()}, zd[keep], [t[i] for i in keep], K)
+    for i in range(3, M, 3):                         # equal rows, equal results
+        assert torch.equal(d["top_ids"][i], d["top_ids"][0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("V,K", [(2049, 1), (3001, 5), (5003, 0), (5003, 32), (5120, 32)])
 @pytest.mark.parametrize("M", [1300, 2437])
 def test_many_short_rows(gpt_lib, dtype, V, K, M):
