@@ -188,8 +188,10 @@ struct Row {
 
 // A warp takes a row (WR = 1; eight rows a block), or a block's eight warps do (WR = 8), or those of a cluster of NC blocks: the
 // row's chunks go round the warps. FEW: no warp has more than two, which then stay in its registers and are not read again.
-template <typename T, int NC, int WR, bool FEW>
-__global__ void __launch_bounds__(kLpWarps * 32, NC > 1 ? 2 : 0)
+// TOP: false where none of the most probable tokens are wanted (K = 0; of the forms with a warp a row, which it leaves a block
+// more an SM).
+template <typename T, int NC, int WR, bool FEW, bool TOP>
+__global__ void __launch_bounds__(kLpWarps * 32, NC > 1 ? 2 : WR == 1 && FEW && TOP ? 3 : 0)
 logprobs_kernel(LpArgs a, int* err) {
   using W = Vec<T>;
   constexpr int N = W::N, VALUES = kLpVecs * N;      // values a lane and chunk
@@ -198,8 +200,8 @@ logprobs_kernel(LpArgs a, int* err) {
   __shared__ float s_max[FEW ? 1 : kLpGroups][kLpWarps * 32];   // the threads' largest logits, by group of chunks
   __shared__ __align__(16) float s_order[kLpWarps][32];   // and over all groups, in order: all, or each warp's four largest
   __shared__ Key s_list[kLpWarps][32], s_lists[NC][32];   // the warps' lists, and the blocks'
-  __shared__ Key s_pool[2][kLpPool], s_best[32];     // the same without an order where they are few, and in order
-  __shared__ int s_count;
+  __shared__ Key s_pool[WR == 1 ? kLpWarps : 2][kLpPool], s_best[kLpWarps / WR][32];   // tokens without an order, and in order
+  __shared__ int s_count[kLpWarps / WR];             // how many
   __shared__ Sums s_sums[8], s_parts[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = NC == 1 ? 0 : static_cast<int>(blockIdx.x % NC);
@@ -209,9 +211,10 @@ logprobs_kernel(LpArgs a, int* err) {
   pdl_trigger();
   if (WR == 1 && m >= a.M) return;
   const bool lead = WR == 1 || (part == 0 && warp == 0);
+  const int team = WR == 1 ? warp : 0;               // of the block's rows
   const Row<T> row(a.z, a.ld, a.V, m);
   const uint4* vecs = reinterpret_cast<const uint4*>(row.z + row.head);
-  const int K = a.K;
+  const int K = TOP ? a.K : 0;
   int target = -1;
   float zt = 0.0f;
   if (lead && lane == 0 && a.targets) {
@@ -320,10 +323,22 @@ logprobs_kernel(LpArgs a, int* err) {
       s_max[group++][threadIdx.x] = noted;
       top = fmaxf(top, noted);
     }
+    if ((WR == 1 || warp == 0) && lane == 0) s_count[team] = 0;   // (of every block of a cluster)
     if constexpr (WR == 1) {
-      reached = __shfl_sync(kAll, sorted_values(top, lane), K - 1);
+      float order = sorted_values(top, lane);
+      if constexpr (FEW) {
+        if (K > kLpFewTop) {                         // of two numbers a lane, as 32 do not let enough be left out
+          float a = cm0, b = cm1;
+          if (chunks < 2) {
+            a = fmaxf(W::most(v[0]), W::most(v[2]));
+            b = fmaxf(W::most(v[1]), W::most(v[3]));
+          }
+          order = join_values(sorted_values(a, lane), sorted_values(b, lane), lane);
+        }
+      }
+      reached = __shfl_sync(kAll, order, K - 1);
+      __syncwarp();
     } else {
-      if (threadIdx.x == 0) s_count = 0;
       if (K <= kLpFewTop) {
         float left = top, mine = 0.0f;
 #pragma unroll
@@ -399,6 +414,7 @@ logprobs_kernel(LpArgs a, int* err) {
     // Puts the lanes' keys that pass into the list, one by one.
     auto insert = [&](Key key) {
       unsigned who = __ballot_sync(kAll, key > floor_key);
+#pragma unroll 1
       while (who) {
         const Key k = __shfl_sync(kAll, key, __ffs(who) - 1);
         const int n = __popc(__ballot_sync(kAll, best > k));
@@ -437,23 +453,49 @@ logprobs_kernel(LpArgs a, int* err) {
     });
     if (lead) insert(edge >= 0 ? key_of(ze, edge) : 0);
   };
-  if constexpr (WR == 1) {
-    if (K) search();
-  } else if (K) {
+  // Up to kLpPool tokens in any order to one warp: each one's place is the number of larger ones. (Reading them all costs a
+  // third of joining eight lists, whose three steps wait for one another.)
+  auto ranked = [&](const Key* pool, int n) {
+    const Key x = lane < n ? pool[lane] : 0, y = lane + 32 < n ? pool[lane + 32] : 0;
+    int at_x = 0, at_y = 0;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const Key z = pool[k];
+      at_x += z > x;
+      at_y += z > y;
+    }
+    s_best[team][lane] = 0;
+    __syncwarp();
+    if (x && at_x < 32) s_best[team][at_x] = x;
+    if (y && at_y < 32) s_best[team][at_y] = y;
+    __syncwarp();
+    best = s_best[team][lane];
+  };
+  if (K) {
     // Every token that reaches it, in any order: as a rule K of them and a few more.
-    auto put = [&](int place, float z, int index) {
-      if (place < kLpPool) s_pool[0][place] = key_of(z, index);
+    const uint32_t room = smem_u32(&s_pool[team][0]);
+    auto put = [&](bool hit, int place, float z, int index) {
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.shared.b64 [%1], %2;\n\t}" ::"r"(
+                       static_cast<int>(hit && static_cast<unsigned>(place) < kLpPool)),
+                   "r"(room + 8 * static_cast<uint32_t>(place)), "l"(key_of(z, index))
+                   : "memory");
     };
     each_chunk([&](float most, int) { return most >= reached; },
                [&](const uint4 (&x)[kLpVecs], bool some, float cm, int chunk, int thread) {
-      if (!some || !(cm >= reached)) return;
       unsigned which = 0;                            // this lane's vectors with such a token
+      if (some && cm >= reached) {
 #pragma unroll
-      for (int k = 0; k < kLpVecs; ++k)
-        if (chunk * kLpChunk + k * 32 + thread < row.nvec && W::most(x[k]) >= reached) which |= 1u << k;
-      while (which) {
-        const int k = __ffs(which) - 1, index = row.head + (chunk * kLpChunk + k * 32 + thread) * N;
-        which &= which - 1;
+        for (int k = 0; k < kLpVecs; ++k)
+          if (chunk * kLpChunk + k * 32 + thread < row.nvec && W::most(x[k]) >= reached) which |= 1u << k;
+      }
+      // Each lane its own one after the other, but where a warp has the row to itself any lane's: of 200 rows of 500 some have a
+      // lane with three, which took 5.7 us instead of 3.5. (A block's warps have fewer to go through: 4,096 x 50,257 in bf16
+      // with K = 8 83 us, with any lane's 86.)
+      unsigned left = WR == 1 ? __reduce_or_sync(kAll, which) : which;
+#pragma unroll 1
+      while (left) {
+        const int k = __ffs(left) - 1, index = row.head + (chunk * kLpChunk + k * 32 + thread) * N;
+        left &= left - 1;
         uint4 y = x[0];
 #pragma unroll
         for (int i = 1; i < kLpVecs; ++i)
@@ -465,14 +507,24 @@ logprobs_kernel(LpArgs a, int* err) {
           if (z.x >= reached) hits |= 1u << (2 * j);
           if (z.y >= reached) hits |= 2u << (2 * j);
         }
-        int place = atomicAdd(&s_count, __popc(hits));
+        if (WR == 1 && !((which >> k) & 1u)) hits = 0;
+        int place = 0;
+        if (hits) place = atomicAdd(&s_count[team], __popc(hits));
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          if ((hits >> j) & 1u) put(place++, j & 1 ? W::pair(y, j / 2).y : W::pair(y, j / 2).x, index + j);
+        for (int j = 0; j < N; ++j) {
+          const bool hit = (hits >> j) & 1u;
+          put(hit, place, j & 1 ? W::pair(y, j / 2).y : W::pair(y, j / 2).x, index + j);
+          place += hit;
+        }
       }
     });
-    if (edge >= 0 && ze >= reached) put(atomicAdd(&s_count, 1), ze, edge);
+    if (edge >= 0 && ze >= reached) put(true, atomicAdd(&s_count[team], 1), ze, edge);
     __syncwarp();
+    if constexpr (WR == 1) {
+      const int n = s_count[team];
+      if (n <= kLpPool) ranked(s_pool[team], n);
+      else search();                                 // (many equal ones, or many large ones in few lanes)
+    }
   }
   auto shuffled = [&](const Sums& x, int k) {
     return joined_sums(x, {__shfl_xor_sync(kAll, x.m, k), __shfl_xor_sync(kAll, x.s, k), __shfl_xor_sync(kAll, x.a, k)});
@@ -492,24 +544,6 @@ logprobs_kernel(LpArgs a, int* err) {
       }
       best = list[0][lane];
     };
-    // Up to kLpPool tokens in any order to one warp: each one's place is the number of larger ones. (Reading them all costs a
-    // third of joining eight lists, whose three steps wait for one another.)
-    auto ranked = [&](const Key* pool, int n) {
-      const Key x = lane < n ? pool[lane] : 0, y = lane + 32 < n ? pool[lane + 32] : 0;
-      int at_x = 0, at_y = 0;
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) {
-        const Key z = pool[k];
-        at_x += z > x;
-        at_y += z > y;
-      }
-      s_best[lane] = 0;
-      __syncwarp();
-      if (x && at_x < 32) s_best[at_x] = x;
-      if (y && at_y < 32) s_best[at_y] = y;
-      __syncwarp();
-      best = s_best[lane];
-    };
     auto join_sums = [&](const Sums* sums, int n) {
       sum = (lane & 7) < n ? sums[lane & 7] : Sums{kLowest, 0.0f, 0.0f};
 #pragma unroll
@@ -518,7 +552,7 @@ logprobs_kernel(LpArgs a, int* err) {
     if (lane == 0) s_sums[warp] = sum;
     __syncthreads();
     if (K) {
-      const int n = s_count;
+      const int n = s_count[0];
       if (n <= kLpPool) {
         if (warp == 0) ranked(s_pool[0], n);
       } else {                                       // (many equal ones, or many large ones in few threads)
@@ -637,7 +671,7 @@ logprobs_grad_kernel(LpGrad a) {
   }
 }
 
-template <typename T, int NC, int WR, bool FEW>
+template <typename T, int NC, int WR, bool FEW, bool TOP>
 cudaError_t launch_rows(const LpArgs& a, int* err, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(WR == 1 ? (a.M + kLpWarps - 1) / kLpWarps : a.M * NC));
@@ -650,12 +684,14 @@ cudaError_t launch_rows(const LpArgs& a, int* err, cudaStream_t s) {
   attr[1].val.clusterDim = {NC, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = NC > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NC, WR, FEW>, a, err);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NC, WR, FEW, TOP>, a, err);
 }
 
 template <typename T, int NC, int WR = kLpWarps>
 cudaError_t launch_form(const LpArgs& a, long long chunks, int* err, cudaStream_t s) {
-  return chunks <= 2 * NC * WR ? launch_rows<T, NC, WR, true>(a, err, s) : launch_rows<T, NC, WR, false>(a, err, s);
+  const bool few = chunks <= 2 * NC * WR;
+  if (WR == 1 && !a.K) return few ? launch_rows<T, NC, WR, true, WR != 1>(a, err, s) : launch_rows<T, NC, WR, false, WR != 1>(a, err, s);
+  return few ? launch_rows<T, NC, WR, true, true>(a, err, s) : launch_rows<T, NC, WR, false, true>(a, err, s);
 }
 
 template <typename T>
