@@ -10,12 +10,12 @@
 // are looked at again (out of L2, where they are not kept in registers), and what reaches it there goes into one pool of keys
 // (logit, then lowest index) in shared memory, in any order. A key's place is the number of larger ones, so the result does
 // not depend on that order. Where more tokens reach the floor than the pool holds (many equal ones), every warp keeps its best
-// 32 in order instead, one a lane, and the lists are joined. A warp that has a row to itself does so from the start. (Lists
-// kept up to date while the row went by took 8 to 16 instructions for every 32 logits, as many as the sums: 4,096 rows of
-// 50,257 with K = 8 took 151 us in fp32 and 124 in bf16; lists for every warp behind the sums 135 and 85.)
+// 32 in order instead, one a lane, and the lists are joined. (Lists kept up to date while the row went by took 8 to 16
+// instructions for every 32 logits, as many as the sums: 4,096 rows of 50,257 with K = 8 took 151 us in fp32 and 124 in bf16;
+// lists for every warp behind the sums 135 and 85.)
 //
-// Bound by memory where rows are many: 4,096 x 50,257 in fp32 123 us with K = 0, 6.7 TB/s, what a copy reaches, and 128 with
-// K = 8; in bf16 70 and 81, 5.9 TB/s, the exponentials' units and the sums' instructions close behind. The part after the
+// Bound by memory where rows are many: 4,096 x 50,257 in fp32 121 us with K = 0, 6.8 TB/s, what a copy reaches, and 129 with
+// K = 8; in bf16 69 and 81, 6.0 TB/s, the exponentials' units and the sums' instructions close behind. The part after the
 // sums reads little and lets the memory rest: that is what K adds. 16 rows with K = 5 4.6 us in a graph, 2.9 with K = 0.
 #include "common.cuh"
 #include "kernels.h"
@@ -188,8 +188,8 @@ struct Row {
 
 // A warp takes a row (WR = 1; eight rows a block), or a block's eight warps do (WR = 8), or those of a cluster of NC blocks: the
 // row's chunks go round the warps. FEW: no warp has more than two, which then stay in its registers and are not read again.
-// TOP: false where none of the most probable tokens are wanted (K = 0; of the forms with a warp a row, which it leaves a block
-// more an SM).
+// TOP: false where none of the most probable tokens are wanted (K = 0; not of the clusters). It takes fewer registers and no
+// shared memory for them: 4,096 x 50,257 121 and 124 us, 256 x 5,000 2.3 and 2.5, 4,096 x 5,000 14.8 and 16.7.
 template <typename T, int NC, int WR, bool FEW, bool TOP>
 __global__ void __launch_bounds__(kLpWarps * 32, NC > 1 ? 2 : WR == 1 && FEW && TOP ? 3 : 0)
 logprobs_kernel(LpArgs a, int* err) {
@@ -690,7 +690,7 @@ cudaError_t launch_rows(const LpArgs& a, int* err, cudaStream_t s) {
 template <typename T, int NC, int WR = kLpWarps>
 cudaError_t launch_form(const LpArgs& a, long long chunks, int* err, cudaStream_t s) {
   const bool few = chunks <= 2 * NC * WR;
-  if (WR == 1 && !a.K) return few ? launch_rows<T, NC, WR, true, WR != 1>(a, err, s) : launch_rows<T, NC, WR, false, WR != 1>(a, err, s);
+  if (NC == 1 && !a.K) return few ? launch_rows<T, NC, WR, true, NC != 1>(a, err, s) : launch_rows<T, NC, WR, false, NC != 1>(a, err, s);
   return few ? launch_rows<T, NC, WR, true, true>(a, err, s) : launch_rows<T, NC, WR, false, true>(a, err, s);
 }
 
@@ -702,9 +702,9 @@ cudaError_t launch_logprobs_of(LpArgs a, int* err, cudaStream_t s) {
   const long long chunks = (static_cast<long long>(a.V) / Vec<T>::N + kLpChunk - 1) / kLpChunk;
   a.ahead = 4 * sms;                                 // (four blocks an SM)
   // A warp a row where its whole row is two chunks, or the rows are short and many and not too many tokens are wanted: 4,096 x
-  // 500 with K = 5 6.2 us, a block a row 42; 4,096 x 5,000 22.3 and 30.3, with K = 16 28.9 and 32.6, but with K = 32 62 and 36;
-  // 1,500 x 8,000 17.1 and 14.8, 620 x 5,000 9.0 and 7.9 (graph replays). Clusters of as many blocks as keep all of them at
-  // work at once.
+  // 500 with K = 5 7.1 us, a block a row 42; 4,096 x 5,000 22.4 and 30.3, with K = 16 25.5 and 32.6, but with K = 32, where 32
+  // lanes' largest logits make a low floor, 62 and 35; 1,500 x 8,000 17.1 and 14.8, 620 x 5,000 9.0 and 7.9 (graph replays).
+  // Clusters of as many blocks as keep all of them at work at once.
   if (chunks <= 2 || (chunks <= 10 && a.M >= 8LL * sms && a.K <= kLpFewTop)) {
     a.ahead *= kLpWarps;
     return launch_form<T, 1, 1>(a, chunks, err, s);
