@@ -208,3 +208,38 @@ def test_a_cache_of_more_than_four_gigabytes(gpt_lib):
     c.d_table = dev_i32(c.table + (pages - n))
     c.call()
     c.check()
+
+
+def test_a_large_cache_in_the_joined_form(gpt_lib):
+    # the same where the table has room for more rows than a cluster takes
+    c = Case(2, 2, 64, 256, [700], seed=8, rows=65536)
+    pages = (5 << 30) // (2 * 2 * 256 * 32)
+    codes = torch.zeros(pages, 2, 2, 256, 32, dtype=torch.uint8, device="cuda")
+    ranges = torch.zeros(pages, 2, 2, 256, 2, dtype=torch.bfloat16, device="cuda")
+    n = c.codes.shape[0]
+    c.device()
+    codes[pages - n:] = c.d_codes
+    ranges[pages - n:] = c.d_ranges
+    c.d_codes, c.d_ranges = codes, ranges
+    c.d_table = dev_i32(c.table + (pages - n))
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("H,Hkv,D,page,lens", [
+    (2, 1, 64, 64, [170000]),                           # a list of more pieces than a large block joins at once
+    (3, 1, 32, 256, [90000, 0, 70001]),
+    (24, 2, 64, 16, [6000, 6001, 5, 6200, -1, 3000, 6100]),   # more heads than a large block each takes
+    (20, 1, 64, 32, [20000, 333]),                      # two groups of heads on one key head
+])
+def test_lists_of_many_pieces(gpt_lib, H, Hkv, D, page, lens):
+    Case(H, Hkv, D, page, lens, seed=len(lens), rows=65536).run()
+
+
+@pytest.mark.parametrize("rows", FORMS)
+@pytest.mark.parametrize("scale", [1e-30, 1e-3])
+def test_small_queries(gpt_lib, rows, scale):
+    c = Case(9, 3, 64, 16, [500, 70], seed=12, rows=rows, q_scale=scale)
+    c.x[:, ::7] *= 2.0 ** -20                          # beside them much smaller values
+    c.x = torch.from_numpy(c.x).bfloat16().float().numpy()
+    c.run()
