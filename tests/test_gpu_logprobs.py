@@ -420,3 +420,31 @@ def test_offsets_past_32_bits(gpt_lib):
     lse = float(torch.logsumexp(z.double(), -1))
     # V / 2048 sums one after another in a lane of the eight blocks: 2^-24 each
     assert abs(float(lp) - (9.0 - lse)) <= 2.0 ** -24 * V / 1024 and abs(float(top[0, 0]) - (11.0 - lse)) <= 2.0 ** -24 * V / 1024
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,V", [(1, 50257), (16, 50257), (60, 20011), (400, 9001), (1300, 3001), (300, 700)])
+def test_one_result_bit_for_bit(gpt_lib, dtype, M, V):
+    # whatever order the tokens come in, alone and beside another call
+    from decoder_only_transformer_gpt_gb300 import binding
+    z = torch.from_numpy(logits(8, V, V)).to(dtype).cuda()[torch.arange(M) % 8].contiguous()
+    z[::3, ::11] = 1.5                                  # a few hundred equal ones at most
+    t = dev_i32(np.arange(M) % V)
+    side = torch.cuda.Stream()
+    for K in (1, 5, 16, 32):
+        out = []
+        for i in range(12):
+            d = [torch.empty(M, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, 2, device="cuda"),
+                 torch.empty(M, K, dtype=torch.int32, device="cuda"), torch.empty(M, K, device="cuda")]
+            torch.cuda.synchronize()
+            if i % 2:
+                with torch.cuda.stream(side):
+                    other = [x.clone() for x in d]
+                    binding.logprobs(z, t, other[0], entropy=other[1], stats=other[2], top_ids=other[3], top_logp=other[4])
+            binding.logprobs(z, t, d[0], entropy=d[1], stats=d[2], top_ids=d[3], top_logp=d[4])
+            torch.cuda.synchronize()
+            out.append(d)
+            if i % 2:
+                out.append(other)
+        for d in out[1:]:
+            assert all(torch.equal(x, y) for x, y in zip(d, out[0]))
