@@ -317,7 +317,8 @@ logprobs_kernel(LpArgs a, int* err) {
     if (NC == 1 && !FEW && lane < 4 && m + a.ahead < a.M) {
       const Row<T> later(a.z, a.ld, a.V, m + a.ahead);
       const int c = first + lane * step;
-      if (c < later.nvec / kLpChunk) prefetch_l2(reinterpret_cast<const uint4*>(later.z + later.head) + static_cast<long long>(c) * kLpChunk, kLpChunk * 16);
+      const uint4* chunk = reinterpret_cast<const uint4*>(later.z + later.head) + static_cast<long long>(c) * kLpChunk;
+      if (c < later.nvec / kLpChunk) prefetch_l2(chunk, kLpChunk * 16);
     }
     if (!FEW && in_group) {
       s_max[group++][threadIdx.x] = noted;
@@ -596,8 +597,9 @@ logprobs_kernel(LpArgs a, int* err) {
 }
 
 // dz = dlogp (1[j = t] - p) - dentropy p (ln p + entropy), from (m, S): p = e^d / S. Bound by memory: the logits once in,
-// once out. A block takes 256 x kGradVecs vectors of a row. The last rows come first: they are what the call that made (m, S)
-// has left in L2 (4,096 x 50,257 in bf16, both calls: 198 us, in the other order 202; with streaming loads or stores more).
+// once out. A block takes 256 x kGradVecs vectors of a row, two values to an instruction (4,096 x 50,257 in bf16, both calls
+// 193 us, one to an instruction 197; eight vectors a thread 192). The last rows come first: they are what the call that made
+// (m, S) has left in L2 (the other order took 4 us more; streaming loads or stores 5 to 10).
 constexpr int kGradVecs = 4;
 
 struct LpGrad {
@@ -632,11 +634,14 @@ logprobs_grad_kernel(LpGrad a) {
     int t = a.targets ? __ldg(a.targets + m) : -1;
     if (static_cast<unsigned>(t) >= static_cast<unsigned>(a.V)) t = -1;
     const float g = t >= 0 && a.dlogp ? __ldg(a.dlogp + m) : 0.0f;
-    // dz = p (c - ge d) with c = -g - ge (entropy - ln S), p = e^d / S
-    const float inv = 1.0f / st.y, c = -g - ge * (h - logf(st.y));
-    auto grad = [&](float z) {
-      const float d = z - st.x;
-      return ex2_approx(d * kL2E) * inv * (c - ge * fmaxf(d, kFar));
+    // dz = e^d (c - ge d) / S with c = -g - ge (entropy - ln S); 1 / S goes into both factors of the row
+    const float inv = 1.0f / st.y, c = (-g - ge * (h - logf(st.y))) * inv;
+    const float2 off = make_float2(-st.x, -st.x), l2e = make_float2(kL2E, kL2E);
+    const float2 slope = make_float2(-ge * inv, -ge * inv), base = make_float2(c, c);
+    auto grad = [&](const float2& z) {
+      const float2 d = add2_rn(z, off), x = mul2_rn(d, l2e);
+      return mul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)),
+                     fma2_rn(make_float2(fmaxf(d.x, kFar), fmaxf(d.y, kFar)), slope, base));
     };
     const bool same = ((reinterpret_cast<uintptr_t>(row.z) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
 #pragma unroll
@@ -647,9 +652,9 @@ logprobs_grad_kernel(LpGrad a) {
       float x[N];
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) {
-        const float2 p = W::pair(v[k], j);
-        x[2 * j] = grad(p.x);
-        x[2 * j + 1] = grad(p.y);
+        const float2 dz = grad(W::pair(v[k], j));
+        x[2 * j] = dz.x;
+        x[2 * j + 1] = dz.y;
       }
       if (static_cast<unsigned>(t - index) < static_cast<unsigned>(N) && t >= 0) {
 #pragma unroll
@@ -666,7 +671,10 @@ logprobs_grad_kernel(LpGrad a) {
     if (seg == 0 && threadIdx.x < 32) {              // the values before and behind the vectors
       const int lane = threadIdx.x, tail = row.head + row.nvec * N;
       const int index = lane < 16 ? (lane < row.head ? lane : -1) : (tail + lane - 16 < a.V ? tail + lane - 16 : -1);
-      if (index >= 0) W::put(out + index, grad(W::get(row.z + index)) + (index == t ? g : 0.0f));
+      if (index >= 0) {
+        const float z = W::get(row.z + index);
+        W::put(out + index, grad(make_float2(z, z)).x + (index == t ? g : 0.0f));
+      }
     }
   }
 }

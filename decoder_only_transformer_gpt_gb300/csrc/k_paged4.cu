@@ -43,7 +43,8 @@ constexpr unsigned kAll = 0xffffffffu;
 //    operands of four products), and of value rows the same byte column of four rows, two of which are interleaved by one
 //    byte permutation into eight operands. The cached rows, and the values, are the 16 rows of a product, the heads its eight
 //    columns, so that one key head for each query head wastes half as much as with the heads as rows; the probabilities are
-//    turned over by movmatrix.
+//    turned over by movmatrix. (tcgen05 takes its operands from shared memory: codes would have to be written there again as 16
+//    bits, four times their bytes, for products of 128 rows of which one to sixteen are heads.)
 //  * A row's scales and lowest values are made into fp32 factors once, by the lane of its number.
 //  * Units are whole tiles of the sequence, so every eight rows of one lie in one page and start on a 16-byte boundary: the
 //    tile's pages, one to a lane, are looked up once and counted in blocks of eight rows, and every lane copies 16 bytes at a
@@ -833,7 +834,8 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const int guess = (rank * upw * 8 + warp) * UNIT;
   int page = __ldg(trow + min((guess + lane) >> c.page_log2, c.max_pages - 1));
   Segment<D, QR> g;
-  g.start(w.scale_log2, gn, lane, [&](int r, int u) { return __ldg(reinterpret_cast<const uint4*>(tok + static_cast<size_t>(r) * D) + u); });
+  g.start(w.scale_log2, gn, lane,
+          [&](int r, int u) { return __ldg(reinterpret_cast<const uint4*>(tok + static_cast<size_t>(r) * D) + u); });
   const int n = rows_of(c, w, len);
   if (n <= 0) {                                      // (the same for the whole cluster)
     if (n == -2 && rank == 0 && tid == 0) record_error(err, GPT_DEV_EPAGE);
@@ -888,7 +890,8 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     const bool is_seen = there && (w.window == 0 || mine >= n - w.window || mine < w.sinks);
     uint32_t kr = 0u, vr = 0u;                       // row `lane`'s ranges
     if (is_seen) {
-      const size_t row = static_cast<size_t>(static_cast<uint32_t>(page)) * prows + (static_cast<size_t>(kh) << c.page_log2) + (mine & pmask);
+      const size_t row = static_cast<size_t>(static_cast<uint32_t>(page)) * prows + (static_cast<size_t>(kh) << c.page_log2) +
+                         (mine & pmask);
       kr = __ldg(ranges + row);
       vr = __ldg(ranges + row + vrows);
     }

@@ -307,7 +307,8 @@ struct Logits {
   int64_t rows(Device& d, PyObject* o, const char* name) {
     const at::Tensor& t = tensor(o, name);
     const int64_t shape[2] = {M, V};
-    if (t.scalar_type() != type || t.sizes() != at::IntArrayRef(shape) || !d.holds(t)) Device::refuse_tensor(o, name, t, type, shape, false);
+    if (t.scalar_type() != type || t.sizes() != at::IntArrayRef(shape) || !d.holds(t))
+      Device::refuse_tensor(o, name, t, type, shape, false);
     if ((t.stride(1) != 1 && V > 1) || (t.stride(0) < V && M > 1))
       refuse(std::string(name) + ": strides " + shape_text(t.strides()) + ", needs rows of contiguous values");
     p = t.data_ptr();
