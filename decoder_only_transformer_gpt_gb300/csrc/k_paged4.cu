@@ -12,9 +12,11 @@
 // register takes its own shift, and a code comes out as 16 + code: taking the 16 back from the finished sums left the outputs
 // of 20,000 rows 1.8e-3 of their norm off, where their own rounding makes 1.6e-3.)
 // fp16 has few exponents: queries enter it times a power of two, exactly (largest value in [2^14, 2^15); what is below 2^-34
-// of that is lost), and p_r scale_r times 2^(15 - E) with 2^E above every scale and lowest value of the rows so far: 11
-// bits (2^-12 of a term is lost; one bf16 part would lose 2^-9, as much as the output's own rounding), and whole multiples of
-// 2^-39 of 2^E for the smallest.
+// of that is lost), and p_r scale_r times 2^(15 - E), where 2^E is above every such term of its head so far, at the present
+// reference of the softmax, and at most 2^9 times the largest: 11 bits (2^-12 of a term is lost; one bf16 part would lose 2^-9,
+// as much as the output's own rounding), and whole multiples of 2^-30 of the largest term for the smallest. (With 2^E above the
+// rows' scales instead, whatever their weight, one row of no weight but 2^36 times the others' size left nothing of their codes.)
+// References of the softmax are whole numbers, so that raising one rescales the sums exactly.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -62,7 +64,9 @@ struct Dec4Cfg {
   static constexpr int FACTORS = 2 * STAGE;                      // the rows' factors: behind two stages
   // one head a key head: its scores of 64 rows, its factors as fp16, zeros for the products' other columns
   static constexpr int WARP = FACTORS + (QR == 1 ? 256 + 128 + 32 : UNIT * 16);
-  static constexpr int WARPS = 16;
+  // more than eight heads: with 16 warps their registers spill (16 x 9,000 to 32,000 rows, 48 heads on 4, 48.0 us, with 12 45.6;
+  // one sequence of 200,000, 12 on one, 30.0 and 25.0)
+  static constexpr int WARPS = QR == 16 ? 12 : 16;
 };
 
 struct Dec4Scratch {
@@ -267,6 +271,11 @@ __device__ __forceinline__ void add_codes(float (&o)[NQ][D / 16][4], float (&eig
   }
 }
 
+// A head's terms, probabilities times their rows' scales, enter the products times 2^(15 - E), kLeast <= E. E is set anew where a
+// term may pass it, kRoom above what that takes, so that rows of ordinary sizes rarely do, and where the reference has risen by more
+// than kSlack since, which has made all earlier terms smaller: 2^E is at most 2^(1 + kRoom + kSlack) times the largest term.
+constexpr int kLeast = -111, kRoom = 4, kSlack = 4;
+
 // What a warp holds of a segment: up to QR heads of one key head. Lane 4 n + q has heads 8 i + 2 q and the next, and of every
 // lane's rows its own share of the sums l and off; with one head (QR = 1) all lanes have rows of it.
 template <int D, int QR>
@@ -274,21 +283,23 @@ struct Segment {
   static constexpr int NQ = (QR + 7) / 8, NT = D / 16;
   static constexpr bool ONE = QR == 1;
   Queries<D> qs[NQ];
-  float o[NQ][NT][4];                                // times 2^(15 - e)
-  float m[NQ][2], l[NQ][2], off[NQ][2];
-  int e;                                             // 2^e is above every scale and lowest value of the rows so far
-  float into;                                        // 2^(15 - e)
+  float o[NQ][NT][4];                                // times `into`, as off is
+  float m[NQ][2], l[NQ][2], off[NQ][2];              // m: the reference, a whole number
+  float into[NQ][2];                                 // 2^(15 - E): 2^E is above every term of the head, at m
+  float due[NQ][2];                                  // the reference above which E has to be set anew
+  float most;                                        // the largest of all heads' 2^(15 - E)
 
   template <typename Load>
   __device__ __forceinline__ void start(float scale_log2, int gn, int lane, Load&& load) {
-    e = -111;
-    into = exp2_of(15 - e);
+    most = exp2_of(15 - kLeast);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         m[i][k] = -INFINITY;
         l[i][k] = off[i][k] = 0.0f;
+        into[i][k] = exp2_of(15 - kLeast);
+        due[i][k] = -INFINITY;
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -302,23 +313,41 @@ struct Segment {
     }
   }
 
-  // Makes room for rows with scales and lowest values of this size (rarely: then 2^e grows, and o and off with it).
-  __device__ __forceinline__ void fit(float size) {
-    if (!__any_sync(kAll, size * into >= 32768.0f)) return;
-    const uint32_t top = __reduce_max_sync(kAll, __float_as_uint(size) & 0x7fffffffu);
-    const int up = min(exponent_of(__uint_as_float(top)) + 1, 128);
-    const float less = up - e > 126 ? 0.0f : exp2_of(e - up);
-    e = up;
-    into = exp2_of(15 - e);
+  __device__ __forceinline__ float reference(int i, int k) const {
+    return m[i][k] == -INFINITY ? 0.0f : m[i][k];    // every score so far -inf: every term is 2^-inf
+  }
+  __device__ __forceinline__ void multiply(int i, int k, float a) {
+    off[i][k] *= a;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      off[i][0] *= less;
-      off[i][1] *= less;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][j][k] *= less;
+    for (int j = 0; j < NT; ++j) {
+      o[i][j][k] *= a;
+      o[i][j][2 + k] *= a;
     }
+  }
+  // Raises a head's reference for a largest score of mx. True: its E has to be set anew.
+  __device__ __forceinline__ bool raise(int i, int k, float mx) {
+    const float before = m[i][k];
+    m[i][k] = fmaxf(before, ceilf(mx));
+    const float a = exp2_of(-static_cast<int>(fminf(reference(i, k) - before, 127.0f)));
+    l[i][k] *= a;
+    multiply(i, k, a);
+    return m[i][k] > due[i][k];
+  }
+  // Sets a head's E anew, where the unit's largest term is t.
+  __device__ __forceinline__ void fit(int i, int k, float t) {
+    const int e = 15 - exponent_of(into[i][k]), need = exponent_of(t);
+    const int risen = static_cast<int>(fminf(fmaxf(m[i][k] - due[i][k] + kSlack, 0.0f), 100.0f));
+    int up = max(e - risen, kLeast);
+    if (need >= up) up = need + 1 + kRoom;
+    multiply(i, k, exp2_of(max(e - up, -127)));
+    into[i][k] = exp2_of(15 - up);
+    due[i][k] = m[i][k] + kSlack;
+  }
+  __device__ __forceinline__ void fitted() {
+    float x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) x = fmax3(x, into[i][0], into[i][1]);
+    most = warp_max(x);
   }
 
   // Adds a unit's -8 sum P to its sums of code P.
@@ -332,10 +361,10 @@ struct Segment {
   }
 
   // Scores of the tiles into probabilities times the rows' scales. factors: shared address of the rows' (key scale, key
-  // lowest, value scale 2^(15 - e), (value lowest + 8 value scale) 2^(15 - e)).
+  // lowest, value scale, value lowest + 8 value scale); large: one of the latter may pass a head's 2^E.
   template <int NJ>
   __device__ __forceinline__ void weigh(float (&s)[NQ][NJ][4], uint32_t factors, const uint32_t (&seen)[NJ / 2],
-                                        uint32_t unseen, int lane) {
+                                        uint32_t unseen, bool large, int lane) {
     const int n8 = lane >> 2;
     float2 vf[2 * NJ];                               // the value rows' factors, of rows 8 r + row_in_eight(n8)
 #pragma unroll
@@ -365,37 +394,48 @@ struct Segment {
         float x = s[i][0][k];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) x = j ? fmax3(x, s[i][j][k], s[i][j][2 + k]) : fmaxf(x, s[i][j][2 + k]);
-        x *= qs[i].c[k];
+        x = __fmul_ru(x, qs[i].c[k]);                // (upwards: no exponent below is above 0)
         x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
         x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
-        mx[k] = fmaxf(x, m[i][k]);
-        ref[k] = mx[k] == -INFINITY ? 0.0f : mx[k];  // every score so far -inf: every term is 2^-inf
+        mx[k] = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
       }
-      if (__any_sync(kAll, mx[0] > m[i][0] || mx[1] > m[i][1])) {   // a new maximum
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float a = ex2_approx(m[i][k] - ref[k]);
-          m[i][k] = mx[k];
-          l[i][k] *= a;
-          off[i][k] *= a;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[i][j][k] *= a;
-            o[i][j][2 + k] *= a;
-          }
-        }
+      bool anew = large;
+      if (__any_sync(kAll, mx[0] > m[i][0] || mx[1] > m[i][1])) {   // a higher reference
+        const bool x = raise(i, 0, mx[0]), y = raise(i, 1, mx[1]);
+        anew = __any_sync(kAll, large || x || y);
       }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) ref[k] = reference(i, k);
 #pragma unroll
       for (int r = 0; r < 2 * NJ; ++r)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float& x = s[i][r >> 1][2 * (r & 1) + k];
-          const float p = ex2_approx(fmaf(x, qs[i].c[k], -ref[k]));
-          l[i][k] += p;
-          off[i][k] = fmaf(p, vf[r].y, off[i][k]);
-          x = p * vf[r].x;
+          x = ex2_approx(fmaf(x, qs[i].c[k], -ref[k]));
+          l[i][k] += x;
         }
+      if (anew) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float t = 0.0f;
+#pragma unroll
+          for (int r = 0; r < 2 * NJ; ++r) t = fmaxf(t, s[i][r >> 1][2 * (r & 1) + k] * fmaxf(vf[r].x, fabsf(vf[r].y)));
+          t = fmaxf(t, __shfl_xor_sync(kAll, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(kAll, t, 8));
+          fit(i, k, fmaxf(t, __shfl_xor_sync(kAll, t, 16)));
+        }
+        fitted();
+      }
+#pragma unroll
+      for (int r = 0; r < 2 * NJ; ++r) {
+        float* x = &s[i][r >> 1][2 * (r & 1)];
+        const float2 p = mul2_rn(make_float2(x[0], x[1]), make_float2(into[i][0], into[i][1]));
+        off[i][0] = fmaf(p.x, vf[r].y, off[i][0]);
+        off[i][1] = fmaf(p.y, vf[r].y, off[i][1]);
+        const float2 t = mul2_rn(p, make_float2(vf[r].x, vf[r].x));
+        x[0] = t.x;
+        x[1] = t.y;
+      }
     }
   }
 
@@ -404,7 +444,7 @@ struct Segment {
   template <int NH, int NJ>
   __device__ __forceinline__ void weigh_one(const float (&s)[1][NJ][4], float (&x)[NH], uint32_t room,
                                             const float (&ks)[NH], const float (&kl)[NH], const float (&vs)[NH],
-                                            const float (&vl)[NH], const uint32_t (&seen)[NH], uint32_t unseen, int lane) {
+                                            const float (&vl)[NH], const uint32_t (&seen)[NH], uint32_t unseen, bool large, int lane) {
     if ((lane & 3) == 0) {
 #pragma unroll
       for (int h = 0; h < NH; ++h)
@@ -420,24 +460,25 @@ struct Segment {
       if (unseen && !((seen[h] >> lane) & 1u)) x[h] = -INFINITY;
       mx = fmaxf(mx, x[h]);
     }
-    mx *= qs[0].c[0];
-    mx = fmaxf(warp_max(mx), m[0][0]);
-    const float ref = mx == -INFINITY ? 0.0f : mx;   // every score so far -inf: every term is 2^-inf
-    if (mx > m[0][0]) {                              // a new maximum (the same for all lanes)
-      const float a = ex2_approx(m[0][0] - ref);
-      m[0][0] = mx;
-      l[0][0] *= a;
-      off[0][0] *= a;
+    mx = warp_max(__fmul_ru(mx, qs[0].c[0]));        // (upwards: no exponent below is above 0)
+    bool anew = large;
+    if (mx > m[0][0]) anew = raise(0, 0, mx) || large;   // a higher reference (the same for all lanes)
+    const float ref = reference(0, 0);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        o[0][j][0] *= a;
-        o[0][j][2] *= a;
-      }
+    for (int h = 0; h < NH; ++h) {
+      x[h] = ex2_approx(fmaf(x[h], qs[0].c[0], -ref));
+      l[0][0] += x[h];
+    }
+    if (anew) {
+      float t = 0.0f;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) t = fmaxf(t, x[h] * fmaxf(vs[h], fabsf(vl[h])));
+      fit(0, 0, warp_max(t));
+      most = into[0][0];
     }
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      const float p = ex2_approx(fmaf(x[h], qs[0].c[0], -ref));
-      l[0][0] += p;
+      const float p = x[h] * into[0][0];
       off[0][0] = fmaf(p, vl[h], off[0][0]);
       x[h] = p * vs[h];
     }
@@ -451,7 +492,8 @@ struct Segment {
       lt += __shfl_xor_sync(kAll, lt, x);
       ot += __shfl_xor_sync(kAll, ot, x);
     }
-    const float back = exp2_of((e - 15) / 2), rest = exp2_of(e - 15 - (e - 15) / 2);   // 2^(e - 15) in two steps
+    const int e = -exponent_of(into[i][k]);
+    const float back = exp2_of(e / 2), rest = exp2_of(e - e / 2);   // 1 / into in two steps
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       v[2 * j] = fmaf(o[i][j][k], 16777216.0f, ot) * back * rest;   // 2^24 and 2^20
@@ -670,10 +712,9 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
                 [&](int r, int u) { return lds128(st + Cfg::QUERIES + (r * (D / 8) + u) * 16); });
       const int f = first_row<UNIT>(at.t, tile), after = at.t.n - w.window;   // the window's first row
       uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
-      float ks[NH], kl[NH], vs[NH], vl[NH];            // the factors of rows `lane` and, of a unit of 64, 32 + lane
+      float ks[NH], kl[NH], vs[NH], vl[NH], size = 0.0f;   // the factors of rows `lane` and, of a unit of 64, 32 + lane
       {
         const bool cut = f + UNIT > at.t.n || (w.window > 0 && f < after && f + UNIT > w.sinks);
-        float size = 0.0f;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const uint32_t kr = lds32(st + Cfg::RANGES + 4 * (32 * h + lane));
@@ -689,17 +730,12 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
           ks[h] = scale_of(kr) * 16777216.0f;
           kl[h] = low_of(kr);
           vs[h] = scale_of(vr);
-          vl[h] = low_of(vr);
+          vl[h] = fmaf(8.0f, vs[h], low_of(vr));
           size = fmax3(size, vs[h], fabsf(vl[h]));
-        }
-        g.fit(size);
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          vl[h] = fmaf(8.0f, vs[h], vl[h]) * g.into;
-          vs[h] *= g.into;
           if constexpr (!ONE) sts128f(factors + 16 * (32 * h + lane), ks[h], kl[h], vs[h], vl[h]);
         }
       }
+      const bool large = __any_sync(kAll, size * g.most >= 32768.0f);
       float s[NQ][NJ][4], eights[NQ][4];
       const uint32_t krow = st + row_in_eight(n8) * ROWB + q4 * (D / 8), vcol = st + Cfg::TILE + q4 * ROWB + n8 * (D / 16);
 #pragma unroll
@@ -726,7 +762,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       };
       if constexpr (ONE) {
         float x[NH];
-        g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, unseen, lane);
+        g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, unseen, large, lane);
         const uint32_t weights = factors + 256;
 #pragma unroll
         for (int h = 0; h < NH; ++h) sts16(weights + weight_place<2 * NJ>(32 * h + lane), x[h]);
@@ -746,7 +782,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         }
       } else {
         __syncwarp();
-        g.weigh(s, factors, seen, unseen, lane);
+        g.weigh(s, factors, seen, unseen, large, lane);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           uint32_t p[NQ][2], u[4];
@@ -896,10 +932,9 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       vr = __ldg(ranges + row + vrows);
     }
     const uint32_t seen[1] = {__ballot_sync(kAll, is_seen)};
-    float ks[1] = {scale_of(kr) * 16777216.0f}, kl[1] = {low_of(kr)}, vs[1] = {scale_of(vr)}, vl[1] = {low_of(vr)};
-    g.fit(fmaxf(vs[0], fabsf(vl[0])));
-    vl[0] = fmaf(8.0f, vs[0], vl[0]) * g.into;
-    vs[0] *= g.into;
+    float ks[1] = {scale_of(kr) * 16777216.0f}, kl[1] = {low_of(kr)}, vs[1] = {scale_of(vr)};
+    float vl[1] = {fmaf(8.0f, vs[0], low_of(vr))};
+    const bool large = __any_sync(kAll, fmaxf(vs[0], fabsf(vl[0])) * g.most >= 32768.0f);
     float s[NQ][2][4], eights[NQ][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -914,7 +949,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     uint32_t p[2][NQ][2];
     if constexpr (ONE) {
       float x[1];
-      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, ~seen[0], lane);
+      g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, ~seen[0], large, lane);
       sts16(factors + 128 + weight_place<4>(lane), x[0]);
       __syncwarp();
       const uint4 w4 = lds128(factors + 128 + (n8 == 0 ? 16 * q4 : 64));   // other columns: zeros
@@ -925,7 +960,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     } else {
       sts128f(factors + 16 * lane, ks[0], kl[0], vs[0], vl[0]);
       __syncwarp();
-      g.weigh(s, factors, seen, ~seen[0], lane);
+      g.weigh(s, factors, seen, ~seen[0], large, lane);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
