@@ -23,9 +23,9 @@ def test_whole_sequences_and_windows():
     x, codes, ranges, table = case(4, 2, 32, 6, 0)
     for n, window, sinks in ((45, 0, 0), (45, 7, 2), (1, 0, 0), (0, 0, 0)):
         seen = [r for r in range(n) if not window or n - 1 - r < window or r < sinks]
-        y, lse2, ey, el = ref.attend_rows(x, codes, ranges, table, [seen], 4)
-        y2, lse3, ey2, _ = serving_ref.attend4(x, codes, ranges, table, [n], 4, window, sinks)
-        assert np.array_equal(y, y2) and np.array_equal(lse2, lse3) and (ey <= ey2).all()
+        y, lse2, _, _ = ref.attend_rows(x, codes, ranges, table, [seen], 4)
+        y2, lse3, _, _ = serving_ref.attend4(x, codes, ranges, table, [n], 4, window, sinks)
+        assert np.array_equal(y, y2) and np.array_equal(lse2, lse3)
 
 
 def test_the_bounds_do_not_hold_where_a_row_without_weight_sets_the_unit():
