@@ -13,10 +13,12 @@
 // of 20,000 rows 1.8e-3 of their norm off, where their own rounding makes 1.6e-3.)
 // fp16 has few exponents: queries enter it times a power of two, exactly (largest value in [2^14, 2^15); what is below 2^-34
 // of that is lost), and p_r scale_r times 2^(15 - E), where 2^E is above every such term of its head so far, at the present
-// reference of the softmax, and at most 2^9 times the largest: 11 bits (2^-12 of a term is lost; one bf16 part would lose 2^-9,
-// as much as the output's own rounding), and whole multiples of 2^-30 of the largest term for the smallest. (With 2^E above the
-// rows' scales instead, whatever their weight, one row of no weight but 2^36 times the others' size left nothing of their codes.)
-// References of the softmax are whole numbers, so that raising one rescales the sums exactly.
+// reference of the softmax, and at most 2^9 times the largest. (With 2^E above the rows' scales instead, whatever their weight, one
+// row of no weight but 2^36 times the others' size left nothing of their codes.) They enter in two parts, what fp16 holds of
+// them and what it holds of the rest: 2^-20 of a term is lost, and 2^-30 of the largest for each part of the smallest. One part
+// alone loses 2^-12 and is less work: 28.6 us with 8 heads on each of 4 key heads below, 44.8 with 12; but the 16-bit
+// cache's attention holds them in two parts as well. References of the softmax are whole numbers, so that raising one rescales the
+// sums exactly.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -35,9 +37,9 @@ constexpr unsigned kAll = 0xffffffffu;
 // Bound by memory once all warps are under way (8 sequences of 20,000 rows more take 19.3 us, 7.2 TB/s), with about 540
 // instructions for 64 rows of a key head close behind: a byte of codes takes a warp twice the unpacking and products of a byte
 // of bf16, and the integer unit takes a warp's instruction only every other cycle. Measured: 16 sequences of 9,000 to 32,000
-// rows x 12 heads 53.2 us, 5.3 TB/s, of which the first rows' chain of loads and the last units take 8 and the join 5; the rows
-// of a 16-bit cache take 160. With 8 query heads on each of 4 key heads 29.9, with 12 46. Work is dealt as in the 16-bit
-// cache's kernel (k_paged.cu):
+// rows x 12 heads 55.7 us (graph replays), 5.1 TB/s, of which the first rows' chain of loads and the last units take 8 and the
+// join 5; the rows of a 16-bit cache take 160. With 4 query heads on each of 4 key heads 28.5, with 8 31.2, with 12 50.8, whose
+// instructions bound them. Work is dealt as in the 16-bit cache's kernel (k_paged.cu):
 // units of 64 rows (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal
 // contiguous ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
@@ -62,10 +64,10 @@ struct Dec4Cfg {
   static constexpr int QUERIES = RANGES + UNIT * 8;               // offset of the query rows (where a unit starts a segment)
   static constexpr int STAGE = QUERIES + QR * D * 2;
   static constexpr int FACTORS = 2 * STAGE;                      // the rows' factors: behind two stages
-  // one head a key head: its scores of 64 rows, its factors as fp16, zeros for the products' other columns
-  static constexpr int WARP = FACTORS + (QR == 1 ? 256 + 128 + 32 : UNIT * 16);
-  // more than eight heads: with 16 warps their registers spill (16 x 9,000 to 32,000 rows, 48 heads on 4, 48.0 us, with 12 45.6;
-  // one sequence of 200,000, 12 on one, 30.0 and 25.0)
+  // one head a key head: its scores of 64 rows, their weights in two fp16 parts, zeros for the products' other columns
+  static constexpr int WARP = FACTORS + (QR == 1 ? 256 + 2 * 128 + 32 : UNIT * 16);
+  // more than eight heads: with 16 warps their registers spill (16 x 9,000 to 32,000 rows, 48 heads on 4, 53.6 us, with 12 50.8;
+  // one sequence of 200,000, 12 on one, 31.4 and 26.2)
   static constexpr int WARPS = QR == 16 ? 12 : 16;
 };
 
@@ -131,12 +133,26 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void sts16(uint32_t a, float x) {   // as fp16
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(__half_as_ushort(__float2half_rn(x))) : "memory");
+__device__ __forceinline__ void sts16(uint32_t a, float x) {   // as fp16, cut off
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(__half_as_ushort(__float2half_rz(x))) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t cut_half2(float lo, float hi) {
+  uint32_t v;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+// What fp16 cuts off a number (below 2^-14 less than that); mask 0: the number itself.
+constexpr uint32_t kHalfBits = 0xffffe000u;
+__device__ __forceinline__ float rest_of(float x) { return x - __uint_as_float(__float_as_uint(x) & kHalfBits); }
+// The same of two, as fp16.
+__device__ __forceinline__ uint32_t cut_rest2(float lo, float hi, uint32_t mask) {
+  const float2 r = add2_rn(make_float2(lo, hi), make_float2(__uint_as_float((__float_as_uint(lo) & mask) ^ 0x80000000u),
+                                                            __uint_as_float((__float_as_uint(hi) & mask) ^ 0x80000000u)));
+  return cut_half2(r.x, r.y);
 }
 
 // An 8 x 8 matrix of 16-bit numbers, a row of pairs to four lanes, transposed.
@@ -169,25 +185,27 @@ __device__ __forceinline__ int rows_of(const PagedCache& c, const Dec4Shape& w, 
 
 // A unit's products have the cached rows, or the value columns, as the 16 rows of their first operand, and eight query heads
 // as the columns (twice for 9 to 16 heads): lane 4 n + q holds, of every tile of scores, rows n and n + 8 under heads 2 q and
-// 2 q + 1. Row n of a tile is row 4 (n % 2) + n / 2 of its eight rows in the cache.
+// 2 q + 1. Row n of a tile is row 4 (n % 2) + n / 2 of its eight rows in the cache. Up to four heads stand in the columns twice, so
+// that the products with the values take the first parts of their weights and the second ones at once (QR = 4).
 __device__ __forceinline__ int row_in_eight(int n) { return (n & 1) * 4 + (n >> 1); }
 
 // Eight heads' queries as second operands, times 2^(14 - e) for 2^e <= the head's largest value < 2^(e + 1). from: what the
 // score products start with, 8 times the sums of heads 2 q and 2 q + 1; sum: these sums; c: the factors from a product to the
 // softmax's base-2 exponent. load(row, i): values 8 i .. of one of the gn heads (none where
-// gn <= 0); zeros behind them.
+// gn <= 0); zeros behind them. TWICE: heads 0 to 3 are heads 4 to 7 too.
 template <int D>
 struct Queries {
   uint32_t f[D / 16][2];
   float sum[2], c[2];
-  template <typename Load>
+  template <bool TWICE, typename Load>
   __device__ __forceinline__ void take(float scale_log2, int gn, int lane, Load&& load) {
     constexpr int C = D / 4;                         // values of a lane: its codes' places
+    const int head = TWICE ? (lane >> 2) & 3 : lane >> 2;
     float v[C], top = 0.0f, mine = 0.0f;
 #pragma unroll
     for (int w = 0; w < C / 8; ++w) {
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if ((lane >> 2) < gn) x = load(lane >> 2, (lane & 3) * (C / 8) + w);   // (no head behind the last one is read)
+      if (head < gn) x = load(head, (lane & 3) * (C / 8) + w);   // (no head behind the last one is read)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 p = unpack_bf16x2((&x.x)[k]);
@@ -281,7 +299,7 @@ constexpr int kLeast = -111, kRoom = 4, kSlack = 4;
 template <int D, int QR>
 struct Segment {
   static constexpr int NQ = (QR + 7) / 8, NT = D / 16;
-  static constexpr bool ONE = QR == 1;
+  static constexpr bool ONE = QR == 1, TWICE = QR == 4;
   Queries<D> qs[NQ];
   float o[NQ][NT][4];                                // times `into`, as off is
   float m[NQ][2], l[NQ][2], off[NQ][2];              // m: the reference, a whole number
@@ -305,7 +323,7 @@ struct Segment {
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][j][k] = 0.0f;
-      qs[i].take(scale_log2, gn - 8 * i, lane, [&](int r, int u) { return load(8 * i + r, u); });
+      qs[i].template take<TWICE>(scale_log2, gn - 8 * i, lane, [&](int r, int u) { return load(8 * i + r, u); });
     }
     if constexpr (ONE) {                             // every lane has rows of the one head
       qs[0].sum[0] = __shfl_sync(kAll, qs[0].sum[0], 0);
@@ -322,6 +340,10 @@ struct Segment {
     for (int j = 0; j < NT; ++j) {
       o[i][j][k] *= a;
       o[i][j][2 + k] *= a;
+      if constexpr (ONE) {                           // the second parts' column
+        o[i][j][1] *= a;
+        o[i][j][3] *= a;
+      }
     }
   }
   // Raises a head's reference for a largest score of mx. True: its E has to be set anew.
@@ -357,7 +379,37 @@ struct Segment {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; k += ONE ? 2 : 1) o[i][j][k] += eights[i][k];
+        for (int k = 0; k < 4; k += 2) {
+          if constexpr (ONE) {
+            o[i][j][k] += eights[i][k] + eights[i][k + 1];
+          } else {
+            const float2 x = add2_rn(make_float2(o[i][j][k], o[i][j][k + 1]), make_float2(eights[i][k], eights[i][k + 1]));
+            o[i][j][k] = x.x;
+            o[i][j][k + 1] = x.y;
+          }
+        }
+  }
+
+  // 16 rows' products with their values: s, their probabilities times their scales, in two parts.
+  template <bool FIRST, int NJ>
+  __device__ __forceinline__ void add(const float (&s)[NQ][NJ][4], int j, float (&eights)[NQ][4], const uint32_t (&w)[4],
+                                      int lane) {
+    uint32_t p[NQ][2];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float x = s[i][j][2 * h], y = s[i][j][2 * h + 1];
+        p[i][h] = transposed(TWICE ? cut_rest2(x, y, (lane & 2) ? kHalfBits : 0u) : cut_half2(x, y));
+      }
+    add_codes<FIRST, D, NQ>(o, eights, p, w);
+    if constexpr (!TWICE) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) p[i][h] = transposed(cut_rest2(s[i][j][2 * h], s[i][j][2 * h + 1], kHalfBits));
+      add_codes<false, D, NQ>(o, eights, p, w);
+    }
   }
 
   // Scores of the tiles into probabilities times the rows' scales. factors: shared address of the rows' (key scale, key
@@ -388,7 +440,7 @@ struct Segment {
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      float mx[2], ref[2];
+      float mx[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float x = s[i][0][k];
@@ -404,16 +456,18 @@ struct Segment {
         const bool x = raise(i, 0, mx[0]), y = raise(i, 1, mx[1]);
         anew = __any_sync(kAll, large || x || y);
       }
+      const float2 c = make_float2(qs[i].c[0], qs[i].c[1]), less = make_float2(-reference(i, 0), -reference(i, 1));
+      float2 sum = make_float2(l[i][0], l[i][1]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) ref[k] = reference(i, k);
-#pragma unroll
-      for (int r = 0; r < 2 * NJ; ++r)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float& x = s[i][r >> 1][2 * (r & 1) + k];
-          x = ex2_approx(fmaf(x, qs[i].c[k], -ref[k]));
-          l[i][k] += x;
-        }
+      for (int r = 0; r < 2 * NJ; ++r) {
+        float* x = &s[i][r >> 1][2 * (r & 1)];
+        const float2 d = fma2_rn(make_float2(x[0], x[1]), c, less);
+        x[0] = ex2_approx(d.x);
+        x[1] = ex2_approx(d.y);
+        sum = add2_rn(sum, make_float2(x[0], x[1]));
+      }
+      l[i][0] = sum.x;
+      l[i][1] = sum.y;
       if (anew) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -484,20 +538,36 @@ struct Segment {
     }
   }
 
-  // The lane's values D / 8 n .. of head 8 i + 2 q + k, not divided by the sum, which is returned.
-  __device__ __forceinline__ float values(int i, int k, float (&v)[D / 8]) const {
-    float lt = l[i][k], ot = off[i][k];
+  // Heads whose values a lane has: NK of each eight, those of `head`. With every head in the columns twice a lane takes one of its
+  // two, and gives the other's to the lane that has its other part.
+  static constexpr int NK = TWICE ? 1 : 2;
+  static __device__ __forceinline__ int head(int i, int k, int lane) {
+    return TWICE ? 2 * (lane & 1) + ((lane >> 1) & 1) : 8 * i + 2 * (lane & 3) + k;
+  }
+  static __device__ __forceinline__ float of(const float (&x)[2], int k, int lane) { return TWICE ? (lane & 2 ? x[1] : x[0]) : x[k]; }
+  __device__ __forceinline__ float maximum(int i, int k, int lane) const { return of(m[i], k, lane); }
+  // Its values D / 8 n .., not divided by the sum, which is returned.
+  __device__ __forceinline__ float values(int i, int k, int lane, float (&v)[D / 8]) const {
+    float lt = of(l[i], k, lane), ot = of(off[i], k, lane);
 #pragma unroll
     for (int x = ONE ? 1 : 4; x < 32; x <<= 1) {
       lt += __shfl_xor_sync(kAll, lt, x);
       ot += __shfl_xor_sync(kAll, ot, x);
     }
-    const int e = -exponent_of(into[i][k]);
+    const int e = -exponent_of(of(into[i], k, lane));
     const float back = exp2_of(e / 2), rest = exp2_of(e - e / 2);   // 1 / into in two steps
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      v[2 * j] = fmaf(o[i][j][k], 16777216.0f, ot) * back * rest;   // 2^24 and 2^20
-      v[2 * j + 1] = fmaf(o[i][j][2 + k], 1048576.0f, ot) * back * rest;
+      float x[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float a = o[i][j][2 * h], b = o[i][j][2 * h + 1];
+        if constexpr (ONE) x[h] = a + b;             // the two parts
+        else if constexpr (TWICE) x[h] = (lane & 2 ? b : a) + __shfl_xor_sync(kAll, lane & 2 ? a : b, 2);
+        else x[h] = k ? b : a;
+      }
+      v[2 * j] = fmaf(x[0], 16777216.0f, ot) * back * rest;   // 2^24 and 2^20
+      v[2 * j + 1] = fmaf(x[1], 1048576.0f, ot) * back * rest;
     }
     return lt;
   }
@@ -683,7 +753,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const int n8 = lane >> 2, q4 = lane & 3;
   const uint32_t factors = ring + Cfg::FACTORS;
   if constexpr (ONE) {
-    if (lane < 2) sts128f(factors + 256 + 128 + 16 * lane, 0.0f, 0.0f, 0.0f, 0.0f);
+    if (lane < 2) sts128f(factors + 256 + 2 * 128 + 16 * lane, 0.0f, 0.0f, 0.0f, 0.0f);
   }
   uint32_t st = ring, other = ring + Cfg::STAGE;     // the stage that is read, and the one that is filled meanwhile
   look_up(at, at.t0);
@@ -765,10 +835,14 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, unseen, large, lane);
         const uint32_t weights = factors + 256;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) sts16(weights + weight_place<2 * NJ>(32 * h + lane), x[h]);
+        for (int h = 0; h < NH; ++h) {
+          const uint32_t to = weights + weight_place<2 * NJ>(32 * h + lane);
+          sts16(to, x[h]);
+          sts16(to + 128, rest_of(x[h]));
+        }
         __syncwarp();
-        const uint32_t pa = n8 == 0 ? weights + 32 * q4 : weights + 128;   // other columns: zeros
-        const uint32_t step = n8 == 0 ? 16 : 0;
+        const uint32_t pa = weights + (n8 < 2 ? 128 * n8 + 32 * q4 : 256);   // the parts' columns; others: zeros
+        const uint32_t step = n8 < 2 ? 16 : 0;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const uint4 w4 = lds128(pa + step * h);
@@ -785,15 +859,10 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         g.weigh(s, factors, seen, unseen, large, lane);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          uint32_t p[NQ][2], u[4];
-#pragma unroll
-          for (int i = 0; i < NQ; ++i) {
-            p[i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
-            p[i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
-          }
+          uint32_t u[4];
           value_words(u, j);
-          if (j == 0) add_codes<true, D, NQ>(g.o, eights, p, u);
-          else add_codes<false, D, NQ>(g.o, eights, p, u);
+          if (j == 0) g.template add<true>(s, j, eights, u, lane);
+          else g.template add<false>(s, j, eights, u, lane);
         }
       }
       g.centre(eights);
@@ -808,10 +877,10 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < g.NK; ++k) {
         float v[D / 8];                               // values D / 8 n8 .. of the head
-        const float lt = g.values(i, k, v);
-        const int r = 8 * i + 2 * q4 + k;
+        const float lt = g.values(i, k, lane, v), mx = g.maximum(i, k, lane);
+        const int r = g.head(i, k, lane);
         if (r >= gn) continue;
         if (whole) {
           const size_t head = static_cast<size_t>(at.b) * w.H + at.kh * w.G + at.mt * 16 + r;
@@ -821,12 +890,12 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
           for (int j = 0; j < NT; ++j) h[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
           if constexpr (D == 64) *reinterpret_cast<uint4*>(y + head * D + 8 * n8) = make_uint4(h[0], h[1], h[2], h[3]);
           else *reinterpret_cast<uint2*>(y + head * D + 4 * n8) = make_uint2(h[0], h[1]);
-          if (n8 == 0 && lse2) lse2[head] = g.m[i][k] + log2f(lt);
+          if (n8 == 0 && lse2) lse2[head] = mx + log2f(lt);
         } else {
           float4* dst = reinterpret_cast<float4*>(ws.o + (slot * QR + r) * D + n8 * (D / 8));
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-          if (n8 == 0) ws.ml[slot * QR + r] = make_float2(g.m[i][k], lt);
+          if (n8 == 0) ws.ml[slot * QR + r] = make_float2(mx, lt);
         }
       }
     if (!more) break;
@@ -848,8 +917,8 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
                     int* err) {
   constexpr int ROWB = D / 2, NQ = (QR + 7) / 8, UNIT = 32;
   constexpr bool ONE = QR == 1;
-  __shared__ __align__(16) float s_own[8][QR][D];    // the warps' outputs, and before them what a unit's rows need
-  __shared__ __align__(16) float s_factors[8][ONE ? 32 + 16 + 4 : UNIT * 4];
+  __shared__ __align__(16) float s_own[8][QR][D];    // the warps' outputs
+  __shared__ __align__(16) float s_factors[8][ONE ? 32 + 2 * 16 + 4 : UNIT * 4];
   __shared__ float2 s_ml[8][QR];                     // the warps' maxima and sums
   __shared__ float2 s_all[8][QR];                    // the blocks', pushed by each of them
   __shared__ float s_o[QR + 7][D];                   // pushed outputs: [row / NB * NB + block][D]
@@ -888,7 +957,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const uint8_t* codes = static_cast<const uint8_t*>(c.pool);
   const uint32_t factors = smem_u32(&s_factors[warp][0]);
   if constexpr (ONE) {
-    if (lane == 0) sts128f(factors + 192, 0.0f, 0.0f, 0.0f, 0.0f);
+    if (lane == 0) sts128f(factors + 256, 0.0f, 0.0f, 0.0f, 0.0f);
   }
   for (int u = 0; u < upw; ++u) {
     const int unit = (rank * upw + u) * 8 + warp;
@@ -946,34 +1015,25 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       }
       code_scores<D, NQ, 2>(s, j, g.qs, x);
     }
-    uint32_t p[2][NQ][2];
     if constexpr (ONE) {
       float x[1];
       g.weigh_one(s, x, factors, ks, kl, vs, vl, seen, ~seen[0], large, lane);
-      sts16(factors + 128 + weight_place<4>(lane), x[0]);
+      const uint32_t to = factors + 128 + weight_place<4>(lane);
+      sts16(to, x[0]);
+      sts16(to + 64, rest_of(x[0]));
       __syncwarp();
-      const uint4 w4 = lds128(factors + 128 + (n8 == 0 ? 16 * q4 : 64));   // other columns: zeros
-      p[0][0][0] = w4.x;
-      p[0][0][1] = w4.y;
-      p[1][0][0] = w4.z;
-      p[1][0][1] = w4.w;
+      const uint4 w4 = lds128(factors + 128 + (n8 < 2 ? 64 * n8 + 16 * q4 : 128));   // the parts' columns; others: zeros
+      const uint32_t p0[1][2] = {{w4.x, w4.y}}, p1[1][2] = {{w4.z, w4.w}};
+      const uint32_t u0[4] = {vw[0], vw[1], vw[2], vw[3]}, u1[4] = {vw[4], vw[5], vw[6], vw[7]};
+      add_codes<true, D, NQ>(g.o, eights, p0, u0);
+      add_codes<false, D, NQ>(g.o, eights, p1, u1);
     } else {
       sts128f(factors + 16 * lane, ks[0], kl[0], vs[0], vl[0]);
       __syncwarp();
       g.weigh(s, factors, seen, ~seen[0], large, lane);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          p[j][i][0] = transposed(pack_half2(s[i][j][0], s[i][j][1]));
-          p[j][i][1] = transposed(pack_half2(s[i][j][2], s[i][j][3]));
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t x[4] = {vw[4 * j], vw[4 * j + 1], vw[4 * j + 2], vw[4 * j + 3]};
-      if (j == 0) add_codes<true, D, NQ>(g.o, eights, p[j], x);
-      else add_codes<false, D, NQ>(g.o, eights, p[j], x);
+      const uint32_t u0[4] = {vw[0], vw[1], vw[2], vw[3]}, u1[4] = {vw[4], vw[5], vw[6], vw[7]};
+      g.template add<true>(s, 0, eights, u0, lane);
+      g.template add<false>(s, 1, eights, u1, lane);
     }
     g.centre(eights);
     __syncwarp();                                    // the factors are read before they are written again
@@ -981,15 +1041,15 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
 #pragma unroll
   for (int i = 0; i < NQ; ++i)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < g.NK; ++k) {
       float v[D / 8];
-      const float lt = g.values(i, k, v);
-      const int r = 8 * i + 2 * q4 + k;
+      const float lt = g.values(i, k, lane, v);
+      const int r = g.head(i, k, lane);
       if (r >= gn) continue;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x)
         *reinterpret_cast<float4*>(&s_own[warp][r][n8 * (D / 8) + 4 * x]) = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-      if (n8 == 0) s_ml[warp][r] = make_float2(g.m[i][k], lt);
+      if (n8 == 0) s_ml[warp][r] = make_float2(g.maximum(i, k, lane), lt);
     }
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -1206,9 +1266,13 @@ cudaError_t launch_paged_attention4(const PagedCache& c, const void* ranges, con
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(qkv);
   const uint32_t* r = static_cast<const uint32_t*>(ranges);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(y);
-  const int qr = w.G == 1 ? 1 : w.G <= 8 ? 8 : 16;
-  auto launch = D == 64 ? (qr == 1 ? launch_decode4<64, 1> : qr == 8 ? launch_decode4<64, 8> : launch_decode4<64, 16>)
-                        : (qr == 1 ? launch_decode4<32, 1> : qr == 8 ? launch_decode4<32, 8> : launch_decode4<32, 16>);
+  // Up to four heads on a key head have a form of their own, whose columns hold each of them twice (16 x 9,000 to 32,000 rows, 16
+  // heads on 4, 28.5 us, with the form for eight 31.2; 16 x up to 1,023 5.3 and 5.6).
+  auto launch = launch_decode4<64, 16>;
+  if (w.G == 1) launch = D == 64 ? launch_decode4<64, 1> : launch_decode4<32, 1>;
+  else if (w.G <= 4) launch = D == 64 ? launch_decode4<64, 4> : launch_decode4<32, 4>;
+  else if (w.G <= 8) launch = D == 64 ? launch_decode4<64, 8> : launch_decode4<32, 8>;
+  else if (D == 32) launch = launch_decode4<32, 16>;
   return launch(c, r, x, lens, o, lse2, w, err, s);
 }
 

@@ -276,13 +276,13 @@ int gptk_paged_append(const void* qkv, void* out, void* pool, float* weight, con
  *   y[b, h] = sum_r a_r u_r,  a = softmax(q_h . k_r / sqrt(D))     bf16 [B, H D]
  *   lse2[b, h] = log2 sum_r 2^(q_h . k_r log2(e) / sqrt(D))         fp32 [B, H], NULL: not wanted
  * n = 0: y 0, lse2 -inf. lens[b] < 0: no sequence, row b of the outputs stays as it was. fp32 scores and sums; a probability
- * times its row's scale enters the product with the codes as one fp16 number (2^-12 of it at most is lost, or 2^-31 of the
+ * times its row's scale enters the product with the codes in two fp16 parts (2^-20 of it at most is lost, or 2^-29 of the
  * largest product of a probability of that head and its row's scale, or |lowest + 8 scale|). Keys' scales and lowest
  * values have to stay below 2^100. A NaN in sight makes its queries' outputs NaN, and so do scores that are all -inf. Rows
  * out of sight count for nothing, whatever they hold (those that share a tile of 64 rows with ones in sight are read). y
  * overlaps no input. B max_pages page / 32 < 2^31, and times Hkv <= 2^40 (GPT_EINVAL otherwise). Scratch (none where the
- * table, or the window and sinks, hold few rows; else 1.3 MB with a key head for each query head, 10 MB for two to eight, 15 MB
- * for more, and 4 (B + 1) bytes) is taken on the stream as for gptk_paged_attention; make a process's first call on a device
+ * table, or the window and sinks, hold few rows; else 1.3 MB with a key head for each query head, 5 MB for two to four, 10 MB
+ * for five to eight, 15 MB for more, and 4 (B + 1) bytes) is taken on the stream as for gptk_paged_attention; make a process's first call on a device
  * before any stream capture.
  */
 int gptk_paged_append4(const void* qkv, void* out, void* codes, void* ranges, const int32_t* table, const int32_t* start,

@@ -7,14 +7,14 @@ from paged_ref import place
 from serving_ref import values
 
 
-def attend_rows(qkv, codes, ranges, table, seen, H, product_bits=12, rounded=None):
+def attend_rows(qkv, codes, ranges, table, seen, H, product_bits=20, rounded=None):
     """(y, lse2, bounds of y's and lse2's errors apart from y's rounding); seen[b]: the rows that sequence b's query sees (None:
     no sequence, NaN).
 
     The bounds of scores, exponentials and sums are serving_ref.attend4's. A weight times its scale enters the product with the
-    codes as one fp16 number: 2^-12 of it is lost, times |code - 8| <= 8. The smallest ones are whole multiples of 2^-24 of
-    2^(E - 15), where 2^E is at most 2^9 times the head's largest product of a weight and its row's scale, or the |lowest + 8
-    scale| of the row: 2^-25 2^-15 2^9 8 = 2^-28 of that product for each row.
+    codes in two fp16 parts, both cut off: 2^-10 of 2^-10 of it is lost, times |code - 8| <= 8. The smallest ones are whole
+    multiples of 2^-24, in either part, of 2^(E - 15), where 2^E is at most 2^9 times the head's largest product of a weight and
+    its row's scale, or the |lowest + 8 scale| of the row: 2 2^-24 2^-15 2^9 8 = 2^-26 of that product for each row.
 
     product_bits: 2^-product_bits of a product may be lost. rounded(x): what stands for a weight times its scale (the weight
     against a largest one of 1), for a calculation that loses more."""
@@ -54,7 +54,7 @@ def attend_rows(qkv, codes, ranges, table, seen, H, product_bits=12, rounded=Non
                 el[b, h] = d + 2.0 ** -20 + 2.0 ** -22 * abs(lse2[b, h])
                 off = 2 * (2 * d * math.log(2.0) + 2.0 ** -20)
                 ey[b, h] = float(a @ (8 * ur[:, 0])) * 2.0 ** -product_bits + \
-                    float(a @ (16 * ur[:, 0] + np.abs(ur[:, 1]))) * off + len(seen[b]) * 2.0 ** -28 * float((a * size).max())
+                    float(a @ (16 * ur[:, 0] + np.abs(ur[:, 1]))) * off + len(seen[b]) * 2.0 ** -26 * float((a * size).max())
     return y.reshape(B, H * D), lse2, ey.reshape(B, H * D), el
 
 

@@ -115,3 +115,21 @@ def test_sizes_that_change_with_the_scores(gpt_lib, rows, H, Hkv, D, down):
     k = k * 0.01 + (r // 4) * 0.1 + 20.0 * (r > 380)
     u = u * 2.0 ** ((-1 if down else 1) * (r * 60 / 400))
     Cache(q, [k], [u], H, 16, rows).device().call().check()
+
+
+@pytest.mark.parametrize("rows", FORMS)
+@pytest.mark.parametrize("H,Hkv,D", HEADS)
+def test_weights_keep_twenty_bits(gpt_lib, rows, H, Hkv, D):
+    # few rows with scores of one value of the query, so that scores and sums lose little; some outputs are sums that cancel
+    for seed in range(4):
+        c = few_rows(H, Hkv, D, rows, seed)
+        c.device().call().check()
+
+
+def few_rows(H, Hkv, D, rows, seed):
+    rng = np.random.default_rng(100 + seed)
+    q = np.zeros((1, H, D))
+    q[0, np.arange(H), rng.integers(0, D, H)] = 0.5
+    k, u = rand_bf16(rng, (3, Hkv, D)), rand_bf16(rng, (3, Hkv, D))
+    k[:, :, :] = np.clip(k, -1.0, 1.0)
+    return Cache(q, [k], [u], H, 8, rows, seed=seed)

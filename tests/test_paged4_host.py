@@ -28,6 +28,29 @@ def test_whole_sequences_and_windows():
         assert np.array_equal(y, y2) and np.array_equal(lse2, lse3)
 
 
+def test_the_bounds_hold_for_two_parts_and_not_for_one():
+    def two_parts(x):
+        x = x * 2.0 ** 8                              # largest near 2^8, as fp16 parts that are cut off
+        e = np.floor(np.log2(np.maximum(x, 2.0 ** -14)))
+        hi = np.trunc(x / 2.0 ** (e - 10)) * 2.0 ** (e - 10)
+        lo = x - hi
+        e = np.floor(np.log2(np.maximum(lo, 2.0 ** -14)))
+        return (hi + np.trunc(lo / 2.0 ** (e - 10)) * 2.0 ** (e - 10)) * 2.0 ** -8
+
+    def one_part(x):
+        return x.astype(np.float16).astype(np.float64)
+
+    off = 0
+    for seed in range(4):
+        x, codes, ranges, table = case(8, 2, 64, 1, seed, q_values=1)
+        y, _, ey, _ = ref.attend_rows(x, codes, ranges, table, [range(3)], 8)
+        assert not ref.outside(round_to_bf16(
+            ref.attend_rows(x, codes, ranges, table, [range(3)], 8, rounded=two_parts)[0].astype(np.float32)), y, ey).any()
+        off += ref.outside(round_to_bf16(
+            ref.attend_rows(x, codes, ranges, table, [range(3)], 8, rounded=one_part)[0].astype(np.float32)), y, ey).sum()
+    assert off > 10
+
+
 def test_the_bounds_do_not_hold_where_a_row_without_weight_sets_the_unit():
     x, codes, ranges, table = case(2, 1, 32, 4, 5, q_values=1)
     y, _, ey, _ = ref.attend_rows(x, codes, ranges, table, [range(30)], 2)
