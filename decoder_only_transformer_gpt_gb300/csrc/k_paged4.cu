@@ -722,7 +722,9 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   uint32_t in_page = 0;                              // and their block in it
   auto look_up = [&](const Piece& x, int tile) {
     const int r = first_row<UNIT>(x.t, tile) + 8 * lane;
-    pg = lane < UNIT / 8 && r < x.t.n ? __ldg(c.table + static_cast<size_t>(x.b) * c.max_pages + (r >> c.page_log2)) : -2;
+    // (no page of eight rows that are all out of sight: it need not exist)
+    const bool wanted = lane < UNIT / 8 && r < x.t.n && (w.window == 0 || r + 7 >= x.t.n - w.window || r < w.sinks);
+    pg = wanted ? __ldg(c.table + static_cast<size_t>(x.b) * c.max_pages + (r >> c.page_log2)) : -2;
     in_page = ((static_cast<uint32_t>(x.kh) << c.page_log2) + (r & pmask)) >> 3;
   };
   auto copy_rows = [&](uint32_t to) {
@@ -964,16 +966,17 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     if (unit >= t.count) break;
     const int r0 = first_row<UNIT>(t, unit), mine = r0 + lane;
     if (r0 != guess) page = mine < n ? __ldg(trow + (mine >> c.page_log2)) : 0;
-    const bool there = mine < n && static_cast<unsigned>(page) < static_cast<unsigned>(c.pages);
-    if (mine < n && !there) record_error(err, GPT_DEV_EPAGE);
+    const bool in_sight = mine < n && (w.window == 0 || mine >= n - w.window || mine < w.sinks);   // (others' pages need not exist)
+    const bool is_seen = in_sight && static_cast<unsigned>(page) < static_cast<unsigned>(c.pages);
+    if (in_sight && !is_seen) record_error(err, GPT_DEV_EPAGE);
     // eight rows lie in one page: theirs, from the lane of the first one
-    const uint32_t have = __ballot_sync(kAll, there);
+    const uint32_t have = __ballot_sync(kAll, is_seen);
     uint32_t kw[4][D / 32], vw[8];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const size_t row = static_cast<size_t>(static_cast<uint32_t>(__shfl_sync(kAll, page, 8 * r))) * prows +
                          (static_cast<size_t>(kh) << c.page_log2) + ((r0 + 8 * r) & pmask);
-      const bool ok = (have >> (8 * r)) & 1u;
+      const bool ok = (have >> (8 * r)) & 255u;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) kw[r][k] = 0u;
       vw[2 * r] = vw[2 * r + 1] = 0u;
@@ -992,7 +995,6 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
         vw[2 * r + 1] = __ldg(reinterpret_cast<const uint16_t*>(v8 + 4 * ROWB));
       }
     }
-    const bool is_seen = there && (w.window == 0 || mine >= n - w.window || mine < w.sinks);
     uint32_t kr = 0u, vr = 0u;                       // row `lane`'s ranges
     if (is_seen) {
       const size_t row = static_cast<size_t>(static_cast<uint32_t>(page)) * prows + (static_cast<size_t>(kh) << c.page_log2) +
@@ -1000,7 +1002,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       kr = __ldg(ranges + row);
       vr = __ldg(ranges + row + vrows);
     }
-    const uint32_t seen[1] = {__ballot_sync(kAll, is_seen)};
+    const uint32_t seen[1] = {have};
     float ks[1] = {scale_of(kr) * 16777216.0f}, kl[1] = {low_of(kr)}, vs[1] = {scale_of(vr)};
     float vl[1] = {fmaf(8.0f, vs[0], low_of(vr))};
     const bool large = __any_sync(kAll, fmaxf(vs[0], fabsf(vl[0])) * g.most >= 32768.0f);

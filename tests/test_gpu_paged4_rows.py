@@ -133,3 +133,22 @@ def few_rows(H, Hkv, D, rows, seed):
     k, u = rand_bf16(rng, (3, Hkv, D)), rand_bf16(rng, (3, Hkv, D))
     k[:, :, :] = np.clip(k, -1.0, 1.0)
     return Cache(q, [k], [u], H, 8, rows, seed=seed)
+
+
+@pytest.mark.parametrize("rows", FORMS)
+@pytest.mark.parametrize("H,Hkv,D,page", [(3, 3, 64, 16), (8, 2, 32, 8), (12, 1, 64, 16), (4, 2, 64, 64)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (50, 0), (50, 3), (200, 20)])
+def test_pages_out_of_sight_need_not_exist(gpt_lib, rows, H, Hkv, D, page, window, sinks):
+    # a caller that gives pages behind the window back leaves no numbers of them in the table
+    from decoder_only_transformer_gpt_gb300 import binding
+    rng = np.random.default_rng(8)
+    for n in (500, 511, 513, 449):
+        k, u = (rand_bf16(rng, (n, Hkv, D)) for _ in range(2))
+        c = Cache(rand_bf16(rng, (1, H, D)), [k], [u], H, page, rows, window, sinks).device()
+        kept = {r // page for r in c.seen()[0]}
+        for i in range(c.table.shape[1]):
+            if i not in kept:
+                c.d[3][0, i] = -1 if i % 2 else 10 ** 9
+        c.call()
+        binding.status()
+        c.check()
