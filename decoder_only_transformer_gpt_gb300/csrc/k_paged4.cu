@@ -718,19 +718,22 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const uint8_t* vfrom = kfrom + static_cast<size_t>(page_blocks / 2) * (8 * ROWB);
   const int rrow = 4 * (lane % (UNIT / 4));
   const uint8_t* rfrom = reinterpret_cast<const uint8_t*>(ranges) + (lane / (UNIT / 4) ? page_blocks * 16 : 0u) + (rrow & 4) * 4;
-  int pg = -2;                                       // the page of this lane's eight rows; -2: none
+  bool wanted = false;                               // whether this lane has eight rows of it, their page
+  int pg = -1;
   uint32_t in_page = 0;                              // and their block in it
   auto look_up = [&](const Piece& x, int tile) {
     const int r = first_row<UNIT>(x.t, tile) + 8 * lane;
     // (no page of eight rows that are all out of sight: it need not exist)
-    const bool wanted = lane < UNIT / 8 && r < x.t.n && (w.window == 0 || r + 7 >= x.t.n - w.window || r < w.sinks);
-    pg = wanted ? __ldg(c.table + static_cast<size_t>(x.b) * c.max_pages + (r >> c.page_log2)) : -2;
+    wanted = lane < UNIT / 8 && r < x.t.n && (w.window == 0 || r + 7 >= x.t.n - w.window || r < w.sinks);
+    pg = wanted ? __ldg(c.table + static_cast<size_t>(x.b) * c.max_pages + (r >> c.page_log2)) : -1;
     in_page = ((static_cast<uint32_t>(x.kh) << c.page_log2) + (r & pmask)) >> 3;
   };
+  // Returns the unit's eight rows whose page does not exist (a bit each): what stands in their place in the ring is not theirs.
   auto copy_rows = [&](uint32_t to) {
-    uint32_t blk = kNoBlock;
-    if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages)) blk = static_cast<uint32_t>(pg) * page_blocks + in_page;
-    else if (pg != -2) record_error(err, GPT_DEV_EPAGE);
+    const bool there = static_cast<unsigned>(pg) < static_cast<unsigned>(c.pages);
+    const uint32_t blk = there ? static_cast<uint32_t>(pg) * page_blocks + in_page : kNoBlock;
+    const uint32_t lost = __ballot_sync(kAll, wanted && !there);
+    if (wanted && !there) record_error(err, GPT_DEV_EPAGE);
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
       const uint32_t mine = __shfl_sync(kAll, blk, block + i * (RPC / 8));
@@ -741,6 +744,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
     }
     const uint32_t mine = __shfl_sync(kAll, blk, rrow / 8);
     if (mine != kNoBlock && lane < UNIT / 2) copy16(to + Cfg::RANGES + lane * 16, rfrom + static_cast<size_t>(mine) * 32);
+    return lost;
   };
   auto copy_queries = [&](const Piece& x, uint32_t to) {
     const int gn = min(w.G - x.mt * 16, 16);
@@ -759,7 +763,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   }
   uint32_t st = ring, other = ring + Cfg::STAGE;     // the stage that is read, and the one that is filled meanwhile
   look_up(at, at.t0);
-  copy_rows(st);
+  uint32_t lost = copy_rows(st), lost_next = 0;      // of the stage that is read, and of the other
   copy_queries(at, st);
   asm volatile("cp.async.commit_group;" ::: "memory");
   if (at.t0 + 1 < at.t1) look_up(at, at.t0 + 1);
@@ -767,12 +771,12 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   while (true) {
     for (int tile = at.t0; tile < at.t1; ++tile) {
       if (tile + 1 < at.t1) {
-        copy_rows(other);
+        lost_next = copy_rows(other);
         if (tile + 2 < at.t1) look_up(at, tile + 2);
         else if (more) look_up(next, 0);
       } else if (more) {
         if (at.t1 == at.t0 + 1) look_up(next, 0);      // (of pieces of one tile not before now)
-        copy_rows(other);
+        lost_next = copy_rows(other);
         copy_queries(next, other);
         if (next.t1 > 1) look_up(next, 1);
       }
@@ -786,7 +790,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
       float ks[NH], kl[NH], vs[NH], vl[NH], size = 0.0f;   // the factors of rows `lane` and, of a unit of 64, 32 + lane
       {
-        const bool cut = f + UNIT > at.t.n || (w.window > 0 && f < after && f + UNIT > w.sinks);
+        const bool cut = lost || f + UNIT > at.t.n || (w.window > 0 && f < after && f + UNIT > w.sinks);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const uint32_t kr = lds32(st + Cfg::RANGES + 4 * (32 * h + lane));
@@ -794,7 +798,8 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
           seen[h] = kAll;
           if (cut) {
             const int r = f + 32 * h + lane;
-            const bool mine = r < at.t.n && (w.window == 0 || r >= after || r < w.sinks);
+            const bool mine = r < at.t.n && (w.window == 0 || r >= after || r < w.sinks) &&
+                              !((lost >> (4 * h + (lane >> 3))) & 1u);
             seen[h] = __ballot_sync(kAll, mine);
             if (!mine) vr = 0u;
           }
@@ -871,6 +876,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       const uint32_t swap = st;
       st = other;
       other = swap;
+      lost = lost_next;
       __syncwarp();                                    // the stage and the factors are read before they are filled again
     }
     const bool whole = at.t0 == 0 && at.t1 == at.t.count;   // the piece is the segment

@@ -136,6 +136,33 @@ def few_rows(H, Hkv, D, rows, seed):
 
 
 @pytest.mark.parametrize("rows", FORMS)
+@pytest.mark.parametrize("H,Hkv,D,page", [(3, 3, 64, 16), (8, 2, 32, 8), (12, 1, 64, 64), (4, 2, 64, 128)])
+@pytest.mark.parametrize("bad", [-1, -2, 10 ** 9])
+def test_rows_of_a_bad_page_are_left_out(gpt_lib, rows, H, Hkv, D, page, bad):
+    # reported, and nothing else takes their place: not the rows of another sequence either
+    from decoder_only_transformer_gpt_gb300 import binding
+    rng = np.random.default_rng(7)
+    lens = [300, 290, 280]
+    k, u = ([rand_bf16(rng, (n, Hkv, D)) * 10.0 ** b for b, n in enumerate(lens)] for _ in range(2))
+    q = rand_bf16(rng, (3, H, D), 0.3)
+    without = {(0, 1), (1, 0), (1, 290 // page), (2, 100 // page)}
+    c = Cache(q, k, u, H, page, rows).device()
+    c.call()
+    for b, i in without:
+        c.d[3][b, i] = bad
+    out = []
+    for _ in range(3):
+        c.y.fill_(7.0)
+        c.call()
+        with pytest.raises(binding.GptError) as e:
+            binding.status()
+        assert e.value.code == binding.GPT_EPAGE
+        c.check(without)
+        out.append(c.y.clone())
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+
+
+@pytest.mark.parametrize("rows", FORMS)
 @pytest.mark.parametrize("H,Hkv,D,page", [(3, 3, 64, 16), (8, 2, 32, 8), (12, 1, 64, 16), (4, 2, 64, 64)])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (50, 0), (50, 3), (200, 20)])
 def test_pages_out_of_sight_need_not_exist(gpt_lib, rows, H, Hkv, D, page, window, sinks):
