@@ -9,8 +9,8 @@
 // of the warps' four largest of those is a floor that K tokens reach, and few others: only the chunks of threads that reach it
 // are looked at again (out of L2, where they are not kept in registers), and what reaches it there goes into one pool of keys
 // (logit, then lowest index) in shared memory, in any order. A key's place is the number of larger ones, so the result does
-// not depend on that order. Where more tokens reach the floor than the pool holds (many equal ones), every warp keeps its best
-// 32 in order instead, one a lane, and the lists are joined. (Lists kept up to date while the row went by took 8 to 16
+// not depend on that order. Where more tokens reach the floor than the pool holds (many equal ones), or there is none (fewer than
+// K threads have a logit above -inf), every warp keeps its best 32 in order instead, one a lane, and the lists are joined. (Lists kept up to date while the row went by took 8 to 16
 // instructions for every 32 logits, as many as the sums: 4,096 rows of 50,257 with K = 8 took 151 us in fp32 and 124 in bf16;
 // lists for every warp behind the sums 135 and 85.)
 //
@@ -130,6 +130,10 @@ template <> struct Vec<float> {
     const float2 a = pair(v, 0), b = pair(v, 1);
     return fmaxf(fmax3(a.x, a.y, b.x), b.y);
   }
+  static __device__ __forceinline__ float2 halves(const uint4& v) {   // the largest of each half
+    const float2 a = pair(v, 0), b = pair(v, 1);
+    return make_float2(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
+  }
   static __device__ __forceinline__ float largest(const uint4 (&v)[kLpVecs]) {
     float m = -INFINITY;
 #pragma unroll
@@ -153,6 +157,11 @@ template <> struct Vec<__nv_bfloat16> {
     const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v.x);
     const float2 f = __bfloat1622float2(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
     return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ float2 halves(const uint4& v) {
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v.x);
+    const float2 a = __bfloat1622float2(__hmax2(w[0], w[1])), b = __bfloat1622float2(__hmax2(w[2], w[3]));
+    return make_float2(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
   }
   static __device__ __forceinline__ float largest(const uint4 (&v)[kLpVecs]) {
     const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
@@ -310,7 +319,7 @@ logprobs_kernel(LpArgs a, int* err) {
     const float mn = fmaxf(sum.m, ze), dm = fmaxf(sum.m - mn, kFar), f = ex2_approx(dm * kL2E), d = ze - mn, e = ex2_approx(d * kL2E);
     sum = {mn, sum.s * f + e, f * (sum.a + sum.s * dm) + e * fmaxf(d, kFar)};
   }
-  float reached = 0.0f;                              // by K threads' largest logits
+  float reached = 0.0f;                              // by K threads' largest logits; -inf: fewer of them are more than that
   if (K) {
     // Blocks take the same time for their rows and so come to this part together, in which nothing is read: the first
     // chunks of a row that comes next are fetched into L2 meanwhile.
@@ -330,9 +339,14 @@ logprobs_kernel(LpArgs a, int* err) {
       if constexpr (FEW) {
         if (K > kLpFewTop) {                         // of two numbers a lane, as 32 do not let enough be left out
           float a = cm0, b = cm1;
-          if (chunks < 2) {
-            a = fmaxf(W::most(v[0]), W::most(v[2]));
-            b = fmaxf(W::most(v[1]), W::most(v[3]));
+          if (chunks < 2) {                          // (of few vectors, of which some lanes have none)
+            a = b = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kLpVecs; ++k) {
+              const float2 x = W::halves(v[k]);
+              a = fmaxf(a, x.x);
+              b = fmaxf(b, x.y);
+            }
           }
           order = join_values(sorted_values(a, lane), sorted_values(b, lane), lane);
         }
@@ -359,7 +373,9 @@ logprobs_kernel(LpArgs a, int* err) {
                 (y.z > x || (y.z == x && k + 2 < lane)) + (y.w > x || (y.w == x && k + 3 < lane));
         }
         reached = __shfl_sync(kAll, x, __ffs(__ballot_sync(kAll, at == K - 1)) - 1);
-      } else {
+      }
+      if (K > kLpFewTop || reached == -INFINITY) {   // (K / 4 warps have no chunk: 16 x 2,500, K = 16, 9.4 and 4.5 us; or a mask)
+        if (K <= kLpFewTop) __syncthreads();         // the four of every warp are read
         float order = sorted_values(top, lane);
         s_order[warp][lane] = order;
         __syncthreads();
@@ -472,7 +488,10 @@ logprobs_kernel(LpArgs a, int* err) {
     __syncwarp();
     best = s_best[team][lane];
   };
-  if (K) {
+  // Without a floor every token would go to the pool, more than it holds (4,096 x 50,257 in fp32, K = 10, of which a mask leaves 8:
+  // 571 us by way of the pool, so 180).
+  const bool no_floor = K && reached == -INFINITY && a.V > kLpPool;
+  if (K && !no_floor) {
     // Every token that reaches it, in any order: as a rule K of them and a few more.
     const uint32_t room = smem_u32(&s_pool[team][0]);
     auto put = [&](bool hit, int place, float z, int index) {
@@ -521,8 +540,10 @@ logprobs_kernel(LpArgs a, int* err) {
     });
     if (edge >= 0 && ze >= reached) put(true, atomicAdd(&s_count[team], 1), ze, edge);
     __syncwarp();
-    if constexpr (WR == 1) {
-      const int n = s_count[team];
+  }
+  if constexpr (WR == 1) {
+    if (K) {
+      const int n = no_floor ? kLpPool + 1 : s_count[team];
       if (n <= kLpPool) ranked(s_pool[team], n);
       else search();                                 // (many equal ones, or many large ones in few lanes)
     }
@@ -553,7 +574,7 @@ logprobs_kernel(LpArgs a, int* err) {
     if (lane == 0) s_sums[warp] = sum;
     __syncthreads();
     if (K) {
-      const int n = s_count[0];
+      const int n = no_floor ? kLpPool + 1 : s_count[0];
       if (n <= kLpPool) {
         if (warp == 0) ranked(s_pool[0], n);
       } else {                                       // (many equal ones, or many large ones in few threads)
