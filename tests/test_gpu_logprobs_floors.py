@@ -61,3 +61,14 @@ def test_rows_of_which_a_mask_leaves_little(gpt_lib, dtype, M, V, K):
     binding.status()
     keep = sorted((set(range(9)) | {M // 2, M - 1}) & set(range(M)))
     check(pick(d, keep), zd[keep], [t[i] for i in keep], K)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,V", [(30, 50257), (60, 50257), (160, 12345), (330, 12345), (1300, 2500)])
+def test_equal_rows_give_equal_results(gpt_lib, dtype, M, V):
+    # every row of a grid: 8 rows apart they start alike in their 16 bytes, whatever V is
+    z = logits(8, V, M)[np.arange(M) % 8]
+    d, _, _ = run(z, (np.arange(M) % 8).tolist(), 7, dtype)
+    for name, x in d.items():
+        for i in range(8, M):
+            assert torch.equal(x[i], x[i % 8]), (name, i)
