@@ -2,14 +2,16 @@
 module _calls.so that calls it with torch's tensors.
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
-one shared library next to this file; the module (csrc/py_calls.cpp, host code
-only) is compiled beside them. Rebuilds only when a source or header is newer
-than either (or when forced).
+one shared library next to this file. The library knows no torch type and is
+built without torch; where there is one, the module (csrc/py_calls.cpp, host
+code only) is compiled beside the others and linked behind the library. Rebuilds
+only when a source or header is newer than either (or when forced).
 
     python -m decoder_only_transformer_gpt_gb300.build [--force] [--verbose]
 """
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -45,10 +47,15 @@ def _deps():
     return files
 
 
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    made = [LIB, CALLS] if has_torch() else [LIB]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -100,9 +107,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        calls = ex.submit(compile_calls)
+        calls = ex.submit(compile_calls) if has_torch() else None
         results = list(ex.map(compile_one, SOURCES))
-        calls_obj = calls.result()
     if verbose or ptxas_verbose:
         for obj, log in results:
             if log.strip():
@@ -113,7 +119,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    link_calls(calls_obj)
+    if calls:
+        link_calls(calls.result())
+    else:
+        print("no torch: the library alone, without _calls.so (the binding needs both)", file=sys.stderr)
     return LIB
 
 
