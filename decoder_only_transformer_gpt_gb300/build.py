@@ -5,17 +5,20 @@ Each translation unit under csrc/ is compiled in parallel, then linked into
 one shared library next to this file. The library knows no torch type and is
 built without torch; where there is one, the module (csrc/py_calls.cpp, host
 code only) is compiled beside the others and linked behind the library. Rebuilds
-only when a source or header is newer than either (or when forced).
+only when a source or header is newer than either (or when forced), and the
+module alone when it was built against another torch or Python.
 
     python -m decoder_only_transformer_gpt_gb300.build [--force] [--verbose]
 """
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -23,6 +26,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgpt_gb300.so")
 CALLS = os.path.join(HERE, "_calls.so")
+CALLS_FOR = os.path.join(BUILD, "calls_for.txt")    # what _calls.so was built against
 
 SOURCES = ["k_gemm_tc.cu", "k_attn_tc.cu", "k_rowwise.cu", "k_simt.cu", "k_decode.cu", "tmap.cu", "gpt_api.cu",
            "gpt_forward.cu", "gptk.cu", "gptk_noalloc.cu", "k_backward.cu", "k_attn_bwd_tc.cu", "gpt_backward.cu",
@@ -51,12 +55,30 @@ def has_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
-def up_to_date() -> bool:
-    made = [LIB, CALLS] if has_torch() else [LIB]
-    if not all(os.path.exists(f) for f in made):
+def calls_for() -> str:
+    """The torch and the Python whose headers and libraries the module is built against (without an import of torch)."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "?"
+    return f"torch {version} in {importlib.util.find_spec('torch').origin}, {sysconfig.get_config_var('SOABI')}\n"
+
+
+def _newer_than_sources(made: str) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(f) <= os.path.getmtime(made) for f in _deps())
+
+
+def calls_up_to_date() -> bool:
+    if not has_torch():
+        return True
+    if not _newer_than_sources(CALLS) or not os.path.exists(CALLS_FOR):
         return False
-    t = min(os.path.getmtime(f) for f in made)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    with open(CALLS_FOR) as f:
+        return f.read() == calls_for()
+
+
+def up_to_date() -> bool:
+    return _newer_than_sources(LIB) and calls_up_to_date()
 
 
 def _torch_dir() -> str:
@@ -66,7 +88,6 @@ def _torch_dir() -> str:
 
 def compile_calls() -> str:
     """The object file of the module, against this machine's Python, torch and CUDA headers."""
-    import sysconfig
     import torch
     obj = os.path.join(BUILD, "py_calls.o")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
@@ -89,12 +110,17 @@ def link_calls(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of _calls.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS_FOR, "w") as f:
+        f.write(calls_for())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    if not force and _newer_than_sources(LIB):
+        link_calls(compile_calls())
+        return LIB
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 

@@ -54,3 +54,20 @@ def test_a_module_that_fails_leaves_the_library(tools, word):
     with pytest.raises(RuntimeError, match="_calls"):
         build.build()
     assert os.path.exists(build.LIB) and not os.path.exists(build.CALLS) and not build.up_to_date()
+
+
+def test_another_torch_or_python_makes_the_module_anew(tools, monkeypatch):
+    build.build()
+    for what, value in (("metadata.version", "9.9"), ("soabi", "cpython-399")):
+        with monkeypatch.context() as m:
+            if what == "soabi":
+                m.setattr(build.sysconfig, "get_config_var", lambda _: value)
+            else:
+                m.setattr(build.importlib.metadata, "version", lambda _: value)
+            assert not build.up_to_date()
+            tools.commands.clear()
+            build.build()
+            assert len(tools.commands) == 2 and not any("nvcc" in c[0] for c in tools.commands)   # the module alone
+            assert build.up_to_date()
+        assert not build.up_to_date()
+        build.build()
