@@ -625,7 +625,8 @@ def logprobs(logits, targets, logp, entropy=None, stats=None, top_ids=None, top_
     and logp may both be None, a target of -1 gives 0.
 
     entropy [M] (optional); stats [M, 2] (optional, needed by the gradient): the largest logit and the sum of exponentials
-    against it; top_ids int32 and top_logp [M, K] (optional, K <= 32): the most probable tokens."""
+    against it; top_ids int32 and top_logp [M, K] (optional, K <= 32): the most probable tokens. M = 0: nothing to do (here
+    and in logprobs_bwd)."""
     rc = (_CALLS or _compiled()).logprobs(logits, targets, logp, entropy, stats, top_ids, top_logp, stream)
     if rc:
         _check(rc, "gptk_logprobs")

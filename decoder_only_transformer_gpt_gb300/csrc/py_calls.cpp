@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include "../../include/gpt.h"
 #include "../../include/gpt_kernels.h"
 
 #include <initializer_list>
@@ -316,6 +317,8 @@ struct Logits {
   }
 };
 
+bool given(PyObject* o) { return o != Py_None; }
+
 PyObject* logprobs(PyObject* const* a) {             // logits, targets, logp, entropy, stats, top_ids, top_logp, stream
   Device d;
   Logits z(a[0]);
@@ -332,6 +335,11 @@ PyObject* logprobs(PyObject* const* a) {             // logits, targets, logp, e
   float* stats = d.maybe<float>(a[4], "stats", at::kFloat, {z.M, 2});
   float* top = d.maybe<float>(a[6], "top_logp", at::kFloat, {z.M, K});
   void* s = d.stream(a[7]);
+  if (z.M == 0) {                                    // no rows: nothing to do, where some would be taken (no tensor has an address)
+    const bool pairs = given(a[1]) == given(a[2]) && given(a[5]) == given(a[6]);
+    const bool some = given(a[2]) || given(a[3]) || given(a[4]) || given(a[5]);
+    return PyLong_FromLong(z.V >= 1 && K <= 32 && K <= z.V && pairs && some ? GPT_OK : GPT_EINVAL);
+  }
   return status_of([&] {
     return gptk_logprobs(z.p, targets, logp, entropy, stats, ids, top, static_cast<int32_t>(z.M), static_cast<int32_t>(z.V), ld,
                          K > 2147483647LL ? 2147483647 : static_cast<int32_t>(K), z.type == at::kBFloat16, s);
@@ -348,6 +356,10 @@ PyObject* logprobs_bwd(PyObject* const* a) {         // logits, targets, stats, 
   const float* dlogp = d.maybe<float>(a[3], "dlogp", at::kFloat, {z.M});
   const float* dentropy = d.maybe<float>(a[6], "dentropy", at::kFloat, {z.M});
   void* s = d.stream(a[7]);
+  if (z.M == 0) {
+    const bool pairs = given(a[1]) == given(a[3]) && given(a[5]) == given(a[6]);
+    return PyLong_FromLong(z.V >= 1 && pairs && (given(a[3]) || given(a[6])) ? GPT_OK : GPT_EINVAL);
+  }
   return status_of([&] {
     return gptk_logprobs_bwd(z.p, targets, stats, entropy, dlogp, dentropy, g.p, static_cast<int32_t>(z.M), static_cast<int32_t>(z.V),
                              ld, dld, z.type == at::kBFloat16, s);
