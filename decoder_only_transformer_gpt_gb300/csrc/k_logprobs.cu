@@ -374,7 +374,7 @@ logprobs_kernel(LpArgs a, int* err) {
         }
         reached = __shfl_sync(kAll, x, __ffs(__ballot_sync(kAll, at == K - 1)) - 1);
       }
-      if (K > kLpFewTop || reached == -INFINITY) {   // (K / 4 warps have no chunk: 16 x 2,500, K = 16, 9.4 and 4.5 us; or a mask)
+      if (K > kLpFewTop || reached == -INFINITY) {   // (too few warps have a chunk, 16 x 2,500 with K = 16 9.4 and 4.5 us; or a mask)
         if (K <= kLpFewTop) __syncthreads();         // the four of every warp are read
         float order = sorted_values(top, lane);
         s_order[warp][lane] = order;
@@ -730,9 +730,11 @@ cudaError_t launch_logprobs_of(LpArgs a, int* err, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long chunks = (static_cast<long long>(a.V) / Vec<T>::N + kLpChunk - 1) / kLpChunk;
   a.ahead = 4 * sms;                                 // (four blocks an SM)
-  // A warp a row where its whole row is two chunks, or the rows are short and many and not too many tokens are wanted: 4,096 x
-  // 500 with K = 5 7.1 us, a block a row 42; 4,096 x 5,000 22.4 and 30.3, with K = 16 25.5 and 32.6, but with K = 32, where 32
-  // lanes' largest logits make a low floor, 62 and 35; 1,500 x 8,000 17.1 and 14.8, 620 x 5,000 9.0 and 7.9 (graph replays).
+  // A warp a row where its whole row is two chunks, or the rows are short and many and not too many tokens are wanted. Against a
+  // block a row (graph replays): 4,096 x 500 with K = 5 7.1 us and 42; 4,096 x 5,000 in fp32 with K = 0 14.6 and 18.6, with K = 5 22.5
+  // and 30.7, with K = 16 25.7 and 32.9, but with K = 32, where 32 lanes' largest logits make a low floor, 87 and 35; 4,096 x 10,000
+  // in bf16 with K = 5 25 and 45; 1,216 x 1,600 in fp32 6.3 and 8.2, 1,216 x 5,000 11.7 and 10.2, 620 x 5,000 8.2 and 7.1; 1,500 x 8,000
+  // in fp32 with K = 0, 16 chunks, 12.5 and 10.9.
   // Clusters of as many blocks as keep all of them at work at once.
   if (chunks <= 2 || (chunks <= 10 && a.M >= 8LL * sms && a.K <= kLpFewTop)) {
     a.ahead *= kLpWarps;

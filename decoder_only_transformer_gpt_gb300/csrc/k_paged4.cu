@@ -189,10 +189,9 @@ __device__ __forceinline__ int rows_of(const PagedCache& c, const Dec4Shape& w, 
 // that the products with the values take the first parts of their weights and the second ones at once (QR = 4).
 __device__ __forceinline__ int row_in_eight(int n) { return (n & 1) * 4 + (n >> 1); }
 
-// Eight heads' queries as second operands, times 2^(14 - e) for 2^e <= the head's largest value < 2^(e + 1). from: what the
-// score products start with, 8 times the sums of heads 2 q and 2 q + 1; sum: these sums; c: the factors from a product to the
-// softmax's base-2 exponent. load(row, i): values 8 i .. of one of the gn heads (none where
-// gn <= 0); zeros behind them. TWICE: heads 0 to 3 are heads 4 to 7 too.
+// Eight heads' queries as second operands, times 2^(14 - e) for 2^e <= the head's largest value < 2^(e + 1). sum: the sums of heads
+// 2 q and 2 q + 1, times that; c: the factors from a product to the softmax's base-2 exponent. load(row, i): values 8 i .. of one
+// of the gn heads (none where gn <= 0); zeros behind them. TWICE: heads 0 to 3 are heads 4 to 7 too.
 template <int D>
 struct Queries {
   uint32_t f[D / 16][2];
@@ -1198,9 +1197,10 @@ cudaError_t launch_decode4(const PagedCache& c, const uint32_t* ranges, const __
   // Few rows in sight: one launch of clusters, eight blocks at most, with as many units a warp as that takes. It pays while
   // there are not many more blocks than run at once (of more than eight heads on one, whose blocks take more registers, one an
   // SM), and not many units behind each other. Graph replays, against the general form: 12 heads, 12 sequences of 1,000 rows 8.7
-  // and 9.5 us, 14 11.6 and 11.2, 32 22.6 and 13.7; 4 of 4,000 rows 10.8 and 11.1, 8 16.1 and 12.5; one of 12,000 9.8 and 10.3, of
-  // 16,000 12.1 and 11.3; 16 heads on 4, 16 of 4,000 rows 12.8 and 13.7; 48 heads on 4, 16 of 1,000 rows 10.4 and 13.1, 8 of 2,000
-  // 14.8 and 12.7, 4 of 4,000 12.5 and 13.9, 8 of 4,000 18.7 and 16.2.
+  // and 9.7 us, 14 11.5 and 11.4, 32 22.6 and 14.1; 4 of 4,000 rows 10.7 and 11.3, 8 16.2 and 12.7; one of 12,000 9.8 and 10.3, of
+  // 16,000 11.3 and 11.3; 16 heads on 4, 32 of 1,000 9.7 and 11.3, 48 14.0 and 12.9, 16 of 4,000 12.9 and 13.9; 32 heads on 4, 32 of 1,000
+  // 10.9 and 12.8, 16 of 4,000 14.5 and 14.8; 48 heads on 4, 16 of 1,000 11.5 and 13.4, 24 16.7 and 15.0, 8 of 2,000 16.2 and 14.3, 4 of
+  // 4,000 14.2 and 15.3, 8 of 4,000 21.2 and 16.1.
   long long units = ((static_cast<long long>(c.max_pages) << c.page_log2) + 31) / 32;
   if (w.window > 0) {
     const long long cut = (w.window + 31LL) / 32 + 1 + (w.sinks + 31LL) / 32;
