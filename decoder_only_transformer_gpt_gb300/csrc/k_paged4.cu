@@ -17,8 +17,9 @@
 // row of no weight but 2^36 times the others' size left nothing of their codes.) They enter in two parts, what fp16 holds of
 // them and what it holds of the rest: 2^-20 of a term is lost, and 2^-30 of the largest for each part of the smallest. One part
 // alone loses 2^-12 and is less work: 28.6 us with 8 heads on each of 4 key heads below, 44.8 with 12; but the 16-bit
-// cache's attention holds them in two parts as well. References of the softmax are whole numbers, so that raising one rescales the
-// sums exactly.
+// cache's attention holds them in two parts as well. References of the softmax start at a score and rise by whole numbers, so that
+// raising one rescales the sums exactly; scores are in the softmax's base-2 units but for a power of two, so that the exponent of
+// the largest is exactly 0: a row seen alone comes out as it is.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -190,14 +191,14 @@ __device__ __forceinline__ int rows_of(const PagedCache& c, const Dec4Shape& w, 
 __device__ __forceinline__ int row_in_eight(int n) { return (n & 1) * 4 + (n >> 1); }
 
 // Eight heads' queries as second operands, times 2^(14 - e) for 2^e <= the head's largest value < 2^(e + 1). sum: the sums of heads
-// 2 q and 2 q + 1, times that; c: the factors from a product to the softmax's base-2 exponent. load(row, i): values 8 i .. of one
+// 2 q and 2 q + 1, times that; c: the powers of two from a score to the softmax's base-2 exponent. load(row, i): values 8 i .. of one
 // of the gn heads (none where gn <= 0); zeros behind them. TWICE: heads 0 to 3 are heads 4 to 7 too.
 template <int D>
 struct Queries {
   uint32_t f[D / 16][2];
   float sum[2], c[2];
   template <bool TWICE, typename Load>
-  __device__ __forceinline__ void take(float scale_log2, int gn, int lane, Load&& load) {
+  __device__ __forceinline__ void take(int gn, int lane, Load&& load) {
     constexpr int C = D / 4;                         // values of a lane: its codes' places
     const int head = TWICE ? (lane >> 2) & 3 : lane >> 2;
     float v[C], top = 0.0f, mine = 0.0f;
@@ -216,7 +217,7 @@ struct Queries {
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
     const int e = max(exponent_of(top), -100);
-    const float factor = exp2_of(14 - e), back = scale_log2 * exp2_of(e - 14);
+    const float factor = exp2_of(14 - e), back = exp2_of(e - 14);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       v[k] *= factor;
@@ -301,13 +302,13 @@ struct Segment {
   static constexpr bool ONE = QR == 1, TWICE = QR == 4;
   Queries<D> qs[NQ];
   float o[NQ][NT][4];                                // times `into`, as off is
-  float m[NQ][2], l[NQ][2], off[NQ][2];              // m: the reference, a whole number
+  float m[NQ][2], l[NQ][2], off[NQ][2];              // m: the reference
   float into[NQ][2];                                 // 2^(15 - E): 2^E is above every term of the head, at m
   float due[NQ][2];                                  // the reference above which E has to be set anew
   float most;                                        // the largest of all heads' 2^(15 - E)
 
   template <typename Load>
-  __device__ __forceinline__ void start(float scale_log2, int gn, int lane, Load&& load) {
+  __device__ __forceinline__ void start(int gn, int lane, Load&& load) {
     most = exp2_of(15 - kLeast);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -322,7 +323,7 @@ struct Segment {
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][j][k] = 0.0f;
-      qs[i].template take<TWICE>(scale_log2, gn - 8 * i, lane, [&](int r, int u) { return load(8 * i + r, u); });
+      qs[i].template take<TWICE>(gn - 8 * i, lane, [&](int r, int u) { return load(8 * i + r, u); });
     }
     if constexpr (ONE) {                             // every lane has rows of the one head
       qs[0].sum[0] = __shfl_sync(kAll, qs[0].sum[0], 0);
@@ -348,8 +349,12 @@ struct Segment {
   // Raises a head's reference for a largest score of mx. True: its E has to be set anew.
   __device__ __forceinline__ bool raise(int i, int k, float mx) {
     const float before = m[i][k];
-    m[i][k] = fmaxf(before, ceilf(mx));
-    const float a = exp2_of(-static_cast<int>(fminf(reference(i, k) - before, 127.0f)));
+    float up = 0.0f;
+    if (mx > before) {                               // (rounded upwards: no score is above its reference)
+      up = ceilf(__fsub_ru(mx, before));
+      m[i][k] = before == -INFINITY ? mx : __fadd_ru(before, up);
+    }
+    const float a = exp2_of(-static_cast<int>(fminf(up, 127.0f)));
     l[i][k] *= a;
     multiply(i, k, a);
     return m[i][k] > due[i][k];
@@ -412,7 +417,7 @@ struct Segment {
   }
 
   // Scores of the tiles into probabilities times the rows' scales. factors: shared address of the rows' (key scale, key
-  // lowest, value scale, value lowest + 8 value scale); large: one of the latter may pass a head's 2^E.
+  // lowest, both in base-2 units, value scale, value lowest + 8 value scale); large: one of the latter may pass a head's 2^E.
   template <int NJ>
   __device__ __forceinline__ void weigh(float (&s)[NQ][NJ][4], uint32_t factors, const uint32_t (&seen)[NJ / 2],
                                         uint32_t unseen, bool large, int lane) {
@@ -445,7 +450,7 @@ struct Segment {
         float x = s[i][0][k];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) x = j ? fmax3(x, s[i][j][k], s[i][j][2 + k]) : fmaxf(x, s[i][j][2 + k]);
-        x = __fmul_ru(x, qs[i].c[k]);                // (upwards: no exponent below is above 0)
+        x *= qs[i].c[k];
         x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
         x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
         mx[k] = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
@@ -513,7 +518,7 @@ struct Segment {
       if (unseen && !((seen[h] >> lane) & 1u)) x[h] = -INFINITY;
       mx = fmaxf(mx, x[h]);
     }
-    mx = warp_max(__fmul_ru(mx, qs[0].c[0]));        // (upwards: no exponent below is above 0)
+    mx = warp_max(mx * qs[0].c[0]);
     bool anew = large;
     if (mx > m[0][0]) anew = raise(0, 0, mx) || large;   // a higher reference (the same for all lanes)
     const float ref = reference(0, 0);
@@ -783,7 +788,7 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
       if (tile == at.t0)
-        g.start(w.scale_log2, min(w.G - at.mt * 16, 16), lane,
+        g.start(min(w.G - at.mt * 16, 16), lane,
                 [&](int r, int u) { return lds128(st + Cfg::QUERIES + (r * (D / 8) + u) * 16); });
       const int f = first_row<UNIT>(at.t, tile), after = at.t.n - w.window;   // the window's first row
       uint32_t seen[NH], unseen = 0u;                  // the tile's rows that are
@@ -803,8 +808,8 @@ paged4_split_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
             if (!mine) vr = 0u;
           }
           unseen |= ~seen[h];
-          ks[h] = scale_of(kr) * 16777216.0f;
-          kl[h] = low_of(kr);
+          ks[h] = scale_of(kr) * (16777216.0f * w.scale_log2);
+          kl[h] = low_of(kr) * w.scale_log2;
           vs[h] = scale_of(vr);
           vl[h] = fmaf(8.0f, vs[h], low_of(vr));
           size = fmax3(size, vs[h], fabsf(vl[h]));
@@ -946,7 +951,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
   const int guess = (rank * upw * 8 + warp) * UNIT;
   int page = __ldg(trow + min((guess + lane) >> c.page_log2, c.max_pages - 1));
   Segment<D, QR> g;
-  g.start(w.scale_log2, gn, lane,
+  g.start(gn, lane,
           [&](int r, int u) { return __ldg(reinterpret_cast<const uint4*>(tok + static_cast<size_t>(r) * D) + u); });
   const int n = rows_of(c, w, len);
   if (n <= 0) {                                      // (the same for the whole cluster)
@@ -1008,7 +1013,7 @@ paged4_short_kernel(PagedCache c, const uint32_t* __restrict__ ranges, const __n
       vr = __ldg(ranges + row + vrows);
     }
     const uint32_t seen[1] = {have};
-    float ks[1] = {scale_of(kr) * 16777216.0f}, kl[1] = {low_of(kr)}, vs[1] = {scale_of(vr)};
+    float ks[1] = {scale_of(kr) * (16777216.0f * w.scale_log2)}, kl[1] = {low_of(kr) * w.scale_log2}, vs[1] = {scale_of(vr)};
     float vl[1] = {fmaf(8.0f, vs[0], low_of(vr))};
     const bool large = __any_sync(kAll, fmaxf(vs[0], fabsf(vl[0])) * g.most >= 32768.0f);
     float s[NQ][2][4], eights[NQ][4];

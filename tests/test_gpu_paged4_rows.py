@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 import paged4_ref as ref  # noqa: E402
 from gpu_util import dev_bf16, dev_i32, host, rand_bf16  # noqa: E402
 from paged_ref import seen_rows  # noqa: E402
-from serving_ref import quantise  # noqa: E402
+from serving_ref import quantise, values  # noqa: E402
 
 FORMS = [None, 1024, 4096, 65536]                 # room of the page table, by which the form is chosen
 HEADS = [(3, 3, 64), (4, 2, 32), (8, 2, 64), (6, 1, 64), (8, 1, 32), (12, 1, 64), (16, 1, 32), (20, 1, 64)]
@@ -179,3 +179,16 @@ def test_pages_out_of_sight_need_not_exist(gpt_lib, rows, H, Hkv, D, page, windo
         c.call()
         binding.status()
         c.check()
+
+
+@pytest.mark.parametrize("rows", FORMS)
+@pytest.mark.parametrize("H,Hkv,D", HEADS)
+def test_a_row_seen_alone_comes_out_as_it_is(gpt_lib, rows, H, Hkv, D):
+    # its weight is 1 and nothing is added: the value in fp32, rounded to bf16
+    rng = np.random.default_rng(9)
+    for n, window in ((1, 0), (200, 1), (65, 1)):
+        k, u = (rand_bf16(rng, (n, Hkv, D)) * 2.0 for _ in range(2))
+        c = Cache(rand_bf16(rng, (1, H, D)), [k], [u], H, 16, rows, window).device().call()
+        pg, slot = c.table[0, (n - 1) // 16], (n - 1) % 16
+        held = values(c.codes[pg, 1, :, slot], c.ranges[pg, 1, :, slot]).repeat(H // Hkv, 0)
+        assert torch.equal(c.y.cpu().view(H, D), torch.from_numpy(held.astype(np.float32)).bfloat16())
