@@ -15,7 +15,7 @@
 // lists for every warp behind the sums 135 and 85.)
 //
 // Bound by memory where rows are many: 4,096 x 50,257 in fp32 121 us with K = 0, 6.8 TB/s, what a copy reaches, and 129 with
-// K = 8; in bf16 69 and 81, 6.0 TB/s, the exponentials' units and the sums' instructions close behind. The part after the
+// K = 8; in bf16 69 and 82, 6.0 TB/s, the exponentials' units and the sums' instructions close behind. The part after the
 // sums reads little and lets the memory rest: that is what K adds. 16 rows with K = 5 4.6 us in a graph, 2.9 with K = 0.
 #include "common.cuh"
 #include "kernels.h"

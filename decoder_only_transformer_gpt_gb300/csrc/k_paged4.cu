@@ -35,14 +35,14 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// Bound by memory once all warps are under way (8 sequences of 20,000 rows more take 19.3 us, 7.2 TB/s), with about 540
+// Bound by memory once all warps are under way (8 sequences of 20,000 rows more take 19.3 us, 7.2 TB/s), with about 570
 // instructions for 64 rows of a key head close behind: a byte of codes takes a warp twice the unpacking and products of a byte
 // of bf16, and the integer unit takes a warp's instruction only every other cycle. Measured: 16 sequences of 9,000 to 32,000
-// rows x 12 heads 55.7 us (graph replays), 5.1 TB/s, of which the first rows' chain of loads and the last units take 8 and the
-// join 5; the rows of a 16-bit cache take 160. With 4 query heads on each of 4 key heads 28.5, with 8 31.2, with 12 50.8, whose
-// instructions bound them. Work is dealt as in the 16-bit cache's kernel (k_paged.cu):
-// units of 64 rows (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal
-// contiguous ranges of the list of all units to every warp, partial results joined by a second kernel. What differs:
+// rows x 12 heads 53.5 us (graph replays of two inputs 56.6), 5.3 TB/s, of which the first rows' chain of loads and the last units
+// take 8 and the join 5; the rows of a 16-bit cache take 160. With 4 query heads on each of 4 key heads 29.5, with 8 31.9, with 12
+// 51.8 (graph replays), whose instructions bound them. Work is dealt as in the 16-bit cache's kernel (k_paged.cu): units of 64 rows
+// (32 for more than eight heads) of one (sequence, key head, group of up to 16 query heads), equal contiguous ranges of the list
+// of all units to every warp, partial results joined by a second kernel. What differs:
 //  * The rows' order inside a unit and the values' order inside a product are free, so fragments are read from shared
 //    memory as they lie there, without ldmatrix: a lane takes a quarter of a key row (8 bytes: its codes are the lane's
 //    operands of four products), and of value rows the same byte column of four rows, two of which are interleaved by one

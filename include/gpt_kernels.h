@@ -280,10 +280,10 @@ int gptk_paged_append(const void* qkv, void* out, void* pool, float* weight, con
  * largest product of a probability of that head and its row's scale, or |lowest + 8 scale|). Keys' scales and lowest
  * values have to stay below 2^100. A NaN in sight makes its queries' outputs NaN, and so do scores that are all -inf. Rows
  * out of sight count for nothing, whatever they hold; a page with none in sight need not exist, whatever the table says;
- * rows in sight whose page does not exist are left out (and reported). y overlaps no input. B max_pages page / 32 < 2^31, and times Hkv <= 2^40 (GPT_EINVAL otherwise). Scratch (none where the
- * table, or the window and sinks, hold few rows; else 1.3 MB with a key head for each query head, 5 MB for two to four, 10 MB
- * for five to eight, 15 MB for more, and 4 (B + 1) bytes) is taken on the stream as for gptk_paged_attention; make a process's first call on a device
- * before any stream capture.
+ * rows in sight whose page does not exist are left out (and reported). y overlaps no input. B max_pages page / 32 < 2^31, and
+ * times Hkv <= 2^40 (GPT_EINVAL otherwise). Scratch (none where the table, or the window and sinks, hold few rows; else 1.3 MB
+ * with a key head for each query head, 5 MB for two to four, 10 MB for five to eight, 15 MB for more, and 4 (B + 1) bytes) is
+ * taken on the stream as for gptk_paged_attention; make a process's first call on a device before any stream capture.
  */
 int gptk_paged_append4(const void* qkv, void* out, void* codes, void* ranges, const int32_t* table, const int32_t* start,
                        const int32_t* count, const int32_t* pos, const uint64_t* turns, int32_t B, int32_t T, int32_t H,

@@ -63,7 +63,8 @@ def attend4(qkv, codes, ranges, table, lens, H, window, sinks, added=0):
     roundings. So the base-2 exponents are off by d, the weights by the factor 2^(2 d), another 2^-20 for exponentials and sums.
     A weight times its scale is rounded to fp16 once, 2^-12 of it, times |code - 8| <= 8; the smallest ones to whole multiples
     of 2^-39 of 2^E, which is at most twice the largest scale or lowest value: 2^-40 8 of that for each row. The sum that
-    stands for low + 8 scale takes the weights as they are.
+    stands for low + 8 scale takes the weights as they are. (The kernels hold such products in two parts, in a unit that follows
+    the head's largest: paged4_ref.attend_rows has those closer bounds.)
     """
     pages, _, Hkv, page, half = codes.shape
     D, B, G = 2 * half, len(lens), H // Hkv
