@@ -14,7 +14,7 @@ def pick(d, rows):
     return {k: None if v is None else v[rows] for k, v in d.items()}
 
 
-@pytest.mark.parametrize("dtype,V", [(BF16, 2049), (BF16, 2056), (BF16, 2500), (BF16, 3072), (F32, 1025), (F32, 1300), (F32, 1536),
+@pytest.mark.parametrize("dtype,V", [(BF16, 2049), (BF16, 2056), (BF16, 2500), (BF16, 3071), (F32, 1025), (F32, 1300), (F32, 1536),
                                      (BF16, 1033), (F32, 700)])
 @pytest.mark.parametrize("K", [4, 5, 9, 10, 12, 13, 16, 17, 32])
 def test_rows_of_few_chunks(gpt_lib, dtype, V, K):
